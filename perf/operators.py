@@ -260,18 +260,18 @@ def _plain_plan(s):
     head, tail = s["state"][0], s["state"][1]
     done = new < 0
     q = new.clamp(min=0)
-    kv = torch.where(done, 0, ctx + q)
     zero = torch.zeros(1, dtype=torch.int64, device=ctx.device)
     cu = torch.cat([zero, q.cumsum(0)])
     have = (ctx + page - 1) // page
-    need = torch.where(done, 0, (kv + page - 1) // page)
+    need = torch.where(done, 0, (ctx + q + page - 1) // page)
     grow = (need - have).clamp(min=0)
-    before = grow.cumsum(0) - grow
+    whole = grow.cumsum(0)
+    fits = (whole <= tail - head) | (grow == 0)
+    kv = torch.where(done, 0, torch.where(fits, ctx + q, ctx))
     j = torch.arange(width, device=ctx.device)
-    rank = before[:, None] + j - have[:, None]
-    fresh = (j >= have[:, None]) & (j < need[:, None])
-    got = torch.where(rank < tail - head, ring[(head + rank.clamp(min=0)) % ring.numel()], -1)
-    table = torch.where(fresh, got, table)
+    rank = (whole - grow)[:, None] + j - have[:, None]
+    fresh = (j >= have[:, None]) & (j < need[:, None]) & fits[:, None]
+    table = torch.where(fresh, ring[(head + rank.clamp(min=0)) % ring.numel()], table)
     back = torch.where(done, have, 0)
     entry = torch.arange(ring.numel(), device=ctx.device)
     upto = back.cumsum(0)
@@ -284,10 +284,9 @@ def _plain_plan(s):
     live = t < cu[-1]
     pos = ctx[r] + t - cu[r]
     block = table[r, (pos // page).clamp(max=width - 1)].long()
-    slots = torch.where(live & (block >= 0), block * page + pos % page, -1)
-    want = grow.sum()
-    taken = torch.minimum(want, tail - head)
-    state = torch.stack([head + taken, tail + upto[-1], want - taken])
+    slots = torch.where(live & fits[r], block * page + pos % page, -1)
+    taken = torch.where(fits, whole, 0).amax().minimum(tail - head)
+    state = torch.stack([head + taken, tail + upto[-1], whole[-1] - taken])
     return dict(cu_q=cu.int(), kv_lens=kv.int(), slots=slots, positions=torch.where(live, pos, -1).int(), table=table, ring=ring, state=state)
 
 
