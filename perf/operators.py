@@ -285,7 +285,7 @@ def _plain_plan(s):
     pos = ctx[r] + t - cu[r]
     block = table[r, (pos // page).clamp(max=width - 1)].long()
     slots = torch.where(live & fits[r], block * page + pos % page, -1)
-    taken = torch.where(fits, whole, 0).amax().minimum(tail - head)
+    taken = torch.where(whole <= tail - head, whole, 0).amax()
     state = torch.stack([head + taken, tail + upto[-1], whole[-1] - taken])
     return dict(cu_q=cu.int(), kv_lens=kv.int(), slots=slots, positions=torch.where(live, pos, -1).int(), table=table, ring=ring, state=state)
 
