@@ -428,6 +428,111 @@ mxfa_status mxfa_gemm_quant_fmt(const mxfa_mx* a, int a_fmt, const mxfa_mx* b, i
                                 int64_t N, int64_t K, void* y_bf16, const mxfa_mx_out* y_row,
                                 const mxfa_mx_out* y_col, mxfa_stream_t stream);
 
+/* ------------------------------------------------------------ 4-bit KV cache
+ * Serving: keys and values of the tokens so far, held as MXFP4 or NVFP4 in pages,
+ * and the attention that reads them.  The web pages above have no counterpart to
+ * these calls; the formats are those of mxfa_quantize_lowp.
+ *
+ * A cache (of one layer) is num_blocks pages of `page` rows (16, 32, 64 or 128)
+ * for each of H key heads, D = 128:
+ *  k, v        E2M1 codes [num_blocks][H][page][64], two to a byte, the even
+ *              channel in the low nibble
+ *  k_sf, v_sf  block scales [num_blocks][H][page][4] (MXFP4: E8M0 per 32
+ *              channels) or [8] (NVFP4: E4M3 per 16 channels)
+ *  k_scale, v_scale  NVFP4: DEVICE fp32, the (finite, positive) scale of the whole
+ *              K and V cache, chosen by the caller before the first store; unused for
+ *              MXFP4
+ * All device pointers, owned by the caller, codes and scales 16-byte aligned.
+ * A slot is block * page + row.  A cached value is code * scale (* k_scale or
+ * v_scale).  MXFP4 scales are 2^X with X = floor(log2 amax) - 2 clamped to
+ * [-23, 13], so that every cached value is a binary16 number: magnitudes
+ * above 49152 saturate and blocks below 2^-21 lose precision, where
+ * mxfa_quantize_lowp clamps to the whole range of E8M0.  NVFP4 scales are
+ * E4M3(amax / (6 st)), codes E2M1(x / (scale st)), as mxfa_quantize_lowp's.  A block
+ * holding Inf or NaN reads back as NaN (scale 0xFF or 0x7F, codes 0). */
+#define MXFA_KV_MXFP4 0
+#define MXFA_KV_NVFP4 1
+typedef struct {
+  uint8_t *k, *v;
+  uint8_t *k_sf, *v_sf;
+  const float *k_scale, *v_scale;
+  int64_t num_blocks;
+  int page, H, D, fmt;
+} mxfa_kv_cache;
+
+/* Bytes of the codes (of k or of v) and of the block scales of a cache. */
+size_t mxfa_kv_codes_bytes(int64_t num_blocks, int page, int H);
+size_t mxfa_kv_sf_bytes(int64_t num_blocks, int page, int H, int fmt);
+
+/* mxfa_kv_plan -- block tables and slots of a step, from request lengths, on
+ * the GPU and without a host read, so that a captured graph can be replayed.
+ *  ctx_lens     int32 [R], tokens in the cache before the step
+ *  new_lens     int32 [R], new tokens of the step; negative: the request is done
+ *  block_table  int32 [R][max_blocks], the first ceil(ctx / page) entries of a
+ *               row in use; new blocks are written behind them, other entries stay
+ *  free_ring    int32 [ring_size], queue of free blocks; ring_size is at least the number of
+ *               blocks, so that blocks given back never reach those still queued
+ *  ring_in/out  int64 [3]: number of blocks ever taken, number ever put in (free
+ *               blocks are the ring entries [taken, put) modulo ring_size), and (written
+ *               only) the blocks that this step lacked
+ *  tokens       rows of slots and positions
+ *  cu_q         int32 [R + 1], prefix sums of max(new_lens, 0)
+ *  kv_lens      int32 [R]: ctx + new; 0 for a done request
+ *  slots        int64 [tokens], positions int32 [tokens]: token t of the step, the
+ *               requests' tokens one after another; -1 for tokens past cu_q[R]
+ * Blocks are taken in request order.  Where the free ones do not suffice, the
+ * first request that would exceed them and all later ones that need a block get none:
+ * their kv_lens stays ctx, their slots are -1 (mxfa_kv_append skips them), and
+ * ring_out[2] > 0 says so.  A done request's blocks go back in request and table
+ * order and can be taken from the next step on.  kv_lens may be ctx_lens and
+ * ring_out may be ring_in (a step captured once and replayed); partly
+ * overlapping buffers are MXFA_ERR_INVALID_ARG.  A request whose tokens exceed
+ * max_blocks pages gets no block and is recorded as a failed index check.
+ * R <= 16384, page as above, max_blocks * page <= 2^30 (else MXFA_ERR_UNSUPPORTED). */
+mxfa_status mxfa_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int R, int32_t* block_table,
+                         int max_blocks, int32_t* free_ring, int64_t ring_size, const int64_t* ring_in,
+                         int64_t* ring_out, int page, int64_t tokens, int32_t* cu_q, int32_t* kv_lens,
+                         int64_t* slots, int32_t* positions, mxfa_stream_t stream);
+
+/* mxfa_kv_append -- quantizes new tokens into their slots.
+ *  k, v      bf16 rows of H * 128, consecutive tokens k_stride / v_stride elements
+ *            apart (multiples of 8, at least H * 128), 16-byte aligned
+ *  slots     DEVICE int64 [tokens]; negative: the token is skipped.  Slots of one call are
+ *            distinct (two tokens with one slot leave it undefined); a slot past the
+ *            cache is skipped and recorded as a failed index check */
+mxfa_status mxfa_kv_append(const mxfa_kv_cache* cache, const void* k, const void* v, int64_t k_stride,
+                           int64_t v_stride, int64_t tokens, const int64_t* slots, mxfa_stream_t stream);
+
+/* mxfa_kv_load -- the cached values of slots as bf16 k, v [tokens][H][128] (MXFP4
+ * exact, NVFP4 rounded to nearest), in any order and repeated at will; zeros
+ * for a negative slot (and for one past the cache, which is recorded). */
+mxfa_status mxfa_kv_load(const mxfa_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k, void* v,
+                         mxfa_stream_t stream);
+
+/* Workspace of mxfa_kv_attn on the current device. */
+size_t mxfa_kv_attn_workspace_size(int R, int max_q, int Hq, int H);
+
+/* mxfa_kv_attn -- attention of new query tokens over the cache.
+ *  q            bf16 rows of Hq * 128, q_stride elements apart (a multiple of 8),
+ *               Hq a multiple of the cache's H: query heads h G .. h G + G - 1 read
+ *               key head h, G = Hq / H
+ *  cu_q         DEVICE int32 [R + 1]; request r's queries are rows cu_q[r] ..
+ *               cu_q[r + 1] - 1, at most max_q of them; rows outside are not written
+ *  kv_lens      DEVICE int32 [R], keys of each request, its new tokens included
+ *  block_table  DEVICE int32 [R][max_blocks]
+ *  causal       1: query i of a request's n sees keys j <= kv - n + i; 0: all keys
+ *  o            bf16 [total_q][Hq][128];  lse fp32 [Hq][total_q], natural log.  A query
+ *               that sees no key gets O = 0 and lse = -inf
+ *  ws           mxfa_kv_attn_workspace_size() bytes, 16-byte aligned, not shared by calls
+ *               that can run at the same time; its contents need not be kept
+ * Keys past kv_lens or in no row's sight are not used, whatever they hold.  A block index
+ * outside the cache (its keys count as not there) and offsets or lengths outside
+ * their tables (the request is left out) are recorded as failed index checks. */
+mxfa_status mxfa_kv_attn(const mxfa_kv_cache* cache, const void* q, int64_t q_stride, int64_t total_q,
+                         const int32_t* cu_q, const int32_t* kv_lens, int R, const int32_t* block_table,
+                         int max_blocks, int max_q, int Hq, float softmax_scale, int causal, void* o,
+                         float* lse, void* ws, size_t ws_bytes, mxfa_stream_t stream);
+
 /* mxfa_tensor_peak_probe -- `ctas` CTAs (one per SM at most) each issue
  * `iters` x 4 back-to-back block-scaled MMAs (M = 128, N = 256, K = 32, E4M3,
  * operands resident in shared memory) and write the SM clock cycles they took

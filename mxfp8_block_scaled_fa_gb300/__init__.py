@@ -19,6 +19,8 @@ def __getattr__(name):
                                             "LOWP_MXFP4", "LOWP_MXFP6_E2M3", "LOWP_MXFP6_E3M2",
                                             "LOWP_NVFP4", "LOWP_CODES", "LOWP_MMA", "ELEM_E4M3", "ELEM_E2M3", "ELEM_E3M2",
                                             "ELEM_E2M1",
+                                            "KV_MXFP4", "KV_NVFP4", "KvCache", "KvPages", "KvStep", "kv_ring", "kv_plan",
+                                            "kv_append", "kv_load", "kv_attention",
                                             "device_status"):
         from . import mxfa as _m
         return getattr(_m, name)

@@ -738,6 +738,183 @@ mxfa_status gemm_common(const mxfa_mx* a, int a_code, const mxfa_mx* b, int b_co
 }
 }  // namespace
 
+namespace {
+
+// Checks of a cache, shared by the calls that take one.
+mxfa_status check_cache(const mxfa_kv_cache* c, KvPages& p) {
+  if (!c || !c->k || !c->v || !c->k_sf || !c->v_sf) return MXFA_ERR_INVALID_ARG;
+  if (c->fmt != MXFA_KV_MXFP4 && c->fmt != MXFA_KV_NVFP4) return MXFA_ERR_INVALID_ARG;
+  if (c->num_blocks <= 0 || c->page <= 0 || c->H <= 0) return MXFA_ERR_INVALID_ARG;
+  if (c->D != 128) return MXFA_ERR_UNSUPPORTED;
+  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return MXFA_ERR_UNSUPPORTED;
+  if (c->num_blocks >= (int64_t(1) << 31) || c->H > 65536) return MXFA_ERR_UNSUPPORTED;
+  if (c->fmt == MXFA_KV_NVFP4 && (!c->k_scale || !c->v_scale)) return MXFA_ERR_INVALID_ARG;
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_sf) || !aligned16(c->v_sf)) return MXFA_ERR_MISALIGNED;
+  if (c->fmt == MXFA_KV_NVFP4 && (!aligned4(c->k_scale) || !aligned4(c->v_scale))) return MXFA_ERR_MISALIGNED;
+  p.k = c->k;
+  p.v = c->v;
+  p.k_sf = c->k_sf;
+  p.v_sf = c->v_sf;
+  p.k_scale = c->k_scale;
+  p.v_scale = c->v_scale;
+  p.blocks = c->num_blocks;
+  p.page = c->page;
+  p.page_shift = c->page == 16 ? 4 : c->page == 32 ? 5 : c->page == 64 ? 6 : 7;
+  p.H = c->H;
+  p.fmt = c->fmt;
+  return MXFA_OK;
+}
+
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+// 0: [a, a + na) and [b, b + nb) do not meet; 1: they begin at one place; 2: they overlap
+int overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  if (x == y) return 1;
+  return x < y + nb && y < x + na ? 2 : 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mxfa_kv_codes_bytes(int64_t num_blocks, int page, int H) {
+  if (num_blocks < 0 || page <= 0 || H <= 0) return 0;
+  return size_t(num_blocks) * size_t(page) * size_t(H) * 64u;
+}
+
+size_t mxfa_kv_sf_bytes(int64_t num_blocks, int page, int H, int fmt) {
+  if (num_blocks < 0 || page <= 0 || H <= 0) return 0;
+  return size_t(num_blocks) * size_t(page) * size_t(H) * (fmt == MXFA_KV_NVFP4 ? 8u : 4u);
+}
+
+mxfa_status mxfa_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int R, int32_t* block_table,
+                         int max_blocks, int32_t* free_ring, int64_t ring_size, const int64_t* ring_in,
+                         int64_t* ring_out, int page, int64_t tokens, int32_t* cu_q, int32_t* kv_lens,
+                         int64_t* slots, int32_t* positions, mxfa_stream_t stream) {
+  if (R < 0 || max_blocks <= 0 || ring_size <= 0 || tokens < 0) return MXFA_ERR_INVALID_ARG;
+  if (!free_ring || !ring_in || !ring_out || !cu_q) return MXFA_ERR_INVALID_ARG;
+  if (R > 0 && (!ctx_lens || !new_lens || !block_table || !kv_lens)) return MXFA_ERR_INVALID_ARG;
+  if (tokens > 0 && (!slots || !positions)) return MXFA_ERR_INVALID_ARG;
+  if (page != 16 && page != 32 && page != 64 && page != 128) return MXFA_ERR_UNSUPPORTED;
+  if (R > kKvPlanMaxRequests || tokens >= (int64_t(1) << 31) || ring_size >= (int64_t(1) << 31) ||
+      int64_t(max_blocks) * page > (int64_t(1) << 30) || int64_t(R) * max_blocks >= (int64_t(1) << 31))
+    return MXFA_ERR_UNSUPPORTED;
+  for (const void* p : {static_cast<const void*>(ctx_lens), static_cast<const void*>(new_lens),
+                        static_cast<const void*>(block_table), static_cast<const void*>(free_ring),
+                        static_cast<const void*>(cu_q), static_cast<const void*>(kv_lens),
+                        static_cast<const void*>(positions)})
+    if (!aligned4(p)) return MXFA_ERR_MISALIGNED;
+  if (!aligned8(ring_in) || !aligned8(ring_out) || !aligned8(slots)) return MXFA_ERR_MISALIGNED;
+  const size_t lens = size_t(R) * 4;
+  const int same_len = R > 0 ? overlap(ctx_lens, lens, kv_lens, lens) : 0;
+  const int same_ring = overlap(ring_in, 24, ring_out, 24);
+  if (same_len == 2 || same_ring == 2) return MXFA_ERR_INVALID_ARG;
+  if (R > 0 && overlap(new_lens, lens, kv_lens, lens) != 0) return MXFA_ERR_INVALID_ARG;
+  KvPlanArgs a;
+  memset(&a, 0, sizeof(a));
+  a.ctx = ctx_lens;
+  a.add = new_lens;
+  a.R = R;
+  a.table = block_table;
+  a.width = max_blocks;
+  a.ring = free_ring;
+  a.ring_size = ring_size;
+  a.ring_in = ring_in;
+  a.ring_out = ring_out;
+  a.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
+  a.tokens = tokens;
+  a.cu_q = cu_q;
+  a.kv_lens = kv_lens;
+  a.slots = slots;
+  a.positions = positions;
+  a.aliased = same_len == 1 || same_ring == 1;
+  return from_cuda(launch_kv_plan(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+mxfa_status mxfa_kv_append(const mxfa_kv_cache* cache, const void* k, const void* v, int64_t k_stride,
+                           int64_t v_stride, int64_t tokens, const int64_t* slots, mxfa_stream_t stream) {
+  KvRowsArgs a;
+  memset(&a, 0, sizeof(a));
+  mxfa_status s = check_cache(cache, a.c);
+  if (s) return s;
+  if (!k || !v || !slots || tokens < 0) return MXFA_ERR_INVALID_ARG;
+  if (tokens > 1 && (k_stride < int64_t(a.c.H) * 128 || v_stride < int64_t(a.c.H) * 128)) return MXFA_ERR_INVALID_ARG;
+  if (tokens >= (int64_t(1) << 31) || tokens * a.c.H >= (int64_t(1) << 31) - 16) return MXFA_ERR_UNSUPPORTED;
+  if (!aligned16(k) || !aligned16(v) || !aligned8(slots) || (tokens > 1 && (k_stride % 8 || v_stride % 8)))
+    return MXFA_ERR_MISALIGNED;
+  if (tokens == 0) return MXFA_OK;
+  a.k = const_cast<uint16_t*>(static_cast<const uint16_t*>(k));
+  a.v = const_cast<uint16_t*>(static_cast<const uint16_t*>(v));
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.tokens = tokens;
+  a.slots = slots;
+  return from_cuda(launch_kv_append(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+mxfa_status mxfa_kv_load(const mxfa_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k, void* v,
+                         mxfa_stream_t stream) {
+  KvRowsArgs a;
+  memset(&a, 0, sizeof(a));
+  mxfa_status s = check_cache(cache, a.c);
+  if (s) return s;
+  if (!k || !v || !slots || tokens < 0) return MXFA_ERR_INVALID_ARG;
+  if (tokens >= (int64_t(1) << 31) || tokens * a.c.H >= (int64_t(1) << 31) - 16) return MXFA_ERR_UNSUPPORTED;
+  if (!aligned16(k) || !aligned16(v) || !aligned8(slots)) return MXFA_ERR_MISALIGNED;
+  if (tokens == 0) return MXFA_OK;
+  a.k = static_cast<uint16_t*>(k);
+  a.v = static_cast<uint16_t*>(v);
+  a.tokens = tokens;
+  a.slots = slots;
+  return from_cuda(launch_kv_load(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t mxfa_kv_attn_workspace_size(int R, int max_q, int Hq, int H) {
+  if (R < 0 || max_q < 0 || H <= 0 || Hq <= 0 || Hq % H) return 0;
+  return kv_attn_workspace(R, max_q, Hq / H);
+}
+
+mxfa_status mxfa_kv_attn(const mxfa_kv_cache* cache, const void* q, int64_t q_stride, int64_t total_q,
+                         const int32_t* cu_q, const int32_t* kv_lens, int R, const int32_t* block_table,
+                         int max_blocks, int max_q, int Hq, float softmax_scale, int causal, void* o,
+                         float* lse, void* ws, size_t ws_bytes, mxfa_stream_t stream) {
+  KvAttnArgs a;
+  memset(&a, 0, sizeof(a));
+  mxfa_status s = check_cache(cache, a.c);
+  if (s) return s;
+  if (!q || !cu_q || !kv_lens || !block_table || !o || !lse || !ws) return MXFA_ERR_INVALID_ARG;
+  if (total_q < 0 || R < 0 || max_blocks <= 0 || max_q < 0 || Hq <= 0 || Hq % a.c.H) return MXFA_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.0f) || !std::isfinite(softmax_scale)) return MXFA_ERR_INVALID_ARG;
+  if (total_q > 1 && q_stride < int64_t(Hq) * 128) return MXFA_ERR_INVALID_ARG;
+  if (total_q >= (int64_t(1) << 31) || total_q * Hq >= (int64_t(1) << 31) || R > (1 << 20) ||
+      int64_t(max_blocks) * a.c.page > (int64_t(1) << 30))
+    return MXFA_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(ws) || (total_q > 1 && q_stride % 8)) return MXFA_ERR_MISALIGNED;
+  if (!aligned4(cu_q) || !aligned4(kv_lens) || !aligned4(block_table) || !aligned4(lse)) return MXFA_ERR_MISALIGNED;
+  if (total_q == 0 || R == 0 || max_q == 0) return MXFA_OK;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_stride;
+  a.total_q = total_q;
+  a.cu_q = cu_q;
+  a.kv_lens = kv_lens;
+  a.R = R;
+  a.table = block_table;
+  a.width = max_blocks;
+  a.max_q = max_q < total_q ? max_q : int(total_q);
+  a.Hq = Hq;
+  a.G = Hq / a.c.H;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.causal = causal ? 1 : 0;
+  a.o = static_cast<uint16_t*>(o);
+  a.lse = lse;
+  a.ws = static_cast<uint8_t*>(ws);
+  if (ws_bytes < kv_attn_workspace(R, max_q, a.G)) return MXFA_ERR_WORKSPACE_TOO_SMALL;
+  return from_cuda(launch_kv_attn(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
 extern "C" {
 
 mxfa_status mxfa_tensor_peak_probe(int iters, int ctas, unsigned long long* cycles, mxfa_stream_t stream) {
@@ -749,7 +926,8 @@ mxfa_status mxfa_tensor_peak_probe(int iters, int ctas, unsigned long long* cycl
 mxfa_status mxfa_get_device_status(mxfa_stream_t stream, unsigned* flags) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(st) != cudaSuccess) return MXFA_ERR_CUDA;
-  unsigned f = read_status_quant(st) | read_status_fwd(st) | read_status_bwd(st) | read_status_gemm(st);
+  unsigned f = read_status_quant(st) | read_status_fwd(st) | read_status_bwd(st) | read_status_gemm(st) | read_status_kv(st) |
+               read_status_kv_attn(st);
   if (flags) *flags = f;
   if (f & 1u) return MXFA_ERR_TIMEOUT;
   if (f & 2u) return MXFA_ERR_DEVICE_INDEX;

@@ -186,10 +186,76 @@ cudaError_t launch_gemm_quant(const GemmArgs& a, cudaStream_t s);
 // Tensor-pipe peak probe: `ctas` CTAs of back-to-back MMAs, cycles per CTA.
 cudaError_t launch_mma_peak(int iters, int ctas, unsigned long long* cycles, cudaStream_t s);
 
+// ------------------------------------------------------------- 4-bit KV cache
+// Pages of one layer's cache (mxfa_kv_cache of the C ABI, checked).
+struct KvPages {
+  uint8_t *k, *v;                  // codes [blocks][H][page][64]
+  uint8_t *k_sf, *v_sf;            // block scales [blocks][H][page][4 or 8]
+  const float *k_scale, *v_scale;  // NVFP4: device fp32, the scale of the whole K or V cache
+  int64_t blocks;
+  int page, page_shift;            // rows of a page (a power of two) and its log2
+  int H;
+  int fmt;                         // 0 MXFP4, 1 NVFP4
+};
+
+struct KvPlanArgs {
+  const int32_t* ctx;   // [R] tokens cached before the step
+  const int32_t* add;   // [R] new tokens; < 0: the request is done
+  int R;
+  int32_t* table;       // [R][width]
+  int width;
+  int32_t* ring;        // free blocks
+  int64_t ring_size;
+  const int64_t* ring_in;
+  int64_t* ring_out;
+  int page_shift;
+  int64_t tokens;       // slots and positions to write
+  int32_t* cu_q;        // [R + 1]
+  int32_t* kv_lens;     // [R]
+  int64_t* slots;
+  int32_t* positions;
+  int aliased;          // kv_lens or ring_out is its own input
+};
+constexpr int kKvPlanMaxRequests = 16384;
+cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t s);
+
+struct KvRowsArgs {
+  KvPages c;
+  uint16_t *k, *v;              // bf16 rows; read by the store, written by the load
+  int64_t k_stride, v_stride;   // elements from one token to the next
+  int64_t tokens;
+  const int64_t* slots;
+};
+cudaError_t launch_kv_append(const KvRowsArgs& a, cudaStream_t s);
+cudaError_t launch_kv_load(const KvRowsArgs& a, cudaStream_t s);
+
+struct KvAttnArgs {
+  KvPages c;
+  const uint16_t* q;      // bf16 rows of Hq * 128, q_stride elements apart
+  int64_t q_stride;
+  int64_t total_q;
+  const int32_t* cu_q;    // [R + 1]
+  const int32_t* kv_lens; // [R]
+  int R;
+  const int32_t* table;   // [R][width]
+  int width;
+  int max_q;
+  int Hq, G;              // query heads, and per key head
+  float scale_log2;       // softmax scale * log2(e)
+  int causal;
+  uint16_t* o;            // bf16 [total_q][Hq][128]
+  float* lse;             // [Hq][total_q]
+  uint8_t* ws;
+};
+size_t kv_attn_workspace(int R, int max_q, int G);
+cudaError_t launch_kv_attn(const KvAttnArgs& a, cudaStream_t s);
+
 // Read (and clear) the device status words of every kernel module.
 unsigned read_status_quant(cudaStream_t s);
 unsigned read_status_gemm(cudaStream_t s);
 unsigned read_status_fwd(cudaStream_t s);
 unsigned read_status_bwd(cudaStream_t s);
+unsigned read_status_kv(cudaStream_t s);
+unsigned read_status_kv_attn(cudaStream_t s);
 
 }  // namespace mxfa

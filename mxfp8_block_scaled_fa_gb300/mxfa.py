@@ -19,9 +19,19 @@ A training step on bf16 q, k, v, do of shape [B * S, H, 128] (dense, causal):
 
 Jagged batches use ``Seqs.varlen(lengths, device)`` for queries and keys;
 ``o_mx=True`` / ``grads_mx=True`` also return O / the gradients as MXFP8.
+
+A serving step over a 4-bit cache (MXFP4 or NVFP4) of R requests, with the new
+tokens' q [T, Hq, 128] and k, v [T, H, 128] in request order:
+
+    cache = KvCache.empty(num_blocks, H, page=64)
+    free, state = kv_ring(num_blocks)
+    step = kv_plan(ctx_lens, new_lens, block_table, free, state, 64, T)
+    kv_append(cache, k, v, step.slots)
+    o, lse = kv_attention(q, cache, step.cu_q, step.kv_lens, block_table, max_q, scale)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -114,6 +124,13 @@ def lib() -> ctypes.CDLL:
             "mxfa_tensor_peak_probe": (I, [I, I, P, P]),
             "mxfa_bwd_noalloc": (I, [P, P, P, P, P, P, P, I, I, I, I, F, I, I, F, P, P, P, P]),
             "mxfa_bwd_noalloc_scratch_bytes": (S, []),
+            "mxfa_kv_codes_bytes": (S, [I64, I, I]),
+            "mxfa_kv_sf_bytes": (S, [I64, I, I, I]),
+            "mxfa_kv_plan": (I, [P, P, I, P, I, P, I64, P, P, I, I64, P, P, P, P, P]),
+            "mxfa_kv_append": (I, [P, P, P, I64, I64, I64, P, P]),
+            "mxfa_kv_load": (I, [P, P, I64, P, P, P]),
+            "mxfa_kv_attn_workspace_size": (S, [I, I, I, I]),
+            "mxfa_kv_attn": (I, [P, P, I64, I64, P, P, I, P, I, I, I, F, I, P, P, P, S, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -598,6 +615,261 @@ def gemm_quant(a: Mx, b: Mx, bf16: bool = True, row: bool = True, col: bool = Tr
     mxfa_gemm_quant(a.mx_in(), b.mx_in(), M, N, K, res.get("bf16"), outs.get("row"),
                     outs.get("col"), stream)
     return res
+
+
+# ------------------------------------------------------------------ 4-bit KV cache
+KV_MXFP4, KV_NVFP4 = 0, 1
+
+
+class KvPages(ctypes.Structure):
+    """mxfa_kv_cache: the device pointers and sizes of one layer's cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_sf", ctypes.c_void_p),
+                ("v_sf", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("num_blocks", ctypes.c_int64), ("page", ctypes.c_int), ("H", ctypes.c_int),
+                ("D", ctypes.c_int), ("fmt", ctypes.c_int)]
+
+
+def mxfa_kv_plan(ctx_lens, new_lens, R, block_table, max_blocks, free_ring, ring_size, ring_in,
+                 ring_out, page, tokens, cu_q, kv_lens, slots, positions, stream=None):
+    _check(lib().mxfa_kv_plan(_p(ctx_lens), _p(new_lens), R, _p(block_table), max_blocks,
+                              _p(free_ring), ring_size, _p(ring_in), _p(ring_out), page, tokens,
+                              _p(cu_q), _p(kv_lens), _p(slots), _p(positions), _stream(stream)),
+           "mxfa_kv_plan")
+
+
+def mxfa_kv_append(pages: KvPages, k, v, k_stride, v_stride, tokens, slots, stream=None):
+    _check(lib().mxfa_kv_append(ctypes.byref(pages), _p(k), _p(v), k_stride, v_stride, tokens,
+                                _p(slots), _stream(stream)), "mxfa_kv_append")
+
+
+def mxfa_kv_load(pages: KvPages, slots, tokens, k, v, stream=None):
+    _check(lib().mxfa_kv_load(ctypes.byref(pages), _p(slots), tokens, _p(k), _p(v),
+                              _stream(stream)), "mxfa_kv_load")
+
+
+def mxfa_kv_attn_workspace_size(R, max_q, Hq, H) -> int:
+    return int(lib().mxfa_kv_attn_workspace_size(R, max_q, Hq, H))
+
+
+def mxfa_kv_attn(pages: KvPages, q, q_stride, total_q, cu_q, kv_lens, R, block_table, max_blocks,
+                 max_q, Hq, scale, causal, o, lse, ws, ws_bytes, stream=None):
+    _check(lib().mxfa_kv_attn(ctypes.byref(pages), _p(q), q_stride, total_q, _p(cu_q), _p(kv_lens),
+                              R, _p(block_table), max_blocks, max_q, Hq, float(scale), int(causal),
+                              _p(o), _p(lse), _p(ws), ws_bytes, _stream(stream)), "mxfa_kv_attn")
+
+
+def _on(dev: torch.device, **tensors):
+    """Every tensor is on device `dev` (None passes)."""
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _flat(dtype, **tensors):
+    """Every tensor has this dtype and is contiguous."""
+    for name, t in tensors.items():
+        if t.dtype != dtype:
+            raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} is not contiguous")
+
+
+def _rows(name: str, x: torch.Tensor, heads: int):
+    """bf16 [tokens, heads, 128] with the heads of a token one after another -> elements
+    between tokens."""
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"{name} is {x.dtype}, expected torch.bfloat16")
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != 128:
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected [tokens, {heads}, 128]")
+    if x.shape[0] and (x.stride(2) != 1 or (heads > 1 and x.stride(1) != 128)):
+        raise ValueError(f"{name}: the heads of a token must lie one after another")
+    return x.stride(0) if x.shape[0] > 1 else heads * 128
+
+
+_same = contextlib.nullcontext()
+
+
+def _place(dev: torch.device, stream):
+    """The context in which a call on `dev` allocates and launches: its stream if one is given
+    (memory taken from the allocator then belongs to that stream), else the current one of `dev`."""
+    if dev.type != "cuda":
+        raise ValueError(f"the 4-bit cache lives on a CUDA device, not {dev}")
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        return torch.cuda.stream(stream)
+    return _same if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+@dataclass
+class KvCache:
+    """One layer's keys and values in 4 bits, in pages (layout: mxfa_kv_cache in mxfa.h)."""
+    k: torch.Tensor                    # uint8 [num_blocks, H, page, 64]
+    v: torch.Tensor
+    k_sf: torch.Tensor                 # uint8 [num_blocks, H, page, 4 (MXFP4) or 8 (NVFP4)]
+    v_sf: torch.Tensor
+    fmt: int
+    k_scale: Optional[torch.Tensor] = None   # NVFP4: fp32, one element
+    v_scale: Optional[torch.Tensor] = None
+
+    def __post_init__(self):
+        if self.fmt not in (KV_MXFP4, KV_NVFP4):
+            raise ValueError(f"unknown cache format {self.fmt}")
+        if self.k.dim() != 4:
+            raise ValueError("k and v must be [num_blocks, H, page, 64]")
+        n, h, page, _ = shape = self.k.shape
+        sf = (n, h, page, 4 if self.fmt == KV_MXFP4 else 8)
+        if shape != (n, h, page, 64) or self.v.shape != shape:
+            raise ValueError("k and v must be [num_blocks, H, page, 64]")
+        if self.k_sf.shape != sf or self.v_sf.shape != sf:
+            raise ValueError(f"k_sf and v_sf must be {list(sf)}")
+        _flat(torch.uint8, k=self.k, v=self.v, k_sf=self.k_sf, v_sf=self.v_sf)
+        if self.fmt == KV_NVFP4:
+            if self.k_scale is None or self.v_scale is None:
+                raise ValueError("an NVFP4 cache needs k_scale and v_scale")
+            _flat(torch.float32, k_scale=self.k_scale, v_scale=self.v_scale)
+            if self.k_scale.numel() != 1 or self.v_scale.numel() != 1:
+                raise ValueError("k_scale and v_scale have one element")
+        else:
+            self.k_scale = self.v_scale = None
+        _on(self.k.device, v=self.v, k_sf=self.k_sf, v_sf=self.v_sf, k_scale=self.k_scale,
+            v_scale=self.v_scale)
+        self.pages = KvPages(self.k.data_ptr(), self.v.data_ptr(), self.k_sf.data_ptr(),
+                             self.v_sf.data_ptr(), _p(self.k_scale), _p(self.v_scale), n, page, h,
+                             128, self.fmt)
+
+    @staticmethod
+    def empty(num_blocks: int, H: int, page: int = 64, fmt: int = KV_MXFP4, k_scale: float = 1.0,
+              v_scale: float = 1.0, device="cuda") -> "KvCache":
+        """A cache whose rows all read as zero.  k_scale and v_scale (NVFP4) are
+        about the largest magnitude to hold, over 448 * 6."""
+        codes, sf = (num_blocks, H, page, 64), (num_blocks, H, page, 4 if fmt == KV_MXFP4 else 8)
+        z = lambda shape: torch.zeros(shape, dtype=torch.uint8, device=device)
+        s = lambda x: torch.tensor([x], dtype=torch.float32, device=device) if fmt == KV_NVFP4 else None
+        return KvCache(z(codes), z(codes), z(sf), z(sf), fmt, s(k_scale), s(v_scale))
+
+
+@dataclass
+class KvStep:
+    """What kv_plan says about a step (mxfa_kv_plan in mxfa.h)."""
+    cu_q: torch.Tensor        # int32 [R + 1]
+    kv_lens: torch.Tensor     # int32 [R]
+    slots: torch.Tensor       # int64 [tokens]
+    positions: torch.Tensor   # int32 [tokens]
+    ring_state: torch.Tensor  # int64 [3]: taken, put, lacked
+
+
+def kv_ring(num_blocks: int, device="cuda"):
+    """The queue of free blocks of a new cache -> (free_ring, ring_state) for kv_plan."""
+    return (torch.arange(num_blocks, dtype=torch.int32, device=device),
+            torch.tensor([0, num_blocks, 0], dtype=torch.int64, device=device))
+
+
+def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
+            free_ring: torch.Tensor, ring_state: torch.Tensor, page: int, tokens: int,
+            out: Optional[KvStep] = None, stream=None) -> KvStep:
+    """The plan of a step from context lengths and counts of new tokens (int32 [R];
+    a negative count ends a request): writes new blocks into block_table (int32
+    [R, max_blocks]), gives the blocks of ended requests back to free_ring, and
+    returns offsets, lengths, and slot and position of `tokens` tokens.  `out`
+    gives the result's buffers; its kv_lens may be ctx_lens and its ring_state
+    may be ring_state, for a step that is captured once and replayed."""
+    R, dev = ctx_lens.numel(), ctx_lens.device
+    if new_lens.numel() != R or block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("ctx_lens, new_lens and block_table describe different numbers of requests")
+    with _place(dev, stream):
+        if out is None:
+            i32, i64 = dict(dtype=torch.int32, device=dev), dict(dtype=torch.int64, device=dev)
+            out = KvStep(torch.empty(R + 1, **i32), torch.empty(R, **i32), torch.empty(tokens, **i64),
+                         torch.empty(tokens, **i32), torch.empty(3, **i64))
+        elif (out.cu_q.numel(), out.kv_lens.numel(), out.slots.numel(), out.positions.numel()) != (
+                R + 1, R, tokens, tokens):
+            raise ValueError("out has buffers of other sizes")
+        if ring_state.numel() != 3 or out.ring_state.numel() != 3:
+            raise ValueError("ring_state has three elements")
+        _flat(torch.int32, ctx_lens=ctx_lens, new_lens=new_lens, block_table=block_table,
+              free_ring=free_ring, cu_q=out.cu_q, kv_lens=out.kv_lens, positions=out.positions)
+        _flat(torch.int64, ring_state=ring_state, slots=out.slots, ring_state_out=out.ring_state)
+        _on(dev, new_lens=new_lens, block_table=block_table, free_ring=free_ring,
+            ring_state=ring_state, cu_q=out.cu_q, kv_lens=out.kv_lens, slots=out.slots,
+            positions=out.positions, ring_state_out=out.ring_state)
+        mxfa_kv_plan(ctx_lens, new_lens, R, block_table, block_table.shape[1], free_ring,
+                     free_ring.numel(), ring_state, out.ring_state, page, tokens, out.cu_q,
+                     out.kv_lens, out.slots, out.positions, stream)
+    return out
+
+
+def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None):
+    """Quantizes bf16 k, v [tokens, H, 128] (tokens may be strided, as slices of a
+    fused projection are) into the cache rows `slots` (int64 [tokens], distinct;
+    negative: skipped)."""
+    H = cache.pages.H
+    ks, vs = _rows("k", k, H), _rows("v", v, H)
+    if v.shape[0] != k.shape[0] or slots.numel() != k.shape[0]:
+        raise ValueError("k, v and slots have different numbers of tokens")
+    _flat(torch.int64, slots=slots)
+    _on(cache.k.device, k=k, v=v, slots=slots)
+    with _place(cache.k.device, stream):
+        if k.shape[0]:
+            mxfa_kv_append(cache.pages, k, v, ks, vs, k.shape[0], slots, stream)
+
+
+def kv_load(cache: KvCache, slots: torch.Tensor, out=None, stream=None):
+    """The cached values of `slots` (int64 [tokens]) -> bf16 (k, v) [tokens, H, 128];
+    zeros for a negative slot."""
+    shape = (slots.numel(), cache.pages.H, 128)
+    dev = cache.k.device
+    with _place(dev, stream):
+        if out is None:
+            out = (torch.empty(shape, dtype=torch.bfloat16, device=dev),
+                   torch.empty(shape, dtype=torch.bfloat16, device=dev))
+        k, v = out
+        if k.shape != shape or v.shape != shape:
+            raise ValueError(f"out must be two tensors of shape {shape}")
+        _flat(torch.int64, slots=slots)
+        _flat(torch.bfloat16, k=k, v=v)
+        _on(dev, slots=slots, k=k, v=v)
+        if shape[0]:
+            mxfa_kv_load(cache.pages, slots, shape[0], k, v, stream)
+    return k, v
+
+
+def kv_attention(q: torch.Tensor, cache: KvCache, cu_q: torch.Tensor, kv_lens: torch.Tensor,
+                 block_table: torch.Tensor, max_q: int, scale: float, causal: bool = True,
+                 out=None, ws=None, stream=None):
+    """Attention of new query tokens over the cache -> (O bf16 [tokens, Hq, 128], lse
+    fp32 [Hq, tokens]).  q: bf16 [tokens, Hq, 128], tokens may be strided; cu_q
+    (int32 [R + 1]), kv_lens (int32 [R], new tokens included) and block_table as
+    kv_plan gives them; max_q: the most query tokens of a request.  causal aligns
+    the last query to the last key.  Rows outside cu_q's are not written."""
+    H, dev = cache.pages.H, cache.k.device
+    if q.dim() != 3 or q.shape[1] == 0 or q.shape[1] % H:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected [tokens, a multiple of {H}, 128]")
+    T, Hq, _ = q.shape
+    qs = _rows("q", q, Hq)
+    R = kv_lens.numel()
+    if cu_q.numel() != R + 1 or block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("cu_q, kv_lens and block_table describe different numbers of requests")
+    _flat(torch.int32, cu_q=cu_q, kv_lens=kv_lens, block_table=block_table)
+    with _place(dev, stream):
+        if out is None:
+            o = torch.empty((T, Hq, 128), dtype=torch.bfloat16, device=dev)
+            lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+        else:
+            o, lse = out
+            if o.shape != q.shape or lse.shape != (Hq, T):
+                raise ValueError(f"out must have shapes {tuple(q.shape)} and {(Hq, T)}")
+            _flat(torch.bfloat16, o=o)
+            _flat(torch.float32, lse=lse)
+        _on(dev, q=q, cu_q=cu_q, kv_lens=kv_lens, block_table=block_table, o=o, lse=lse, ws=ws)
+        if T == 0 or R == 0:
+            return o, lse
+        if ws is None:
+            ws = torch.empty(mxfa_kv_attn_workspace_size(R, max_q, Hq, H), dtype=torch.uint8,
+                             device=dev)
+        mxfa_kv_attn(cache.pages, q, qs, T, cu_q, kv_lens, R, block_table, block_table.shape[1], max_q,
+                     Hq, scale, causal, o, lse, ws, ws.numel() * ws.element_size(), stream)
+    return o, lse
 
 
 def device_status(stream=None) -> int:
