@@ -248,7 +248,7 @@ def within(go, gl, ref, n, vmax):
     np.testing.assert_array_equal(np.isneginf(gl), np.isneginf(rl))
     np.testing.assert_array_equal(np.isnan(gl), np.isnan(rl))
     fine = np.isfinite(rl)
-    assert (np.abs(gl - rl)[fine] <= (ds + 2.0 ** -22 * np.abs(rl))[fine]).all()
+    assert (np.abs(gl[fine] - rl[fine]) <= ds[fine] + 2.0 ** -22 * np.abs(rl[fine])).all()
 
 
 def compare(c, q, cu, slots, causal, scale, o, lse):
