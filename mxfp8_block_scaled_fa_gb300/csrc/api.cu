@@ -901,7 +901,7 @@ mxfa_status mxfa_kv_attn(const mxfa_kv_cache* cache, const void* q, int64_t q_st
   a.R = R;
   a.table = block_table;
   a.width = max_blocks;
-  a.max_q = max_q < total_q ? max_q : int(total_q);
+  a.max_q = max_q;
   a.Hq = Hq;
   a.G = Hq / a.c.H;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;

@@ -25,12 +25,15 @@
 // ring of asynchronous copies and its own softmax state, so warps never wait on
 // one another inside an item.
 //
-// Fragments.  m16n8k16 with the query rows as M.  The contraction order is free
-// as long as both operands agree, so a lane's K fragments over all of D are
-// the 32 consecutive channels (one 16-byte load, one MXFP4 block) of its key,
-// and Q is laid out to match; its V fragments are 16 consecutive channels of
-// four keys, two keys' codes merged into bytes before conversion so that the
-// pair (key, key + 1) comes out of one conversion.
+// Fragments.  m16n8k16 with sixteen keys (then sixteen channels) as M and eight
+// query rows as N, so that a group of up to eight heads fills the tensor core's
+// tile: S^T = K Q^T, O^T += V^T P^T, with P^T's fragment from S^T's by an 8x8
+// transpose (movmatrix).  The contraction order is free as long as both operands
+// agree, so a lane's K fragments over all of D are the 32 consecutive channels
+// (one 16-byte load, one MXFP4 block) of its key, and Q is laid out to match;
+// its V fragments are 16 consecutive channels of four keys, two keys' codes
+// merged into bytes before conversion so that the pair (key, key + 1) comes
+// out of one conversion.
 #include "mx_ptx.cuh"
 #include "mxfa_internal.h"
 
@@ -47,33 +50,31 @@ constexpr int kTile = kStep * kWarps;     // keys of one CTA step
 constexpr int kStages = 3;
 constexpr float kOffset = 8.0f;           // log2 offset of P
 constexpr float kLazy = 6.0f;             // growth of a row maximum that moves m
-constexpr int kCtasPerSm = 3;
+constexpr int kMaxNt = 4;                 // blocks of at most 32 query rows
 constexpr int kMinTiles = 4;              // least tiles of a run, as long as items are cut
+// CTAs of an SM for NT 8-row tiles: what 32 NT accumulator registers a thread allow
+__host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
 
 __host__ __device__ constexpr int sf_bytes(int fmt) { return fmt == 0 ? 4 : 8; }
 __host__ __device__ constexpr int stage_bytes(int fmt) { return kStep * 64 * 2 + kStep * sf_bytes(fmt) * 2; }
 
-// Merge layout: row r, quarter c (32 channels) at r * 144 + c * 36 floats, so that
-// the 128-bit stores of two rows' four lanes each fall on different banks.
-constexpr int kMergeRow = 144;
-__host__ __device__ constexpr int area_bytes(int fmt) {
-  const int ring = kWarps * kStages * stage_bytes(fmt);
-  const int merge = kWarps * 16 * kMergeRow * 4;
-  return ring > merge ? ring : merge;
+// Merge layout of eight rows: row r, channel d at r * 164 + (d / 16) * 20 + d % 16
+// floats, so that a quad's rows and two neighbours' channels fall on different banks.
+constexpr int kMergeRow = 164;
+__host__ __device__ constexpr int smem_bytes(int fmt, int nt) {
+  return kWarps * kStages * stage_bytes(fmt) + nt * 8 * 128 * 2 /* Q */ + kWarps * nt * 8 * 8 /* m, l */ + nt * 8 * 4 /* row scales */;
 }
-__host__ __device__ constexpr int smem_bytes(int fmt, int mt) {
-  return area_bytes(fmt) + mt * 16 * 128 * 2 /* Q */ + kWarps * mt * 16 * 8 /* m, l */ + mt * 16 * 4 /* row scales */;
-}
+static_assert(kWarps * 8 * kMergeRow * 4 <= kWarps * kStages * stage_bytes(0), "the merge area lies over the rings");
 
 // Workspace: per CTA of the grid a header and two partial records.
 struct Header {
   int r, rb, h;   // the item that begins in this CTA's run and ends behind it
   int parts;      // number of further CTAs that hold a part of it; 0: none
 };
-template <int MT>
+template <int NT>
 struct Partial {
-  float o[16 * MT][128];
-  float m[16 * MT], l[16 * MT];
+  float o[8 * NT][128];
+  float m[8 * NT], l[8 * NT];
 };
 __host__ __device__ inline size_t header_bytes(int ctas) { return (size_t(ctas) * sizeof(Header) + 255) & ~size_t(255); }
 
@@ -154,7 +155,13 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
   return r;
 }
 
-// Key (0..7) held by column n of an 8-key score tile.  The swap of the pairs 2, 3 and
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+
+// Key (0..7) held by row n of an 8-key score tile.  The swap of the pairs 2, 3 and
 // 6, 7 puts the four lanes of a quad on keys of both parities, so that their
 // 8-byte loads of V (64-byte rows, chunks swizzled by bit 2 of the key) cover all banks.
 __device__ __forceinline__ int key_of(int n) { return n ^ ((n >> 1) & 1); }
@@ -208,20 +215,21 @@ __device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t* warp_sums, int64
   return v;
 }
 
-// One warp's softmax state and work on its keys of an item.
-template <int FMT, int MT>
+// One warp's softmax state and work on its keys of an item.  Lane (c, g) = (lane % 4,
+// lane / 4) holds query rows 8 t + 2 c, + 1 and of them channels 16 g .. 16 g + 15.
+template <int FMT, int NT>
 struct Worker {
   static constexpr int kSf = sf_bytes(FMT);
   uint32_t ring;        // this warp's stages
   int lane, c, g;
-  float acc[MT][16][4];
-  float m[MT][2], l[MT][2];
+  float acc[NT][8][4];  // [.][j]: channels 16 g + 2 j (rows 2c, 2c + 1), 16 g + 2 j + 1 (the same)
+  float m[NT][2], l[NT][2];
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int t = 0; t < MT; t++) {
+    for (int t = 0; t < NT; t++) {
 #pragma unroll
-      for (int j = 0; j < 16; j++)
+      for (int j = 0; j < 8; j++)
 #pragma unroll
         for (int e = 0; e < 4; e++) acc[t][j][e] = 0.0f;
       m[t][0] = m[t][1] = -INFINITY;
@@ -229,137 +237,147 @@ struct Worker {
     }
   }
 
-  // Issue the copies of 32 keys from key0 on; `block` is the block of key
-  // key0 + lane (not `live`: the row is zero-filled and not visible).
-  __device__ __forceinline__ void copy(const KvPages& p, int stage, int key0, int h, int64_t block, bool live) {
+  // Issue the copies of 32 keys from key0 on.  Two lanes per key and pass, a 32-byte
+  // sector at a time; `block[i]` is the block of key key0 + 16 i + lane / 2 (not `live`:
+  // the row is zero-filled and not visible).
+  __device__ __forceinline__ void copy(const KvPages& p, int stage, int key0, int h, const int (&block)[2], const bool (&live)[2]) {
     const uint32_t s = ring + stage * stage_bytes(FMT);
-    const int64_t row = ((live ? block : 0) * p.H + h) * p.page + ((key0 + lane) & (p.page - 1));
+    const int half = lane & 1;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int64_t rr = __shfl_sync(0xFFFFFFFFu, row, i * 8 + (lane >> 2));
-      const bool ok = __shfl_sync(0xFFFFFFFFu, int(live), i * 8 + (lane >> 2)) != 0;
-      const uint32_t dst = s + (i * 8 + (lane >> 2)) * 64 + (((lane & 3) ^ ((lane >> 4) << 1)) << 4);
-      cp16(dst, p.k + rr * 64 + (lane & 3) * 16, ok);
-      cp16(dst + kStep * 64, p.v + rr * 64 + (lane & 3) * 16, ok);
+    for (int i = 0; i < 2; i++) {
+      const int key = 16 * i + (lane >> 1);
+      const int in_page = h * p.page + ((key0 + key) & (p.page - 1));
+      const uint64_t row = uint64_t(uint32_t(live[i] ? block[i] : 0)) * uint32_t(p.H * p.page) + uint32_t(in_page);
+      const uint8_t* k = p.k + row * 64 + half * 16;
+      const uint8_t* v = p.v + row * 64 + half * 16;
+      const int swz = ((key >> 2) & 1) << 1;
+      const uint32_t d0 = s + key * 64 + ((half ^ swz) << 4), d1 = s + key * 64 + (((2 + half) ^ swz) << 4);
+      cp16(d0, k, live[i]);
+      cp16(d1, k + 32, live[i]);
+      cp16(d0 + kStep * 64, v, live[i]);
+      cp16(d1 + kStep * 64, v + 32, live[i]);
+      cp_sf<kSf>(s + kStep * 128 + (half * kStep + key) * kSf, (half ? p.v_sf : p.k_sf) + row * kSf, live[i]);
     }
-    cp_sf<kSf>(s + kStep * 128 + lane * kSf, p.k_sf + row * kSf, live);
-    cp_sf<kSf>(s + kStep * 128 + kStep * kSf + lane * kSf, p.v_sf + row * kSf, live);
   }
 
-  // Scores, softmax and P V of the 32 keys in `stage`.  `seen` has a bit per key of
-  // the step; limit[t][i]: keys of the row that count, relative to the first (both
-  // only read if `masked`).
-  __device__ __forceinline__ void compute(int stage, uint32_t qs, const float (&cs)[MT][2], uint32_t seen, bool masked,
-                                          const int (&limit)[MT][2]) {
+  // Scores, softmax and P V of the 32 keys in `stage`.  MASKED: `seen` has a bit per key
+  // of the step, and limit[t][i] is the number of its keys that count for the row.
+  template <bool MASKED>
+  __device__ __forceinline__ void compute(int stage, uint32_t qs, const float (&cs)[NT][2], uint32_t seen,
+                                          const int (&limit)[NT][2]) {
     const uint32_t s = ring + stage * stage_bytes(FMT);
     const uint32_t sfk = s + kStep * 128, sfv = sfk + kStep * kSf;
-    float sc[MT][4][4];
+    const int kg = key_of(g);
+    float sc[NT][2][4];
 #pragma unroll
-    for (int t = 0; t < MT; t++)
+    for (int t = 0; t < NT; t++)
 #pragma unroll
-      for (int n = 0; n < 4; n++)
+      for (int u = 0; u < 2; u++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) sc[t][n][e] = 0.0f;
+        for (int e = 0; e < 4; e++) sc[t][u][e] = 0.0f;
     {
-      uint4 kw[4];
-      uint32_t ks[4][2];
-      const int kg = key_of(g);
+      uint32_t kw[2][2][4], ks[2][2][2];  // [16 keys][first or second eight][word or scale]
 #pragma unroll
-      for (int n = 0; n < 4; n++) {
-        const int key = n * 8 + kg;
-        kw[n] = lds16(s + key * 64 + ((c ^ (((kg >> 2) & 1) << 1)) << 4));
-        if (FMT == 0) {
-          const uint32_t b = lds_u8(sfk + key * 4 + c);
-          ks[n][0] = ks[n][1] = e8m0_pair(b, b);
-        } else {
-          const uint32_t b = e4m3_pair(lds_u16(sfk + key * 8 + 2 * c));
-          ks[n][0] = __byte_perm(b, b, 0x1010);
-          ks[n][1] = __byte_perm(b, b, 0x3232);
+      for (int u = 0; u < 2; u++)
+#pragma unroll
+        for (int x = 0; x < 2; x++) {
+          const int key = u * 16 + x * 8 + kg;
+          const uint4 w = lds16(s + key * 64 + ((c ^ (((kg >> 2) & 1) << 1)) << 4));
+          kw[u][x][0] = w.x, kw[u][x][1] = w.y, kw[u][x][2] = w.z, kw[u][x][3] = w.w;
+          if (FMT == 0) {
+            const uint32_t b = lds_u8(sfk + key * 4 + c);
+            ks[u][x][0] = ks[u][x][1] = e8m0_pair(b, b);
+          } else {
+            const uint32_t b = e4m3_pair(lds_u16(sfk + key * 8 + 2 * c));
+            ks[u][x][0] = __byte_perm(b, b, 0x1010);
+            ks[u][x][1] = __byte_perm(b, b, 0x3232);
+          }
         }
-      }
 #pragma unroll
       for (int w = 0; w < 4; w++) {
-        uint32_t a0[MT][4], a1[MT][4];
+        uint4 q[NT];
 #pragma unroll
-        for (int t = 0; t < MT; t++) {
-          const uint4 x = lds16(qs + ((t * 8 + 2 * w) * 32 + lane) * 16);
-          const uint4 y = lds16(qs + ((t * 8 + 2 * w + 1) * 32 + lane) * 16);
-          a0[t][0] = x.x, a0[t][1] = x.y, a0[t][2] = x.z, a0[t][3] = x.w;
-          a1[t][0] = y.x, a1[t][1] = y.y, a1[t][2] = y.z, a1[t][3] = y.w;
-        }
+        for (int t = 0; t < NT; t++) q[t] = lds16(qs + ((t * 4 + w) * 32 + lane) * 16);
 #pragma unroll
-        for (int n = 0; n < 4; n++) {
-          const uint32_t word = w == 0 ? kw[n].x : w == 1 ? kw[n].y : w == 2 ? kw[n].z : kw[n].w;
-          uint32_t hv[4];
-          e2m1x8_to_f16(word, hv);
+        for (int u = 0; u < 2; u++) {
+          uint32_t h0[4], h1[4];
+          e2m1x8_to_f16(kw[u][0][w], h0);
+          e2m1x8_to_f16(kw[u][1][w], h1);
 #pragma unroll
-          for (int i = 0; i < 4; i++) hv[i] = hmul2(hv[i], ks[n][w >> 1]);
+          for (int i = 0; i < 4; i++) {
+            h0[i] = hmul2(h0[i], ks[u][0][w >> 1]);
+            h1[i] = hmul2(h1[i], ks[u][1][w >> 1]);
+          }
+          const uint32_t a0[4] = {h0[0], h1[0], h0[1], h1[1]}, a1[4] = {h0[2], h1[2], h0[3], h1[3]};
 #pragma unroll
-          for (int t = 0; t < MT; t++) {
-            mma_f16(sc[t][n], a0[t], hv[0], hv[1]);
-            mma_f16(sc[t][n], a1[t], hv[2], hv[3]);
+          for (int t = 0; t < NT; t++) {
+            mma_f16(sc[t][u], a0, q[t].x, q[t].y);
+            mma_f16(sc[t][u], a1, q[t].z, q[t].w);
           }
         }
       }
     }
-    // scores in log2 units, masked
+    if (MASKED) {
 #pragma unroll
-    for (int t = 0; t < MT; t++)
+      for (int u = 0; u < 2; u++)
 #pragma unroll
-      for (int n = 0; n < 4; n++)
+        for (int x = 0; x < 2; x++) {
+          const int key = u * 16 + x * 8 + kg;
+          const bool there = (seen >> key) & 1u;
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-          float x = sc[t][n][e] * cs[t][e >> 1];
-          if (masked) {
-            const int key = n * 8 + key_of(2 * c + (e & 1));
-            if (!((seen >> key) & 1u) || key >= limit[t][e >> 1]) x = -INFINITY;
-          }
-          sc[t][n][e] = x;
+          for (int t = 0; t < NT; t++)
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+              if (!there || key >= limit[t][i]) sc[t][u][2 * x + i] = -INFINITY;
         }
-    uint32_t pf[MT][4][2];
+    }
+    // a row's maximum moves only where a score passes it by more than kLazy (and
+    // from -inf on), so its lanes are joined only then
     bool grow = false;
-    float top[MT][2];
+    float top[NT][2];
 #pragma unroll
-    for (int t = 0; t < MT; t++)
+    for (int t = 0; t < NT; t++)
 #pragma unroll
       for (int i = 0; i < 2; i++) {
-        float x = fmaxf(sc[t][0][2 * i], sc[t][0][2 * i + 1]);
-#pragma unroll
-        for (int n = 1; n < 4; n++) x = fmax3(x, sc[t][n][2 * i], sc[t][n][2 * i + 1]);
-        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
-        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
-        top[t][i] = x;
-        grow |= x > m[t][i] + kLazy;   // also from m = -inf on
+        top[t][i] = fmaxf(fmax3(sc[t][0][i], sc[t][0][2 + i], sc[t][1][i]), sc[t][1][2 + i]) * cs[t][i];
+        grow |= top[t][i] > m[t][i] + kLazy;
       }
     if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
-      for (int t = 0; t < MT; t++)
+      for (int t = 0; t < NT; t++)
 #pragma unroll
         for (int i = 0; i < 2; i++) {
-          if (top[t][i] > m[t][i] + kLazy) {
-            const float f = m[t][i] == -INFINITY ? 0.0f : ex2(m[t][i] - top[t][i]);
-            m[t][i] = top[t][i];
+          float x = top[t][i];
+#pragma unroll
+          for (int o = 4; o <= 16; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+          if (x > m[t][i] + kLazy) {
+            const float f = m[t][i] == -INFINITY ? 0.0f : ex2(m[t][i] - x);
+            m[t][i] = x;
             l[t][i] *= f;
 #pragma unroll
-            for (int j = 0; j < 16; j++) {
-              acc[t][j][2 * i] *= f;
-              acc[t][j][2 * i + 1] *= f;
+            for (int j = 0; j < 8; j++) {
+              acc[t][j][i] *= f;
+              acc[t][j][2 + i] *= f;
             }
           }
         }
     }
+    uint32_t pf[NT][2][2];  // P^T fragments: [16 keys][first or second eight]
 #pragma unroll
-    for (int t = 0; t < MT; t++)
+    for (int t = 0; t < NT; t++) {
+      const float off0 = m[t][0] == -INFINITY ? 0.0f : kOffset - m[t][0];
+      const float off1 = m[t][1] == -INFINITY ? 0.0f : kOffset - m[t][1];
 #pragma unroll
-      for (int i = 0; i < 2; i++) {
-        const float off = m[t][i] == -INFINITY ? 0.0f : kOffset - m[t][i];
+      for (int u = 0; u < 2; u++)
 #pragma unroll
-        for (int n = 0; n < 4; n++) {
-          const float p0 = ex2(sc[t][n][2 * i] + off), p1 = ex2(sc[t][n][2 * i + 1] + off);
-          l[t][i] += p0 + p1;
-          pf[t][n][i] = pack_f16(p0, p1);
+        for (int x = 0; x < 2; x++) {
+          const float p0 = ex2(fmaf(sc[t][u][2 * x], cs[t][0], off0));
+          const float p1 = ex2(fmaf(sc[t][u][2 * x + 1], cs[t][1], off1));
+          l[t][0] += p0;
+          l[t][1] += p1;
+          pf[t][u][x] = transpose8x8(pack_f16(p0, p1));
         }
-      }
+    }
     // V: a NaN block (scale byte 0xFF or 0x7F) reaches every row through 0 x NaN, so
     // where rows see different keys it is taken out of the product and put into the
     // rows that see its key
@@ -378,7 +396,7 @@ struct Worker {
         if (FMT == 0) {
           b0 = lds_u8(sfv + (key + ka) * 4 + (g >> 1));
           b1 = lds_u8(sfv + (key + kb) * 4 + (g >> 1));
-          if (masked) {
+          if (MASKED) {
             if (b0 == 0xFFu) b0 = 0;
             if (b1 == 0xFFu) b1 = 0;
           }
@@ -386,7 +404,7 @@ struct Worker {
         } else {
           b0 = lds_u8(sfv + (key + ka) * 8 + g);
           b1 = lds_u8(sfv + (key + kb) * 8 + g);
-          if (masked) {
+          if (MASKED) {
             if ((b0 & 0x7Fu) == 0x7Fu) b0 = 0;
             if ((b1 & 0x7Fu) == 0x7Fu) b1 = 0;
           }
@@ -395,75 +413,61 @@ struct Worker {
       }
 #pragma unroll
       for (int w = 0; w < 2; w++) {
-        uint32_t b0e[4], b0o[4], b1e[4], b1o[4];
+        uint32_t e0[4], o0[4], e1[4], o1[4];  // even and odd channels of the first and second eight keys
         {
           const uint32_t x = w ? va[0].y : va[0].x, y = w ? vb[0].y : vb[0].x;
-          e2m1x8_to_f16((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), b0e);
-          e2m1x8_to_f16(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), b0o);
+          e2m1x8_to_f16((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), e0);
+          e2m1x8_to_f16(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), o0);
         }
         {
           const uint32_t x = w ? va[1].y : va[1].x, y = w ? vb[1].y : vb[1].x;
-          e2m1x8_to_f16((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), b1e);
-          e2m1x8_to_f16(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), b1o);
+          e2m1x8_to_f16((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), e1);
+          e2m1x8_to_f16(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), o1);
         }
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-          const uint32_t e0 = hmul2(b0e[j], bs[0]), e1 = hmul2(b1e[j], bs[1]);
-          const uint32_t o0 = hmul2(b0o[j], bs[0]), o1 = hmul2(b1o[j], bs[1]);
+          const uint32_t a[4] = {hmul2(e0[j], bs[0]), hmul2(o0[j], bs[0]), hmul2(e1[j], bs[1]), hmul2(o1[j], bs[1])};
 #pragma unroll
-          for (int t = 0; t < MT; t++) {
-            const uint32_t pa[4] = {pf[t][2 * u][0], pf[t][2 * u][1], pf[t][2 * u + 1][0], pf[t][2 * u + 1][1]};
-            mma_f16(acc[t][w * 8 + 2 * j], pa, e0, e1);
-            mma_f16(acc[t][w * 8 + 2 * j + 1], pa, o0, o1);
-          }
+          for (int t = 0; t < NT; t++) mma_f16(acc[t][w * 4 + j], a, pf[t][u][0], pf[t][u][1]);
         }
       }
     }
-    if (masked) {
-      // this lane's accumulators: channels 32c .. 32c + 31 of its rows
+    if (MASKED) {
       const float nan = __uint_as_float(0x7FC00000u);
 #pragma unroll 1
       for (int key = 0; key < kStep; key++) {
-        bool lo, hi;  // NaN in channels 32c .. +15, 32c + 16 .. +31
-        if (FMT == 0) {
-          lo = hi = lds_u8(sfv + key * 4 + c) == 0xFFu;
-        } else {
-          const uint32_t b = lds_u16(sfv + key * 8 + 2 * c);
-          lo = (b & 0x7Fu) == 0x7Fu;
-          hi = (b & 0x7F00u) == 0x7F00u;
-        }
-        if (!(lo || hi) || !((seen >> key) & 1u)) continue;
+        bool bad;  // in channels 16 g .. + 15
+        if (FMT == 0) bad = lds_u8(sfv + key * 4 + (g >> 1)) == 0xFFu;
+        else bad = (lds_u8(sfv + key * 8 + g) & 0x7Fu) == 0x7Fu;
+        if (!bad || !((seen >> key) & 1u)) continue;
 #pragma unroll
-        for (int t = 0; t < MT; t++)
+        for (int t = 0; t < NT; t++)
 #pragma unroll
           for (int i = 0; i < 2; i++)
             if (key < limit[t][i]) {
 #pragma unroll
-              for (int j = 0; j < 16; j++) {
-                if (lo) acc[t][j][2 * i] = nan;
-                if (hi) acc[t][j][2 * i + 1] = nan;
-              }
+              for (int j = 0; j < 8; j++) acc[t][j][i] = acc[t][j][2 + i] = nan;
             }
       }
     }
   }
 };
 
-template <int FMT, int MT>
-__global__ void __launch_bounds__(kThreads, MT == 1 ? kCtasPerSm : 2) kv_attn_kernel(KvAttnArgs a) {
-  constexpr int ROWS = 16 * MT;
+template <int FMT, int NT>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAttnArgs a) {
+  constexpr int ROWS = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_scan[kWarps];
   __shared__ int64_t s_before;
   __shared__ int s_r;
-  uint8_t* s_q = smem + area_bytes(FMT);
+  uint8_t* s_q = smem + kWarps * kStages * stage_bytes(FMT);
   float* s_ml = reinterpret_cast<float*>(s_q + ROWS * 256);  // [warp][row][m, l]
   float* s_cs = s_ml + kWarps * ROWS * 2;
   float* s_merge = reinterpret_cast<float*>(smem);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   Header* headers = reinterpret_cast<Header*>(a.ws);
-  Partial<MT>* partials = reinterpret_cast<Partial<MT>*>(a.ws + header_bytes(gridDim.x));
+  Partial<NT>* partials = reinterpret_cast<Partial<NT>*>(a.ws + header_bytes(gridDim.x));
   if (tid == 0) headers[blockIdx.x].parts = 0;
 
   // the line of tiles and this CTA's run of it
@@ -496,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? kCtasPerSm : 2) kv_attn_ke
   int r = s_r;
   int64_t base = s_before;
 
-  Worker<FMT, MT> wk;
+  Worker<FMT, NT> wk;
   wk.ring = smem_u32(smem) + warp * kStages * stage_bytes(FMT);
   wk.lane = lane;
   wk.c = lane & 3;
@@ -520,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? kCtasPerSm : 2) kv_attn_ke
     const int nt = int(min(int64_t(tiles - t0), end - pos));
     const int row0 = rb * ROWS, rows = min(ROWS, x.n * a.G - row0);
     const int first_tok = row0 / a.G, last_tok = (row0 + rows - 1) / a.G;
-    // keys that some row of the block sees
+    // keys that some row of the block sees, and that all see
     const int keys = a.causal ? max(0, x.kv - x.n + last_tok + 1) : x.kv;
     const int all_see = a.causal ? x.kv - x.n + first_tok + 1 : x.kv;
     const int k_lo = t0 * kTile + warp * kStep;
@@ -528,30 +532,48 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? kCtasPerSm : 2) kv_attn_ke
     const int steps = k_lo < k_end ? (k_end - k_lo + kTile - 1) / kTile : 0;
     const int32_t* table = a.table + int64_t(r) * a.width;
 
-    auto block_of = [&](int step) -> int {
-      const int key = k_lo + step * kTile + lane;
-      return step < steps && key < k_end ? __ldg(table + (key >> a.c.page_shift)) : -1;
+    int nb[2];  // blocks of the next step to issue
+    auto look_up = [&](int step) {
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+        const int key = k_lo + step * kTile + 16 * i + (lane >> 1);
+        nb[i] = step < steps && key < k_end ? __ldg(table + (key >> a.c.page_shift)) : -1;
+      }
     };
-    uint32_t seen_ring[kStages];
-    auto issue = [&](int step, int stage, int block) {
-      const bool live = block >= 0 && block < a.c.blocks;
-      const int key0 = k_lo + step * kTile;
-      if (step < steps && key0 + lane < k_end && !live) atomicOr(&g_status_kv_attn, DEV_BAD_INDEX);
-      if (step < steps) wk.copy(a.c, stage, key0, h, block, live);
+    // copies of a step (none past the last), and a bit per visible key
+    auto issue = [&](int step, int stage) -> uint32_t {
+      uint32_t seen = 0;
+      if (step < steps) {
+        const int key0 = k_lo + step * kTile;
+        bool live[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+          live[i] = nb[i] >= 0 && nb[i] < a.c.blocks;
+          if (!live[i] && key0 + 16 * i + (lane >> 1) < k_end) atomicOr(&g_status_kv_attn, DEV_BAD_INDEX);
+        }
+        wk.copy(a.c, stage, key0, h, nb, live);
+        // lanes 2k and 2k + 1 speak for key k: all keys unless some are missing
+        const uint32_t b0 = __ballot_sync(0xFFFFFFFFu, live[0]), b1 = __ballot_sync(0xFFFFFFFFu, live[1]);
+        seen = 0xFFFFFFFFu;
+        if ((b0 & b1) != 0xFFFFFFFFu) {
+          const int k = lane & 15;
+          seen = __ballot_sync(0xFFFFFFFFu, ((lane < 16 ? b0 : b1) >> (2 * k)) & 1u);
+        }
+      }
       cp_commit();
-      return __ballot_sync(0xFFFFFFFFu, live);
+      return seen;
     };
-    int nb[kStages];
-#pragma unroll
-    for (int i = 0; i < kStages; i++) nb[i] = block_of(i);
-#pragma unroll
-    for (int i = 0; i < kStages - 1; i++) seen_ring[i] = issue(i, i, nb[i]);
-    int next_block = nb[kStages - 1];
+    static_assert(kStages == 3, "two steps in flight ahead of the one computed");
+    look_up(0);
+    uint32_t seen0 = issue(0, 0);
+    look_up(1);
+    uint32_t seen1 = issue(1, 1);
+    look_up(2);
 
     // Q of the item: binary16 with a power of two per row, in fragment order;
     // eight threads per row, 16 channels each
 #pragma unroll
-    for (int pass = 0; pass < MT; pass++) {
+    for (int pass = 0; pass < (ROWS * 8 + kThreads - 1) / kThreads; pass++) {
       const int i = pass * kThreads + tid;
       const int row = i >> 3, part = i & 7;
       uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
@@ -572,86 +594,86 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? kCtasPerSm : 2) kv_attn_ke
       const int fe = mx == 0 ? 127 : min(253, 268 - ex);
       const float f = __uint_as_float(uint32_t(fe) << 23);
       const float inv = __uint_as_float(uint32_t(254 - fe) << 23);
-      // channels 16 part + 0..15 belong to lane column c = part / 2, steps
-      // 4 (part % 2) .. + 3, four channels a step: pairs a0/a2 (rows g), a1/a3 (rows g + 8)
-      const int t = row >> 4, r16 = row & 15, cc = part >> 1;
+      // channels 16 part + 0..15 belong to lane column c = part / 2, contraction steps
+      // 4 (part % 2) .. + 3, four channels a step (b0, b1); a 16-byte word of lane
+      // (c, row % 8) holds two steps
+      if (row < ROWS) {
+        uint4* dst = reinterpret_cast<uint4*>(s_q) + ((row >> 3) * 4 + (part & 1) * 2) * 32 + (row & 7) * 4 + (part >> 1);
 #pragma unroll
-      for (int st = 0; st < 4; st++) {
-        const int ks = (part & 1) * 4 + st;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(s_q) + ((t * 8 + ks) * 32 + (r16 & 7) * 4 + cc) * 4 + (r16 >> 3);
-        dst[0] = pack_f16(bf_lo(w[2 * st]) * f, bf_hi(w[2 * st]) * f);
-        dst[2] = pack_f16(bf_lo(w[2 * st + 1]) * f, bf_hi(w[2 * st + 1]) * f);
+        for (int st = 0; st < 2; st++)
+          dst[st * 32] = make_uint4(pack_f16(bf_lo(w[4 * st]) * f, bf_hi(w[4 * st]) * f),
+                                    pack_f16(bf_lo(w[4 * st + 1]) * f, bf_hi(w[4 * st + 1]) * f),
+                                    pack_f16(bf_lo(w[4 * st + 2]) * f, bf_hi(w[4 * st + 2]) * f),
+                                    pack_f16(bf_lo(w[4 * st + 3]) * f, bf_hi(w[4 * st + 3]) * f));
+        // never 0: the score of a hidden key, -inf, is multiplied by it
+        if (part == 0) s_cs[row] = fmaxf(a.scale_log2 * kst * inv, 1.17549435e-38f);
       }
-      if (part == 0) s_cs[row] = a.scale_log2 * kst * inv;
     }
     __syncthreads();
-    float cs[MT][2];
-    int lim[MT][2];
+    float cs[NT][2];
+    int lim[NT][2];
 #pragma unroll
-    for (int t = 0; t < MT; t++)
+    for (int t = 0; t < NT; t++)
 #pragma unroll
       for (int i = 0; i < 2; i++) {
-        const int row = t * 16 + wk.g + 8 * i;
+        const int row = t * 8 + 2 * wk.c + i;
         cs[t][i] = s_cs[row];
         lim[t][i] = !a.causal || row >= rows ? x.kv : x.kv - x.n + (row0 + row) / a.G + 1;
       }
     wk.clear();
     const uint32_t qs = smem_u32(s_q);
-    for (int s0 = 0; s0 < steps; s0 += kStages) {
+    int stage = 0;
+#pragma unroll 1
+    for (int step = 0; step < steps; step++) {
+      // the stage of step - 1 is free: every lane has read it
+      __syncwarp();
+      const uint32_t seen2 = issue(step + 2, stage == 0 ? 2 : stage - 1);
+      look_up(step + 3);
+      cp_wait<kStages - 1>();
+      __syncwarp();
+      const int key0 = k_lo + step * kTile;
+      int limit[NT][2];
 #pragma unroll
-      for (int u = 0; u < kStages; u++) {
-        const int step = s0 + u;
-        if (step >= steps) break;
-        // the stage of step - 1 is free: every lane has read it
-        __syncwarp();
-        seen_ring[(u + kStages - 1) % kStages] = issue(step + kStages - 1, (u + kStages - 1) % kStages, next_block);
-        next_block = block_of(step + kStages);
-        cp_wait<kStages - 1>();
-        __syncwarp();
-        const int key0 = k_lo + step * kTile;
-        const uint32_t seen = seen_ring[u];
-        const bool masked = seen != 0xFFFFFFFFu || key0 + kStep > all_see;
-        int limit[MT][2];
+      for (int t = 0; t < NT; t++)
 #pragma unroll
-        for (int t = 0; t < MT; t++)
-#pragma unroll
-          for (int i = 0; i < 2; i++) limit[t][i] = lim[t][i] - key0;
-        wk.compute(u, qs, cs, seen, masked, limit);
-      }
+        for (int i = 0; i < 2; i++) limit[t][i] = lim[t][i] - key0;
+      if (seen0 != 0xFFFFFFFFu || key0 + kStep > all_see) wk.template compute<true>(stage, qs, cs, seen0, limit);
+      else wk.template compute<false>(stage, qs, cs, seen0, limit);
+      seen0 = seen1;
+      seen1 = seen2;
+      stage = stage == 2 ? 0 : stage + 1;
     }
     cp_wait<0>();
     // join the warps' states
 #pragma unroll
-    for (int t = 0; t < MT; t++)
+    for (int t = 0; t < NT; t++)
 #pragma unroll
       for (int i = 0; i < 2; i++) {
         float v = wk.l[t][i];
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
-        if (wk.c == 0) {
-          float* p = s_ml + (warp * ROWS + t * 16 + wk.g + 8 * i) * 2;
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        if (wk.g == 0) {
+          float* p = s_ml + (warp * ROWS + t * 8 + 2 * wk.c + i) * 2;
           p[0] = wk.m[t][i];
           p[1] = v;
         }
       }
     const bool head_part = t0 > 0, cut = t0 + nt < tiles;
-    Partial<MT>* part = &partials[2 * blockIdx.x + (head_part ? 0 : 1)];
+    Partial<NT>* part = &partials[2 * blockIdx.x + (head_part ? 0 : 1)];
 #pragma unroll
-    for (int t = 0; t < MT; t++) {
-      __syncthreads();  // the rings, or the previous sixteen rows, are no longer read
+    for (int t = 0; t < NT; t++) {
+      __syncthreads();  // the rings, or the previous eight rows, are no longer read
 #pragma unroll
       for (int i = 0; i < 2; i++) {
-        float* dst = s_merge + (warp * 16 + wk.g + 8 * i) * kMergeRow + wk.c * 36;
+        float* dst = s_merge + (warp * 8 + 2 * wk.c + i) * kMergeRow + wk.g * 20;
 #pragma unroll
-        for (int e = 0; e < 2; e++)
-#pragma unroll
-          for (int j = 0; j < 16; j += 4)
-            *reinterpret_cast<float4*>(dst + e * 16 + j) = make_float4(wk.acc[t][j][2 * i + e], wk.acc[t][j + 1][2 * i + e],
-                                                                       wk.acc[t][j + 2][2 * i + e], wk.acc[t][j + 3][2 * i + e]);
+        for (int j = 0; j < 8; j += 2)
+          *reinterpret_cast<float4*>(dst + 2 * j) =
+              make_float4(wk.acc[t][j][i], wk.acc[t][j][2 + i], wk.acc[t][j + 1][i], wk.acc[t][j + 1][2 + i]);
       }
       __syncthreads();
-      const int row = tid >> 3, col = (tid & 7) * 16;  // sixteen channels a thread
-      const int frow = t * 16 + row;
+      const int row = tid >> 4, col = (tid & 15) * 8;  // eight channels a thread
+      const int frow = t * 8 + row;
       float M = -INFINITY, L = 0.0f, w[kWarps];
 #pragma unroll
       for (int k = 0; k < kWarps; k++) M = fmaxf(M, s_ml[(k * ROWS + frow) * 2]);
@@ -662,14 +684,14 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? kCtasPerSm : 2) kv_attn_ke
         w[k] = mk == -INFINITY ? 1.0f : ex2(mk - M);
         L += w[k] * s_ml[(k * ROWS + frow) * 2 + 1];
       }
-      float o[16];
+      float o[8];
 #pragma unroll
-      for (int j = 0; j < 16; j++) o[j] = 0.0f;
+      for (int j = 0; j < 8; j++) o[j] = 0.0f;
 #pragma unroll
       for (int k = 0; k < kWarps; k++) {
-        const float* src = s_merge + (k * 16 + row) * kMergeRow + (col >> 5) * 36 + (col & 16);
+        const float* src = s_merge + (k * 8 + row) * kMergeRow + (col >> 4) * 20 + (col & 15);
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
+        for (int j = 0; j < 8; j += 4) {
           const float4 v = *reinterpret_cast<const float4*>(src + j);
           o[j] += w[k] * v.x;
           o[j + 1] += w[k] * v.y;
@@ -680,21 +702,19 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? kCtasPerSm : 2) kv_attn_ke
       if (frow < rows) {
         if (head_part || cut) {
 #pragma unroll
-          for (int j = 0; j < 16; j += 4)
+          for (int j = 0; j < 8; j += 4)
             *reinterpret_cast<float4*>(&part->o[frow][col + j]) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-          if ((tid & 7) == 0) {
+          if ((tid & 15) == 0) {
             part->m[frow] = M;
             part->l[frow] = L;
           }
         } else {
           const int rr = row0 + frow, tok = rr / a.G, hd = h * a.G + rr - tok * a.G;
           const float f = L == 0.0f ? 1.0f : vst / L;
-          uint4* dst = reinterpret_cast<uint4*>(a.o + (int64_t(x.q0 + tok) * a.Hq + hd) * 128 + col);
-#pragma unroll
-          for (int j = 0; j < 16; j += 8)
-            dst[j >> 3] = make_uint4(pack_bf16(o[j] * f, o[j + 1] * f), pack_bf16(o[j + 2] * f, o[j + 3] * f),
-                                     pack_bf16(o[j + 4] * f, o[j + 5] * f), pack_bf16(o[j + 6] * f, o[j + 7] * f));
-          if ((tid & 7) == 0)
+          *reinterpret_cast<uint4*>(a.o + (int64_t(x.q0 + tok) * a.Hq + hd) * 128 + col) =
+              make_uint4(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f), pack_bf16(o[4] * f, o[5] * f),
+                         pack_bf16(o[6] * f, o[7] * f));
+          if ((tid & 15) == 0)
             a.lse[int64_t(hd) * a.total_q + x.q0 + tok] =
                 L == 0.0f ? -INFINITY : (M - kOffset + log2f(L)) * 0.6931471805599453f;
         }
@@ -716,16 +736,16 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? kCtasPerSm : 2) kv_attn_ke
 
 // Joins the parts of the item that begins in CTA blockIdx.x's run and ends behind
 // it: one warp per row, four channels a lane, parts in the order of the keys.
-template <int FMT, int MT>
+template <int FMT, int NT>
 __global__ void __launch_bounds__(128) kv_join_kernel(KvAttnArgs a, int ctas) {
   const Header hd = reinterpret_cast<const Header*>(a.ws)[blockIdx.x];
   if (hd.parts == 0) return;
-  const Partial<MT>* partials = reinterpret_cast<const Partial<MT>*>(a.ws + header_bytes(ctas));
+  const Partial<NT>* partials = reinterpret_cast<const Partial<NT>*>(a.ws + header_bytes(ctas));
   const int row = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const Request x = request_of(a, hd.r);
-  const int rr = hd.rb * 16 * MT + row;
+  const int rr = hd.rb * 8 * NT + row;
   if (rr >= x.n * a.G) return;
-  auto part = [&](int i) -> const Partial<MT>& { return partials[2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)]; };
+  auto part = [&](int i) -> const Partial<NT>& { return partials[2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)]; };
   float M = -INFINITY;
   for (int i = lane; i <= hd.parts; i += 32) M = fmaxf(M, part(i).m[row]);
 #pragma unroll
@@ -734,7 +754,7 @@ __global__ void __launch_bounds__(128) kv_join_kernel(KvAttnArgs a, int ctas) {
   float4 s = make_float4(0, 0, 0, 0);
 #pragma unroll 4
   for (int i = 0; i <= hd.parts; i++) {
-    const Partial<MT>& p = part(i);
+    const Partial<NT>& p = part(i);
     const float m = p.m[row];
     const float w = m == -INFINITY ? 1.0f : ex2(m - M);  // without keys l and O are 0, or NaN
     const float4 v = *reinterpret_cast<const float4*>(&p.o[row][lane * 4]);
@@ -754,26 +774,44 @@ __global__ void __launch_bounds__(128) kv_join_kernel(KvAttnArgs a, int ctas) {
         L == 0.0f ? -INFINITY : (M - kOffset + log2f(L)) * 0.6931471805599453f;
 }
 
-template <int MT>
-size_t workspace(int ctas) {
-  return header_bytes(ctas) + size_t(ctas) * 2 * sizeof(Partial<MT>);
+// Tiles of eight query rows in a block: as few blocks of at most 32 rows as there
+// can be, of equal size (48 rows: two of 24).
+int row_tiles(int64_t rows) {
+  const int64_t blocks = (rows + 8 * kMaxNt - 1) / (8 * kMaxNt);
+  return int((rows + 8 * blocks - 1) / (8 * blocks));
 }
 
-template <int FMT, int MT>
+template <int NT>
+size_t workspace(int sms) {
+  const int ctas = sms * ctas_per_sm(NT);
+  return header_bytes(ctas) + size_t(ctas) * 2 * sizeof(Partial<NT>);
+}
+
+template <int FMT, int NT>
 cudaError_t launch(const KvAttnArgs& a, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  constexpr int bytes = smem_bytes(FMT, MT);
+  constexpr int bytes = smem_bytes(FMT, NT);
   cudaError_t e = once_per_device(done, [] {
-    return cudaFuncSetAttribute(kv_attn_kernel<FMT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    return cudaFuncSetAttribute(kv_attn_kernel<FMT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   });
   if (e != cudaSuccess) return e;
-  const int ctas = sm_count_current_device() * (MT == 1 ? kCtasPerSm : 2);
+  const int ctas = sm_count_current_device() * ctas_per_sm(NT);
   if (ctas <= 0) return cudaErrorInvalidDevice;
-  kv_attn_kernel<FMT, MT><<<ctas, kThreads, bytes, st>>>(a);
+  kv_attn_kernel<FMT, NT><<<ctas, kThreads, bytes, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  kv_join_kernel<FMT, MT><<<dim3(unsigned(ctas), 4 * MT), 128, 0, st>>>(a, ctas);
+  kv_join_kernel<FMT, NT><<<dim3(unsigned(ctas), 2 * NT), 128, 0, st>>>(a, ctas);
   return cudaGetLastError();
+}
+
+template <int FMT>
+cudaError_t launch_fmt(const KvAttnArgs& a, cudaStream_t st) {
+  switch (row_tiles(int64_t(a.max_q) * a.G)) {
+    case 1: return launch<FMT, 1>(a, st);
+    case 2: return launch<FMT, 2>(a, st);
+    case 3: return launch<FMT, 3>(a, st);
+    default: return launch<FMT, 4>(a, st);
+  }
 }
 
 }  // namespace kva
@@ -781,13 +819,17 @@ cudaError_t launch(const KvAttnArgs& a, cudaStream_t st) {
 size_t kv_attn_workspace(int R, int max_q, int G) {
   (void)R;
   const int sms = sm_count_current_device();
-  return int64_t(max_q) * G <= 16 ? kva::workspace<1>(sms * kva::kCtasPerSm) : kva::workspace<2>(sms * 2);
+  switch (kva::row_tiles(int64_t(max_q < 1 ? 1 : max_q) * G)) {
+    case 1: return kva::workspace<1>(sms);
+    case 2: return kva::workspace<2>(sms);
+    case 3: return kva::workspace<3>(sms);
+    default: return kva::workspace<4>(sms);
+  }
 }
 
 cudaError_t launch_kv_attn(const KvAttnArgs& a, cudaStream_t st) {
   clear_stale_error();
-  if (int64_t(a.max_q) * a.G <= 16) return a.c.fmt == 0 ? kva::launch<0, 1>(a, st) : kva::launch<1, 1>(a, st);
-  return a.c.fmt == 0 ? kva::launch<0, 2>(a, st) : kva::launch<1, 2>(a, st);
+  return a.c.fmt == 0 ? kva::launch_fmt<0>(a, st) : kva::launch_fmt<1>(a, st);
 }
 
 unsigned read_status_kv_attn(cudaStream_t st) {
