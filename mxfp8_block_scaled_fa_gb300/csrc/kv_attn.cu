@@ -22,7 +22,7 @@
 // finished there; one cut by a border leaves partial (m, l, O) records that a
 // second kernel joins in the order of the keys, so results do not depend on
 // timing.  Each of the CTA's four warps takes 32 of a tile's keys with its own
-// ring of asynchronous copies and its own softmax state, so warps never wait on
+// ring of bulk copies and its own softmax state, so warps never wait on
 // one another inside an item.
 //
 // Fragments.  m16n8k16 with sixteen keys (then sixteen channels) as M and eight
@@ -43,16 +43,17 @@ static __device__ unsigned g_status_kv_attn;
 
 namespace kva {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 32;                 // keys of one warp step
-constexpr int kTile = kStep * kWarps;     // keys of one CTA step
+constexpr int kTile = 128;                // keys of one CTA step, by which work is counted and cut
 constexpr int kStages = 3;
 constexpr float kOffset = 8.0f;           // log2 offset of P
 constexpr float kLazy = 6.0f;             // growth of a row maximum that moves m
 constexpr int kMaxNt = 4;                 // blocks of at most 32 query rows
 constexpr int kMinTiles = 4;              // least tiles of a run, as long as items are cut
-// CTAs of an SM for NT 8-row tiles: what 32 NT accumulator registers a thread allow
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+// CTAs of an SM for NT 8-row tiles: 16, 12 or 8 warps, as 32 NT accumulator registers
+// a thread allow.
 __host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
 
 __host__ __device__ constexpr int sf_bytes(int fmt) { return fmt == 0 ? 4 : 8; }
@@ -61,10 +62,16 @@ __host__ __device__ constexpr int stage_bytes(int fmt) { return kStep * 64 * 2 +
 // Merge layout of eight rows: row r, channel d at r * 164 + (d / 16) * 20 + d % 16
 // floats, so that a quad's rows and two neighbours' channels fall on different banks.
 constexpr int kMergeRow = 164;
+constexpr int merge_bytes = kWarps * 8 * kMergeRow * 4;
+// Q's fragments of one tile of eight rows live in registers (staged through a ring
+// at the start of an item), those of more tiles in shared memory.  Row scales, and the
+// warps' m and l behind the merge area, complete it: 57,328 bytes for NVFP4 and NT = 1, of
+// which four CTAs fit an SM.
+__host__ __device__ constexpr int ring_bytes(int fmt) { return kWarps * kStages * stage_bytes(fmt); }
 __host__ __device__ constexpr int smem_bytes(int fmt, int nt) {
-  return kWarps * kStages * stage_bytes(fmt) + nt * 8 * 128 * 2 /* Q */ + kWarps * nt * 8 * 8 /* m, l */ + nt * 8 * 4 /* row scales */;
+  return ring_bytes(fmt) + (nt > 1 ? nt * 8 * 128 * 2 : 0) + nt * 8 * 4;
 }
-static_assert(kWarps * 8 * kMergeRow * 4 <= kWarps * kStages * stage_bytes(0), "the merge area lies over the rings");
+static_assert(merge_bytes + kWarps * kMaxNt * 8 * 8 <= ring_bytes(0), "merge area, m and l lie over the rings");
 
 // Workspace: per CTA of the grid a header and two partial records.
 struct Header {
@@ -77,19 +84,6 @@ struct Partial {
   float m[8 * NT], l[8 * NT];
 };
 __host__ __device__ inline size_t header_bytes(int ctas) { return (size_t(ctas) * sizeof(Header) + 255) & ~size_t(255); }
-
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_sf(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(live ? N : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -162,8 +156,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
 }
 
 // Key (0..7) held by row n of an 8-key score tile.  The swap of the pairs 2, 3 and
-// 6, 7 puts the four lanes of a quad on keys of both parities, so that their
-// 8-byte loads of V (64-byte rows, chunks swizzled by bit 2 of the key) cover all banks.
+// 6, 7 puts the four lanes of a quad on keys of both parities, which halves the bank
+// conflicts of their 8-byte loads of V (64-byte rows).
 __device__ __forceinline__ int key_of(int n) { return n ^ ((n >> 1) & 1); }
 
 struct Request {
@@ -224,6 +218,7 @@ struct Worker {
   int lane, c, g;
   float acc[NT][8][4];  // [.][j]: channels 16 g + 2 j (rows 2c, 2c + 1), 16 g + 2 j + 1 (the same)
   float m[NT][2], l[NT][2];
+  uint4 qf[NT == 1 ? 4 : 1];  // Q's fragments of one tile
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -237,27 +232,22 @@ struct Worker {
     }
   }
 
-  // Issue the copies of 32 keys from key0 on.  Two lanes per key and pass, a 32-byte
-  // sector at a time; `block[i]` is the block of key key0 + 16 i + lane / 2 (not `live`:
-  // the row is zero-filled and not visible).
-  __device__ __forceinline__ void copy(const KvPages& p, int stage, int key0, int h, const int (&block)[2], const bool (&live)[2]) {
-    const uint32_t s = ring + stage * stage_bytes(FMT);
-    const int half = lane & 1;
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-      const int key = 16 * i + (lane >> 1);
-      const int in_page = h * p.page + ((key0 + key) & (p.page - 1));
-      const uint64_t row = uint64_t(uint32_t(live[i] ? block[i] : 0)) * uint32_t(p.H * p.page) + uint32_t(in_page);
-      const uint8_t* k = p.k + row * 64 + half * 16;
-      const uint8_t* v = p.v + row * 64 + half * 16;
-      const int swz = ((key >> 2) & 1) << 1;
-      const uint32_t d0 = s + key * 64 + ((half ^ swz) << 4), d1 = s + key * 64 + (((2 + half) ^ swz) << 4);
-      cp16(d0, k, live[i]);
-      cp16(d1, k + 32, live[i]);
-      cp16(d0 + kStep * 64, v, live[i]);
-      cp16(d1 + kStep * 64, v + 32, live[i]);
-      cp_sf<kSf>(s + kStep * 128 + (half * kStep + key) * kSf, (half ? p.v_sf : p.k_sf) + row * kSf, live[i]);
-    }
+  // Copies.  Rows of a block lie one after another, so the 32 keys of a step are one
+  // run of each of K, V and their scales, or two where pages have 16 rows: lane
+  // 4 i + j < 4 runs brings run i of kind j (K, V, K scales, V scales) with one bulk copy,
+  // its address the lane's base plus block times the bytes of a block.  A warp's
+  // steps lie kTile keys apart, a multiple of every page size, so the place in the
+  // page stays the same for all steps of an item.
+  const uint8_t* src;         // kind's array + place in the page
+  uint32_t block_bytes, dst, bytes;
+  __device__ __forceinline__ void aim(const KvPages& p, int key0, int h) {
+    const int kind = lane & 3, run = (lane >> 2) & 1;
+    const int row_bytes = kind < 2 ? 64 : kSf;
+    const uint8_t* base = kind == 0 ? p.k : kind == 1 ? p.v : kind == 2 ? p.k_sf : p.v_sf;
+    block_bytes = uint32_t(p.H * p.page * row_bytes);
+    src = base + (h * p.page + ((key0 + 16 * run) & (p.page - 1))) * row_bytes;
+    bytes = (p.page == 16 ? 16 : kStep) * row_bytes;
+    dst = ring + (kind == 0 ? 0 : kind == 1 ? kStep * 64 : kStep * 128 + (kind - 2) * kStep * kSf) + 16 * run * row_bytes;
   }
 
   // Scores, softmax and P V of the 32 keys in `stage`.  MASKED: `seen` has a bit per key
@@ -282,7 +272,7 @@ struct Worker {
 #pragma unroll
         for (int x = 0; x < 2; x++) {
           const int key = u * 16 + x * 8 + kg;
-          const uint4 w = lds16(s + key * 64 + ((c ^ (((kg >> 2) & 1) << 1)) << 4));
+          const uint4 w = lds16(s + key * 64 + (c << 4));
           kw[u][x][0] = w.x, kw[u][x][1] = w.y, kw[u][x][2] = w.z, kw[u][x][3] = w.w;
           if (FMT == 0) {
             const uint32_t b = lds_u8(sfk + key * 4 + c);
@@ -297,7 +287,7 @@ struct Worker {
       for (int w = 0; w < 4; w++) {
         uint4 q[NT];
 #pragma unroll
-        for (int t = 0; t < NT; t++) q[t] = lds16(qs + ((t * 4 + w) * 32 + lane) * 16);
+        for (int t = 0; t < NT; t++) q[t] = NT == 1 ? qf[NT == 1 ? w : 0] : lds16(qs + ((t * 4 + w) * 32 + lane) * 16);
 #pragma unroll
         for (int u = 0; u < 2; u++) {
           uint32_t h0[4], h1[4];
@@ -380,8 +370,7 @@ struct Worker {
     }
     // V: a NaN block (scale byte 0xFF or 0x7F) reaches every row through 0 x NaN, so
     // where rows see different keys it is taken out of the product and put into the
-    // rows that see its key
-    const uint32_t vrow = ((((g >> 1) ^ (((c >> 1) & 1) << 1)) << 4) + ((g & 1) << 3));
+    // rows that see its key; so are rows that are no keys and may hold anything
     const int ka = key_of(2 * c), kb = key_of(2 * c + 1);
 #pragma unroll
     for (int u = 0; u < 2; u++) {
@@ -390,23 +379,23 @@ struct Worker {
 #pragma unroll
       for (int x = 0; x < 2; x++) {
         const int key = (2 * u + x) * 8;
-        va[x] = lds8(s + kStep * 64 + (key + ka) * 64 + vrow);
-        vb[x] = lds8(s + kStep * 64 + (key + kb) * 64 + vrow);
+        va[x] = lds8(s + kStep * 64 + (key + ka) * 64 + g * 8);
+        vb[x] = lds8(s + kStep * 64 + (key + kb) * 64 + g * 8);
         uint32_t b0, b1;
         if (FMT == 0) {
           b0 = lds_u8(sfv + (key + ka) * 4 + (g >> 1));
           b1 = lds_u8(sfv + (key + kb) * 4 + (g >> 1));
           if (MASKED) {
-            if (b0 == 0xFFu) b0 = 0;
-            if (b1 == 0xFFu) b1 = 0;
+            if (b0 == 0xFFu || !((seen >> (key + ka)) & 1u)) b0 = 0;
+            if (b1 == 0xFFu || !((seen >> (key + kb)) & 1u)) b1 = 0;
           }
           bs[x] = e8m0_pair(b0, b1);
         } else {
           b0 = lds_u8(sfv + (key + ka) * 8 + g);
           b1 = lds_u8(sfv + (key + kb) * 8 + g);
           if (MASKED) {
-            if ((b0 & 0x7Fu) == 0x7Fu) b0 = 0;
-            if ((b1 & 0x7Fu) == 0x7Fu) b1 = 0;
+            if ((b0 & 0x7Fu) == 0x7Fu || !((seen >> (key + ka)) & 1u)) b0 = 0;
+            if ((b1 & 0x7Fu) == 0x7Fu || !((seen >> (key + kb)) & 1u)) b1 = 0;
           }
           bs[x] = e4m3_pair(b0 | (b1 << 8));
         }
@@ -459,46 +448,67 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_scan[kWarps];
   __shared__ int64_t s_before;
-  __shared__ int s_r;
-  uint8_t* s_q = smem + kWarps * kStages * stage_bytes(FMT);
-  float* s_ml = reinterpret_cast<float*>(s_q + ROWS * 256);  // [warp][row][m, l]
-  float* s_cs = s_ml + kWarps * ROWS * 2;
+  __shared__ __align__(8) uint64_t s_bar[kWarps * kStages];
+  __shared__ int s_r, s_abort;
+  float* s_cs = reinterpret_cast<float*>(smem + ring_bytes(FMT));
+  uint8_t* s_q = NT > 1 ? smem + ring_bytes(FMT) + ROWS * 4 : smem + 2 * stage_bytes(FMT);  // NT = 1: warp 0's last stage
   float* s_merge = reinterpret_cast<float*>(smem);
+  float* s_ml = reinterpret_cast<float*>(smem + merge_bytes);  // [warp][row][m, l]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t bars = smem_u32(s_bar) + warp * kStages * 8;
+  if (lane == 0) {
+    for (int i = 0; i < kStages; i++) mbar_init(bars + 8 * i, 1);
+    fence_mbar_init();
+  }
+  if (tid == 0) s_abort = 0;
   Header* headers = reinterpret_cast<Header*>(a.ws);
   Partial<NT>* partials = reinterpret_cast<Partial<NT>*>(a.ws + header_bytes(gridDim.x));
-  if (tid == 0) headers[blockIdx.x].parts = 0;
 
-  // the line of tiles and this CTA's run of it
-  int64_t total = 0;
-  for (int r0 = 0; r0 < a.R; r0 += kThreads) {
-    int64_t sum;
-    cta_scan(r0 + tid < a.R ? request_tiles<ROWS>(a, r0 + tid) : 0, s_scan, sum);
-    total += sum;
-  }
-  const int64_t most = (total + kMinTiles - 1) / kMinTiles;
-  const int64_t C = most < int64_t(gridDim.x) ? most : int64_t(gridDim.x);
-  if (int64_t(blockIdx.x) >= C) return;
-  const int64_t start = total * blockIdx.x / C, end = total * (blockIdx.x + 1) / C;
-  if (start == end) return;
-  {
-    int64_t before = 0;
+  // the line of tiles and this CTA's run of it; or, where all contexts are short,
+  // whole items one after another
+  int64_t total = 0, C = 0, pos = 0, end = 0, base = 0;
+  int r = 0;
+  if (a.whole) {
+    end = int64_t(a.R) * a.c.H;
+    pos = blockIdx.x;
+    __syncthreads();
+  } else {
+    if (tid == 0) headers[blockIdx.x].parts = 0;
+    int64_t first_own = 0, first_upto = 0;  // of the first kThreads requests, the only ones most often
     for (int r0 = 0; r0 < a.R; r0 += kThreads) {
       int64_t sum;
       const int64_t own = r0 + tid < a.R ? request_tiles<ROWS>(a, r0 + tid) : 0;
-      const int64_t upto = before + cta_scan(own, s_scan, sum);
-      if (upto - own <= start && start < upto) {
+      const int64_t upto = cta_scan(own, s_scan, sum);
+      if (r0 == 0) {
+        first_own = own;
+        first_upto = upto;
+      }
+      total += sum;
+    }
+    const int64_t most = (total + kMinTiles - 1) / kMinTiles;
+    C = most < int64_t(gridDim.x) ? most : int64_t(gridDim.x);
+    if (int64_t(blockIdx.x) >= C) return;
+    pos = total * blockIdx.x / C, end = total * (blockIdx.x + 1) / C;
+    if (pos == end) return;
+    int64_t before = 0;
+    for (int r0 = 0; r0 < a.R; r0 += kThreads) {
+      int64_t sum = total, own = first_own, upto = first_upto;
+      if (a.R > kThreads) {
+        own = r0 + tid < a.R ? request_tiles<ROWS>(a, r0 + tid) : 0;
+        upto = before + cta_scan(own, s_scan, sum);
+      }
+      if (upto - own <= pos && pos < upto) {
         s_r = r0 + tid;
         s_before = upto - own;
       }
       before += sum;
-      if (start < before) break;
+      if (pos < before) break;
     }
+    __syncthreads();
+    r = s_r;
+    base = s_before;
   }
-  __syncthreads();
-  int r = s_r;
-  int64_t base = s_before;
 
   Worker<FMT, NT> wk;
   wk.ring = smem_u32(smem) + warp * kStages * stage_bytes(FMT);
@@ -507,21 +517,34 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
   wk.g = lane >> 2;
   const float kst = FMT == 1 ? __ldg(a.c.k_scale) : 1.0f;
   const float vst = FMT == 1 ? __ldg(a.c.v_scale) : 1.0f;
+  uint32_t phases = 0;  // bit i: phase of stage i
 
-  for (int64_t pos = start; pos < end && r < a.R;) {
-    const Request x = request_of(a, r);
-    const int tiles = tiles_of(x);
-    const int nrb = (x.n * a.G + ROWS - 1) / ROWS;
-    const int64_t all = x.n == 0 ? 0 : int64_t(nrb) * a.c.H * tiles;
-    if (pos >= base + all) {
-      base += all;
-      r++;
-      continue;
+  while (pos < end && r < a.R) {
+    int rb, h, t0, nt, tiles, item = 0;
+    if (a.whole) {
+      r = int(pos / a.c.H);
+      rb = 0, h = int(pos - int64_t(r) * a.c.H);
     }
-    const int64_t local = pos - base;
-    const int item = int(local / tiles), t0 = int(local - int64_t(item) * tiles);
-    const int rb = item / a.c.H, h = item - rb * a.c.H;
-    const int nt = int(min(int64_t(tiles - t0), end - pos));
+    const Request x = request_of(a, r);
+    tiles = tiles_of(x);
+    if (a.whole) {
+      pos += gridDim.x;
+      if (x.n == 0) continue;
+      t0 = 0, nt = tiles;
+    } else {
+      const int nrb = (x.n * a.G + ROWS - 1) / ROWS;
+      const int64_t all = x.n == 0 ? 0 : int64_t(nrb) * a.c.H * tiles;
+      if (pos >= base + all) {
+        base += all;
+        r++;
+        continue;
+      }
+      const int64_t local = pos - base;
+      item = int(local / tiles), t0 = int(local - int64_t(item) * tiles);
+      rb = item / a.c.H, h = item - rb * a.c.H;
+      nt = int(min(int64_t(tiles - t0), end - pos));
+      pos += nt;
+    }
     const int row0 = rb * ROWS, rows = min(ROWS, x.n * a.G - row0);
     const int first_tok = row0 / a.G, last_tok = (row0 + rows - 1) / a.G;
     // keys that some row of the block sees, and that all see
@@ -530,37 +553,29 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
     const int k_lo = t0 * kTile + warp * kStep;
     const int k_end = min((t0 + nt) * kTile, keys);
     const int steps = k_lo < k_end ? (k_end - k_lo + kTile - 1) / kTile : 0;
+    // copies: the lane's run of a step, looked up one step ahead
     const int32_t* table = a.table + int64_t(r) * a.width;
-
-    int nb[2];  // blocks of the next step to issue
+    const int run_key = k_lo + 16 * ((lane >> 2) & 1);
+    const bool copies = lane < (a.c.page == 16 ? 8 : 4);
+    wk.aim(a.c, k_lo, h);
+    int block;
     auto look_up = [&](int step) {
-#pragma unroll
-      for (int i = 0; i < 2; i++) {
-        const int key = k_lo + step * kTile + 16 * i + (lane >> 1);
-        nb[i] = step < steps && key < k_end ? __ldg(table + (key >> a.c.page_shift)) : -1;
-      }
+      const int key = run_key + step * kTile;
+      block = copies && step < steps && key < k_end ? __ldg(table + (key >> a.c.page_shift)) : -1;
     };
-    // copies of a step (none past the last), and a bit per visible key
-    auto issue = [&](int step, int stage) -> uint32_t {
-      uint32_t seen = 0;
-      if (step < steps) {
-        const int key0 = k_lo + step * kTile;
-        bool live[2];
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-          live[i] = nb[i] >= 0 && nb[i] < a.c.blocks;
-          if (!live[i] && key0 + 16 * i + (lane >> 1) < k_end) atomicOr(&g_status_kv_attn, DEV_BAD_INDEX);
-        }
-        wk.copy(a.c, stage, key0, h, nb, live);
-        // lanes 2k and 2k + 1 speak for key k: all keys unless some are missing
-        const uint32_t b0 = __ballot_sync(0xFFFFFFFFu, live[0]), b1 = __ballot_sync(0xFFFFFFFFu, live[1]);
-        seen = 0xFFFFFFFFu;
-        if ((b0 & b1) != 0xFFFFFFFFu) {
-          const int k = lane & 15;
-          seen = __ballot_sync(0xFFFFFFFFu, ((lane < 16 ? b0 : b1) >> (2 * k)) & 1u);
-        }
-      }
-      cp_commit();
+    // starts the copies of a step (none past the last) and returns a bit per visible key
+    auto issue = [&](int step, int st) -> uint32_t {
+      if (step >= steps) return 0;
+      const int key0 = k_lo + step * kTile;
+      const bool live = block >= 0 && block < a.c.blocks;
+      if (copies && !live && run_key + step * kTile < k_end) atomicOr(&g_status_kv_attn, DEV_BAD_INDEX);
+      const uint32_t runs = __ballot_sync(0xFFFFFFFFu, live);
+      if (lane == 0)
+        mbar_arrive_expect_tx(bars + 8 * st, __popc(runs & 0x11u) * ((a.c.page == 16 ? 16 : kStep) * (128 + 2 * sf_bytes(FMT))));
+      if (live)
+        bulk_load(wk.dst + st * stage_bytes(FMT), wk.src + uint64_t(uint32_t(block)) * wk.block_bytes, wk.bytes, bars + 8 * st);
+      uint32_t seen = a.c.page == 16 ? ((runs & 1u) ? 0x0000FFFFu : 0u) | ((runs & 16u) ? 0xFFFF0000u : 0u) : (runs & 1u) ? 0xFFFFFFFFu : 0u;
+      if (k_end - key0 < kStep) seen &= (1u << (k_end - key0)) - 1u;
       return seen;
     };
     static_assert(kStages == 3, "two steps in flight ahead of the one computed");
@@ -571,7 +586,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
     look_up(2);
 
     // Q of the item: binary16 with a power of two per row, in fragment order;
-    // eight threads per row, 16 channels each
+    // eight threads per row, 16 channels each (NT = 1: through warp 0's third
+    // stage, which is free now)
 #pragma unroll
     for (int pass = 0; pass < (ROWS * 8 + kThreads - 1) / kThreads; pass++) {
       const int i = pass * kThreads + tid;
@@ -622,15 +638,21 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
       }
     wk.clear();
     const uint32_t qs = smem_u32(s_q);
-    int stage = 0;
+    if (NT == 1) {
+#pragma unroll
+      for (int w = 0; w < 4; w++) wk.qf[NT == 1 ? w : 0] = lds16(qs + (w * 32 + lane) * 16);
+      fence_async_smem();
+      __syncthreads();  // the stage is free for copies
+    }
+    int stage = 0;  // every item begins with stage 0
 #pragma unroll 1
     for (int step = 0; step < steps; step++) {
       // the stage of step - 1 is free: every lane has read it
       __syncwarp();
       const uint32_t seen2 = issue(step + 2, stage == 0 ? 2 : stage - 1);
       look_up(step + 3);
-      cp_wait<kStages - 1>();
-      __syncwarp();
+      mbar_wait(bars + 8 * stage, (phases >> stage) & 1u, &s_abort, &g_status_kv_attn);
+      phases ^= 1u << stage;
       const int key0 = k_lo + step * kTile;
       int limit[NT][2];
 #pragma unroll
@@ -641,9 +663,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
       else wk.template compute<false>(stage, qs, cs, seen0, limit);
       seen0 = seen1;
       seen1 = seen2;
-      stage = stage == 2 ? 0 : stage + 1;
+      stage = stage == kStages - 1 ? 0 : stage + 1;
     }
-    cp_wait<0>();
+    __syncthreads();  // every warp's copies have arrived and been read
     // join the warps' states
 #pragma unroll
     for (int t = 0; t < NT; t++)
@@ -662,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
     Partial<NT>* part = &partials[2 * blockIdx.x + (head_part ? 0 : 1)];
 #pragma unroll
     for (int t = 0; t < NT; t++) {
-      __syncthreads();  // the rings, or the previous eight rows, are no longer read
+      if (t > 0) __syncthreads();  // the previous eight rows are no longer read
 #pragma unroll
       for (int i = 0; i < 2; i++) {
         float* dst = s_merge + (warp * 8 + 2 * wk.c + i) * kMergeRow + wk.g * 20;
@@ -672,7 +694,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
               make_float4(wk.acc[t][j][i], wk.acc[t][j][2 + i], wk.acc[t][j + 1][i], wk.acc[t][j + 1][2 + i]);
       }
       __syncthreads();
-      const int row = tid >> 4, col = (tid & 15) * 8;  // eight channels a thread
+      constexpr int CH = 1024 / kThreads;  // channels a thread: eight rows of 128
+      const int row = tid / (128 / CH), col = (tid % (128 / CH)) * CH;
       const int frow = t * 8 + row;
       float M = -INFINITY, L = 0.0f, w[kWarps];
 #pragma unroll
@@ -684,14 +707,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
         w[k] = mk == -INFINITY ? 1.0f : ex2(mk - M);
         L += w[k] * s_ml[(k * ROWS + frow) * 2 + 1];
       }
-      float o[8];
+      float o[CH];
 #pragma unroll
-      for (int j = 0; j < 8; j++) o[j] = 0.0f;
+      for (int j = 0; j < CH; j++) o[j] = 0.0f;
 #pragma unroll
       for (int k = 0; k < kWarps; k++) {
         const float* src = s_merge + (k * 8 + row) * kMergeRow + (col >> 4) * 20 + (col & 15);
 #pragma unroll
-        for (int j = 0; j < 8; j += 4) {
+        for (int j = 0; j < CH; j += 4) {
           const float4 v = *reinterpret_cast<const float4*>(src + j);
           o[j] += w[k] * v.x;
           o[j + 1] += w[k] * v.y;
@@ -702,19 +725,20 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
       if (frow < rows) {
         if (head_part || cut) {
 #pragma unroll
-          for (int j = 0; j < 8; j += 4)
+          for (int j = 0; j < CH; j += 4)
             *reinterpret_cast<float4*>(&part->o[frow][col + j]) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-          if ((tid & 15) == 0) {
+          if (col == 0) {
             part->m[frow] = M;
             part->l[frow] = L;
           }
         } else {
           const int rr = row0 + frow, tok = rr / a.G, hd = h * a.G + rr - tok * a.G;
           const float f = L == 0.0f ? 1.0f : vst / L;
-          *reinterpret_cast<uint4*>(a.o + (int64_t(x.q0 + tok) * a.Hq + hd) * 128 + col) =
-              make_uint4(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f), pack_bf16(o[4] * f, o[5] * f),
-                         pack_bf16(o[6] * f, o[7] * f));
-          if ((tid & 15) == 0)
+          uint2* dst = reinterpret_cast<uint2*>(a.o + (int64_t(x.q0 + tok) * a.Hq + hd) * 128 + col);
+#pragma unroll
+          for (int j = 0; j < CH; j += 4)
+            dst[j >> 2] = make_uint2(pack_bf16(o[j] * f, o[j + 1] * f), pack_bf16(o[j + 2] * f, o[j + 3] * f));
+          if (col == 0)
             a.lse[int64_t(hd) * a.total_q + x.q0 + tok] =
                 L == 0.0f ? -INFINITY : (M - kOffset + log2f(L)) * 0.6931471805599453f;
         }
@@ -729,8 +753,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
       hd.parts = int(((last + 1) * C - 1) / total) - int(blockIdx.x);
       headers[blockIdx.x] = hd;
     }
-    pos += nt;
-    __syncthreads();  // Q and the row states are no longer read
+    fence_async_smem();
+    __syncthreads();  // Q, the merge area and the row states are no longer read: copies may follow
   }
 }
 
@@ -797,6 +821,12 @@ cudaError_t launch(const KvAttnArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int ctas = sm_count_current_device() * ctas_per_sm(NT);
   if (ctas <= 0) return cudaErrorInvalidDevice;
+  if (a.whole) {
+    const int64_t items = int64_t(a.R) * a.c.H;
+    const int64_t most = int64_t(ctas) * 16;
+    kv_attn_kernel<FMT, NT><<<unsigned(items < most ? items : most), kThreads, bytes, st>>>(a);
+    return cudaGetLastError();
+  }
   kv_attn_kernel<FMT, NT><<<ctas, kThreads, bytes, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -827,8 +857,13 @@ size_t kv_attn_workspace(int R, int max_q, int G) {
   }
 }
 
-cudaError_t launch_kv_attn(const KvAttnArgs& a, cudaStream_t st) {
+cudaError_t launch_kv_attn(const KvAttnArgs& args, cudaStream_t st) {
   clear_stale_error();
+  KvAttnArgs a = args;
+  // one block of query rows per request, and no request has more keys than a row of its
+  // table: up to the least run, no item needs cutting
+  a.whole = int64_t(a.max_q) * a.G <= 8 * kva::kMaxNt &&
+            (int64_t(a.width) << a.c.page_shift) <= int64_t(kva::kMinTiles) * kva::kTile;
   return a.c.fmt == 0 ? kva::launch_fmt<0>(a, st) : kva::launch_fmt<1>(a, st);
 }
 

@@ -243,6 +243,7 @@ struct KvAttnArgs {
   int Hq, G;              // query heads, and per key head
   float scale_log2;       // softmax scale * log2(e)
   int causal;
+  int whole;              // no context is long enough to be cut (set by launch_kv_attn)
   uint16_t* o;            // bf16 [total_q][Hq][128]
   float* lse;             // [Hq][total_q]
   uint8_t* ws;
