@@ -22,7 +22,7 @@
 // finished there; one cut by a border leaves partial (m, l, O) records that a
 // second kernel joins in the order of the keys, so results do not depend on
 // timing.  Each of the CTA's four warps takes 32 of a tile's keys with its own
-// ring of bulk copies and its own softmax state, so warps never wait on
+// ring of asynchronous copies and its own softmax state, so warps never wait on
 // one another inside an item.
 //
 // Fragments.  m16n8k16 with sixteen keys (then sixteen channels) as M and eight
@@ -84,6 +84,19 @@ struct Partial {
   float m[8 * NT], l[8 * NT];
 };
 __host__ __device__ inline size_t header_bytes(int ctas) { return (size_t(ctas) * sizeof(Header) + 255) & ~size_t(255); }
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_sf(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -156,8 +169,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
 }
 
 // Key (0..7) held by row n of an 8-key score tile.  The swap of the pairs 2, 3 and
-// 6, 7 puts the four lanes of a quad on keys of both parities, which halves the bank
-// conflicts of their 8-byte loads of V (64-byte rows).
+// 6, 7 puts the four lanes of a quad on keys of both parities, so that their
+// 8-byte loads of V (64-byte rows, chunks swizzled by bit 2 of the key) cover all banks.
 __device__ __forceinline__ int key_of(int n) { return n ^ ((n >> 1) & 1); }
 
 struct Request {
@@ -232,29 +245,54 @@ struct Worker {
     }
   }
 
-  // Copies.  Rows of a block lie one after another, so the 32 keys of a step are one
-  // run of each of K, V and their scales, or two where pages have 16 rows: lane
-  // 4 i + j < 4 runs brings run i of kind j (K, V, K scales, V scales) with one bulk copy,
-  // its address the lane's base plus block times the bytes of a block.  A warp's
-  // steps lie kTile keys apart, a multiple of every page size, so the place in the
-  // page stays the same for all steps of an item.
-  const uint8_t* src;         // kind's array + place in the page
-  uint32_t block_bytes, dst, bytes;
+  // Copies: two lanes per key and pass, a 32-byte sector at a time; pass i brings key
+  // 16 i + lane / 2 of a step.  A warp's steps lie kTile keys apart, a multiple of every
+  // page size, so a lane's rows within the pages stay the same for all steps of an
+  // item, and an address is the lane's base plus block times the bytes of a block; from
+  // pages of 32 rows on both passes are in one block, 16 rows apart.  Chunks of 16
+  // bytes are swizzled by bit 2 of the key (see key_of).
+  const uint8_t *k_src, *sf_src;  // of pass 0; lane % 2 brings the scales of K or of V
+  int64_t v_from_k;
+  uint32_t to0, to1, to_sf;       // in the stage, of pass 0
+  uint32_t block_bytes;
   __device__ __forceinline__ void aim(const KvPages& p, int key0, int h) {
-    const int kind = lane & 3, run = (lane >> 2) & 1;
-    const int row_bytes = kind < 2 ? 64 : kSf;
-    const uint8_t* base = kind == 0 ? p.k : kind == 1 ? p.v : kind == 2 ? p.k_sf : p.v_sf;
-    block_bytes = uint32_t(p.H * p.page * row_bytes);
-    src = base + (h * p.page + ((key0 + 16 * run) & (p.page - 1))) * row_bytes;
-    bytes = (p.page == 16 ? 16 : kStep) * row_bytes;
-    dst = ring + (kind == 0 ? 0 : kind == 1 ? kStep * 64 : kStep * 128 + (kind - 2) * kStep * kSf) + 16 * run * row_bytes;
+    const int half = lane & 1, key = lane >> 1, swz = ((key >> 2) & 1) << 1;
+    to0 = ring + key * 64 + ((half ^ swz) << 4);
+    to1 = ring + key * 64 + (((2 + half) ^ swz) << 4);
+    to_sf = ring + kStep * 128 + (half * kStep + key) * kSf;
+    block_bytes = uint32_t(p.H * p.page * 64);
+    v_from_k = p.v - p.k;
+    const int row = h * p.page + ((key0 + key) & (p.page - 1));
+    k_src = p.k + row * 64 + half * 16;
+    sf_src = (half ? p.v_sf : p.k_sf) + row * kSf;
+  }
+  __device__ __forceinline__ void copy_pass(uint32_t s, const uint8_t* k, const uint8_t* v, const uint8_t* sf, int i, int rows) {
+    cp16(to0 + s + i * 1024, k + rows * 64);
+    cp16(to1 + s + i * 1024, k + rows * 64 + 32);
+    cp16(to0 + s + i * 1024 + kStep * 64, v + rows * 64);
+    cp16(to1 + s + i * 1024 + kStep * 64, v + rows * 64 + 32);
+    cp_sf<kSf>(to_sf + s + i * 16 * kSf, sf + rows * kSf);
+  }
+  // `b0`, `b1`: blocks of the two passes, within the cache (any block for rows that do not count)
+  __device__ __forceinline__ void copy(int stage, bool small_pages, uint32_t b0, uint32_t b1) {
+    const uint32_t s = stage * stage_bytes(FMT);
+    const uint8_t* k = k_src + uint64_t(b0) * block_bytes;
+    const uint8_t* sf = sf_src + uint64_t(b0) * (block_bytes / (64 / kSf));
+    copy_pass(s, k, k + v_from_k, sf, 0, 0);
+    if (small_pages) {
+      k = k_src + uint64_t(b1) * block_bytes;
+      sf = sf_src + uint64_t(b1) * (block_bytes / (64 / kSf));
+      copy_pass(s, k, k + v_from_k, sf, 1, 0);
+    } else {
+      copy_pass(s, k, k + v_from_k, sf, 1, 16);
+    }
   }
 
   // Scores, softmax and P V of the 32 keys in `stage`.  MASKED: `seen` has a bit per key
-  // of the step, and limit[t][i] is the number of its keys that count for the row.
+  // of the step, and the row counts keys before limit[t][i], the first here being key0.
   template <bool MASKED>
   __device__ __forceinline__ void compute(int stage, uint32_t qs, const float (&cs)[NT][2], uint32_t seen,
-                                          const int (&limit)[NT][2]) {
+                                          const int (&limit)[NT][2], int key0) {
     const uint32_t s = ring + stage * stage_bytes(FMT);
     const uint32_t sfk = s + kStep * 128, sfv = sfk + kStep * kSf;
     const int kg = key_of(g);
@@ -272,7 +310,7 @@ struct Worker {
 #pragma unroll
         for (int x = 0; x < 2; x++) {
           const int key = u * 16 + x * 8 + kg;
-          const uint4 w = lds16(s + key * 64 + (c << 4));
+          const uint4 w = lds16(s + key * 64 + ((c ^ (((kg >> 2) & 1) << 1)) << 4));
           kw[u][x][0] = w.x, kw[u][x][1] = w.y, kw[u][x][2] = w.z, kw[u][x][3] = w.w;
           if (FMT == 0) {
             const uint32_t b = lds_u8(sfk + key * 4 + c);
@@ -318,7 +356,7 @@ struct Worker {
           for (int t = 0; t < NT; t++)
 #pragma unroll
             for (int i = 0; i < 2; i++)
-              if (!there || key >= limit[t][i]) sc[t][u][2 * x + i] = -INFINITY;
+              if (!there || key0 + key >= limit[t][i]) sc[t][u][2 * x + i] = -INFINITY;
         }
     }
     // a row's maximum moves only where a score passes it by more than kLazy (and
@@ -371,6 +409,7 @@ struct Worker {
     // V: a NaN block (scale byte 0xFF or 0x7F) reaches every row through 0 x NaN, so
     // where rows see different keys it is taken out of the product and put into the
     // rows that see its key; so are rows that are no keys and may hold anything
+    const uint32_t vrow = ((((g >> 1) ^ (((c >> 1) & 1) << 1)) << 4) + ((g & 1) << 3));
     const int ka = key_of(2 * c), kb = key_of(2 * c + 1);
 #pragma unroll
     for (int u = 0; u < 2; u++) {
@@ -379,8 +418,8 @@ struct Worker {
 #pragma unroll
       for (int x = 0; x < 2; x++) {
         const int key = (2 * u + x) * 8;
-        va[x] = lds8(s + kStep * 64 + (key + ka) * 64 + g * 8);
-        vb[x] = lds8(s + kStep * 64 + (key + kb) * 64 + g * 8);
+        va[x] = lds8(s + kStep * 64 + (key + ka) * 64 + vrow);
+        vb[x] = lds8(s + kStep * 64 + (key + kb) * 64 + vrow);
         uint32_t b0, b1;
         if (FMT == 0) {
           b0 = lds_u8(sfv + (key + ka) * 4 + (g >> 1));
@@ -433,7 +472,7 @@ struct Worker {
         for (int t = 0; t < NT; t++)
 #pragma unroll
           for (int i = 0; i < 2; i++)
-            if (key < limit[t][i]) {
+            if (key0 + key < limit[t][i]) {
 #pragma unroll
               for (int j = 0; j < 8; j++) acc[t][j][i] = acc[t][j][2 + i] = nan;
             }
@@ -448,31 +487,24 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_scan[kWarps];
   __shared__ int64_t s_before;
-  __shared__ __align__(8) uint64_t s_bar[kWarps * kStages];
-  __shared__ int s_r, s_abort;
+  __shared__ int s_r;
   float* s_cs = reinterpret_cast<float*>(smem + ring_bytes(FMT));
   uint8_t* s_q = NT > 1 ? smem + ring_bytes(FMT) + ROWS * 4 : smem + 2 * stage_bytes(FMT);  // NT = 1: warp 0's last stage
   float* s_merge = reinterpret_cast<float*>(smem);
   float* s_ml = reinterpret_cast<float*>(smem + merge_bytes);  // [warp][row][m, l]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t bars = smem_u32(s_bar) + warp * kStages * 8;
-  if (lane == 0) {
-    for (int i = 0; i < kStages; i++) mbar_init(bars + 8 * i, 1);
-    fence_mbar_init();
-  }
-  if (tid == 0) s_abort = 0;
+  asm volatile("griddepcontrol.launch_dependents;");  // kv_join_kernel may take its place and wait
   Header* headers = reinterpret_cast<Header*>(a.ws);
   Partial<NT>* partials = reinterpret_cast<Partial<NT>*>(a.ws + header_bytes(gridDim.x));
 
   // the line of tiles and this CTA's run of it; or, where all contexts are short,
   // whole items one after another
-  int64_t total = 0, C = 0, pos = 0, end = 0, base = 0;
+  int64_t total = 0, pos = 0, end = 0, base = 0, run = 0, extra = 0;
   int r = 0;
   if (a.whole) {
     end = int64_t(a.R) * a.c.H;
     pos = blockIdx.x;
-    __syncthreads();
   } else {
     if (tid == 0) headers[blockIdx.x].parts = 0;
     int64_t first_own = 0, first_upto = 0;  // of the first kThreads requests, the only ones most often
@@ -487,10 +519,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
       total += sum;
     }
     const int64_t most = (total + kMinTiles - 1) / kMinTiles;
-    C = most < int64_t(gridDim.x) ? most : int64_t(gridDim.x);
+    const int64_t C = most < int64_t(gridDim.x) ? most : int64_t(gridDim.x);
     if (int64_t(blockIdx.x) >= C) return;
-    pos = total * blockIdx.x / C, end = total * (blockIdx.x + 1) / C;
-    if (pos == end) return;
+    run = total / C, extra = total - run * C;  // the first `extra` CTAs take one tile more
+    pos = run * blockIdx.x + min(extra, int64_t(blockIdx.x));
+    end = pos + run + (int64_t(blockIdx.x) < extra ? 1 : 0);
     int64_t before = 0;
     for (int r0 = 0; r0 < a.R; r0 += kThreads) {
       int64_t sum = total, own = first_own, upto = first_upto;
@@ -517,7 +550,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
   wk.g = lane >> 2;
   const float kst = FMT == 1 ? __ldg(a.c.k_scale) : 1.0f;
   const float vst = FMT == 1 ? __ldg(a.c.v_scale) : 1.0f;
-  uint32_t phases = 0;  // bit i: phase of stage i
 
   while (pos < end && r < a.R) {
     int rb, h, t0, nt, tiles, item = 0;
@@ -540,7 +572,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
         continue;
       }
       const int64_t local = pos - base;
-      item = int(local / tiles), t0 = int(local - int64_t(item) * tiles);
+      item = local >> 32 ? int(local / tiles) : int(uint32_t(local) / uint32_t(tiles));
+      t0 = int(local - int64_t(item) * tiles);
       rb = item / a.c.H, h = item - rb * a.c.H;
       nt = int(min(int64_t(tiles - t0), end - pos));
       pos += nt;
@@ -553,37 +586,48 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
     const int k_lo = t0 * kTile + warp * kStep;
     const int k_end = min((t0 + nt) * kTile, keys);
     const int steps = k_lo < k_end ? (k_end - k_lo + kTile - 1) / kTile : 0;
-    // copies: the lane's run of a step, looked up one step ahead
+    // copies: the blocks of the lane's two keys of a step, looked up one step ahead
     const int32_t* table = a.table + int64_t(r) * a.width;
-    const int run_key = k_lo + 16 * ((lane >> 2) & 1);
-    const bool copies = lane < (a.c.page == 16 ? 8 : 4);
+    const int lane_key = k_lo + (lane >> 1);
+    const bool small_pages = a.c.page == 16;
     wk.aim(a.c, k_lo, h);
-    int block;
+    uint32_t b0 = 0, b1 = 0;
     auto look_up = [&](int step) {
-      const int key = run_key + step * kTile;
-      block = copies && step < steps && key < k_end ? __ldg(table + (key >> a.c.page_shift)) : -1;
+      const int key = lane_key + step * kTile;
+      b0 = key < k_end ? uint32_t(__ldg(table + (key >> a.c.page_shift))) : 0xFFFFFFFFu;
+      if (small_pages) b1 = key + 16 < k_end ? uint32_t(__ldg(table + (key >> 4) + 1)) : 0xFFFFFFFFu;
+      else b1 = key + 16 < k_end ? b0 : 0xFFFFFFFFu;
     };
-    // starts the copies of a step (none past the last) and returns a bit per visible key
+    // starts the copies of a step and returns a bit per visible key; rows that are none
+    // (past the last key, or of a block outside the cache) bring some other row, unseen
+    const uint32_t last_block = uint32_t(a.c.blocks) - 1u;
     auto issue = [&](int step, int st) -> uint32_t {
-      if (step >= steps) return 0;
-      const int key0 = k_lo + step * kTile;
-      const bool live = block >= 0 && block < a.c.blocks;
-      if (copies && !live && run_key + step * kTile < k_end) atomicOr(&g_status_kv_attn, DEV_BAD_INDEX);
-      const uint32_t runs = __ballot_sync(0xFFFFFFFFu, live);
-      if (lane == 0)
-        mbar_arrive_expect_tx(bars + 8 * st, __popc(runs & 0x11u) * ((a.c.page == 16 ? 16 : kStep) * (128 + 2 * sf_bytes(FMT))));
-      if (live)
-        bulk_load(wk.dst + st * stage_bytes(FMT), wk.src + uint64_t(uint32_t(block)) * wk.block_bytes, wk.bytes, bars + 8 * st);
-      uint32_t seen = a.c.page == 16 ? ((runs & 1u) ? 0x0000FFFFu : 0u) | ((runs & 16u) ? 0xFFFF0000u : 0u) : (runs & 1u) ? 0xFFFFFFFFu : 0u;
-      if (k_end - key0 < kStep) seen &= (1u << (k_end - key0)) - 1u;
+      const bool live0 = b0 <= last_block, live1 = b1 <= last_block;
+      wk.copy(st, small_pages, min(b0, last_block), min(b1, last_block));
+      cp_commit();
+      uint32_t seen = 0xFFFFFFFFu;
+      if (!__all_sync(0xFFFFFFFFu, live0 && live1)) {
+        // lanes 2k and 2k + 1 speak for keys k and 16 + k
+        const uint32_t v0 = __ballot_sync(0xFFFFFFFFu, live0), v1 = __ballot_sync(0xFFFFFFFFu, live1);
+        seen = __ballot_sync(0xFFFFFFFFu, ((lane < 16 ? v0 : v1) >> (2 * (lane & 15))) & 1u);
+        const int key = lane_key + step * kTile;
+        if ((!live0 && key < k_end) || (!live1 && key + 16 < k_end)) atomicOr(&g_status_kv_attn, DEV_BAD_INDEX);
+      }
       return seen;
     };
     static_assert(kStages == 3, "two steps in flight ahead of the one computed");
-    look_up(0);
-    uint32_t seen0 = issue(0, 0);
-    look_up(1);
-    uint32_t seen1 = issue(1, 1);
-    look_up(2);
+    uint32_t seen0 = 0, seen1 = 0;
+    if (steps > 0) {
+      look_up(0);
+      seen0 = issue(0, 0);
+      look_up(1);
+    }
+    if (steps > 1) {
+      seen1 = issue(1, 1);
+      look_up(2);
+    } else {
+      cp_commit();
+    }
 
     // Q of the item: binary16 with a power of two per row, in fragment order;
     // eight threads per row, 16 channels each (NT = 1: through warp 0's third
@@ -641,7 +685,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
     if (NT == 1) {
 #pragma unroll
       for (int w = 0; w < 4; w++) wk.qf[NT == 1 ? w : 0] = lds16(qs + (w * 32 + lane) * 16);
-      fence_async_smem();
       __syncthreads();  // the stage is free for copies
     }
     int stage = 0;  // every item begins with stage 0
@@ -649,22 +692,23 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
     for (int step = 0; step < steps; step++) {
       // the stage of step - 1 is free: every lane has read it
       __syncwarp();
-      const uint32_t seen2 = issue(step + 2, stage == 0 ? 2 : stage - 1);
-      look_up(step + 3);
-      mbar_wait(bars + 8 * stage, (phases >> stage) & 1u, &s_abort, &g_status_kv_attn);
-      phases ^= 1u << stage;
+      uint32_t seen2 = 0;
+      if (step + 2 < steps) {
+        seen2 = issue(step + 2, stage == 0 ? 2 : stage - 1);
+        look_up(step + 3);
+      } else {
+        cp_commit();
+      }
+      cp_wait<kStages - 1>();
+      __syncwarp();
       const int key0 = k_lo + step * kTile;
-      int limit[NT][2];
-#pragma unroll
-      for (int t = 0; t < NT; t++)
-#pragma unroll
-        for (int i = 0; i < 2; i++) limit[t][i] = lim[t][i] - key0;
-      if (seen0 != 0xFFFFFFFFu || key0 + kStep > all_see) wk.template compute<true>(stage, qs, cs, seen0, limit);
-      else wk.template compute<false>(stage, qs, cs, seen0, limit);
+      if (seen0 != 0xFFFFFFFFu || key0 + kStep > all_see) wk.template compute<true>(stage, qs, cs, seen0, lim, key0);
+      else wk.template compute<false>(stage, qs, cs, seen0, lim, key0);
       seen0 = seen1;
       seen1 = seen2;
       stage = stage == kStages - 1 ? 0 : stage + 1;
     }
+    cp_wait<0>();
     __syncthreads();  // every warp's copies have arrived and been read
     // join the warps' states
 #pragma unroll
@@ -750,10 +794,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
       hd.r = r;
       hd.rb = rb;
       hd.h = h;
-      hd.parts = int(((last + 1) * C - 1) / total) - int(blockIdx.x);
+      const int64_t larger = extra * (run + 1);  // tiles of the CTAs that take one more
+      hd.parts = int(last < larger ? last / (run + 1) : extra + (last - larger) / run) - int(blockIdx.x);
       headers[blockIdx.x] = hd;
     }
-    fence_async_smem();
     __syncthreads();  // Q, the merge area and the row states are no longer read: copies may follow
   }
 }
@@ -762,6 +806,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
 // it: one warp per row, four channels a lane, parts in the order of the keys.
 template <int FMT, int NT>
 __global__ void __launch_bounds__(128) kv_join_kernel(KvAttnArgs a, int ctas) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the end of kv_attn_kernel
   const Header hd = reinterpret_cast<const Header*>(a.ws)[blockIdx.x];
   if (hd.parts == 0) return;
   const Partial<NT>* partials = reinterpret_cast<const Partial<NT>*>(a.ws + header_bytes(ctas));
@@ -830,8 +875,16 @@ cudaError_t launch(const KvAttnArgs& a, cudaStream_t st) {
   kv_attn_kernel<FMT, NT><<<ctas, kThreads, bytes, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  kv_join_kernel<FMT, NT><<<dim3(unsigned(ctas), 2 * NT), 128, 0, st>>>(a, ctas);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(ctas), 2 * NT);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<FMT, NT>, a, ctas);
 }
 
 template <int FMT>
