@@ -50,6 +50,7 @@ constexpr float kOffset = 8.0f;           // log2 offset of P
 constexpr float kLazy = 6.0f;             // growth of a row maximum that moves m
 constexpr int kMaxNt = 4;                 // blocks of at most 32 query rows
 constexpr int kMinTiles = 4;              // least tiles of a run, as long as items are cut
+constexpr int kItemTiles = 2;             // what an item costs beside its tiles (drain, merge), in tiles
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 // CTAs of an SM for NT 8-row tiles: 16, 12 or 8 warps, as 32 NT accumulator registers
@@ -59,19 +60,19 @@ __host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : nt 
 __host__ __device__ constexpr int sf_bytes(int fmt) { return fmt == 0 ? 4 : 8; }
 __host__ __device__ constexpr int stage_bytes(int fmt) { return kStep * 64 * 2 + kStep * sf_bytes(fmt) * 2; }
 
-// Merge layout of eight rows: row r, channel d at r * 164 + (d / 16) * 20 + d % 16
-// floats, so that a quad's rows and two neighbours' channels fall on different banks.
-constexpr int kMergeRow = 164;
-constexpr int merge_bytes = kWarps * 8 * kMergeRow * 4;
-// Q's fragments of one tile of eight rows live in registers (staged through a ring
-// at the start of an item), those of more tiles in shared memory.  Row scales, and the
-// warps' m and l behind the merge area, complete it: 57,328 bytes for NVFP4 and NT = 1, of
-// which four CTAs fit an SM.
+// A warp's result of an item passes through the third stage of its ring, eight rows
+// at a time: row r, 16-byte quad q at r * 512 + (q ^ (r / 2)) * 16 bytes, so that the
+// stores of a quad's rows and two neighbours' channels fall on different banks; then
+// m and l of all rows.  The first two stages receive the next item meanwhile.
+__host__ __device__ constexpr int last_stage(int fmt) { return (kStages - 1) * stage_bytes(fmt); }
+static_assert(8 * 512 + 8 * kMaxNt * 8 <= stage_bytes(0), "a stage holds eight rows, and m and l");
+// Q's fragments of one tile of eight rows live in registers (staged through warp 0's
+// third stage at the start of an item), those of more tiles in shared memory.  With
+// the row scales that is 55,328 bytes for NVFP4 and NT = 1, of which four fit an SM.
 __host__ __device__ constexpr int ring_bytes(int fmt) { return kWarps * kStages * stage_bytes(fmt); }
 __host__ __device__ constexpr int smem_bytes(int fmt, int nt) {
   return ring_bytes(fmt) + (nt > 1 ? nt * 8 * 128 * 2 : 0) + nt * 8 * 4;
 }
-static_assert(merge_bytes + kWarps * kMaxNt * 8 * 8 <= ring_bytes(0), "merge area, m and l lie over the rings");
 
 // Workspace: per CTA of the grid a header and two partial records.
 struct Header {
@@ -141,6 +142,11 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
+__device__ __forceinline__ uint32_t lds_u32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
 __device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
@@ -194,12 +200,12 @@ __device__ __forceinline__ Request request_of(const KvAttnArgs& a, int r) {
 }
 __device__ __forceinline__ int tiles_of(const Request& x) { return max(1, (x.kv + kTile - 1) / kTile); }
 
-// Tiles of all items of request r.
+// Units of work (tiles, and kItemTiles for each item) of request r.
 template <int ROWS>
-__device__ __forceinline__ int64_t request_tiles(const KvAttnArgs& a, int r) {
+__device__ __forceinline__ int64_t request_units(const KvAttnArgs& a, int r) {
   const Request x = request_of(a, r);
   if (x.n == 0) return 0;
-  return int64_t((x.n * a.G + ROWS - 1) / ROWS) * a.c.H * tiles_of(x);
+  return int64_t((x.n * a.G + ROWS - 1) / ROWS) * a.c.H * (tiles_of(x) + kItemTiles);
 }
 
 // Inclusive scan of `v` over the CTA; `total` gets the sum.
@@ -462,6 +468,15 @@ struct Worker {
     }
     if (MASKED) {
       const float nan = __uint_as_float(0x7FC00000u);
+      bool any;  // a NaN block in the row of this lane's key
+      if (FMT == 0) {
+        const uint32_t b = lds_u32(sfv + lane * 4);
+        any = __vcmpeq4(b, 0xFFFFFFFFu) != 0;
+      } else {
+        const uint2 b = lds8(sfv + lane * 8);
+        any = (__vcmpeq4(b.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(b.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu)) != 0;
+      }
+      if (!__any_sync(0xFFFFFFFFu, any && ((seen >> lane) & 1u))) return;
 #pragma unroll 1
       for (int key = 0; key < kStep; key++) {
         bool bad;  // in channels 16 g .. + 15
@@ -481,6 +496,15 @@ struct Worker {
   }
 };
 
+// Part of an item that a CTA computes: tiles t0 .. t0 + nt - 1 of the `tiles` of
+// (request r, query rows row0 .. row0 + rows - 1 of it, key head h).
+struct Item {
+  int r, rb, h, t0, nt, tiles;
+  int q0, row0, rows;
+  int n, kv;
+  int64_t last_unit;  // of the item, on the line
+};
+
 template <int FMT, int NT>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAttnArgs a) {
   constexpr int ROWS = 8 * NT;
@@ -489,16 +513,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
   __shared__ int64_t s_before;
   __shared__ int s_r;
   float* s_cs = reinterpret_cast<float*>(smem + ring_bytes(FMT));
-  uint8_t* s_q = NT > 1 ? smem + ring_bytes(FMT) + ROWS * 4 : smem + 2 * stage_bytes(FMT);  // NT = 1: warp 0's last stage
-  float* s_merge = reinterpret_cast<float*>(smem);
-  float* s_ml = reinterpret_cast<float*>(smem + merge_bytes);  // [warp][row][m, l]
+  uint8_t* s_q = NT > 1 ? smem + ring_bytes(FMT) + ROWS * 4 : smem + last_stage(FMT);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.launch_dependents;");  // kv_join_kernel may take its place and wait
   Header* headers = reinterpret_cast<Header*>(a.ws);
   Partial<NT>* partials = reinterpret_cast<Partial<NT>*>(a.ws + header_bytes(gridDim.x));
 
-  // the line of tiles and this CTA's run of it; or, where all contexts are short,
+  // the line of units and this CTA's run of it; or, where all contexts are short,
   // whole items one after another
   int64_t total = 0, pos = 0, end = 0, base = 0, run = 0, extra = 0;
   int r = 0;
@@ -510,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
     int64_t first_own = 0, first_upto = 0;  // of the first kThreads requests, the only ones most often
     for (int r0 = 0; r0 < a.R; r0 += kThreads) {
       int64_t sum;
-      const int64_t own = r0 + tid < a.R ? request_tiles<ROWS>(a, r0 + tid) : 0;
+      const int64_t own = r0 + tid < a.R ? request_units<ROWS>(a, r0 + tid) : 0;
       const int64_t upto = cta_scan(own, s_scan, sum);
       if (r0 == 0) {
         first_own = own;
@@ -521,14 +543,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
     const int64_t most = (total + kMinTiles - 1) / kMinTiles;
     const int64_t C = most < int64_t(gridDim.x) ? most : int64_t(gridDim.x);
     if (int64_t(blockIdx.x) >= C) return;
-    run = total / C, extra = total - run * C;  // the first `extra` CTAs take one tile more
+    run = total / C, extra = total - run * C;  // the first `extra` CTAs take one unit more
     pos = run * blockIdx.x + min(extra, int64_t(blockIdx.x));
     end = pos + run + (int64_t(blockIdx.x) < extra ? 1 : 0);
     int64_t before = 0;
     for (int r0 = 0; r0 < a.R; r0 += kThreads) {
       int64_t sum = total, own = first_own, upto = first_upto;
       if (a.R > kThreads) {
-        own = r0 + tid < a.R ? request_tiles<ROWS>(a, r0 + tid) : 0;
+        own = r0 + tid < a.R ? request_units<ROWS>(a, r0 + tid) : 0;
         upto = before + cta_scan(own, s_scan, sum);
       }
       if (upto - own <= pos && pos < upto) {
@@ -543,6 +565,44 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
     base = s_before;
   }
 
+  // the next part of an item of this CTA, if there is one
+  auto next = [&](Item& it) -> bool {
+    while (pos < end && r < a.R) {
+      if (a.whole) r = int(pos / a.c.H);
+      const Request x = request_of(a, r);
+      it.tiles = tiles_of(x);
+      it.q0 = x.q0, it.n = x.n, it.kv = x.kv;
+      if (a.whole) {
+        it.rb = 0, it.h = int(pos - int64_t(r) * a.c.H);
+        it.t0 = 0, it.nt = x.n == 0 ? 0 : it.tiles;
+        it.last_unit = 0;
+        pos += gridDim.x;
+      } else {
+        const int nrb = (x.n * a.G + ROWS - 1) / ROWS, units = it.tiles + kItemTiles;
+        const int64_t all = x.n == 0 ? 0 : int64_t(nrb) * a.c.H * units;
+        if (pos >= base + all) {
+          base += all;
+          r++;
+          continue;
+        }
+        const int64_t local = pos - base;
+        const int item = local >> 32 ? int(local / units) : int(uint32_t(local) / uint32_t(units));
+        const int u0 = int(local - int64_t(item) * units), u1 = int(min(int64_t(units), u0 + (end - pos)));
+        it.rb = item / a.c.H, it.h = item - it.rb * a.c.H;
+        it.t0 = max(0, u0 - kItemTiles);  // the first units of an item stand for its cost as such
+        it.nt = max(0, u1 - kItemTiles) - it.t0;
+        it.last_unit = base + int64_t(item + 1) * units - 1;
+        pos += u1 - u0;
+      }
+      if (it.nt == 0) continue;
+      it.r = r;
+      it.row0 = it.rb * ROWS;
+      it.rows = min(ROWS, x.n * a.G - it.row0);
+      return true;
+    }
+    return false;
+  };
+
   Worker<FMT, NT> wk;
   wk.ring = smem_u32(smem) + warp * kStages * stage_bytes(FMT);
   wk.lane = lane;
@@ -550,77 +610,56 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
   wk.g = lane >> 2;
   const float kst = FMT == 1 ? __ldg(a.c.k_scale) : 1.0f;
   const float vst = FMT == 1 ? __ldg(a.c.v_scale) : 1.0f;
+  float* const mine = reinterpret_cast<float*>(smem + warp * kStages * stage_bytes(FMT) + last_stage(FMT));
+  const bool small_pages = a.c.page == 16;
+  const uint32_t last_block = uint32_t(a.c.blocks) - 1u;
 
-  while (pos < end && r < a.R) {
-    int rb, h, t0, nt, tiles, item = 0;
-    if (a.whole) {
-      r = int(pos / a.c.H);
-      rb = 0, h = int(pos - int64_t(r) * a.c.H);
+  // copies of the current item: the blocks of the lane's two keys of a step, looked
+  // up one step ahead
+  int k_lo, k_end, steps;
+  const int32_t* table;
+  uint32_t b0 = 0, b1 = 0;
+  auto look_up = [&](int step) {
+    const int key = k_lo + (lane >> 1) + step * kTile;
+    b0 = key < k_end ? uint32_t(__ldg(table + (key >> a.c.page_shift))) : 0xFFFFFFFFu;
+    if (small_pages) b1 = key + 16 < k_end ? uint32_t(__ldg(table + (key >> 4) + 1)) : 0xFFFFFFFFu;
+    else b1 = key + 16 < k_end ? b0 : 0xFFFFFFFFu;
+  };
+  // starts the copies of a step and returns a bit per visible key; rows that are none
+  // (past the last key, or of a block outside the cache) bring some other row, unseen
+  auto issue = [&](int step, int st) -> uint32_t {
+    const bool live0 = b0 <= last_block, live1 = b1 <= last_block;
+    wk.copy(st, small_pages, min(b0, last_block), min(b1, last_block));
+    cp_commit();
+    uint32_t seen = 0xFFFFFFFFu;
+    if (!__all_sync(0xFFFFFFFFu, live0 && live1)) {
+      // lanes 2k and 2k + 1 speak for keys k and 16 + k
+      const uint32_t v0 = __ballot_sync(0xFFFFFFFFu, live0), v1 = __ballot_sync(0xFFFFFFFFu, live1);
+      seen = __ballot_sync(0xFFFFFFFFu, ((lane < 16 ? v0 : v1) >> (2 * (lane & 15))) & 1u);
+      const int key = k_lo + (lane >> 1) + step * kTile;
+      if ((!live0 && key < k_end) || (!live1 && key + 16 < k_end)) atomicOr(&g_status_kv_attn, DEV_BAD_INDEX);
     }
-    const Request x = request_of(a, r);
-    tiles = tiles_of(x);
-    if (a.whole) {
-      pos += gridDim.x;
-      if (x.n == 0) continue;
-      t0 = 0, nt = tiles;
-    } else {
-      const int nrb = (x.n * a.G + ROWS - 1) / ROWS;
-      const int64_t all = x.n == 0 ? 0 : int64_t(nrb) * a.c.H * tiles;
-      if (pos >= base + all) {
-        base += all;
-        r++;
-        continue;
-      }
-      const int64_t local = pos - base;
-      item = local >> 32 ? int(local / tiles) : int(uint32_t(local) / uint32_t(tiles));
-      t0 = int(local - int64_t(item) * tiles);
-      rb = item / a.c.H, h = item - rb * a.c.H;
-      nt = int(min(int64_t(tiles - t0), end - pos));
-      pos += nt;
-    }
-    const int row0 = rb * ROWS, rows = min(ROWS, x.n * a.G - row0);
-    const int first_tok = row0 / a.G, last_tok = (row0 + rows - 1) / a.G;
-    // keys that some row of the block sees, and that all see
-    const int keys = a.causal ? max(0, x.kv - x.n + last_tok + 1) : x.kv;
-    const int all_see = a.causal ? x.kv - x.n + first_tok + 1 : x.kv;
-    const int k_lo = t0 * kTile + warp * kStep;
-    const int k_end = min((t0 + nt) * kTile, keys);
-    const int steps = k_lo < k_end ? (k_end - k_lo + kTile - 1) / kTile : 0;
-    // copies: the blocks of the lane's two keys of a step, looked up one step ahead
-    const int32_t* table = a.table + int64_t(r) * a.width;
-    const int lane_key = k_lo + (lane >> 1);
-    const bool small_pages = a.c.page == 16;
-    wk.aim(a.c, k_lo, h);
-    uint32_t b0 = 0, b1 = 0;
-    auto look_up = [&](int step) {
-      const int key = lane_key + step * kTile;
-      b0 = key < k_end ? uint32_t(__ldg(table + (key >> a.c.page_shift))) : 0xFFFFFFFFu;
-      if (small_pages) b1 = key + 16 < k_end ? uint32_t(__ldg(table + (key >> 4) + 1)) : 0xFFFFFFFFu;
-      else b1 = key + 16 < k_end ? b0 : 0xFFFFFFFFu;
-    };
-    // starts the copies of a step and returns a bit per visible key; rows that are none
-    // (past the last key, or of a block outside the cache) bring some other row, unseen
-    const uint32_t last_block = uint32_t(a.c.blocks) - 1u;
-    auto issue = [&](int step, int st) -> uint32_t {
-      const bool live0 = b0 <= last_block, live1 = b1 <= last_block;
-      wk.copy(st, small_pages, min(b0, last_block), min(b1, last_block));
-      cp_commit();
-      uint32_t seen = 0xFFFFFFFFu;
-      if (!__all_sync(0xFFFFFFFFu, live0 && live1)) {
-        // lanes 2k and 2k + 1 speak for keys k and 16 + k
-        const uint32_t v0 = __ballot_sync(0xFFFFFFFFu, live0), v1 = __ballot_sync(0xFFFFFFFFu, live1);
-        seen = __ballot_sync(0xFFFFFFFFu, ((lane < 16 ? v0 : v1) >> (2 * (lane & 15))) & 1u);
-        const int key = lane_key + step * kTile;
-        if ((!live0 && key < k_end) || (!live1 && key + 16 < k_end)) atomicOr(&g_status_kv_attn, DEV_BAD_INDEX);
-      }
-      return seen;
-    };
-    static_assert(kStages == 3, "two steps in flight ahead of the one computed");
-    uint32_t seen0 = 0, seen1 = 0;
+    return seen;
+  };
+  static_assert(kStages == 3, "two steps in flight ahead of the one computed");
+  uint32_t seen0 = 0, seen1 = 0;
+  uint4 qv[NT > 2 ? 4 : 2];  // this thread's channels of the item's queries
+  constexpr int kPasses = (ROWS * 8 + kThreads - 1) / kThreads;
+  // starts an item: its first two steps, and its queries' loads
+  auto begin = [&](const Item& it) {
+    const int last_tok = (it.row0 + it.rows - 1) / a.G;
+    const int keys = a.causal ? max(0, it.kv - it.n + last_tok + 1) : it.kv;  // that some row sees
+    k_lo = it.t0 * kTile + warp * kStep;
+    k_end = min((it.t0 + it.nt) * kTile, keys);
+    steps = k_lo < k_end ? (k_end - k_lo + kTile - 1) / kTile : 0;
+    table = a.table + int64_t(it.r) * a.width;
+    wk.aim(a.c, k_lo, it.h);
     if (steps > 0) {
       look_up(0);
       seen0 = issue(0, 0);
       look_up(1);
+    } else {
+      cp_commit();
     }
     if (steps > 1) {
       seen1 = issue(1, 1);
@@ -628,21 +667,29 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
     } else {
       cp_commit();
     }
-
-    // Q of the item: binary16 with a power of two per row, in fragment order;
-    // eight threads per row, 16 channels each (NT = 1: through warp 0's third
-    // stage, which is free now)
+    // eight threads per row, 16 channels each
 #pragma unroll
-    for (int pass = 0; pass < (ROWS * 8 + kThreads - 1) / kThreads; pass++) {
-      const int i = pass * kThreads + tid;
-      const int row = i >> 3, part = i & 7;
-      uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-      if (row < rows) {
-        const int rr = row0 + row, tok = rr / a.G, hd = rr - tok * a.G;
-        const uint16_t* src = a.q + int64_t(x.q0 + tok) * a.q_stride + int64_t(h * a.G + hd) * 128 + part * 16;
-        v0 = __ldg(reinterpret_cast<const uint4*>(src));
-        v1 = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+    for (int pass = 0; pass < kPasses; pass++) {
+      const int row = (pass * kThreads + tid) >> 3, part = tid & 7;
+      qv[2 * pass] = qv[2 * pass + 1] = make_uint4(0, 0, 0, 0);
+      if (row < it.rows) {
+        const int rr = it.row0 + row, tok = rr / a.G, hd = rr - tok * a.G;
+        const uint16_t* src = a.q + int64_t(it.q0 + tok) * a.q_stride + int64_t(it.h * a.G + hd) * 128 + part * 16;
+        qv[2 * pass] = __ldg(reinterpret_cast<const uint4*>(src));
+        qv[2 * pass + 1] = __ldg(reinterpret_cast<const uint4*>(src) + 1);
       }
+    }
+  };
+
+  Item it;
+  if (!next(it)) return;
+  begin(it);
+  for (bool more = true; more;) {
+    // Q: binary16 with a power of two per row, in fragment order
+#pragma unroll
+    for (int pass = 0; pass < kPasses; pass++) {
+      const int row = (pass * kThreads + tid) >> 3, part = tid & 7;
+      const uint4 v0 = qv[2 * pass], v1 = qv[2 * pass + 1];
       const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
       uint32_t mx = 0;
 #pragma unroll
@@ -678,8 +725,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
       for (int i = 0; i < 2; i++) {
         const int row = t * 8 + 2 * wk.c + i;
         cs[t][i] = s_cs[row];
-        lim[t][i] = !a.causal || row >= rows ? x.kv : x.kv - x.n + (row0 + row) / a.G + 1;
+        lim[t][i] = !a.causal || row >= it.rows ? it.kv : it.kv - it.n + (it.row0 + row) / a.G + 1;
       }
+    const int all_see = a.causal ? it.kv - it.n + it.row0 / a.G + 1 : it.kv;  // keys that every row sees
     wk.clear();
     const uint32_t qs = smem_u32(s_q);
     if (NT == 1) {
@@ -708,9 +756,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
       seen1 = seen2;
       stage = stage == kStages - 1 ? 0 : stage + 1;
     }
-    cp_wait<0>();
-    __syncthreads();  // every warp's copies have arrived and been read
-    // join the warps' states
+    __syncwarp();
+    // the next item's first copies run while this one's warps are joined
+    const Item cur = it;
+    more = next(it);
+    if (more) begin(it);
 #pragma unroll
     for (int t = 0; t < NT; t++)
 #pragma unroll
@@ -718,111 +768,115 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
         float v = wk.l[t][i];
 #pragma unroll
         for (int o = 4; o <= 16; o <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        if (wk.g == 0) {
-          float* p = s_ml + (warp * ROWS + t * 8 + 2 * wk.c + i) * 2;
-          p[0] = wk.m[t][i];
-          p[1] = v;
-        }
+        if (wk.g == 0) *reinterpret_cast<float2*>(mine + 1024 + (t * 8 + 2 * wk.c + i) * 2) = make_float2(wk.m[t][i], v);
       }
-    const bool head_part = t0 > 0, cut = t0 + nt < tiles;
+    const bool head_part = cur.t0 > 0, cut = cur.t0 + cur.nt < cur.tiles;
     Partial<NT>* part = &partials[2 * blockIdx.x + (head_part ? 0 : 1)];
+    const float* const theirs = reinterpret_cast<const float*>(smem + last_stage(FMT));  // of warp 0
+    constexpr int kRing = kStages * stage_bytes(FMT) / 4;                                // floats from warp to warp
 #pragma unroll
     for (int t = 0; t < NT; t++) {
       if (t > 0) __syncthreads();  // the previous eight rows are no longer read
 #pragma unroll
       for (int i = 0; i < 2; i++) {
-        float* dst = s_merge + (warp * 8 + 2 * wk.c + i) * kMergeRow + wk.g * 20;
+        float4* dst = reinterpret_cast<float4*>(mine) + (2 * wk.c + i) * 32;
 #pragma unroll
         for (int j = 0; j < 8; j += 2)
-          *reinterpret_cast<float4*>(dst + 2 * j) =
+          dst[(wk.g * 4 + (j >> 1)) ^ wk.c] =
               make_float4(wk.acc[t][j][i], wk.acc[t][j][2 + i], wk.acc[t][j + 1][i], wk.acc[t][j + 1][2 + i]);
       }
       __syncthreads();
-      constexpr int CH = 1024 / kThreads;  // channels a thread: eight rows of 128
-      const int row = tid / (128 / CH), col = (tid % (128 / CH)) * CH;
+      const int row = tid >> 4, quad = (tid & 15) * 2;  // eight channels a thread
       const int frow = t * 8 + row;
       float M = -INFINITY, L = 0.0f, w[kWarps];
+      float2 ml[kWarps];
 #pragma unroll
-      for (int k = 0; k < kWarps; k++) M = fmaxf(M, s_ml[(k * ROWS + frow) * 2]);
+      for (int k = 0; k < kWarps; k++) {
+        ml[k] = *reinterpret_cast<const float2*>(theirs + k * kRing + 1024 + frow * 2);
+        M = fmaxf(M, ml[k].x);
+      }
 #pragma unroll
       for (int k = 0; k < kWarps; k++) {
         // without keys (m = -inf) l and O are 0, or NaN where every score was
-        const float mk = s_ml[(k * ROWS + frow) * 2];
-        w[k] = mk == -INFINITY ? 1.0f : ex2(mk - M);
-        L += w[k] * s_ml[(k * ROWS + frow) * 2 + 1];
+        w[k] = ml[k].x == -INFINITY ? 1.0f : ex2(ml[k].x - M);
+        L += w[k] * ml[k].y;
       }
-      float o[CH];
+      float o[8];
 #pragma unroll
-      for (int j = 0; j < CH; j++) o[j] = 0.0f;
+      for (int j = 0; j < 8; j++) o[j] = 0.0f;
 #pragma unroll
       for (int k = 0; k < kWarps; k++) {
-        const float* src = s_merge + (k * 8 + row) * kMergeRow + (col >> 4) * 20 + (col & 15);
+        const float4* src = reinterpret_cast<const float4*>(theirs + k * kRing) + row * 32;
 #pragma unroll
-        for (int j = 0; j < CH; j += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src + j);
-          o[j] += w[k] * v.x;
-          o[j + 1] += w[k] * v.y;
-          o[j + 2] += w[k] * v.z;
-          o[j + 3] += w[k] * v.w;
+        for (int j = 0; j < 2; j++) {
+          const float4 v = src[(quad + j) ^ (row >> 1)];
+          o[4 * j] += w[k] * v.x;
+          o[4 * j + 1] += w[k] * v.y;
+          o[4 * j + 2] += w[k] * v.z;
+          o[4 * j + 3] += w[k] * v.w;
         }
       }
-      if (frow < rows) {
+      if (frow < cur.rows) {
         if (head_part || cut) {
-#pragma unroll
-          for (int j = 0; j < CH; j += 4)
-            *reinterpret_cast<float4*>(&part->o[frow][col + j]) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-          if (col == 0) {
+          float4* dst = reinterpret_cast<float4*>(part->o[frow]) + quad;
+          dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+          dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+          if (quad == 0) {
             part->m[frow] = M;
             part->l[frow] = L;
           }
         } else {
-          const int rr = row0 + frow, tok = rr / a.G, hd = h * a.G + rr - tok * a.G;
+          const int rr = cur.row0 + frow, tok = rr / a.G, hd = cur.h * a.G + rr - tok * a.G;
           const float f = L == 0.0f ? 1.0f : vst / L;
-          uint2* dst = reinterpret_cast<uint2*>(a.o + (int64_t(x.q0 + tok) * a.Hq + hd) * 128 + col);
-#pragma unroll
-          for (int j = 0; j < CH; j += 4)
-            dst[j >> 2] = make_uint2(pack_bf16(o[j] * f, o[j + 1] * f), pack_bf16(o[j + 2] * f, o[j + 3] * f));
-          if (col == 0)
-            a.lse[int64_t(hd) * a.total_q + x.q0 + tok] =
+          *reinterpret_cast<uint4*>(a.o + (int64_t(cur.q0 + tok) * a.Hq + hd) * 128 + quad * 4) =
+              make_uint4(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f), pack_bf16(o[4] * f, o[5] * f),
+                         pack_bf16(o[6] * f, o[7] * f));
+          if (quad == 0)
+            a.lse[int64_t(hd) * a.total_q + cur.q0 + tok] =
                 L == 0.0f ? -INFINITY : (M - kOffset + log2f(L)) * 0.6931471805599453f;
         }
       }
     }
     if (cut && !head_part && tid == 0) {
-      const int64_t last = base + int64_t(item + 1) * tiles - 1;  // the CTA of the item's last tile
+      const int64_t larger = extra * (run + 1);  // units of the CTAs that take one more
       Header hd;
-      hd.r = r;
-      hd.rb = rb;
-      hd.h = h;
-      const int64_t larger = extra * (run + 1);  // tiles of the CTAs that take one more
-      hd.parts = int(last < larger ? last / (run + 1) : extra + (last - larger) / run) - int(blockIdx.x);
+      hd.r = cur.r;
+      hd.rb = cur.rb;
+      hd.h = cur.h;
+      hd.parts = int(cur.last_unit < larger ? cur.last_unit / (run + 1) : extra + (cur.last_unit - larger) / run) - int(blockIdx.x);
       headers[blockIdx.x] = hd;
     }
-    __syncthreads();  // Q, the merge area and the row states are no longer read: copies may follow
+    __syncthreads();  // the third stages and the row scales are free
   }
 }
 
 // Joins the parts of the item that begins in CTA blockIdx.x's run and ends behind
-// it: one warp per row, four channels a lane, parts in the order of the keys.
+// it.  Two warps per row, four channels a lane: one takes the first half of the parts and
+// one the second, each in the order of the keys.
 template <int FMT, int NT>
-__global__ void __launch_bounds__(128) kv_join_kernel(KvAttnArgs a, int ctas) {
+__global__ void __launch_bounds__(256) kv_join_kernel(KvAttnArgs a, int ctas) {
+  __shared__ float4 s_o[4][32];
+  __shared__ float s_l[4];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // for the end of kv_attn_kernel
   const Header hd = reinterpret_cast<const Header*>(a.ws)[blockIdx.x];
   if (hd.parts == 0) return;
   const Partial<NT>* partials = reinterpret_cast<const Partial<NT>*>(a.ws + header_bytes(ctas));
-  const int row = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp >> 2;
+  const int row = blockIdx.y * 4 + (warp & 3);
   const Request x = request_of(a, hd.r);
   const int rr = hd.rb * 8 * NT + row;
-  if (rr >= x.n * a.G) return;
+  const bool live = rr < x.n * a.G;
   auto part = [&](int i) -> const Partial<NT>& { return partials[2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)]; };
+  const int count = live ? hd.parts + 1 : 0, mid = (count + 1) / 2;
   float M = -INFINITY;
-  for (int i = lane; i <= hd.parts; i += 32) M = fmaxf(M, part(i).m[row]);
+  for (int i = lane; i < count; i += 32) M = fmaxf(M, part(i).m[row]);
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
   float L = 0.0f;
   float4 s = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-  for (int i = 0; i <= hd.parts; i++) {
+  const int last = half ? count : mid;
+#pragma unroll 8
+  for (int i = half ? mid : 0; i < last; i++) {
     const Partial<NT>& p = part(i);
     const float m = p.m[row];
     const float w = m == -INFINITY ? 1.0f : ex2(m - M);  // without keys l and O are 0, or NaN
@@ -833,11 +887,19 @@ __global__ void __launch_bounds__(128) kv_join_kernel(KvAttnArgs a, int ctas) {
     s.z += w * v.z;
     s.w += w * v.w;
   }
+  if (half) {
+    s_o[warp & 3][lane] = s;
+    if (lane == 0) s_l[warp & 3] = L;
+  }
+  __syncthreads();
+  if (half || !live) return;
+  const float4 v = s_o[warp][lane];
+  L += s_l[warp];
   const float vst = FMT == 1 ? __ldg(a.c.v_scale) : 1.0f;
   const float f = L == 0.0f ? 1.0f : vst / L;
   const int tok = rr / a.G, head = hd.h * a.G + rr - tok * a.G;
   *reinterpret_cast<uint2*>(a.o + (int64_t(x.q0 + tok) * a.Hq + head) * 128 + lane * 4) =
-      make_uint2(pack_bf16(s.x * f, s.y * f), pack_bf16(s.z * f, s.w * f));
+      make_uint2(pack_bf16((s.x + v.x) * f, (s.y + v.y) * f), pack_bf16((s.z + v.z) * f, (s.w + v.w) * f));
   if (lane == 0)
     a.lse[int64_t(head) * a.total_q + x.q0 + tok] =
         L == 0.0f ? -INFINITY : (M - kOffset + log2f(L)) * 0.6931471805599453f;
@@ -877,7 +939,7 @@ cudaError_t launch(const KvAttnArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas), 2 * NT);
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
