@@ -50,7 +50,7 @@ constexpr float kOffset = 8.0f;           // log2 offset of P
 constexpr float kLazy = 6.0f;             // growth of a row maximum that moves m
 constexpr int kMaxNt = 4;                 // blocks of at most 32 query rows
 constexpr int kMinTiles = 4;              // least tiles of a run, as long as items are cut
-constexpr int kItemTiles = 2;             // what an item costs beside its tiles (drain, merge), in tiles
+constexpr int kItemTiles = 3;             // what an item costs beside its tiles (drain, merge), in tiles
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 // CTAs of an SM for NT 8-row tiles: 16, 12 or 8 warps, as 32 NT accumulator registers
