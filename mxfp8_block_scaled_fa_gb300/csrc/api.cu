@@ -927,7 +927,7 @@ mxfa_status mxfa_get_device_status(mxfa_stream_t stream, unsigned* flags) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(st) != cudaSuccess) return MXFA_ERR_CUDA;
   unsigned f = read_status_quant(st) | read_status_fwd(st) | read_status_bwd(st) | read_status_gemm(st) | read_status_kv(st) |
-               read_status_kv_attn(st);
+               read_status_kv_attn(st) | read_status_kv_prefill(st);
   if (flags) *flags = f;
   if (f & 1u) return MXFA_ERR_TIMEOUT;
   if (f & 2u) return MXFA_ERR_DEVICE_INDEX;

@@ -34,6 +34,7 @@
 // its V fragments are 16 consecutive channels of four keys, two keys' codes
 // merged into bytes before conversion so that the pair (key, key + 1) comes
 // out of one conversion.
+#include "kv_fp4.cuh"
 #include "mx_ptx.cuh"
 #include "mxfa_internal.h"
 
@@ -105,28 +106,6 @@ __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t* h) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -157,17 +136,6 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
   return v;
 }
-// A pair of E8M0 bytes -> binary16 pair 2^(b - 127); 0xFF gives Inf, which times
-// the code 0 it comes with is NaN; a zero-filled byte gives 0.
-__device__ __forceinline__ uint32_t e8m0_pair(uint32_t lo, uint32_t hi) {
-  return pack_f16(__uint_as_float(lo << 23), __uint_as_float(hi << 23));
-}
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(uint16_t(two)));
-  return r;
-}
-
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
@@ -194,7 +162,7 @@ __device__ __forceinline__ Request request_of(const KvAttnArgs& a, int r) {
     return x;
   }
   x.q0 = int(b);
-  x.n = int(e - b);
+  x.n = (e - b) * a.G <= a.split_rows ? int(e - b) : 0;
   x.kv = kv;
   return x;
 }
@@ -696,11 +664,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
       for (int e = 0; e < 8; e++) mx = max(mx, hmax2(abs2(w[e])));
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-      // 2^(14 - floor(log2 amax)), exponent field 268 - E, at most 2^126
-      const int ex = int(mx >> 7);
-      const int fe = mx == 0 ? 127 : min(253, 268 - ex);
-      const float f = __uint_as_float(uint32_t(fe) << 23);
-      const float inv = __uint_as_float(uint32_t(254 - fe) << 23);
+      const float2 sc = q_row_scale(mx);
+      const float f = sc.x, inv = sc.y;
       // channels 16 part + 0..15 belong to lane column c = part / 2, contraction steps
       // 4 (part % 2) .. + 3, four channels a step (b0, b1); a 16-byte word of lane
       // (c, row % 8) holds two steps
@@ -950,8 +915,8 @@ cudaError_t launch(const KvAttnArgs& a, cudaStream_t st) {
 }
 
 template <int FMT>
-cudaError_t launch_fmt(const KvAttnArgs& a, cudaStream_t st) {
-  switch (row_tiles(int64_t(a.max_q) * a.G)) {
+cudaError_t launch_fmt(const KvAttnArgs& a, int nt, cudaStream_t st) {
+  switch (nt) {
     case 1: return launch<FMT, 1>(a, st);
     case 2: return launch<FMT, 2>(a, st);
     case 3: return launch<FMT, 3>(a, st);
@@ -959,27 +924,52 @@ cudaError_t launch_fmt(const KvAttnArgs& a, cudaStream_t st) {
   }
 }
 
+size_t workspace_of(int nt) {
+  const int sms = sm_count_current_device();
+  switch (nt) {
+    case 1: return workspace<1>(sms);
+    case 2: return workspace<2>(sms);
+    case 3: return workspace<3>(sms);
+    default: return workspace<4>(sms);
+  }
+}
+
+// Which kernels a call runs, by the most query rows (tokens x G) a request can have.
+// Up to kFewRows: this file's alone, with tiles for that many rows.  Above: this
+// file's for the requests of at most kMixedRows rows, with tiles for a single token
+// (the decoding requests of a mixed batch), and kv_prefill.cu's for the others.
+constexpr int kFewRows = 64, kMixedRows = 32;
+struct Plan {
+  int nt, split_rows;
+  bool prefill;
+};
+Plan plan_of(int max_q, int G) {
+  const int64_t rows = int64_t(max_q < 1 ? 1 : max_q) * G;
+  if (rows <= kFewRows) return Plan{row_tiles(rows), kFewRows, false};
+  return Plan{row_tiles(G < kMixedRows ? G : kMixedRows), kMixedRows, true};
+}
+
 }  // namespace kva
 
 size_t kv_attn_workspace(int R, int max_q, int G) {
-  (void)R;
-  const int sms = sm_count_current_device();
-  switch (kva::row_tiles(int64_t(max_q < 1 ? 1 : max_q) * G)) {
-    case 1: return kva::workspace<1>(sms);
-    case 2: return kva::workspace<2>(sms);
-    case 3: return kva::workspace<3>(sms);
-    default: return kva::workspace<4>(sms);
-  }
+  const kva::Plan p = kva::plan_of(max_q, G);
+  const size_t few = (kva::workspace_of(p.nt) + 255) & ~size_t(255);
+  return p.prefill ? few + kv_prefill_workspace(R) : few;
 }
 
 cudaError_t launch_kv_attn(const KvAttnArgs& args, cudaStream_t st) {
   clear_stale_error();
   KvAttnArgs a = args;
+  const kva::Plan p = kva::plan_of(a.max_q, a.G);
+  a.split_rows = p.split_rows;
   // one block of query rows per request, and no request has more keys than a row of its
   // table: up to the least run, no item needs cutting
-  a.whole = int64_t(a.max_q) * a.G <= 8 * kva::kMaxNt &&
-            (int64_t(a.width) << a.c.page_shift) <= int64_t(kva::kMinTiles) * kva::kTile;
-  return a.c.fmt == 0 ? kva::launch_fmt<0>(a, st) : kva::launch_fmt<1>(a, st);
+  a.whole = int64_t(a.max_q) * a.G <= 8 * p.nt && (int64_t(a.width) << a.c.page_shift) <= int64_t(kva::kMinTiles) * kva::kTile;
+  if (!p.prefill || a.G <= kva::kMixedRows) {
+    const cudaError_t e = a.c.fmt == 0 ? kva::launch_fmt<0>(a, p.nt, st) : kva::launch_fmt<1>(a, p.nt, st);
+    if (e != cudaSuccess || !p.prefill) return e;
+  }
+  return launch_kv_prefill(a, a.ws + ((kva::workspace_of(p.nt) + 255) & ~size_t(255)), st);
 }
 
 unsigned read_status_kv_attn(cudaStream_t st) {

@@ -16,6 +16,7 @@
 // it reads back as NaN.
 #include <cooperative_groups.h>
 
+#include "kv_fp4.cuh"
 #include "mx_ptx.cuh"
 #include "mxfa_internal.h"
 
@@ -320,21 +321,6 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvRowsArgs a) {
   }
 }
 
-// Eight E2M1 codes -> four pairs of binary16 (exact).
-__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t* h) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // A row without a slot reads as zeros.
 template <int FMT>
 __global__ void __launch_bounds__(256) kv_load_kernel(KvRowsArgs a) {
@@ -368,7 +354,7 @@ __global__ void __launch_bounds__(256) kv_load_kernel(KvRowsArgs a) {
         f.x = __fmul_rn(f.x, st);
         f.y = __fmul_rn(f.y, st);
       }
-      out[i] = pack_bf16x2(f.x, f.y);
+      out[i] = pack_bf16(f.x, f.y);
     }
   }
   uint16_t* dst = w.is_v ? a.v : a.k;

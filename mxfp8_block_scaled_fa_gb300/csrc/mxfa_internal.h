@@ -244,12 +244,15 @@ struct KvAttnArgs {
   float scale_log2;       // softmax scale * log2(e)
   int causal;
   int whole;              // no context is long enough to be cut (set by launch_kv_attn)
+  int split_rows;         // requests of more query rows (tokens x G) belong to kv_prefill.cu (set by launch_kv_attn)
   uint16_t* o;            // bf16 [total_q][Hq][128]
   float* lse;             // [Hq][total_q]
   uint8_t* ws;
 };
 size_t kv_attn_workspace(int R, int max_q, int G);
 cudaError_t launch_kv_attn(const KvAttnArgs& a, cudaStream_t s);
+size_t kv_prefill_workspace(int R);
+cudaError_t launch_kv_prefill(const KvAttnArgs& a, uint8_t* ws, cudaStream_t s);
 
 // Read (and clear) the device status words of every kernel module.
 unsigned read_status_quant(cudaStream_t s);
@@ -258,5 +261,6 @@ unsigned read_status_fwd(cudaStream_t s);
 unsigned read_status_bwd(cudaStream_t s);
 unsigned read_status_kv(cudaStream_t s);
 unsigned read_status_kv_attn(cudaStream_t s);
+unsigned read_status_kv_prefill(cudaStream_t s);
 
 }  // namespace mxfa

@@ -311,6 +311,27 @@ def test_attention_long(mx, fmt, ql, kv):
     assert mx.device_status() == 0
 
 
+MIXED = [
+    # G, H, page, query lengths, kv lengths: prompts among decoding requests, many keys behind
+    # few rows, blocks of rows that end inside a token's group, empty ones
+    (8, 2, 16, [130, 1, 1, 3, 40, 0], [400, 900, 17, 64, 2000, 30]), (4, 1, 64, [100], [9000]), (16, 1, 32, [17, 1, 5], [5000, 3000, 5]),
+    (12, 2, 16, [50, 2], [64, 700]), (1, 4, 128, [513, 1], [513, 1300]), (5, 1, 16, [300, 60, 1], [100, 60, 0]),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("G,H,page,ql,kv", MIXED)
+def test_attention_mixed(mx, fmt, causal, G, H, page, ql, kv):
+    import torch
+    rng = np.random.default_rng(sum(kv) + 3 * sum(ql))
+    args = build(mx, rng, fmt, page, H, G, ql, kv)
+    o, lse = check(mx, *args, causal=causal)
+    o2, lse2 = check(mx, *args, causal=causal, max_q=max(ql) + 5)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert mx.device_status() == 0
+
+
 @pytest.mark.parametrize("fmt", [0, 1])
 @pytest.mark.parametrize("size", [1e-30, 1e-3, 300.0, 1e30])
 def test_attention_query_range(mx, fmt, size):
