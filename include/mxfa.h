@@ -509,8 +509,10 @@ mxfa_status mxfa_kv_append(const mxfa_kv_cache* cache, const void* k, const void
 mxfa_status mxfa_kv_load(const mxfa_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k, void* v,
                          mxfa_stream_t stream);
 
-/* Workspace of mxfa_kv_attn on the current device. */
-size_t mxfa_kv_attn_workspace_size(int R, int max_q, int Hq, int H);
+/* Workspace of mxfa_kv_attn on the current device, for the same R, max_q, Hq and
+ * cache, and max_k = max_blocks * page; 0 where short contexts need none (ws may
+ * then be NULL). */
+size_t mxfa_kv_attn_workspace_size(int R, int max_q, int64_t max_k, int Hq, int H);
 
 /* mxfa_kv_attn -- attention of new query tokens over the cache.
  *  q            bf16 rows of Hq * 128, q_stride elements apart (a multiple of 8),

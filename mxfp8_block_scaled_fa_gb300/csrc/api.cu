@@ -870,9 +870,9 @@ mxfa_status mxfa_kv_load(const mxfa_kv_cache* cache, const int64_t* slots, int64
   return from_cuda(launch_kv_load(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-size_t mxfa_kv_attn_workspace_size(int R, int max_q, int Hq, int H) {
-  if (R < 0 || max_q < 0 || H <= 0 || Hq <= 0 || Hq % H) return 0;
-  return kv_attn_workspace(R, max_q, Hq / H);
+size_t mxfa_kv_attn_workspace_size(int R, int max_q, int64_t max_k, int Hq, int H) {
+  if (R < 0 || max_q < 0 || max_k < 0 || H <= 0 || Hq <= 0 || Hq % H) return 0;
+  return kv_attn_workspace(R, max_q, max_k, Hq / H);
 }
 
 mxfa_status mxfa_kv_attn(const mxfa_kv_cache* cache, const void* q, int64_t q_stride, int64_t total_q,
@@ -883,7 +883,7 @@ mxfa_status mxfa_kv_attn(const mxfa_kv_cache* cache, const void* q, int64_t q_st
   memset(&a, 0, sizeof(a));
   mxfa_status s = check_cache(cache, a.c);
   if (s) return s;
-  if (!q || !cu_q || !kv_lens || !block_table || !o || !lse || !ws) return MXFA_ERR_INVALID_ARG;
+  if (!q || !cu_q || !kv_lens || !block_table || !o || !lse) return MXFA_ERR_INVALID_ARG;
   if (total_q < 0 || R < 0 || max_blocks <= 0 || max_q < 0 || Hq <= 0 || Hq % a.c.H) return MXFA_ERR_INVALID_ARG;
   if (!(softmax_scale > 0.0f) || !std::isfinite(softmax_scale)) return MXFA_ERR_INVALID_ARG;
   if (total_q > 1 && q_stride < int64_t(Hq) * 128) return MXFA_ERR_INVALID_ARG;
@@ -909,7 +909,9 @@ mxfa_status mxfa_kv_attn(const mxfa_kv_cache* cache, const void* q, int64_t q_st
   a.o = static_cast<uint16_t*>(o);
   a.lse = lse;
   a.ws = static_cast<uint8_t*>(ws);
-  if (ws_bytes < kv_attn_workspace(R, max_q, a.G)) return MXFA_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = kv_attn_workspace(R, max_q, int64_t(max_blocks) * a.c.page, a.G);
+  if (need > 0 && !ws) return MXFA_ERR_INVALID_ARG;
+  if (ws_bytes < need) return MXFA_ERR_WORKSPACE_TOO_SMALL;
   return from_cuda(launch_kv_attn(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -942,17 +942,19 @@ constexpr int kFewRows = 64, kMixedRows = 32;
 struct Plan {
   int nt, split_rows;
   bool prefill;
+  bool whole;  // one block of rows per request and no item worth cutting: no workspace
 };
-Plan plan_of(int max_q, int G) {
+Plan plan_of(int max_q, int64_t max_k, int G) {
   const int64_t rows = int64_t(max_q < 1 ? 1 : max_q) * G;
-  if (rows <= kFewRows) return Plan{row_tiles(rows), kFewRows, false};
-  return Plan{row_tiles(G < kMixedRows ? G : kMixedRows), kMixedRows, true};
+  if (rows <= kFewRows) return Plan{row_tiles(rows), kFewRows, false, rows <= 8 * kMaxNt && max_k <= kMinTiles * kTile};
+  return Plan{row_tiles(G < kMixedRows ? G : kMixedRows), kMixedRows, true, false};
 }
 
 }  // namespace kva
 
-size_t kv_attn_workspace(int R, int max_q, int G) {
-  const kva::Plan p = kva::plan_of(max_q, G);
+size_t kv_attn_workspace(int R, int max_q, int64_t max_k, int G) {
+  const kva::Plan p = kva::plan_of(max_q, max_k, G);
+  if (p.whole) return 0;
   const size_t few = (kva::workspace_of(p.nt) + 255) & ~size_t(255);
   return p.prefill ? few + kv_prefill_workspace(R) : few;
 }
@@ -960,11 +962,10 @@ size_t kv_attn_workspace(int R, int max_q, int G) {
 cudaError_t launch_kv_attn(const KvAttnArgs& args, cudaStream_t st) {
   clear_stale_error();
   KvAttnArgs a = args;
-  const kva::Plan p = kva::plan_of(a.max_q, a.G);
+  // no request has more keys than a row of its table
+  const kva::Plan p = kva::plan_of(a.max_q, int64_t(a.width) << a.c.page_shift, a.G);
   a.split_rows = p.split_rows;
-  // one block of query rows per request, and no request has more keys than a row of its
-  // table: up to the least run, no item needs cutting
-  a.whole = int64_t(a.max_q) * a.G <= 8 * p.nt && (int64_t(a.width) << a.c.page_shift) <= int64_t(kva::kMinTiles) * kva::kTile;
+  a.whole = p.whole;
   if (!p.prefill || a.G <= kva::kMixedRows) {
     const cudaError_t e = a.c.fmt == 0 ? kva::launch_fmt<0>(a, p.nt, st) : kva::launch_fmt<1>(a, p.nt, st);
     if (e != cudaSuccess || !p.prefill) return e;

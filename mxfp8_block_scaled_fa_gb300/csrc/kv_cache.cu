@@ -215,10 +215,15 @@ cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t st) {
   const int most = a.aliased ? 8 : 128;
   int grid = 1;
   while (grid < most && grid < ctas) grid *= 2;
+  const size_t bytes = size_t(3 * int64_t(a.R) + 1) * sizeof(int32_t);
+  if (grid == 1) {  // a cluster of its own
+    kv_plan_kernel<<<1, kPlanThreads, bytes, st>>>(a);
+    return cudaGetLastError();
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid));
   cfg.blockDim = dim3(kPlanThreads);
-  cfg.dynamicSmemBytes = size_t(3 * int64_t(a.R) + 1) * sizeof(int32_t);
+  cfg.dynamicSmemBytes = bytes;
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;

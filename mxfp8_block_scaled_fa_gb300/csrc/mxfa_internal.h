@@ -249,7 +249,7 @@ struct KvAttnArgs {
   float* lse;             // [Hq][total_q]
   uint8_t* ws;
 };
-size_t kv_attn_workspace(int R, int max_q, int G);
+size_t kv_attn_workspace(int R, int max_q, int64_t max_k, int G);
 cudaError_t launch_kv_attn(const KvAttnArgs& a, cudaStream_t s);
 size_t kv_prefill_workspace(int R);
 cudaError_t launch_kv_prefill(const KvAttnArgs& a, uint8_t* ws, cudaStream_t s);

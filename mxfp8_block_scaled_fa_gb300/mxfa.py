@@ -31,7 +31,6 @@ tokens' q [T, Hq, 128] and k, v [T, H, 128] in request order:
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -129,7 +128,7 @@ def lib() -> ctypes.CDLL:
             "mxfa_kv_plan": (I, [P, P, I, P, I, P, I64, P, P, I, I64, P, P, P, P, P]),
             "mxfa_kv_append": (I, [P, P, P, I64, I64, I64, P, P]),
             "mxfa_kv_load": (I, [P, P, I64, P, P, P]),
-            "mxfa_kv_attn_workspace_size": (S, [I, I, I, I]),
+            "mxfa_kv_attn_workspace_size": (S, [I, I, I64, I, I]),
             "mxfa_kv_attn": (I, [P, P, I64, I64, P, P, I, P, I, I, I, F, I, P, P, P, S, P]),
         }
         for name, (res, args) in sig.items():
@@ -647,8 +646,8 @@ def mxfa_kv_load(pages: KvPages, slots, tokens, k, v, stream=None):
                               _stream(stream)), "mxfa_kv_load")
 
 
-def mxfa_kv_attn_workspace_size(R, max_q, Hq, H) -> int:
-    return int(lib().mxfa_kv_attn_workspace_size(R, max_q, Hq, H))
+def mxfa_kv_attn_workspace_size(R, max_q, max_k, Hq, H) -> int:
+    return int(lib().mxfa_kv_attn_workspace_size(R, max_q, max_k, Hq, H))
 
 
 def mxfa_kv_attn(pages: KvPages, q, q_stride, total_q, cu_q, kv_lens, R, block_table, max_blocks,
@@ -658,47 +657,53 @@ def mxfa_kv_attn(pages: KvPages, q, q_stride, total_q, cu_q, kv_lens, R, block_t
                               _p(o), _p(lse), _p(ws), ws_bytes, _stream(stream)), "mxfa_kv_attn")
 
 
-def _on(dev: torch.device, **tensors):
-    """Every tensor is on device `dev` (None passes)."""
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+def _raw_stream(index: int) -> int:
+    """The current stream of CUDA device `index`."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
-def _flat(dtype, **tensors):
-    """Every tensor has this dtype and is contiguous."""
-    for name, t in tensors.items():
-        if t.dtype != dtype:
-            raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} is not contiguous")
+def _flat(name: str, t: torch.Tensor, dtype, index: int):
+    """t has this dtype, is contiguous and on CUDA device `index` (-1: the CPU)."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected device {index}")
 
 
-def _rows(name: str, x: torch.Tensor, heads: int):
-    """bf16 [tokens, heads, 128] with the heads of a token one after another -> elements
-    between tokens."""
-    if x.dtype != torch.bfloat16:
+def _rows(name: str, x: torch.Tensor, heads: int, index: int):
+    """bf16 [tokens, heads, 128] with the heads of a token one after another, on device `index` ->
+    elements between tokens."""
+    if x.dtype is not torch.bfloat16:
         raise TypeError(f"{name} is {x.dtype}, expected torch.bfloat16")
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != 128:
-        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected [tokens, {heads}, 128]")
-    if x.shape[0] and (x.stride(2) != 1 or (heads > 1 and x.stride(1) != 128)):
+    shape = x.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != 128:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [tokens, {heads}, 128]")
+    stride = x.stride()
+    if shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != 128)):
         raise ValueError(f"{name}: the heads of a token must lie one after another")
-    return x.stride(0) if x.shape[0] > 1 else heads * 128
+    if x.get_device() != index:
+        raise ValueError(f"{name} is on {x.device}, expected device {index}")
+    return stride[0] if shape[0] > 1 else heads * 128
 
 
-_same = contextlib.nullcontext()
+def _here(index: int, stream) -> bool:
+    """Whether a call on device `index` can go ahead: it is the current device, and the stream the
+    current one.  Otherwise the caller starts again within _place()."""
+    if index < 0:
+        raise ValueError("the 4-bit cache lives on a CUDA device")
+    return stream is None and torch._C._cuda_getDevice() == index
 
 
-def _place(dev: torch.device, stream):
-    """The context in which a call on `dev` allocates and launches: its stream if one is given
-    (memory taken from the allocator then belongs to that stream), else the current one of `dev`."""
-    if dev.type != "cuda":
-        raise ValueError(f"the 4-bit cache lives on a CUDA device, not {dev}")
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-        return torch.cuda.stream(stream)
-    return _same if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+def _place(index: int, stream):
+    """The context in which a call on device `index` allocates and launches: its stream if one is
+    given (memory taken from the allocator then belongs to that stream), else the device's current one."""
+    if stream is None:
+        return torch.cuda.device(index)
+    if stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on device {index}")
+    return torch.cuda.stream(stream)
 
 
 @dataclass
@@ -713,30 +718,36 @@ class KvCache:
     v_scale: Optional[torch.Tensor] = None
 
     def __post_init__(self):
-        if self.fmt not in (KV_MXFP4, KV_NVFP4):
-            raise ValueError(f"unknown cache format {self.fmt}")
-        if self.k.dim() != 4:
+        fmt, k = self.fmt, self.k
+        if fmt != KV_MXFP4 and fmt != KV_NVFP4:
+            raise ValueError(f"unknown cache format {fmt}")
+        shape = k.shape
+        if len(shape) != 4 or shape[3] != 64 or self.v.shape != shape:
             raise ValueError("k and v must be [num_blocks, H, page, 64]")
-        n, h, page, _ = shape = self.k.shape
-        sf = (n, h, page, 4 if self.fmt == KV_MXFP4 else 8)
-        if shape != (n, h, page, 64) or self.v.shape != shape:
-            raise ValueError("k and v must be [num_blocks, H, page, 64]")
+        n, h, page, _ = shape
+        sf = (n, h, page, 4 if fmt == KV_MXFP4 else 8)
         if self.k_sf.shape != sf or self.v_sf.shape != sf:
             raise ValueError(f"k_sf and v_sf must be {list(sf)}")
-        _flat(torch.uint8, k=self.k, v=self.v, k_sf=self.k_sf, v_sf=self.v_sf)
-        if self.fmt == KV_NVFP4:
-            if self.k_scale is None or self.v_scale is None:
+        index = self.index = k.get_device()
+        _flat("k", k, torch.uint8, index)
+        _flat("v", self.v, torch.uint8, index)
+        _flat("k_sf", self.k_sf, torch.uint8, index)
+        _flat("v_sf", self.v_sf, torch.uint8, index)
+        ks = vs = None
+        if fmt == KV_NVFP4:
+            ks, vs = self.k_scale, self.v_scale
+            if ks is None or vs is None:
                 raise ValueError("an NVFP4 cache needs k_scale and v_scale")
-            _flat(torch.float32, k_scale=self.k_scale, v_scale=self.v_scale)
-            if self.k_scale.numel() != 1 or self.v_scale.numel() != 1:
+            _flat("k_scale", ks, torch.float32, index)
+            _flat("v_scale", vs, torch.float32, index)
+            if ks.numel() != 1 or vs.numel() != 1:
                 raise ValueError("k_scale and v_scale have one element")
+            ks, vs = ks.data_ptr(), vs.data_ptr()
         else:
             self.k_scale = self.v_scale = None
-        _on(self.k.device, v=self.v, k_sf=self.k_sf, v_sf=self.v_sf, k_scale=self.k_scale,
-            v_scale=self.v_scale)
-        self.pages = KvPages(self.k.data_ptr(), self.v.data_ptr(), self.k_sf.data_ptr(),
-                             self.v_sf.data_ptr(), _p(self.k_scale), _p(self.v_scale), n, page, h,
-                             128, self.fmt)
+        self.H, self.page = h, page
+        self.pages = KvPages(k.data_ptr(), self.v.data_ptr(), self.k_sf.data_ptr(),
+                             self.v_sf.data_ptr(), ks, vs, n, page, h, 128, fmt)
 
     @staticmethod
     def empty(num_blocks: int, H: int, page: int = 64, fmt: int = KV_MXFP4, k_scale: float = 1.0,
@@ -774,28 +785,40 @@ def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.T
     returns offsets, lengths, and slot and position of `tokens` tokens.  `out`
     gives the result's buffers; its kv_lens may be ctx_lens and its ring_state
     may be ring_state, for a step that is captured once and replayed."""
-    R, dev = ctx_lens.numel(), ctx_lens.device
-    if new_lens.numel() != R or block_table.dim() != 2 or block_table.shape[0] != R:
+    R, index = ctx_lens.numel(), ctx_lens.get_device()
+    shape = block_table.shape
+    if new_lens.numel() != R or len(shape) != 2 or shape[0] != R:
         raise ValueError("ctx_lens, new_lens and block_table describe different numbers of requests")
-    with _place(dev, stream):
-        if out is None:
-            i32, i64 = dict(dtype=torch.int32, device=dev), dict(dtype=torch.int64, device=dev)
-            out = KvStep(torch.empty(R + 1, **i32), torch.empty(R, **i32), torch.empty(tokens, **i64),
-                         torch.empty(tokens, **i32), torch.empty(3, **i64))
-        elif (out.cu_q.numel(), out.kv_lens.numel(), out.slots.numel(), out.positions.numel()) != (
+    i32, i64 = torch.int32, torch.int64
+    _flat("ctx_lens", ctx_lens, i32, index)
+    _flat("new_lens", new_lens, i32, index)
+    _flat("block_table", block_table, i32, index)
+    _flat("free_ring", free_ring, i32, index)
+    _flat("ring_state", ring_state, i64, index)
+    if not _here(index, stream):
+        with _place(index, stream):
+            return kv_plan(ctx_lens, new_lens, block_table, free_ring, ring_state, page, tokens, out)
+    if out is None:
+        dev = ctx_lens.device
+        out = KvStep(torch.empty(R + 1, dtype=i32, device=dev), torch.empty(R, dtype=i32, device=dev),
+                     torch.empty(tokens, dtype=i64, device=dev),
+                     torch.empty(tokens, dtype=i32, device=dev), torch.empty(3, dtype=i64, device=dev))
+    else:
+        if (out.cu_q.numel(), out.kv_lens.numel(), out.slots.numel(), out.positions.numel()) != (
                 R + 1, R, tokens, tokens):
             raise ValueError("out has buffers of other sizes")
-        if ring_state.numel() != 3 or out.ring_state.numel() != 3:
-            raise ValueError("ring_state has three elements")
-        _flat(torch.int32, ctx_lens=ctx_lens, new_lens=new_lens, block_table=block_table,
-              free_ring=free_ring, cu_q=out.cu_q, kv_lens=out.kv_lens, positions=out.positions)
-        _flat(torch.int64, ring_state=ring_state, slots=out.slots, ring_state_out=out.ring_state)
-        _on(dev, new_lens=new_lens, block_table=block_table, free_ring=free_ring,
-            ring_state=ring_state, cu_q=out.cu_q, kv_lens=out.kv_lens, slots=out.slots,
-            positions=out.positions, ring_state_out=out.ring_state)
-        mxfa_kv_plan(ctx_lens, new_lens, R, block_table, block_table.shape[1], free_ring,
-                     free_ring.numel(), ring_state, out.ring_state, page, tokens, out.cu_q,
-                     out.kv_lens, out.slots, out.positions, stream)
+        _flat("cu_q", out.cu_q, i32, index)
+        _flat("kv_lens", out.kv_lens, i32, index)
+        _flat("slots", out.slots, i64, index)
+        _flat("positions", out.positions, i32, index)
+        _flat("out.ring_state", out.ring_state, i64, index)
+    if ring_state.numel() != 3 or out.ring_state.numel() != 3:
+        raise ValueError("ring_state has three elements")
+    _check(lib().mxfa_kv_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), R, block_table.data_ptr(),
+                              shape[1], free_ring.data_ptr(), free_ring.numel(),
+                              ring_state.data_ptr(), out.ring_state.data_ptr(), page, tokens,
+                              out.cu_q.data_ptr(), out.kv_lens.data_ptr(), out.slots.data_ptr(),
+                              out.positions.data_ptr(), _raw_stream(index)), "mxfa_kv_plan")
     return out
 
 
@@ -803,34 +826,42 @@ def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
     """Quantizes bf16 k, v [tokens, H, 128] (tokens may be strided, as slices of a
     fused projection are) into the cache rows `slots` (int64 [tokens], distinct;
     negative: skipped)."""
-    H = cache.pages.H
-    ks, vs = _rows("k", k, H), _rows("v", v, H)
-    if v.shape[0] != k.shape[0] or slots.numel() != k.shape[0]:
+    index, H = cache.index, cache.H
+    ks, vs = _rows("k", k, H, index), _rows("v", v, H, index)
+    T = k.shape[0]
+    if v.shape[0] != T or slots.numel() != T:
         raise ValueError("k, v and slots have different numbers of tokens")
-    _flat(torch.int64, slots=slots)
-    _on(cache.k.device, k=k, v=v, slots=slots)
-    with _place(cache.k.device, stream):
-        if k.shape[0]:
-            mxfa_kv_append(cache.pages, k, v, ks, vs, k.shape[0], slots, stream)
+    _flat("slots", slots, torch.int64, index)
+    if not _here(index, stream):
+        with _place(index, stream):
+            return kv_append(cache, k, v, slots)
+    if T:
+        _check(lib().mxfa_kv_append(ctypes.byref(cache.pages), k.data_ptr(), v.data_ptr(), ks, vs, T,
+                                    slots.data_ptr(), _raw_stream(index)), "mxfa_kv_append")
 
 
 def kv_load(cache: KvCache, slots: torch.Tensor, out=None, stream=None):
     """The cached values of `slots` (int64 [tokens]) -> bf16 (k, v) [tokens, H, 128];
     zeros for a negative slot."""
-    shape = (slots.numel(), cache.pages.H, 128)
-    dev = cache.k.device
-    with _place(dev, stream):
-        if out is None:
-            out = (torch.empty(shape, dtype=torch.bfloat16, device=dev),
-                   torch.empty(shape, dtype=torch.bfloat16, device=dev))
+    index, T = cache.index, slots.numel()
+    shape = (T, cache.H, 128)
+    _flat("slots", slots, torch.int64, index)
+    if not _here(index, stream):
+        with _place(index, stream):
+            return kv_load(cache, slots, out)
+    if out is None:
+        dev = slots.device
+        k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
         k, v = out
         if k.shape != shape or v.shape != shape:
             raise ValueError(f"out must be two tensors of shape {shape}")
-        _flat(torch.int64, slots=slots)
-        _flat(torch.bfloat16, k=k, v=v)
-        _on(dev, slots=slots, k=k, v=v)
-        if shape[0]:
-            mxfa_kv_load(cache.pages, slots, shape[0], k, v, stream)
+        _flat("out k", k, torch.bfloat16, index)
+        _flat("out v", v, torch.bfloat16, index)
+    if T:
+        _check(lib().mxfa_kv_load(ctypes.byref(cache.pages), slots.data_ptr(), T, k.data_ptr(),
+                                  v.data_ptr(), _raw_stream(index)), "mxfa_kv_load")
     return k, v
 
 
@@ -842,33 +873,50 @@ def kv_attention(q: torch.Tensor, cache: KvCache, cu_q: torch.Tensor, kv_lens: t
     (int32 [R + 1]), kv_lens (int32 [R], new tokens included) and block_table as
     kv_plan gives them; max_q: the most query tokens of a request.  causal aligns
     the last query to the last key.  Rows outside cu_q's are not written."""
-    H, dev = cache.pages.H, cache.k.device
-    if q.dim() != 3 or q.shape[1] == 0 or q.shape[1] % H:
-        raise ValueError(f"q has shape {tuple(q.shape)}, expected [tokens, a multiple of {H}, 128]")
-    T, Hq, _ = q.shape
-    qs = _rows("q", q, Hq)
+    H, index = cache.H, cache.index
+    shape = q.shape
+    if len(shape) != 3 or shape[1] == 0 or shape[1] % H:
+        raise ValueError(f"q has shape {tuple(shape)}, expected [tokens, a multiple of {H}, 128]")
+    T, Hq, _ = shape
+    qs = _rows("q", q, Hq, index)
     R = kv_lens.numel()
-    if cu_q.numel() != R + 1 or block_table.dim() != 2 or block_table.shape[0] != R:
+    tshape = block_table.shape
+    if cu_q.numel() != R + 1 or len(tshape) != 2 or tshape[0] != R:
         raise ValueError("cu_q, kv_lens and block_table describe different numbers of requests")
-    _flat(torch.int32, cu_q=cu_q, kv_lens=kv_lens, block_table=block_table)
-    with _place(dev, stream):
-        if out is None:
-            o = torch.empty((T, Hq, 128), dtype=torch.bfloat16, device=dev)
-            lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
-        else:
-            o, lse = out
-            if o.shape != q.shape or lse.shape != (Hq, T):
-                raise ValueError(f"out must have shapes {tuple(q.shape)} and {(Hq, T)}")
-            _flat(torch.bfloat16, o=o)
-            _flat(torch.float32, lse=lse)
-        _on(dev, q=q, cu_q=cu_q, kv_lens=kv_lens, block_table=block_table, o=o, lse=lse, ws=ws)
-        if T == 0 or R == 0:
-            return o, lse
-        if ws is None:
-            ws = torch.empty(mxfa_kv_attn_workspace_size(R, max_q, Hq, H), dtype=torch.uint8,
-                             device=dev)
-        mxfa_kv_attn(cache.pages, q, qs, T, cu_q, kv_lens, R, block_table, block_table.shape[1], max_q,
-                     Hq, scale, causal, o, lse, ws, ws.numel() * ws.element_size(), stream)
+    i32 = torch.int32
+    _flat("cu_q", cu_q, i32, index)
+    _flat("kv_lens", kv_lens, i32, index)
+    _flat("block_table", block_table, i32, index)
+    if not _here(index, stream):
+        with _place(index, stream):
+            return kv_attention(q, cache, cu_q, kv_lens, block_table, max_q, scale, causal, out, ws)
+    dev = q.device
+    if out is None:
+        o = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+    else:
+        o, lse = out
+        if o.shape != shape or lse.shape != (Hq, T):
+            raise ValueError(f"out must have shapes {tuple(shape)} and {(Hq, T)}")
+        _flat("out o", o, torch.bfloat16, index)
+        _flat("out lse", lse, torch.float32, index)
+    if T == 0 or R == 0:
+        return o, lse
+    L = lib()
+    ws_at, ws_bytes = None, 0
+    if ws is None:
+        ws_bytes = L.mxfa_kv_attn_workspace_size(R, max_q, tshape[1] * cache.page, Hq, H)
+        if ws_bytes:
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+            ws_at = ws.data_ptr()
+    elif ws.get_device() != index:
+        raise ValueError(f"ws is on {ws.device}, expected device {index}")
+    else:
+        ws_at, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    _check(L.mxfa_kv_attn(ctypes.byref(cache.pages), q.data_ptr(), qs, T, cu_q.data_ptr(),
+                          kv_lens.data_ptr(), R, block_table.data_ptr(), tshape[1], max_q, Hq, scale,
+                          1 if causal else 0, o.data_ptr(), lse.data_ptr(), ws_at, ws_bytes,
+                          _raw_stream(index)), "mxfa_kv_attn")
     return o, lse
 
 

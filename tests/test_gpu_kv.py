@@ -522,7 +522,7 @@ def test_two_graphs_and_streams_at_once(mx):
     graphs, outs = [], []
     for c, q, cu, kv, table, _ in sets:
         o = (torch.full(q.shape, 77.0, dtype=torch.bfloat16, device="cuda"), torch.full((8, q.shape[0]), 77.0, device="cuda"))
-        ws = torch.full((mx.mxfa_kv_attn_workspace_size(3, 1, 8, 2),), 0xFF, dtype=torch.uint8, device="cuda")
+        ws = torch.full((mx.mxfa_kv_attn_workspace_size(3, 1, table.shape[1] * 64, 8, 2),), 0xFF, dtype=torch.uint8, device="cuda")
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             mx.kv_attention(q, c, cu, kv, table, 1, 128 ** -0.5, out=o, ws=ws)
@@ -539,11 +539,18 @@ def test_two_graphs_and_streams_at_once(mx):
     assert mx.device_status() == 0
 
 
-def test_workspace_too_small(mx):
+def test_workspace(mx):
+    """Short contexts need none; where one is needed, too small a one is refused."""
     import torch
     rng = np.random.default_rng(13)
-    c, q, cu, kv, table, _ = build(mx, rng, 0, 16, 1, 4, [1], [50])
-    need = mx.mxfa_kv_attn_workspace_size(1, 1, 4, 1)
-    with pytest.raises(mx.MxfaError) as e:
-        mx.kv_attention(q, c, cu, kv, table, 1, 0.1, ws=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
-    assert e.value.status == 4
+    for keys, need_any in ((50, False), (5000, True)):
+        c, q, cu, kv, table, slots = build(mx, rng, 0, 16, 1, 4, [1], [keys])
+        need = mx.mxfa_kv_attn_workspace_size(1, 1, table.shape[1] * 16, 4, 1)
+        assert (need > 0) == need_any
+        if need:
+            with pytest.raises(mx.MxfaError) as e:
+                mx.kv_attention(q, c, cu, kv, table, 1, 0.1, ws=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+            assert e.value.status == 4
+            o = [torch.full(x, 77.0, dtype=d, device="cuda") for x, d in ((q.shape, torch.bfloat16), ((4, q.shape[0]), torch.float32))]
+            mx.kv_attention(q, c, cu, kv, table, 1, 128 ** -0.5, out=o, ws=torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda"))
+            compare(c, q, cu, slots, True, 128 ** -0.5, *o)

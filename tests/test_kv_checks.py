@@ -87,13 +87,13 @@ def test_row_call_checks(mx):
 
 def test_attention_checks(mx):
     L, ref = mx.lib(), ctypes.byref(_cache(mx))
-    base = dict(q=0x10, qs=512, T=3, cu=0x10, kv=0x10, R=1, bt=0x10, nb=4, mq=3, Hq=4, s=0.1, c=1, o=0x10, lse=0x10, ws=0x10,
+    base = dict(q=0x10, qs=512, T=3, cu=0x10, kv=0x10, R=1, bt=0x10, nb=64, mq=3, Hq=4, s=0.1, c=1, o=0x10, lse=0x10, ws=0x10,
                 wb=1 << 30)
 
     def call(**kw):
         d = dict(base, **kw)
         return L.mxfa_kv_attn(ref, *d.values(), None)
-    for n in ("q", "cu", "kv", "bt", "o", "lse", "ws"):
+    for n in ("q", "cu", "kv", "bt", "o", "lse"):
         assert call(**{n: None}) == 1, n
     assert call(Hq=3) == 1 and call(Hq=0) == 1 and call(nb=0) == 1 and call(R=-1) == 1 and call(mq=-1) == 1
     assert call(s=0.0) == 1 and call(s=float("nan")) == 1 and call(s=float("inf")) == 1
@@ -168,4 +168,4 @@ def test_sizes(mx):
     L = mx.lib()
     assert L.mxfa_kv_codes_bytes(10, 16, 3) == 10 * 16 * 3 * 64
     assert L.mxfa_kv_sf_bytes(10, 16, 3, 0) == 10 * 16 * 3 * 4 and L.mxfa_kv_sf_bytes(10, 16, 3, 1) == 10 * 16 * 3 * 8
-    assert L.mxfa_kv_codes_bytes(-1, 16, 3) == 0 and L.mxfa_kv_attn_workspace_size(1, 1, 5, 2) == 0
+    assert L.mxfa_kv_codes_bytes(-1, 16, 3) == 0 and L.mxfa_kv_attn_workspace_size(1, 1, 100, 5, 2) == 0
