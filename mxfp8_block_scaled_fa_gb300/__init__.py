@@ -23,5 +23,6 @@ def __getattr__(name):
                                             "kv_append", "kv_load", "kv_attention",
                                             "device_status"):
         from . import mxfa as _m
-        return getattr(_m, name)
+        value = globals()[name] = getattr(_m, name)  # later uses find it without this function
+        return value
     raise AttributeError(name)

@@ -840,7 +840,7 @@ mxfa_status mxfa_kv_append(const mxfa_kv_cache* cache, const void* k, const void
   if (s) return s;
   if (!k || !v || !slots || tokens < 0) return MXFA_ERR_INVALID_ARG;
   if (tokens > 1 && (k_stride < int64_t(a.c.H) * 128 || v_stride < int64_t(a.c.H) * 128)) return MXFA_ERR_INVALID_ARG;
-  if (tokens >= (int64_t(1) << 31) || tokens * a.c.H >= (int64_t(1) << 31) - 16) return MXFA_ERR_UNSUPPORTED;
+  if (tokens >= (int64_t(1) << 31) || tokens * a.c.H >= (int64_t(1) << 31) - 128) return MXFA_ERR_UNSUPPORTED;
   if (!aligned16(k) || !aligned16(v) || !aligned8(slots) || (tokens > 1 && (k_stride % 8 || v_stride % 8)))
     return MXFA_ERR_MISALIGNED;
   if (tokens == 0) return MXFA_OK;
@@ -860,7 +860,7 @@ mxfa_status mxfa_kv_load(const mxfa_kv_cache* cache, const int64_t* slots, int64
   mxfa_status s = check_cache(cache, a.c);
   if (s) return s;
   if (!k || !v || !slots || tokens < 0) return MXFA_ERR_INVALID_ARG;
-  if (tokens >= (int64_t(1) << 31) || tokens * a.c.H >= (int64_t(1) << 31) - 16) return MXFA_ERR_UNSUPPORTED;
+  if (tokens >= (int64_t(1) << 31) || tokens * a.c.H >= (int64_t(1) << 31) - 128) return MXFA_ERR_UNSUPPORTED;
   if (!aligned16(k) || !aligned16(v) || !aligned8(slots)) return MXFA_ERR_MISALIGNED;
   if (tokens == 0) return MXFA_OK;
   a.k = static_cast<uint16_t*>(k);

@@ -250,6 +250,13 @@ __device__ __forceinline__ uint32_t pack8_e2m1(const float* y) {
   return r;
 }
 
+// Sixteen bytes that nothing reads again soon.
+__device__ __forceinline__ uint4 ldg_stream(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 // Where row `r` of the call (token, head, K or V) lives in the cache; false if
 // its slot is negative or out of range.
 struct KvRow {
@@ -274,111 +281,143 @@ __device__ __forceinline__ bool kv_row(const KvRowsArgs& a, uint32_t r, KvRow& w
   return true;
 }
 
-template <int FMT>
+// The rows of a CTA: sixteen lanes to each, N a lane group, whose loads are all in
+// flight before the first is used.
+template <int FMT, int N>
 __global__ void __launch_bounds__(256) kv_append_kernel(KvRowsArgs a) {
   const int lane = threadIdx.x & 15;
-  const uint32_t rows = uint32_t(a.tokens * a.c.H * 2);  // below 2^32 - 16
-  const uint32_t r = blockIdx.x * 16u + (threadIdx.x >> 4);
-  KvRow w;
-  const bool live = r < rows && kv_row(a, r, w);
-  uint4 x = make_uint4(0, 0, 0, 0);
-  if (live) {
-    const uint16_t* src = w.is_v ? a.v + w.token * a.v_stride : a.k + w.token * a.k_stride;
-    x = __ldg(reinterpret_cast<const uint4*>(src + w.head * 128 + lane * 8));
-  }
-  const uint32_t m2 = __vmaxu2(__vmaxu2(abs2(x.x), abs2(x.y)), __vmaxu2(abs2(x.z), abs2(x.w)));
-  uint32_t mx = hmax2(m2);
-  mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-  if (FMT == 0) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-  if (!live) return;
-  const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-  float y[8];
-  uint32_t sc;
-  const bool bad = mx >= 0x7F80u;
-  if (FMT == 0) {
-    // bf16 exponent field - 2, clamped to the fields of 2^-23 and 2^13
-    sc = min(max(int(mx >> 7) - 2, 104), 140);
-    const float f = __uint_as_float((254u - sc) << 23);
+  const uint32_t rows = uint32_t(a.tokens * a.c.H * 2);  // below 2^32 - 128
+  KvRow w[N];
+  uint4 x[N];
+  bool live[N];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      y[2 * i] = bf_lo(xs[i]) * f;
-      y[2 * i + 1] = bf_hi(xs[i]) * f;
+  for (int i = 0; i < N; i++) {
+    const uint32_t r = blockIdx.x * uint32_t(16 * N) + i * 16u + (threadIdx.x >> 4);
+    live[i] = r < rows && kv_row(a, r, w[i]);
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (live[i]) {
+      const uint16_t* src = w[i].is_v ? a.v + w[i].token * a.v_stride : a.k + w[i].token * a.k_stride;
+      x[i] = ldg_stream(reinterpret_cast<const uint4*>(src + w[i].head * 128 + lane * 8));
     }
-    if (bad) sc = 0xFFu;
-  } else {
-    const float st = __ldg(w.is_v ? a.c.v_scale : a.c.k_scale);
-    sc = cvt_e4m3x2(__fdiv_rn(__uint_as_float(mx << 16), __fmul_rn(6.0f, st)), 0.0f) & 0xFFu;
-    const float unit = __fmul_rn(e4m3x2_to_float2(sc).x, st);
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      y[2 * i] = unit > 0.0f ? __fdiv_rn(bf_lo(xs[i]), unit) : 0.0f;
-      y[2 * i + 1] = unit > 0.0f ? __fdiv_rn(bf_hi(xs[i]), unit) : 0.0f;
-    }
-    if (bad) sc = 0x7Fu;
   }
-  uint8_t* codes = w.is_v ? a.c.v : a.c.k;
-  uint8_t* sf = w.is_v ? a.c.v_sf : a.c.k_sf;
-  reinterpret_cast<uint32_t*>(codes + w.at * 64)[lane] = bad ? 0u : pack8_e2m1(y);
-  if (FMT == 0) {
-    if ((lane & 3) == 0) sf[w.at * 4 + (lane >> 2)] = uint8_t(sc);
-  } else {
-    if ((lane & 1) == 0) sf[w.at * 8 + (lane >> 1)] = uint8_t(sc);
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    const uint32_t m2 = __vmaxu2(__vmaxu2(abs2(x[i].x), abs2(x[i].y)), __vmaxu2(abs2(x[i].z), abs2(x[i].w)));
+    uint32_t mx = hmax2(m2);
+    mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+    if (FMT == 0) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+    if (!live[i]) continue;
+    const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    float y[8];
+    uint32_t sc;
+    const bool bad = mx >= 0x7F80u;
+    if (FMT == 0) {
+      // bf16 exponent field - 2, clamped to the fields of 2^-23 and 2^13
+      sc = min(max(int(mx >> 7) - 2, 104), 140);
+      const float f = __uint_as_float((254u - sc) << 23);
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        y[2 * e] = bf_lo(xs[e]) * f;
+        y[2 * e + 1] = bf_hi(xs[e]) * f;
+      }
+      if (bad) sc = 0xFFu;
+    } else {
+      const float st = __ldg(w[i].is_v ? a.c.v_scale : a.c.k_scale);
+      sc = cvt_e4m3x2(__fdiv_rn(__uint_as_float(mx << 16), __fmul_rn(6.0f, st)), 0.0f) & 0xFFu;
+      const float unit = __fmul_rn(e4m3x2_to_float2(sc).x, st);
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        y[2 * e] = unit > 0.0f ? __fdiv_rn(bf_lo(xs[e]), unit) : 0.0f;
+        y[2 * e + 1] = unit > 0.0f ? __fdiv_rn(bf_hi(xs[e]), unit) : 0.0f;
+      }
+      if (bad) sc = 0x7Fu;
+    }
+    uint8_t* codes = w[i].is_v ? a.c.v : a.c.k;
+    uint8_t* sf = w[i].is_v ? a.c.v_sf : a.c.k_sf;
+    reinterpret_cast<uint32_t*>(codes + w[i].at * 64)[lane] = bad ? 0u : pack8_e2m1(y);
+    if (FMT == 0) {
+      if ((lane & 3) == 0) sf[w[i].at * 4 + (lane >> 2)] = uint8_t(sc);
+    } else {
+      if ((lane & 1) == 0) sf[w[i].at * 8 + (lane >> 1)] = uint8_t(sc);
+    }
   }
 }
 
 // A row without a slot reads as zeros.
-template <int FMT>
+template <int FMT, int N>
 __global__ void __launch_bounds__(256) kv_load_kernel(KvRowsArgs a) {
   const int lane = threadIdx.x & 15;
-  const uint32_t rows = uint32_t(a.tokens * a.c.H * 2);  // below 2^32 - 16
-  const uint32_t r = blockIdx.x * 16u + (threadIdx.x >> 4);
-  if (r >= rows) return;
-  KvRow w;
-  const bool live = kv_row(a, r, w);
-  uint32_t out[4] = {0, 0, 0, 0};
-  if (live) {
-    const uint8_t* codes = w.is_v ? a.c.v : a.c.k;
-    const uint8_t* sf = w.is_v ? a.c.v_sf : a.c.k_sf;
-    const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(codes + w.at * 64) + lane);
-    float s, st = 1.0f;
-    if (FMT == 0) {
-      const uint32_t b = __ldg(sf + w.at * 4 + (lane >> 2));
-      s = b == 0xFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float(b << 23);
-    } else {
-      s = e4m3x2_to_float2(__ldg(sf + w.at * 8 + (lane >> 1))).x;
-      st = __ldg(w.is_v ? a.c.v_scale : a.c.k_scale);
-    }
-    uint32_t h[4];
-    e2m1x8_to_f16(c, h);
+  const uint32_t rows = uint32_t(a.tokens * a.c.H * 2);  // below 2^32 - 128
+  KvRow w[N];
+  uint32_t c[N], b[N];
+  bool live[N], mine[N];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-      f.x = __fmul_rn(f.x, s);
-      f.y = __fmul_rn(f.y, s);
-      if (FMT == 1) {
-        f.x = __fmul_rn(f.x, st);
-        f.y = __fmul_rn(f.y, st);
-      }
-      out[i] = pack_bf16(f.x, f.y);
+  for (int i = 0; i < N; i++) {
+    const uint32_t r = blockIdx.x * uint32_t(16 * N) + i * 16u + (threadIdx.x >> 4);
+    mine[i] = r < rows;
+    live[i] = mine[i] && kv_row(a, r, w[i]);
+    c[i] = b[i] = 0;
+    if (live[i]) {
+      c[i] = __ldg(reinterpret_cast<const uint32_t*>((w[i].is_v ? a.c.v : a.c.k) + w[i].at * 64) + lane);
+      const uint8_t* sf = w[i].is_v ? a.c.v_sf : a.c.k_sf;
+      b[i] = FMT == 0 ? __ldg(sf + w[i].at * 4 + (lane >> 2)) : __ldg(sf + w[i].at * 8 + (lane >> 1));
     }
   }
-  uint16_t* dst = w.is_v ? a.v : a.k;
-  *reinterpret_cast<uint4*>(dst + (w.token * a.c.H + w.head) * 128 + lane * 8) = make_uint4(out[0], out[1], out[2], out[3]);
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    if (!mine[i]) continue;
+    uint32_t out[4] = {0, 0, 0, 0};
+    if (live[i]) {
+      float s, st = 1.0f;
+      if (FMT == 0) {
+        s = b[i] == 0xFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float(b[i] << 23);
+      } else {
+        s = e4m3x2_to_float2(b[i]).x;
+        st = __ldg(w[i].is_v ? a.c.v_scale : a.c.k_scale);
+      }
+      uint32_t h[4];
+      e2m1x8_to_f16(c[i], h);
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[e]));
+        f.x = __fmul_rn(f.x, s);
+        f.y = __fmul_rn(f.y, s);
+        if (FMT == 1) {
+          f.x = __fmul_rn(f.x, st);
+          f.y = __fmul_rn(f.y, st);
+        }
+        out[e] = pack_bf16(f.x, f.y);
+      }
+    }
+    uint16_t* dst = w[i].is_v ? a.v : a.k;
+    __stcs(reinterpret_cast<uint4*>(dst + (w[i].token * a.c.H + w[i].head) * 128 + lane * 8),
+           make_uint4(out[0], out[1], out[2], out[3]));
+  }
 }
+
+// Several rows to a lane group once one row each fills the GPU (about 16 CTAs of 16
+// rows an SM); below that, one row each spreads the work over more SMs.
+bool many_rows(const KvRowsArgs& a) { return a.tokens * a.c.H * 2 >= int64_t(sm_count_current_device()) * 16 * 16; }
 
 cudaError_t launch_kv_append(const KvRowsArgs& a, cudaStream_t s) {
   clear_stale_error();
-  const unsigned g = unsigned((a.tokens * a.c.H * 2 + 15) / 16);
-  if (a.c.fmt == 0) kv_append_kernel<0><<<g, 256, 0, s>>>(a);
-  else kv_append_kernel<1><<<g, 256, 0, s>>>(a);
+  constexpr int N = 4;
+  const bool many = many_rows(a);
+  const int64_t per = many ? 16 * N : 16;
+  const unsigned g = unsigned((a.tokens * a.c.H * 2 + per - 1) / per);
+  if (a.c.fmt == 0) many ? kv_append_kernel<0, N><<<g, 256, 0, s>>>(a) : kv_append_kernel<0, 1><<<g, 256, 0, s>>>(a);
+  else many ? kv_append_kernel<1, N><<<g, 256, 0, s>>>(a) : kv_append_kernel<1, 1><<<g, 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv_load(const KvRowsArgs& a, cudaStream_t s) {
   clear_stale_error();
-  const unsigned g = unsigned((a.tokens * a.c.H * 2 + 15) / 16);
-  if (a.c.fmt == 0) kv_load_kernel<0><<<g, 256, 0, s>>>(a);
-  else kv_load_kernel<1><<<g, 256, 0, s>>>(a);
+  constexpr int N = 4;
+  const bool many = many_rows(a);
+  const int64_t per = many ? 16 * N : 16;
+  const unsigned g = unsigned((a.tokens * a.c.H * 2 + per - 1) / per);
+  if (a.c.fmt == 0) many ? kv_load_kernel<0, N><<<g, 256, 0, s>>>(a) : kv_load_kernel<0, 1><<<g, 256, 0, s>>>(a);
+  else many ? kv_load_kernel<1, N><<<g, 256, 0, s>>>(a) : kv_load_kernel<1, 1><<<g, 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 
