@@ -141,22 +141,39 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(KvPlanArgs a) {
   const int page = 1 << a.page_shift;
   const int64_t head0 = (head % a.ring_size + a.ring_size) % a.ring_size;
   const int64_t tail0 = (tail % a.ring_size + a.ring_size) % a.ring_size;
-  // table entries: one warp per request
-  const int nwarps = gridDim.x * (kPlanThreads / 32);
-  for (int r = blockIdx.x * (kPlanThreads / 32) + (tid >> 5); r < a.R; r += nwarps) {
+  auto wrap = [&](int64_t i) {  // into the ring; one subtraction unless a caller's counters are off
+    if (i >= a.ring_size) i -= a.ring_size;
+    return i < a.ring_size ? i : i % a.ring_size;
+  };
+  const int total = s_cu[a.R];
+  // blocks given back, and (where not every token has a row below) blocks taken: one
+  // CTA per request, four entries of a thread in flight
+  for (int r = blockIdx.x; r < a.R; r += gridDim.x) {
     const int rank = s_rank[r];
-    if (rank == -1) continue;
+    if (rank == -1 || (rank >= 0 && total <= a.tokens)) continue;
     const int have = pages_of(s_ctx[r], a.page_shift);
     int32_t* row = a.table + int64_t(r) * a.width;
-    if (rank >= 0) {
-      const int need = pages_of(s_ctx[r] + s_cu[r + 1] - s_cu[r], a.page_shift);
-      for (int j = have + (tid & 31); j < need; j += 32) row[j] = a.ring[(head0 + rank + j - have) % a.ring_size];
-    } else {
-      for (int j = tid & 31; j < min(have, a.width); j += 32) a.ring[(tail0 + (-2 - rank) + j) % a.ring_size] = row[j];
+    const bool take = rank >= 0;
+    const int from = take ? have : 0;
+    const int to = take ? pages_of(s_ctx[r] + s_cu[r + 1] - s_cu[r], a.page_shift) : min(have, a.width);
+    const int64_t at = take ? head0 + rank - have : tail0 + (-2 - rank);  // ring place of entry 0
+    for (int j0 = from + tid; j0 < to; j0 += 4 * kPlanThreads) {
+      int32_t v[4];
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const int j = j0 + kPlanThreads * i;
+        if (j < to) v[i] = take ? a.ring[wrap(at + j)] : row[j];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const int j = j0 + kPlanThreads * i;
+        if (j >= to) continue;
+        if (take) row[j] = v[i];
+        else a.ring[wrap(at + j)] = v[i];
+      }
     }
   }
-  // tokens
-  const int total = s_cu[a.R];
+  // tokens; the first of a new page writes the page's table entry
   for (int64_t t = int64_t(blockIdx.x) * kPlanThreads + tid; t < a.tokens; t += int64_t(gridDim.x) * kPlanThreads) {
     int64_t slot = -1;
     int pos = -1;
@@ -171,9 +188,16 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(KvPlanArgs a) {
       const int rank = s_rank[lo];
       if (rank >= 0) {
         const int have = pages_of(s_ctx[lo], a.page_shift), j = pos >> a.page_shift;
-        const int32_t b = j < 0 || j >= a.width ? -1
-                          : j < have            ? a.table[int64_t(lo) * a.width + j]
-                                                : a.ring[(head0 + rank + j - have) % a.ring_size];
+        int32_t b = -1;
+        if (j >= 0 && j < a.width) {
+          int32_t* entry = a.table + int64_t(lo) * a.width + j;
+          if (j < have) {
+            b = *entry;
+          } else {
+            b = a.ring[wrap(head0 + rank + j - have)];
+            if ((pos & (page - 1)) == 0) *entry = b;
+          }
+        }
         if (b >= 0) slot = int64_t(b) * page + (pos & (page - 1));
       }
     }
