@@ -265,17 +265,40 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
         tc_commit_w(BAR(B_ODONE + x));
       };
       int kt = 0, items_q = 0;   // tiles passed, items whose Q was used
-      int sx[2] = {0, 0};        // S products of each tile so far
+      int sa = 0, sb = 0;        // S products of each tile so far
       bool ok = true;
-      Item it;
-      for (int i = 0; take(i, it, ok); i++) {
+      // The loops over items have fixed trip counts and skip their turns once the run is
+      // over (64^4 items, far more than a run has): a loop that ended on a loaded item
+      // would not be warp-uniform to the compiler, and the issue code in it took 130
+      // cycles a product instead of 64.
+      bool over = false;
+      int i = 0;
+#pragma unroll 1
+      for (int l0 = 0; l0 < 64; l0++) {
+        if (over) continue;
+#pragma unroll 1
+      for (int l1 = 0; l1 < 64; l1++) {
+        if (over) continue;
+#pragma unroll 1
+      for (int l2 = 0; l2 < 64; l2++) {
+        if (over) continue;
+#pragma unroll 1
+      for (int l3 = 0; l3 < 64; l3++) {
+        if (over) continue;
+        Item it;
+        if (!take(i++, it, ok)) {
+          over = true;
+          continue;
+        }
         const int nmax = max(it.na, it.nb);
         if (nmax == 0) continue;
         ok = wait_all(BAR(B_QFULL), items_q & 1) && wait_all(BAR(B_KFULL + (kt & 1)), (kt >> 1) & 1);
-        if (!ok) break;
+        if (!ok) over = true;
+        if (!ok) continue;
         tc_fence_after();
-        if (it.na > 0) issue_s(0, kt);
-        if (it.nb > 0) issue_s(1, kt);
+#pragma unroll 1
+        for (int x = 0; x < 2; x++)
+          if ((x ? it.nb : it.na) > 0) issue_s(x, kt);
         tc_commit_w(BAR(B_KEMPTY + (kt & 1)));
         if (nmax == 1) tc_commit_w(BAR(B_QEMPTY));
 #pragma unroll 1
@@ -287,7 +310,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
           const int kj = kt + j;
           ok = wait_all(BAR(B_VFULL + (kj & 1)), (kj >> 1) & 1) &&
                (!next || wait_all(BAR(B_KFULL + ((kj + 1) & 1)), ((kj + 1) >> 1) & 1)) &&
-               wait_all(BAR(B_PFULL + x), uint32_t(sx[x] + j) & 1);
+               wait_all(BAR(B_PFULL + x), uint32_t((x ? sb : sa) + j) & 1);
           if (!ok) break;
           tc_fence_after();
           issue_pv(x, kj, j == 0);
@@ -301,10 +324,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
           }
         }
         kt += nmax;
-        sx[0] += it.na;
-        sx[1] += it.nb;
+        sa += it.na;
+        sb += it.nb;
         items_q++;
-        if (!ok) break;
+        if (!ok) over = true;
+      }
+      }
+      }
       }
       // every product has retired before TMEM is released
       tc_commit_w(BAR(B_TEAR));
