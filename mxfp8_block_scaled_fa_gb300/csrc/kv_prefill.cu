@@ -13,11 +13,12 @@
 // CTA: 16 warps.
 //   warp 0       tcgen05 issuer and TMEM owner
 //   warp 1       walks the run and publishes its items (two-entry ring)
-//   warps 4-7    softmax of rows 0..127 (tile A): thread = row = TMEM lane
-//   warps 8-11   softmax of rows 128..255 (tile B)
+//   warps 4-7    softmax of rows 0..127 (tile A): thread = row = TMEM lane; and tile A's
+//                queries of the next item, as soon as its last S is done
+//   warps 8-11   the same of rows 128..255 (tile B)
 //   warps 12-15  conversion: 4-bit rows of K and V from global memory (held in
 //                registers half a tile ahead) to binary16 tiles in shared memory, 128B
-//                swizzle, two of each; and the item's queries
+//                swizzle, two of each
 // The tensor core alternates between the tiles: S_A(j+1) and PV_A(j) run while tile
 // B's softmax does, and so on.  K is read as the K-major and V as the MN-major operand
 // of the same layout: [channel half][key][64 channels].
@@ -47,14 +48,14 @@ constexpr float kOffset = 8.0f, kLazy = 6.0f;  // as in kv_attn.cu
 constexpr int OFF_Q = 0;                           // tiles A, B
 constexpr int OFF_K = OFF_Q + 2 * OP_BYTES;        // two stages
 constexpr int OFF_V = OFF_K + 2 * OP_BYTES;        // two stages
-constexpr int OFF_CS = OFF_V + 2 * OP_BYTES;       // float [item parity][256]
-constexpr int OFF_NAN = OFF_CS + 2 * ROWS * 4;     // u8 [4][128]: NaN blocks of V of a tile's keys
+constexpr int OFF_CS = OFF_V + 2 * OP_BYTES;       // float [256]: row scales
+constexpr int OFF_NAN = OFF_CS + ROWS * 4;     // u8 [4][128]: NaN blocks of V of a tile's keys
 constexpr int OFF_BAD = OFF_NAN + 4 * TILE;        // u32 [4][4]: keys that are not there
 constexpr int OFF_FLAG = OFF_BAD + 64;             // u32 [4][4]: per conversion warp, 1: NaN blocks, 2: missing keys
 constexpr int OFF_ITEM = OFF_FLAG + 64;            // Item [2]
 constexpr int OFF_BAR = OFF_ITEM + 128;
 enum {
-  B_QFULL = 0, B_QEMPTY, B_KFULL, B_KEMPTY = B_KFULL + 2, B_VFULL = B_KEMPTY + 2, B_VEMPTY = B_VFULL + 2,
+  B_QFULL = 0, B_KFULL = B_QFULL + 2, B_KEMPTY = B_KFULL + 2, B_VFULL = B_KEMPTY + 2, B_VEMPTY = B_VFULL + 2,
   B_SFULL = B_VEMPTY + 2, B_PFULL = B_SFULL + 2, B_ODONE = B_PFULL + 2, B_IFULL = B_ODONE + 2, B_IEMPTY = B_IFULL + 2,
   B_TEAR = B_IEMPTY + 2, NBAR
 };
@@ -193,9 +194,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
 
   if (tid == 0) {
     *abort_flag = 0;
-    mbar_init(BAR(B_QFULL), 4);
-    mbar_init(BAR(B_QEMPTY), 1);
     for (int s = 0; s < 2; s++) {
+      mbar_init(BAR(B_QFULL + s), 4);
       mbar_init(BAR(B_KFULL + s), 4);
       mbar_init(BAR(B_KEMPTY + s), 1);
       mbar_init(BAR(B_VFULL + s), 4);
@@ -264,8 +264,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
                    !first || k > 0);
         tc_commit_w(BAR(B_ODONE + x));
       };
-      int kt = 0, items_q = 0;   // tiles passed, items whose Q was used
-      int sa = 0, sb = 0;        // S products of each tile so far
+      int kt = 0;            // tiles passed
+      int sa = 0, sb = 0;    // S products of each tile so far
+      int qa = 0, qb = 0;    // items of each tile so far
       bool ok = true;
       // The loops over items have fixed trip counts and skip their turns once the run is
       // over (64^4 items, far more than a run has): a loop that ended on a loaded item
@@ -292,15 +293,18 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
         }
         const int nmax = max(it.na, it.nb);
         if (nmax == 0) continue;
-        ok = wait_all(BAR(B_QFULL), items_q & 1) && wait_all(BAR(B_KFULL + (kt & 1)), (kt >> 1) & 1);
+        ok = wait_all(BAR(B_KFULL + (kt & 1)), (kt >> 1) & 1);
         if (!ok) over = true;
         if (!ok) continue;
         tc_fence_after();
 #pragma unroll 1
-        for (int x = 0; x < 2; x++)
-          if ((x ? it.nb : it.na) > 0) issue_s(x, kt);
+        for (int x = 0; ok && x < 2; x++) {
+          if ((x ? it.nb : it.na) == 0) continue;
+          ok = wait_all(BAR(B_QFULL + x), uint32_t(x ? qb : qa) & 1);
+          tc_fence_after();
+          if (ok) issue_s(x, kt);
+        }
         tc_commit_w(BAR(B_KEMPTY + (kt & 1)));
-        if (nmax == 1) tc_commit_w(BAR(B_QEMPTY));
 #pragma unroll 1
         for (int bl = 0; ok && bl < 2 * nmax; bl++) {
           const int j = bl >> 1, x = bl & 1, n_x = x ? it.nb : it.na;
@@ -319,14 +323,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
             issue_s(x, kj + 1);
             if (x == 1 || j + 1 >= it.nb) {  // last user of K(j + 1)
               tc_commit_w(BAR(B_KEMPTY + ((kj + 1) & 1)));
-              if (j + 2 == nmax) tc_commit_w(BAR(B_QEMPTY));
             }
           }
         }
         kt += nmax;
         sa += it.na;
         sb += it.nb;
-        items_q++;
+        qa += it.na > 0;
+        qb += it.nb > 0;
         if (!ok) over = true;
       }
       }
@@ -425,9 +429,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_CONVERT));
     const int t = tid - 384;  // row of the tile
     const int cw = warp - 12;
-    const float kst = FMT == 1 ? __ldg(a.c.k_scale) : 1.0f;
     const uint32_t swz = uint32_t(t & 7) << 4;
-    int kt = 0, items_q = 0;
+    int kt = 0;
     bool ok = true;
     Item it;
     for (int i = 0; take(i, it, ok); i++) {
@@ -477,42 +480,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       load_k(row);
       load_v(row);
       next_row = find(1);
-      // the item's queries, eight threads per row, 16 channels each
-      if (items_q > 0 && !mbar_wait(BAR(B_QEMPTY), (items_q - 1) & 1, abort_flag, status)) ok = false;
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
-      const int qrows = it.rows > TILE ? ROWS : TILE;
-#pragma unroll 2
-      for (int r0 = 0; r0 < qrows; r0 += 16) {
-        const int qr = r0 + (t >> 3), part = t & 7;
-        uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-        if (qr < it.rows) {
-          const int rr = it.row0 + qr, tok = rr / a.G, hd = rr - tok * a.G;
-          const uint16_t* src = a.q + int64_t(it.q0 + tok) * a.q_stride + int64_t(it.h * a.G + hd) * 128 + part * 16;
-          v0 = __ldg(reinterpret_cast<const uint4*>(src));
-          v1 = __ldg(reinterpret_cast<const uint4*>(src) + 1);
-        }
-        const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-        uint32_t mx = 0;
-#pragma unroll
-        for (int e = 0; e < 8; e++) mx = max(mx, hmax2(abs2(w[e])));
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-        const float2 sc = q_row_scale(mx);
-        const uint32_t dst = base + OFF_Q + (qr >> 7) * OP_BYTES + (part >> 2) * (OP_BYTES / 2) + (qr & 127) * 128;
-#pragma unroll
-        for (int e = 0; e < 2; e++)
-          st_shared_v4(dst + ((((part & 3) * 2 + e) ^ (qr & 7)) << 4), pack_f16(bf_lo(w[4 * e]) * sc.x, bf_hi(w[4 * e]) * sc.x),
-                       pack_f16(bf_lo(w[4 * e + 1]) * sc.x, bf_hi(w[4 * e + 1]) * sc.x),
-                       pack_f16(bf_lo(w[4 * e + 2]) * sc.x, bf_hi(w[4 * e + 2]) * sc.x),
-                       pack_f16(bf_lo(w[4 * e + 3]) * sc.x, bf_hi(w[4 * e + 3]) * sc.x));
-        // never 0: the score of a hidden key, -inf, is multiplied by it
-        if (part == 0)
-          reinterpret_cast<float*>(smem + OFF_CS)[(items_q & 1) * ROWS + qr] = fmaxf(a.scale_log2 * kst * sc.y, 1.17549435e-38f);
-      }
-      fence_async_smem();
-      warp_arrive(BAR(B_QFULL));
-      items_q++;
       // a row of a tile: sixteen words of eight channels, chunk (16 bytes) w of 16
       auto put = [&](uint32_t tile, const uint4* c, const uint32_t* s2) {
         const uint32_t dst = tile + uint32_t(t) * 128u;
@@ -598,16 +565,62 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     const uint32_t col_s = tmem + lane_base + COL_S + 128u * uint32_t(x), col_o = tmem + lane_base + COL_O + 128u * uint32_t(x);
     const float vst = FMT == 1 ? __ldg(a.c.v_scale) : 1.0f;
-    int st = 0, kt = 0, items_q = 0;  // S products of this tile, tiles and items passed
+    const float kst = FMT == 1 ? __ldg(a.c.k_scale) : 1.0f;
+    float* s_cs = reinterpret_cast<float*>(smem + OFF_CS) + x * TILE + (warp & 3) * 32;  // of this warp's rows
+    // this warp's 32 query rows of an item: binary16 with a power of two per row; eight
+    // lanes per row, 16 channels each, all loads in flight at once
+    auto load_q = [&](const Item& it) {
+      if ((x ? it.nb : it.na) == 0) return;
+      const int part = lane & 7;
+      uint4 v[8][2];
+#pragma unroll
+      for (int p = 0; p < 8; p++) {
+        const int qr = x * TILE + (warp & 3) * 32 + p * 4 + (lane >> 3);
+        v[p][0] = v[p][1] = make_uint4(0, 0, 0, 0);
+        if (qr < it.rows) {
+          const int rr = it.row0 + qr, tok = rr / a.G, hd = rr - tok * a.G;
+          const uint16_t* src = a.q + int64_t(it.q0 + tok) * a.q_stride + int64_t(it.h * a.G + hd) * 128 + part * 16;
+          v[p][0] = __ldg(reinterpret_cast<const uint4*>(src));
+          v[p][1] = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < 8; p++) {
+        const int lr = p * 4 + (lane >> 3), qr = (warp & 3) * 32 + lr;
+        const uint32_t w[8] = {v[p][0].x, v[p][0].y, v[p][0].z, v[p][0].w, v[p][1].x, v[p][1].y, v[p][1].z, v[p][1].w};
+        uint32_t mx = 0;
+#pragma unroll
+        for (int e = 0; e < 8; e++) mx = max(mx, hmax2(abs2(w[e])));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+        const float2 sc = q_row_scale(mx);
+        const uint32_t dst = base + OFF_Q + x * OP_BYTES + (part >> 2) * (OP_BYTES / 2) + qr * 128;
+#pragma unroll
+        for (int e = 0; e < 2; e++)
+          st_shared_v4(dst + ((((part & 3) * 2 + e) ^ (qr & 7)) << 4), pack_f16(bf_lo(w[4 * e]) * sc.x, bf_hi(w[4 * e]) * sc.x),
+                       pack_f16(bf_lo(w[4 * e + 1]) * sc.x, bf_hi(w[4 * e + 1]) * sc.x),
+                       pack_f16(bf_lo(w[4 * e + 2]) * sc.x, bf_hi(w[4 * e + 2]) * sc.x),
+                       pack_f16(bf_lo(w[4 * e + 3]) * sc.x, bf_hi(w[4 * e + 3]) * sc.x));
+        // never 0: the score of a hidden key, -inf, is multiplied by it
+        if (part == 0) s_cs[lr] = fmaxf(a.scale_log2 * kst * sc.y, 1.17549435e-38f);
+      }
+      fence_async_smem();
+      warp_arrive(BAR(B_QFULL + x));
+    };
+    int st = 0, kt = 0;  // S products of this tile, tiles passed
     bool ok = true;
-    Item it;
-    for (int i = 0; take(i, it, ok); i++) {
+    Item it, next_it;
+    int i = 0;
+    bool more = take(i++, it, ok);
+    if (more) load_q(it);
+    for (; more; it = next_it) {
       const int n_x = x ? it.nb : it.na, nmax = max(it.na, it.nb);
       const int idx = x * TILE + row;
       const bool valid = idx < it.rows;
       const int tok = (it.row0 + idx) / a.G;
       const int klim = a.causal && valid ? it.kv - it.n + tok + 1 : it.kv;  // keys before it are visible
-      float m = -INFINITY, l = 0.0f, cs = 0.0f;
+      float m = -INFINITY, l = 0.0f;
+      const float cs = n_x > 0 ? s_cs[lane] : 0.0f;
       uint32_t nan_blocks = 0;
       for (int j = 0; ok && j < n_x; j++) {
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(B_SFULL + x), uint32_t(st + j) & 1, abort_flag, status));
@@ -616,7 +629,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
         float s[128];
 #pragma unroll
         for (int c = 0; c < 4; c++) tmem_ld32(col_s + 32 * c, reinterpret_cast<uint32_t*>(s) + 32 * c);
-        if (j == 0) cs = reinterpret_cast<const float*>(smem + OFF_CS)[(items_q & 1) * ROWS + idx];
         const int f4 = (kt + j) & 3;
         const volatile uint32_t* fl = reinterpret_cast<const volatile uint32_t*>(smem + OFF_FLAG) + f4 * 4;
         const uint32_t flags = fl[0] | fl[1] | fl[2] | fl[3];
@@ -692,6 +704,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
         tc_fence_before();
         warp_arrive(BAR(B_PFULL + x));
       }
+      // the last S has been read, so the tile's queries may be replaced
+      if (!ok) break;
+      more = take(i++, next_it, ok);
+      if (more) load_q(next_it);
       // the part's rows: O / l and lse, or a partial record
       if (ok && n_x > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(B_ODONE + x), uint32_t(st + n_x - 1) & 1, abort_flag, status));
       if (!ok) break;
@@ -740,7 +756,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       }
       st += n_x;
       kt += nmax;
-      if (nmax > 0) items_q++;
     }
   }
   tc_fence_before();
