@@ -485,8 +485,9 @@ size_t mxfa_kv_sf_bytes(int64_t num_blocks, int page, int H, int fmt);
  * their kv_lens stays ctx, their slots are -1 (mxfa_kv_append skips them), and
  * ring_out[2] > 0 says so.  A done request's blocks go back in request and table
  * order and can be taken from the next step on.  kv_lens may be ctx_lens and
- * ring_out may be ring_in (a step captured once and replayed); partly
- * overlapping buffers are MXFA_ERR_INVALID_ARG.  A request whose tokens exceed
+ * ring_out may be ring_in (a step captured once and replayed); any other
+ * buffers that overlap are MXFA_ERR_INVALID_ARG.  The new lengths sum to less than 2^31.
+ * A request whose tokens exceed
  * max_blocks pages gets no block and is recorded as a failed index check.
  * R <= 16384, page as above, max_blocks * page <= 2^30 (else MXFA_ERR_UNSUPPORTED). */
 mxfa_status mxfa_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int R, int32_t* block_table,
@@ -505,7 +506,8 @@ mxfa_status mxfa_kv_append(const mxfa_kv_cache* cache, const void* k, const void
 
 /* mxfa_kv_load -- the cached values of slots as bf16 k, v [tokens][H][128] (MXFP4
  * exact, NVFP4 rounded to nearest), in any order and repeated at will; zeros
- * for a negative slot (and for one past the cache, which is recorded). */
+ * for a negative slot (and for one past the cache, which is recorded).  k, v and
+ * slots do not overlap (MXFA_ERR_INVALID_ARG). */
 mxfa_status mxfa_kv_load(const mxfa_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k, void* v,
                          mxfa_stream_t stream);
 
@@ -529,7 +531,10 @@ size_t mxfa_kv_attn_workspace_size(int R, int max_q, int64_t max_k, int Hq, int 
  *               that can run at the same time; its contents need not be kept
  * Keys past kv_lens or in no row's sight are not used, whatever they hold.  A block index
  * outside the cache (its keys count as not there) and offsets or lengths outside
- * their tables (the request is left out) are recorded as failed index checks. */
+ * their tables (the request is left out) are recorded as failed index checks.
+ * o, lse and ws overlap neither each other nor an input (MXFA_ERR_INVALID_ARG).
+ * max_blocks * page <= 2^30, and <= 2^25 where max_q * G > 64 (else
+ * MXFA_ERR_UNSUPPORTED). */
 mxfa_status mxfa_kv_attn(const mxfa_kv_cache* cache, const void* q, int64_t q_stride, int64_t total_q,
                          const int32_t* cu_q, const int32_t* kv_lens, int R, const int32_t* block_table,
                          int max_blocks, int max_q, int Hq, float softmax_scale, int causal, void* o,

@@ -774,6 +774,12 @@ int overlap(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na ? 2 : 0;
 }
 
+struct Range {
+  const void* at;
+  size_t bytes;
+};
+bool meet(const Range& a, const Range& b) { return a.bytes && b.bytes && overlap(a.at, a.bytes, b.at, b.bytes) != 0; }
+
 }  // namespace
 
 extern "C" {
@@ -810,7 +816,19 @@ mxfa_status mxfa_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int R
   const int same_len = R > 0 ? overlap(ctx_lens, lens, kv_lens, lens) : 0;
   const int same_ring = overlap(ring_in, 24, ring_out, 24);
   if (same_len == 2 || same_ring == 2) return MXFA_ERR_INVALID_ARG;
-  if (R > 0 && overlap(new_lens, lens, kv_lens, lens) != 0) return MXFA_ERR_INVALID_ARG;
+  // every CTA reads the inputs while others write: no other two buffers may meet
+  const size_t toks = size_t(tokens);
+  const Range written[] = {{block_table, lens * size_t(max_blocks)}, {free_ring, size_t(ring_size) * 4}, {cu_q, lens + 4},
+                           {slots, toks * 8}, {positions, toks * 4}, {ring_out, 24}, {kv_lens, lens}};
+  const Range read[] = {{new_lens, lens}, {ctx_lens, lens}, {ring_in, 24}};
+  for (const Range& w : written) {
+    for (const Range& r : read) {
+      const bool own = (w.at == kv_lens && r.at == ctx_lens && same_len) || (w.at == ring_out && r.at == ring_in && same_ring);
+      if (!own && meet(w, r)) return MXFA_ERR_INVALID_ARG;
+    }
+    for (const Range& o : written)
+      if (&o != &w && meet(w, o)) return MXFA_ERR_INVALID_ARG;
+  }
   KvPlanArgs a;
   memset(&a, 0, sizeof(a));
   a.ctx = ctx_lens;
@@ -863,6 +881,9 @@ mxfa_status mxfa_kv_load(const mxfa_kv_cache* cache, const int64_t* slots, int64
   if (tokens >= (int64_t(1) << 31) || tokens * a.c.H >= (int64_t(1) << 31) - 128) return MXFA_ERR_UNSUPPORTED;
   if (!aligned16(k) || !aligned16(v) || !aligned8(slots)) return MXFA_ERR_MISALIGNED;
   if (tokens == 0) return MXFA_OK;
+  const size_t bytes = size_t(tokens) * size_t(a.c.H) * 256;
+  const Range kr{k, bytes}, vr{v, bytes}, sr{slots, size_t(tokens) * 8};
+  if (meet(kr, vr) || meet(kr, sr) || meet(vr, sr)) return MXFA_ERR_INVALID_ARG;
   a.k = static_cast<uint16_t*>(k);
   a.v = static_cast<uint16_t*>(v);
   a.tokens = tokens;
@@ -909,9 +930,20 @@ mxfa_status mxfa_kv_attn(const mxfa_kv_cache* cache, const void* q, int64_t q_st
   a.o = static_cast<uint16_t*>(o);
   a.lse = lse;
   a.ws = static_cast<uint8_t*>(ws);
+  if (!kv_attn_reaches(max_q, int64_t(max_blocks) * a.c.page, a.G)) return MXFA_ERR_UNSUPPORTED;
   const size_t need = kv_attn_workspace(R, max_q, int64_t(max_blocks) * a.c.page, a.G);
   if (need > 0 && !ws) return MXFA_ERR_INVALID_ARG;
   if (ws_bytes < need) return MXFA_ERR_WORKSPACE_TOO_SMALL;
+  const size_t row = size_t(Hq) * 256, rows = size_t(total_q);
+  const Range written[] = {{o, rows * row}, {lse, rows * size_t(Hq) * 4}, {ws, need}};
+  const Range read[] = {{q, (rows - 1) * size_t(total_q > 1 ? q_stride : 0) * 2 + row}, {cu_q, size_t(R) * 4 + 4}, {kv_lens, size_t(R) * 4},
+                        {block_table, size_t(R) * size_t(max_blocks) * 4}};
+  for (const Range& w : written) {
+    for (const Range& r : read)
+      if (meet(w, r)) return MXFA_ERR_INVALID_ARG;
+    for (const Range& x : written)
+      if (&x != &w && meet(w, x)) return MXFA_ERR_INVALID_ARG;
+  }
   return from_cuda(launch_kv_attn(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

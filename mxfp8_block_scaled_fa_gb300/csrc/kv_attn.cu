@@ -952,6 +952,13 @@ Plan plan_of(int max_q, int64_t max_k, int G) {
 
 }  // namespace kva
 
+// Whether a call's longest context is within what its kernels take: kv_prefill.cu's
+// waits end after 2 s, and its longest one, for an item to pass, takes 2 us a tile of
+// 128 keys: 0.6 s for 2^25 keys.
+bool kv_attn_reaches(int max_q, int64_t max_k, int G) {
+  return !kva::plan_of(max_q, max_k, G).prefill || max_k <= (int64_t(1) << 25);
+}
+
 size_t kv_attn_workspace(int R, int max_q, int64_t max_k, int G) {
   const kva::Plan p = kva::plan_of(max_q, max_k, G);
   if (p.whole) return 0;

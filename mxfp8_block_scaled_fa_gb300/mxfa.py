@@ -911,6 +911,8 @@ def kv_attention(q: torch.Tensor, cache: KvCache, cu_q: torch.Tensor, kv_lens: t
             ws_at = ws.data_ptr()
     elif ws.get_device() != index:
         raise ValueError(f"ws is on {ws.device}, expected device {index}")
+    elif not ws.is_contiguous():
+        raise ValueError("ws is not contiguous")
     else:
         ws_at, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
     _check(L.mxfa_kv_attn(ctypes.byref(cache.pages), q.data_ptr(), qs, T, cu_q.data_ptr(),

@@ -169,3 +169,37 @@ def test_sizes(mx):
     assert L.mxfa_kv_codes_bytes(10, 16, 3) == 10 * 16 * 3 * 64
     assert L.mxfa_kv_sf_bytes(10, 16, 3, 0) == 10 * 16 * 3 * 4 and L.mxfa_kv_sf_bytes(10, 16, 3, 1) == 10 * 16 * 3 * 8
     assert L.mxfa_kv_codes_bytes(-1, 16, 3) == 0 and L.mxfa_kv_attn_workspace_size(1, 1, 100, 5, 2) == 0
+
+
+def test_overlapping_buffers(mx):
+    L, ref = mx.lib(), ctypes.byref(_cache(mx))
+    # a plan: R = 8 requests of 4 pages, 64 ring entries, 32 tokens
+    base = dict(ctx=0x1000, new=0x2000, R=8, bt=0x3000, nb=4, ring=0x4000, rs=64, ri=0x5000, ro=0x6000, page=16, T=32,
+                cu=0x7000, kv=0x8000, slots=0x9000, pos=0xA000)
+    size = dict(ctx=32, new=32, bt=128, ring=256, ri=24, ro=24, cu=36, kv=32, slots=256, pos=128)
+    for w in ("bt", "ring", "ro", "cu", "kv", "slots", "pos"):
+        for o in size:
+            if o == w or (w, o) in (("kv", "ctx"), ("ro", "ri")):
+                continue
+            for at in (base[o], base[o] + (size[o] - 1) // 8 * 8):             # at its beginning and over its end
+                assert L.mxfa_kv_plan(*dict(base, **{w: at}).values(), None) == 1, (w, o)
+    # a load of 3 tokens: 3 * 512 bytes of k and of v, 24 of slots
+    for slots, k, v in ((0x100, 0x1000, 0x1000), (0x100, 0x1000, 0x1500), (0x1000, 0x1000, 0x2000), (0x2100, 0x1000, 0x2000)):
+        assert L.mxfa_kv_load(ref, slots, 3, k, v, None) == 1
+    # attention of 3 tokens: q rows of 1024 bytes 2048 apart, o of 1024, lse 48 bytes
+    base = dict(q=0x10000, qs=1024, T=3, cu=0x20000, kv=0x30000, R=1, bt=0x40000, nb=64, mq=3, Hq=4, s=0.1, c=1, o=0x50000,
+                lse=0x60000, ws=0x10000000, wb=1 << 30)
+    bad = [dict(o=0x10000), dict(o=0x10000 + 2 * 2048), dict(o=0x10400), dict(o=0x20000 - 16), dict(o=0x40000), dict(lse=0x50000),
+           dict(lse=0x30000), dict(lse=0x10000 + 2 * 2048 + 1020)]
+    if L.mxfa_kv_attn_workspace_size(1, 3, 1024, 4, 2):
+        bad += [dict(ws=0x50000), dict(ws=0x10000)]
+    for kw in bad:
+        assert L.mxfa_kv_attn(ref, *dict(base, **kw).values(), None) == 1, kw
+
+
+def test_attention_context_limits(mx):
+    L, ref = mx.lib(), ctypes.byref(_cache(mx, page=128))
+    call = lambda nb, mq: L.mxfa_kv_attn(ref, 0x10000, 512, 200, 0x20000, 0x30000, 1, 0x40000, nb, mq, 4, 0.1, 1, 0x50000, 0x90000, None, 0, None)
+    # no workspace is given: 1 or 6 (too small) where the sizes are accepted
+    assert call(1 << 24, 200) == 2 and call((1 << 18) + 1, 33) == 2             # more than 2^25 keys for more than 64 rows
+    assert call(1 << 18, 33) != 2 and call(1 << 23, 32) != 2 and call((1 << 23) + 1, 32) == 2
