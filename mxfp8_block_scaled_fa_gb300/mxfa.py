@@ -32,6 +32,8 @@ tokens' q [T, Hq, 128] and k, v [T, H, 128] in request order:
 from __future__ import annotations
 
 import ctypes
+import functools
+import importlib.util
 import math
 import os
 from dataclasses import dataclass
@@ -657,6 +659,24 @@ def mxfa_kv_attn(pages: KvPages, q, q_stride, total_q, cu_q, kv_lens, R, block_t
                               _p(o), _p(lse), _p(ws), ws_bytes, _stream(stream)), "mxfa_kv_attn")
 
 
+_kv = None
+
+
+def _fast():
+    """kv_py: the calls below for ordinary arguments (new buffers, the current device and
+    stream).  Its functions return None where they do not apply, and for arguments that do not
+    fit; what follows each of them here checks the arguments one by one."""
+    global _kv
+    if _kv is None:
+        lib()
+        spec = importlib.util.spec_from_file_location("kv_py", _build.PY_MODULE)
+        if spec is None or not os.path.exists(_build.PY_MODULE):
+            raise RuntimeError(f"{_build.PY_MODULE} is missing; build it with mxfp8_block_scaled_fa_gb300.build")
+        _kv = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_kv)
+    return _kv
+
+
 def _raw_stream(index: int) -> int:
     """The current stream of CUDA device `index`."""
     return torch._C._cuda_getCurrentRawStream(index)
@@ -719,6 +739,13 @@ class KvCache:
 
     def __post_init__(self):
         fmt, k = self.fmt, self.k
+        made = _fast().cache(k, self.v, self.k_sf, self.v_sf, fmt, self.k_scale, self.v_scale)
+        if made is not None:
+            self.raw, self.H, self.page, self.index = made
+            if fmt == KV_MXFP4:
+                self.k_scale = self.v_scale = None
+            return
+        self.raw = None
         if fmt != KV_MXFP4 and fmt != KV_NVFP4:
             raise ValueError(f"unknown cache format {fmt}")
         shape = k.shape
@@ -746,8 +773,12 @@ class KvCache:
         else:
             self.k_scale = self.v_scale = None
         self.H, self.page = h, page
-        self.pages = KvPages(k.data_ptr(), self.v.data_ptr(), self.k_sf.data_ptr(),
-                             self.v_sf.data_ptr(), ks, vs, n, page, h, 128, fmt)
+        self.__dict__["pages"] = KvPages(k.data_ptr(), self.v.data_ptr(), self.k_sf.data_ptr(),
+                                         self.v_sf.data_ptr(), ks, vs, n, page, h, 128, fmt)
+
+    @functools.cached_property
+    def pages(self) -> KvPages:
+        return KvPages.from_buffer_copy(self.raw)
 
     @staticmethod
     def empty(num_blocks: int, H: int, page: int = 64, fmt: int = KV_MXFP4, k_scale: float = 1.0,
@@ -785,6 +816,12 @@ def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.T
     returns offsets, lengths, and slot and position of `tokens` tokens.  `out`
     gives the result's buffers; its kv_lens may be ctx_lens and its ring_state
     may be ring_state, for a step that is captured once and replayed."""
+    if out is None and stream is None:
+        made = _fast().plan(ctx_lens, new_lens, block_table, free_ring, ring_state, page, tokens)
+        if type(made) is tuple:
+            return KvStep(*made)
+        if made is not None:
+            _check(made, "mxfa_kv_plan")
     R, index = ctx_lens.numel(), ctx_lens.get_device()
     shape = block_table.shape
     if new_lens.numel() != R or len(shape) != 2 or shape[0] != R:
@@ -826,6 +863,10 @@ def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
     """Quantizes bf16 k, v [tokens, H, 128] (tokens may be strided, as slices of a
     fused projection are) into the cache rows `slots` (int64 [tokens], distinct;
     negative: skipped)."""
+    if stream is None:
+        status = _fast().append(cache.raw, k, v, slots)
+        if status is not None:
+            return _check(status, "mxfa_kv_append")
     index, H = cache.index, cache.H
     ks, vs = _rows("k", k, H, index), _rows("v", v, H, index)
     T = k.shape[0]
@@ -843,6 +884,12 @@ def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
 def kv_load(cache: KvCache, slots: torch.Tensor, out=None, stream=None):
     """The cached values of `slots` (int64 [tokens]) -> bf16 (k, v) [tokens, H, 128];
     zeros for a negative slot."""
+    if out is None and stream is None:
+        made = _fast().load(cache.raw, slots)
+        if type(made) is tuple:
+            return made
+        if made is not None:
+            _check(made, "mxfa_kv_load")
     index, T = cache.index, slots.numel()
     shape = (T, cache.H, 128)
     _flat("slots", slots, torch.int64, index)
@@ -873,6 +920,12 @@ def kv_attention(q: torch.Tensor, cache: KvCache, cu_q: torch.Tensor, kv_lens: t
     (int32 [R + 1]), kv_lens (int32 [R], new tokens included) and block_table as
     kv_plan gives them; max_q: the most query tokens of a request.  causal aligns
     the last query to the last key.  Rows outside cu_q's are not written."""
+    if out is None and ws is None and stream is None:
+        made = _fast().attention(q, cache.raw, cu_q, kv_lens, block_table, max_q, scale, causal)
+        if type(made) is tuple:
+            return made
+        if made is not None:
+            _check(made, "mxfa_kv_attn")
     H, index = cache.H, cache.index
     shape = q.shape
     if len(shape) != 3 or shape[1] == 0 or shape[1] % H:

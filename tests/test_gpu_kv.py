@@ -554,3 +554,89 @@ def test_workspace(mx):
             o = [torch.full(x, 77.0, dtype=d, device="cuda") for x, d in ((q.shape, torch.bfloat16), ((4, q.shape[0]), torch.float32))]
             mx.kv_attention(q, c, cu, kv, table, 1, 128 ** -0.5, out=o, ws=torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda"))
             compare(c, q, cu, slots, True, 128 ** -0.5, *o)
+
+
+# ------------------------------------------------------- calls that allocate their results
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("page,G,ql,kv", [(16, 4, [1, 1, 1], [70, 0, 9]), (64, 8, [1, 3], [3000, 41]), (32, 2, [90, 1, 0, 12], [500, 77, 30, 12])])
+def test_new_buffers_are_as_given_ones(mx, fmt, page, G, ql, kv):
+    """The same bits from a call that allocates its results, one that is given them, and one on another stream."""
+    import torch
+    rng = np.random.default_rng(29)
+    c, q, cu, lens, table, slots = build(mx, rng, fmt, page, 2, G, ql, kv)
+    n, most, scale = int(cu[-1]), max(ql), 128 ** -0.5
+    o, lse = mx.kv_attention(q, c, cu, lens, table, most, scale)
+    assert o.shape == q.shape and o.dtype == torch.bfloat16 and lse.shape == (2 * G, q.shape[0]) and o.is_contiguous()
+    given = torch.empty_like(o, memory_format=torch.contiguous_format), torch.empty_like(lse)
+    mx.kv_attention(q, c, cu, lens, table, most, scale, causal=1, out=given)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = mx.kv_attention(q, c, cu, lens, table, most, scale, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    for x, y in (given, other):
+        assert torch.equal(o[:n].view(torch.int16), x[:n].view(torch.int16)) and torch.equal(lse[:, :n], y[:, :n])
+    o[n:], lse[:, n:] = 77.0, 77.0                                   # not written by the call
+    compare(c, q, cu, slots, True, scale, o, lse)
+    sl = torch.from_numpy(np.concatenate(slots + [np.array([-1])])).cuda()
+    k, v = mx.kv_load(c, sl)
+    k2, v2 = mx.kv_load(c, sl, out=(torch.empty_like(k), torch.empty_like(v)))
+    assert torch.equal(k.view(torch.int16), k2.view(torch.int16)) and torch.equal(v.view(torch.int16), v2.view(torch.int16))
+
+
+def test_plan_with_new_buffers(mx):
+    import torch
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    made = []
+    for own in (False, True):
+        ring, state = mx.kv_ring(9)
+        table = torch.full((3, 4), -1, dtype=torch.int32, device="cuda")
+        e = lambda n, t: torch.empty(n, dtype=t, device="cuda")
+        out = mx.KvStep(e(4, torch.int32), e(3, torch.int32), e(40, torch.int64), e(40, torch.int32), e(3, torch.int64)) if own else None
+        s = mx.kv_plan(i32(0, 0, 0), i32(17, 1, 16), table, ring, state, 16, 40, out=out)
+        made.append([s.cu_q, s.kv_lens, s.slots, s.positions, s.ring_state, table, ring])
+    for x, y in zip(*made):
+        assert x.dtype == y.dtype and torch.equal(x, y)
+    empty = mx.kv_plan(i32(), i32(), torch.empty((0, 4), dtype=torch.int32, device="cuda"), ring, state, 16, 0)
+    assert empty.cu_q.tolist() == [0] and empty.slots.shape == (0,)
+
+
+def test_refusals_name_what_is_wrong(mx):
+    """Nothing of a refused call runs, whichever check it fails."""
+    import torch
+    c = new_cache(mx, 4, 2, 16, 0)
+    before = c.k.clone()
+    rows = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    slots = torch.zeros(5, dtype=torch.int64, device="cuda")
+    bad_rows = [(ValueError, rows(5, 3, 128)), (TypeError, rows(5, 2, 128).float()), (ValueError, rows(5, 128, 2).transpose(1, 2)),
+                (ValueError, rows(5, 2, 128).cpu()), (ValueError, rows(4, 2, 128)), (mx.MxfaError, rows(1, 2, 128).expand(5, 2, 128)),
+                (mx.MxfaError, rows(2600)[1:1 + 5 * 256].view(5, 2, 128))]
+    for err, x in bad_rows:
+        with pytest.raises(err):
+            mx.kv_append(c, x, rows(5, 2, 128), slots)
+        with pytest.raises(err):
+            mx.kv_append(c, rows(5, 2, 128), x, slots)
+    for err, s in ((TypeError, slots.int()), (ValueError, slots[:4]), (ValueError, slots.cpu()), (ValueError, torch.zeros(10, dtype=torch.int64, device="cuda")[::2])):
+        with pytest.raises(err):
+            mx.kv_append(c, rows(5, 2, 128), rows(5, 2, 128), s)
+    with pytest.raises(TypeError):
+        mx.kv_load(c, slots.int())
+    with pytest.raises(ValueError):
+        mx.kv_load(c, slots.cpu())
+    good = dict(q=rows(5, 4, 128), cache=c, cu_q=i32(2), kv_lens=i32(1), block_table=i32(1, 4), max_q=5, scale=0.1)
+    for err, kw in ((ValueError, dict(q=rows(5, 3, 128))), (TypeError, dict(q=rows(5, 4, 128).half())), (ValueError, dict(cu_q=i32(3))),
+                    (TypeError, dict(kv_lens=i32(1).long())), (ValueError, dict(block_table=i32(2, 4))), (ValueError, dict(block_table=i32(4))),
+                    (ValueError, dict(block_table=i32(1, 8)[:, ::2])), (mx.MxfaError, dict(scale=0.0)), (mx.MxfaError, dict(scale=float("nan"))),
+                    (mx.MxfaError, dict(max_q=-1)), (ValueError, dict(ws=torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 20)))):
+        with pytest.raises(err):
+            mx.kv_attention(**{**good, **kw})
+    plan = dict(ctx_lens=i32(3), new_lens=i32(3), block_table=i32(3, 4), free_ring=i32(8), ring_state=torch.zeros(3, dtype=torch.int64, device="cuda"),
+                page=16, tokens=4)
+    for err, kw in ((ValueError, dict(new_lens=i32(2))), (TypeError, dict(free_ring=i32(8).long())), (mx.MxfaError, dict(page=48)),
+                    (ValueError, dict(ring_state=torch.zeros(2, dtype=torch.int64, device="cuda"))), (mx.MxfaError, dict(block_table=i32(3, 0)))):
+        with pytest.raises(err):
+            mx.kv_plan(**{**plan, **kw})
+    with pytest.raises(mx.MxfaError):
+        mx.kv_plan(**{**plan, "new_lens": plan["ctx_lens"], "free_ring": plan["ctx_lens"]})     # written and read
+    torch.cuda.synchronize()
+    assert torch.equal(c.k, before) and mx.device_status() == 0
