@@ -56,13 +56,13 @@ constexpr int OFF_ITEM = OFF_FLAG + 64;            // Item [2]
 constexpr int OFF_BAR = OFF_ITEM + 128;
 enum {
   B_QFULL = 0, B_KFULL = B_QFULL + 2, B_KEMPTY = B_KFULL + 2, B_VFULL = B_KEMPTY + 2, B_VEMPTY = B_VFULL + 2,
-  B_SFULL = B_VEMPTY + 2, B_PFULL = B_SFULL + 2, B_ODONE = B_PFULL + 2, B_IFULL = B_ODONE + 2, B_IEMPTY = B_IFULL + 2,
+  B_SFULL = B_VEMPTY + 2, B_PFULL = B_SFULL + 4, B_ODONE = B_PFULL + 4, B_IFULL = B_ODONE + 4, B_IEMPTY = B_IFULL + 2,
   B_TEAR = B_IEMPTY + 2, NBAR
 };
 constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
 constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;   // + alignment slack
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
-constexpr int READERS = 1 + 8 + 4;                 // warps that read an item
+constexpr int READERS = 2 + 8 + 4;                 // warps that read an item
 
 constexpr uint32_t COL_S = 0, COL_O = 256;         // + 128 * tile
 constexpr int NTHREADS = 512;
@@ -197,16 +197,18 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
     for (int s = 0; s < 2; s++) {
       mbar_init(BAR(B_QFULL + s), 4);
       mbar_init(BAR(B_KFULL + s), 4);
-      mbar_init(BAR(B_KEMPTY + s), 1);
+      mbar_init(BAR(B_KEMPTY + s), 2);
       mbar_init(BAR(B_VFULL + s), 4);
-      mbar_init(BAR(B_VEMPTY + s), 1);
-      mbar_init(BAR(B_SFULL + s), 1);
-      mbar_init(BAR(B_PFULL + s), 4);
-      mbar_init(BAR(B_ODONE + s), 1);
+      mbar_init(BAR(B_VEMPTY + s), 2);
       mbar_init(BAR(B_IFULL + s), 1);
       mbar_init(BAR(B_IEMPTY + s), READERS);
     }
-    mbar_init(BAR(B_TEAR), 1);
+    for (int s = 0; s < 4; s++) {  // tile, half of the keys
+      mbar_init(BAR(B_SFULL + s), 1);
+      mbar_init(BAR(B_PFULL + s), 4);
+      mbar_init(BAR(B_ODONE + s), 1);
+    }
+    mbar_init(BAR(B_TEAR), 2);
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -239,34 +241,37 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_ISSUE));
-    if (warp == 0) {
-      // ---------------------------------------------------------------- issuer
+    if (warp == 0 || warp == 2) {
+      // --------------------------------------------------------------- issuers
       warp_converged();
+      const int x = warp >> 1;  // tile A or B
       const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-      auto wait_all = [&](uint32_t bar, uint32_t par) { return __all_sync(0xFFFFFFFFu, mbar_wait(bar, par, abort_flag, status)); };
-      // S_X = Q_X K^T of running tile kt
-      auto issue_s = [&](int x, int kt) {
+      auto wait_all = [&](uint32_t bar, uint32_t par) {
+        if (__all_sync(0xFFFFFFFFu, mbar_test(bar, par))) return true;
+        return __all_sync(0xFFFFFFFFu, mbar_wait(bar, par, abort_flag, status)) != 0;
+      };
+      // S_X = Q_X K^T for half h of running tile kt's keys
+      auto issue_s = [&](int h, int kt) {
         const uint64_t dq = smem_desc(base + OFF_Q + x * OP_BYTES, 16, 1024, 2);
-        const uint64_t dk = smem_desc(base + OFF_K + (kt & 1) * OP_BYTES, 16, 1024, 2);
+        const uint64_t dk = smem_desc(base + OFF_K + (kt & 1) * OP_BYTES, 16, 1024, 2) + uint64_t(h * (OP_BYTES / 64));
 #pragma unroll
         for (int k = 0; k < 8; k++) {
           const uint64_t off = uint64_t((k >> 2) * (OP_BYTES / 32) + (k & 3) * 2);  // channel half, 32 bytes of it
-          mma_ss_w(tm + COL_S + 128 * x, dq + off, dk + off, idesc_f16(128, 128, 0), k > 0);
+          mma_ss_w(tm + COL_S + 128 * x + 64 * h, dq + off, dk + off, idesc_f16(128, 64, 0), k > 0);
         }
-        tc_commit_w(BAR(B_SFULL + x));
+        tc_commit_w(BAR(B_SFULL + 2 * x + h));
       };
-      // O_X (+)= P_X V
-      auto issue_pv = [&](int x, int kt, bool first) {
-        const uint64_t dv = smem_desc(base + OFF_V + (kt & 1) * OP_BYTES, OP_BYTES / 2, 1024, 2);
+      // O_X (+)= P_X V for half h
+      auto issue_pv = [&](int h, int kt, bool first) {
+        const uint64_t dv = smem_desc(base + OFF_V + (kt & 1) * OP_BYTES, OP_BYTES / 2, 1024, 2) + uint64_t(h * 512);
 #pragma unroll
-        for (int k = 0; k < 8; k++)  // 16 keys: 2048 bytes of each half
-          mma_ts_w(tm + COL_O + 128 * x, tm + COL_S + 128 * x + 8 * k, dv + uint64_t(128 * k), idesc_f16(128, 128, 1),
+        for (int k = 0; k < 4; k++)  // 16 keys: 2048 bytes of each channel half
+          mma_ts_w(tm + COL_O + 128 * x, tm + COL_S + 128 * x + 64 * h + 8 * k, dv + uint64_t(128 * k), idesc_f16(128, 128, 1),
                    !first || k > 0);
-        tc_commit_w(BAR(B_ODONE + x));
+        tc_commit_w(BAR(B_ODONE + 2 * x + h));
       };
-      int kt = 0;            // tiles passed
-      int sa = 0, sb = 0;    // S products of each tile so far
-      int qa = 0, qb = 0;    // items of each tile so far
+      int kt = 0;             // tiles passed
+      int sn = 0, qn = 0;     // S products and items of this tile so far
       bool ok = true;
       // The loops over items have fixed trip counts and skip their turns once the run is
       // over (64^4 items, far more than a run has): a loop that ended on a loaded item
@@ -291,46 +296,50 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
           over = true;
           continue;
         }
-        const int nmax = max(it.na, it.nb);
-        if (nmax == 0) continue;
-        ok = wait_all(BAR(B_KFULL + (kt & 1)), (kt >> 1) & 1);
-        if (!ok) over = true;
-        if (!ok) continue;
-        tc_fence_after();
-#pragma unroll 1
-        for (int x = 0; ok && x < 2; x++) {
-          if ((x ? it.nb : it.na) == 0) continue;
-          ok = wait_all(BAR(B_QFULL + x), uint32_t(x ? qb : qa) & 1);
+        const int n = x ? it.nb : it.na, nmax = max(it.na, it.nb);
+        if (n > 0) {
+          ok = wait_all(BAR(B_QFULL + x), uint32_t(qn) & 1) && wait_all(BAR(B_KFULL + (kt & 1)), (kt >> 1) & 1);
           tc_fence_after();
-          if (ok) issue_s(x, kt);
+          if (ok) {
+            issue_s(0, kt);
+            issue_s(1, kt);
+            tc_commit_w(BAR(B_KEMPTY + (kt & 1)));
+          }
+          qn++;
         }
-        tc_commit_w(BAR(B_KEMPTY + (kt & 1)));
+        // P V and the next S of a half one after the other: the tensor core runs them in this
+        // order, so S overwrites P only when it has been read
 #pragma unroll 1
-        for (int bl = 0; ok && bl < 2 * nmax; bl++) {
-          const int j = bl >> 1, x = bl & 1, n_x = x ? it.nb : it.na;
-          const bool last_user = x == 1 || j >= it.nb;  // of V(j) in this order
-          if (j >= n_x) continue;
-          const bool next = j + 1 < n_x;
+        for (int j = 0; ok && j < n; j++) {
           const int kj = kt + j;
-          ok = wait_all(BAR(B_VFULL + (kj & 1)), (kj >> 1) & 1) &&
-               (!next || wait_all(BAR(B_KFULL + ((kj + 1) & 1)), ((kj + 1) >> 1) & 1)) &&
-               wait_all(BAR(B_PFULL + x), uint32_t((x ? sb : sa) + j) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          issue_pv(x, kj, j == 0);
-          if (last_user) tc_commit_w(BAR(B_VEMPTY + (kj & 1)));
-          if (next) {
-            issue_s(x, kj + 1);
-            if (x == 1 || j + 1 >= it.nb) {  // last user of K(j + 1)
-              tc_commit_w(BAR(B_KEMPTY + ((kj + 1) & 1)));
-            }
+          const bool next = j + 1 < n;
+          // K(j + 1) is converted after V(j) by the same warps, so its barrier covers both
+          ok = next ? wait_all(BAR(B_KFULL + ((kj + 1) & 1)), ((kj + 1) >> 1) & 1) : wait_all(BAR(B_VFULL + (kj & 1)), (kj >> 1) & 1);
+#pragma unroll 1
+          for (int h = 0; ok && h < 2; h++) {
+            ok = wait_all(BAR(B_PFULL + 2 * x + h), uint32_t(sn + j) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(h, kj, j + h == 0);
+            if (next) issue_s(h, kj + 1);
+          }
+          if (ok) {
+            tc_commit_w(BAR(B_VEMPTY + (kj & 1)));
+            if (next) tc_commit_w(BAR(B_KEMPTY + ((kj + 1) & 1)));
           }
         }
+        // tiles that only the other rows need: released once they are there
+#pragma unroll 1
+        for (int j = n; ok && j < nmax; j++) {
+          const int kj = kt + j;
+          ok = wait_all(BAR(B_KFULL + (kj & 1)), (kj >> 1) & 1);
+          if (ok && lane == 0) mbar_arrive(BAR(B_KEMPTY + (kj & 1)));
+          ok = ok && wait_all(BAR(B_VFULL + (kj & 1)), (kj >> 1) & 1);
+          if (ok && lane == 0) mbar_arrive(BAR(B_VEMPTY + (kj & 1)));
+          __syncwarp();
+        }
         kt += nmax;
-        sa += it.na;
-        sb += it.nb;
-        qa += it.na > 0;
-        qb += it.nb > 0;
+        sn += n;
         if (!ok) over = true;
       }
       }
@@ -622,45 +631,51 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       float m = -INFINITY, l = 0.0f;
       const float cs = n_x > 0 ? s_cs[lane] : 0.0f;
       uint32_t nan_blocks = 0;
-      for (int j = 0; ok && j < n_x; j++) {
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(B_SFULL + x), uint32_t(st + j) & 1, abort_flag, status));
+      for (int n = 0; ok && n < 2 * n_x; n++) {
+        const int j = n >> 1, h = n & 1;  // tile, half of its keys
+        const uint32_t col = col_s + 64u * uint32_t(h);
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(B_SFULL + 2 * x + h), uint32_t(st + j) & 1, abort_flag, status));
         if (!ok) break;
         tc_fence_after();
-        float s[128];
+        float s[64];
 #pragma unroll
-        for (int c = 0; c < 4; c++) tmem_ld32(col_s + 32 * c, reinterpret_cast<uint32_t*>(s) + 32 * c);
+        for (int c = 0; c < 2; c++) tmem_ld32(col + 32 * c, reinterpret_cast<uint32_t*>(s) + 32 * c);
         const int f4 = (kt + j) & 3;
-        const volatile uint32_t* fl = reinterpret_cast<const volatile uint32_t*>(smem + OFF_FLAG) + f4 * 4;
-        const uint32_t flags = fl[0] | fl[1] | fl[2] | fl[3];
+        const volatile uint32_t* fl = reinterpret_cast<const volatile uint32_t*>(smem + OFF_FLAG) + f4 * 4 + 2 * h;
+        const uint32_t flags = fl[0] | fl[1];
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 4; c++) reg_fence32(reinterpret_cast<uint32_t*>(s) + 32 * c);
-        const int kbase = (it.t0 + j) * TILE;
-        if (__any_sync(0xFFFFFFFFu, kbase + TILE > klim)) {
+        for (int c = 0; c < 2; c++) reg_fence32(reinterpret_cast<uint32_t*>(s) + 32 * c);
+        const int kbase = (it.t0 + j) * TILE + 64 * h;
+        if (__any_sync(0xFFFFFFFFu, kbase + 64 > klim)) {
           const int lim = klim - kbase;
 #pragma unroll
-          for (int e = 0; e < 128; e++)
+          for (int e = 0; e < 64; e++)
             if (e >= lim) s[e] = -INFINITY;
         }
         if (flags) {  // the same for the whole CTA
-          const volatile uint32_t* bad = reinterpret_cast<const volatile uint32_t*>(smem + OFF_BAD) + f4 * 4;
+          const volatile uint32_t* bad = reinterpret_cast<const volatile uint32_t*>(smem + OFF_BAD) + f4 * 4 + 2 * h;
 #pragma unroll
-          for (int q = 0; q < 4; q++) {
+          for (int q = 0; q < 2; q++) {
             const uint32_t w = bad[q];
 #pragma unroll
             for (int e = 0; e < 32; e++)
               if ((w >> e) & 1u) s[32 * q + e] = -INFINITY;
           }
           if (flags & 1u) {
-            const volatile uint8_t* nb = smem + OFF_NAN + f4 * TILE;
-            for (int e = 0; e < TILE && kbase + e < klim; e++) nan_blocks |= nb[e];
+            const volatile uint8_t* nb = smem + OFF_NAN + f4 * TILE + 64 * h;
+            for (int e = 0; e < 64 && kbase + e < klim; e++) nan_blocks |= nb[e];
           }
           __syncwarp();
         }
-        float pm = fmaxf(s[0], s[127]);
+        float pm[2];  // two chains
 #pragma unroll
-        for (int e = 1; e < 127; e += 2) pm = fmax3(pm, s[e], s[e + 1]);
-        const float top = pm * cs;
+        for (int q = 0; q < 2; q++) {
+          pm[q] = fmaxf(s[32 * q], s[32 * q + 1]);
+#pragma unroll
+          for (int e = 2; e < 32; e += 2) pm[q] = fmax3(pm[q], s[32 * q + e], s[32 * q + e + 1]);
+        }
+        const float top = fmaxf(pm[0], pm[1]) * cs;
         float alpha = 1.0f;
         bool rescale = false;
         if (top > m + kLazy) {  // also from m = -inf on
@@ -669,19 +684,21 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
           m = top;
         }
         const float off = m == -INFINITY ? 0.0f : kOffset - m;
-        uint32_t p[64];
+        uint32_t p[32];
         float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int e = 0; e < 64; e++) {
+        for (int e = 0; e < 32; e++) {
           const float2 v = ffma2(make_float2(s[2 * e], s[2 * e + 1]), make_float2(cs, cs), make_float2(off, off));
           const float2 y = make_float2(ex2(v.x), ex2(v.y));
           sum = fadd2(sum, y);
           p[e] = pack_f16(y.x, y.y);
         }
         l = l * alpha + (sum.x + sum.y);
-        // O_X holds PV_X(j - 1): S_X(j) has completed, and its commit covers every
-        // earlier product.  PV_X(j) waits for this tile's P.
+        // O_X is added to by the product of the half before; this half's waits for its P
         if (__any_sync(0xFFFFFFFFu, rescale)) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(B_ODONE + 2 * x + (h ^ 1)), uint32_t(st + j - (h ^ 1)) & 1, abort_flag, status));
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
           for (int c = 0; c < 4; c++) {
             uint32_t o[32];
@@ -699,17 +716,17 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
           }
         }
 #pragma unroll
-        for (int c = 0; c < 4; c++) tmem_st16(col_s + 16 * c, p + 16 * c);
+        for (int c = 0; c < 2; c++) tmem_st16(col + 16 * c, p + 16 * c);
         tmem_wait_st();
         tc_fence_before();
-        warp_arrive(BAR(B_PFULL + x));
+        warp_arrive(BAR(B_PFULL + 2 * x + h));
       }
       // the last S has been read, so the tile's queries may be replaced
       if (!ok) break;
       more = take(i++, next_it, ok);
       if (more) load_q(next_it);
       // the part's rows: O / l and lse, or a partial record
-      if (ok && n_x > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(B_ODONE + x), uint32_t(st + n_x - 1) & 1, abort_flag, status));
+      if (ok && n_x > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(B_ODONE + 2 * x + 1), uint32_t(st + n_x - 1) & 1, abort_flag, status));
       if (!ok) break;
       tc_fence_after();
       const float nanv = __uint_as_float(0x7FC00000u);
