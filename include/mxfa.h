@@ -533,7 +533,7 @@ size_t mxfa_kv_attn_workspace_size(int R, int max_q, int64_t max_k, int Hq, int 
  * outside the cache (its keys count as not there) and offsets or lengths outside
  * their tables (the request is left out) are recorded as failed index checks.
  * o, lse and ws overlap neither each other nor an input (MXFA_ERR_INVALID_ARG).
- * max_blocks * page <= 2^30, and <= 2^25 where max_q * G > 64 (else
+ * max_blocks * page <= 2^30, and <= 2^25 where max_q * G > 48 (else
  * MXFA_ERR_UNSUPPORTED). */
 mxfa_status mxfa_kv_attn(const mxfa_kv_cache* cache, const void* q, int64_t q_stride, int64_t total_q,
                          const int32_t* cu_q, const int32_t* kv_lens, int R, const int32_t* block_table,

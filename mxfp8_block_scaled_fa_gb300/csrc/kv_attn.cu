@@ -34,6 +34,17 @@
 // its V fragments are 16 consecutive channels of four keys, two keys' codes
 // merged into bytes before conversion so that the pair (key, key + 1) comes
 // out of one conversion.
+//
+// What bounds it.  A row of 136 or 144 bytes takes the SM some ten cycles of instructions:
+// 617 a warp for 32 keys and one tile of rows (a quarter of them conversions), which
+// keeps the schedulers 59% and the ALUs 50% busy.  64 requests of up to 8192 keys, 8 key
+// heads, G = 4, MXFP4: 66 us, 3.8 TB/s (56% of a copy's rate); three of 97,000 to 130,000
+// keys, G = 8, NVFP4: 87 us, 4.4 TB/s.  Requests of 24 to 48 rows (3 to 6 tokens x 8) over
+// up to 12288 keys: 110 us, 207 TFLOP/s; there every tile of rows adds 150 instructions,
+// and a second block of rows converts the cache again.  Other forms, in their time: query
+// rows as M 115 us for the first case where keys as M took 88; bulk copies, which
+// compile to a loop over the lanes, 91 where these take 85; two chains of score
+// products, no change.
 #include "kv_fp4.cuh"
 #include "mx_ptx.cuh"
 #include "mxfa_internal.h"
@@ -50,8 +61,14 @@ constexpr int kStages = 3;
 constexpr float kOffset = 8.0f;           // log2 offset of P
 constexpr float kLazy = 6.0f;             // growth of a row maximum that moves m
 constexpr int kMaxNt = 4;                 // blocks of at most 32 query rows
-constexpr int kMinTiles = 4;              // least tiles of a run, as long as items are cut
-constexpr int kItemTiles = 3;             // what an item costs beside its tiles (drain, merge), in tiles
+// Least units of a run, as long as items are cut.  Contexts of at most as many tiles
+// (512 keys) are not cut at all: us for 1, 16 and 64 requests of 512 keys 7.7, 8.2, 16.3
+// whole and 10.8, 13.0, 21.6 cut; of 2048 keys 19.4, 21.9, 40.7 and 11.6, 20.9, 44.5.
+constexpr int kMinTiles = 4;
+// What an item costs beside its tiles (drain, merge), in tiles: 1, 2, 3 and 4 take 133,
+// 116, 110.7 and 110.7 us for the drafted tokens above, 72.6, 66.8, 65.9 and 66.7 us for
+// the 64 requests.
+constexpr int kItemTiles = 3;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 // CTAs of an SM for NT 8-row tiles: 16, 12 or 8 warps, as 32 NT accumulator registers
@@ -871,7 +888,8 @@ __global__ void __launch_bounds__(256) kv_join_kernel(KvAttnArgs a, int ctas) {
 }
 
 // Tiles of eight query rows in a block: as few blocks of at most 32 rows as there
-// can be, of equal size (48 rows: two of 24).
+// can be, of equal size (48 rows: two of 24; 110 us for the drafted tokens above, where
+// blocks of 32 take 132, as four tiles spill, and blocks of 16 take 125).
 int row_tiles(int64_t rows) {
   const int64_t blocks = (rows + 8 * kMaxNt - 1) / (8 * kMaxNt);
   return int((rows + 8 * blocks - 1) / (8 * blocks));
@@ -938,7 +956,11 @@ size_t workspace_of(int nt) {
 // Up to kFewRows: this file's alone, with tiles for that many rows.  Above: this
 // file's for the requests of at most kMixedRows rows, with tiles for a single token
 // (the decoding requests of a mixed batch), and kv_prefill.cu's for the others.
-constexpr int kFewRows = 64, kMixedRows = 32;
+// Measured here / there, in us, with 8 key heads and MXFP4: 24 requests of 6000 keys
+// with 24 rows each 70 / 119, 32 rows 85 / 121, 48 rows 123 / 121, 56 rows 153 / 122.
+// One prompt of 512 tokens with 48 requests of 4096 keys, these with 16 rows 197 / 237,
+// 24 rows 239 / 244, 32 rows 281 / 245.
+constexpr int kFewRows = 48, kMixedRows = 24;
 struct Plan {
   int nt, split_rows;
   bool prefill;

@@ -11,7 +11,7 @@
 // writes the requests' places on the line first.
 //
 // CTA: 16 warps.
-//   warp 0       tcgen05 issuer and TMEM owner
+//   warps 0, 2   tcgen05 issuers of the row tiles A and B; warp 0 owns the TMEM
 //   warp 1       walks the run and publishes its items (two-entry ring)
 //   warps 4-7    softmax of rows 0..127 (tile A): thread = row = TMEM lane; and tile A's
 //                queries of the next item, as soon as its last S is done
@@ -19,15 +19,27 @@
 //   warps 12-15  conversion: 4-bit rows of K and V from global memory (held in
 //                registers half a tile ahead) to binary16 tiles in shared memory, 128B
 //                swizzle, two of each
-// The tensor core alternates between the tiles: S_A(j+1) and PV_A(j) run while tile
-// B's softmax does, and so on.  K is read as the K-major and V as the MN-major operand
-// of the same layout: [channel half][key][64 channels].
-//   TMEM (512 columns): S_A, S_B, O_A, O_B of 128; P_X (64 columns of binary16
-//   pairs) replaces S_X, whose next product is issued after the one that reads P_X.
+// K is read as the K-major and V as the MN-major operand of the same layout: [channel
+// half][key][64 channels].
+//   TMEM (512 columns): S_A, S_B, O_A, O_B of 128.  S_X is two halves of 64 keys; a
+//   half's P (32 columns of binary16 pairs) replaces its S, and the half's next S is
+//   issued behind the product that reads P.  So the tensor core works on one half
+//   while the softmax warps are at the other, of both tiles.
 //
-// A tile takes 4 x 512 tensor cycles for 256 rows, and as long for the 32768
-// exponentials at 16 a cycle; the conversions (1/4 code each of the ALUs' 64 a cycle) fit
-// beside them.
+// What bounds it.  A tile of 128 keys x 256 rows is 4 x 512 cycles of the tensor core, and
+// half as long for the 32768 exponentials.  The products of 64 keys read Q again for
+// each half (6 KB of shared memory in 32 cycles, where 128 B a cycle is the most), and
+// take 50 to 90 cycles each instead of 32.  Chunks of 2048 and 1687 tokens over 8192 and
+// 5331 keys, 8 key heads, G = 4, NVFP4: 312 us, 1170 TFLOP/s, of which the main
+// kernel 292 us; about 3400 cycles a tile (issuers: P V 750, S 1400, four waits), and
+// 12000 cycles between items, when the softmax warps bring the next queries and write
+// O.  Other forms of it, same case: whole S products of 128 keys and one issuer,
+// softmax, P V and S in turn, 347 us; these with two issuers 360 to 407 us; halves with
+// one issuer 457 us (a product is issued in 40 to 55 cycles, a commit in 100);
+// conversion with coalesced loads (four lanes a row) 435 against 379 us, as the swizzled
+// stores then cost more; items of up to 128 rows with both softmax groups on the same
+// rows, even and odd key tiles, 137 against 134 us for 24 x 64 rows over 6000 keys;
+// the three small kernels launched early 317 us.
 #include "kv_fp4.cuh"
 #include "mx_ptx.cuh"
 #include "mxfa_internal.h"
@@ -41,8 +53,10 @@ namespace kvp {
 constexpr int TILE = 128;                // keys of a tile, rows of an MMA
 constexpr int ROWS = 256;                // query rows of an item
 constexpr int OP_BYTES = TILE * 256;     // 128 rows x 128 binary16
-constexpr int kItemTiles = 2;            // what an item costs beside its tiles
-constexpr int kMinUnits = 6;             // least units of a run
+// What an item costs beside its tiles, in tiles: 319 us with 1 for the prompts above, 317
+// with 2, 314 with 3, 312 with 4.
+constexpr int kItemTiles = 4;
+constexpr int kMinUnits = 6;             // least units of a run: a shorter one costs more to join than it saves
 constexpr float kOffset = 8.0f, kLazy = 6.0f;  // as in kv_attn.cu
 
 constexpr int OFF_Q = 0;                           // tiles A, B

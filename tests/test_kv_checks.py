@@ -201,5 +201,5 @@ def test_attention_context_limits(mx):
     L, ref = mx.lib(), ctypes.byref(_cache(mx, page=128))
     call = lambda nb, mq: L.mxfa_kv_attn(ref, 0x10000, 512, 200, 0x20000, 0x30000, 1, 0x40000, nb, mq, 4, 0.1, 1, 0x50000, 0x90000, None, 0, None)
     # no workspace is given: 1 or 6 (too small) where the sizes are accepted
-    assert call(1 << 24, 200) == 2 and call((1 << 18) + 1, 33) == 2             # more than 2^25 keys for more than 64 rows
-    assert call(1 << 18, 33) != 2 and call(1 << 23, 32) != 2 and call((1 << 23) + 1, 32) == 2
+    assert call(1 << 24, 200) == 2 and call((1 << 18) + 1, 25) == 2             # more than 2^25 keys for more than 48 rows
+    assert call(1 << 18, 25) != 2 and call(1 << 23, 24) != 2 and call((1 << 23) + 1, 24) == 2
