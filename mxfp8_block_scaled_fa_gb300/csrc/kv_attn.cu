@@ -12,7 +12,7 @@
 // to binary16 with a power of two per row that puts its largest element in
 // [2^14, 2^15): bf16 has 8 significant bits, so only elements 2^28 below the
 // row's largest lose any.  The products accumulate in fp32.  P = 2^(s - m + 8)
-// is rounded to binary16 (11 bits; relative 2^-12, against 2^-9 for the bf16
+// is rounded to binary16 (11 bits; relative 2^-11, against 2^-8 for the bf16
 // result), where the offset 8 keeps weights down to 2^-32 of the largest from
 // vanishing; m moves when a score exceeds it by more than 6, so P <= 2^14.
 //
