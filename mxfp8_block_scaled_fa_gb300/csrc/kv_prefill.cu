@@ -594,19 +594,27 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
     float* s_cs = reinterpret_cast<float*>(smem + OFF_CS) + x * TILE + (warp & 3) * 32;  // of this warp's rows
     // this warp's 32 query rows of an item: binary16 with a power of two per row; eight
     // lanes per row, 16 channels each, all loads in flight at once
+    const int tok4 = 4 / a.G, hd4 = 4 - tok4 * a.G;  // four rows further
     auto load_q = [&](const Item& it) {
       if ((x ? it.nb : it.na) == 0) return;
       const int part = lane & 7;
       uint4 v[8][2];
+      int qr = x * TILE + (warp & 3) * 32 + (lane >> 3);
+      int tok = (it.row0 + qr) / a.G, hd = it.row0 + qr - tok * a.G;
+      const int tok0 = it.row0 / a.G, hd0 = it.row0 - tok0 * a.G;
 #pragma unroll
       for (int p = 0; p < 8; p++) {
-        const int qr = x * TILE + (warp & 3) * 32 + p * 4 + (lane >> 3);
-        v[p][0] = v[p][1] = make_uint4(0, 0, 0, 0);
-        if (qr < it.rows) {
-          const int rr = it.row0 + qr, tok = rr / a.G, hd = rr - tok * a.G;
-          const uint16_t* src = a.q + int64_t(it.q0 + tok) * a.q_stride + int64_t(it.h * a.G + hd) * 128 + part * 16;
-          v[p][0] = __ldg(reinterpret_cast<const uint4*>(src));
-          v[p][1] = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+        // rows that are none take the item's first: nothing of them is written
+        const int64_t t = it.q0 + (qr < it.rows ? tok : tok0);
+        const uint16_t* src = a.q + t * a.q_stride + int64_t(it.h * a.G + (qr < it.rows ? hd : hd0)) * 128 + part * 16;
+        v[p][0] = __ldg(reinterpret_cast<const uint4*>(src));
+        v[p][1] = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+        qr += 4;
+        tok += tok4;
+        hd += hd4;
+        if (hd >= a.G) {
+          hd -= a.G;
+          tok++;
         }
       }
 #pragma unroll
