@@ -466,45 +466,52 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       x.q0 = it.q0, x.n = it.n, x.kv = it.kv;
       const int keys = keys_of(a, x, it.row0 + it.rows);  // that some row sees
       // this thread's row of tile j of the part: codes and scales, K and V
+      // What a load brings is first looked at half a tile later, or it would be waited for:
+      // the table entry two tiles ahead, V's scales with K's row.
       uint4 kc[4], vc[4];
-      uint2 ks, vs;
-      int64_t row;      // cache row of the tile's key, -1: none
-      int64_t next_row;
-      auto find = [&](int j) -> int64_t {
+      uint2 ks, vs, next_vs;
+      int64_t row;      // cache row of the tile's key, -1: none, -2: not in the cache
+      int next_block;   // table entry of the next tile's key
+      auto entry = [&](int j) -> int {
+        const int key = (it.t0 + j) * TILE + t;
+        return j < nmax && key < keys ? __ldg(table + (key >> a.c.page_shift)) : -1;
+      };
+      auto find = [&](int b, int j) -> int64_t {
         const int key = (it.t0 + j) * TILE + t;
         if (j >= nmax || key >= keys) return -1;
-        const int b = __ldg(table + (key >> a.c.page_shift));
         if (b < 0 || b >= a.c.blocks) return -2;
         return (int64_t(b) * a.c.H + it.h) * a.c.page + (key & (a.c.page - 1));
       };
       auto load_k = [&](int64_t at) {
 #pragma unroll
         for (int w = 0; w < 4; w++) kc[w] = make_uint4(0, 0, 0, 0);
-        ks = make_uint2(0, 0);
+        ks = next_vs = make_uint2(0, 0);
         if (at >= 0) {
           const uint4* src = reinterpret_cast<const uint4*>(a.c.k + at * 64);
 #pragma unroll
           for (int w = 0; w < 4; w++) kc[w] = __ldg(src + w);
-          if (FMT == 0) ks.x = __ldg(reinterpret_cast<const uint32_t*>(a.c.k_sf + at * 4));
-          else ks = __ldg(reinterpret_cast<const uint2*>(a.c.k_sf + at * 8));
+          if (FMT == 0) {
+            ks.x = __ldg(reinterpret_cast<const uint32_t*>(a.c.k_sf + at * 4));
+            next_vs.x = __ldg(reinterpret_cast<const uint32_t*>(a.c.v_sf + at * 4));
+          } else {
+            ks = __ldg(reinterpret_cast<const uint2*>(a.c.k_sf + at * 8));
+            next_vs = __ldg(reinterpret_cast<const uint2*>(a.c.v_sf + at * 8));
+          }
         }
       };
       auto load_v = [&](int64_t at) {
 #pragma unroll
         for (int w = 0; w < 4; w++) vc[w] = make_uint4(0, 0, 0, 0);
-        vs = make_uint2(0, 0);
         if (at >= 0) {
           const uint4* src = reinterpret_cast<const uint4*>(a.c.v + at * 64);
 #pragma unroll
           for (int w = 0; w < 4; w++) vc[w] = __ldg(src + w);
-          if (FMT == 0) vs.x = __ldg(reinterpret_cast<const uint32_t*>(a.c.v_sf + at * 4));
-          else vs = __ldg(reinterpret_cast<const uint2*>(a.c.v_sf + at * 8));
         }
       };
-      row = find(0);
+      row = find(entry(0), 0);
       load_k(row);
       load_v(row);
-      next_row = find(1);
+      next_block = entry(1);
       // a row of a tile: sixteen words of eight channels, chunk (16 bytes) w of 16
       auto put = [&](uint32_t tile, const uint4* c, const uint32_t* s2) {
         const uint32_t dst = tile + uint32_t(t) * 128u;
@@ -545,6 +552,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
         // NaN blocks of V: taken out of the product here, put into the rows that see the
         // key by their softmax threads; keys whose block is not in the cache
         uint32_t nan = 0;
+        vs = next_vs;
         if (FMT == 0) {
           const uint32_t m = __vcmpeq4(vs.x, 0xFFFFFFFFu);
           vs.x &= ~m;
@@ -567,18 +575,18 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
         uint32_t s2[8];
         scales(ks, s2);
         put(base + OFF_K + st * OP_BYTES, kc, s2);
-        load_k(next_row);
+        row = find(next_block, j + 1);
+        load_k(row);
         fence_async_smem();
         warp_arrive(BAR(B_KFULL + st));
         if (kt >= 2) ok = wait_all(BAR(B_VEMPTY + st), ((kt >> 1) - 1) & 1);
         if (!ok) break;
         scales(vs, s2);
         put(base + OFF_V + st * OP_BYTES, vc, s2);
-        load_v(next_row);
+        load_v(row);
+        next_block = entry(j + 2);
         fence_async_smem();
         warp_arrive(BAR(B_VFULL + st));
-        row = next_row;
-        next_row = find(j + 2);
       }
       if (!ok) break;
     }
