@@ -957,9 +957,9 @@ size_t workspace_of(int nt) {
 // file's for the requests of at most kMixedRows rows, with tiles for a single token
 // (the decoding requests of a mixed batch), and kv_prefill.cu's for the others.
 // Measured here / there, in us, with 8 key heads and MXFP4: 24 requests of 6000 keys
-// with 24 rows each 70 / 119, 32 rows 85 / 121, 48 rows 123 / 121, 56 rows 153 / 122.
-// One prompt of 512 tokens with 48 requests of 4096 keys, these with 16 rows 197 / 237,
-// 24 rows 239 / 244, 32 rows 281 / 245.
+// with 24 rows each 70 / 114, 32 rows 85 / 115, 48 rows 123 / 116, 56 rows 153 / 116; 24
+// to 48 rows over up to 12288 keys 111 / 118.  One prompt of 512 tokens with 48 requests
+// of 4096 keys, these with 16 rows 195 / 232, 24 rows 237 / 232, 32 rows 281 / 233.
 constexpr int kFewRows = 48, kMixedRows = 24;
 struct Plan {
   int nt, split_rows;

@@ -30,16 +30,17 @@
 // half as long for the 32768 exponentials.  The products of 64 keys read Q again for
 // each half (6 KB of shared memory in 32 cycles, where 128 B a cycle is the most), and
 // take 50 to 90 cycles each instead of 32.  Chunks of 2048 and 1687 tokens over 8192 and
-// 5331 keys, 8 key heads, G = 4, NVFP4: 312 us, 1170 TFLOP/s, of which the main
-// kernel 292 us; about 3400 cycles a tile (issuers: P V 750, S 1400, four waits), and
-// 12000 cycles between items, when the softmax warps bring the next queries and write
-// O.  Other forms of it, same case: whole S products of 128 keys and one issuer,
-// softmax, P V and S in turn, 347 us; these with two issuers 360 to 407 us; halves with
-// one issuer 457 us (a product is issued in 40 to 55 cycles, a commit in 100);
-// conversion with coalesced loads (four lanes a row) 435 against 379 us, as the swizzled
-// stores then cost more; items of up to 128 rows with both softmax groups on the same
-// rows, even and odd key tiles, 137 against 134 us for 24 x 64 rows over 6000 keys;
-// the three small kernels launched early 317 us.
+// 5331 keys, 8 key heads, G = 4, NVFP4: 309 us, 1180 TFLOP/s, of which the main
+// kernel 290 us; about 3300 cycles a tile (issuers: P V 750, S 1400, waits), and
+// 12000 cycles between items, when the softmax warps bring the next queries (half of
+// them) and write O.  Other forms of it, same case: whole S products of 128 keys and
+// one issuer, softmax, P V and S in turn, 347 us; these with two issuers 360 to 407 us;
+// halves with one issuer 457 us (a product is issued in 40 to 55 cycles, a commit in
+// 100); conversion with coalesced loads (four lanes a row) 435 against 379 us, as the
+// swizzled stores then cost more; O written through shared memory by rows, 315 against
+// 312 us; the small kernels launched early 317 against 314 us.  For items of up to 128
+// rows both softmax groups on the same rows, each with half of the keys, 137 against 117
+// us for 24 x 64 rows over 6000 keys.
 #include "kv_fp4.cuh"
 #include "mx_ptx.cuh"
 #include "mxfa_internal.h"
@@ -53,8 +54,8 @@ namespace kvp {
 constexpr int TILE = 128;                // keys of a tile, rows of an MMA
 constexpr int ROWS = 256;                // query rows of an item
 constexpr int OP_BYTES = TILE * 256;     // 128 rows x 128 binary16
-// What an item costs beside its tiles, in tiles: 319 us with 1 for the prompts above, 317
-// with 2, 314 with 3, 312 with 4.
+// What an item costs beside its tiles, in tiles: 1, 2, 3 and 4 took 319, 317, 314 and 312
+// us for the prompts above.
 constexpr int kItemTiles = 4;
 constexpr int kMinUnits = 6;             // least units of a run: a shorter one costs more to join than it saves
 constexpr float kOffset = 8.0f, kLazy = 6.0f;  // as in kv_attn.cu
