@@ -3,6 +3,7 @@ Python module of the 4-bit cache's calls, with g++."""
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -13,7 +14,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libmxfa.so")
-PY_MODULE = os.path.join(OUT, "kv_py.so")
+# named by the torch it is built for, whose C++ interface it uses
+PY_MODULE = os.path.join(OUT, f"kv_py-{importlib.metadata.version('torch')}.so")
 PY_SRC = os.path.join(CSRC, "kv_py.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
