@@ -40,7 +40,7 @@
 // keeps the schedulers 59% and the ALUs 50% busy.  64 requests of up to 8192 keys, 8 key
 // heads, G = 4, MXFP4: 66 us, 3.8 TB/s (56% of a copy's rate); three of 97,000 to 130,000
 // keys, G = 8, NVFP4: 87 us, 4.4 TB/s.  Requests of 24 to 48 rows (3 to 6 tokens x 8) over
-// up to 12288 keys: 110 us, 207 TFLOP/s; there every tile of rows adds 150 instructions,
+// up to 12288 keys: 109 us, 210 TFLOP/s; there every tile of rows adds 150 instructions,
 // and a second block of rows converts the cache again.  Other forms, in their time: query
 // rows as M 115 us for the first case where keys as M took 88; bulk copies, which
 // compile to a loop over the lanes, 91 where these take 85; two chains of score
@@ -61,10 +61,11 @@ constexpr int kStages = 3;
 constexpr float kOffset = 8.0f;           // log2 offset of P
 constexpr float kLazy = 6.0f;             // growth of a row maximum that moves m
 constexpr int kMaxNt = 4;                 // blocks of at most 32 query rows
-// Least units of a run, as long as items are cut.  Contexts of at most as many tiles
-// (512 keys) are not cut at all: us for 1, 16 and 64 requests of 512 keys 7.7, 8.2, 16.3
-// whole and 10.8, 13.0, 21.6 cut; of 2048 keys 19.4, 21.9, 40.7 and 11.6, 20.9, 44.5.
-constexpr int kMinTiles = 4;
+constexpr int kMinTiles = 4;              // least units of a run, as long as items are cut
+// Contexts of at most as many tiles (1024 keys) are not cut at all: us for 1, 16 and 64
+// requests of 512 keys 7.7, 8.2, 16.3 whole and 10.8, 13.0, 21.6 cut; of 1024 keys
+// 11.8, 12.0, 24.6 and 11.4, 14.7, 29.8; of 2048 keys 19.4, 21.9, 40.7 and 11.6, 20.9, 44.5.
+constexpr int kWholeTiles = 8;
 // What an item costs beside its tiles (drain, merge), in tiles: 1, 2, 3 and 4 take 133,
 // 116, 110.7 and 110.7 us for the drafted tokens above, 72.6, 66.8, 65.9 and 66.7 us for
 // the 64 requests.
@@ -604,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
   int k_lo, k_end, steps;
   const int32_t* table;
   uint32_t b0 = 0, b1 = 0;
-  auto look_up = [&](int step) {
+  auto look_up = [&](int step, uint32_t& b0, uint32_t& b1) {
     const int key = k_lo + (lane >> 1) + step * kTile;
     b0 = key < k_end ? uint32_t(__ldg(table + (key >> a.c.page_shift))) : 0xFFFFFFFFu;
     if (small_pages) b1 = key + 16 < k_end ? uint32_t(__ldg(table + (key >> 4) + 1)) : 0xFFFFFFFFu;
@@ -639,19 +640,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
     steps = k_lo < k_end ? (k_end - k_lo + kTile - 1) / kTile : 0;
     table = a.table + int64_t(it.r) * a.width;
     wk.aim(a.c, k_lo, it.h);
-    if (steps > 0) {
-      look_up(0);
-      seen0 = issue(0, 0);
-      look_up(1);
-    } else {
-      cp_commit();
+    // the first three steps' blocks at once, or each would be waited for
+    uint32_t e0[3], e1[3];
+#pragma unroll
+    for (int s = 0; s < 3; s++) look_up(s, e0[s], e1[s]);
+#pragma unroll
+    for (int s = 0; s < 2; s++) {
+      b0 = e0[s], b1 = e1[s];
+      if (s < steps) (s == 0 ? seen0 : seen1) = issue(s, s);
+      else cp_commit();
     }
-    if (steps > 1) {
-      seen1 = issue(1, 1);
-      look_up(2);
-    } else {
-      cp_commit();
-    }
+    b0 = e0[2], b1 = e1[2];
     // eight threads per row, 16 channels each
 #pragma unroll
     for (int pass = 0; pass < kPasses; pass++) {
@@ -725,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
       uint32_t seen2 = 0;
       if (step + 2 < steps) {
         seen2 = issue(step + 2, stage == 0 ? 2 : stage - 1);
-        look_up(step + 3);
+        look_up(step + 3, b0, b1);
       } else {
         cp_commit();
       }
@@ -968,7 +967,7 @@ struct Plan {
 };
 Plan plan_of(int max_q, int64_t max_k, int G) {
   const int64_t rows = int64_t(max_q < 1 ? 1 : max_q) * G;
-  if (rows <= kFewRows) return Plan{row_tiles(rows), kFewRows, false, rows <= 8 * kMaxNt && max_k <= kMinTiles * kTile};
+  if (rows <= kFewRows) return Plan{row_tiles(rows), kFewRows, false, rows <= 8 * kMaxNt && max_k <= kWholeTiles * kTile};
   return Plan{row_tiles(G < kMixedRows ? G : kMixedRows), kMixedRows, true, false};
 }
 
