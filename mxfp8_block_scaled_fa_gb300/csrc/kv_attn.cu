@@ -37,7 +37,7 @@
 //
 // What bounds it.  A row of 136 or 144 bytes takes the SM some ten cycles of instructions:
 // 617 a warp for 32 keys and one tile of rows (a quarter of them conversions), which
-// keeps the schedulers 59% and the ALUs 50% busy.  64 requests of up to 8192 keys, 8 key
+// keeps the schedulers 55% and the ALUs 44% busy.  64 requests of up to 8192 keys, 8 key
 // heads, G = 4, MXFP4: 66 us, 3.8 TB/s (56% of a copy's rate); three of 97,000 to 130,000
 // keys, G = 8, NVFP4: 87 us, 4.4 TB/s.  Requests of 24 to 48 rows (3 to 6 tokens x 8) over
 // up to 12288 keys: 109 us, 210 TFLOP/s; there every tile of rows adds 150 instructions,
