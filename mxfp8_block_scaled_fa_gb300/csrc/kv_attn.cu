@@ -40,7 +40,7 @@
 // keeps the schedulers 55% and the ALUs 44% busy.  64 requests of up to 8192 keys, 8 key
 // heads, G = 4, MXFP4: 66 us, 3.8 TB/s (56% of a copy's rate); three of 97,000 to 130,000
 // keys, G = 8, NVFP4: 87 us, 4.4 TB/s.  Requests of 24 to 48 rows (3 to 6 tokens x 8) over
-// up to 12288 keys: 109 us, 210 TFLOP/s; there every tile of rows adds 150 instructions,
+// up to 12288 keys: 108 us, 212 TFLOP/s; there every tile of rows adds 150 instructions,
 // and a second block of rows converts the cache again.  Other forms, in their time: query
 // rows as M 115 us for the first case where keys as M took 88; bulk copies, which
 // compile to a loop over the lanes, 91 where these take 85; two chains of score
@@ -295,6 +295,41 @@ struct Worker {
       for (int u = 0; u < 2; u++)
 #pragma unroll
         for (int e = 0; e < 4; e++) sc[t][u][e] = 0.0f;
+    // V: a NaN block (scale byte 0xFF or 0x7F) reaches every row through 0 x NaN, so
+    // where rows see different keys it is taken out of the product and put into the
+    // rows that see its key; so are rows that are no keys and may hold anything.  Its
+    // words are read ahead of K's products (drafted tokens 109 -> 108 us).
+    const uint32_t vrow = ((((g >> 1) ^ (((c >> 1) & 1) << 1)) << 4) + ((g & 1) << 3));
+    const int ka = key_of(2 * c), kb = key_of(2 * c + 1);
+    uint2 va[2][2], vb[2][2];
+    uint32_t bs[2][2];
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+#pragma unroll
+      for (int x = 0; x < 2; x++) {
+        const int key = (2 * u + x) * 8;
+        va[u][x] = lds8(s + kStep * 64 + (key + ka) * 64 + vrow);
+        vb[u][x] = lds8(s + kStep * 64 + (key + kb) * 64 + vrow);
+        uint32_t b0, b1;
+        if (FMT == 0) {
+          b0 = lds_u8(sfv + (key + ka) * 4 + (g >> 1));
+          b1 = lds_u8(sfv + (key + kb) * 4 + (g >> 1));
+          if (MASKED) {
+            if (b0 == 0xFFu || !((seen >> (key + ka)) & 1u)) b0 = 0;
+            if (b1 == 0xFFu || !((seen >> (key + kb)) & 1u)) b1 = 0;
+          }
+          bs[u][x] = e8m0_pair(b0, b1);
+        } else {
+          b0 = lds_u8(sfv + (key + ka) * 8 + g);
+          b1 = lds_u8(sfv + (key + kb) * 8 + g);
+          if (MASKED) {
+            if ((b0 & 0x7Fu) == 0x7Fu || !((seen >> (key + ka)) & 1u)) b0 = 0;
+            if ((b1 & 0x7Fu) == 0x7Fu || !((seen >> (key + kb)) & 1u)) b1 = 0;
+          }
+          bs[u][x] = e4m3_pair(b0 | (b1 << 8));
+        }
+      }
+    }
     {
       uint32_t kw[2][2][4], ks[2][2][2];  // [16 keys][first or second eight][word or scale]
 #pragma unroll
@@ -398,55 +433,24 @@ struct Worker {
           pf[t][u][x] = transpose8x8(pack_f16(p0, p1));
         }
     }
-    // V: a NaN block (scale byte 0xFF or 0x7F) reaches every row through 0 x NaN, so
-    // where rows see different keys it is taken out of the product and put into the
-    // rows that see its key; so are rows that are no keys and may hold anything
-    const uint32_t vrow = ((((g >> 1) ^ (((c >> 1) & 1) << 1)) << 4) + ((g & 1) << 3));
-    const int ka = key_of(2 * c), kb = key_of(2 * c + 1);
 #pragma unroll
     for (int u = 0; u < 2; u++) {
-      uint32_t bs[2];
-      uint2 va[2], vb[2];
-#pragma unroll
-      for (int x = 0; x < 2; x++) {
-        const int key = (2 * u + x) * 8;
-        va[x] = lds8(s + kStep * 64 + (key + ka) * 64 + vrow);
-        vb[x] = lds8(s + kStep * 64 + (key + kb) * 64 + vrow);
-        uint32_t b0, b1;
-        if (FMT == 0) {
-          b0 = lds_u8(sfv + (key + ka) * 4 + (g >> 1));
-          b1 = lds_u8(sfv + (key + kb) * 4 + (g >> 1));
-          if (MASKED) {
-            if (b0 == 0xFFu || !((seen >> (key + ka)) & 1u)) b0 = 0;
-            if (b1 == 0xFFu || !((seen >> (key + kb)) & 1u)) b1 = 0;
-          }
-          bs[x] = e8m0_pair(b0, b1);
-        } else {
-          b0 = lds_u8(sfv + (key + ka) * 8 + g);
-          b1 = lds_u8(sfv + (key + kb) * 8 + g);
-          if (MASKED) {
-            if ((b0 & 0x7Fu) == 0x7Fu || !((seen >> (key + ka)) & 1u)) b0 = 0;
-            if ((b1 & 0x7Fu) == 0x7Fu || !((seen >> (key + kb)) & 1u)) b1 = 0;
-          }
-          bs[x] = e4m3_pair(b0 | (b1 << 8));
-        }
-      }
 #pragma unroll
       for (int w = 0; w < 2; w++) {
         uint32_t e0[4], o0[4], e1[4], o1[4];  // even and odd channels of the first and second eight keys
         {
-          const uint32_t x = w ? va[0].y : va[0].x, y = w ? vb[0].y : vb[0].x;
+          const uint32_t x = w ? va[u][0].y : va[u][0].x, y = w ? vb[u][0].y : vb[u][0].x;
           e2m1x8_to_f16((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), e0);
           e2m1x8_to_f16(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), o0);
         }
         {
-          const uint32_t x = w ? va[1].y : va[1].x, y = w ? vb[1].y : vb[1].x;
+          const uint32_t x = w ? va[u][1].y : va[u][1].x, y = w ? vb[u][1].y : vb[u][1].x;
           e2m1x8_to_f16((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), e1);
           e2m1x8_to_f16(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), o1);
         }
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-          const uint32_t a[4] = {hmul2(e0[j], bs[0]), hmul2(o0[j], bs[0]), hmul2(e1[j], bs[1]), hmul2(o1[j], bs[1])};
+          const uint32_t a[4] = {hmul2(e0[j], bs[u][0]), hmul2(o0[j], bs[u][0]), hmul2(e1[j], bs[u][1]), hmul2(o1[j], bs[u][1])};
 #pragma unroll
           for (int t = 0; t < NT; t++) mma_f16(acc[t][w * 4 + j], a, pf[t][u][0], pf[t][u][1]);
         }
