@@ -38,11 +38,11 @@ static __device__ unsigned g_status_kv;
 // then takes its share of table entries and tokens: nothing waits on another
 // CTA, except that the lengths and the ring counters, which may be updated in
 // place, are written after a barrier of the only cluster.  The work is a few
-// kilobytes for a decoding step, bound by latency (16 requests: 4.1 us, the chain
+// kilobytes for a decoding step, bound by latency (16 requests: 4.4 us, the chain
 // lengths, scans, ring, table, slots); a step with prompts writes 12 bytes per token
-// (1024 requests, 24 prompts, 131072 tokens: 8.6 us; 15.2 us when the tokens' threads
+// (1024 requests, 24 prompts, 131072 tokens: 8.1 us; 15.2 us when the tokens' threads
 // looked for the blocks of finished requests, too).
-constexpr int kPlanThreads = 512;
+constexpr int kPlanThreads = 256;  // 16 / 1024 requests: 4.4 / 8.1 us; with 512 (and half the CTAs) 5.0 / 8.6, with 1024 6.9 / 12.0
 
 __device__ __forceinline__ int pages_of(int len, int shift) { return int((int64_t(len) + (1 << shift) - 1) >> shift); }
 
@@ -104,14 +104,18 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(KvPlanArgs a) {
   __syncthreads();
   PlanSums run{0, 0, 0};
   int taken = 0;
+  int next_c = tid < a.R ? a.ctx[tid] : 0, next_n = tid < a.R ? a.add[tid] : 0;
   for (int r0 = 0; r0 < a.R; r0 += kPlanThreads) {
     const int r = r0 + tid;
     PlanSums v{0, 0, 0};
-    int c = 0, n = 0;
+    int c = next_c, n = next_n;
     bool fits_table = true;
+    if (r + kPlanThreads < a.R) {  // the next ones' are on their way during the scan
+      next_c = a.ctx[r + kPlanThreads];
+      next_n = a.add[r + kPlanThreads];
+    }
     if (r < a.R) {
-      c = max(a.ctx[r], 0);
-      n = a.add[r];
+      c = max(c, 0);
       const int have = pages_of(c, a.page_shift);
       if (n < 0) {
         v.back = min(have, a.width);
@@ -233,12 +237,12 @@ cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t st) {
                                 (3 * kKvPlanMaxRequests + 1) * int(sizeof(int32_t)));
   });
   if (e != cudaSuccess) return e;
-  // a cluster of 1, 2, 4 or 8 CTAs, one CTA per 512 tokens or 16 requests; many
+  // a cluster of 1, 2, 4 or 8 CTAs, one CTA per 256 tokens or 16 requests; many
   // clusters for long steps whose outputs are not their own inputs
   int64_t ctas = (a.tokens + kPlanThreads - 1) / kPlanThreads;
   const int64_t by_requests = (int64_t(a.R) + 15) / 16;
   ctas = ctas > by_requests ? ctas : by_requests;
-  const int most = a.aliased ? 8 : 128;
+  const int most = a.aliased ? 8 : 256;
   int grid = 1;
   while (grid < most && grid < ctas) grid *= 2;
   const size_t bytes = size_t(3 * int64_t(a.R) + 1) * sizeof(int32_t);
