@@ -728,7 +728,8 @@ def _place(index: int, stream):
 
 @dataclass
 class KvCache:
-    """One layer's keys and values in 4 bits, in pages (layout: mxfa_kv_cache in mxfa.h)."""
+    """One layer's keys and values in 4 bits, in pages (layout: mxfa_kv_cache in mxfa.h).  Its
+    tensors are those it was made with: another buffer takes another KvCache."""
     k: torch.Tensor                    # uint8 [num_blocks, H, page, 64]
     v: torch.Tensor
     k_sf: torch.Tensor                 # uint8 [num_blocks, H, page, 4 (MXFP4) or 8 (NVFP4)]
@@ -775,6 +776,9 @@ class KvCache:
         self.H, self.page = h, page
         self.__dict__["pages"] = KvPages(k.data_ptr(), self.v.data_ptr(), self.k_sf.data_ptr(),
                                          self.v_sf.data_ptr(), ks, vs, n, page, h, 128, fmt)
+
+    def __reduce__(self):  # a copy is made of its own tensors, not of their addresses
+        return KvCache, (self.k, self.v, self.k_sf, self.v_sf, self.fmt, self.k_scale, self.v_scale)
 
     @functools.cached_property
     def pages(self) -> KvPages:

@@ -640,3 +640,22 @@ def test_refusals_name_what_is_wrong(mx):
         mx.kv_plan(**{**plan, "new_lens": plan["ctx_lens"], "free_ring": plan["ctx_lens"]})     # written and read
     torch.cuda.synchronize()
     assert torch.equal(c.k, before) and mx.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_copies_of_a_cache(mx, fmt):
+    """A deep copy has its own rows, a shallow one shares them."""
+    import copy
+    import torch
+    rng = np.random.default_rng(31)
+    c = new_cache(mx, 3, 2, 16, fmt)
+    x, slots = bf16(rng, 7, 2, 128).cuda(), torch.arange(7, device="cuda")
+    mx.kv_append(c, x, x, slots)
+    k0, v0 = mx.kv_load(c, slots)
+    deep, flat = copy.deepcopy(c), copy.copy(c)
+    y = bf16(rng, 7, 2, 128).cuda()
+    mx.kv_append(deep, y, y, slots)
+    assert torch.equal(mx.kv_load(c, slots)[0], k0) and not torch.equal(mx.kv_load(deep, slots)[0], k0)
+    mx.kv_append(flat, y, y, slots)
+    for a, b in zip(mx.kv_load(c, slots), mx.kv_load(deep, slots)):
+        assert torch.equal(a, b)

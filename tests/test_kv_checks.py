@@ -164,6 +164,15 @@ def test_python_refusals(mx):
         mx.kv_plan(i32(3), i32(3), i32(3, 4), i32(8), torch.zeros(3, dtype=torch.int64), 16, 4)   # not on a GPU
 
 
+def test_copy_has_its_own_addresses(mx):
+    import copy
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    c = mx.KvCache(u8(3, 2, 16, 64), u8(3, 2, 16, 64), u8(3, 2, 16, 4), u8(3, 2, 16, 4), 0)
+    d = copy.deepcopy(c)
+    assert d.pages.k == d.k.data_ptr() != c.k.data_ptr() == c.pages.k and d.pages.v_sf == d.v_sf.data_ptr()
+    assert copy.copy(c).pages.k == c.k.data_ptr()
+
+
 def test_sizes(mx):
     L = mx.lib()
     assert L.mxfa_kv_codes_bytes(10, 16, 3) == 10 * 16 * 3 * 64
