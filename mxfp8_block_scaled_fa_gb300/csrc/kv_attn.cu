@@ -904,8 +904,9 @@ size_t workspace(int sms) {
   return header_bytes(ctas) + size_t(ctas) * 2 * sizeof(Partial<NT>);
 }
 
+// `line_ws`: the prompts' workspace, whose line is made beside kv_attn_kernel; NULL: no prompts.
 template <int FMT, int NT>
-cudaError_t launch(const KvAttnArgs& a, cudaStream_t st) {
+cudaError_t launch(const KvAttnArgs& a, uint8_t* line_ws, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   constexpr int bytes = smem_bytes(FMT, NT);
   cudaError_t e = once_per_device(done, [] {
@@ -923,6 +924,7 @@ cudaError_t launch(const KvAttnArgs& a, cudaStream_t st) {
   kv_attn_kernel<FMT, NT><<<ctas, kThreads, bytes, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  if (line_ws && (e = launch_kv_prefill_line(a, line_ws, true, st)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas), 2 * NT);
   cfg.blockDim = dim3(256);
@@ -936,12 +938,12 @@ cudaError_t launch(const KvAttnArgs& a, cudaStream_t st) {
 }
 
 template <int FMT>
-cudaError_t launch_fmt(const KvAttnArgs& a, int nt, cudaStream_t st) {
+cudaError_t launch_fmt(const KvAttnArgs& a, int nt, uint8_t* line_ws, cudaStream_t st) {
   switch (nt) {
-    case 1: return launch<FMT, 1>(a, st);
-    case 2: return launch<FMT, 2>(a, st);
-    case 3: return launch<FMT, 3>(a, st);
-    default: return launch<FMT, 4>(a, st);
+    case 1: return launch<FMT, 1>(a, line_ws, st);
+    case 2: return launch<FMT, 2>(a, line_ws, st);
+    case 3: return launch<FMT, 3>(a, line_ws, st);
+    default: return launch<FMT, 4>(a, line_ws, st);
   }
 }
 
@@ -998,11 +1000,13 @@ cudaError_t launch_kv_attn(const KvAttnArgs& args, cudaStream_t st) {
   const kva::Plan p = kva::plan_of(a.max_q, int64_t(a.width) << a.c.page_shift, a.G);
   a.split_rows = p.split_rows;
   a.whole = p.whole;
-  if (!p.prefill || a.G <= kva::kMixedRows) {
-    const cudaError_t e = a.c.fmt == 0 ? kva::launch_fmt<0>(a, p.nt, st) : kva::launch_fmt<1>(a, p.nt, st);
-    if (e != cudaSuccess || !p.prefill) return e;
-  }
-  return launch_kv_prefill(a, a.ws + ((kva::workspace_of(p.nt) + 255) & ~size_t(255)), st);
+  uint8_t* const line_ws = p.prefill ? a.ws + ((kva::workspace_of(p.nt) + 255) & ~size_t(255)) : nullptr;
+  cudaError_t e;
+  if (!p.prefill || a.G <= kva::kMixedRows)
+    e = a.c.fmt == 0 ? kva::launch_fmt<0>(a, p.nt, line_ws, st) : kva::launch_fmt<1>(a, p.nt, line_ws, st);
+  else
+    e = launch_kv_prefill_line(a, line_ws, false, st);
+  return e != cudaSuccess || !p.prefill ? e : launch_kv_prefill(a, line_ws, st);
 }
 
 unsigned read_status_kv_attn(cudaStream_t st) {

@@ -38,9 +38,10 @@
 // halves with one issuer 457 us (a product is issued in 40 to 55 cycles, a commit in
 // 100); conversion with coalesced loads (four lanes a row) 435 against 379 us, as the
 // swizzled stores then cost more; O written through shared memory by rows, 315 against
-// 312 us; the small kernels launched early 317 against 314 us.  For items of up to 128
-// rows both softmax groups on the same rows, each with half of the keys, 137 against 117
-// us for 24 x 64 rows over 6000 keys.
+// 312 us.  For items of up to 128 rows both softmax groups on the same rows, each with
+// half of the keys, 137 against 117 us for 24 x 64 rows over 6000 keys.  Launched ahead
+// of the kernels they wait for, the five kernels of a call take 313 instead of 319 us
+// from a stream (310 from a graph, either way).
 #include "kv_fp4.cuh"
 #include "mx_ptx.cuh"
 #include "mxfa_internal.h"
@@ -159,6 +160,7 @@ __device__ __forceinline__ int tiles_of(const KvAttnArgs& a, const Request& x, i
 // line[r] = units (tiles, and kItemTiles per item) of the requests before r.
 __global__ void __launch_bounds__(512) kv_prefill_line_kernel(KvAttnArgs a, int64_t* line) {
   __shared__ int64_t s_sum[16];
+  asm volatile("griddepcontrol.launch_dependents;");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t base = 0;
   for (int r0 = 0; r0 < a.R; r0 += 512) {
@@ -187,6 +189,8 @@ __global__ void __launch_bounds__(512) kv_prefill_line_kernel(KvAttnArgs a, int6
     __syncthreads();
   }
   if (threadIdx.x == 0) line[a.R] = base;
+  // it runs beside kv_attn_kernel, and its end stands for that one's too
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int FMT>
@@ -203,10 +207,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + OFF_MISC + 8);
   unsigned* status = &g_status_kv_prefill;
 
-  if (tid == 0) headers[blockIdx.x].parts = 0;
-  const int64_t total = __ldg(line + a.R);
-  if (total == 0) return;  // no request with that many rows
-
+  asm volatile("griddepcontrol.launch_dependents;");
   if (tid == 0) {
     *abort_flag = 0;
     for (int s = 0; s < 2; s++) {
@@ -234,6 +235,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the line, and what runs before it
+  if (tid == 0) headers[blockIdx.x].parts = 0;
+  const int64_t total = __ldcg(line + a.R);
+  if (total == 0) {  // no request with that many rows
+    if (warp == 0) tmem_dealloc(tmem, 512);
+    return;
+  }
   const Item* items = reinterpret_cast<const Item*>(smem + OFF_ITEM);
   // whole warp: waits for item i of the run and reads it; a part with rows == 0 ends the run
   auto take = [&](int i, Item& it, bool& ok) {
@@ -379,7 +387,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       int lo = 0, hi = a.R;  // the request with line[lo] <= pos < line[hi]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(line + mid) <= pos) lo = mid;
+        if (__ldcg(line + mid) <= pos) lo = mid;
         else hi = mid;
       }
       int r = lo, i = 0;
@@ -395,7 +403,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       };
       bool ok = true;
       while (ok && pos < end && r < a.R) {
-        const int64_t lr = __ldg(line + r), next_r = __ldg(line + r + 1);
+        const int64_t lr = __ldcg(line + r), next_r = __ldcg(line + r + 1);
         if (pos >= next_r) {
           r++;
           continue;
@@ -820,6 +828,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
 // it: one warp per row, four channels a lane, parts in the order of the keys.
 template <int FMT>
 __global__ void __launch_bounds__(256) kv_prefill_join_kernel(KvAttnArgs a, const Header* headers, const Partial* partials) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the end of kv_prefill_kernel
   const Header hd = headers[blockIdx.x];
   if (hd.parts == 0) return;
   const int idx = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -854,6 +863,23 @@ __global__ void __launch_bounds__(256) kv_prefill_join_kernel(KvAttnArgs a, cons
         L == 0.0f ? -INFINITY : (M - kOffset + log2f(L)) * 0.6931471805599453f;
 }
 
+// Launches a kernel that may start before the one before it has ended, and waits for it
+// itself.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
 template <int FMT>
 cudaError_t launch(const KvAttnArgs& a, uint8_t* ws, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
@@ -866,12 +892,11 @@ cudaError_t launch(const KvAttnArgs& a, uint8_t* ws, cudaStream_t st) {
   int64_t* line = reinterpret_cast<int64_t*>(ws);
   Header* headers = reinterpret_cast<Header*>(ws + line_bytes(a.R));
   Partial* partials = reinterpret_cast<Partial*>(ws + line_bytes(a.R) + header_bytes(ctas));
-  kv_prefill_line_kernel<<<1, 512, 0, st>>>(a, line);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  kv_prefill_kernel<FMT><<<unsigned(ctas), NTHREADS, SMEM_BYTES, st>>>(a, line, headers, partials);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  kv_prefill_join_kernel<FMT><<<dim3(unsigned(ctas), ROWS / 8), 256, 0, st>>>(a, headers, partials);
-  return cudaGetLastError();
+  e = launch_early(kv_prefill_kernel<FMT>, dim3(unsigned(ctas)), NTHREADS, SMEM_BYTES, st, a, static_cast<const int64_t*>(line), headers,
+                   partials);
+  if (e != cudaSuccess) return e;
+  return launch_early(kv_prefill_join_kernel<FMT>, dim3(unsigned(ctas), ROWS / 8), 256, 0, st, a, static_cast<const Header*>(headers),
+                      static_cast<const Partial*>(partials));
 }
 
 }  // namespace kvp
@@ -879,6 +904,15 @@ cudaError_t launch(const KvAttnArgs& a, uint8_t* ws, cudaStream_t st) {
 size_t kv_prefill_workspace(int R) {
   const int ctas = sm_count_current_device();
   return kvp::line_bytes(R) + kvp::header_bytes(ctas) + size_t(ctas) * 2 * sizeof(kvp::Partial);
+}
+
+// The places of the requests on the line; `after_attn`: beside kv_attn_kernel, which is
+// the launch before it.
+cudaError_t launch_kv_prefill_line(const KvAttnArgs& a, uint8_t* ws, bool after_attn, cudaStream_t st) {
+  int64_t* line = reinterpret_cast<int64_t*>(ws);
+  if (after_attn) return kvp::launch_early(kvp::kv_prefill_line_kernel, dim3(1), 512, 0, st, a, line);
+  kvp::kv_prefill_line_kernel<<<1, 512, 0, st>>>(a, line);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_kv_prefill(const KvAttnArgs& a, uint8_t* ws, cudaStream_t st) {

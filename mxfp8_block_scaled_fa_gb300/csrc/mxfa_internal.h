@@ -253,6 +253,7 @@ size_t kv_attn_workspace(int R, int max_q, int64_t max_k, int G);
 bool kv_attn_reaches(int max_q, int64_t max_k, int G);
 cudaError_t launch_kv_attn(const KvAttnArgs& a, cudaStream_t s);
 size_t kv_prefill_workspace(int R);
+cudaError_t launch_kv_prefill_line(const KvAttnArgs& a, uint8_t* ws, bool after_attn, cudaStream_t st);
 cudaError_t launch_kv_prefill(const KvAttnArgs& a, uint8_t* ws, cudaStream_t s);
 
 // Read (and clear) the device status words of every kernel module.
