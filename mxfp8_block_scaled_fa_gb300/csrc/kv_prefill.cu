@@ -236,7 +236,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // for the line, and what runs before it
-  if (tid == 0) headers[blockIdx.x].parts = 0;
+  // by the scheduler's lane, which may replace it: no barrier follows that would order two threads
+  if (warp == 1 && lane == 0) headers[blockIdx.x].parts = 0;
   const int64_t total = __ldcg(line + a.R);
   if (total == 0) {  // no request with that many rows
     if (warp == 0) tmem_dealloc(tmem, 512);

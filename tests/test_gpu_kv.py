@@ -659,3 +659,38 @@ def test_copies_of_a_cache(mx, fmt):
     mx.kv_append(flat, y, y, slots)
     for a, b in zip(mx.kv_load(c, slots), mx.kv_load(deep, slots)):
         assert torch.equal(a, b)
+
+
+def test_mixed_calls_at_once_on_filled_workspaces(mx):
+    """Prompts among decoding requests, items cut between CTAs: two captured calls on two streams and two eager ones,
+    each on a workspace that is filled anew before every run, leave no row unjoined."""
+    import torch
+    rng = np.random.default_rng(41)
+    runs = []
+    for fmt, ql, kv in ((0, [100, 1, 1, 3], [9000, 700, 4000, 64]), (1, [1, 300, 1], [3000, 5000, 17])):
+        args = build(mx, rng, fmt, 64, 2, 4, ql, kv)
+        c, q, cu, lens, table, _ = args
+        need = mx.mxfa_kv_attn_workspace_size(len(ql), max(ql), table.shape[1] * 64, 8, 2)
+        assert need > 0
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        o = torch.empty(q.shape, dtype=torch.bfloat16, device="cuda"), torch.empty(8, q.shape[0], device="cuda")
+
+        def call(c=c, q=q, cu=cu, lens=lens, table=table, most=max(ql), o=o, ws=ws):
+            ws.fill_(0xFF), o[0].fill_(77.0), o[1].fill_(77.0)
+            mx.kv_attention(q, c, cu, lens, table, most, 128 ** -0.5, out=o, ws=ws)
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        runs.append((args, call, g, o, torch.cuda.Stream()))
+    for captured in (False, True):
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for _, call, g, _, s in runs:
+                with torch.cuda.stream(s):
+                    g.replay() if captured else call()
+        torch.cuda.synchronize()
+        for (c, q, cu, _, _, slots), _, _, o, _ in runs:
+            compare(c, q, cu, slots, True, 128 ** -0.5, *o)
+    assert mx.device_status() == 0

@@ -212,3 +212,19 @@ def test_attention_context_limits(mx):
     # no workspace is given: 1 or 6 (too small) where the sizes are accepted
     assert call(1 << 24, 200) == 2 and call((1 << 18) + 1, 25) == 2             # more than 2^25 keys for more than 48 rows
     assert call(1 << 18, 25) != 2 and call(1 << 23, 24) != 2 and call((1 << 23) + 1, 24) == 2
+
+
+def test_join_headers_have_one_writer():
+    """Nothing orders two warps' stores of a join header after the launch's only barrier: each store of one
+    kernel stands under the same test of the thread."""
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "mxfp8_block_scaled_fa_gb300", "csrc")
+    for name in ("kv_attn.cu", "kv_prefill.cu"):
+        lines = open(os.path.join(csrc, name)).read().splitlines()
+        writers = []
+        for i, line in enumerate(lines):
+            if re.search(r"headers\[blockIdx\.x\](\.parts)?\s*=[^=]", line):
+                test = next(x for x in reversed(lines[: i + 1]) if re.search(r"\bif \(.*\b(tid|lane) == \d", x))
+                writers.append(" ".join(sorted(re.findall(r"\b(?:tid|warp|lane) == \d+", test))))
+        assert len(writers) == 2 and len(set(writers)) == 1, (name, writers)
