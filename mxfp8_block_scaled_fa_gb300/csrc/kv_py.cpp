@@ -107,7 +107,8 @@ PyObject* cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto size = k->sizes();
     const int64_t sf = fmt == MXFA_KV_MXFP4 ? 4 : 8;
     if (size[3] != 64 || v->sizes() != size || ksf->sizes() != vsf->sizes() || ksf->size(0) != size[0] ||
-        ksf->size(1) != size[1] || ksf->size(2) != size[2] || ksf->size(3) != sf || size[1] > 65536 || size[2] > 128)
+        ksf->size(1) != size[1] || ksf->size(2) != size[2] || ksf->size(3) != sf || size[0] < 1 || size[1] < 1 ||
+        size[1] > 65536 || size[2] < 1 || size[2] > 128)
       Py_RETURN_NONE;
     Cache x;
     std::memset(&x, 0, sizeof(x));

@@ -753,6 +753,8 @@ class KvCache:
         if len(shape) != 4 or shape[3] != 64 or self.v.shape != shape:
             raise ValueError("k and v must be [num_blocks, H, page, 64]")
         n, h, page, _ = shape
+        if 0 in shape:
+            raise ValueError("a cache has at least one block, one head and one row a page")
         sf = (n, h, page, 4 if fmt == KV_MXFP4 else 8)
         if self.k_sf.shape != sf or self.v_sf.shape != sf:
             raise ValueError(f"k_sf and v_sf must be {list(sf)}")

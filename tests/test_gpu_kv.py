@@ -694,3 +694,10 @@ def test_mixed_calls_at_once_on_filled_workspaces(mx):
         for (c, q, cu, _, _, slots), _, _, o, _ in runs:
             compare(c, q, cu, slots, True, 128 ** -0.5, *o)
     assert mx.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("n,h,page", [(3, 0, 16), (0, 2, 16), (3, 2, 0)])
+def test_empty_cache_refused_on_a_gpu(mx, fmt, n, h, page):
+    with pytest.raises(ValueError):
+        mx.KvCache.empty(n, h, page, fmt)

@@ -228,3 +228,14 @@ def test_join_headers_have_one_writer():
                 test = next(x for x in reversed(lines[: i + 1]) if re.search(r"\bif \(.*\b(tid|lane) == \d", x))
                 writers.append(" ".join(sorted(re.findall(r"\b(?:tid|warp|lane) == \d+", test))))
         assert len(writers) == 2 and len(set(writers)) == 1, (name, writers)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("n,h,page", [(3, 0, 16), (0, 2, 16), (3, 2, 0), (0, 0, 0)])
+def test_empty_cache_refused(mx, fmt, n, h, page):
+    u8, one = (lambda *s: torch.zeros(s, dtype=torch.uint8)), torch.ones(1)
+    sf = 4 if fmt == 0 else 8
+    with pytest.raises(ValueError):
+        mx.KvCache(u8(n, h, page, 64), u8(n, h, page, 64), u8(n, h, page, sf), u8(n, h, page, sf), fmt, one, one)
+    with pytest.raises(ValueError):
+        mx.KvCache.empty(n, h, page, fmt, device="cpu")
