@@ -506,8 +506,8 @@ mxfa_status mxfa_kv_append(const mxfa_kv_cache* cache, const void* k, const void
 
 /* mxfa_kv_load -- the cached values of slots as bf16 k, v [tokens][H][128] (MXFP4
  * exact, NVFP4 rounded to nearest), in any order and repeated at will; zeros
- * for a negative slot (and for one past the cache, which is recorded).  k, v and
- * slots do not overlap (MXFA_ERR_INVALID_ARG). */
+ * for a negative slot (and for one past the cache, which is recorded).  k and v overlap
+ * neither each other nor slots nor the cache (MXFA_ERR_INVALID_ARG). */
 mxfa_status mxfa_kv_load(const mxfa_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k, void* v,
                          mxfa_stream_t stream);
 
@@ -532,7 +532,8 @@ size_t mxfa_kv_attn_workspace_size(int R, int max_q, int64_t max_k, int Hq, int 
  * Keys past kv_lens or in no row's sight are not used, whatever they hold.  A block index
  * outside the cache (its keys count as not there) and offsets or lengths outside
  * their tables (the request is left out) are recorded as failed index checks.
- * o, lse and ws overlap neither each other nor an input (MXFA_ERR_INVALID_ARG).
+ * o, lse and ws overlap neither each other nor an input, the cache's buffers among them
+ * (MXFA_ERR_INVALID_ARG).
  * max_blocks * page <= 2^30, and <= 2^25 where max_q * G > 48 (else
  * MXFA_ERR_UNSUPPORTED). */
 mxfa_status mxfa_kv_attn(const mxfa_kv_cache* cache, const void* q, int64_t q_stride, int64_t total_q,

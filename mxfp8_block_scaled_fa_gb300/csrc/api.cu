@@ -779,6 +779,25 @@ struct Range {
   size_t bytes;
 };
 bool meet(const Range& a, const Range& b) { return a.bytes && b.bytes && overlap(a.at, a.bytes, b.at, b.bytes) != 0; }
+template <typename A, typename B>
+bool any_meet(const A& a, const B& b) {
+  for (const Range& x : a)
+    for (const Range& y : b)
+      if (meet(x, y)) return true;
+  return false;
+}
+
+// The buffers of a (checked) cache: codes and block scales of K and V, then NVFP4's scales.
+struct CacheRanges {
+  Range r[6];
+  const Range* begin() const { return r; }
+  const Range* end() const { return r + 6; }
+};
+CacheRanges ranges_of(const KvPages& c) {
+  const size_t rows = size_t(c.blocks) * size_t(c.H) * size_t(c.page), sf = c.fmt == MXFA_KV_NVFP4 ? 8 : 4;
+  const size_t st = c.fmt == MXFA_KV_NVFP4 ? 4 : 0;
+  return {{{c.k, rows * 64}, {c.v, rows * 64}, {c.k_sf, rows * sf}, {c.v_sf, rows * sf}, {c.k_scale, st}, {c.v_scale, st}}};
+}
 
 }  // namespace
 
@@ -882,8 +901,9 @@ mxfa_status mxfa_kv_load(const mxfa_kv_cache* cache, const int64_t* slots, int64
   if (!aligned16(k) || !aligned16(v) || !aligned8(slots)) return MXFA_ERR_MISALIGNED;
   if (tokens == 0) return MXFA_OK;
   const size_t bytes = size_t(tokens) * size_t(a.c.H) * 256;
-  const Range kr{k, bytes}, vr{v, bytes}, sr{slots, size_t(tokens) * 8};
-  if (meet(kr, vr) || meet(kr, sr) || meet(vr, sr)) return MXFA_ERR_INVALID_ARG;
+  const Range written[] = {{k, bytes}, {v, bytes}}, sr{slots, size_t(tokens) * 8};
+  if (meet(written[0], written[1]) || meet(written[0], sr) || meet(written[1], sr)) return MXFA_ERR_INVALID_ARG;
+  if (any_meet(written, ranges_of(a.c))) return MXFA_ERR_INVALID_ARG;
   a.k = static_cast<uint16_t*>(k);
   a.v = static_cast<uint16_t*>(v);
   a.tokens = tokens;
@@ -938,12 +958,8 @@ mxfa_status mxfa_kv_attn(const mxfa_kv_cache* cache, const void* q, int64_t q_st
   const Range written[] = {{o, rows * row}, {lse, rows * size_t(Hq) * 4}, {ws, need}};
   const Range read[] = {{q, (rows - 1) * size_t(total_q > 1 ? q_stride : 0) * 2 + row}, {cu_q, size_t(R) * 4 + 4}, {kv_lens, size_t(R) * 4},
                         {block_table, size_t(R) * size_t(max_blocks) * 4}};
-  for (const Range& w : written) {
-    for (const Range& r : read)
-      if (meet(w, r)) return MXFA_ERR_INVALID_ARG;
-    for (const Range& x : written)
-      if (&x != &w && meet(w, x)) return MXFA_ERR_INVALID_ARG;
-  }
+  if (any_meet(written, read) || any_meet(written, ranges_of(a.c))) return MXFA_ERR_INVALID_ARG;
+  if (meet(written[0], written[1]) || meet(written[0], written[2]) || meet(written[1], written[2])) return MXFA_ERR_INVALID_ARG;
   return from_cuda(launch_kv_attn(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

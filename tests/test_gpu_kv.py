@@ -701,3 +701,28 @@ def test_mixed_calls_at_once_on_filled_workspaces(mx):
 def test_empty_cache_refused_on_a_gpu(mx, fmt, n, h, page):
     with pytest.raises(ValueError):
         mx.KvCache.empty(n, h, page, fmt)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_results_over_the_cache_refused_on_a_gpu(mx, fmt):
+    """Results that lie over the cache they are read from: refused, and nothing of the cache changes."""
+    import torch
+    rng = np.random.default_rng(43)
+    c, q, cu, lens, table, slots = build(mx, rng, fmt, 16, 2, 2, [1, 2], [70, 50], poison=False)
+    before = [t.clone() for t in (c.k, c.v, c.k_sf, c.v_sf)]
+    n = q.shape[0]
+    o, lse = torch.empty(q.shape, dtype=torch.bfloat16, device="cuda"), torch.empty((4, n), device="cuda")
+    over = lambda t, like: t.view(-1)[: like.numel() * like.element_size()].view(like.dtype).view(like.shape)
+    sl = torch.arange(3, device="cuda")
+    k = torch.empty((3, 2, 128), dtype=torch.bfloat16, device="cuda")
+    for t in (c.k, c.v):
+        for out in ((over(t, o), lse), (o, over(t, lse))):
+            with pytest.raises(mx.MxfaError) as e:
+                mx.kv_attention(q, c, cu, lens, table, 2, 0.1, out=out)
+            assert e.value.status == 1
+        for out in ((over(t, k), k), (k, over(t, k))):
+            with pytest.raises(mx.MxfaError) as e:
+                mx.kv_load(c, sl, out=out)
+            assert e.value.status == 1
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(before, (c.k, c.v, c.k_sf, c.v_sf))) and mx.device_status() == 0

@@ -239,3 +239,27 @@ def test_empty_cache_refused(mx, fmt, n, h, page):
         mx.KvCache(u8(n, h, page, 64), u8(n, h, page, 64), u8(n, h, page, sf), u8(n, h, page, sf), fmt, one, one)
     with pytest.raises(ValueError):
         mx.KvCache.empty(n, h, page, fmt, device="cpu")
+
+
+# a cache of 4 blocks, 2 heads, pages of 16: 8192 bytes each of codes, 1024 of NVFP4's scales
+_FAR = dict(k=0x100000, v=0x110000, k_sf=0x120000, v_sf=0x130000, k_scale=0x140000, v_scale=0x150000, fmt=1)
+_FAR_BYTES = dict(k=8192, v=8192, k_sf=1024, v_sf=1024, k_scale=4, v_scale=4)
+
+
+@pytest.mark.parametrize("part", list(_FAR_BYTES))
+def test_results_over_the_cache_refused(mx, part):
+    L, ref = mx.lib(), ctypes.byref(_cache(mx, **_FAR))
+    at, size = _FAR[part], _FAR_BYTES[part]
+    last = at + (size - 1) // 16 * 16
+    # a load of 3 tokens writes 1536 bytes each of k and v: over the beginning and over the end
+    for x in (at, at - 1536 + 16, last):
+        assert L.mxfa_kv_load(ref, 0x1000, 3, x, 0x20000, None) == 1
+        assert L.mxfa_kv_load(ref, 0x1000, 3, 0x20000, x, None) == 1
+    # attention of 3 tokens and 4 heads: o of 3072 bytes, lse of 48
+    base = dict(q=0x10000, qs=1024, T=3, cu=0x20000, kv=0x30000, R=1, bt=0x40000, nb=128, mq=3, Hq=4, s=0.1, c=1, o=0x50000,
+                lse=0x60000, ws=0x10000000, wb=1 << 30)
+    bad = [dict(o=at), dict(o=at - 3072 + 16), dict(o=last), dict(lse=at), dict(lse=at - 44), dict(lse=last)]
+    if L.mxfa_kv_attn_workspace_size(1, 3, 128 * 16, 4, 2):
+        bad += [dict(ws=at), dict(ws=last), dict(ws=at - 16)]
+    for kw in bad:
+        assert L.mxfa_kv_attn(ref, *dict(base, **kw).values(), None) == 1, kw
