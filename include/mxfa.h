@@ -500,7 +500,9 @@ mxfa_status mxfa_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int R
  *            apart (multiples of 8, at least H * 128), 16-byte aligned
  *  slots     DEVICE int64 [tokens]; negative: the token is skipped.  Slots of one call are
  *            distinct (two tokens with one slot leave it undefined); a slot past the
- *            cache is skipped and recorded as a failed index check */
+ *            cache is skipped and recorded as a failed index check
+ * k, v and slots do not overlap the cache's codes and block scales, nor do these
+ * overlap one another, k_scale or v_scale (MXFA_ERR_INVALID_ARG). */
 mxfa_status mxfa_kv_append(const mxfa_kv_cache* cache, const void* k, const void* v, int64_t k_stride,
                            int64_t v_stride, int64_t tokens, const int64_t* slots, mxfa_stream_t stream);
 

@@ -881,6 +881,16 @@ mxfa_status mxfa_kv_append(const mxfa_kv_cache* cache, const void* k, const void
   if (!aligned16(k) || !aligned16(v) || !aligned8(slots) || (tokens > 1 && (k_stride % 8 || v_stride % 8)))
     return MXFA_ERR_MISALIGNED;
   if (tokens == 0) return MXFA_OK;
+  // what is written (codes and block scales) meets neither what is read nor itself
+  const CacheRanges own = ranges_of(a.c);
+  const size_t row = size_t(a.c.H) * 256, steps = size_t(tokens) - 1;
+  const Range read[] = {{k, steps * size_t(k_stride) * 2 + row}, {v, steps * size_t(v_stride) * 2 + row}, {slots, size_t(tokens) * 8}};
+  for (int i = 0; i < 4; i++) {
+    for (const Range& x : read)
+      if (meet(own.r[i], x)) return MXFA_ERR_INVALID_ARG;
+    for (int j = i + 1; j < 6; j++)
+      if (meet(own.r[i], own.r[j])) return MXFA_ERR_INVALID_ARG;
+  }
   a.k = const_cast<uint16_t*>(static_cast<const uint16_t*>(k));
   a.v = const_cast<uint16_t*>(static_cast<const uint16_t*>(v));
   a.k_stride = k_stride;

@@ -263,3 +263,22 @@ def test_results_over_the_cache_refused(mx, part):
         bad += [dict(ws=at), dict(ws=last), dict(ws=at - 16)]
     for kw in bad:
         assert L.mxfa_kv_attn(ref, *dict(base, **kw).values(), None) == 1, kw
+
+
+@pytest.mark.parametrize("part", list(_FAR_BYTES))
+def test_store_over_its_inputs_refused(mx, part):
+    L, ref = mx.lib(), ctypes.byref(_cache(mx, **_FAR))
+    at, size = _FAR[part], _FAR_BYTES[part]
+    last = at + (size - 1) // 16 * 16
+    good = dict(k=0x10000, v=0x20000, ks=256, vs=512, T=3, slots=0x30000)
+    # 3 rows of 512 bytes: k's one after another, v's 1024 bytes apart; 24 bytes of slots
+    bad = [dict(k=at), dict(k=last), dict(k=at - 1536 + 16), dict(v=at), dict(v=last), dict(v=at - 2560 + 16), dict(slots=at),
+           dict(slots=last), dict(slots=at - 16)]
+    for kw in bad if size > 4 else []:
+        assert L.mxfa_kv_append(ref, *dict(good, **kw).values(), None) == 1, kw
+    # its own buffers over one another: the rows are written, and NVFP4's scales read, by every CTA
+    for other in ("k", "v", "k_sf", "v_sf"):
+        if other == part:
+            continue
+        c = _cache(mx, **{**_FAR, part: _FAR[other] + _FAR_BYTES[other] // 2})
+        assert L.mxfa_kv_append(ctypes.byref(c), *good.values(), None) == 1, other
