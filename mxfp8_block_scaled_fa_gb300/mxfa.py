@@ -36,7 +36,7 @@ import functools
 import importlib.util
 import math
 import os
-from dataclasses import dataclass
+from dataclasses import FrozenInstanceError, dataclass
 from typing import Optional, Sequence
 
 import numpy as np
@@ -726,10 +726,14 @@ def _place(index: int, stream):
     return torch.cuda.stream(stream)
 
 
-@dataclass
+_KV_FIXED = frozenset(("k", "v", "k_sf", "v_sf", "fmt", "k_scale", "v_scale", "H", "page", "index", "raw", "pages"))
+
+
+@dataclass(init=False)
 class KvCache:
-    """One layer's keys and values in 4 bits, in pages (layout: mxfa_kv_cache in mxfa.h).  Its
-    tensors are those it was made with: another buffer takes another KvCache."""
+    """One layer's keys and values in 4 bits, in pages (layout: mxfa_kv_cache in mxfa.h).  Calls
+    go by the addresses of the tensors that it was made with: its fields cannot be assigned, and
+    a tensor of it must keep its storage.  Other buffers take another KvCache."""
     k: torch.Tensor                    # uint8 [num_blocks, H, page, 64]
     v: torch.Tensor
     k_sf: torch.Tensor                 # uint8 [num_blocks, H, page, 4 (MXFP4) or 8 (NVFP4)]
@@ -738,46 +742,54 @@ class KvCache:
     k_scale: Optional[torch.Tensor] = None   # NVFP4: fp32, one element
     v_scale: Optional[torch.Tensor] = None
 
-    def __post_init__(self):
-        fmt, k = self.fmt, self.k
-        made = _fast().cache(k, self.v, self.k_sf, self.v_sf, fmt, self.k_scale, self.v_scale)
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_sf: torch.Tensor, v_sf: torch.Tensor, fmt: int,
+                 k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None):
+        d = self.__dict__
+        d["k"], d["v"], d["k_sf"], d["v_sf"], d["fmt"] = k, v, k_sf, v_sf, fmt
+        made = _fast().cache(k, v, k_sf, v_sf, fmt, k_scale, v_scale)
+        if fmt == KV_MXFP4:
+            k_scale = v_scale = None
+        d["k_scale"], d["v_scale"] = k_scale, v_scale
         if made is not None:
-            self.raw, self.H, self.page, self.index = made
-            if fmt == KV_MXFP4:
-                self.k_scale = self.v_scale = None
+            d["raw"], d["H"], d["page"], d["index"] = made
             return
-        self.raw = None
         if fmt != KV_MXFP4 and fmt != KV_NVFP4:
             raise ValueError(f"unknown cache format {fmt}")
         shape = k.shape
-        if len(shape) != 4 or shape[3] != 64 or self.v.shape != shape:
+        if len(shape) != 4 or shape[3] != 64 or v.shape != shape:
             raise ValueError("k and v must be [num_blocks, H, page, 64]")
         n, h, page, _ = shape
         if 0 in shape:
             raise ValueError("a cache has at least one block, one head and one row a page")
         sf = (n, h, page, 4 if fmt == KV_MXFP4 else 8)
-        if self.k_sf.shape != sf or self.v_sf.shape != sf:
+        if k_sf.shape != sf or v_sf.shape != sf:
             raise ValueError(f"k_sf and v_sf must be {list(sf)}")
-        index = self.index = k.get_device()
+        index = k.get_device()
         _flat("k", k, torch.uint8, index)
-        _flat("v", self.v, torch.uint8, index)
-        _flat("k_sf", self.k_sf, torch.uint8, index)
-        _flat("v_sf", self.v_sf, torch.uint8, index)
+        _flat("v", v, torch.uint8, index)
+        _flat("k_sf", k_sf, torch.uint8, index)
+        _flat("v_sf", v_sf, torch.uint8, index)
         ks = vs = None
         if fmt == KV_NVFP4:
-            ks, vs = self.k_scale, self.v_scale
-            if ks is None or vs is None:
+            if k_scale is None or v_scale is None:
                 raise ValueError("an NVFP4 cache needs k_scale and v_scale")
-            _flat("k_scale", ks, torch.float32, index)
-            _flat("v_scale", vs, torch.float32, index)
-            if ks.numel() != 1 or vs.numel() != 1:
+            _flat("k_scale", k_scale, torch.float32, index)
+            _flat("v_scale", v_scale, torch.float32, index)
+            if k_scale.numel() != 1 or v_scale.numel() != 1:
                 raise ValueError("k_scale and v_scale have one element")
-            ks, vs = ks.data_ptr(), vs.data_ptr()
-        else:
-            self.k_scale = self.v_scale = None
-        self.H, self.page = h, page
-        self.__dict__["pages"] = KvPages(k.data_ptr(), self.v.data_ptr(), self.k_sf.data_ptr(),
-                                         self.v_sf.data_ptr(), ks, vs, n, page, h, 128, fmt)
+            ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+        d["raw"], d["H"], d["page"], d["index"] = None, h, page, index
+        d["pages"] = KvPages(k.data_ptr(), v.data_ptr(), k_sf.data_ptr(), v_sf.data_ptr(), ks, vs, n, page, h, 128, fmt)
+
+    def __setattr__(self, name, value):
+        if name in _KV_FIXED:
+            raise FrozenInstanceError(f"a KvCache keeps its {name}; other buffers take another KvCache")
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        if name in _KV_FIXED:
+            raise FrozenInstanceError(f"a KvCache keeps its {name}")
+        object.__delattr__(self, name)
 
     def __reduce__(self):  # a copy is made of its own tensors, not of their addresses
         return KvCache, (self.k, self.v, self.k_sf, self.v_sf, self.fmt, self.k_scale, self.v_scale)

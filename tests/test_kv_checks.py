@@ -282,3 +282,26 @@ def test_store_over_its_inputs_refused(mx, part):
             continue
         c = _cache(mx, **{**_FAR, part: _FAR[other] + _FAR_BYTES[other] // 2})
         assert L.mxfa_kv_append(ctypes.byref(c), *good.values(), None) == 1, other
+
+
+def test_a_caches_tensors_stay(mx):
+    """Calls go by the addresses of the tensors a cache was made with, so those cannot be exchanged."""
+    import copy
+    import dataclasses
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    c = mx.KvCache(u8(3, 2, 16, 64), u8(3, 2, 16, 64), u8(3, 2, 16, 8), u8(3, 2, 16, 8), 1, torch.ones(1), torch.ones(1))
+    for name in ("k", "v", "k_sf", "v_sf", "fmt", "k_scale", "v_scale", "H", "page", "index", "raw", "pages"):
+        value = getattr(c, name)
+        with pytest.raises(AttributeError):
+            setattr(c, name, value)
+        with pytest.raises(AttributeError):
+            delattr(c, name)
+        assert getattr(c, name) is value
+    c.note = 1                                                       # anything else is the owner's
+    assert c.note == 1
+    d = dataclasses.replace(c, k=u8(3, 2, 16, 64))
+    assert d.pages.k == d.k.data_ptr() != c.pages.k and d.v is c.v
+    for e in (d, copy.copy(c)):
+        with pytest.raises(AttributeError):
+            e.k = u8(3, 2, 16, 64)
+    assert mx.KvCache(u8(3, 2, 16, 64), u8(3, 2, 16, 64), u8(3, 2, 16, 4), u8(3, 2, 16, 4), 0, torch.ones(1)).k_scale is None
