@@ -528,7 +528,9 @@ size_t mxfa_kv_attn_workspace_size(int R, int max_q, int64_t max_k, int Hq, int 
  *  block_table  DEVICE int32 [R][max_blocks]
  *  causal       1: query i of a request's n sees keys j <= kv - n + i; 0: all keys
  *  o            bf16 [total_q][Hq][128];  lse fp32 [Hq][total_q], natural log.  A query
- *               that sees no key gets O = 0 and lse = -inf
+ *               that sees no key gets O = 0 and lse = -inf; one with Inf or NaN
+ *               that sees a key gets NaN.  Scores, times softmax_scale, stay within fp32's
+ *               range; those past it count as infinite
  *  ws           mxfa_kv_attn_workspace_size() bytes, 16-byte aligned, not shared by calls
  *               that can run at the same time; its contents need not be kept
  * Keys past kv_lens or in no row's sight are not used, whatever they hold.  A block index

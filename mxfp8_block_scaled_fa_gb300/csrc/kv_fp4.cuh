@@ -42,10 +42,13 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
 }
 
 // The power of two that brings a query row whose largest |bf16| pattern is `mx`
-// to [2^14, 2^15) (at most 2^126; 1 for a row of zeros), and its inverse.
+// to [2^14, 2^15) (at most 2^126; 1 for a row of zeros), and its inverse.  For a row with
+// Inf or NaN, whose scores are all infinite or NaN and so its results NaN, the first is NaN:
+// scores of -inf alone would look like a row that sees no key.
 __device__ __forceinline__ float2 q_row_scale(uint32_t mx) {
   const int fe = mx == 0 ? 127 : min(253, 268 - int(mx >> 7));
-  return make_float2(__uint_as_float(uint32_t(fe) << 23), __uint_as_float(uint32_t(254 - fe) << 23));
+  const float f = __uint_as_float(mx >= 0x7F80u ? 0x7FC00000u : uint32_t(fe) << 23);
+  return make_float2(f, __uint_as_float(uint32_t(254 - fe) << 23));
 }
 
 }  // namespace mxfa

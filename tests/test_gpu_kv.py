@@ -726,3 +726,25 @@ def test_results_over_the_cache_refused_on_a_gpu(mx, fmt):
             assert e.value.status == 1
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(before, (c.k, c.v, c.k_sf, c.v_sf))) and mx.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("ql,kv", [([1, 2], [1, 40]), ([6, 3], [300, 3]), ([1, 1], [5000, 2]), ([70, 20], [90, 10])])
+def test_attention_infinite_query(mx, fmt, ql, kv):
+    """An infinite channel makes every score of its row infinite or NaN, and so the row NaN, also
+    where all of them are -inf; a row that sees no key has O = 0, lse = -inf whatever it holds."""
+    import torch
+    rng = np.random.default_rng(47)
+    c, q, cu, lens, table, slots = build(mx, rng, fmt, 16, 2, 2, ql, kv)
+    ones = torch.ones(sum(kv), 2, 128, dtype=torch.bfloat16, device="cuda")
+    mx.kv_append(c, ones, bf16(rng, sum(kv), 2, 128).cuda(), torch.from_numpy(np.concatenate(slots)).cuda())
+    q = q.contiguous()
+    q[0, 0, 5] = -np.inf                                      # every score -inf
+    q[0, 3, 7] = np.inf
+    q[ql[0] + ql[1] - 1, 1, 9] = -np.inf                      # the last query of the second request
+    q[ql[0] + ql[1] - 1, 2, 100] = np.nan
+    if ql[1] > kv[1]:
+        q[ql[0], :, 3] = -np.inf                              # sees no key
+    o, lse = check(mx, c, q, cu, lens, table, slots, causal=True)
+    assert torch.isnan(o[0, 0]).all() and torch.isnan(lse[0, 0]) and not torch.isnan(o[0, 1]).any()
+    assert mx.device_status() == 0
