@@ -748,3 +748,49 @@ def test_attention_infinite_query(mx, fmt, ql, kv):
     o, lse = check(mx, c, q, cu, lens, table, slots, causal=True)
     assert torch.isnan(o[0, 0]).all() and torch.isnan(lse[0, 0]) and not torch.isnan(o[0, 1]).any()
     assert mx.device_status() == 0
+
+
+def many_requests(rng, R, prompts, most, long):
+    """Query and key lengths of R requests: decoding ones, idle ones, requests without keys, some prompts, one long context."""
+    ql, kv = [1] * R, [int(k) for k in rng.integers(1, most, R)]
+    for i in rng.permutation(R)[: R // 10]:
+        ql[i] = 0
+    for i in rng.permutation(R)[: R // 20]:
+        kv[i] = 0
+    for i in (0, R // 2, R - 1)[:prompts]:
+        ql[i] = int(rng.integers(50, 90))
+        kv[i] = ql[i] + int(rng.integers(0, 200))
+    if long:
+        ql[R - 2], kv[R - 2] = 1, long
+    return ql, kv
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("R,prompts,most,long", [
+    (127, 0, 60, 3000), (128, 0, 60, 3000), (129, 0, 60, 3000), (600, 0, 40, 1500), (1300, 0, 24, 2000),   # several turns of the scans
+    (130, 2, 60, 3000), (513, 3, 30, 1500), (1300, 3, 20, 1100)])                                        # the same with prompts
+def test_attention_many_requests(mx, fmt, R, prompts, most, long):
+    import torch
+    rng = np.random.default_rng(R + prompts)
+    ql, kv = many_requests(rng, R, prompts, most, long)
+    args = build(mx, rng, fmt, 16, 2, 2, ql, kv)
+    assert mx.mxfa_kv_attn_workspace_size(R, max(ql), args[4].shape[1] * 16, 4, 2) > 0
+    o, lse = check(mx, *args, causal=True)
+    o2, lse2 = check(mx, *args, causal=True)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert mx.device_status() == 0
+
+
+@pytest.mark.parametrize("R,H,G,q", [(1300, 8, 1, 1), (1000, 8, 3, 4)])
+def test_attention_more_whole_items_than_ctas(mx, R, H, G, q):
+    """Short contexts whose items are dealt out in more than one turn of the grid."""
+    import torch
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert R * H > 16 * sms * (4 if G * q <= 8 else 3)
+    rng = np.random.default_rng(R)
+    ql, kv = many_requests(rng, R, 0, 40, 0)
+    ql = [n * q for n in ql]
+    args = build(mx, rng, 0, 16, H, G, ql, kv)
+    assert mx.mxfa_kv_attn_workspace_size(R, q, args[4].shape[1] * 16, H * G, H) == 0
+    check(mx, *args, causal=True)
+    assert mx.device_status() == 0
