@@ -483,7 +483,11 @@ size_t mxfa_kv_sf_bytes(int64_t num_blocks, int page, int H, int fmt);
  * Blocks are taken in request order.  Where the free ones do not suffice, the
  * first request that would exceed them and all later ones that need a block get none:
  * their kv_lens stays ctx, their slots are -1 (mxfa_kv_append skips them), and
- * ring_out[2] > 0 says so.  A done request's blocks go back in request and table
+ * ring_out[2] > 0 says so.  Such a request's tokens stay in cu_q, so mxfa_kv_attn
+ * computes their rows too, as if they were the last of the ctx stored ones: these rows mean
+ * nothing.  The same holds for a request past max_blocks.
+ * Where cu_q[R] exceeds `tokens`, all tokens are planned (blocks, kv_lens) and the last ones
+ * get no slot.  A done request's blocks go back in request and table
  * order and can be taken from the next step on.  kv_lens may be ctx_lens and
  * ring_out may be ring_in (a step captured once and replayed); any other
  * buffers that overlap are MXFA_ERR_INVALID_ARG.  The new lengths sum to less than 2^31.

@@ -17,11 +17,12 @@
 // vanishing; m moves when a score exceeds it by more than 6, so P <= 2^14.
 //
 // Work.  The key tiles (128 keys) of all (request, key head, block of query
-// rows) items form one line, cut into equal runs, one per CTA: no CTA has more
-// than one tile above another whatever the lengths.  An item inside one run is
-// finished there; one cut by a border leaves partial (m, l, O) records that a
-// second kernel joins in the order of the keys, so results do not depend on
-// timing.  Each of the CTA's four warps takes 32 of a tile's keys with its own
+// rows) items form one line, with kItemTiles units more for each item, cut into
+// equal runs, one per CTA: no CTA has more than one unit above another whatever the
+// lengths.  An item inside one run is finished there; one cut by a border leaves
+// partial (m, l, O) records that a second kernel joins in the order of the keys, so
+// results do not depend on timing.  Where all contexts are short (kWholeTiles) there is
+// no line: whole items go round the CTAs, whose tiles may then differ.  Each of the CTA's four warps takes 32 of a tile's keys with its own
 // ring of asynchronous copies and its own softmax state, so warps never wait on
 // one another inside an item.
 //
@@ -35,15 +36,15 @@
 // merged into bytes before conversion so that the pair (key, key + 1) comes
 // out of one conversion.
 //
-// What bounds it.  A row of 136 or 144 bytes takes the SM some ten cycles of instructions:
-// 617 a warp for 32 keys and one tile of rows (a quarter of them conversions), which
-// keeps the schedulers 55% and the ALUs 44% busy.  64 requests of up to 8192 keys, 8 key
-// heads, G = 4, MXFP4: 66 us, 3.8 TB/s (56% of a copy's rate); three of 97,000 to 130,000
-// keys, G = 8, NVFP4: 87 us, 4.4 TB/s.  Requests of 24 to 48 rows (3 to 6 tokens x 8) over
-// up to 12288 keys: 108 us, 212 TFLOP/s; there every tile of rows adds 150 instructions,
-// and a second block of rows converts the cache again.  Other forms, in their time: query
-// rows as M 115 us for the first case where keys as M took 88; bulk copies, which
-// compile to a loop over the lanes, 91 where these take 85; two chains of score
+// What bounds it.  Latency: 3.7 warps a scheduler, each on one chain of dependent
+// instructions (617 a warp for 32 keys and one tile of rows, a quarter of them
+// conversions), keep the schedulers 55%, the ALUs 45% and HBM 54% busy; no unit is full.
+// 64 requests of up to 8192 keys, 8 key heads, G = 4, MXFP4: 65 us, 3.8 TB/s (57% of a
+// copy's rate); three of 97,000 to 130,000 keys, G = 8, NVFP4: 87 us, 4.4 TB/s.  Requests
+// of 24 to 48 rows (3 to 6 tokens x 8) over up to 12288 keys: 107 us, 214 TFLOP/s; there
+// every tile of rows adds 150 instructions, and a second block of rows converts the
+// cache again.  Other forms, in their time: query rows as M 115 us for the first case
+// where keys as M took 88; bulk copies 91 where these took 85; two chains of score
 // products, no change.
 #include "kv_fp4.cuh"
 #include "mx_ptx.cuh"
@@ -66,7 +67,7 @@ constexpr int kMinTiles = 4;              // least units of a run, as long as it
 // requests of 512 keys 7.7, 8.2, 16.3 whole and 10.8, 13.0, 21.6 cut; of 1024 keys
 // 11.8, 12.0, 24.6 and 11.4, 14.7, 29.8; of 2048 keys 19.4, 21.9, 40.7 and 11.6, 20.9, 44.5.
 constexpr int kWholeTiles = 8;
-// What an item costs beside its tiles (drain, merge), in tiles: 1, 2, 3 and 4 take 133,
+// What an item costs beside its tiles (drain, merge), in tiles: 1, 2, 3 and 4 took 133,
 // 116, 110.7 and 110.7 us for the drafted tokens above, 72.6, 66.8, 65.9 and 66.7 us for
 // the 64 requests.
 constexpr int kItemTiles = 3;
@@ -891,8 +892,8 @@ __global__ void __launch_bounds__(256) kv_join_kernel(KvAttnArgs a, int ctas) {
 }
 
 // Tiles of eight query rows in a block: as few blocks of at most 32 rows as there
-// can be, of equal size (48 rows: two of 24; 110 us for the drafted tokens above, where
-// blocks of 32 take 132, as four tiles spill, and blocks of 16 take 125).
+// can be, of equal size (48 rows: two of 24; in their time 110 us for the drafted tokens
+// above, where blocks of 32 took 132, as four tiles spill, and blocks of 16 took 125).
 int row_tiles(int64_t rows) {
   const int64_t blocks = (rows + 8 * kMaxNt - 1) / (8 * kMaxNt);
   return int((rows + 8 * blocks - 1) / (8 * blocks));

@@ -267,9 +267,12 @@ cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t st) {
 // --------------------------------------------------------------- store and load
 // Sixteen lanes per cache row of K or of V, eight channels a lane: 16 bytes of
 // bf16 on one side, 4 bytes of codes on the other, and one lane of each block
-// for its scale.  Bound by HBM: 256 bytes of bf16 and 68 or 72 bytes of cache
-// per row.  32768 tokens x 8 heads, MXFP4: store 41 us (4.1 TB/s), load 37 us (4.6 TB/s),
-// of a copy's 6.8 TB/s; the rows of a page lie H pages apart, 64 bytes each.
+// for its scale.  256 bytes of bf16 and 68 or 72 bytes of cache per row move.  32768
+// tokens x 8 heads: store 41 us (MXFP4, 4.1 TB/s) and 71 us (NVFP4, 2.4 TB/s:
+// instructions, 3.4 a cycle, with eight correctly rounded divisions a lane), load 36
+// and 38 us (4.7 and 4.5 TB/s); a plain elementwise kernel that moves as many bytes
+// takes 29 us (5.9 TB/s).  A token's rows in a page are 64 bytes each, a page of
+// one head apart.
 __device__ __forceinline__ uint32_t pack8_e2m1(const float* y) {
   uint32_t r;
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"

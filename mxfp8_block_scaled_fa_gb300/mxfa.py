@@ -811,7 +811,8 @@ class KvCache:
 
 @dataclass
 class KvStep:
-    """What kv_plan says about a step (mxfa_kv_plan in mxfa.h)."""
+    """What kv_plan says about a step (mxfa_kv_plan in mxfa.h).  Where ring_state[2] > 0 some requests
+    got no blocks: their tokens' slots are -1, and what the attention returns for them is to be left aside."""
     cu_q: torch.Tensor        # int32 [R + 1]
     kv_lens: torch.Tensor     # int32 [R]
     slots: torch.Tensor       # int64 [tokens]
