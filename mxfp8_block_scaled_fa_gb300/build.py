@@ -3,6 +3,7 @@ Python module of the 4-bit cache's calls, with g++.  The library stands without 
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
 import importlib.metadata
 import importlib.util
 import os
@@ -92,9 +93,16 @@ def _py_module_fresh() -> bool:
     return _fresh(PY_MODULE, [__file__, PY_SRC, *_deps()])
 
 
+def _drop_py_module() -> None:
+    """An outdated module goes before a new one is tried: it may not fit the library."""
+    with contextlib.suppress(FileNotFoundError):
+        os.remove(PY_MODULE)
+
+
 def build_py_module() -> str:
     """The Python module alone, beside a built library; raises where it cannot be built."""
     if not _py_module_fresh():
+        _drop_py_module()
         _link_py_module(_compile_py_module())
     return PY_MODULE
 
@@ -107,6 +115,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     new_lib = force or not _fresh(LIB, srcs + _deps() + [__file__])
     new_module = force or not _py_module_fresh()
     py_obj = None
+    if new_module:
+        _drop_py_module()
     if new_lib:
         nvcc = _nvcc()
 

@@ -78,3 +78,20 @@ def test_a_missing_module_is_named(monkeypatch, tmp_path):
     mxfa.lib()                                                # the library's calls need none of it
     with pytest.raises(RuntimeError, match="absent.so"):
         mxfa._fast()
+
+
+@pytest.mark.parametrize("call", ["build", "build_py_module"])
+def test_an_outdated_module_does_not_stay(small, monkeypatch, call):
+    """A module of older sources may disagree with the new library on its structures."""
+    def fail(*a):
+        raise RuntimeError("no such compiler")
+    monkeypatch.setattr(small, "_compile_py_module", lambda *a: "kv_py.o")
+    monkeypatch.setattr(small, "_link_py_module", lambda *a: None)
+    small.build()
+    with open(small.PY_MODULE, "w") as f:
+        f.write("old")
+    os.utime(small.PY_MODULE, (1, 1))
+    monkeypatch.setattr(small, "_compile_py_module", fail)
+    with (pytest.warns(RuntimeWarning) if call == "build" else pytest.raises(RuntimeError)):
+        getattr(small, call)()
+    assert not os.path.exists(small.PY_MODULE) and os.path.exists(small.LIB)
