@@ -794,3 +794,37 @@ def test_attention_more_whole_items_than_ctas(mx, R, H, G, q):
     assert mx.mxfa_kv_attn_workspace_size(R, q, args[4].shape[1] * 16, H * G, H) == 0
     check(mx, *args, causal=True)
     assert mx.device_status() == 0
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("R,page,width,spare,prompts", [(7, 16, 9, 40, 2), (33, 32, 5, 7, 4), (513, 16, 8, 90, 30)])
+def test_plan_of_more_tokens_than_rows(mx, R, page, width, spare, prompts, inplace):
+    """Tokens behind the last row of slots are planned all the same: blocks, lengths and counters are as with rows for all."""
+    for seed, share in enumerate((0.0, 0.3, 0.9)):
+        rng = np.random.default_rng(2000 * R + seed)
+        ctx, new, table, ring, head, tail = random_step(rng, R, page, width, spare, prompts)
+        tokens = int(np.maximum(new, 0).sum() * share)
+        got, gt, gf = run_plan(mx, ctx, new, table, ring, head, tail, page, tokens, inplace)
+        t, f = table.tolist(), ring.tolist()
+        cu, kv, slots, pos, state = kv_ref.plan(ctx.tolist(), new.tolist(), t, f, head, tail, page, tokens)
+        assert got == [cu, kv, slots[:tokens], pos[:tokens], state]
+        np.testing.assert_array_equal(gt, t)
+        np.testing.assert_array_equal(gf, f)
+        assert mx.device_status() == 0
+
+
+def test_attention_of_unserved_requests(mx):
+    """A request without blocks keeps its length and gets no slots; its rows read the stored keys alone, and no other request's change."""
+    import torch
+    rng = np.random.default_rng(53)
+    c, q, cu, lens, table, slots = build(mx, rng, 0, 16, 2, 2, [0, 0, 0], [16, 40, 32], extra=0, pad_rows=9)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    ring, state = torch.full((c.k.shape[0],), -7, dtype=torch.int32, device="cuda"), torch.zeros(3, dtype=torch.int64, device="cuda")
+    s = mx.kv_plan(lens, i32(3, 4, 2), table, ring, state, 16, 9)
+    assert s.ring_state.tolist() == [0, 0, 2] and s.kv_lens.tolist() == [16, 44, 32] and s.cu_q.tolist() == [0, 3, 7, 9]
+    at = int(table[1, 2]) * 16 + 8
+    assert s.slots.tolist() == [-1] * 3 + list(range(at, at + 4)) + [-1] * 2 and s.positions.tolist() == [16, 17, 18, 40, 41, 42, 43, 32, 33]
+    k = bf16(rng, 9, 2, 128).cuda()
+    mx.kv_append(c, k, k, s.slots)
+    check(mx, c, q, s.cu_q, s.kv_lens, table, [slots[0], np.concatenate([slots[1], np.arange(at, at + 4)]), slots[2]], causal=True)
+    assert mx.device_status() == 0
