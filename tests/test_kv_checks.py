@@ -255,10 +255,10 @@ def test_results_over_the_cache_refused(mx, part):
     for x in (at, at - 1536 + 16, last):
         assert L.mxfa_kv_load(ref, 0x1000, 3, x, 0x20000, None) == 1
         assert L.mxfa_kv_load(ref, 0x1000, 3, 0x20000, x, None) == 1
-    # attention of 3 tokens and 4 heads: o of 3072 bytes, lse of 48
-    base = dict(q=0x10000, qs=1024, T=3, cu=0x20000, kv=0x30000, R=1, bt=0x40000, nb=128, mq=3, Hq=4, s=0.1, c=1, o=0x50000,
+    # attention of 5 tokens and 4 heads: o of 5120 bytes, lse of 80
+    base = dict(q=0x10000, qs=1024, T=5, cu=0x20000, kv=0x30000, R=1, bt=0x40000, nb=128, mq=3, Hq=4, s=0.1, c=1, o=0x50000,
                 lse=0x60000, ws=0x10000000, wb=1 << 30)
-    bad = [dict(o=at), dict(o=at - 3072 + 16), dict(o=last), dict(lse=at), dict(lse=at - 44), dict(lse=last)]
+    bad = [dict(o=at), dict(o=at - 5120 + 16), dict(o=last), dict(lse=at), dict(lse=at - 76), dict(lse=last)]
     if L.mxfa_kv_attn_workspace_size(1, 3, 128 * 16, 4, 2):
         bad += [dict(ws=at), dict(ws=last), dict(ws=at - 16)]
     for kw in bad:
