@@ -549,6 +549,113 @@ mxfa_status mxfa_kv_attn(const mxfa_kv_cache* cache, const void* q, int64_t q_st
                          int max_blocks, int max_q, int Hq, float softmax_scale, int causal, void* o,
                          float* lse, void* ws, size_t ws_bytes, mxfa_stream_t stream);
 
+/* mxfa_kv_attn_window -- mxfa_kv_attn (causal) where a query at position p (query i of a request's n:
+ * p = kv - n + i) sees the last `window` keys, p - window + 1 .. p, and the first `sinks` ones,
+ * j < sinks, j <= p.  window >= 1, sinks >= 0.  Pages without a key in a row's sight are not read, and
+ * their table entries may be anything (pages given back by mxfa_kv_free).  The workspace is of
+ * mxfa_kv_attn_window_workspace_size() bytes; everything else as mxfa_kv_attn, the limit of 2^25 keys
+ * taken of window + sinks. */
+size_t mxfa_kv_attn_window_workspace_size(int R, int max_q, int64_t max_k, int Hq, int H, int window, int sinks);
+mxfa_status mxfa_kv_attn_window(const mxfa_kv_cache* cache, const void* q, int64_t q_stride, int64_t total_q,
+                                const int32_t* cu_q, const int32_t* kv_lens, int R, const int32_t* block_table,
+                                int max_blocks, int max_q, int Hq, float softmax_scale, int window, int sinks,
+                                void* o, float* lse, void* ws, size_t ws_bytes, mxfa_stream_t stream);
+
+/* mxfa_kv_attn_shared -- mxfa_kv_attn (causal) for requests that share prefixes: the keys of a group's
+ * prefix are read once for the queries of all its requests.
+ *  group_starts DEVICE int32 [groups + 1], ascending: group g is requests group_starts[g] ..
+ *               group_starts[g + 1] - 1; requests of no group are computed as by mxfa_kv_attn
+ *  prefix_lens  DEVICE int32 [groups]: the first prefix_lens[g] keys of each request of the group are
+ *               those of its first request, whose row of block_table they are read from; each
+ *               request's further keys from its own row.  Any length, 0 included
+ *  max_group_q  the most query tokens of a group
+ * Each request with queries has at least the prefix before them (kv - n >= prefix).  One that has not,
+ * and the requests of a group whose starts, queries or prefix are outside their bounds, are left out
+ * and recorded as failed index checks.  The workspace is of mxfa_kv_attn_shared_workspace_size() bytes,
+ * max_k = max_blocks * page; everything else as mxfa_kv_attn.  groups may be 0. */
+size_t mxfa_kv_attn_shared_workspace_size(int R, int groups, int64_t total_q, int max_q, int max_group_q, int64_t max_k,
+                                          int Hq, int H);
+mxfa_status mxfa_kv_attn_shared(const mxfa_kv_cache* cache, const void* q, int64_t q_stride, int64_t total_q,
+                                const int32_t* cu_q, const int32_t* kv_lens, int R, const int32_t* block_table,
+                                int max_blocks, int max_q, int Hq, float softmax_scale, const int32_t* group_starts,
+                                const int32_t* prefix_lens, int groups, int max_group_q, void* o, float* lse,
+                                void* ws, size_t ws_bytes, mxfa_stream_t stream);
+
+/* ---------------------------------------------------------- rotary positions
+ * The first `rot` of a head's 128 channels turn by their token's position p: pair i by the angle
+ * t = p f_i,  (a, b) -> gain (a cos t - b sin t, b cos t + a sin t);  the others stay.  The pages have
+ * no counterpart to these calls.
+ *  turns   DEVICE int64 [rot / 2]: f_i / 2 pi in 2^-64ths of a turn, modulo 2^64 (negative where it is
+ *          half a turn or more), so that the angle of any position is exact to 2^-32 turns
+ *  rot     16, 32, .., 128
+ *  layout  pairs (i, i + rot / 2) or (2 i, 2 i + 1) */
+#define MXFA_ROPE_HALF 0
+#define MXFA_ROPE_INTERLEAVED 1
+typedef struct {
+  const int64_t* turns;
+  int rot, layout;
+  float gain;
+} mxfa_rotation;
+
+/* mxfa_rope -- y = x turned (before mxfa_quantize, mxfa_kv_append or mxfa_kv_attn), or with inverse = 1
+ * turned back with the same gain: the gradient of x from that of y.
+ *  x, y       bf16 rows of H * 128, consecutive tokens x_stride / y_stride elements apart (multiples of
+ *             8, at least H * 128), 16-byte aligned; y may be x (same stride), else they do not overlap
+ *  positions  DEVICE int32 [tokens], as mxfa_kv_plan gives them; negative: the token's row of y stays
+ * fp32, one rounding to bf16.  y overlaps neither positions nor turns (MXFA_ERR_INVALID_ARG). */
+mxfa_status mxfa_rope(const void* x, int64_t x_stride, void* y, int64_t y_stride, const int32_t* positions,
+                      int64_t tokens, int H, int D, const mxfa_rotation* rot, int inverse, mxfa_stream_t stream);
+
+/* mxfa_kv_append_rope -- a step's new tokens in one call: q_out = q turned, k turned and v into the
+ * cache, byte for byte as mxfa_rope of q and k and mxfa_kv_append of the turned k and v.
+ *  q, q_out   bf16 rows of Hq * 128, q_out may be q (same stride)
+ *  positions  DEVICE int32 [tokens]; negative: the token is left out altogether
+ *  slots      as mxfa_kv_append; a token without a slot still gets its q_out
+ * Other arguments and errors as mxfa_kv_append and mxfa_rope. */
+mxfa_status mxfa_kv_append_rope(const mxfa_kv_cache* cache, const void* q, int64_t q_stride, int Hq, const void* k,
+                                int64_t k_stride, const void* v, int64_t v_stride, int64_t tokens,
+                                const int32_t* positions, const int64_t* slots, const mxfa_rotation* rot, void* q_out,
+                                int64_t q_out_stride, mxfa_stream_t stream);
+
+/* ------------------------------------------------- pages shared by requests
+ * refs int32 [num_blocks] (DEVICE, zeros at first) counts the owners of a block beside the first.  A
+ * request that may share pages is ended by mxfa_kv_free, not by a negative count in mxfa_kv_plan, which
+ * gives back all its blocks whoever else owns them. */
+
+/* mxfa_kv_fork -- requests that continue other ones: row dst[f] of block_table gets the first lens[f]
+ * tokens of row src[f].  Whole pages are shared (refs + 1).  A last page that is not full would be
+ * written by both, so it gets a new block from the ring, the k-th such fork the k-th free block.
+ *  src, dst, lens  DEVICE int32 [F], F <= 16384; a row is dst of one fork only and src of none then;
+ *               0 <= lens <= the tokens that row src holds
+ *  from_blocks, to_blocks  int32 [F] (written): the block to copy and the new one, for mxfa_kv_copy_blocks
+ *               in each layer's cache; -1, -1 where there is none
+ *  lens_out     int32 [F] (written): tokens that row dst holds: lens, or where the ring had no block left
+ *               (ring_out[2] counts them) the whole pages of it alone, with -1 behind them in the table
+ *  free_ring, ring_in/out  as mxfa_kv_plan; ring_out may be ring_in
+ * Other entries of row dst stay.  Forks outside their bounds give nothing (lens_out 0), and entries that are no
+ * blocks are copied as -1 without an owner; both are recorded as failed index checks.  Other buffers that
+ * overlap are MXFA_ERR_INVALID_ARG. */
+mxfa_status mxfa_kv_fork(int32_t* block_table, int R, int max_blocks, const int32_t* src, const int32_t* dst,
+                         const int32_t* lens, int F, int32_t* refs, int64_t num_blocks, const int32_t* free_ring,
+                         int64_t ring_size, const int64_t* ring_in, int64_t* ring_out, int page, int32_t* from_blocks,
+                         int32_t* to_blocks, int32_t* lens_out, mxfa_stream_t stream);
+
+/* mxfa_kv_free -- pages given up: for each f, entries first[f] .. end[f] - 1 of row rows[f] (ended requests,
+ * rejected continuations, pages behind a window) have one owner fewer; negative entries are skipped.  Blocks left
+ * without an owner go to the ring in ascending order.  The table stays as it is: an entry given up is not given
+ * up again.  ring_size is at least num_blocks; ring_out may be ring_in; ring_out[2] is ring_in[2].  Rows and ranges
+ * outside the table, entries past num_blocks and blocks given up more often than owned are recorded as failed
+ * index checks.  Other buffers that overlap are MXFA_ERR_INVALID_ARG. */
+mxfa_status mxfa_kv_free(const int32_t* block_table, int R, int max_blocks, const int32_t* rows, const int32_t* first,
+                         const int32_t* end, int F, int32_t* refs, int64_t num_blocks, int32_t* free_ring,
+                         int64_t ring_size, const int64_t* ring_in, int64_t* ring_out, mxfa_stream_t stream);
+
+/* mxfa_kv_copy_blocks -- block from_blocks[i] of the cache (all heads, codes and scales of K and V) over
+ * to_blocks[i]; pairs with a negative one are skipped, ones past the cache skipped and recorded.  The
+ * blocks written are distinct and none of those read (but for from = to, which does nothing). */
+mxfa_status mxfa_kv_copy_blocks(const mxfa_kv_cache* cache, const int32_t* from_blocks, const int32_t* to_blocks, int n,
+                                mxfa_stream_t stream);
+
 /* mxfa_tensor_peak_probe -- `ctas` CTAs (one per SM at most) each issue
  * `iters` x 4 back-to-back block-scaled MMAs (M = 128, N = 256, K = 32, E4M3,
  * operands resident in shared memory) and write the SM clock cycles they took

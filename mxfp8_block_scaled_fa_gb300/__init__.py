@@ -21,6 +21,9 @@ def __getattr__(name):
                                             "ELEM_E2M1",
                                             "KV_MXFP4", "KV_NVFP4", "KvCache", "KvPages", "KvStep", "kv_ring", "kv_plan",
                                             "kv_append", "kv_load", "kv_attention",
+                                            "Rope", "Rotation", "ROPE_HALF", "ROPE_INTERLEAVED", "rope", "rope_bwd", "rope_positions",
+                                            "kv_append_rope", "kv_attention_shared", "KvFork", "kv_refs", "kv_fork", "kv_free",
+                                            "kv_copy_blocks",
                                             "device_status"):
         from . import mxfa as _m
         value = globals()[name] = getattr(_m, name)  # later uses find it without this function

@@ -799,6 +799,103 @@ CacheRanges ranges_of(const KvPages& c) {
   return {{{c.k, rows * 64}, {c.v, rows * 64}, {c.k_sf, rows * sf}, {c.v_sf, rows * sf}, {c.k_scale, st}, {c.v_scale, st}}};
 }
 
+// Checks of an attention call over the cache, shared by its forms; what they have in common goes into `a`.
+mxfa_status check_attn(const mxfa_kv_cache* cache, const void* q, int64_t q_stride, int64_t total_q, const int32_t* cu_q, const int32_t* kv_lens,
+                       int R, const int32_t* block_table, int max_blocks, int max_q, int Hq, float softmax_scale, void* o, float* lse, void* ws,
+                       KvAttnArgs& a) {
+  memset(&a, 0, sizeof(a));
+  mxfa_status s = check_cache(cache, a.c);
+  if (s) return s;
+  if (!q || !cu_q || !kv_lens || !block_table || !o || !lse) return MXFA_ERR_INVALID_ARG;
+  if (total_q < 0 || R < 0 || max_blocks <= 0 || max_q < 0 || Hq <= 0 || Hq % a.c.H) return MXFA_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.0f) || !std::isfinite(softmax_scale)) return MXFA_ERR_INVALID_ARG;
+  if (total_q > 1 && q_stride < int64_t(Hq) * 128) return MXFA_ERR_INVALID_ARG;
+  if (total_q >= (int64_t(1) << 31) || total_q * Hq >= (int64_t(1) << 31) || R > (1 << 20) ||
+      int64_t(max_blocks) * a.c.page > (int64_t(1) << 30))
+    return MXFA_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(ws) || (total_q > 1 && q_stride % 8)) return MXFA_ERR_MISALIGNED;
+  if (!aligned4(cu_q) || !aligned4(kv_lens) || !aligned4(block_table) || !aligned4(lse)) return MXFA_ERR_MISALIGNED;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_stride;
+  a.total_q = total_q;
+  a.cu_q = cu_q;
+  a.kv_lens = kv_lens;
+  a.R = R;
+  a.table = block_table;
+  a.width = max_blocks;
+  a.max_q = max_q;
+  a.Hq = Hq;
+  a.G = Hq / a.c.H;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.o = static_cast<uint16_t*>(o);
+  a.lse = lse;
+  a.ws = static_cast<uint8_t*>(ws);
+  return MXFA_OK;
+}
+
+// The workspace suffices, and what the call writes meets nothing else of it.
+mxfa_status check_attn_buffers(const KvAttnArgs& a, size_t need, size_t ws_bytes, const int32_t* starts, const int32_t* prefix_lens, int groups) {
+  if (need > 0 && !a.ws) return MXFA_ERR_INVALID_ARG;
+  if (ws_bytes < need) return MXFA_ERR_WORKSPACE_TOO_SMALL;
+  const size_t row = size_t(a.Hq) * 256, rows = size_t(a.total_q), R = size_t(a.R);
+  const Range written[] = {{a.o, rows * row}, {a.lse, rows * size_t(a.Hq) * 4}, {a.ws, need}};
+  const Range read[] = {{a.q, (rows - 1) * size_t(a.total_q > 1 ? a.q_stride : 0) * 2 + row}, {a.cu_q, R * 4 + 4}, {a.kv_lens, R * 4},
+                        {a.table, R * size_t(a.width) * 4}, {starts, starts ? size_t(groups) * 4 + 4 : 0},
+                        {prefix_lens, prefix_lens ? size_t(groups) * 4 : 0}};
+  if (any_meet(written, read) || any_meet(written, ranges_of(a.c))) return MXFA_ERR_INVALID_ARG;
+  if (meet(written[0], written[1]) || meet(written[0], written[2]) || meet(written[1], written[2])) return MXFA_ERR_INVALID_ARG;
+  return MXFA_OK;
+}
+
+mxfa_status check_rotation(const mxfa_rotation* r, Rotation& x) {
+  if (!r || !r->turns || r->rot <= 0 || r->rot > 128 || !std::isfinite(r->gain)) return MXFA_ERR_INVALID_ARG;
+  if (r->layout != MXFA_ROPE_HALF && r->layout != MXFA_ROPE_INTERLEAVED) return MXFA_ERR_INVALID_ARG;
+  if (r->rot % 16) return MXFA_ERR_UNSUPPORTED;
+  if (!aligned8(r->turns)) return MXFA_ERR_MISALIGNED;
+  x.turns = reinterpret_cast<const uint64_t*>(r->turns);
+  x.rot = r->rot;
+  x.inter = r->layout == MXFA_ROPE_INTERLEAVED ? 1 : 0;
+  x.inverse = 0;
+  x.gain = r->gain;
+  return MXFA_OK;
+}
+
+// Rows of `heads` heads of 128 bf16, `stride` elements apart.
+Range rows_range(const void* at, int64_t stride, int64_t tokens, int heads) {
+  return {at, size_t(tokens - 1) * size_t(tokens > 1 ? stride : 0) * 2 + size_t(heads) * 256};
+}
+// Rows of a and of b, of one distance, that lie beside one another.
+bool rows_apart(const Range& a, const Range& b, int64_t tokens, int64_t a_stride, int64_t b_stride, int a_heads, int b_heads) {
+  if (tokens < 2 || a_stride != b_stride) return false;
+  const int64_t period = a_stride * 2, an = int64_t(a_heads) * 256, bn = int64_t(b_heads) * 256;
+  const int64_t far = static_cast<const char*>(b.at) - static_cast<const char*>(a.at);
+  const int64_t off = (far % period + period) % period;  // of b's rows behind a's
+  return off >= an && off + bn <= period;
+}
+
+mxfa_status check_pages(const void* table, int R, int max_blocks, int F, const void* refs, int64_t blocks, const void* ring, int64_t ring_size,
+                        const void* ring_in, const void* ring_out) {
+  if (!table || !refs || !ring || !ring_in || !ring_out) return MXFA_ERR_INVALID_ARG;
+  if (R <= 0 || max_blocks <= 0 || F < 0 || blocks <= 0 || ring_size <= 0) return MXFA_ERR_INVALID_ARG;
+  if (R > (1 << 20) || F > kKvPlanMaxRequests || int64_t(R) * max_blocks >= (int64_t(1) << 31) || blocks >= (int64_t(1) << 31) ||
+      ring_size >= (int64_t(1) << 31))
+    return MXFA_ERR_UNSUPPORTED;
+  if (!aligned4(table) || !aligned4(refs) || !aligned4(ring) || !aligned8(ring_in) || !aligned8(ring_out)) return MXFA_ERR_MISALIGNED;
+  return MXFA_OK;
+}
+
+// Whether a written buffer meets another one; `own` (nullable), the last written one, is the last read one in place.
+template <size_t N, size_t M>
+bool clash(const Range (&written)[N], const Range (&read)[M], const Range* own) {
+  for (size_t i = 0; i < N; i++) {
+    for (size_t j = 0; j < M; j++)
+      if (!(own == &written[i] && j == M - 1) && meet(written[i], read[j])) return true;
+    for (size_t j = i + 1; j < N; j++)
+      if (meet(written[i], written[j])) return true;
+  }
+  return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -931,46 +1028,233 @@ mxfa_status mxfa_kv_attn(const mxfa_kv_cache* cache, const void* q, int64_t q_st
                          int max_blocks, int max_q, int Hq, float softmax_scale, int causal, void* o,
                          float* lse, void* ws, size_t ws_bytes, mxfa_stream_t stream) {
   KvAttnArgs a;
+  const mxfa_status s = check_attn(cache, q, q_stride, total_q, cu_q, kv_lens, R, block_table, max_blocks, max_q, Hq, softmax_scale, o, lse, ws, a);
+  if (s) return s;
+  if (total_q == 0 || R == 0 || max_q == 0) return MXFA_OK;
+  a.causal = causal ? 1 : 0;
+  const int64_t max_k = int64_t(max_blocks) * a.c.page;
+  if (!kv_attn_reaches(max_q, max_k, a.G)) return MXFA_ERR_UNSUPPORTED;
+  const mxfa_status t = check_attn_buffers(a, kv_attn_workspace(R, max_q, max_k, a.G), ws_bytes, nullptr, nullptr, 0);
+  return t ? t : from_cuda(launch_kv_attn(kAll, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t mxfa_kv_attn_window_workspace_size(int R, int max_q, int64_t max_k, int Hq, int H, int window, int sinks) {
+  if (R < 0 || max_q < 0 || max_k < 0 || H <= 0 || Hq <= 0 || Hq % H || window < 1 || sinks < 0) return 0;
+  return kv_attn_workspace(R, max_q, kv_window_reach(max_q, max_k, window, sinks), Hq / H);
+}
+
+mxfa_status mxfa_kv_attn_window(const mxfa_kv_cache* cache, const void* q, int64_t q_stride, int64_t total_q,
+                                const int32_t* cu_q, const int32_t* kv_lens, int R, const int32_t* block_table,
+                                int max_blocks, int max_q, int Hq, float softmax_scale, int window, int sinks,
+                                void* o, float* lse, void* ws, size_t ws_bytes, mxfa_stream_t stream) {
+  KvAttnArgs a;
+  const mxfa_status s = check_attn(cache, q, q_stride, total_q, cu_q, kv_lens, R, block_table, max_blocks, max_q, Hq, softmax_scale, o, lse, ws, a);
+  if (s) return s;
+  if (window < 1 || sinks < 0) return MXFA_ERR_INVALID_ARG;
+  if (total_q == 0 || R == 0 || max_q == 0) return MXFA_OK;
+  a.causal = 1;
+  // no context is longer than 2^30 keys
+  a.window = window < (1 << 30) ? window : 1 << 30;
+  a.sinks = sinks < (1 << 30) ? sinks : 1 << 30;
+  const int64_t max_k = kv_window_reach(max_q, int64_t(max_blocks) * a.c.page, a.window, a.sinks);
+  if (!kv_attn_reaches(max_q, max_k, a.G)) return MXFA_ERR_UNSUPPORTED;
+  const mxfa_status t = check_attn_buffers(a, kv_attn_workspace(R, max_q, max_k, a.G), ws_bytes, nullptr, nullptr, 0);
+  return t ? t : from_cuda(launch_kv_attn(kWindow, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t mxfa_kv_attn_shared_workspace_size(int R, int groups, int64_t total_q, int max_q, int max_group_q, int64_t max_k,
+                                          int Hq, int H) {
+  if (R < 0 || groups < 0 || total_q < 0 || max_q < 0 || max_group_q < 0 || max_k < 0 || H <= 0 || Hq <= 0 || Hq % H) return 0;
+  if (groups == 0) return kv_attn_workspace(R, max_q, max_k, Hq / H);
+  return kv_shared_workspace(R, groups, total_q, max_q, max_group_q, max_k, Hq, Hq / H).bytes;
+}
+
+mxfa_status mxfa_kv_attn_shared(const mxfa_kv_cache* cache, const void* q, int64_t q_stride, int64_t total_q,
+                                const int32_t* cu_q, const int32_t* kv_lens, int R, const int32_t* block_table,
+                                int max_blocks, int max_q, int Hq, float softmax_scale, const int32_t* group_starts,
+                                const int32_t* prefix_lens, int groups, int max_group_q, void* o, float* lse,
+                                void* ws, size_t ws_bytes, mxfa_stream_t stream) {
+  KvAttnArgs a;
+  const mxfa_status s = check_attn(cache, q, q_stride, total_q, cu_q, kv_lens, R, block_table, max_blocks, max_q, Hq, softmax_scale, o, lse, ws, a);
+  if (s) return s;
+  if (groups < 0 || max_group_q < 0 || (groups > 0 && (!group_starts || !prefix_lens))) return MXFA_ERR_INVALID_ARG;
+  if (!aligned4(group_starts) || !aligned4(prefix_lens)) return MXFA_ERR_MISALIGNED;
+  if (groups > (1 << 20)) return MXFA_ERR_UNSUPPORTED;
+  if (total_q == 0 || R == 0 || max_q == 0) return MXFA_OK;
+  a.causal = 1;
+  const int64_t max_k = int64_t(max_blocks) * a.c.page;
+  if (!kv_attn_reaches(max_q, max_k, a.G) || (groups > 0 && !kv_attn_reaches(max_group_q, max_k, a.G))) return MXFA_ERR_UNSUPPORTED;
+  const size_t need = mxfa_kv_attn_shared_workspace_size(R, groups, total_q, max_q, max_group_q, max_k, Hq, a.c.H);
+  const mxfa_status t = check_attn_buffers(a, need, ws_bytes, group_starts, prefix_lens, groups);
+  if (t) return t;
+  if (groups == 0) return from_cuda(launch_kv_attn(kAll, a, reinterpret_cast<cudaStream_t>(stream)));
+  a.starts = group_starts;
+  return from_cuda(launch_kv_attn_shared(a, prefix_lens, groups, max_group_q, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+mxfa_status mxfa_rope(const void* x, int64_t x_stride, void* y, int64_t y_stride, const int32_t* positions,
+                      int64_t tokens, int H, int D, const mxfa_rotation* rot, int inverse, mxfa_stream_t stream) {
+  RopeArgs a;
+  memset(&a, 0, sizeof(a));
+  mxfa_status s = check_rotation(rot, a.rot);
+  if (s) return s;
+  if (!x || !y || !positions || tokens < 0 || H <= 0) return MXFA_ERR_INVALID_ARG;
+  if (tokens > 1 && (x_stride < int64_t(H) * 128 || y_stride < int64_t(H) * 128)) return MXFA_ERR_INVALID_ARG;
+  if (D != 128 || H > 65536 || tokens >= (int64_t(1) << 31) || tokens * H >= (int64_t(1) << 31)) return MXFA_ERR_UNSUPPORTED;
+  if (!aligned16(x) || !aligned16(y) || !aligned4(positions) || (tokens > 1 && (x_stride % 8 || y_stride % 8))) return MXFA_ERR_MISALIGNED;
+  if (tokens == 0) return MXFA_OK;
+  const Range xr = rows_range(x, x_stride, tokens, H), yr = rows_range(y, y_stride, tokens, H);
+  const bool in_place = x == y && (tokens == 1 || x_stride == y_stride);
+  const Range read[] = {{positions, size_t(tokens) * 4}, {a.rot.turns, size_t(a.rot.rot) * 4}};
+  if ((!in_place && meet(xr, yr)) || meet(yr, read[0]) || meet(yr, read[1])) return MXFA_ERR_INVALID_ARG;
+  a.rot.inverse = inverse ? 1 : 0;
+  a.x = static_cast<const uint16_t*>(x);
+  a.y = static_cast<uint16_t*>(y);
+  a.x_stride = x_stride;
+  a.y_stride = y_stride;
+  a.positions = positions;
+  a.tokens = tokens;
+  a.H = H;
+  return from_cuda(launch_rope(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+mxfa_status mxfa_kv_append_rope(const mxfa_kv_cache* cache, const void* q, int64_t q_stride, int Hq, const void* k,
+                                int64_t k_stride, const void* v, int64_t v_stride, int64_t tokens,
+                                const int32_t* positions, const int64_t* slots, const mxfa_rotation* rot, void* q_out,
+                                int64_t q_out_stride, mxfa_stream_t stream) {
+  KvAppendRopeArgs a;
   memset(&a, 0, sizeof(a));
   mxfa_status s = check_cache(cache, a.c);
-  if (s) return s;
-  if (!q || !cu_q || !kv_lens || !block_table || !o || !lse) return MXFA_ERR_INVALID_ARG;
-  if (total_q < 0 || R < 0 || max_blocks <= 0 || max_q < 0 || Hq <= 0 || Hq % a.c.H) return MXFA_ERR_INVALID_ARG;
-  if (!(softmax_scale > 0.0f) || !std::isfinite(softmax_scale)) return MXFA_ERR_INVALID_ARG;
-  if (total_q > 1 && q_stride < int64_t(Hq) * 128) return MXFA_ERR_INVALID_ARG;
-  if (total_q >= (int64_t(1) << 31) || total_q * Hq >= (int64_t(1) << 31) || R > (1 << 20) ||
-      int64_t(max_blocks) * a.c.page > (int64_t(1) << 30))
-    return MXFA_ERR_UNSUPPORTED;
-  if (!aligned16(q) || !aligned16(o) || !aligned16(ws) || (total_q > 1 && q_stride % 8)) return MXFA_ERR_MISALIGNED;
-  if (!aligned4(cu_q) || !aligned4(kv_lens) || !aligned4(block_table) || !aligned4(lse)) return MXFA_ERR_MISALIGNED;
-  if (total_q == 0 || R == 0 || max_q == 0) return MXFA_OK;
+  if (s || (s = check_rotation(rot, a.rot))) return s;
+  if (!q || !k || !v || !positions || !slots || !q_out || tokens < 0 || Hq <= 0) return MXFA_ERR_INVALID_ARG;
+  const int64_t kv_row = int64_t(a.c.H) * 128, q_row = int64_t(Hq) * 128;
+  if (tokens > 1 && (k_stride < kv_row || v_stride < kv_row || q_stride < q_row || q_out_stride < q_row)) return MXFA_ERR_INVALID_ARG;
+  if (Hq > 65536 || tokens >= (int64_t(1) << 31) || tokens * (int64_t(Hq) + 2 * int64_t(a.c.H)) >= (int64_t(1) << 31)) return MXFA_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned4(positions) || !aligned8(slots) ||
+      (tokens > 1 && (q_stride % 8 || k_stride % 8 || v_stride % 8 || q_out_stride % 8)))
+    return MXFA_ERR_MISALIGNED;
+  if (tokens == 0) return MXFA_OK;
+  // what is written (the turned q, codes and block scales) meets neither what is read nor itself, but for q in place
+  const CacheRanges own = ranges_of(a.c);
+  const Range out = rows_range(q_out, q_out_stride, tokens, Hq), qr = rows_range(q, q_stride, tokens, Hq);
+  const Range read[] = {rows_range(k, k_stride, tokens, a.c.H), rows_range(v, v_stride, tokens, a.c.H), {positions, size_t(tokens) * 4},
+                        {slots, size_t(tokens) * 8}, {a.rot.turns, size_t(a.rot.rot) * 4}};
+  const bool in_place = q == q_out && (tokens == 1 || q_stride == q_out_stride);
+  if (!in_place && meet(out, qr)) return MXFA_ERR_INVALID_ARG;
+  for (const Range& x : read)
+    // q in place may be a part of the projection that k and v are other parts of
+    if (meet(out, x) && !(in_place && (&x == &read[0] || &x == &read[1]) && rows_apart(out, x, tokens, q_out_stride, &x == &read[0] ? k_stride : v_stride, Hq, a.c.H)))
+      return MXFA_ERR_INVALID_ARG;
+  for (int i = 0; i < 6; i++) {
+    if (meet(own.r[i], out)) return MXFA_ERR_INVALID_ARG;
+    if (i >= 4) continue;
+    if (meet(own.r[i], qr)) return MXFA_ERR_INVALID_ARG;
+    for (const Range& x : read)
+      if (meet(own.r[i], x)) return MXFA_ERR_INVALID_ARG;
+    for (int j = i + 1; j < 6; j++)
+      if (meet(own.r[i], own.r[j])) return MXFA_ERR_INVALID_ARG;
+  }
   a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.y = static_cast<uint16_t*>(q_out);
   a.q_stride = q_stride;
-  a.total_q = total_q;
-  a.cu_q = cu_q;
-  a.kv_lens = kv_lens;
-  a.R = R;
-  a.table = block_table;
-  a.width = max_blocks;
-  a.max_q = max_q;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.y_stride = q_out_stride;
+  a.tokens = tokens;
   a.Hq = Hq;
-  a.G = Hq / a.c.H;
-  a.scale_log2 = softmax_scale * 1.4426950408889634f;
-  a.causal = causal ? 1 : 0;
-  a.o = static_cast<uint16_t*>(o);
-  a.lse = lse;
-  a.ws = static_cast<uint8_t*>(ws);
-  if (!kv_attn_reaches(max_q, int64_t(max_blocks) * a.c.page, a.G)) return MXFA_ERR_UNSUPPORTED;
-  const size_t need = kv_attn_workspace(R, max_q, int64_t(max_blocks) * a.c.page, a.G);
-  if (need > 0 && !ws) return MXFA_ERR_INVALID_ARG;
-  if (ws_bytes < need) return MXFA_ERR_WORKSPACE_TOO_SMALL;
-  const size_t row = size_t(Hq) * 256, rows = size_t(total_q);
-  const Range written[] = {{o, rows * row}, {lse, rows * size_t(Hq) * 4}, {ws, need}};
-  const Range read[] = {{q, (rows - 1) * size_t(total_q > 1 ? q_stride : 0) * 2 + row}, {cu_q, size_t(R) * 4 + 4}, {kv_lens, size_t(R) * 4},
-                        {block_table, size_t(R) * size_t(max_blocks) * 4}};
-  if (any_meet(written, read) || any_meet(written, ranges_of(a.c))) return MXFA_ERR_INVALID_ARG;
-  if (meet(written[0], written[1]) || meet(written[0], written[2]) || meet(written[1], written[2])) return MXFA_ERR_INVALID_ARG;
-  return from_cuda(launch_kv_attn(a, reinterpret_cast<cudaStream_t>(stream)));
+  a.positions = positions;
+  a.slots = slots;
+  return from_cuda(launch_kv_append_rope(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+mxfa_status mxfa_kv_fork(int32_t* block_table, int R, int max_blocks, const int32_t* src, const int32_t* dst,
+                         const int32_t* lens, int F, int32_t* refs, int64_t num_blocks, const int32_t* free_ring,
+                         int64_t ring_size, const int64_t* ring_in, int64_t* ring_out, int page, int32_t* from_blocks,
+                         int32_t* to_blocks, int32_t* lens_out, mxfa_stream_t stream) {
+  mxfa_status s = check_pages(block_table, R, max_blocks, F, refs, num_blocks, free_ring, ring_size, ring_in, ring_out);
+  if (s) return s;
+  if (F > 0 && (!src || !dst || !lens || !from_blocks || !to_blocks || !lens_out)) return MXFA_ERR_INVALID_ARG;
+  if (page != 16 && page != 32 && page != 64 && page != 128) return MXFA_ERR_UNSUPPORTED;
+  if (int64_t(max_blocks) * page > (int64_t(1) << 30)) return MXFA_ERR_UNSUPPORTED;
+  for (const void* p : {static_cast<const void*>(src), static_cast<const void*>(dst), static_cast<const void*>(lens),
+                        static_cast<const void*>(from_blocks), static_cast<const void*>(to_blocks), static_cast<const void*>(lens_out)})
+    if (!aligned4(p)) return MXFA_ERR_MISALIGNED;
+  const size_t list = size_t(F) * 4;
+  const Range written[] = {{block_table, size_t(R) * size_t(max_blocks) * 4}, {refs, size_t(num_blocks) * 4}, {from_blocks, list},
+                           {to_blocks, list}, {lens_out, list}, {ring_out, 24}};
+  const Range read[] = {{src, list}, {dst, list}, {lens, list}, {free_ring, size_t(ring_size) * 4}, {ring_in, 24}};
+  if (clash(written, read, ring_in == ring_out ? &written[5] : nullptr)) return MXFA_ERR_INVALID_ARG;
+  KvForkArgs a;
+  memset(&a, 0, sizeof(a));
+  a.table = block_table;
+  a.R = R;
+  a.width = max_blocks;
+  a.src = src;
+  a.dst = dst;
+  a.lens = lens;
+  a.F = F;
+  a.refs = refs;
+  a.blocks = num_blocks;
+  a.ring = free_ring;
+  a.ring_size = ring_size;
+  a.ring_in = ring_in;
+  a.ring_out = ring_out;
+  a.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
+  a.from_blocks = from_blocks;
+  a.to_blocks = to_blocks;
+  a.lens_out = lens_out;
+  return from_cuda(launch_kv_fork(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+mxfa_status mxfa_kv_free(const int32_t* block_table, int R, int max_blocks, const int32_t* rows, const int32_t* first,
+                         const int32_t* end, int F, int32_t* refs, int64_t num_blocks, int32_t* free_ring,
+                         int64_t ring_size, const int64_t* ring_in, int64_t* ring_out, mxfa_stream_t stream) {
+  mxfa_status s = check_pages(block_table, R, max_blocks, F, refs, num_blocks, free_ring, ring_size, ring_in, ring_out);
+  if (s) return s;
+  if (F > 0 && (!rows || !first || !end)) return MXFA_ERR_INVALID_ARG;
+  if (max_blocks > (1 << 26)) return MXFA_ERR_UNSUPPORTED;
+  if (!aligned4(rows) || !aligned4(first) || !aligned4(end)) return MXFA_ERR_MISALIGNED;
+  const size_t list = size_t(F) * 4;
+  const Range written[] = {{refs, size_t(num_blocks) * 4}, {free_ring, size_t(ring_size) * 4}, {ring_out, 24}};
+  const Range read[] = {{block_table, size_t(R) * size_t(max_blocks) * 4}, {rows, list}, {first, list}, {end, list}, {ring_in, 24}};
+  if (clash(written, read, ring_in == ring_out ? &written[2] : nullptr)) return MXFA_ERR_INVALID_ARG;
+  KvFreeArgs a;
+  memset(&a, 0, sizeof(a));
+  a.table = block_table;
+  a.R = R;
+  a.width = max_blocks;
+  a.rows = rows;
+  a.first = first;
+  a.end = end;
+  a.F = F;
+  a.refs = refs;
+  a.blocks = num_blocks;
+  a.ring = free_ring;
+  a.ring_size = ring_size;
+  a.ring_in = ring_in;
+  a.ring_out = ring_out;
+  return from_cuda(launch_kv_free(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+mxfa_status mxfa_kv_copy_blocks(const mxfa_kv_cache* cache, const int32_t* from_blocks, const int32_t* to_blocks, int n,
+                                mxfa_stream_t stream) {
+  KvPages c;
+  const mxfa_status s = check_cache(cache, c);
+  if (s) return s;
+  if (n < 0 || !from_blocks || !to_blocks) return MXFA_ERR_INVALID_ARG;
+  if (!aligned4(from_blocks) || !aligned4(to_blocks)) return MXFA_ERR_MISALIGNED;
+  if (int64_t(c.H) * c.page > (1 << 24) || int64_t(n) * kv_copy_chunks(c) >= (int64_t(1) << 31)) return MXFA_ERR_UNSUPPORTED;
+  if (n == 0) return MXFA_OK;
+  const CacheRanges own = ranges_of(c);
+  const Range read[] = {{from_blocks, size_t(n) * 4}, {to_blocks, size_t(n) * 4}};
+  for (int i = 0; i < 4; i++) {
+    if (meet(own.r[i], read[0]) || meet(own.r[i], read[1])) return MXFA_ERR_INVALID_ARG;
+    for (int j = i + 1; j < 6; j++)
+      if (meet(own.r[i], own.r[j])) return MXFA_ERR_INVALID_ARG;
+  }
+  return from_cuda(launch_kv_copy(c, from_blocks, to_blocks, n, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
@@ -987,7 +1271,7 @@ mxfa_status mxfa_get_device_status(mxfa_stream_t stream, unsigned* flags) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(st) != cudaSuccess) return MXFA_ERR_CUDA;
   unsigned f = read_status_quant(st) | read_status_fwd(st) | read_status_bwd(st) | read_status_gemm(st) | read_status_kv(st) |
-               read_status_kv_attn(st) | read_status_kv_prefill(st);
+               read_status_kv_attn(st) | read_status_kv_prefill(st) | read_status_rope(st) | read_status_kv_pages(st);
   if (flags) *flags = f;
   if (f & 1u) return MXFA_ERR_TIMEOUT;
   if (f & 2u) return MXFA_ERR_DEVICE_INDEX;

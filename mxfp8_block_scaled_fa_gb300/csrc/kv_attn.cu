@@ -169,9 +169,29 @@ __device__ __forceinline__ int key_of(int n) { return n ^ ((n >> 1) & 1); }
 struct Request {
   int q0, n;      // first query token and their number
   int kv;         // keys
+  // kWindow, kTail: keys lo .. hi - 1 are in no row's sight; the tiles that hold nothing else,
+  // `jump` keys of them from key `at` on, are left out of the line
+  int lo, hi, at, jump;
 };
+// Keys lo .. hi - 1 hidden from every row of a request.
+__device__ __forceinline__ void hide(Request& x, int lo, int hi) {
+  x.lo = lo, x.hi = hi;
+  x.at = (lo + kTile - 1) / kTile * kTile;
+  x.jump = max(0, hi / kTile * kTile - x.at);
+}
+template <int KIND>
 __device__ __forceinline__ Request request_of(const KvAttnArgs& a, int r) {
   Request x;
+  x.lo = x.hi = x.at = x.jump = 0;
+  if constexpr (KIND == kPrefix) {  // checked by kv_shared_kernel, whose result is 0 for a group that is none
+    x.kv = __ldg(a.prefix + r);
+    x.q0 = x.n = 0;
+    if (x.kv <= 0) return x;
+    x.q0 = __ldg(a.cu_q + __ldg(a.starts + r));
+    const int n = __ldg(a.cu_q + __ldg(a.starts + r + 1)) - x.q0;
+    x.n = int64_t(n) * a.G <= a.split_rows ? n : 0;
+    return x;
+  }
   const int64_t b = __ldg(a.cu_q + r), e = __ldg(a.cu_q + r + 1);
   const int kv = __ldg(a.kv_lens + r);
   const int64_t most = int64_t(a.width) << a.c.page_shift;
@@ -183,14 +203,68 @@ __device__ __forceinline__ Request request_of(const KvAttnArgs& a, int r) {
   x.q0 = int(b);
   x.n = (e - b) * a.G <= a.split_rows ? int(e - b) : 0;
   x.kv = kv;
+  if constexpr (KIND == kWindow) {
+    const int lo = int(max(int64_t(0), int64_t(kv) - (e - b) - a.window + 1));  // of the first token
+    hide(x, min(a.sinks, lo), lo);
+  }
+  if constexpr (KIND == kTail) {
+    const int p = __ldg(a.prefix + r);  // negative: of a group that is none
+    if (p > 0 && e > b && kv - (e - b) < p) atomicOr(&g_status_kv_attn, DEV_BAD_INDEX);
+    if (p < 0 || kv - (e - b) < p) x.n = 0;
+    if (x.n > 0) hide(x, 0, p);
+  }
   return x;
 }
-__device__ __forceinline__ int tiles_of(const Request& x) { return max(1, (x.kv + kTile - 1) / kTile); }
+// Row of the block table whose keys the call's request r reads.
+template <int KIND>
+__device__ __forceinline__ int table_row(const KvAttnArgs& a, int r) {
+  return KIND == kPrefix ? __ldg(a.starts + r) : r;
+}
+__device__ __forceinline__ int tiles_of(const Request& x) { return max(1, (x.kv - x.jump + kTile - 1) / kTile); }
+
+// N = 4 or 8 channels from c of a finished row: `row` = token * Hq + head; m, l, o of the keys seen
+// here.  `behind`: the row's keys of its group's prefix, whose m, l, o another kernel has left.
+template <int KIND, int N>
+__device__ __forceinline__ void finish(const KvAttnArgs& a, int64_t token, int head, int c, float m, float l, float (&o)[N],
+                                       float vst, bool behind) {
+  const int64_t row = token * a.Hq + head;
+  if constexpr (KIND == kPrefix) {
+    float4* dst = reinterpret_cast<float4*>(a.prefix_o + row * 128 + c);
+#pragma unroll
+    for (int i = 0; i < N / 4; i++) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    if (c == 0) a.prefix_ml[row] = make_float2(m, l);
+    return;
+  }
+  if (KIND == kTail && behind) {
+    const float2 ml = a.prefix_ml[row];
+    const float4* src = reinterpret_cast<const float4*>(a.prefix_o + row * 128 + c);
+    const float top = fmaxf(m, ml.x);
+    const float w = m == -INFINITY ? 1.0f : ex2(m - top), u = ml.x == -INFINITY ? 1.0f : ex2(ml.x - top);
+    l = w * l + u * ml.y;
+    m = top;
+#pragma unroll
+    for (int i = 0; i < N / 4; i++) {
+      const float4 v = src[i];
+      o[4 * i] = w * o[4 * i] + u * v.x;
+      o[4 * i + 1] = w * o[4 * i + 1] + u * v.y;
+      o[4 * i + 2] = w * o[4 * i + 2] + u * v.z;
+      o[4 * i + 3] = w * o[4 * i + 3] + u * v.w;
+    }
+  }
+  const float f = l == 0.0f ? 1.0f : vst / l;
+  uint32_t p[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; i++) p[i] = pack_bf16(o[2 * i] * f, o[2 * i + 1] * f);
+  uint16_t* dst = a.o + row * 128 + c;
+  if constexpr (N == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(p[0], p[1], p[2], p[3]);
+  else *reinterpret_cast<uint2*>(dst) = make_uint2(p[0], p[1]);
+  if (c == 0) a.lse[int64_t(head) * a.total_q + token] = l == 0.0f ? -INFINITY : (m - kOffset + log2f(l)) * 0.6931471805599453f;
+}
 
 // Units of work (tiles, and kItemTiles for each item) of request r.
-template <int ROWS>
+template <int KIND, int ROWS>
 __device__ __forceinline__ int64_t request_units(const KvAttnArgs& a, int r) {
-  const Request x = request_of(a, r);
+  const Request x = request_of<KIND>(a, r);
   if (x.n == 0) return 0;
   return int64_t((x.n * a.G + ROWS - 1) / ROWS) * a.c.H * (tiles_of(x) + kItemTiles);
 }
@@ -217,7 +291,7 @@ __device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t* warp_sums, int64
 
 // One warp's softmax state and work on its keys of an item.  Lane (c, g) = (lane % 4,
 // lane / 4) holds query rows 8 t + 2 c, + 1 and of them channels 16 g .. 16 g + 15.
-template <int FMT, int NT>
+template <int KIND, int FMT, int NT>
 struct Worker {
   static constexpr int kSf = sf_bytes(FMT);
   uint32_t ring;        // this warp's stages
@@ -282,7 +356,12 @@ struct Worker {
   }
 
   // Scores, softmax and P V of the 32 keys in `stage`.  MASKED: `seen` has a bit per key
-  // of the step, and the row counts keys before limit[t][i], the first here being key0.
+  // of the step, and the row counts keys before limit[t][i], the first here being key0; of
+  // these with a window the sinks and the last `window`.
+  int window, sinks;
+  __device__ __forceinline__ bool sees(int key, int limit) const {
+    return key < limit && (KIND != kWindow || key >= limit - window || key < sinks);
+  }
   template <bool MASKED>
   __device__ __forceinline__ void compute(int stage, uint32_t qs, const float (&cs)[NT][2], uint32_t seen,
                                           const int (&limit)[NT][2], int key0) {
@@ -384,7 +463,7 @@ struct Worker {
           for (int t = 0; t < NT; t++)
 #pragma unroll
             for (int i = 0; i < 2; i++)
-              if (!there || key0 + key >= limit[t][i]) sc[t][u][2 * x + i] = -INFINITY;
+              if (!there || !sees(key0 + key, limit[t][i])) sc[t][u][2 * x + i] = -INFINITY;
         }
     }
     // a row's maximum moves only where a score passes it by more than kLazy (and
@@ -478,7 +557,7 @@ struct Worker {
         for (int t = 0; t < NT; t++)
 #pragma unroll
           for (int i = 0; i < 2; i++)
-            if (key0 + key < limit[t][i]) {
+            if (sees(key0 + key, limit[t][i])) {
 #pragma unroll
               for (int j = 0; j < 8; j++) acc[t][j][i] = acc[t][j][2 + i] = nan;
             }
@@ -493,10 +572,11 @@ struct Item {
   int r, rb, h, t0, nt, tiles;
   int q0, row0, rows;
   int n, kv;
+  int lo, hi, at, jump;  // as in Request
   int64_t last_unit;  // of the item, on the line
 };
 
-template <int FMT, int NT>
+template <int KIND, int FMT, int NT>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAttnArgs a) {
   constexpr int ROWS = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -523,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
     int64_t first_own = 0, first_upto = 0;  // of the first kThreads requests, the only ones most often
     for (int r0 = 0; r0 < a.R; r0 += kThreads) {
       int64_t sum;
-      const int64_t own = r0 + tid < a.R ? request_units<ROWS>(a, r0 + tid) : 0;
+      const int64_t own = r0 + tid < a.R ? request_units<KIND, ROWS>(a, r0 + tid) : 0;
       const int64_t upto = cta_scan(own, s_scan, sum);
       if (r0 == 0) {
         first_own = own;
@@ -541,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
     for (int r0 = 0; r0 < a.R; r0 += kThreads) {
       int64_t sum = total, own = first_own, upto = first_upto;
       if (a.R > kThreads) {
-        own = r0 + tid < a.R ? request_units<ROWS>(a, r0 + tid) : 0;
+        own = r0 + tid < a.R ? request_units<KIND, ROWS>(a, r0 + tid) : 0;
         upto = before + cta_scan(own, s_scan, sum);
       }
       if (upto - own <= pos && pos < upto) {
@@ -560,9 +640,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
   auto next = [&](Item& it) -> bool {
     while (pos < end && r < a.R) {
       if (a.whole) r = int(pos / a.c.H);
-      const Request x = request_of(a, r);
+      const Request x = request_of<KIND>(a, r);
       it.tiles = tiles_of(x);
       it.q0 = x.q0, it.n = x.n, it.kv = x.kv;
+      it.lo = x.lo, it.hi = x.hi, it.at = x.at, it.jump = x.jump;
       if (a.whole) {
         it.rb = 0, it.h = int(pos - int64_t(r) * a.c.H);
         it.t0 = 0, it.nt = x.n == 0 ? 0 : it.tiles;
@@ -594,7 +675,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
     return false;
   };
 
-  Worker<FMT, NT> wk;
+  Worker<KIND, FMT, NT> wk;
+  wk.window = a.window, wk.sinks = a.sinks;
   wk.ring = smem_u32(smem) + warp * kStages * stage_bytes(FMT);
   wk.lane = lane;
   wk.c = lane & 3;
@@ -607,19 +689,31 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
 
   // copies of the current item: the blocks of the lane's two keys of a step, looked
   // up one step ahead
-  int k_lo, k_end, steps;
+  int k_lo, k_end, steps;  // kWindow, kTail: places on the line, which leaves `jump` keys out at `jump_at`
+  int jump_at = 0, jump = 0, hide_lo = 0, hide_hi = 0;
+  constexpr bool kHides = KIND == kWindow || KIND == kTail;
+  auto key_at = [&](int place) { return kHides && place >= jump_at ? place + jump : place; };
+  auto in_sight = [&](int place) {
+    if (!kHides) return place < k_end;
+    const int key = key_at(place);
+    return place < k_end && (key < hide_lo || key >= hide_hi);
+  };
   const int32_t* table;
   uint32_t b0 = 0, b1 = 0;
   auto look_up = [&](int step, uint32_t& b0, uint32_t& b1) {
-    const int key = k_lo + (lane >> 1) + step * kTile;
-    b0 = key < k_end ? uint32_t(__ldg(table + (key >> a.c.page_shift))) : 0xFFFFFFFFu;
-    if (small_pages) b1 = key + 16 < k_end ? uint32_t(__ldg(table + (key >> 4) + 1)) : 0xFFFFFFFFu;
-    else b1 = key + 16 < k_end ? b0 : 0xFFFFFFFFu;
+    const int place = k_lo + (lane >> 1) + step * kTile, key = key_at(place);
+    const bool second = in_sight(place + 16);
+    // where keys are hidden, a block of both passes may have only the second one's key in sight
+    const bool first = in_sight(place) || (kHides && !small_pages && second);
+    b0 = first ? uint32_t(__ldg(table + (key >> a.c.page_shift))) : 0xFFFFFFFFu;
+    if (small_pages) b1 = second ? uint32_t(__ldg(table + (key >> 4) + 1)) : 0xFFFFFFFFu;
+    else b1 = second ? b0 : 0xFFFFFFFFu;
   };
   // starts the copies of a step and returns a bit per visible key; rows that are none
   // (past the last key, or of a block outside the cache) bring some other row, unseen
   auto issue = [&](int step, int st) -> uint32_t {
-    const bool live0 = b0 <= last_block, live1 = b1 <= last_block;
+    const int place = k_lo + (lane >> 1) + step * kTile;
+    const bool live0 = b0 <= last_block && (!kHides || in_sight(place)), live1 = b1 <= last_block;
     wk.copy(st, small_pages, min(b0, last_block), min(b1, last_block));
     cp_commit();
     uint32_t seen = 0xFFFFFFFFu;
@@ -627,8 +721,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
       // lanes 2k and 2k + 1 speak for keys k and 16 + k
       const uint32_t v0 = __ballot_sync(0xFFFFFFFFu, live0), v1 = __ballot_sync(0xFFFFFFFFu, live1);
       seen = __ballot_sync(0xFFFFFFFFu, ((lane < 16 ? v0 : v1) >> (2 * (lane & 15))) & 1u);
-      const int key = k_lo + (lane >> 1) + step * kTile;
-      if ((!live0 && key < k_end) || (!live1 && key + 16 < k_end)) atomicOr(&g_status_kv_attn, DEV_BAD_INDEX);
+      if ((!live0 && in_sight(place)) || (!live1 && in_sight(place + 16))) atomicOr(&g_status_kv_attn, DEV_BAD_INDEX);
     }
     return seen;
   };
@@ -641,9 +734,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
     const int last_tok = (it.row0 + it.rows - 1) / a.G;
     const int keys = a.causal ? max(0, it.kv - it.n + last_tok + 1) : it.kv;  // that some row sees
     k_lo = it.t0 * kTile + warp * kStep;
-    k_end = min((it.t0 + it.nt) * kTile, keys);
+    if (kHides) {
+      jump_at = it.at, jump = it.jump, hide_lo = it.lo, hide_hi = it.hi;
+      k_end = min((it.t0 + it.nt) * kTile, keys - jump);  // the last key is behind the hidden ones
+    } else {
+      k_end = min((it.t0 + it.nt) * kTile, keys);
+    }
     steps = k_lo < k_end ? (k_end - k_lo + kTile - 1) / kTile : 0;
-    table = a.table + int64_t(it.r) * a.width;
+    table = a.table + int64_t(table_row<KIND>(a, it.r)) * a.width;
     wk.aim(a.c, k_lo, it.h);
     // the first three steps' blocks at once, or each would be waited for
     uint32_t e0[3], e1[3];
@@ -712,8 +810,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
         const int row = t * 8 + 2 * wk.c + i;
         cs[t][i] = s_cs[row];
         lim[t][i] = !a.causal || row >= it.rows ? it.kv : it.kv - it.n + (it.row0 + row) / a.G + 1;
+        if (KIND == kWindow) lim[t][i] = max(lim[t][i], 0);
       }
     const int all_see = a.causal ? it.kv - it.n + it.row0 / a.G + 1 : it.kv;  // keys that every row sees
+    // and with a window from here on
+    const int all_from = KIND == kWindow ? max(0, it.kv - it.n + (it.row0 + it.rows - 1) / a.G + 1) - a.window : 0;
     wk.clear();
     const uint32_t qs = smem_u32(s_q);
     if (NT == 1) {
@@ -735,8 +836,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
       }
       cp_wait<kStages - 1>();
       __syncwarp();
-      const int key0 = k_lo + step * kTile;
-      if (seen0 != 0xFFFFFFFFu || key0 + kStep > all_see) wk.template compute<true>(stage, qs, cs, seen0, lim, key0);
+      const int key0 = key_at(k_lo + step * kTile);
+      const bool behind = KIND == kWindow && key0 < all_from && key0 + kStep > a.sinks;
+      if (seen0 != 0xFFFFFFFFu || key0 + kStep > all_see || behind) wk.template compute<true>(stage, qs, cs, seen0, lim, key0);
       else wk.template compute<false>(stage, qs, cs, seen0, lim, key0);
       seen0 = seen1;
       seen1 = seen2;
@@ -813,13 +915,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
           }
         } else {
           const int rr = cur.row0 + frow, tok = rr / a.G, hd = cur.h * a.G + rr - tok * a.G;
-          const float f = L == 0.0f ? 1.0f : vst / L;
-          *reinterpret_cast<uint4*>(a.o + (int64_t(cur.q0 + tok) * a.Hq + hd) * 128 + quad * 4) =
-              make_uint4(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f), pack_bf16(o[4] * f, o[5] * f),
-                         pack_bf16(o[6] * f, o[7] * f));
-          if (quad == 0)
-            a.lse[int64_t(hd) * a.total_q + cur.q0 + tok] =
-                L == 0.0f ? -INFINITY : (M - kOffset + log2f(L)) * 0.6931471805599453f;
+          finish<KIND, 8>(a, cur.q0 + tok, hd, quad * 4, M, L, o, vst, cur.hi > 0);
         }
       }
     }
@@ -839,7 +935,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
 // Joins the parts of the item that begins in CTA blockIdx.x's run and ends behind
 // it.  Two warps per row, four channels a lane: one takes the first half of the parts and
 // one the second, each in the order of the keys.
-template <int FMT, int NT>
+template <int KIND, int FMT, int NT>
 __global__ void __launch_bounds__(256) kv_join_kernel(KvAttnArgs a, int ctas) {
   __shared__ float4 s_o[4][32];
   __shared__ float s_l[4];
@@ -849,7 +945,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(KvAttnArgs a, int ctas) {
   const Partial<NT>* partials = reinterpret_cast<const Partial<NT>*>(a.ws + header_bytes(ctas));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp >> 2;
   const int row = blockIdx.y * 4 + (warp & 3);
-  const Request x = request_of(a, hd.r);
+  const Request x = request_of<KIND>(a, hd.r);
   const int rr = hd.rb * 8 * NT + row;
   const bool live = rr < x.n * a.G;
   auto part = [&](int i) -> const Partial<NT>& { return partials[2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)]; };
@@ -882,13 +978,9 @@ __global__ void __launch_bounds__(256) kv_join_kernel(KvAttnArgs a, int ctas) {
   const float4 v = s_o[warp][lane];
   L += s_l[warp];
   const float vst = FMT == 1 ? __ldg(a.c.v_scale) : 1.0f;
-  const float f = L == 0.0f ? 1.0f : vst / L;
   const int tok = rr / a.G, head = hd.h * a.G + rr - tok * a.G;
-  *reinterpret_cast<uint2*>(a.o + (int64_t(x.q0 + tok) * a.Hq + head) * 128 + lane * 4) =
-      make_uint2(pack_bf16((s.x + v.x) * f, (s.y + v.y) * f), pack_bf16((s.z + v.z) * f, (s.w + v.w) * f));
-  if (lane == 0)
-    a.lse[int64_t(head) * a.total_q + x.q0 + tok] =
-        L == 0.0f ? -INFINITY : (M - kOffset + log2f(L)) * 0.6931471805599453f;
+  float o[4] = {s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w};
+  finish<KIND, 4>(a, x.q0 + tok, head, lane * 4, M, L, o, vst, x.hi > 0);
 }
 
 // Tiles of eight query rows in a block: as few blocks of at most 32 rows as there
@@ -906,12 +998,12 @@ size_t workspace(int sms) {
 }
 
 // `line_ws`: the prompts' workspace, whose line is made beside kv_attn_kernel; NULL: no prompts.
-template <int FMT, int NT>
+template <int KIND, int FMT, int NT>
 cudaError_t launch(const KvAttnArgs& a, uint8_t* line_ws, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   constexpr int bytes = smem_bytes(FMT, NT);
   cudaError_t e = once_per_device(done, [] {
-    return cudaFuncSetAttribute(kv_attn_kernel<FMT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    return cudaFuncSetAttribute(kv_attn_kernel<KIND, FMT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   });
   if (e != cudaSuccess) return e;
   const int ctas = sm_count_current_device() * ctas_per_sm(NT);
@@ -919,13 +1011,13 @@ cudaError_t launch(const KvAttnArgs& a, uint8_t* line_ws, cudaStream_t st) {
   if (a.whole) {
     const int64_t items = int64_t(a.R) * a.c.H;
     const int64_t most = int64_t(ctas) * 16;
-    kv_attn_kernel<FMT, NT><<<unsigned(items < most ? items : most), kThreads, bytes, st>>>(a);
+    kv_attn_kernel<KIND, FMT, NT><<<unsigned(items < most ? items : most), kThreads, bytes, st>>>(a);
     return cudaGetLastError();
   }
-  kv_attn_kernel<FMT, NT><<<ctas, kThreads, bytes, st>>>(a);
+  kv_attn_kernel<KIND, FMT, NT><<<ctas, kThreads, bytes, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (line_ws && (e = launch_kv_prefill_line(a, line_ws, true, st)) != cudaSuccess) return e;
+  if (line_ws && (e = launch_kv_prefill_line(KIND, a, line_ws, true, st)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas), 2 * NT);
   cfg.blockDim = dim3(256);
@@ -935,16 +1027,29 @@ cudaError_t launch(const KvAttnArgs& a, uint8_t* line_ws, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_join_kernel<FMT, NT>, a, ctas);
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<KIND, FMT, NT>, a, ctas);
 }
 
-template <int FMT>
+template <int KIND, int FMT>
 cudaError_t launch_fmt(const KvAttnArgs& a, int nt, uint8_t* line_ws, cudaStream_t st) {
   switch (nt) {
-    case 1: return launch<FMT, 1>(a, line_ws, st);
-    case 2: return launch<FMT, 2>(a, line_ws, st);
-    case 3: return launch<FMT, 3>(a, line_ws, st);
-    default: return launch<FMT, 4>(a, line_ws, st);
+    case 1: return launch<KIND, FMT, 1>(a, line_ws, st);
+    case 2: return launch<KIND, FMT, 2>(a, line_ws, st);
+    case 3: return launch<KIND, FMT, 3>(a, line_ws, st);
+    default: return launch<KIND, FMT, 4>(a, line_ws, st);
+  }
+}
+
+cudaError_t launch_kind(int kind, const KvAttnArgs& a, int nt, uint8_t* line_ws, cudaStream_t st) {
+  switch (kind * 2 + (a.c.fmt == 0 ? 0 : 1)) {
+    case kAll * 2: return launch_fmt<kAll, 0>(a, nt, line_ws, st);
+    case kAll * 2 + 1: return launch_fmt<kAll, 1>(a, nt, line_ws, st);
+    case kWindow * 2: return launch_fmt<kWindow, 0>(a, nt, line_ws, st);
+    case kWindow * 2 + 1: return launch_fmt<kWindow, 1>(a, nt, line_ws, st);
+    case kPrefix * 2: return launch_fmt<kPrefix, 0>(a, nt, line_ws, st);
+    case kPrefix * 2 + 1: return launch_fmt<kPrefix, 1>(a, nt, line_ws, st);
+    case kTail * 2: return launch_fmt<kTail, 0>(a, nt, line_ws, st);
+    default: return launch_fmt<kTail, 1>(a, nt, line_ws, st);
   }
 }
 
@@ -987,6 +1092,13 @@ bool kv_attn_reaches(int max_q, int64_t max_k, int G) {
   return !kva::plan_of(max_q, max_k, G).prefill || max_k <= (int64_t(1) << 25);
 }
 
+// The most keys of a context that a row can see, and those its tiles hold beside them.
+int64_t kv_window_reach(int max_q, int64_t max_k, int window, int sinks) {
+  const int64_t tile = kva::kTile, sunk = (sinks + tile - 1) / tile * tile;
+  const int64_t most = sunk + (int64_t(window) + max_q + 2 * tile - 3) / tile * tile;
+  return most < max_k ? most : max_k;
+}
+
 size_t kv_attn_workspace(int R, int max_q, int64_t max_k, int G) {
   const kva::Plan p = kva::plan_of(max_q, max_k, G);
   if (p.whole) return 0;
@@ -994,20 +1106,86 @@ size_t kv_attn_workspace(int R, int max_q, int64_t max_k, int G) {
   return p.prefill ? few + kv_prefill_workspace(R) : few;
 }
 
-cudaError_t launch_kv_attn(const KvAttnArgs& args, cudaStream_t st) {
+cudaError_t launch_kv_attn(int kind, const KvAttnArgs& args, cudaStream_t st) {
   clear_stale_error();
   KvAttnArgs a = args;
   // no request has more keys than a row of its table
-  const kva::Plan p = kva::plan_of(a.max_q, int64_t(a.width) << a.c.page_shift, a.G);
+  int64_t max_k = int64_t(a.width) << a.c.page_shift;
+  if (kind == kWindow) max_k = kv_window_reach(a.max_q, max_k, a.window, a.sinks);
+  const kva::Plan p = kva::plan_of(a.max_q, max_k, a.G);
   a.split_rows = p.split_rows;
   a.whole = p.whole;
   uint8_t* const line_ws = p.prefill ? a.ws + ((kva::workspace_of(p.nt) + 255) & ~size_t(255)) : nullptr;
   cudaError_t e;
-  if (!p.prefill || a.G <= kva::kMixedRows)
-    e = a.c.fmt == 0 ? kva::launch_fmt<0>(a, p.nt, line_ws, st) : kva::launch_fmt<1>(a, p.nt, line_ws, st);
-  else
-    e = launch_kv_prefill_line(a, line_ws, false, st);
-  return e != cudaSuccess || !p.prefill ? e : launch_kv_prefill(a, line_ws, st);
+  if (!p.prefill || a.G <= kva::kMixedRows) e = kva::launch_kind(kind, a, p.nt, line_ws, st);
+  else e = launch_kv_prefill_line(kind, a, line_ws, false, st);
+  return e != cudaSuccess || !p.prefill ? e : launch_kv_prefill(kind, a, line_ws, st);
+}
+
+// The prefixes of a call's groups, checked: of group g at gpre[g] (0: none, or not as documented), and of
+// each request at pre[r] (-1: of a group not as documented; 0 for a request of no group).
+__global__ void __launch_bounds__(256) kv_shared_kernel(KvAttnArgs a, const int32_t* prefix_lens, int groups, int max_rows, int32_t* gpre,
+                                                        int32_t* pre) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  auto checked = [&](int g) -> int {  // -1: not as documented
+    const int s = __ldg(a.starts + g), e = __ldg(a.starts + g + 1), p = __ldg(prefix_lens + g);
+    if (s < 0 || e < s || e > a.R || p < 0 || p > int64_t(a.width) << a.c.page_shift) return -1;
+    const int b = __ldg(a.cu_q + s), t = __ldg(a.cu_q + e);
+    return b < 0 || t < b || t > a.total_q || t - b > max_rows ? -1 : s == e ? 0 : p;
+  };
+  if (i < groups) {
+    const int p = checked(i);
+    if (p < 0) atomicOr(&g_status_kv_attn, DEV_BAD_INDEX);
+    gpre[i] = max(p, 0);
+  }
+  if (i < a.R) {
+    int lo = 0, hi = groups;  // the group with starts[lo] <= i < starts[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(a.starts + mid) <= i) lo = mid;
+      else hi = mid;
+    }
+    const bool in = __ldg(a.starts + lo) <= i && i < __ldg(a.starts + lo + 1);
+    pre[i] = in ? checked(lo) : 0;
+  }
+}
+
+// Workspace of a call over shared prefixes: rows' partial results of their prefixes, checked prefixes, and the
+// larger of the two passes' own.
+KvSharedWs kv_shared_workspace(int R, int groups, int64_t total_q, int max_q, int max_group_q, int64_t max_k, int Hq, int G) {
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  KvSharedWs w;
+  w.ml = up(size_t(total_q) * size_t(Hq) * 512);
+  w.gpre = w.ml + up(size_t(total_q) * size_t(Hq) * 8);
+  w.pre = w.gpre + up(size_t(groups) * 4);
+  w.pass = w.pre + up(size_t(R) * 4);
+  const size_t first = kv_attn_workspace(groups, max_group_q, max_k, G), second = kv_attn_workspace(R, max_q, max_k, G);
+  w.bytes = w.pass + (first > second ? first : second);
+  return w;
+}
+
+cudaError_t launch_kv_attn_shared(const KvAttnArgs& args, const int32_t* prefix_lens, int groups, int max_group_q, cudaStream_t st) {
+  clear_stale_error();
+  KvAttnArgs a = args;
+  const KvSharedWs w = kv_shared_workspace(a.R, groups, a.total_q, a.max_q, max_group_q, int64_t(a.width) << a.c.page_shift, a.Hq, a.G);
+  int32_t* const gpre = reinterpret_cast<int32_t*>(a.ws + w.gpre);
+  int32_t* const pre = reinterpret_cast<int32_t*>(a.ws + w.pre);
+  a.prefix_o = reinterpret_cast<float*>(a.ws);
+  a.prefix_ml = reinterpret_cast<float2*>(a.ws + w.ml);
+  const int most = a.R > groups ? a.R : groups;
+  kv_shared_kernel<<<unsigned((most + 255) / 256), 256, 0, st>>>(a, prefix_lens, groups, max_group_q, gpre, pre);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  a.ws += w.pass;
+  KvAttnArgs first = a;  // the groups as requests, whose keys are the prefixes
+  first.R = groups;
+  first.max_q = max_group_q;
+  first.causal = 0;
+  first.prefix = gpre;
+  if ((e = launch_kv_attn(kPrefix, first, st)) != cudaSuccess) return e;
+  a.causal = 1;
+  a.prefix = pre;
+  return launch_kv_attn(kTail, a, st);
 }
 
 unsigned read_status_kv_attn(cudaStream_t st) {

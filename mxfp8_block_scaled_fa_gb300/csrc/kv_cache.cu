@@ -16,9 +16,7 @@
 // it reads back as NaN.
 #include <cooperative_groups.h>
 
-#include "kv_fp4.cuh"
-#include "mx_ptx.cuh"
-#include "mxfa_internal.h"
+#include "kv_rows.cuh"
 
 namespace mxfa {
 
@@ -273,24 +271,6 @@ cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t st) {
 // and 38 us (4.7 and 4.5 TB/s); a plain elementwise kernel that moves as many bytes
 // takes 29 us (5.9 TB/s).  A token's rows in a page are 64 bytes each, a page of
 // one head apart.
-__device__ __forceinline__ uint32_t pack8_e2m1(const float* y) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-      "mov.b32 %0, {a, b, c, d};\n\t}"
-      : "=r"(r)
-      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
-  return r;
-}
-
-// Sixteen bytes that nothing reads again soon.
-__device__ __forceinline__ uint4 ldg_stream(const uint4* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-
 // Where row `r` of the call (token, head, K or V) lives in the cache; false if
 // its slot is negative or out of range.
 struct KvRow {
@@ -336,44 +316,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvRowsArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < N; i++) {
-    const uint32_t m2 = __vmaxu2(__vmaxu2(abs2(x[i].x), abs2(x[i].y)), __vmaxu2(abs2(x[i].z), abs2(x[i].w)));
-    uint32_t mx = hmax2(m2);
-    mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-    if (FMT == 0) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-    if (!live[i]) continue;
-    const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    float y[8];
-    uint32_t sc;
-    const bool bad = mx >= 0x7F80u;
-    if (FMT == 0) {
-      // bf16 exponent field - 2, clamped to the fields of 2^-23 and 2^13
-      sc = min(max(int(mx >> 7) - 2, 104), 140);
-      const float f = __uint_as_float((254u - sc) << 23);
-#pragma unroll
-      for (int e = 0; e < 4; e++) {
-        y[2 * e] = bf_lo(xs[e]) * f;
-        y[2 * e + 1] = bf_hi(xs[e]) * f;
-      }
-      if (bad) sc = 0xFFu;
-    } else {
-      const float st = __ldg(w[i].is_v ? a.c.v_scale : a.c.k_scale);
-      sc = cvt_e4m3x2(__fdiv_rn(__uint_as_float(mx << 16), __fmul_rn(6.0f, st)), 0.0f) & 0xFFu;
-      const float unit = __fmul_rn(e4m3x2_to_float2(sc).x, st);
-#pragma unroll
-      for (int e = 0; e < 4; e++) {
-        y[2 * e] = unit > 0.0f ? __fdiv_rn(bf_lo(xs[e]), unit) : 0.0f;
-        y[2 * e + 1] = unit > 0.0f ? __fdiv_rn(bf_hi(xs[e]), unit) : 0.0f;
-      }
-      if (bad) sc = 0x7Fu;
-    }
-    uint8_t* codes = w[i].is_v ? a.c.v : a.c.k;
-    uint8_t* sf = w[i].is_v ? a.c.v_sf : a.c.k_sf;
-    reinterpret_cast<uint32_t*>(codes + w[i].at * 64)[lane] = bad ? 0u : pack8_e2m1(y);
-    if (FMT == 0) {
-      if ((lane & 3) == 0) sf[w[i].at * 4 + (lane >> 2)] = uint8_t(sc);
-    } else {
-      if ((lane & 1) == 0) sf[w[i].at * 8 + (lane >> 1)] = uint8_t(sc);
-    }
+    kv_store_row<FMT>(a.c, live[i], w[i].is_v, w[i].at, lane, x[i]);
   }
 }
 

@@ -1,0 +1,283 @@
+// kv_pages.cu -- pages of the 4-bit cache that several requests share: forking a request's
+// pages, copying blocks, and giving pages back to the ring of free blocks.
+//
+// refs[b] counts the owners of block b beside the first: kv_plan's blocks have 0.
+//   fork   request d gets the first c tokens of request s: each whole page has one owner more; a last page
+//          that is not full is written again by both, so d gets a new block for it (the k-th such fork the
+//          k-th free block) and the pair (old, new) is a block to copy, layer by layer
+//   free   each page given up has one owner fewer; blocks without an owner go to the ring, in ascending order
+// Counts change by whole-number atomics, so no result depends on timing: which of a block's owners comes last
+// is not seen, as blocks are collected by looking at the counts afterwards.
+#include <cooperative_groups.h>
+
+#include "kv_fp4.cuh"
+#include "mx_ptx.cuh"
+#include "mxfa_internal.h"
+
+namespace mxfa {
+
+static __device__ unsigned g_status_kv_pages;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kSegment = 2048;  // table entries of a CTA
+constexpr int kScan = 1024;     // threads of a CTA that collects
+constexpr int kCluster = 8;
+
+struct Fork {
+  int src, dst, whole;
+  bool part;   // a last page that is not full
+};
+__device__ __forceinline__ bool fork_of(const KvForkArgs& a, int f, Fork& x) {
+  x.src = __ldg(a.src + f), x.dst = __ldg(a.dst + f);
+  const int len = __ldg(a.lens + f);
+  x.whole = 0;
+  x.part = false;
+  if (x.src < 0 || x.src >= a.R || x.dst < 0 || x.dst >= a.R || x.src == x.dst || len < 0 || len > int64_t(a.width) << a.page_shift) return false;
+  x.whole = len >> a.page_shift;
+  x.part = (len & ((1 << a.page_shift) - 1)) != 0;
+  return true;
+}
+
+// Forks before f that need a block; all threads of the CTA.
+__device__ __forceinline__ int parts_before(const KvForkArgs& a, int f, int* s_sum) {
+  int n = 0;
+  for (int i = threadIdx.x; i < f; i += kThreads) {
+    Fork x;
+    n += fork_of(a, i, x) && x.part;
+  }
+  n = __reduce_add_sync(0xFFFFFFFFu, n);
+  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = n;
+  __syncthreads();
+  n = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; w++) n += s_sum[w];
+  return n;
+}
+
+__device__ __forceinline__ int64_t in_ring(int64_t i, int64_t size) { return (i % size + size) % size; }
+
+// One fork and kSegment entries of its row a CTA; the CTA with the last page looks for a block.
+__global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvForkArgs a) {
+  __shared__ int s_sum[kThreads / 32];
+  const int f = blockIdx.x, j0 = blockIdx.y * kSegment;
+  Fork x;
+  x.src = x.dst = x.whole = 0;
+  x.part = false;
+  const bool good = f < a.F && fork_of(a, f, x);
+  if (good) {
+    const int32_t* from = a.table + int64_t(x.src) * a.width;
+    int32_t* to = a.table + int64_t(x.dst) * a.width;
+    const int end = min(x.whole, j0 + kSegment);
+    for (int j = j0 + threadIdx.x; j < end; j += kThreads) {
+      int32_t b = from[j];
+      if (b < 0 || b >= a.blocks) {
+        atomicOr(&g_status_kv_pages, DEV_BAD_INDEX);
+        b = -1;
+      } else {
+        atomicAdd(a.refs + b, 1);
+      }
+      to[j] = b;
+    }
+  }
+  if (blockIdx.y != 0) return;
+  const bool last = f + 1 >= a.F;
+  if (f < a.F && !good && threadIdx.x == 0) atomicOr(&g_status_kv_pages, DEV_BAD_INDEX);
+  const int64_t head = a.ring_in[0], tail = a.ring_in[1];
+  const int64_t room = tail - head;
+  const int64_t avail = room < 0 ? 0 : room < a.ring_size ? room : a.ring_size;
+  int rank = 0;
+  if (x.part || last) rank = parts_before(a, min(f, a.F), s_sum);
+  if (threadIdx.x != 0) return;
+  if (f < a.F) {
+    int32_t old = -1, fresh = -1;
+    int len = good ? __ldg(a.lens + f) : 0;
+    if (x.part) {
+      if (rank < avail) {
+        old = a.table[int64_t(x.src) * a.width + x.whole];
+        fresh = a.ring[in_ring(head + rank, a.ring_size)];
+        if (old < 0 || old >= a.blocks || fresh < 0 || fresh >= a.blocks) {
+          atomicOr(&g_status_kv_pages, DEV_BAD_INDEX);
+          old = fresh = -1;
+        }
+      }
+      if (fresh < 0) len = x.whole << a.page_shift;
+      a.table[int64_t(x.dst) * a.width + x.whole] = fresh;
+    }
+    a.from_blocks[f] = old;
+    a.to_blocks[f] = fresh;
+    a.lens_out[f] = len;
+  }
+  if (last && a.ring_out) {
+    const int64_t want = rank + (x.part ? 1 : 0), took = want < avail ? want : avail;
+    a.ring_out[0] = head + took;
+    a.ring_out[1] = tail;
+    a.ring_out[2] = want - took;
+  }
+}
+
+// The ring's counters behind a fork that writes them in place.
+__global__ void __launch_bounds__(kThreads) kv_fork_ring_kernel(KvForkArgs a, int64_t* ring_out) {
+  __shared__ int s_sum[kThreads / 32];
+  const int64_t want = parts_before(a, a.F, s_sum);
+  if (threadIdx.x != 0) return;
+  const int64_t head = a.ring_in[0], tail = a.ring_in[1];
+  const int64_t room = tail - head;
+  const int64_t avail = room < 0 ? 0 : room < a.ring_size ? room : a.ring_size;
+  const int64_t took = want < avail ? want : avail;
+  ring_out[0] = head + took;
+  ring_out[1] = tail;
+  ring_out[2] = want - took;
+}
+
+// One owner fewer for the blocks of a range of pages.
+__global__ void __launch_bounds__(kThreads) kv_unref_kernel(KvFreeArgs a) {
+  const int f = blockIdx.x, j0 = blockIdx.y * kSegment;
+  const int r = __ldg(a.rows + f), first = __ldg(a.first + f), end = __ldg(a.end + f);
+  if (r < 0 || r >= a.R || first < 0 || end > a.width) {
+    if (blockIdx.y == 0 && threadIdx.x == 0) atomicOr(&g_status_kv_pages, DEV_BAD_INDEX);
+    return;
+  }
+  const int32_t* row = a.table + int64_t(r) * a.width;
+  const int stop = min(end, j0 + kSegment);
+  for (int j = max(first, j0) + threadIdx.x; j < stop; j += kThreads) {
+    const int32_t b = __ldg(row + j);
+    if (b >= a.blocks) atomicOr(&g_status_kv_pages, DEV_BAD_INDEX);
+    else if (b >= 0) atomicSub(a.refs + b, 1);
+  }
+}
+
+// Blocks whose count is negative, in ascending order, to the ring: one cluster, a run of blocks a CTA, a run
+// of it a warp step.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScan) kv_collect_kernel(KvFreeArgs a) {
+  namespace cg = cooperative_groups;
+  __shared__ int s_warp[kScan / 32];
+  __shared__ int s_total;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = int(cluster.block_rank());
+  const int64_t head = a.ring_in[0], tail = a.ring_in[1], lacked = a.ring_in[2];
+  // runs of whole warps' steps of 32 blocks: warp w of CTA c has steps [w, w + 1) * steps of its CTA's
+  const int64_t steps = (a.blocks + 31) / 32, warps = kCluster * (kScan / 32);
+  const int64_t per = (steps + warps - 1) / warps, mine = int64_t(rank) * (kScan / 32) + warp;
+  const int64_t s0 = min(steps, mine * per), s1 = min(steps, s0 + per);
+  int count = 0;
+  for (int64_t s = s0; s < s1; s++) {
+    const int64_t b = s * 32 + lane;
+    const int c = b < a.blocks ? a.refs[b] : 0;
+    if (c < -1) atomicOr(&g_status_kv_pages, DEV_BAD_INDEX);  // given up more often than owned
+    count += __popc(__ballot_sync(0xFFFFFFFFu, c < 0));
+  }
+  if (lane == 0) s_warp[warp] = count;
+  __syncthreads();
+  if (tid == 0) {
+    int t = 0;
+    for (int w = 0; w < kScan / 32; w++) t += s_warp[w];
+    s_total = t;
+  }
+  cluster.sync();
+  int64_t before = 0, total = 0;
+  for (int c = 0; c < kCluster; c++) {
+    const int t = *cluster.map_shared_rank(&s_total, c);
+    if (c < rank) before += t;
+    total += t;
+  }
+  for (int w = 0; w < warp; w++) before += s_warp[w];
+  for (int64_t s = s0; s < s1; s++) {
+    const int64_t b = s * 32 + lane;
+    const bool gone = b < a.blocks && a.refs[b] < 0;
+    const unsigned m = __ballot_sync(0xFFFFFFFFu, gone);
+    if (gone) {
+      a.ring[in_ring(tail + before + __popc(m & ((1u << lane) - 1u)), a.ring_size)] = int32_t(b);
+      a.refs[b] = 0;
+    }
+    before += __popc(m);
+  }
+  cluster.sync();  // every CTA has read the counters and the totals
+  if (rank == 0 && tid == 0) {
+    a.ring_out[0] = head;
+    a.ring_out[1] = tail + total;
+    a.ring_out[2] = lacked;
+  }
+}
+
+// Whole blocks: the codes and scales of all heads of one lie in one piece each.
+__global__ void __launch_bounds__(kThreads) kv_copy_kernel(KvPages c, const int32_t* from, const int32_t* to, int chunks, int code_words,
+                                                           int sf_words) {
+  constexpr int N = 4;
+  const int i = int(blockIdx.x) / chunks, chunk = int(blockIdx.x) - i * chunks;
+  const int32_t a = __ldg(from + i), b = __ldg(to + i);
+  if (a < 0 || b < 0 || a == b) return;
+  if (a >= c.blocks || b >= c.blocks) {
+    if (threadIdx.x == 0) atomicOr(&g_status_kv_pages, DEV_BAD_INDEX);
+    return;
+  }
+  uint4 v[N];
+  uint4* dst[N];
+#pragma unroll
+  for (int e = 0; e < N; e++) {
+    int w = (chunk * N + e) * kThreads + threadIdx.x;
+    const bool codes = w < 2 * code_words;
+    if (!codes) w -= 2 * code_words;
+    const int words = codes ? code_words : sf_words;
+    const bool second = w >= words;
+    if (second) w -= words;
+    dst[e] = nullptr;
+    if (w < words) {
+      uint4* p = reinterpret_cast<uint4*>(codes ? (second ? c.v : c.k) : (second ? c.v_sf : c.k_sf));
+      v[e] = p[int64_t(a) * words + w];
+      dst[e] = p + int64_t(b) * words + w;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < N; e++)
+    if (dst[e]) *dst[e] = v[e];
+}
+
+}  // namespace
+
+cudaError_t launch_kv_fork(const KvForkArgs& args, cudaStream_t st) {
+  clear_stale_error();
+  KvForkArgs a = args;
+  const bool in_place = a.ring_out == a.ring_in;
+  if (in_place) a.ring_out = nullptr;
+  const dim3 grid(unsigned(a.F > 0 ? a.F : 1), unsigned((a.width + kSegment - 1) / kSegment));
+  kv_fork_kernel<<<grid, kThreads, 0, st>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !in_place) return e;
+  kv_fork_ring_kernel<<<1, kThreads, 0, st>>>(a, args.ring_out);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_free(const KvFreeArgs& a, cudaStream_t st) {
+  clear_stale_error();
+  if (a.F > 0) {
+    kv_unref_kernel<<<dim3(unsigned(a.F), unsigned((a.width + kSegment - 1) / kSegment)), kThreads, 0, st>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  kv_collect_kernel<<<kCluster, kScan, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+int kv_copy_chunks(const KvPages& c) {
+  const int64_t words = 2 * (int64_t(c.H) * c.page * 4 + int64_t(c.H) * c.page / (c.fmt == 0 ? 4 : 2));
+  return int((words + 4 * kThreads - 1) / (4 * kThreads));
+}
+
+cudaError_t launch_kv_copy(const KvPages& c, const int32_t* from, const int32_t* to, int n, cudaStream_t st) {
+  clear_stale_error();
+  const int chunks = kv_copy_chunks(c);
+  kv_copy_kernel<<<unsigned(int64_t(n) * chunks), kThreads, 0, st>>>(c, from, to, chunks, c.H * c.page * 4, c.H * c.page / (c.fmt == 0 ? 4 : 2));
+  return cudaGetLastError();
+}
+
+unsigned read_status_kv_pages(cudaStream_t st) {
+  unsigned v = 0, z = 0;
+  cudaMemcpyFromSymbolAsync(&v, g_status_kv_pages, sizeof(v), 0, cudaMemcpyDeviceToHost, st);
+  cudaMemcpyToSymbolAsync(g_status_kv_pages, &z, sizeof(z), 0, cudaMemcpyHostToDevice, st);
+  cudaStreamSynchronize(st);
+  return v;
+}
+
+}  // namespace mxfa

@@ -90,7 +90,8 @@ struct Item {
   int q0, n, kv, t0;
   int na, nb;       // tiles of A and of B in this part
   int slot;         // -1: the whole item, else partial record
-  int pad[5];
+  int lo, hi, at, jump;  // as in Request
+  int pad;
 };
 static_assert(sizeof(Item) == 64, "an item record");
 
@@ -131,11 +132,30 @@ __device__ __forceinline__ float ex2(float x) {
 
 // A request whose rows belong here: more than a.split_rows of them, offsets and
 // lengths within their tables (a failed check leaves n = 0).
+// kWindow, kTail: keys lo .. hi - 1 are in no row's sight (of an item, as item_of() sets them); the tiles that hold
+// nothing else, `jump` keys of them from key `at` on, are left out of the item's tiles.
 struct Request {
   int q0, n, kv;
+  int lo, hi, at, jump;
 };
+__device__ __forceinline__ void hide(Request& x, int lo, int hi) {
+  x.lo = lo, x.hi = hi;
+  x.at = (lo + TILE - 1) / TILE * TILE;
+  x.jump = max(0, hi / TILE * TILE - x.at);
+}
+template <int KIND>
 __device__ __forceinline__ Request request_of(const KvAttnArgs& a, int r) {
   Request x;
+  x.lo = x.hi = x.at = x.jump = 0;
+  if constexpr (KIND == kPrefix) {  // checked by kv_shared_kernel, whose result is 0 for a group that is none
+    x.kv = __ldg(a.prefix + r);
+    x.q0 = x.n = 0;
+    if (x.kv <= 0) return x;
+    x.q0 = __ldg(a.cu_q + __ldg(a.starts + r));
+    const int n = __ldg(a.cu_q + __ldg(a.starts + r + 1)) - x.q0;
+    x.n = int64_t(n) * a.G > a.split_rows ? n : 0;
+    return x;
+  }
   const int64_t b = __ldg(a.cu_q + r), e = __ldg(a.cu_q + r + 1);
   const int kv = __ldg(a.kv_lens + r);
   const int64_t most = int64_t(a.width) << a.c.page_shift;
@@ -147,17 +167,32 @@ __device__ __forceinline__ Request request_of(const KvAttnArgs& a, int r) {
   x.q0 = int(b);
   x.n = (e - b) * a.G > a.split_rows ? int(e - b) : 0;
   x.kv = kv;
+  if constexpr (KIND == kTail) {
+    const int p = __ldg(a.prefix + r);  // negative: of a group that is none
+    if (p > 0 && e > b && kv - (e - b) < p) atomicOr(&g_status_kv_prefill, DEV_BAD_INDEX);
+    if (p < 0 || kv - (e - b) < p) x.n = 0;
+    if (x.n > 0) hide(x, 0, p);
+  }
   return x;
+}
+// What the item of rows row0 on leaves out.
+template <int KIND>
+__device__ __forceinline__ void item_of(const KvAttnArgs& a, Request& x, int row0) {
+  if constexpr (KIND == kWindow) {
+    const int lo = int(max(int64_t(0), int64_t(x.kv) - x.n + row0 / a.G - a.window + 1));
+    hide(x, min(a.sinks, lo), lo);
+  }
 }
 // Keys that the last of the rows before `row_end` sees.
 __device__ __forceinline__ int keys_of(const KvAttnArgs& a, const Request& x, int row_end) {
   return a.causal ? max(0, x.kv - x.n + (row_end - 1) / a.G + 1) : x.kv;
 }
 __device__ __forceinline__ int tiles_of(const KvAttnArgs& a, const Request& x, int row0) {
-  return max(1, (keys_of(a, x, min(row0 + ROWS, x.n * a.G)) + TILE - 1) / TILE);
+  return max(1, (keys_of(a, x, min(row0 + ROWS, x.n * a.G)) - x.jump + TILE - 1) / TILE);
 }
 
 // line[r] = units (tiles, and kItemTiles per item) of the requests before r.
+template <int KIND>
 __global__ void __launch_bounds__(512) kv_prefill_line_kernel(KvAttnArgs a, int64_t* line) {
   __shared__ int64_t s_sum[16];
   asm volatile("griddepcontrol.launch_dependents;");
@@ -167,8 +202,11 @@ __global__ void __launch_bounds__(512) kv_prefill_line_kernel(KvAttnArgs a, int6
     const int r = r0 + threadIdx.x;
     int64_t u = 0;
     if (r < a.R) {
-      const Request x = request_of(a, r);
-      for (int row0 = 0; row0 < x.n * a.G; row0 += ROWS) u += tiles_of(a, x, row0) + kItemTiles;
+      Request x = request_of<KIND>(a, r);
+      for (int row0 = 0; row0 < x.n * a.G; row0 += ROWS) {
+        item_of<KIND>(a, x, row0);
+        u += tiles_of(a, x, row0) + kItemTiles;
+      }
       u *= a.c.H;
     }
     int64_t v = u;
@@ -193,7 +231,7 @@ __global__ void __launch_bounds__(512) kv_prefill_line_kernel(KvAttnArgs a, int6
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-template <int FMT>
+template <int KIND, int FMT>
 __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_constant__ KvAttnArgs a, const int64_t* line,
                                                                  Header* headers, Partial* partials) {
   extern __shared__ uint8_t smem_raw[];
@@ -243,6 +281,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
     if (warp == 0) tmem_dealloc(tmem, 512);
     return;
   }
+  constexpr bool kHides = KIND == kWindow || KIND == kTail;
   const Item* items = reinterpret_cast<const Item*>(smem + OFF_ITEM);
   // whole warp: waits for item i of the run and reads it; a part with rows == 0 ends the run
   auto take = [&](int i, Item& it, bool& ok) {
@@ -253,6 +292,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       it.r = v->r, it.h = v->h, it.row0 = v->row0, it.rows = v->rows;
       it.q0 = v->q0, it.n = v->n, it.kv = v->kv, it.t0 = v->t0;
       it.na = v->na, it.nb = v->nb, it.slot = v->slot;
+      if (kHides) it.lo = v->lo, it.hi = v->hi, it.at = v->at, it.jump = v->jump;
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(BAR(B_IEMPTY + (i & 1)));
@@ -398,6 +438,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
         v->r = it.r, v->h = it.h, v->row0 = it.row0, v->rows = it.rows;
         v->q0 = it.q0, v->n = it.n, v->kv = it.kv, v->t0 = it.t0;
         v->na = it.na, v->nb = it.nb, v->slot = it.slot;
+        if (kHides) v->lo = it.lo, v->hi = it.hi, v->at = it.at, v->jump = it.jump;
         mbar_arrive(BAR(B_IFULL + (i & 1)));
         i++;
         return true;
@@ -409,7 +450,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
           r++;
           continue;
         }
-        const Request x = request_of(a, r);
+        Request x = request_of<KIND>(a, r);
         const int64_t per_head = (next_r - lr) / a.c.H;
         int h = int((pos - lr) / per_head);
         int64_t at = lr + h * per_head;  // start of the item that is looked at
@@ -421,6 +462,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
             h++;
             continue;
           }
+          item_of<KIND>(a, x, row0);
           const int tiles = tiles_of(a, x, row0), units = tiles + kItemTiles;
           if (pos >= at + units) {
             at += units;
@@ -435,8 +477,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
             it.r = r, it.h = h, it.row0 = row0;
             it.rows = min(ROWS, x.n * a.G - row0);
             it.q0 = x.q0, it.n = x.n, it.kv = x.kv, it.t0 = t0;
-            const int va = (keys_of(a, x, row0 + min(TILE, it.rows)) + TILE - 1) / TILE;
-            const int vb = it.rows > TILE ? (keys_of(a, x, row0 + it.rows) + TILE - 1) / TILE : 0;
+            it.lo = x.lo, it.hi = x.hi, it.at = x.at, it.jump = x.jump;
+            const int va = (keys_of(a, x, row0 + min(TILE, it.rows)) - x.jump + TILE - 1) / TILE;
+            const int vb = it.rows > TILE ? (keys_of(a, x, row0 + it.rows) - x.jump + TILE - 1) / TILE : 0;
             it.na = max(0, min(va, t1) - t0);
             it.nb = max(0, min(vb, t1) - t0);
             it.slot = t0 > 0 ? 2 * int(blockIdx.x) : t1 < tiles ? 2 * int(blockIdx.x) + 1 : -1;
@@ -455,6 +498,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       if (ok) {
         Item none;
         none.r = none.h = none.row0 = none.rows = none.q0 = none.n = none.kv = none.t0 = none.na = none.nb = none.slot = 0;
+        none.lo = none.hi = none.at = none.jump = 0;
         publish(none);
       }
     }
@@ -471,7 +515,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
     for (int i = 0; take(i, it, ok); i++) {
       const int nmax = max(it.na, it.nb);
       if (nmax == 0) continue;
-      const int32_t* table = a.table + int64_t(it.r) * a.width;
+      const int32_t* table = a.table + int64_t(KIND == kPrefix ? __ldg(a.starts + it.r) : it.r) * a.width;
       Request x;
       x.q0 = it.q0, x.n = it.n, x.kv = it.kv;
       const int keys = keys_of(a, x, it.row0 + it.rows);  // that some row sees
@@ -482,13 +526,18 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       uint2 ks, vs, next_vs;
       int64_t row;      // cache row of the tile's key, -1: none, -2: not in the cache
       int next_block;   // table entry of the next tile's key
+      auto key_of = [&](int j) {
+        const int place = (it.t0 + j) * TILE;
+        return (kHides && place >= it.at ? place + it.jump : place) + t;
+      };
+      auto in_sight = [&](int key) { return key < keys && (!kHides || key < it.lo || key >= it.hi); };
       auto entry = [&](int j) -> int {
-        const int key = (it.t0 + j) * TILE + t;
-        return j < nmax && key < keys ? __ldg(table + (key >> a.c.page_shift)) : -1;
+        const int key = key_of(j);
+        return j < nmax && in_sight(key) ? __ldg(table + (key >> a.c.page_shift)) : -1;
       };
       auto find = [&](int b, int j) -> int64_t {
-        const int key = (it.t0 + j) * TILE + t;
-        if (j >= nmax || key >= keys) return -1;
+        const int key = key_of(j);
+        if (j >= nmax || !in_sight(key)) return -1;
         if (b < 0 || b >= a.c.blocks) return -2;
         return (int64_t(b) * a.c.H + it.h) * a.c.page + (key & (a.c.page - 1));
       };
@@ -670,6 +719,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       const bool valid = idx < it.rows;
       const int tok = (it.row0 + idx) / a.G;
       const int klim = a.causal && valid ? it.kv - it.n + tok + 1 : it.kv;  // keys before it are visible
+      // but not from kgap to kfrom - 1
+      const int kgap = KIND == kWindow ? a.sinks : 0;
+      const int kfrom = KIND == kWindow ? max(klim, 0) - a.window : KIND == kTail ? it.hi : 0;
       float m = -INFINITY, l = 0.0f;
       const float cs = n_x > 0 ? s_cs[lane] : 0.0f;
       uint32_t nan_blocks = 0;
@@ -688,12 +740,20 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
         tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 2; c++) reg_fence32(reinterpret_cast<uint32_t*>(s) + 32 * c);
-        const int kbase = (it.t0 + j) * TILE + 64 * h;
+        int kbase = (it.t0 + j) * TILE;
+        if (kHides && kbase >= it.at) kbase += it.jump;
+        kbase += 64 * h;
         if (__any_sync(0xFFFFFFFFu, kbase + 64 > klim)) {
           const int lim = klim - kbase;
 #pragma unroll
           for (int e = 0; e < 64; e++)
             if (e >= lim) s[e] = -INFINITY;
+        }
+        if (kHides && __any_sync(0xFFFFFFFFu, kbase < kfrom && kbase + 64 > kgap)) {
+          const int from = kfrom - kbase, gap = kgap - kbase;
+#pragma unroll
+          for (int e = 0; e < 64; e++)
+            if (e < from && e >= gap) s[e] = -INFINITY;
         }
         if (flags) {  // the same for the whole CTA
           const volatile uint32_t* bad = reinterpret_cast<const volatile uint32_t*>(smem + OFF_BAD) + f4 * 4 + 2 * h;
@@ -706,7 +766,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
           }
           if (flags & 1u) {
             const volatile uint8_t* nb = smem + OFF_NAN + f4 * TILE + 64 * h;
-            for (int e = 0; e < 64 && kbase + e < klim; e++) nan_blocks |= nb[e];
+            for (int e = 0; e < 64 && kbase + e < klim; e++)
+              if (!kHides || kbase + e >= kfrom || kbase + e < kgap) nan_blocks |= nb[e];
           }
           __syncwarp();
         }
@@ -773,9 +834,22 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       tc_fence_after();
       const float nanv = __uint_as_float(0x7FC00000u);
       const int hd = it.h * a.G + (it.row0 + idx) - tok * a.G;
+      // where the row's prefix has been done for the group: its m, l, o join these
+      const int64_t out_row = int64_t(it.q0 + tok) * a.Hq + hd;
+      const bool behind = KIND == kTail && it.hi > 0 && valid && it.slot < 0;
+      float w = 1.0f, u = 0.0f;
+      if (behind) {
+        const float2 ml = a.prefix_ml[out_row];
+        const float top = fmaxf(m, ml.x);
+        w = m == -INFINITY ? 1.0f : ex2(m - top);
+        u = ml.x == -INFINITY ? 1.0f : ex2(ml.x - top);
+        l = w * l + u * ml.y;
+        m = top;
+      }
       const float f = l == 0.0f ? 1.0f : vst / l;
-      uint4* orow = reinterpret_cast<uint4*>(a.o + (int64_t(it.q0 + tok) * a.Hq + hd) * 128);
-      Partial* part = partials + (it.slot < 0 ? 0 : it.slot);
+      uint4* orow = reinterpret_cast<uint4*>(a.o + out_row * 128);
+      const float4* prow = reinterpret_cast<const float4*>(a.prefix_o + out_row * 128);
+      float* record = it.slot < 0 ? a.prefix_o + out_row * 128 : partials[it.slot].o[idx];  // kPrefix: there is always one
 #pragma unroll
       for (int c = 0; c < 4; c++) {
         float o[32];
@@ -793,24 +867,36 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
           for (int e = 0; e < 32; e++)
             if ((nan_blocks >> (2 * c + (e >> 4))) & 1u) o[e] = nanv;
         }
-        if (valid && it.slot < 0) {
+        if (behind) {
+#pragma unroll
+          for (int e = 0; e < 8; e++) {
+            const float4 v = prow[8 * c + e];
+            o[4 * e] = w * o[4 * e] + u * v.x;
+            o[4 * e + 1] = w * o[4 * e + 1] + u * v.y;
+            o[4 * e + 2] = w * o[4 * e + 2] + u * v.z;
+            o[4 * e + 3] = w * o[4 * e + 3] + u * v.w;
+          }
+        }
+        if (valid && it.slot < 0 && KIND != kPrefix) {
 #pragma unroll
           for (int e = 0; e < 4; e++)
             orow[4 * c + e] = make_uint4(pack_bf16(o[8 * e] * f, o[8 * e + 1] * f), pack_bf16(o[8 * e + 2] * f, o[8 * e + 3] * f),
                                          pack_bf16(o[8 * e + 4] * f, o[8 * e + 5] * f), pack_bf16(o[8 * e + 6] * f, o[8 * e + 7] * f));
         } else if (valid) {
-          float4* dst = reinterpret_cast<float4*>(part->o[idx]) + 8 * c;
+          float4* dst = reinterpret_cast<float4*>(record) + 8 * c;
 #pragma unroll
           for (int e = 0; e < 8; e++) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       }
       tc_fence_before();
       if (valid) {
-        if (it.slot < 0) {
-          a.lse[int64_t(hd) * a.total_q + it.q0 + tok] = l == 0.0f ? -INFINITY : (m - kOffset + log2f(l)) * 0.6931471805599453f;
+        if (it.slot >= 0) {
+          partials[it.slot].m[idx] = m;
+          partials[it.slot].l[idx] = l;
+        } else if (KIND == kPrefix) {
+          a.prefix_ml[out_row] = make_float2(m, l);
         } else {
-          part->m[idx] = m;
-          part->l[idx] = l;
+          a.lse[int64_t(hd) * a.total_q + it.q0 + tok] = l == 0.0f ? -INFINITY : (m - kOffset + log2f(l)) * 0.6931471805599453f;
         }
       }
       st += n_x;
@@ -827,13 +913,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
 
 // Joins the parts of the item that begins in CTA blockIdx.x's run and ends behind
 // it: one warp per row, four channels a lane, parts in the order of the keys.
-template <int FMT>
+template <int KIND, int FMT>
 __global__ void __launch_bounds__(256) kv_prefill_join_kernel(KvAttnArgs a, const Header* headers, const Partial* partials) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // for the end of kv_prefill_kernel
   const Header hd = headers[blockIdx.x];
   if (hd.parts == 0) return;
   const int idx = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const Request x = request_of(a, hd.r);
+  const Request x = request_of<KIND>(a, hd.r);
   if (hd.row0 + idx >= x.n * a.G) return;
   auto part = [&](int i) -> const Partial& { return partials[2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)]; };
   float M = -INFINITY;
@@ -855,10 +941,24 @@ __global__ void __launch_bounds__(256) kv_prefill_join_kernel(KvAttnArgs a, cons
     s.w += w * v.w;
   }
   const float vst = FMT == 1 ? __ldg(a.c.v_scale) : 1.0f;
-  const float f = L == 0.0f ? 1.0f : vst / L;
   const int rr = hd.row0 + idx, tok = rr / a.G, head = hd.h * a.G + rr - tok * a.G;
-  *reinterpret_cast<uint2*>(a.o + (int64_t(x.q0 + tok) * a.Hq + head) * 128 + lane * 4) =
-      make_uint2(pack_bf16(s.x * f, s.y * f), pack_bf16(s.z * f, s.w * f));
+  const int64_t row = int64_t(x.q0 + tok) * a.Hq + head;
+  if (KIND == kPrefix) {
+    reinterpret_cast<float4*>(a.prefix_o + row * 128)[lane] = s;
+    if (lane == 0) a.prefix_ml[row] = make_float2(M, L);
+    return;
+  }
+  if (KIND == kTail && x.hi > 0) {
+    const float2 ml = a.prefix_ml[row];
+    const float4 v = reinterpret_cast<const float4*>(a.prefix_o + row * 128)[lane];
+    const float top = fmaxf(M, ml.x);
+    const float w = M == -INFINITY ? 1.0f : ex2(M - top), u = ml.x == -INFINITY ? 1.0f : ex2(ml.x - top);
+    L = w * L + u * ml.y;
+    M = top;
+    s = make_float4(w * s.x + u * v.x, w * s.y + u * v.y, w * s.z + u * v.z, w * s.w + u * v.w);
+  }
+  const float f = L == 0.0f ? 1.0f : vst / L;
+  *reinterpret_cast<uint2*>(a.o + row * 128 + lane * 4) = make_uint2(pack_bf16(s.x * f, s.y * f), pack_bf16(s.z * f, s.w * f));
   if (lane == 0)
     a.lse[int64_t(head) * a.total_q + x.q0 + tok] =
         L == 0.0f ? -INFINITY : (M - kOffset + log2f(L)) * 0.6931471805599453f;
@@ -881,11 +981,11 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t sm
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
-template <int FMT>
+template <int KIND, int FMT>
 cudaError_t launch(const KvAttnArgs& a, uint8_t* ws, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = once_per_device(done, [] {
-    return cudaFuncSetAttribute(kv_prefill_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    return cudaFuncSetAttribute(kv_prefill_kernel<KIND, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   });
   if (e != cudaSuccess) return e;
   const int ctas = sm_count_current_device();
@@ -893,10 +993,10 @@ cudaError_t launch(const KvAttnArgs& a, uint8_t* ws, cudaStream_t st) {
   int64_t* line = reinterpret_cast<int64_t*>(ws);
   Header* headers = reinterpret_cast<Header*>(ws + line_bytes(a.R));
   Partial* partials = reinterpret_cast<Partial*>(ws + line_bytes(a.R) + header_bytes(ctas));
-  e = launch_early(kv_prefill_kernel<FMT>, dim3(unsigned(ctas)), NTHREADS, SMEM_BYTES, st, a, static_cast<const int64_t*>(line), headers,
+  e = launch_early(kv_prefill_kernel<KIND, FMT>, dim3(unsigned(ctas)), NTHREADS, SMEM_BYTES, st, a, static_cast<const int64_t*>(line), headers,
                    partials);
   if (e != cudaSuccess) return e;
-  return launch_early(kv_prefill_join_kernel<FMT>, dim3(unsigned(ctas), ROWS / 8), 256, 0, st, a, static_cast<const Header*>(headers),
+  return launch_early(kv_prefill_join_kernel<KIND, FMT>, dim3(unsigned(ctas), ROWS / 8), 256, 0, st, a, static_cast<const Header*>(headers),
                       static_cast<const Partial*>(partials));
 }
 
@@ -907,17 +1007,41 @@ size_t kv_prefill_workspace(int R) {
   return kvp::line_bytes(R) + kvp::header_bytes(ctas) + size_t(ctas) * 2 * sizeof(kvp::Partial);
 }
 
-// The places of the requests on the line; `after_attn`: beside kv_attn_kernel, which is
-// the launch before it.
-cudaError_t launch_kv_prefill_line(const KvAttnArgs& a, uint8_t* ws, bool after_attn, cudaStream_t st) {
-  int64_t* line = reinterpret_cast<int64_t*>(ws);
-  if (after_attn) return kvp::launch_early(kvp::kv_prefill_line_kernel, dim3(1), 512, 0, st, a, line);
-  kvp::kv_prefill_line_kernel<<<1, 512, 0, st>>>(a, line);
+namespace {
+
+template <int KIND>
+cudaError_t launch_line(const KvAttnArgs& a, int64_t* line, bool after_attn, cudaStream_t st) {
+  if (after_attn) return kvp::launch_early(kvp::kv_prefill_line_kernel<KIND>, dim3(1), 512, 0, st, a, line);
+  kvp::kv_prefill_line_kernel<KIND><<<1, 512, 0, st>>>(a, line);
   return cudaGetLastError();
 }
 
-cudaError_t launch_kv_prefill(const KvAttnArgs& a, uint8_t* ws, cudaStream_t st) {
-  return a.c.fmt == 0 ? kvp::launch<0>(a, ws, st) : kvp::launch<1>(a, ws, st);
+template <int KIND>
+cudaError_t launch_kind(const KvAttnArgs& a, uint8_t* ws, cudaStream_t st) {
+  return a.c.fmt == 0 ? kvp::launch<KIND, 0>(a, ws, st) : kvp::launch<KIND, 1>(a, ws, st);
+}
+
+}  // namespace
+
+// The places of the requests on the line; `after_attn`: beside kv_attn_kernel, which is
+// the launch before it.
+cudaError_t launch_kv_prefill_line(int kind, const KvAttnArgs& a, uint8_t* ws, bool after_attn, cudaStream_t st) {
+  int64_t* line = reinterpret_cast<int64_t*>(ws);
+  switch (kind) {
+    case kAll: return launch_line<kAll>(a, line, after_attn, st);
+    case kWindow: return launch_line<kWindow>(a, line, after_attn, st);
+    case kPrefix: return launch_line<kPrefix>(a, line, after_attn, st);
+    default: return launch_line<kTail>(a, line, after_attn, st);
+  }
+}
+
+cudaError_t launch_kv_prefill(int kind, const KvAttnArgs& a, uint8_t* ws, cudaStream_t st) {
+  switch (kind) {
+    case kAll: return launch_kind<kAll>(a, ws, st);
+    case kWindow: return launch_kind<kWindow>(a, ws, st);
+    case kPrefix: return launch_kind<kPrefix>(a, ws, st);
+    default: return launch_kind<kTail>(a, ws, st);
+  }
 }
 
 unsigned read_status_kv_prefill(cudaStream_t st) {

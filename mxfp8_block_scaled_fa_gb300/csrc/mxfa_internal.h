@@ -248,13 +248,94 @@ struct KvAttnArgs {
   uint16_t* o;            // bf16 [total_q][Hq][128]
   float* lse;             // [Hq][total_q]
   uint8_t* ws;
+  int window, sinks;      // kWindow: a query at position p sees keys p - window + 1 .. p, and those before `sinks`
+  const int32_t* starts;  // kPrefix: [R + 1] first requests of the groups, into cu_q and table
+  const int32_t* prefix;  // kPrefix: [R] keys of a group's prefix; kTail: [R] keys that a request does not read itself
+  float* prefix_o;        // fp32 [total_q][Hq][128], (m, l) [total_q][Hq]: written by kPrefix, read by kTail
+  float2* prefix_ml;
 };
+// What the keys of an attention call are: all up to the query; a window of them and the first ones; the groups'
+// prefixes, for all of a group's queries (results stay in prefix_o, prefix_ml); what is behind them.
+enum KvKind { kAll = 0, kWindow = 1, kPrefix = 2, kTail = 3 };
 size_t kv_attn_workspace(int R, int max_q, int64_t max_k, int G);
 bool kv_attn_reaches(int max_q, int64_t max_k, int G);
-cudaError_t launch_kv_attn(const KvAttnArgs& a, cudaStream_t s);
+cudaError_t launch_kv_attn(int kind, const KvAttnArgs& a, cudaStream_t s);
+int64_t kv_window_reach(int max_q, int64_t max_k, int window, int sinks);
+struct KvSharedWs {
+  size_t ml, gpre, pre, pass, bytes;  // places of its parts
+};
+KvSharedWs kv_shared_workspace(int R, int groups, int64_t total_q, int max_q, int max_group_q, int64_t max_k, int Hq, int G);
+cudaError_t launch_kv_attn_shared(const KvAttnArgs& a, const int32_t* prefix_lens, int groups, int max_group_q, cudaStream_t s);
 size_t kv_prefill_workspace(int R);
-cudaError_t launch_kv_prefill_line(const KvAttnArgs& a, uint8_t* ws, bool after_attn, cudaStream_t st);
-cudaError_t launch_kv_prefill(const KvAttnArgs& a, uint8_t* ws, cudaStream_t s);
+cudaError_t launch_kv_prefill_line(int kind, const KvAttnArgs& a, uint8_t* ws, bool after_attn, cudaStream_t st);
+cudaError_t launch_kv_prefill(int kind, const KvAttnArgs& a, uint8_t* ws, cudaStream_t s);
+
+// ------------------------------------------------------------ rotary positions
+struct Rotation {
+  const uint64_t* turns;  // [rot / 2] 2^-64ths of a turn a position
+  int rot;                // channels that turn, a multiple of 16
+  int inter;              // 1: pairs (2 i, 2 i + 1), 0: (i, i + rot / 2)
+  int inverse;
+  float gain;
+};
+struct RopeArgs {
+  const uint16_t* x;
+  uint16_t* y;
+  int64_t x_stride, y_stride;  // elements from one token to the next
+  const int32_t* positions;    // negative: the token is left out
+  int64_t tokens;
+  int H;
+  Rotation rot;
+  int parts, heads_per_part;   // warps of a token (set by launch_rope)
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
+
+struct KvAppendRopeArgs {
+  KvPages c;
+  const uint16_t *q, *k, *v;
+  uint16_t* y;                 // q turned
+  int64_t q_stride, k_stride, v_stride, y_stride;
+  int64_t tokens;
+  int Hq;
+  const int32_t* positions;
+  const int64_t* slots;
+  Rotation rot;
+  int q_parts, kv_parts, heads_per_part;  // set by launch_kv_append_rope
+};
+cudaError_t launch_kv_append_rope(const KvAppendRopeArgs& a, cudaStream_t s);
+
+// ------------------------------------------------------- shared pages of a cache
+struct KvForkArgs {
+  int32_t* table;       // [R][width]
+  int R, width;
+  const int32_t *src, *dst, *lens;  // [F]
+  int F;
+  int32_t* refs;        // [blocks] owners beside the first
+  int64_t blocks;
+  const int32_t* ring;
+  int64_t ring_size;
+  const int64_t* ring_in;
+  int64_t* ring_out;
+  int page_shift;
+  int32_t *from_blocks, *to_blocks, *lens_out;  // [F]
+};
+cudaError_t launch_kv_fork(const KvForkArgs& a, cudaStream_t s);
+
+struct KvFreeArgs {
+  const int32_t* table;  // [R][width]
+  int R, width;
+  const int32_t *rows, *first, *end;  // [F]
+  int F;
+  int32_t* refs;
+  int64_t blocks;
+  int32_t* ring;
+  int64_t ring_size;
+  const int64_t* ring_in;
+  int64_t* ring_out;
+};
+cudaError_t launch_kv_free(const KvFreeArgs& a, cudaStream_t s);
+int kv_copy_chunks(const KvPages& c);  // CTAs of a block
+cudaError_t launch_kv_copy(const KvPages& c, const int32_t* from, const int32_t* to, int n, cudaStream_t s);
 
 // Read (and clear) the device status words of every kernel module.
 unsigned read_status_quant(cudaStream_t s);
@@ -264,5 +345,7 @@ unsigned read_status_bwd(cudaStream_t s);
 unsigned read_status_kv(cudaStream_t s);
 unsigned read_status_kv_attn(cudaStream_t s);
 unsigned read_status_kv_prefill(cudaStream_t s);
+unsigned read_status_rope(cudaStream_t s);
+unsigned read_status_kv_pages(cudaStream_t s);
 
 }  // namespace mxfa

@@ -28,6 +28,18 @@ tokens' q [T, Hq, 128] and k, v [T, H, 128] in request order:
     step = kv_plan(ctx_lens, new_lens, block_table, free, state, 64, T)
     kv_append(cache, k, v, step.slots)
     o, lse = kv_attention(q, cache, step.cu_q, step.kv_lens, block_table, max_q, scale)
+
+With rotary positions the store is q = kv_append_rope(cache, q, k, v, rp, step.positions,
+step.slots), rp = Rope.make(); training turns q and k by rope(q, rp, rope_positions(seqs)) before
+quantize() and the gradients back by rope_bwd().  kv_attention(..., window=w, sinks=s) sees the
+last w keys and the first s.  Requests that continue others share their pages:
+
+    refs = kv_refs(num_blocks)
+    f = kv_fork(block_table, src, dst, lens, refs, free, state, 64)
+    kv_copy_blocks(cache, f.from_blocks, f.to_blocks)          # of each layer
+    o, lse = kv_attention_shared(q, cache, cu_q, kv_lens, block_table, group_starts, prefix_lens,
+                                 max_q, max_group_q, scale)
+    state = kv_free(block_table, rows, first, end, refs, free, f.ring_state)
 """
 from __future__ import annotations
 
@@ -37,6 +49,7 @@ import importlib.util
 import math
 import os
 from dataclasses import FrozenInstanceError, dataclass
+from fractions import Fraction
 from typing import Optional, Sequence
 
 import numpy as np
@@ -132,6 +145,15 @@ def lib() -> ctypes.CDLL:
             "mxfa_kv_load": (I, [P, P, I64, P, P, P]),
             "mxfa_kv_attn_workspace_size": (S, [I, I, I64, I, I]),
             "mxfa_kv_attn": (I, [P, P, I64, I64, P, P, I, P, I, I, I, F, I, P, P, P, S, P]),
+            "mxfa_kv_attn_window_workspace_size": (S, [I, I, I64, I, I, I, I]),
+            "mxfa_kv_attn_window": (I, [P, P, I64, I64, P, P, I, P, I, I, I, F, I, I, P, P, P, S, P]),
+            "mxfa_kv_attn_shared_workspace_size": (S, [I, I, I64, I, I, I64, I, I]),
+            "mxfa_kv_attn_shared": (I, [P, P, I64, I64, P, P, I, P, I, I, I, F, P, P, I, I, P, P, P, S, P]),
+            "mxfa_rope": (I, [P, I64, P, I64, P, I64, I, I, P, I, P]),
+            "mxfa_kv_append_rope": (I, [P, P, I64, I, P, I64, P, I64, I64, P, P, P, P, I64, P]),
+            "mxfa_kv_fork": (I, [P, I, I, P, P, P, I, P, I64, P, I64, P, P, I, P, P, P, P]),
+            "mxfa_kv_free": (I, [P, I, I, P, P, P, I, P, I64, P, I64, P, P, P]),
+            "mxfa_kv_copy_blocks": (I, [P, P, P, I, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -659,6 +681,67 @@ def mxfa_kv_attn(pages: KvPages, q, q_stride, total_q, cu_q, kv_lens, R, block_t
                               _p(o), _p(lse), _p(ws), ws_bytes, _stream(stream)), "mxfa_kv_attn")
 
 
+def mxfa_kv_attn_window_workspace_size(R, max_q, max_k, Hq, H, window, sinks) -> int:
+    return int(lib().mxfa_kv_attn_window_workspace_size(R, max_q, max_k, Hq, H, window, sinks))
+
+
+def mxfa_kv_attn_window(pages: KvPages, q, q_stride, total_q, cu_q, kv_lens, R, block_table, max_blocks,
+                        max_q, Hq, scale, window, sinks, o, lse, ws, ws_bytes, stream=None):
+    _check(lib().mxfa_kv_attn_window(ctypes.byref(pages), _p(q), q_stride, total_q, _p(cu_q), _p(kv_lens), R,
+                                     _p(block_table), max_blocks, max_q, Hq, float(scale), window, sinks,
+                                     _p(o), _p(lse), _p(ws), ws_bytes, _stream(stream)), "mxfa_kv_attn_window")
+
+
+def mxfa_kv_attn_shared_workspace_size(R, groups, total_q, max_q, max_group_q, max_k, Hq, H) -> int:
+    return int(lib().mxfa_kv_attn_shared_workspace_size(R, groups, total_q, max_q, max_group_q, max_k, Hq, H))
+
+
+def mxfa_kv_attn_shared(pages: KvPages, q, q_stride, total_q, cu_q, kv_lens, R, block_table, max_blocks, max_q,
+                        Hq, scale, group_starts, prefix_lens, groups, max_group_q, o, lse, ws, ws_bytes, stream=None):
+    _check(lib().mxfa_kv_attn_shared(ctypes.byref(pages), _p(q), q_stride, total_q, _p(cu_q), _p(kv_lens), R,
+                                     _p(block_table), max_blocks, max_q, Hq, float(scale), _p(group_starts),
+                                     _p(prefix_lens), groups, max_group_q, _p(o), _p(lse), _p(ws), ws_bytes,
+                                     _stream(stream)), "mxfa_kv_attn_shared")
+
+
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+
+
+class Rotation(ctypes.Structure):
+    """mxfa_rotation: the device pointer of a rotation's turns, and its form."""
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int), ("layout", ctypes.c_int), ("gain", ctypes.c_float)]
+
+
+def mxfa_rope(x, x_stride, y, y_stride, positions, tokens, H, D, rot: Rotation, inverse, stream=None):
+    _check(lib().mxfa_rope(_p(x), x_stride, _p(y), y_stride, _p(positions), tokens, H, D, ctypes.byref(rot),
+                           int(inverse), _stream(stream)), "mxfa_rope")
+
+
+def mxfa_kv_append_rope(pages: KvPages, q, q_stride, Hq, k, k_stride, v, v_stride, tokens, positions, slots,
+                        rot: Rotation, q_out, q_out_stride, stream=None):
+    _check(lib().mxfa_kv_append_rope(ctypes.byref(pages), _p(q), q_stride, Hq, _p(k), k_stride, _p(v), v_stride,
+                                     tokens, _p(positions), _p(slots), ctypes.byref(rot), _p(q_out), q_out_stride,
+                                     _stream(stream)), "mxfa_kv_append_rope")
+
+
+def mxfa_kv_fork(block_table, R, max_blocks, src, dst, lens, F, refs, num_blocks, free_ring, ring_size, ring_in,
+                 ring_out, page, from_blocks, to_blocks, lens_out, stream=None):
+    _check(lib().mxfa_kv_fork(_p(block_table), R, max_blocks, _p(src), _p(dst), _p(lens), F, _p(refs), num_blocks,
+                              _p(free_ring), ring_size, _p(ring_in), _p(ring_out), page, _p(from_blocks),
+                              _p(to_blocks), _p(lens_out), _stream(stream)), "mxfa_kv_fork")
+
+
+def mxfa_kv_free(block_table, R, max_blocks, rows, first, end, F, refs, num_blocks, free_ring, ring_size, ring_in,
+                 ring_out, stream=None):
+    _check(lib().mxfa_kv_free(_p(block_table), R, max_blocks, _p(rows), _p(first), _p(end), F, _p(refs), num_blocks,
+                              _p(free_ring), ring_size, _p(ring_in), _p(ring_out), _stream(stream)), "mxfa_kv_free")
+
+
+def mxfa_kv_copy_blocks(pages: KvPages, from_blocks, to_blocks, n, stream=None):
+    _check(lib().mxfa_kv_copy_blocks(ctypes.byref(pages), _p(from_blocks), _p(to_blocks), n, _stream(stream)),
+           "mxfa_kv_copy_blocks")
+
+
 _kv = None
 
 
@@ -933,18 +1016,42 @@ def kv_load(cache: KvCache, slots: torch.Tensor, out=None, stream=None):
 
 def kv_attention(q: torch.Tensor, cache: KvCache, cu_q: torch.Tensor, kv_lens: torch.Tensor,
                  block_table: torch.Tensor, max_q: int, scale: float, causal: bool = True,
-                 out=None, ws=None, stream=None):
+                 out=None, ws=None, stream=None, window: Optional[int] = None, sinks: int = 0):
     """Attention of new query tokens over the cache -> (O bf16 [tokens, Hq, 128], lse
     fp32 [Hq, tokens]).  q: bf16 [tokens, Hq, 128], tokens may be strided; cu_q
     (int32 [R + 1]), kv_lens (int32 [R], new tokens included) and block_table as
     kv_plan gives them; max_q: the most query tokens of a request.  causal aligns
-    the last query to the last key.  Rows outside cu_q's are not written."""
+    the last query to the last key.  Rows outside cu_q's are not written.  With a `window` (causal
+    only) a query sees the last `window` keys up to its own and the first `sinks`; pages without a
+    key in sight are not read."""
+    if window is not None or sinks:
+        if window is None:
+            raise ValueError("sinks go with a window")
+        if not causal:
+            raise ValueError("a window goes with causal attention")
+        return _attention(q, cache, cu_q, kv_lens, block_table, max_q, scale, out, ws, stream, ("window", window, sinks))
     if out is None and ws is None and stream is None:
         made = _fast().attention(q, cache.raw, cu_q, kv_lens, block_table, max_q, scale, causal)
         if type(made) is tuple:
             return made
         if made is not None:
             _check(made, "mxfa_kv_attn")
+    return _attention(q, cache, cu_q, kv_lens, block_table, max_q, scale, out, ws, stream, ("all", causal))
+
+
+def kv_attention_shared(q: torch.Tensor, cache: KvCache, cu_q: torch.Tensor, kv_lens: torch.Tensor,
+                        block_table: torch.Tensor, group_starts: torch.Tensor, prefix_lens: torch.Tensor,
+                        max_q: int, max_group_q: int, scale: float, out=None, ws=None, stream=None):
+    """kv_attention (causal) of requests that share prefixes: group g is requests group_starts[g] ..
+    group_starts[g + 1] - 1 (int32 [groups + 1]), whose first prefix_lens[g] (int32 [groups]) keys are
+    read from its first request's row of block_table, once for all of the group's queries, at most
+    max_group_q of them.  Every request with queries has at least its group's prefix before them."""
+    return _attention(q, cache, cu_q, kv_lens, block_table, max_q, scale, out, ws, stream,
+                      ("shared", group_starts, prefix_lens, max_group_q))
+
+
+def _attention(q, cache, cu_q, kv_lens, block_table, max_q, scale, out, ws, stream, form):
+    """kv_attention and its forms with arguments checked one by one."""
     H, index = cache.H, cache.index
     shape = q.shape
     if len(shape) != 3 or shape[1] == 0 or shape[1] % H:
@@ -959,9 +1066,16 @@ def kv_attention(q: torch.Tensor, cache: KvCache, cu_q: torch.Tensor, kv_lens: t
     _flat("cu_q", cu_q, i32, index)
     _flat("kv_lens", kv_lens, i32, index)
     _flat("block_table", block_table, i32, index)
+    if form[0] == "shared":
+        _, starts, prefix_lens, max_group_q = form
+        groups = prefix_lens.numel()
+        if starts.numel() != groups + 1:
+            raise ValueError("group_starts and prefix_lens describe different numbers of groups")
+        _flat("group_starts", starts, i32, index)
+        _flat("prefix_lens", prefix_lens, i32, index)
     if not _here(index, stream):
         with _place(index, stream):
-            return kv_attention(q, cache, cu_q, kv_lens, block_table, max_q, scale, causal, out, ws)
+            return _attention(q, cache, cu_q, kv_lens, block_table, max_q, scale, out, ws, None, form)
     dev = q.device
     if out is None:
         o = torch.empty(shape, dtype=torch.bfloat16, device=dev)
@@ -977,7 +1091,13 @@ def kv_attention(q: torch.Tensor, cache: KvCache, cu_q: torch.Tensor, kv_lens: t
     L = lib()
     ws_at, ws_bytes = None, 0
     if ws is None:
-        ws_bytes = L.mxfa_kv_attn_workspace_size(R, max_q, tshape[1] * cache.page, Hq, H)
+        most = tshape[1] * cache.page
+        if form[0] == "window":
+            ws_bytes = L.mxfa_kv_attn_window_workspace_size(R, max_q, most, Hq, H, form[1], form[2])
+        elif form[0] == "shared":
+            ws_bytes = L.mxfa_kv_attn_shared_workspace_size(R, groups, T, max_q, max_group_q, most, Hq, H)
+        else:
+            ws_bytes = L.mxfa_kv_attn_workspace_size(R, max_q, most, Hq, H)
         if ws_bytes:
             ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
             ws_at = ws.data_ptr()
@@ -987,11 +1107,239 @@ def kv_attention(q: torch.Tensor, cache: KvCache, cu_q: torch.Tensor, kv_lens: t
         raise ValueError("ws is not contiguous")
     else:
         ws_at, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
-    _check(L.mxfa_kv_attn(ctypes.byref(cache.pages), q.data_ptr(), qs, T, cu_q.data_ptr(),
-                          kv_lens.data_ptr(), R, block_table.data_ptr(), tshape[1], max_q, Hq, scale,
-                          1 if causal else 0, o.data_ptr(), lse.data_ptr(), ws_at, ws_bytes,
-                          _raw_stream(index)), "mxfa_kv_attn")
+    args = (ctypes.byref(cache.pages), q.data_ptr(), qs, T, cu_q.data_ptr(), kv_lens.data_ptr(), R,
+            block_table.data_ptr(), tshape[1], max_q, Hq, scale)
+    rest = (o.data_ptr(), lse.data_ptr(), ws_at, ws_bytes, _raw_stream(index))
+    if form[0] == "window":
+        _check(L.mxfa_kv_attn_window(*args, form[1], form[2], *rest), "mxfa_kv_attn_window")
+    elif form[0] == "shared":
+        _check(L.mxfa_kv_attn_shared(*args, starts.data_ptr(), prefix_lens.data_ptr(), groups, max_group_q, *rest),
+               "mxfa_kv_attn_shared")
+    else:
+        _check(L.mxfa_kv_attn(*args, 1 if form[1] else 0, *rest), "mxfa_kv_attn")
     return o, lse
+
+
+# ------------------------------------------------------------------ rotary positions
+_TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+
+
+@dataclass
+class Rope:
+    """A rotation by positions (mxfa_rotation in mxfa.h): turns int64 [rot / 2] on the GPU, pairs
+    interleaved (2 i, 2 i + 1) or in halves (i, i + rot / 2) of the first rot channels, and a gain."""
+    turns: torch.Tensor
+    interleaved: bool = False
+    gain: float = 1.0
+
+    @staticmethod
+    def from_freqs(freqs, interleaved: bool = False, gain: float = 1.0, device="cuda") -> "Rope":
+        """From radians a position of each pair, rounded to 2^-64 of a turn."""
+        turns = [round(Fraction(float(f)) / _TWO_PI * 2 ** 64) % 2 ** 64 for f in freqs]
+        turns = [t - 2 ** 64 if t >= 2 ** 63 else t for t in turns]
+        return Rope(torch.tensor(turns, dtype=torch.int64, device=device), interleaved, gain)
+
+    @staticmethod
+    def make(rot: int = 128, base: float = 10000.0, interleaved: bool = False, scaling: Optional[str] = None,
+             factor: float = 1.0, original: int = 4096, device="cuda") -> "Rope":
+        """Frequencies base^(-2 i / rot), for a context `factor` times the `original` one scaled
+          "linear"  all of them divided by factor,
+          "ntk"     with base * factor^(rot / (rot - 2)): the slowest divided by factor, the fastest as it was,
+          "yarn"    divided by factor where a pair turns less than once in the original context, kept
+                    where it turns 32 times or more, blended in between over the logarithm of its
+                    wavelength's inverse, and the gain 0.1 ln(factor) + 1."""
+        if rot <= 0 or rot % 16 or rot > 128:
+            raise ValueError(f"{rot} rotated channels, expected 16, 32, .., 128")
+        if not base > 1.0 or not factor >= 1.0 or original < 1:
+            raise ValueError("base is above 1, factor and original at least 1")
+        if scaling not in (None, "linear", "ntk", "yarn"):
+            raise ValueError(f"unknown scaling {scaling!r}")
+        if scaling == "ntk":
+            base = base * factor ** (rot / (rot - 2))
+        f = [base ** (-2 * i / rot) for i in range(rot // 2)]
+        gain = 1.0
+        if scaling == "linear":
+            f = [x / factor for x in f]
+        elif scaling == "yarn":
+            keep = [min(1.0, max(0.0, math.log(original * x / (2 * math.pi)) / math.log(32.0))) for x in f]
+            f = [x * (k + (1.0 - k) / factor) for x, k in zip(f, keep)]
+            gain = 0.1 * math.log(factor) + 1.0
+        return Rope.from_freqs(f, interleaved, gain, device)
+
+
+def rope_positions(seqs: Seqs, device="cuda") -> torch.Tensor:
+    """Positions int32 [tokens] of packed sequences, each from 0 on."""
+    if seqs.cu_host is None:
+        return torch.arange(seqs.max_len, dtype=torch.int32, device=device).repeat(seqs.nseq)
+    lens = np.diff(seqs.cu_host)
+    return torch.from_numpy((np.arange(seqs.total) - np.repeat(seqs.cu_host[:-1], lens)).astype(np.int32)).to(device)
+
+
+def _rotation(rp: Rope, index: int) -> Rotation:
+    _flat("turns", rp.turns, torch.int64, index)
+    return Rotation(rp.turns.data_ptr(), 2 * rp.turns.numel(), 1 if rp.interleaved else 0, rp.gain)
+
+
+def _positions(positions: torch.Tensor, T: int, index: int):
+    _flat("positions", positions, torch.int32, index)
+    if positions.numel() != T:
+        raise ValueError(f"{positions.numel()} positions for {T} tokens")
+
+
+def _rope(x, rp, positions, inverse, out, stream):
+    if len(x.shape) != 3:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [tokens, heads, 128]")
+    index, (T, H, _) = x.get_device(), x.shape
+    if index < 0:
+        raise ValueError("x must be on a CUDA device")
+    xs = _rows("x", x, H, index)
+    _positions(positions, T, index)
+    rot = _rotation(rp, index)
+    if not _here(index, stream):
+        with _place(index, stream):
+            return _rope(x, rp, positions, inverse, out, None)
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+    elif out.shape != x.shape:
+        raise ValueError(f"out must have shape {tuple(x.shape)}")
+    if T and H:
+        _check(lib().mxfa_rope(x.data_ptr(), xs, out.data_ptr(), _rows("out", out, H, index), positions.data_ptr(), T, H, 128,
+                               ctypes.byref(rot), inverse, _raw_stream(index)), "mxfa_rope")
+    return out
+
+
+def rope(x: torch.Tensor, rp: Rope, positions: torch.Tensor, out=None, stream=None) -> torch.Tensor:
+    """bf16 [tokens, heads, 128] (tokens may be strided) turned by positions int32 [tokens].
+    `out` may be x; its rows of tokens with a negative position stay as they are."""
+    return _rope(x, rp, positions, 0, out, stream)
+
+
+def rope_bwd(dy: torch.Tensor, rp: Rope, positions: torch.Tensor, out=None, stream=None) -> torch.Tensor:
+    """The gradient of rope()'s x from that of its result: turned back, with the same gain."""
+    return _rope(dy, rp, positions, 1, out, stream)
+
+
+def kv_append_rope(cache: KvCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rp: Rope,
+                   positions: torch.Tensor, slots: torch.Tensor, out=None, stream=None) -> torch.Tensor:
+    """A step's new tokens: turns q [tokens, Hq, 128] (the result, or into `out`, which may be q), and
+    stores k turned and v [tokens, H, 128] into the cache rows `slots`, as rope() and kv_append() do.
+    Tokens with a negative position are left out; those without a slot still get their q."""
+    index, H = cache.index, cache.H
+    if len(q.shape) != 3 or q.shape[1] == 0:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected [tokens, heads, 128]")
+    T, Hq, _ = q.shape
+    qs, ks, vs = _rows("q", q, Hq, index), _rows("k", k, H, index), _rows("v", v, H, index)
+    if k.shape[0] != T or v.shape[0] != T or slots.numel() != T:
+        raise ValueError("q, k, v and slots have different numbers of tokens")
+    _flat("slots", slots, torch.int64, index)
+    _positions(positions, T, index)
+    rot = _rotation(rp, index)
+    if not _here(index, stream):
+        with _place(index, stream):
+            return kv_append_rope(cache, q, k, v, rp, positions, slots, out)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError(f"out must have shape {tuple(q.shape)}")
+    if T:
+        _check(lib().mxfa_kv_append_rope(ctypes.byref(cache.pages), q.data_ptr(), qs, Hq, k.data_ptr(), ks, v.data_ptr(), vs, T,
+                                         positions.data_ptr(), slots.data_ptr(), ctypes.byref(rot), out.data_ptr(),
+                                         _rows("out", out, Hq, index), _raw_stream(index)), "mxfa_kv_append_rope")
+    return out
+
+
+# ------------------------------------------------------------- pages shared by requests
+@dataclass
+class KvFork:
+    """What kv_fork says (mxfa_kv_fork in mxfa.h).  Where ring_state[2] > 0 some forks got no block for
+    their last page: their lens end with the whole pages."""
+    from_blocks: torch.Tensor  # int32 [F]: blocks to copy, for kv_copy_blocks; -1: none
+    to_blocks: torch.Tensor    # int32 [F]
+    lens: torch.Tensor         # int32 [F]: tokens that the new rows hold
+    ring_state: torch.Tensor   # int64 [3]: taken, put, lacked
+
+
+def kv_refs(num_blocks: int, device="cuda") -> torch.Tensor:
+    """The counts of a new cache's blocks' owners beside the first, for kv_fork and kv_free."""
+    return torch.zeros(num_blocks, dtype=torch.int32, device=device)
+
+
+def _pages(block_table, refs, free_ring, ring_state, lists):
+    """Checks what kv_fork and kv_free have in common -> (device index, entries of a list)."""
+    index, (names, tensors) = block_table.get_device(), lists
+    if len(block_table.shape) != 2:
+        raise ValueError(f"block_table has shape {tuple(block_table.shape)}, expected [requests, max_blocks]")
+    F = tensors[0].numel()
+    _flat("block_table", block_table, torch.int32, index)
+    for name, t in zip(names, tensors):
+        _flat(name, t, torch.int32, index)
+        if t.numel() != F:
+            raise ValueError(", ".join(names) + " have different lengths")
+    _flat("refs", refs, torch.int32, index)
+    _flat("free_ring", free_ring, torch.int32, index)
+    _flat("ring_state", ring_state, torch.int64, index)
+    if ring_state.numel() != 3:
+        raise ValueError("ring_state has three elements")
+    return index, F
+
+
+def kv_fork(block_table: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
+            free_ring: torch.Tensor, ring_state: torch.Tensor, page: int, out: Optional[KvFork] = None,
+            stream=None) -> KvFork:
+    """Rows dst (int32 [F]) of block_table get the first lens tokens of rows src: whole pages shared
+    (refs counts their owners), a last page that is not full in a block of its own, to be copied by
+    kv_copy_blocks in each layer's cache.  `out` gives the result's buffers; its ring_state may be
+    ring_state."""
+    index, F = _pages(block_table, refs, free_ring, ring_state, (("src", "dst", "lens"), (src, dst, lens)))
+    if not _here(index, stream):
+        with _place(index, stream):
+            return kv_fork(block_table, src, dst, lens, refs, free_ring, ring_state, page, out)
+    if out is None:
+        i32 = dict(dtype=torch.int32, device=block_table.device)
+        out = KvFork(torch.empty(F, **i32), torch.empty(F, **i32), torch.empty(F, **i32), torch.empty_like(ring_state))
+    else:
+        _pages(block_table, refs, free_ring, out.ring_state,
+               (("out.from_blocks", "out.to_blocks", "out.lens", "src"), (out.from_blocks, out.to_blocks, out.lens, src)))
+    _check(lib().mxfa_kv_fork(block_table.data_ptr(), block_table.shape[0], block_table.shape[1], src.data_ptr(), dst.data_ptr(),
+                              lens.data_ptr(), F, refs.data_ptr(), refs.numel(), free_ring.data_ptr(), free_ring.numel(),
+                              ring_state.data_ptr(), out.ring_state.data_ptr(), page, out.from_blocks.data_ptr(),
+                              out.to_blocks.data_ptr(), out.lens.data_ptr(), _raw_stream(index)), "mxfa_kv_fork")
+    return out
+
+
+def kv_free(block_table: torch.Tensor, rows: torch.Tensor, first: torch.Tensor, end: torch.Tensor, refs: torch.Tensor,
+            free_ring: torch.Tensor, ring_state: torch.Tensor, out=None, stream=None) -> torch.Tensor:
+    """Gives up pages first .. end - 1 of `rows` (int32 [F] each): one owner fewer for each, blocks
+    without an owner back to free_ring, in ascending order -> the ring's new state.  `out` (which may be
+    ring_state) gives its buffer.  The table stays as it is."""
+    index, F = _pages(block_table, refs, free_ring, ring_state, (("rows", "first", "end"), (rows, first, end)))
+    if not _here(index, stream):
+        with _place(index, stream):
+            return kv_free(block_table, rows, first, end, refs, free_ring, ring_state, out)
+    if out is None:
+        out = torch.empty_like(ring_state)
+    else:
+        _pages(block_table, refs, free_ring, out, (("rows",), (rows,)))
+    _check(lib().mxfa_kv_free(block_table.data_ptr(), block_table.shape[0], block_table.shape[1], rows.data_ptr(), first.data_ptr(),
+                              end.data_ptr(), F, refs.data_ptr(), refs.numel(), free_ring.data_ptr(), free_ring.numel(),
+                              ring_state.data_ptr(), out.data_ptr(), _raw_stream(index)), "mxfa_kv_free")
+    return out
+
+
+def kv_copy_blocks(cache: KvCache, from_blocks: torch.Tensor, to_blocks: torch.Tensor, stream=None):
+    """Copies blocks from_blocks (int32 [n]) of the cache over to_blocks, all heads; pairs with a
+    negative one are skipped.  The blocks written are distinct and none of those read."""
+    index, n = cache.index, from_blocks.numel()
+    _flat("from_blocks", from_blocks, torch.int32, index)
+    _flat("to_blocks", to_blocks, torch.int32, index)
+    if to_blocks.numel() != n:
+        raise ValueError("from_blocks and to_blocks have different lengths")
+    if not _here(index, stream):
+        with _place(index, stream):
+            return kv_copy_blocks(cache, from_blocks, to_blocks)
+    if n:
+        _check(lib().mxfa_kv_copy_blocks(ctypes.byref(cache.pages), from_blocks.data_ptr(), to_blocks.data_ptr(), n,
+                                         _raw_stream(index)), "mxfa_kv_copy_blocks")
 
 
 def device_status(stream=None) -> int:
