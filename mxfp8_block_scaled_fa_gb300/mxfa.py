@@ -1029,6 +1029,12 @@ def kv_attention(q: torch.Tensor, cache: KvCache, cu_q: torch.Tensor, kv_lens: t
             raise ValueError("sinks go with a window")
         if not causal:
             raise ValueError("a window goes with causal attention")
+        if out is None and ws is None and stream is None:
+            made = _fast().window(q, cache.raw, cu_q, kv_lens, block_table, max_q, scale, window, sinks)
+            if type(made) is tuple:
+                return made
+            if made is not None:
+                _check(made, "mxfa_kv_attn_window")
         return _attention(q, cache, cu_q, kv_lens, block_table, max_q, scale, out, ws, stream, ("window", window, sinks))
     if out is None and ws is None and stream is None:
         made = _fast().attention(q, cache.raw, cu_q, kv_lens, block_table, max_q, scale, causal)
@@ -1046,6 +1052,12 @@ def kv_attention_shared(q: torch.Tensor, cache: KvCache, cu_q: torch.Tensor, kv_
     group_starts[g + 1] - 1 (int32 [groups + 1]), whose first prefix_lens[g] (int32 [groups]) keys are
     read from its first request's row of block_table, once for all of the group's queries, at most
     max_group_q of them.  Every request with queries has at least its group's prefix before them."""
+    if out is None and ws is None and stream is None:
+        made = _fast().shared(q, cache.raw, cu_q, kv_lens, block_table, max_q, scale, group_starts, prefix_lens, max_group_q)
+        if type(made) is tuple:
+            return made
+        if made is not None:
+            _check(made, "mxfa_kv_attn_shared")
     return _attention(q, cache, cu_q, kv_lens, block_table, max_q, scale, out, ws, stream,
                       ("shared", group_starts, prefix_lens, max_group_q))
 
@@ -1187,6 +1199,12 @@ def _positions(positions: torch.Tensor, T: int, index: int):
 
 
 def _rope(x, rp, positions, inverse, out, stream):
+    if out is None and stream is None:
+        made = _fast().rope(x, rp.turns, rp.interleaved, rp.gain, positions, inverse)
+        if type(made) is int:
+            _check(made, "mxfa_rope")
+        if made is not None:
+            return made
     if len(x.shape) != 3:
         raise ValueError(f"x has shape {tuple(x.shape)}, expected [tokens, heads, 128]")
     index, (T, H, _) = x.get_device(), x.shape
@@ -1224,6 +1242,12 @@ def kv_append_rope(cache: KvCache, q: torch.Tensor, k: torch.Tensor, v: torch.Te
     """A step's new tokens: turns q [tokens, Hq, 128] (the result, or into `out`, which may be q), and
     stores k turned and v [tokens, H, 128] into the cache rows `slots`, as rope() and kv_append() do.
     Tokens with a negative position are left out; those without a slot still get their q."""
+    if stream is None:
+        made = _fast().append_rope(cache.raw, q, k, v, rp.turns, rp.interleaved, rp.gain, positions, slots, out)
+        if type(made) is int:
+            _check(made, "mxfa_kv_append_rope")
+        if made is not None:
+            return made
     index, H = cache.index, cache.H
     if len(q.shape) != 3 or q.shape[1] == 0:
         raise ValueError(f"q has shape {tuple(q.shape)}, expected [tokens, heads, 128]")
@@ -1290,6 +1314,12 @@ def kv_fork(block_table: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, len
     (refs counts their owners), a last page that is not full in a block of its own, to be copied by
     kv_copy_blocks in each layer's cache.  `out` gives the result's buffers; its ring_state may be
     ring_state."""
+    if out is None and stream is None:
+        made = _fast().fork(block_table, src, dst, lens, refs, free_ring, ring_state, page)
+        if type(made) is tuple:
+            return KvFork(*made)
+        if made is not None:
+            _check(made, "mxfa_kv_fork")
     index, F = _pages(block_table, refs, free_ring, ring_state, (("src", "dst", "lens"), (src, dst, lens)))
     if not _here(index, stream):
         with _place(index, stream):
@@ -1312,6 +1342,12 @@ def kv_free(block_table: torch.Tensor, rows: torch.Tensor, first: torch.Tensor, 
     """Gives up pages first .. end - 1 of `rows` (int32 [F] each): one owner fewer for each, blocks
     without an owner back to free_ring, in ascending order -> the ring's new state.  `out` (which may be
     ring_state) gives its buffer.  The table stays as it is."""
+    if out is None and stream is None:
+        made = _fast().free_pages(block_table, rows, first, end, refs, free_ring, ring_state)
+        if type(made) is int:
+            _check(made, "mxfa_kv_free")
+        if made is not None:
+            return made
     index, F = _pages(block_table, refs, free_ring, ring_state, (("rows", "first", "end"), (rows, first, end)))
     if not _here(index, stream):
         with _place(index, stream):
@@ -1329,6 +1365,10 @@ def kv_free(block_table: torch.Tensor, rows: torch.Tensor, first: torch.Tensor, 
 def kv_copy_blocks(cache: KvCache, from_blocks: torch.Tensor, to_blocks: torch.Tensor, stream=None):
     """Copies blocks from_blocks (int32 [n]) of the cache over to_blocks, all heads; pairs with a
     negative one are skipped.  The blocks written are distinct and none of those read."""
+    if stream is None:
+        status = _fast().copy_blocks(cache.raw, from_blocks, to_blocks)
+        if status is not None:
+            return _check(status, "mxfa_kv_copy_blocks")
     index, n = cache.index, from_blocks.numel()
     _flat("from_blocks", from_blocks, torch.int32, index)
     _flat("to_blocks", to_blocks, torch.int32, index)
