@@ -1066,7 +1066,7 @@ size_t mxfa_kv_attn_shared_workspace_size(int R, int groups, int64_t total_q, in
                                           int Hq, int H) {
   if (R < 0 || groups < 0 || total_q < 0 || max_q < 0 || max_group_q < 0 || max_k < 0 || H <= 0 || Hq <= 0 || Hq % H) return 0;
   if (groups == 0) return kv_attn_workspace(R, max_q, max_k, Hq / H);
-  return kv_shared_workspace(R, groups, total_q, max_q, max_group_q, max_k, Hq, Hq / H).bytes;
+  return kv_shared_workspace(R, groups, total_q, max_q, max_group_q, max_k, Hq, Hq / H);
 }
 
 mxfa_status mxfa_kv_attn_shared(const mxfa_kv_cache* cache, const void* q, int64_t q_stride, int64_t total_q,
@@ -1271,7 +1271,8 @@ mxfa_status mxfa_get_device_status(mxfa_stream_t stream, unsigned* flags) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(st) != cudaSuccess) return MXFA_ERR_CUDA;
   unsigned f = read_status_quant(st) | read_status_fwd(st) | read_status_bwd(st) | read_status_gemm(st) | read_status_kv(st) |
-               read_status_kv_attn(st) | read_status_kv_prefill(st) | read_status_rope(st) | read_status_kv_pages(st);
+               read_status_kv_attn(st) | read_status_kv_prefill(st) | read_status_rope(st) | read_status_kv_pages(st) |
+               read_status_kv_shared(st);
   if (flags) *flags = f;
   if (f & 1u) return MXFA_ERR_TIMEOUT;
   if (f & 2u) return MXFA_ERR_DEVICE_INDEX;

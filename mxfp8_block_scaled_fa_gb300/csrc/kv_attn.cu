@@ -183,7 +183,7 @@ template <int KIND>
 __device__ __forceinline__ Request request_of(const KvAttnArgs& a, int r) {
   Request x;
   x.lo = x.hi = x.at = x.jump = 0;
-  if constexpr (KIND == kPrefix) {  // checked by kv_shared_kernel, whose result is 0 for a group that is none
+  if constexpr (KIND == kPrefix) {  // checked by kv_shared_plan_kernel, whose result is 0 for a group that is none
     x.kv = __ldg(a.prefix + r);
     x.q0 = x.n = 0;
     if (x.kv <= 0) return x;
@@ -222,34 +222,17 @@ __device__ __forceinline__ int table_row(const KvAttnArgs& a, int r) {
 }
 __device__ __forceinline__ int tiles_of(const Request& x) { return max(1, (x.kv - x.jump + kTile - 1) / kTile); }
 
-// N = 4 or 8 channels from c of a finished row: `row` = token * Hq + head; m, l, o of the keys seen
-// here.  `behind`: the row's keys of its group's prefix, whose m, l, o another kernel has left.
+// N = 4 or 8 channels from c of a finished row: `row` = token * Hq + head; m, l, o of its keys.  Records stay as
+// they are, for kv_shared_join_kernel.
 template <int KIND, int N>
-__device__ __forceinline__ void finish(const KvAttnArgs& a, int64_t token, int head, int c, float m, float l, float (&o)[N],
-                                       float vst, bool behind) {
+__device__ __forceinline__ void finish(const KvAttnArgs& a, int64_t token, int head, int c, float m, float l, const float (&o)[N], float vst) {
   const int64_t row = token * a.Hq + head;
-  if constexpr (KIND == kPrefix) {
-    float4* dst = reinterpret_cast<float4*>(a.prefix_o + row * 128 + c);
+  if constexpr (kRecords<KIND>) {
+    float4* dst = reinterpret_cast<float4*>(a.rows_o + row * 128 + c);
 #pragma unroll
     for (int i = 0; i < N / 4; i++) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-    if (c == 0) a.prefix_ml[row] = make_float2(m, l);
+    if (c == 0) a.rows_ml[row] = make_float2(m, l);
     return;
-  }
-  if (KIND == kTail && behind) {
-    const float2 ml = a.prefix_ml[row];
-    const float4* src = reinterpret_cast<const float4*>(a.prefix_o + row * 128 + c);
-    const float top = fmaxf(m, ml.x);
-    const float w = m == -INFINITY ? 1.0f : ex2(m - top), u = ml.x == -INFINITY ? 1.0f : ex2(ml.x - top);
-    l = w * l + u * ml.y;
-    m = top;
-#pragma unroll
-    for (int i = 0; i < N / 4; i++) {
-      const float4 v = src[i];
-      o[4 * i] = w * o[4 * i] + u * v.x;
-      o[4 * i + 1] = w * o[4 * i + 1] + u * v.y;
-      o[4 * i + 2] = w * o[4 * i + 2] + u * v.z;
-      o[4 * i + 3] = w * o[4 * i + 3] + u * v.w;
-    }
   }
   const float f = l == 0.0f ? 1.0f : vst / l;
   uint32_t p[N / 2];
@@ -587,7 +570,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
   uint8_t* s_q = NT > 1 ? smem + ring_bytes(FMT) + ROWS * 4 : smem + last_stage(FMT);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (kRecords<KIND> && !a.late) asm volatile("griddepcontrol.wait;" ::: "memory");  // for the prefixes' checks
   asm volatile("griddepcontrol.launch_dependents;");  // kv_join_kernel may take its place and wait
+  // `late`: nothing is read of the kernel before this one, but its end is this one's, too.  One CTA waits for
+  // it; the others make room.
+  auto leave = [&] {
+    if (kRecords<KIND> && a.late && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  };
   Header* headers = reinterpret_cast<Header*>(a.ws);
   Partial<NT>* partials = reinterpret_cast<Partial<NT>*>(a.ws + header_bytes(gridDim.x));
 
@@ -599,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
     end = int64_t(a.R) * a.c.H;
     pos = blockIdx.x;
   } else {
-    if (tid == 0) headers[blockIdx.x].parts = 0;
+    if (!kRecords<KIND> && tid == 0) headers[blockIdx.x].parts = 0;
     int64_t first_own = 0, first_upto = 0;  // of the first kThreads requests, the only ones most often
     for (int r0 = 0; r0 < a.R; r0 += kThreads) {
       int64_t sum;
@@ -613,7 +602,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
     }
     const int64_t most = (total + kMinTiles - 1) / kMinTiles;
     const int64_t C = most < int64_t(gridDim.x) ? most : int64_t(gridDim.x);
-    if (int64_t(blockIdx.x) >= C) return;
+    if (int64_t(blockIdx.x) >= C) {
+      leave();
+      return;
+    }
     run = total / C, extra = total - run * C;  // the first `extra` CTAs take one unit more
     pos = run * blockIdx.x + min(extra, int64_t(blockIdx.x));
     end = pos + run + (int64_t(blockIdx.x) < extra ? 1 : 0);
@@ -768,8 +760,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
     }
   };
 
+  // further CTAs that hold a part of an item that begins here
+  auto parts_behind = [&](const Item& x) {
+    const int64_t larger = extra * (run + 1);  // units of the CTAs that take one more
+    return int(x.last_unit < larger ? x.last_unit / (run + 1) : extra + (x.last_unit - larger) / run) - int(blockIdx.x);
+  };
+
   Item it;
-  if (!next(it)) return;
+  if (!next(it)) {
+    leave();
+    return;
+  }
   begin(it);
   for (bool more = true; more;) {
     // Q: binary16 with a power of two per row, in fragment order
@@ -915,21 +916,26 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
           }
         } else {
           const int rr = cur.row0 + frow, tok = rr / a.G, hd = cur.h * a.G + rr - tok * a.G;
-          finish<KIND, 8>(a, cur.q0 + tok, hd, quad * 4, M, L, o, vst, cur.hi > 0);
+          finish<KIND, 8>(a, cur.q0 + tok, hd, quad * 4, M, L, o, vst);
+        }
+        if (kRecords<KIND> && !head_part && quad == 0) {
+          const int rr = cur.row0 + frow, tok = rr / a.G, hd = cur.h * a.G + rr - tok * a.G;
+          a.places[int64_t(cur.q0 + tok) * a.Hq + hd] =
+              make_uint2(blockIdx.x, kv_place(cut ? parts_behind(cur) + 1 : 0, frow, false, cur.hi > 0));
         }
       }
     }
-    if (cut && !head_part && tid == 0) {
-      const int64_t larger = extra * (run + 1);  // units of the CTAs that take one more
+    if (!kRecords<KIND> && cut && !head_part && tid == 0) {
       Header hd;
       hd.r = cur.r;
       hd.rb = cur.rb;
       hd.h = cur.h;
-      hd.parts = int(cur.last_unit < larger ? cur.last_unit / (run + 1) : extra + (cur.last_unit - larger) / run) - int(blockIdx.x);
+      hd.parts = parts_behind(cur);
       headers[blockIdx.x] = hd;
     }
     __syncthreads();  // the third stages and the row scales are free
   }
+  leave();
 }
 
 // Joins the parts of the item that begins in CTA blockIdx.x's run and ends behind
@@ -980,7 +986,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(KvAttnArgs a, int ctas) {
   const float vst = FMT == 1 ? __ldg(a.c.v_scale) : 1.0f;
   const int tok = rr / a.G, head = hd.h * a.G + rr - tok * a.G;
   float o[4] = {s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w};
-  finish<KIND, 4>(a, x.q0 + tok, head, lane * 4, M, L, o, vst, x.hi > 0);
+  finish<KIND, 4>(a, x.q0 + tok, head, lane * 4, M, L, o, vst);
 }
 
 // Tiles of eight query rows in a block: as few blocks of at most 32 rows as there
@@ -1011,23 +1017,20 @@ cudaError_t launch(const KvAttnArgs& a, uint8_t* line_ws, cudaStream_t st) {
   if (a.whole) {
     const int64_t items = int64_t(a.R) * a.c.H;
     const int64_t most = int64_t(ctas) * 16;
-    kv_attn_kernel<KIND, FMT, NT><<<unsigned(items < most ? items : most), kThreads, bytes, st>>>(a);
+    const unsigned grid = unsigned(items < most ? items : most);
+    if constexpr (kRecords<KIND>) return launch_early(kv_attn_kernel<KIND, FMT, NT>, dim3(grid), kThreads, bytes, st, a);
+    kv_attn_kernel<KIND, FMT, NT><<<grid, kThreads, bytes, st>>>(a);
     return cudaGetLastError();
+  }
+  if constexpr (kRecords<KIND>) {
+    if (a.late || !line_ws) return launch_early(kv_attn_kernel<KIND, FMT, NT>, dim3(unsigned(ctas)), kThreads, bytes, st, a);
   }
   kv_attn_kernel<KIND, FMT, NT><<<ctas, kThreads, bytes, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (line_ws && (e = launch_kv_prefill_line(KIND, a, line_ws, true, st)) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(ctas), 2 * NT);
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_join_kernel<KIND, FMT, NT>, a, ctas);
+  if constexpr (kRecords<KIND>) return cudaSuccess;
+  else return launch_early(kv_join_kernel<KIND, FMT, NT>, dim3(unsigned(ctas), 2 * NT), 256, 0, st, a, ctas);
 }
 
 template <int KIND, int FMT>
@@ -1106,6 +1109,19 @@ size_t kv_attn_workspace(int R, int max_q, int64_t max_k, int G) {
   return p.prefill ? few + kv_prefill_workspace(R) : few;
 }
 
+bool kv_attn_few(int max_q, int64_t max_k, int G) { return !kva::plan_of(max_q, max_k, G).prefill; }
+
+// The parts of a call's workspace: where the kernels of few and of many rows leave records.
+KvRecords kv_attn_records(uint8_t* ws, int R, int max_q, int64_t max_k, int G) {
+  const kva::Plan p = kva::plan_of(max_q, max_k, G);
+  KvRecords x;
+  x.many_ws = ws + ((kva::workspace_of(p.nt) + 255) & ~size_t(255));
+  x.few = ws + kva::header_bytes(sm_count_current_device() * kva::ctas_per_sm(p.nt));
+  x.few_rows = 8 * p.nt;
+  x.many = p.prefill ? kv_prefill_records(x.many_ws, R) : nullptr;
+  return x;
+}
+
 cudaError_t launch_kv_attn(int kind, const KvAttnArgs& args, cudaStream_t st) {
   clear_stale_error();
   KvAttnArgs a = args;
@@ -1115,77 +1131,15 @@ cudaError_t launch_kv_attn(int kind, const KvAttnArgs& args, cudaStream_t st) {
   const kva::Plan p = kva::plan_of(a.max_q, max_k, a.G);
   a.split_rows = p.split_rows;
   a.whole = p.whole;
-  uint8_t* const line_ws = p.prefill ? a.ws + ((kva::workspace_of(p.nt) + 255) & ~size_t(255)) : nullptr;
+  uint8_t* const line_ws = p.prefill ? kv_attn_records(a.ws, a.R, a.max_q, max_k, a.G).many_ws : nullptr;
+  if (kind == kPrefix && p.prefill) {  // all groups, by the line that kv_shared_plan_kernel has made
+    a.split_rows = 0;
+    return launch_kv_prefill(kind, a, line_ws, st);
+  }
   cudaError_t e;
   if (!p.prefill || a.G <= kva::kMixedRows) e = kva::launch_kind(kind, a, p.nt, line_ws, st);
   else e = launch_kv_prefill_line(kind, a, line_ws, false, st);
   return e != cudaSuccess || !p.prefill ? e : launch_kv_prefill(kind, a, line_ws, st);
-}
-
-// The prefixes of a call's groups, checked: of group g at gpre[g] (0: none, or not as documented), and of
-// each request at pre[r] (-1: of a group not as documented; 0 for a request of no group).
-__global__ void __launch_bounds__(256) kv_shared_kernel(KvAttnArgs a, const int32_t* prefix_lens, int groups, int max_rows, int32_t* gpre,
-                                                        int32_t* pre) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  auto checked = [&](int g) -> int {  // -1: not as documented
-    const int s = __ldg(a.starts + g), e = __ldg(a.starts + g + 1), p = __ldg(prefix_lens + g);
-    if (s < 0 || e < s || e > a.R || p < 0 || p > int64_t(a.width) << a.c.page_shift) return -1;
-    const int b = __ldg(a.cu_q + s), t = __ldg(a.cu_q + e);
-    return b < 0 || t < b || t > a.total_q || t - b > max_rows ? -1 : s == e ? 0 : p;
-  };
-  if (i < groups) {
-    const int p = checked(i);
-    if (p < 0) atomicOr(&g_status_kv_attn, DEV_BAD_INDEX);
-    gpre[i] = max(p, 0);
-  }
-  if (i < a.R) {
-    int lo = 0, hi = groups;  // the group with starts[lo] <= i < starts[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(a.starts + mid) <= i) lo = mid;
-      else hi = mid;
-    }
-    const bool in = __ldg(a.starts + lo) <= i && i < __ldg(a.starts + lo + 1);
-    pre[i] = in ? checked(lo) : 0;
-  }
-}
-
-// Workspace of a call over shared prefixes: rows' partial results of their prefixes, checked prefixes, and the
-// larger of the two passes' own.
-KvSharedWs kv_shared_workspace(int R, int groups, int64_t total_q, int max_q, int max_group_q, int64_t max_k, int Hq, int G) {
-  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-  KvSharedWs w;
-  w.ml = up(size_t(total_q) * size_t(Hq) * 512);
-  w.gpre = w.ml + up(size_t(total_q) * size_t(Hq) * 8);
-  w.pre = w.gpre + up(size_t(groups) * 4);
-  w.pass = w.pre + up(size_t(R) * 4);
-  const size_t first = kv_attn_workspace(groups, max_group_q, max_k, G), second = kv_attn_workspace(R, max_q, max_k, G);
-  w.bytes = w.pass + (first > second ? first : second);
-  return w;
-}
-
-cudaError_t launch_kv_attn_shared(const KvAttnArgs& args, const int32_t* prefix_lens, int groups, int max_group_q, cudaStream_t st) {
-  clear_stale_error();
-  KvAttnArgs a = args;
-  const KvSharedWs w = kv_shared_workspace(a.R, groups, a.total_q, a.max_q, max_group_q, int64_t(a.width) << a.c.page_shift, a.Hq, a.G);
-  int32_t* const gpre = reinterpret_cast<int32_t*>(a.ws + w.gpre);
-  int32_t* const pre = reinterpret_cast<int32_t*>(a.ws + w.pre);
-  a.prefix_o = reinterpret_cast<float*>(a.ws);
-  a.prefix_ml = reinterpret_cast<float2*>(a.ws + w.ml);
-  const int most = a.R > groups ? a.R : groups;
-  kv_shared_kernel<<<unsigned((most + 255) / 256), 256, 0, st>>>(a, prefix_lens, groups, max_group_q, gpre, pre);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  a.ws += w.pass;
-  KvAttnArgs first = a;  // the groups as requests, whose keys are the prefixes
-  first.R = groups;
-  first.max_q = max_group_q;
-  first.causal = 0;
-  first.prefix = gpre;
-  if ((e = launch_kv_attn(kPrefix, first, st)) != cudaSuccess) return e;
-  a.causal = 1;
-  a.prefix = pre;
-  return launch_kv_attn(kTail, a, st);
 }
 
 unsigned read_status_kv_attn(cudaStream_t st) {

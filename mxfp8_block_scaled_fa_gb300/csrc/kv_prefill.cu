@@ -52,13 +52,17 @@ static __device__ unsigned g_status_kv_prefill;
 
 namespace kvp {
 
-constexpr int TILE = 128;                // keys of a tile, rows of an MMA
-constexpr int ROWS = 256;                // query rows of an item
+constexpr int TILE = kPrefillTile;       // keys of a tile, rows of an MMA
+constexpr int ROWS = kPrefillRows;       // query rows of an item
 constexpr int OP_BYTES = TILE * 256;     // 128 rows x 128 binary16
 // What an item costs beside its tiles, in tiles: 1, 2, 3 and 4 took 319, 317, 314 and 312
 // us for the prompts above.
-constexpr int kItemTiles = 4;
+constexpr int kItemTiles = kPrefillItemTiles;
 constexpr int kMinUnits = 6;             // least units of a run: a shorter one costs more to join than it saves
+// Of prefixes, which leave SMs to the requests' own keys: 3, 4, 6, 8 and 10 units took 58, 57, 56, 46 and 51 us for one
+// prefix of 8192 keys, 64 requests with up to 1024 keys behind it, and 41, 32, 33, 36 and 39 us for six
+// prefixes of up to 3000 keys, 30 requests with up to 300.
+constexpr int kMinPrefixUnits = 8;
 constexpr float kOffset = 8.0f, kLazy = 6.0f;  // as in kv_attn.cu
 
 constexpr int OFF_Q = 0;                           // tiles A, B
@@ -91,7 +95,7 @@ struct Item {
   int na, nb;       // tiles of A and of B in this part
   int slot;         // -1: the whole item, else partial record
   int lo, hi, at, jump;  // as in Request
-  int pad;
+  int parts;        // of the item that begins here: CTAs that hold one (0: this one alone)
 };
 static_assert(sizeof(Item) == 64, "an item record");
 
@@ -147,7 +151,7 @@ template <int KIND>
 __device__ __forceinline__ Request request_of(const KvAttnArgs& a, int r) {
   Request x;
   x.lo = x.hi = x.at = x.jump = 0;
-  if constexpr (KIND == kPrefix) {  // checked by kv_shared_kernel, whose result is 0 for a group that is none
+  if constexpr (KIND == kPrefix) {  // checked by kv_shared_plan_kernel, whose result is 0 for a group that is none
     x.kv = __ldg(a.prefix + r);
     x.q0 = x.n = 0;
     if (x.kv <= 0) return x;
@@ -245,7 +249,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + OFF_MISC + 8);
   unsigned* status = &g_status_kv_prefill;
 
-  asm volatile("griddepcontrol.launch_dependents;");
+  if (KIND != kPrefix) asm volatile("griddepcontrol.launch_dependents;");
   if (tid == 0) {
     *abort_flag = 0;
     for (int s = 0; s < 2; s++) {
@@ -274,14 +278,20 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // for the line, and what runs before it
+  // the kernel behind the prefixes' reads what was written before this one
+  if (KIND == kPrefix) asm volatile("griddepcontrol.launch_dependents;");
   // by the scheduler's lane, which may replace it: no barrier follows that would order two threads
-  if (warp == 1 && lane == 0) headers[blockIdx.x].parts = 0;
+  if (!kRecords<KIND> && warp == 1 && lane == 0) headers[blockIdx.x].parts = 0;
   const int64_t total = __ldcg(line + a.R);
   if (total == 0) {  // no request with that many rows
     if (warp == 0) tmem_dealloc(tmem, 512);
     return;
   }
   constexpr bool kHides = KIND == kWindow || KIND == kTail;
+  if (kRecords<KIND> && int64_t(blockIdx.x) * a.min_units >= total) {  // no run: makes room
+    if (warp == 0) tmem_dealloc(tmem, 512);
+    return;
+  }
   const Item* items = reinterpret_cast<const Item*>(smem + OFF_ITEM);
   // whole warp: waits for item i of the run and reads it; a part with rows == 0 ends the run
   auto take = [&](int i, Item& it, bool& ok) {
@@ -293,6 +303,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       it.q0 = v->q0, it.n = v->n, it.kv = v->kv, it.t0 = v->t0;
       it.na = v->na, it.nb = v->nb, it.slot = v->slot;
       if (kHides) it.lo = v->lo, it.hi = v->hi, it.at = v->at, it.jump = v->jump;
+      if (kRecords<KIND>) it.parts = v->parts;
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(BAR(B_IEMPTY + (i & 1)));
@@ -419,7 +430,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       __syncwarp();
     } else if (warp == 1 && lane == 0) {
       // -------------------------------------------------------------- scheduler
-      const int64_t most = (total + kMinUnits - 1) / kMinUnits;
+      const int64_t most = (total + a.min_units - 1) / a.min_units;
       const int64_t C = most < int64_t(gridDim.x) ? most : int64_t(gridDim.x);
       const int64_t run = total / C, extra = total - run * C;  // the first `extra` CTAs take one unit more
       int64_t pos = run * blockIdx.x + min(extra, int64_t(blockIdx.x));
@@ -439,6 +450,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
         v->q0 = it.q0, v->n = it.n, v->kv = it.kv, v->t0 = it.t0;
         v->na = it.na, v->nb = it.nb, v->slot = it.slot;
         if (kHides) v->lo = it.lo, v->hi = it.hi, v->at = it.at, v->jump = it.jump;
+        if (kRecords<KIND>) v->parts = it.parts;
         mbar_arrive(BAR(B_IFULL + (i & 1)));
         i++;
         return true;
@@ -483,12 +495,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
             it.na = max(0, min(va, t1) - t0);
             it.nb = max(0, min(vb, t1) - t0);
             it.slot = t0 > 0 ? 2 * int(blockIdx.x) : t1 < tiles ? 2 * int(blockIdx.x) + 1 : -1;
+            it.parts = 0;
             if (t0 == 0 && t1 < tiles) {
               const int64_t last = at + units - 1, larger = extra * (run + 1);
               Header hd;
               hd.r = r, hd.h = h, hd.row0 = row0;
               hd.parts = int(last < larger ? last / (run + 1) : extra + (last - larger) / run) - int(blockIdx.x);
-              headers[blockIdx.x] = hd;
+              it.parts = hd.parts + 1;
+              if (!kRecords<KIND>) headers[blockIdx.x] = hd;
             }
             ok = publish(it);
           }
@@ -498,7 +512,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       if (ok) {
         Item none;
         none.r = none.h = none.row0 = none.rows = none.q0 = none.n = none.kv = none.t0 = none.na = none.nb = none.slot = 0;
-        none.lo = none.hi = none.at = none.jump = 0;
+        none.lo = none.hi = none.at = none.jump = none.parts = 0;
         publish(none);
       }
     }
@@ -834,22 +848,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       tc_fence_after();
       const float nanv = __uint_as_float(0x7FC00000u);
       const int hd = it.h * a.G + (it.row0 + idx) - tok * a.G;
-      // where the row's prefix has been done for the group: its m, l, o join these
       const int64_t out_row = int64_t(it.q0 + tok) * a.Hq + hd;
-      const bool behind = KIND == kTail && it.hi > 0 && valid && it.slot < 0;
-      float w = 1.0f, u = 0.0f;
-      if (behind) {
-        const float2 ml = a.prefix_ml[out_row];
-        const float top = fmaxf(m, ml.x);
-        w = m == -INFINITY ? 1.0f : ex2(m - top);
-        u = ml.x == -INFINITY ? 1.0f : ex2(ml.x - top);
-        l = w * l + u * ml.y;
-        m = top;
-      }
       const float f = l == 0.0f ? 1.0f : vst / l;
       uint4* orow = reinterpret_cast<uint4*>(a.o + out_row * 128);
-      const float4* prow = reinterpret_cast<const float4*>(a.prefix_o + out_row * 128);
-      float* record = it.slot < 0 ? a.prefix_o + out_row * 128 : partials[it.slot].o[idx];  // kPrefix: there is always one
+      float* record = it.slot < 0 ? a.rows_o + out_row * 128 : partials[it.slot].o[idx];  // kRecords: there is always one
 #pragma unroll
       for (int c = 0; c < 4; c++) {
         float o[32];
@@ -867,17 +869,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
           for (int e = 0; e < 32; e++)
             if ((nan_blocks >> (2 * c + (e >> 4))) & 1u) o[e] = nanv;
         }
-        if (behind) {
-#pragma unroll
-          for (int e = 0; e < 8; e++) {
-            const float4 v = prow[8 * c + e];
-            o[4 * e] = w * o[4 * e] + u * v.x;
-            o[4 * e + 1] = w * o[4 * e + 1] + u * v.y;
-            o[4 * e + 2] = w * o[4 * e + 2] + u * v.z;
-            o[4 * e + 3] = w * o[4 * e + 3] + u * v.w;
-          }
-        }
-        if (valid && it.slot < 0 && KIND != kPrefix) {
+        if (valid && it.slot < 0 && !kRecords<KIND>) {
 #pragma unroll
           for (int e = 0; e < 4; e++)
             orow[4 * c + e] = make_uint4(pack_bf16(o[8 * e] * f, o[8 * e + 1] * f), pack_bf16(o[8 * e + 2] * f, o[8 * e + 3] * f),
@@ -893,12 +885,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
         if (it.slot >= 0) {
           partials[it.slot].m[idx] = m;
           partials[it.slot].l[idx] = l;
-        } else if (KIND == kPrefix) {
-          a.prefix_ml[out_row] = make_float2(m, l);
+        } else if (kRecords<KIND>) {
+          a.rows_ml[out_row] = make_float2(m, l);
         } else {
           a.lse[int64_t(hd) * a.total_q + it.q0 + tok] = l == 0.0f ? -INFINITY : (m - kOffset + log2f(l)) * 0.6931471805599453f;
         }
       }
+      if (kRecords<KIND> && valid && it.t0 == 0) a.places[out_row] = make_uint2(blockIdx.x, kv_place(it.parts, idx, true, kHides && it.hi > 0));
       st += n_x;
       kt += nmax;
     }
@@ -943,42 +936,11 @@ __global__ void __launch_bounds__(256) kv_prefill_join_kernel(KvAttnArgs a, cons
   const float vst = FMT == 1 ? __ldg(a.c.v_scale) : 1.0f;
   const int rr = hd.row0 + idx, tok = rr / a.G, head = hd.h * a.G + rr - tok * a.G;
   const int64_t row = int64_t(x.q0 + tok) * a.Hq + head;
-  if (KIND == kPrefix) {
-    reinterpret_cast<float4*>(a.prefix_o + row * 128)[lane] = s;
-    if (lane == 0) a.prefix_ml[row] = make_float2(M, L);
-    return;
-  }
-  if (KIND == kTail && x.hi > 0) {
-    const float2 ml = a.prefix_ml[row];
-    const float4 v = reinterpret_cast<const float4*>(a.prefix_o + row * 128)[lane];
-    const float top = fmaxf(M, ml.x);
-    const float w = M == -INFINITY ? 1.0f : ex2(M - top), u = ml.x == -INFINITY ? 1.0f : ex2(ml.x - top);
-    L = w * L + u * ml.y;
-    M = top;
-    s = make_float4(w * s.x + u * v.x, w * s.y + u * v.y, w * s.z + u * v.z, w * s.w + u * v.w);
-  }
   const float f = L == 0.0f ? 1.0f : vst / L;
   *reinterpret_cast<uint2*>(a.o + row * 128 + lane * 4) = make_uint2(pack_bf16(s.x * f, s.y * f), pack_bf16(s.z * f, s.w * f));
   if (lane == 0)
     a.lse[int64_t(head) * a.total_q + x.q0 + tok] =
         L == 0.0f ? -INFINITY : (M - kOffset + log2f(L)) * 0.6931471805599453f;
-}
-
-// Launches a kernel that may start before the one before it has ended, and waits for it
-// itself.
-template <typename... P, typename... A>
-cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(unsigned(threads));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
 template <int KIND, int FMT>
@@ -995,7 +957,7 @@ cudaError_t launch(const KvAttnArgs& a, uint8_t* ws, cudaStream_t st) {
   Partial* partials = reinterpret_cast<Partial*>(ws + line_bytes(a.R) + header_bytes(ctas));
   e = launch_early(kv_prefill_kernel<KIND, FMT>, dim3(unsigned(ctas)), NTHREADS, SMEM_BYTES, st, a, static_cast<const int64_t*>(line), headers,
                    partials);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || kRecords<KIND>) return e;
   return launch_early(kv_prefill_join_kernel<KIND, FMT>, dim3(unsigned(ctas), ROWS / 8), 256, 0, st, a, static_cast<const Header*>(headers),
                       static_cast<const Partial*>(partials));
 }
@@ -1007,11 +969,13 @@ size_t kv_prefill_workspace(int R) {
   return kvp::line_bytes(R) + kvp::header_bytes(ctas) + size_t(ctas) * 2 * sizeof(kvp::Partial);
 }
 
+uint8_t* kv_prefill_records(uint8_t* ws, int R) { return ws + kvp::line_bytes(R) + kvp::header_bytes(sm_count_current_device()); }
+
 namespace {
 
 template <int KIND>
 cudaError_t launch_line(const KvAttnArgs& a, int64_t* line, bool after_attn, cudaStream_t st) {
-  if (after_attn) return kvp::launch_early(kvp::kv_prefill_line_kernel<KIND>, dim3(1), 512, 0, st, a, line);
+  if (after_attn) return launch_early(kvp::kv_prefill_line_kernel<KIND>, dim3(1), 512, 0, st, a, line);
   kvp::kv_prefill_line_kernel<KIND><<<1, 512, 0, st>>>(a, line);
   return cudaGetLastError();
 }
@@ -1035,7 +999,9 @@ cudaError_t launch_kv_prefill_line(int kind, const KvAttnArgs& a, uint8_t* ws, b
   }
 }
 
-cudaError_t launch_kv_prefill(int kind, const KvAttnArgs& a, uint8_t* ws, cudaStream_t st) {
+cudaError_t launch_kv_prefill(int kind, const KvAttnArgs& args, uint8_t* ws, cudaStream_t st) {
+  KvAttnArgs a = args;
+  a.min_units = kind == kPrefix ? kvp::kMinPrefixUnits : kvp::kMinUnits;
   switch (kind) {
     case kAll: return launch_kind<kAll>(a, ws, st);
     case kWindow: return launch_kind<kWindow>(a, ws, st);

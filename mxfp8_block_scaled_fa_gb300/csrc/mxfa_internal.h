@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <utility>
 
 namespace mxfa {
 
@@ -244,6 +245,7 @@ struct KvAttnArgs {
   float scale_log2;       // softmax scale * log2(e)
   int causal;
   int whole;              // no context is long enough to be cut (set by launch_kv_attn)
+  int min_units;          // least units of a CTA's run in kv_prefill.cu (set by launch_kv_prefill)
   int split_rows;         // requests of more query rows (tokens x G) belong to kv_prefill.cu (set by launch_kv_attn)
   uint16_t* o;            // bf16 [total_q][Hq][128]
   float* lse;             // [Hq][total_q]
@@ -251,23 +253,60 @@ struct KvAttnArgs {
   int window, sinks;      // kWindow: a query at position p sees keys p - window + 1 .. p, and those before `sinks`
   const int32_t* starts;  // kPrefix: [R + 1] first requests of the groups, into cu_q and table
   const int32_t* prefix;  // kPrefix: [R] keys of a group's prefix; kTail: [R] keys that a request does not read itself
-  float* prefix_o;        // fp32 [total_q][Hq][128], (m, l) [total_q][Hq]: written by kPrefix, read by kTail
-  float2* prefix_ml;
+  // kPrefix, kTail: what a row's keys give, for kv_shared_join_kernel: rows in one piece o [total_q][Hq][128], (m, l)
+  // [total_q][Hq]; and of all rows [total_q][Hq] (first CTA, kv_place()) of their partial records
+  float* rows_o;
+  float2* rows_ml;
+  uint2* places;
+  int late;               // the kernel before this one may still run, and ends before this one does
 };
 // What the keys of an attention call are: all up to the query; a window of them and the first ones; the groups'
-// prefixes, for all of a group's queries (results stay in prefix_o, prefix_ml); what is behind them.
+// prefixes, for all of a group's queries; what is behind them.
 enum KvKind { kAll = 0, kWindow = 1, kPrefix = 2, kTail = 3 };
+template <int KIND>
+constexpr bool kRecords = KIND == kPrefix || KIND == kTail;
+// A row's records: `parts` CTAs (0: one piece) have one, its row there, whether kv_prefill.cu's kernel wrote them, whether
+// the row has a prefix; 0 is a row without any.
+constexpr __host__ __device__ uint32_t kv_place(int parts, int row, bool many, bool prefix) {
+  return (uint32_t(parts) << 16) | (uint32_t(row) << 3) | (many ? 4u : 0u) | (prefix ? 2u : 0u) | 1u;
+}
+struct KvRecords {
+  uint8_t *few, *many;    // records of kv_attn.cu's and of kv_prefill.cu's kernel
+  int few_rows;           // rows of one of the former
+  uint8_t* many_ws;       // workspace of kv_prefill.cu
+};
+// Launches a kernel that may start before the one before it has ended, and waits for it
+// itself.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
 size_t kv_attn_workspace(int R, int max_q, int64_t max_k, int G);
 bool kv_attn_reaches(int max_q, int64_t max_k, int G);
 cudaError_t launch_kv_attn(int kind, const KvAttnArgs& a, cudaStream_t s);
 int64_t kv_window_reach(int max_q, int64_t max_k, int window, int sinks);
-struct KvSharedWs {
-  size_t ml, gpre, pre, pass, bytes;  // places of its parts
-};
-KvSharedWs kv_shared_workspace(int R, int groups, int64_t total_q, int max_q, int max_group_q, int64_t max_k, int Hq, int G);
+bool kv_attn_few(int max_q, int64_t max_k, int G);  // whether kv_prefill.cu has no part in a call
+KvRecords kv_attn_records(uint8_t* ws, int R, int max_q, int64_t max_k, int G);
+uint8_t* kv_prefill_records(uint8_t* ws, int R);
+size_t kv_shared_workspace(int R, int groups, int64_t total_q, int max_q, int max_group_q, int64_t max_k, int Hq, int G);
 cudaError_t launch_kv_attn_shared(const KvAttnArgs& a, const int32_t* prefix_lens, int groups, int max_group_q, cudaStream_t s);
 size_t kv_prefill_workspace(int R);
 cudaError_t launch_kv_prefill_line(int kind, const KvAttnArgs& a, uint8_t* ws, bool after_attn, cudaStream_t st);
+// Units of the line that kv_prefill.cu works off, of a group of n query tokens behind p keys.
+constexpr int kPrefillRows = 256, kPrefillTile = 128, kPrefillItemTiles = 4;
+constexpr __host__ __device__ int64_t kv_prefix_units(int n, int p, int G, int H) {
+  return (int64_t(n) * G + kPrefillRows - 1) / kPrefillRows * H * ((p + kPrefillTile - 1) / kPrefillTile + kPrefillItemTiles);
+}
 cudaError_t launch_kv_prefill(int kind, const KvAttnArgs& a, uint8_t* ws, cudaStream_t s);
 
 // ------------------------------------------------------------ rotary positions
@@ -345,6 +384,7 @@ unsigned read_status_bwd(cudaStream_t s);
 unsigned read_status_kv(cudaStream_t s);
 unsigned read_status_kv_attn(cudaStream_t s);
 unsigned read_status_kv_prefill(cudaStream_t s);
+unsigned read_status_kv_shared(cudaStream_t s);
 unsigned read_status_rope(cudaStream_t s);
 unsigned read_status_kv_pages(cudaStream_t s);
 
