@@ -22,7 +22,7 @@ static __device__ unsigned g_status_rope;
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 
 // The (cos, sin) of a token's pairs, times the gain, into a warp's `cs`.
 __device__ __forceinline__ void angles(const Rotation& r, int pos, int lane, float2* cs) {
@@ -39,11 +39,10 @@ __device__ __forceinline__ void angles(const Rotation& r, int pos, int lane, flo
   __syncwarp();
 }
 
-// A lane's cosines and sines: channels 8 l .. 8 l + 7 of a head.
+// A lane's cosines and sines: channels 8 l .. 8 l + 7 of a head, two to a register pair.
 template <bool INTER>
 struct Turn {
-  static constexpr int N = INTER ? 4 : 8;
-  float c[N], s[N];
+  float2 c[4], s[4];
   bool turned;
   int partner;
   __device__ __forceinline__ Turn(const float2* cs, int rot, int lane) {
@@ -53,10 +52,15 @@ struct Turn {
     const int first = !turned ? 0 : INTER ? 4 * l : second ? 8 * l - rot / 2 : 8 * l;
     partner = !turned ? lane : second ? lane - rot / 16 : lane + rot / 16;
 #pragma unroll
-    for (int e = 0; e < N; e += 2) {
-      const float4 v = *reinterpret_cast<const float4*>(cs + first + e);
-      c[e] = v.x, c[e + 1] = v.z;
-      s[e] = second ? v.y : -v.y, s[e + 1] = second ? v.w : -v.w;
+    for (int e = 0; e < (INTER ? 2 : 4); e++) {
+      const float4 v = *reinterpret_cast<const float4*>(cs + first + 2 * e);
+      if (INTER) {
+        c[2 * e] = make_float2(v.x, v.x), c[2 * e + 1] = make_float2(v.z, v.z);
+        s[2 * e] = make_float2(-v.y, v.y), s[2 * e + 1] = make_float2(-v.w, v.w);
+      } else {
+        c[e] = make_float2(v.x, v.z);
+        s[e] = second ? make_float2(v.y, v.w) : make_float2(-v.y, -v.w);
+      }
     }
   }
   // All lanes of the warp.
@@ -65,13 +69,12 @@ struct Turn {
     uint32_t y[4];
 #pragma unroll
     for (int e = 0; e < 4; e++) {
-      const float lo = bf_lo(w[e]), hi = bf_hi(w[e]);
-      if (INTER) {
-        y[e] = pack_bf16(fmaf(lo, c[e], hi * s[e]), fmaf(hi, c[e], -lo * s[e]));
-      } else {
-        const uint32_t p = __shfl_sync(0xFFFFFFFFu, w[e], partner);
-        y[e] = pack_bf16(fmaf(lo, c[2 * e], bf_lo(p) * s[2 * e]), fmaf(hi, c[2 * e + 1], bf_hi(p) * s[2 * e + 1]));
-      }
+      // the other channel of each pair: beside it, or in the partner's word
+      const uint32_t p = INTER ? w[e] : __shfl_sync(0xFFFFFFFFu, w[e], partner);
+      const float2 own = make_float2(bf_lo(w[e]), bf_hi(w[e]));
+      const float2 other = INTER ? make_float2(own.y, own.x) : make_float2(bf_lo(p), bf_hi(p));
+      const float2 r = ffma2(own, c[e], fmul2(other, s[e]));
+      y[e] = pack_bf16(r.x, r.y);
     }
     return turned ? make_uint4(y[0], y[1], y[2], y[3]) : x;
   }
@@ -171,10 +174,12 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append_rope_kernel(KvAppendRop
   }
 }
 
-// Heads a warp takes: fewer where there are few tokens, so that the call spreads over the GPU.
-int heads_per_part(int64_t tokens, int heads) {
+// Heads a warp takes, `most` at most: fewer where there are few tokens, so that the call spreads over the GPU; many
+// share a token's angles.  16384 tokens of 32 + 8 heads stored take 89, 74, 67 and 67 us with 8, 16, 32 and 64, of 32
+// heads turned 47, 43, 44 and 44 us.
+int heads_per_part(int64_t tokens, int heads, int most) {
   const int64_t warps = int64_t(sm_count_current_device()) * 32;
-  for (int n = 16; n > 2; n /= 2)
+  for (int n = most; n > 2; n /= 2)
     if (tokens * ((heads + n - 1) / n) >= warps) return n;
   return 2;
 }
@@ -196,7 +201,7 @@ void append_n(const KvAppendRopeArgs& a, unsigned grid, cudaStream_t s) {
 cudaError_t launch_rope(const RopeArgs& args, cudaStream_t s) {
   clear_stale_error();
   RopeArgs a = args;
-  a.heads_per_part = heads_per_part(a.tokens, a.H);
+  a.heads_per_part = heads_per_part(a.tokens, a.H, 16);
   a.parts = (a.H + a.heads_per_part - 1) / a.heads_per_part;
   const int64_t grid = (a.tokens * a.parts + kWarps - 1) / kWarps;
   if (a.rot.inter) rope_n<true>(a, unsigned(grid), s);
@@ -207,7 +212,7 @@ cudaError_t launch_rope(const RopeArgs& args, cudaStream_t s) {
 cudaError_t launch_kv_append_rope(const KvAppendRopeArgs& args, cudaStream_t s) {
   clear_stale_error();
   KvAppendRopeArgs a = args;
-  a.heads_per_part = heads_per_part(a.tokens, a.Hq + 2 * a.c.H);
+  a.heads_per_part = heads_per_part(a.tokens, a.Hq + 2 * a.c.H, 32);
   a.q_parts = (a.Hq + a.heads_per_part - 1) / a.heads_per_part;
   a.kv_parts = (2 * a.c.H + a.heads_per_part - 1) / a.heads_per_part;
   const int64_t grid = (a.tokens * (a.q_parts + a.kv_parts) + kWarps - 1) / kWarps;
