@@ -98,22 +98,29 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(RopeArgs a) {
   const int pos = __ldg(a.positions + token);
   if (pos < 0) return;
   const int h0 = int(item - token * a.parts) * a.heads_per_part, h1 = min(h0 + a.heads_per_part, a.H);
-  angles(a.rot, pos, lane, s_cs[warp]);
-  const Turn<INTER> turn(s_cs[warp], a.rot.rot, lane);
   const uint16_t* x = a.x + token * a.x_stride + (lane & 15) * 8;
   uint16_t* y = a.y + token * a.y_stride + (lane & 15) * 8;
-  for (int h = h0 + (lane >> 4); h - (lane >> 4) < h1; h += 2 * N) {
-    uint4 v[N];
+  uint4 v[N];
+  auto load = [&](int h) {
 #pragma unroll
     for (int i = 0; i < N; i++) {
       v[i] = make_uint4(0, 0, 0, 0);
       if (h + 2 * i < h1) v[i] = load_stream(reinterpret_cast<const uint4*>(x + (h + 2 * i) * 128));
     }
+  };
+  int h = h0 + (lane >> 4);
+  load(h);  // on their way while the angles are computed
+  angles(a.rot, pos, lane, s_cs[warp]);
+  const Turn<INTER> turn(s_cs[warp], a.rot.rot, lane);
+  while (true) {
 #pragma unroll
     for (int i = 0; i < N; i++) {
       const uint4 o = turn(v[i]);
       if (h + 2 * i < h1) __stcs(reinterpret_cast<uint4*>(y + (h + 2 * i) * 128), o);
     }
+    h += 2 * N;
+    if (h - (lane >> 4) >= h1) break;
+    load(h);
   }
 }
 
@@ -142,14 +149,12 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append_rope_kernel(KvAppendRop
   }
   const int all = is_q ? a.Hq : 2 * a.c.H;
   const int h0 = (is_q ? part : part - a.q_parts) * a.heads_per_part, h1 = min(h0 + a.heads_per_part, all);
-  angles(a.rot, pos, lane, s_cs[warp]);
-  const Turn<INTER> turn(s_cs[warp], a.rot.rot, lane);
   const uint16_t* q = a.q + token * a.q_stride;
   const uint16_t* k = a.k + token * a.k_stride;
   const uint16_t* v = a.v + token * a.v_stride;
   uint16_t* y = a.y + token * a.y_stride;
-  for (int h = h0 + (lane >> 4); h - (lane >> 4) < h1; h += 2 * N) {
-    uint4 x[N];
+  uint4 x[N];
+  auto load = [&](int h) {
 #pragma unroll
     for (int i = 0; i < N; i++) {
       const int r = h + 2 * i;
@@ -159,6 +164,12 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append_rope_kernel(KvAppendRop
         x[i] = load_stream(reinterpret_cast<const uint4*>(src + l16 * 8));
       }
     }
+  };
+  int h = h0 + (lane >> 4);
+  load(h);  // on their way while the angles are computed
+  angles(a.rot, pos, lane, s_cs[warp]);
+  const Turn<INTER> turn(s_cs[warp], a.rot.rot, lane);
+  while (true) {
 #pragma unroll
     for (int i = 0; i < N; i++) {
       const int r = h + 2 * i;
@@ -171,6 +182,9 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append_rope_kernel(KvAppendRop
         kv_store_row<FMT>(a.c, r < h1, is_v, at, l16, is_v ? x[i] : o);
       }
     }
+    h += 2 * N;
+    if (h - (lane >> 4) >= h1) break;
+    load(h);
   }
 }
 
