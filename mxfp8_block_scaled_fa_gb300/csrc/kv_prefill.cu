@@ -205,13 +205,24 @@ __global__ void __launch_bounds__(512) kv_prefill_line_kernel(KvAttnArgs a, int6
   for (int r0 = 0; r0 < a.R; r0 += 512) {
     const int r = r0 + threadIdx.x;
     int64_t u = 0;
-    if (r < a.R) {
-      Request x = request_of<KIND>(a, r);
-      for (int row0 = 0; row0 < x.n * a.G; row0 += ROWS) {
-        item_of<KIND>(a, x, row0);
-        u += tiles_of(a, x, row0) + kItemTiles;
+    Request x;
+    x.q0 = x.n = x.kv = x.lo = x.hi = x.at = x.jump = 0;
+    if (r < a.R) x = request_of<KIND>(a, r);
+    // a block of rows a lane, of the warp's requests one after another
+    for (unsigned left = __ballot_sync(0xFFFFFFFFu, x.n > 0); left; left &= left - 1) {
+      const int who = __ffs(left) - 1;
+      Request y;
+      y.q0 = 0;
+      y.n = __shfl_sync(0xFFFFFFFFu, x.n, who), y.kv = __shfl_sync(0xFFFFFFFFu, x.kv, who);
+      y.lo = y.hi = y.at = 0, y.jump = __shfl_sync(0xFFFFFFFFu, x.jump, who);
+      int64_t all = 0;
+      for (int row0 = lane * ROWS; row0 < y.n * a.G; row0 += 32 * ROWS) {
+        item_of<KIND>(a, y, row0);
+        all += tiles_of(a, y, row0) + kItemTiles;
       }
-      u *= a.c.H;
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+      if (lane == who) u = all * a.c.H;
     }
     int64_t v = u;
 #pragma unroll
@@ -234,6 +245,9 @@ __global__ void __launch_bounds__(512) kv_prefill_line_kernel(KvAttnArgs a, int6
   // it runs beside kv_attn_kernel, and its end stands for that one's too
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
+
+// Bits 0 .. n - 1 of 64.
+__device__ __forceinline__ uint64_t below(int n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; }
 
 template <int KIND, int FMT>
 __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_constant__ KvAttnArgs a, const int64_t* line,
@@ -757,17 +771,23 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
         int kbase = (it.t0 + j) * TILE;
         if (kHides && kbase >= it.at) kbase += it.jump;
         kbase += 64 * h;
-        if (__any_sync(0xFFFFFFFFu, kbase + 64 > klim)) {
+        if (kHides) {
+          // a bit per key: a mask of bits costs little more than a select a key (comparisons two for each border)
+          const uint64_t seen = below(klim - kbase) & (~below(kfrom - kbase) | below(kgap - kbase));
+          if (__any_sync(0xFFFFFFFFu, ~seen != 0)) {
+#pragma unroll
+            for (int q = 0; q < 2; q++) {
+              const uint32_t w = uint32_t(seen >> (32 * q));
+#pragma unroll
+              for (int e = 0; e < 32; e++)
+                if (!((w >> e) & 1u)) s[32 * q + e] = -INFINITY;
+            }
+          }
+        } else if (__any_sync(0xFFFFFFFFu, kbase + 64 > klim)) {
           const int lim = klim - kbase;
 #pragma unroll
           for (int e = 0; e < 64; e++)
             if (e >= lim) s[e] = -INFINITY;
-        }
-        if (kHides && __any_sync(0xFFFFFFFFu, kbase < kfrom && kbase + 64 > kgap)) {
-          const int from = kfrom - kbase, gap = kgap - kbase;
-#pragma unroll
-          for (int e = 0; e < 64; e++)
-            if (e < from && e >= gap) s[e] = -INFINITY;
         }
         if (flags) {  // the same for the whole CTA
           const volatile uint32_t* bad = reinterpret_cast<const volatile uint32_t*>(smem + OFF_BAD) + f4 * 4 + 2 * h;
