@@ -839,7 +839,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
       __syncwarp();
       const int key0 = key_at(k_lo + step * kTile);
       const bool behind = KIND == kWindow && key0 < all_from && key0 + kStep > a.sinks;
-      if (seen0 != 0xFFFFFFFFu || key0 + kStep > all_see || behind) wk.template compute<true>(stage, qs, cs, seen0, lim, key0);
+      if (kHides && seen0 == 0u) {
+        // nothing: beside a few sinks, or before the window's first key
+      } else if (seen0 != 0xFFFFFFFFu || key0 + kStep > all_see || behind) wk.template compute<true>(stage, qs, cs, seen0, lim, key0);
       else wk.template compute<false>(stage, qs, cs, seen0, lim, key0);
       seen0 = seen1;
       seen1 = seen2;

@@ -46,6 +46,8 @@
 #include "mx_ptx.cuh"
 #include "mxfa_internal.h"
 
+#include <cmath>
+
 namespace mxfa {
 
 static __device__ unsigned g_status_kv_prefill;
@@ -58,11 +60,11 @@ constexpr int OP_BYTES = TILE * 256;     // 128 rows x 128 binary16
 // What an item costs beside its tiles, in tiles: 1, 2, 3 and 4 took 319, 317, 314 and 312
 // us for the prompts above.
 constexpr int kItemTiles = kPrefillItemTiles;
-constexpr int kMinUnits = 6;             // least units of a run: a shorter one costs more to join than it saves
-// Of prefixes, which leave SMs to the requests' own keys: 3, 4, 6, 8 and 10 units took 58, 57, 56, 46 and 51 us for one
-// prefix of 8192 keys, 64 requests with up to 1024 keys behind it, and 41, 32, 33, 36 and 39 us for six
-// prefixes of up to 3000 keys, 30 requests with up to 300.
-constexpr int kMinPrefixUnits = 8;
+// Least units of a run: a shorter one costs more to join than it saves.  Of prefixes 4, 6, 8 and 10 units took 52, 51, 47 and
+// 45 us for one of 8192 keys and 64 requests with up to 1024 keys behind it (whose kernel gets the other SMs), 29, 27, 30
+// and 32 us for six of up to 3000 keys and 30 requests with up to 300, and 6, 8 and 10 units 32, 35 and 40 us for one of
+// 8192 keys and next to nothing behind it.
+constexpr int kMinUnits = 6;
 constexpr float kOffset = 8.0f, kLazy = 6.0f;  // as in kv_attn.cu
 
 constexpr int OFF_Q = 0;                           // tiles A, B
@@ -302,7 +304,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
     return;
   }
   constexpr bool kHides = KIND == kWindow || KIND == kTail;
-  if (kRecords<KIND> && int64_t(blockIdx.x) * a.min_units >= total) {  // no run: makes room
+  // CTAs with a run: as many as it is worth, and for prefixes one an item at least
+  auto runs = [&]() -> int64_t {
+    int64_t most = (total + kMinUnits - 1) / kMinUnits;
+    if (KIND == kPrefix) most = max(most, int64_t(__ldcg(a.prefix + a.R)));
+    return min(most, int64_t(gridDim.x));
+  };
+  if (kRecords<KIND> && int64_t(blockIdx.x) >= runs()) {  // makes room
     if (warp == 0) tmem_dealloc(tmem, 512);
     return;
   }
@@ -364,23 +372,21 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       int kt = 0;             // tiles passed
       int sn = 0, qn = 0;     // S products and items of this tile so far
       bool ok = true;
-      // The loops over items have fixed trip counts and skip their turns once the run is
-      // over (64^4 items, far more than a run has): a loop that ended on a loaded item
+      // The loops over items have trip counts of the call's arguments (a.item_loops^3 is no fewer than
+      // a run can have) and skip their turns once the run is over: a loop that ended on a loaded item
       // would not be warp-uniform to the compiler, and the issue code in it took 130
-      // cycles a product instead of 64.
+      // cycles a product instead of 64.  A skipped turn takes 60 ns: four loops of 64, whatever the
+      // call, cost it 16 us.
       bool over = false;
       int i = 0;
 #pragma unroll 1
-      for (int l0 = 0; l0 < 64; l0++) {
+      for (int l0 = 0; l0 < a.item_loops; l0++) {
         if (over) continue;
 #pragma unroll 1
-      for (int l1 = 0; l1 < 64; l1++) {
+      for (int l1 = 0; l1 < a.item_loops; l1++) {
         if (over) continue;
 #pragma unroll 1
-      for (int l2 = 0; l2 < 64; l2++) {
-        if (over) continue;
-#pragma unroll 1
-      for (int l3 = 0; l3 < 64; l3++) {
+      for (int l2 = 0; l2 < a.item_loops; l2++) {
         if (over) continue;
         Item it;
         if (!take(i++, it, ok)) {
@@ -435,7 +441,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       }
       }
       }
-      }
       // every product has retired before TMEM is released
       tc_commit_w(BAR(B_TEAR));
       const unsigned long long t0 = global_ns();
@@ -444,8 +449,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       __syncwarp();
     } else if (warp == 1 && lane == 0) {
       // -------------------------------------------------------------- scheduler
-      const int64_t most = (total + a.min_units - 1) / a.min_units;
-      const int64_t C = most < int64_t(gridDim.x) ? most : int64_t(gridDim.x);
+      const int64_t C = runs();
       const int64_t run = total / C, extra = total - run * C;  // the first `extra` CTAs take one unit more
       int64_t pos = run * blockIdx.x + min(extra, int64_t(blockIdx.x));
       int64_t end = pos + run + (int64_t(blockIdx.x) < extra ? 1 : 0);
@@ -871,7 +875,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       const int64_t out_row = int64_t(it.q0 + tok) * a.Hq + hd;
       const float f = l == 0.0f ? 1.0f : vst / l;
       uint4* orow = reinterpret_cast<uint4*>(a.o + out_row * 128);
-      float* record = it.slot < 0 ? a.rows_o + out_row * 128 : partials[it.slot].o[idx];  // kRecords: there is always one
+      float4* const record = reinterpret_cast<float4*>(it.slot < 0 ? a.rows_o + out_row * 128 : partials[it.slot].o[idx]);  // kRecords: always one
 #pragma unroll
       for (int c = 0; c < 4; c++) {
         float o[32];
@@ -895,7 +899,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
             orow[4 * c + e] = make_uint4(pack_bf16(o[8 * e] * f, o[8 * e + 1] * f), pack_bf16(o[8 * e + 2] * f, o[8 * e + 3] * f),
                                          pack_bf16(o[8 * e + 4] * f, o[8 * e + 5] * f), pack_bf16(o[8 * e + 6] * f, o[8 * e + 7] * f));
         } else if (valid) {
-          float4* dst = reinterpret_cast<float4*>(record) + 8 * c;
+          float4* const dst = record + 8 * c;
 #pragma unroll
           for (int e = 0; e < 8; e++) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
@@ -1021,7 +1025,9 @@ cudaError_t launch_kv_prefill_line(int kind, const KvAttnArgs& a, uint8_t* ws, b
 
 cudaError_t launch_kv_prefill(int kind, const KvAttnArgs& args, uint8_t* ws, cudaStream_t st) {
   KvAttnArgs a = args;
-  a.min_units = kind == kPrefix ? kvp::kMinPrefixUnits : kvp::kMinUnits;
+  // every request's blocks for every head in one run, and the record that ends it
+  const int64_t items = int64_t(a.R) * a.c.H * ((int64_t(a.max_q) * a.G + kvp::ROWS - 1) / kvp::ROWS) + 1;
+  a.item_loops = int(ceil(cbrt(double(items)))) + 1;
   switch (kind) {
     case kAll: return launch_kind<kAll>(a, ws, st);
     case kWindow: return launch_kind<kWindow>(a, ws, st);

@@ -32,7 +32,8 @@ struct SharedArgs {
   int64_t words;
 };
 
-// The first CTA goes through the groups: prefix of group g at gpre[g] (0: none, or not as documented); the
+// The first CTA goes through the groups: prefix of group g at gpre[g] (0: none, or not as documented), behind them
+// their number of items for kv_prefill.cu; the
 // others take a request a thread: pre[r] (-1: of a group not as documented; 0: of none).
 __global__ void __launch_bounds__(kPlan) kv_shared_plan_kernel(KvAttnArgs a, SharedArgs s) {
   __shared__ int64_t s_sum[kPlan / 32];
@@ -62,6 +63,7 @@ __global__ void __launch_bounds__(kPlan) kv_shared_plan_kernel(KvAttnArgs a, Sha
     return;
   }
   int64_t base = 0;
+  int items = 0;
   for (int g0 = 0; g0 < s.groups; g0 += kPlan) {
     const int g = g0 + tid;
     int64_t u = 0;
@@ -70,7 +72,10 @@ __global__ void __launch_bounds__(kPlan) kv_shared_plan_kernel(KvAttnArgs a, Sha
       const int p = checked(g, n);
       if (p < 0) atomicOr(&g_status_kv_shared, DEV_BAD_INDEX);
       s.gpre[g] = max(p, 0);
-      if (p > 0) u = kv_prefix_units(n, p, a.G, a.c.H);
+      if (p > 0) {
+        u = kv_prefix_units(n, p, a.G, a.c.H);
+        items = min(int64_t(items) + kv_prefix_items(n, a.G, a.c.H), int64_t(1) << 20);
+      }
     }
     if (!s.line) continue;
     int64_t v = u;
@@ -90,7 +95,17 @@ __global__ void __launch_bounds__(kPlan) kv_shared_plan_kernel(KvAttnArgs a, Sha
     base += all;
     __syncthreads();
   }
-  if (s.line && tid == 0) s.line[s.groups] = base;
+  if (!s.line) return;
+  // items, as many as the GPU can have runs for (the sum of saturated counts is below 2^30)
+  items = __reduce_add_sync(0xFFFFFFFFu, items);
+  if (lane == 0) s_sum[warp] = items;
+  __syncthreads();
+  if (tid == 0) {
+    int64_t n = 0;
+    for (int w = 0; w < kPlan / 32; w++) n += s_sum[w];
+    s.gpre[s.groups] = int(min(n, int64_t(1) << 20));
+    s.line[s.groups] = base;
+  }
 }
 
 // One pass's records.
@@ -149,8 +164,18 @@ __global__ void __launch_bounds__(256) kv_shared_join_kernel(KvAttnArgs a, Pass 
   const Row x(tail, pt, r), y(prefix, two ? pp : pt, r);
   const int ny = two ? y.count() : 0, n = ny + x.count();
   auto ml_of = [&](int i) { return i < ny ? y.ml_of(i) : x.ml_of(i - ny); };
+  constexpr int N = 8;  // records in flight
+  float4 v[N];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+      const int i = min(i0 + j, n - 1);
+      v[j] = __ldcg((i < ny ? y.o_at(i) : x.o_at(i - ny)) + lane);
+    }
+  };
   // a lane has the (m, l) of every 32nd record: of the first 32, most often all, they stay
   const float2 mine = lane < n ? ml_of(lane) : make_float2(-INFINITY, 0.0f);
+  load(0);
   float M = mine.x;
   for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, ml_of(i).x);
 #pragma unroll
@@ -162,15 +187,8 @@ __global__ void __launch_bounds__(256) kv_shared_join_kernel(KvAttnArgs a, Pass 
     const float w = ml.x == -INFINITY ? 1.0f : ex2(ml.x - M);  // without keys l and O are 0, or NaN
     L += w * ml.y;
     const int end = min(32, n - i0);
-    constexpr int N = 8;  // in flight
     for (int j0 = 0; j0 < end; j0 += N) {
-      float4 v[N];
-#pragma unroll
-      for (int j = 0; j < N; j++) {
-        const int i = min(i0 + j0 + j, n - 1);
-        const float4* at = i < ny ? y.o_at(i) : x.o_at(i - ny);
-        v[j] = __ldcg(at + lane);
-      }
+      if (i0 + j0 > 0) load(i0 + j0);
 #pragma unroll
       for (int j = 0; j < N; j++) {
         const float u = __shfl_sync(0xFFFFFFFFu, w, j0 + j);
@@ -210,7 +228,7 @@ Places places_of(int R, int groups, int64_t total_q, int max_q, int max_group_q,
     p.ml[i] = take(rows * 8);
   }
   p.where = take(rows * 16);
-  p.gpre = take(size_t(groups) * 4);
+  p.gpre = take(size_t(groups) * 4 + 4);
   p.pre = take(size_t(R) * 4);
   p.pass[0] = take(kv_attn_workspace(groups, max_group_q, max_k, G));
   p.pass[1] = take(kv_attn_workspace(R, max_q, max_k, G));

@@ -245,14 +245,14 @@ struct KvAttnArgs {
   float scale_log2;       // softmax scale * log2(e)
   int causal;
   int whole;              // no context is long enough to be cut (set by launch_kv_attn)
-  int min_units;          // least units of a CTA's run in kv_prefill.cu (set by launch_kv_prefill)
+  int item_loops;         // trip count of kv_prefill.cu's loops over items (set by launch_kv_prefill)
   int split_rows;         // requests of more query rows (tokens x G) belong to kv_prefill.cu (set by launch_kv_attn)
   uint16_t* o;            // bf16 [total_q][Hq][128]
   float* lse;             // [Hq][total_q]
   uint8_t* ws;
   int window, sinks;      // kWindow: a query at position p sees keys p - window + 1 .. p, and those before `sinks`
   const int32_t* starts;  // kPrefix: [R + 1] first requests of the groups, into cu_q and table
-  const int32_t* prefix;  // kPrefix: [R] keys of a group's prefix; kTail: [R] keys that a request does not read itself
+  const int32_t* prefix;  // kPrefix: [R] keys of a group's prefix, and the number of all items; kTail: [R] keys that a request does not read itself
   // kPrefix, kTail: what a row's keys give, for kv_shared_join_kernel: rows in one piece o [total_q][Hq][128], (m, l)
   // [total_q][Hq]; and of all rows [total_q][Hq] (first CTA, kv_place()) of their partial records
   float* rows_o;
@@ -304,8 +304,9 @@ size_t kv_prefill_workspace(int R);
 cudaError_t launch_kv_prefill_line(int kind, const KvAttnArgs& a, uint8_t* ws, bool after_attn, cudaStream_t st);
 // Units of the line that kv_prefill.cu works off, of a group of n query tokens behind p keys.
 constexpr int kPrefillRows = 256, kPrefillTile = 128, kPrefillItemTiles = 4;
+constexpr __host__ __device__ int64_t kv_prefix_items(int n, int G, int H) { return (int64_t(n) * G + kPrefillRows - 1) / kPrefillRows * H; }
 constexpr __host__ __device__ int64_t kv_prefix_units(int n, int p, int G, int H) {
-  return (int64_t(n) * G + kPrefillRows - 1) / kPrefillRows * H * ((p + kPrefillTile - 1) / kPrefillTile + kPrefillItemTiles);
+  return kv_prefix_items(n, G, H) * ((p + kPrefillTile - 1) / kPrefillTile + kPrefillItemTiles);
 }
 cudaError_t launch_kv_prefill(int kind, const KvAttnArgs& a, uint8_t* ws, cudaStream_t s);
 
