@@ -619,8 +619,10 @@ mxfa_status mxfa_kv_append_rope(const mxfa_kv_cache* cache, const void* q, int64
 
 /* ------------------------------------------------- pages shared by requests
  * refs int32 [num_blocks] (DEVICE, zeros at first) counts the owners of a block beside the first.  A
- * request that may share pages is ended by mxfa_kv_free, not by a negative count in mxfa_kv_plan, which
- * gives back all its blocks whoever else owns them. */
+ * request that may share pages, or has given some up, is ended by mxfa_kv_free, not by a negative count in
+ * mxfa_kv_plan, which gives back all blocks of its row whoever else owns them.  Shared pages are full:
+ * a request goes on behind the tokens it was forked with, and one that is cut back to fewer (rejected
+ * drafts) is cut back no further than that. */
 
 /* mxfa_kv_fork -- requests that continue other ones: row dst[f] of block_table gets the first lens[f]
  * tokens of row src[f].  Whole pages are shared (refs + 1).  A last page that is not full would be
@@ -643,7 +645,7 @@ mxfa_status mxfa_kv_fork(int32_t* block_table, int R, int max_blocks, const int3
 /* mxfa_kv_free -- pages given up: for each f, entries first[f] .. end[f] - 1 of row rows[f] (ended requests,
  * rejected continuations, pages behind a window) have one owner fewer; negative entries are skipped.  Blocks left
  * without an owner go to the ring in ascending order.  The table stays as it is: an entry given up is not given
- * up again.  ring_size is at least num_blocks; ring_out may be ring_in; ring_out[2] is ring_in[2].  Rows and ranges
+ * up again.  ring_size is at least num_blocks (MXFA_ERR_INVALID_ARG); ring_out may be ring_in; ring_out[2] is ring_in[2].  Rows and ranges
  * outside the table, entries past num_blocks and blocks given up more often than owned are recorded as failed
  * index checks.  Other buffers that overlap are MXFA_ERR_INVALID_ARG. */
 mxfa_status mxfa_kv_free(const int32_t* block_table, int R, int max_blocks, const int32_t* rows, const int32_t* first,

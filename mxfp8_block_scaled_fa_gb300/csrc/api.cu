@@ -1214,6 +1214,7 @@ mxfa_status mxfa_kv_free(const int32_t* block_table, int R, int max_blocks, cons
   mxfa_status s = check_pages(block_table, R, max_blocks, F, refs, num_blocks, free_ring, ring_size, ring_in, ring_out);
   if (s) return s;
   if (F > 0 && (!rows || !first || !end)) return MXFA_ERR_INVALID_ARG;
+  if (ring_size < num_blocks) return MXFA_ERR_INVALID_ARG;
   if (max_blocks > (1 << 26)) return MXFA_ERR_UNSUPPORTED;
   if (!aligned4(rows) || !aligned4(first) || !aligned4(end)) return MXFA_ERR_MISALIGNED;
   const size_t list = size_t(F) * 4;

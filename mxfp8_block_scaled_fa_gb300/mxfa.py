@@ -1035,6 +1035,8 @@ def kv_attention(q: torch.Tensor, cache: KvCache, cu_q: torch.Tensor, kv_lens: t
                 return made
             if made is not None:
                 _check(made, "mxfa_kv_attn_window")
+        _int32("window", window, 1)
+        _int32("sinks", sinks, 0)
         return _attention(q, cache, cu_q, kv_lens, block_table, max_q, scale, out, ws, stream, ("window", window, sinks))
     if out is None and ws is None and stream is None:
         made = _fast().attention(q, cache.raw, cu_q, kv_lens, block_table, max_q, scale, causal)
@@ -1043,6 +1045,12 @@ def kv_attention(q: torch.Tensor, cache: KvCache, cu_q: torch.Tensor, kv_lens: t
         if made is not None:
             _check(made, "mxfa_kv_attn")
     return _attention(q, cache, cu_q, kv_lens, block_table, max_q, scale, out, ws, stream, ("all", causal))
+
+
+def _int32(name: str, value, least: int):
+    """A whole number that the C calls take as an int."""
+    if not least <= value < 1 << 31:
+        raise ValueError(f"{name} is {value}, expected {least} .. 2^31 - 1")
 
 
 def kv_attention_shared(q: torch.Tensor, cache: KvCache, cu_q: torch.Tensor, kv_lens: torch.Tensor,
@@ -1058,6 +1066,7 @@ def kv_attention_shared(q: torch.Tensor, cache: KvCache, cu_q: torch.Tensor, kv_
             return made
         if made is not None:
             _check(made, "mxfa_kv_attn_shared")
+    _int32("max_group_q", max_group_q, 0)
     return _attention(q, cache, cu_q, kv_lens, block_table, max_q, scale, out, ws, stream,
                       ("shared", group_starts, prefix_lens, max_group_q))
 

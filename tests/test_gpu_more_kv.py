@@ -122,6 +122,49 @@ def test_rope_gradient(mx):
             assert (np.abs(want - f64(dx)[..., c]) <= bound + 2.0 ** -18).all()
 
 
+@pytest.mark.parametrize("lengths", [None, [129, 0, 70, 256]])
+def test_rope_in_a_training_step(mx, lengths):
+    """q and k turned, quantized, attended; the gradients turned back: those of the unturned q and k."""
+    import torch
+    rng = np.random.default_rng(6)
+    seqs = mx.Seqs.dense(2, 192) if lengths is None else mx.Seqs.varlen(lengths, "cuda")
+    T, H = seqs.total, 2
+    rp, pos = mx.Rope.make(128), mx.rope_positions(seqs)
+    q, k, v, do = (bf16(rng, T, H, 128).cuda() for _ in range(4))
+    qr, kr = mx.rope(q, rp, pos), mx.rope(k, rp, pos)
+    check_rotation(qr, q, pos, rp)
+    scale = 128 ** -0.5
+    quant = lambda x, b: mx.quantize(x, b, seqs)
+    o, lse = mx.attention_fwd(quant(qr, mx.ROW), quant(kr, mx.ROW), quant(v, mx.COL), seqs, seqs, scale, causal=True)
+    dq, dk, dv = mx.attention_bwd(quant(qr, mx.SQ), quant(kr, mx.SQ), quant(v, mx.ROW), quant(do, mx.SQ), o, do, lse, seqs, seqs, scale, causal=True)
+    gq, gk = mx.rope_bwd(dq, rp, pos), mx.rope_bwd(dk, rp, pos)
+    check_rotation(gq, dq, pos, rp, inverse=True)
+    check_rotation(gk, dk, pos, rp, inverse=True)
+    # against differences of the unquantized loss <do, o>: MXFP8's own bar for a gradient's direction
+    n = 192 if lengths is None else 129
+    angle = more_ref.angles([int(t) for t in host(rp.turns)], range(n))
+
+    def loss(x, y):
+        xr, yr = (more_ref.rotate(z, angle, 128, False)[0] for z in (x, y))
+        w = np.einsum("ihd,jhd->hij", xr, yr) * scale
+        w = np.where(np.tril(np.ones((n, n), bool)), w, -np.inf)
+        p = np.exp(w - w.max(-1, keepdims=True))
+        p /= p.sum(-1, keepdims=True)
+        return (np.einsum("hij,jhd->ihd", p, f64(v)[:n]) * f64(do)[:n]).sum()
+    x, y = f64(q)[:n], f64(k)[:n]
+    for g, which in ((f64(gq)[:n], 0), (f64(gk)[:n], 1)):
+        along = g / np.linalg.norm(g)
+        args = [x, y]
+        step = []
+        for h in (1e-3, -1e-3):
+            moved = list(args)
+            moved[which] = args[which] + h * along
+            step.append(loss(*moved))
+        slope = (step[0] - step[1]) / 2e-3
+        assert abs(slope - np.linalg.norm(g)) <= 0.1 * np.linalg.norm(g)   # 20 dB, as for the gradients themselves
+    assert mx.device_status() == 0
+
+
 @pytest.mark.parametrize("fmt", [0, 1])
 @pytest.mark.parametrize("T,Hq,H,page,rot,inter", [
     (1, 1, 1, 16, 128, False), (3, 6, 3, 16, 64, True), (61, 32, 8, 16, 128, False), (257, 10, 5, 32, 96, False),
@@ -683,6 +726,71 @@ def test_two_streams_at_once(mx):
     compare(shared[0], shared[1], shared[2], shared[5], *outs[0][0], lambda r, n, k: more_ref.window_mask(n, k, 1 << 30, 0), scale=0.1)
     compare(c, q, cu, slots, *outs[0][1], lambda r, n, k: more_ref.window_mask(n, k, 333, 5), scale=0.1)
     assert mx.device_status() == 0
+
+
+def test_calls_on_a_given_stream(mx):
+    """With stream= the work and the memory of the results belong to that stream, behind what it already holds."""
+    import torch
+    rng = np.random.default_rng(51)
+    side = torch.cuda.Stream()
+    rp, pos = mx.Rope.make(32), dev(np.arange(3000))
+    x = bf16(rng, 3000, 8, 128).cuda()
+    want = mx.rope(x, rp, pos)
+    late = torch.empty_like(x)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        big = torch.randn(4096, 4096, device="cuda")
+        for _ in range(3):
+            big = big @ big * 1e-4                           # keeps the stream busy
+        late.copy_(x)
+    got = mx.rope(late, rp, pos, stream=side)
+    back = mx.rope_bwd(got, rp, pos, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want) and torch.equal(back, mx.rope_bwd(want, rp, pos))
+    c = new_cache(mx, 9, 2, 16, 0)
+    q, k, v = (bf16(rng, 5, n, 128).cuda() for n in (4, 2, 2))
+    slots = dev([3, 40, 41, 100, 7], np.int64)
+    torch.cuda.synchronize()
+    qr = mx.kv_append_rope(c, q, k, v, rp, pos[:5], slots, stream=side)
+    mx.kv_copy_blocks(c, dev([0, 2]), dev([8, 7]), stream=side)
+    t, refs, ring, state = dev([[0, 2], [-1, -1]]), mx.kv_refs(9), dev([1, 3, 4, 5, 6, 7, 8, -1, -1]), dev([0, 7, 0], np.int64)
+    torch.cuda.synchronize()
+    f = mx.kv_fork(t, dev([0]), dev([1]), dev([20]), refs, ring, state, 16, stream=side)
+    st = mx.kv_free(t, dev([0, 1]), dev([0, 0]), dev([2, 2]), refs, ring, f.ring_state, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(qr, mx.rope(q, rp, pos[:5])) and torch.equal(c.k[8], c.k[0]) and c.k[0].any()
+    assert host(f.lens).tolist() == [20] and host(st).tolist() == [1, 10, 0] and host(ring)[[7, 8, 0]].tolist() == [0, 1, 2]
+    assert mx.device_status() == 0
+
+
+def test_many_requests_behind_many_prefixes(mx):
+    """Hundreds of groups, of one and of several requests, and more requests than a CTA of the plan has threads."""
+    import torch
+    rng = np.random.default_rng(61)
+    groups = []
+    for g in range(300):
+        m = int(rng.integers(1, 5))
+        groups.append(([1] * m, int(rng.integers(0, 60)), [int(x) for x in rng.integers(1, 40, m)]))
+    c, q, cu, kv, table, slots, starts, pre, max_q, most, q_lens, _ = shared_case(mx, rng, 0, 16, 1, 4, groups, [(1, 5)], [(1, 9)])
+    o, lse = results(q)
+    mx.kv_attention_shared(q, c, cu, kv, table, starts, pre, max_q, most, 128 ** -0.5, out=(o, lse))
+    assert mx.device_status() == 0
+    compare(c, q, cu, slots, o, lse, lambda r, n, k: more_ref.window_mask(n, k, 1 << 30, 0))
+    # by the prompts' kernel: every group may have 20 tokens
+    o2, lse2 = results(q)
+    mx.kv_attention_shared(q, c, cu, kv, table, starts, pre, max_q, 20, 128 ** -0.5, out=(o2, lse2))
+    assert mx.device_status() == 0
+    compare(c, q, cu, slots, o2, lse2, lambda r, n, k: more_ref.window_mask(n, k, 1 << 30, 0))
+
+
+def test_prompts_of_many_blocks_in_a_window(mx):
+    """More blocks of rows than a warp has lanes, for one request beside others."""
+    rng = np.random.default_rng(71)
+    c, q, cu, kv, table, slots = build(mx, rng, 0, 64, 1, 8, [1200, 1, 40], [1300, 200, 90])
+    o, lse = results(q)
+    mx.kv_attention(q, c, cu, kv, table, 1200, 128 ** -0.5, out=(o, lse), window=130, sinks=3)
+    assert mx.device_status() == 0
+    compare(c, q, cu, slots, o, lse, lambda r, n, k: more_ref.window_mask(n, k, 130, 3))
 
 
 def test_far_blocks(mx):

@@ -242,6 +242,7 @@ def test_page_call_checks(mx, which):
         assert call(page=24) == 2 and call(w=1 << 27, R=1) == 2
     else:
         assert call(w=(1 << 26) + 1, R=1) == 2
+        assert call(rs=15) == 1                                      # fewer places than blocks
 
 
 def test_copy_checks(mx):
@@ -286,6 +287,12 @@ def test_python_refusals(mx):
         mx.kv_attention(*attn, 5, 0.1, sinks=4)                      # without a window
     with pytest.raises(ValueError):
         mx.kv_attention(*attn, 5, 0.1, causal=False, window=4)
+    for kw in (dict(window=0), dict(window=-3), dict(window=1 << 31), dict(window=(1 << 32) + 5), dict(window=4, sinks=-1),
+               dict(window=4, sinks=(1 << 32) + 1)):
+        with pytest.raises(ValueError):
+            mx.kv_attention(*attn, 5, 0.1, **kw)
+    with pytest.raises(ValueError):
+        mx.kv_attention_shared(*attn, i32(2), i32(1), 5, (1 << 32) + 5, 0.1)
     with pytest.raises(ValueError):
         mx.kv_attention(*attn, 5, 0.1, window=4)                     # not on a GPU
     with pytest.raises(ValueError):
