@@ -594,7 +594,7 @@ mxfa_status mxfa_kv_attn_shared(const mxfa_kv_cache* cache, const void* q, int64
 typedef struct {
   const int64_t* turns;
   int rot, layout;
-  float gain;
+  double gain;
 } mxfa_rotation;
 
 /* mxfa_rope -- y = x turned (before mxfa_quantize, mxfa_kv_append or mxfa_kv_attn), or with inverse = 1
@@ -602,7 +602,8 @@ typedef struct {
  *  x, y       bf16 rows of H * 128, consecutive tokens x_stride / y_stride elements apart (multiples of
  *             8, at least H * 128), 16-byte aligned; y may be x (same stride), else they do not overlap
  *  positions  DEVICE int32 [tokens], as mxfa_kv_plan gives them; negative: the token's row of y stays
- * fp32, one rounding to bf16.  y overlaps neither positions nor turns (MXFA_ERR_INVALID_ARG). */
+ * Each step is rounded once: c = fp32(gain cos t), s = fp32(gain sin t) (all but a few in ten thousand
+ * correctly), the fp32 products a c and b s, their fp32 difference or sum, and bf16 of it.  y overlaps neither positions nor turns (MXFA_ERR_INVALID_ARG). */
 mxfa_status mxfa_rope(const void* x, int64_t x_stride, void* y, int64_t y_stride, const int32_t* positions,
                       int64_t tokens, int H, int D, const mxfa_rotation* rot, int inverse, mxfa_stream_t stream);
 

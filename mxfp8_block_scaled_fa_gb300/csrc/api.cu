@@ -848,7 +848,7 @@ mxfa_status check_attn_buffers(const KvAttnArgs& a, size_t need, size_t ws_bytes
 }
 
 mxfa_status check_rotation(const mxfa_rotation* r, Rotation& x) {
-  if (!r || !r->turns || r->rot <= 0 || r->rot > 128 || !std::isfinite(r->gain)) return MXFA_ERR_INVALID_ARG;
+  if (!r || !r->turns || r->rot <= 0 || r->rot > 128 || !std::isfinite(float(r->gain))) return MXFA_ERR_INVALID_ARG;
   if (r->layout != MXFA_ROPE_HALF && r->layout != MXFA_ROPE_INTERLEAVED) return MXFA_ERR_INVALID_ARG;
   if (r->rot % 16) return MXFA_ERR_UNSUPPORTED;
   if (!aligned8(r->turns)) return MXFA_ERR_MISALIGNED;
@@ -856,7 +856,8 @@ mxfa_status check_rotation(const mxfa_rotation* r, Rotation& x) {
   x.rot = r->rot;
   x.inter = r->layout == MXFA_ROPE_INTERLEAVED ? 1 : 0;
   x.inverse = 0;
-  x.gain = r->gain;
+  x.gain = float(r->gain);
+  x.gain_rest = float(r->gain - double(x.gain));
   return MXFA_OK;
 }
 

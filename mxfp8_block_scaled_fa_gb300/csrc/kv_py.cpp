@@ -294,7 +294,7 @@ bool rotation(PyObject* const* a, int64_t index, mxfa_rotation& r) {
   r.turns = i64(turns);
   r.rot = int(2 * turns->numel());
   r.layout = a[1] == Py_True ? MXFA_ROPE_INTERLEAVED : MXFA_ROPE_HALF;
-  r.gain = float(PyFloat_AS_DOUBLE(a[2]));
+  r.gain = PyFloat_AS_DOUBLE(a[2]);
   return true;
 }
 PyObject* wrapped(const at::Tensor& t) { return THPVariable_Wrap(t); }

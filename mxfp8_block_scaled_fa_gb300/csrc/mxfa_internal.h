@@ -316,7 +316,7 @@ struct Rotation {
   int rot;                // channels that turn, a multiple of 16
   int inter;              // 1: pairs (2 i, 2 i + 1), 0: (i, i + rot / 2)
   int inverse;
-  float gain;
+  float gain, gain_rest;  // their sum
 };
 struct RopeArgs {
   const uint16_t* x;

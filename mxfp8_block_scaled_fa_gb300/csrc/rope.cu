@@ -5,11 +5,17 @@
 //   t = p f_i; the pair is channels (i, i + rot / 2) or (2 i, 2 i + 1); the other channels stay.
 // The gradient of (a, b) is the same turn by -t of the gradient of (a', b').
 //
+// Every step is one correctly rounded fp32 operation, as an elementwise program has them: c = fp32(g cos t) and
+// s = fp32(g sin t), two products, their sum, and bf16 of it.  So what an elementwise form of the same steps turns and
+// stores is the same codes here, where an fp32 step off would now and then move a 4-bit code by a quarter.
+//
 // Angles.  An fp32 product p f loses the angle for far positions (a position of 2^20 leaves 2^-4
 // radians), and fp64 is slow here, so frequencies are whole numbers of 2^-64ths of a turn: p times one,
 // modulo 2^64, is the fraction of a turn exactly (the frequency's own rounding, 2^-65 turns, grows to 2^-34 for
-// p = 2^31), and its upper 32 bits, as a signed fraction of a half turn, are the argument of sincospi: within
-// 2^-24 of pi radians, well below the bf16 results' 2^-9.
+// p = 2^31).  Its quarter turn, the nearest of 64 equal parts of that and the rest b, |b| <= pi / 256, are whole numbers, too, and
+//   cos(a + b) = cos a + (cos a (cos b - 1) - sin a sin b),  sin(a + b) = sin a + (sin a (cos b - 1) + cos a sin b)
+// with cos a, sin a, b and the first sum in pairs of fp32 values and short series for b: off by 2^-35 at most
+// before the rounding, so all but one in 3000 of the results are the correctly rounded ones.
 //
 // A warp takes some heads of one token: its lanes compute the token's angles once, two pairs a lane, and pass them
 // through shared memory; then sixteen lanes a head, eight channels a lane, whose partners in the half layout are
@@ -24,16 +30,85 @@ namespace {
 
 constexpr int kWarps = 4;
 
+// cos a, what it lacks of 53 bits, and sin a likewise: a = i pi / 128.
+__device__ const float4 kParts[33] = {
+    {0x1.0p+0f, 0x0.0p+0f, 0x0.0p+0f, 0x0.0p+0f},
+    {0x1.ffd886p-1f, 0x1.099a1ap-30f, 0x1.92156p-6f, -0x1.0b933p-31f},
+    {0x1.ff621ep-1f, 0x1.bcb6bep-28f, 0x1.91f66p-5f, -0x1.de44fep-30f},
+    {0x1.fe9cdap-1f, 0x1.a03108p-26f, 0x1.2d520ap-4f, -0x1.a63cc2p-29f},
+    {0x1.fd88dap-1f, 0x1.e89292p-28f, 0x1.917a6cp-4f, -0x1.eb25eap-31f},
+    {0x1.fc2648p-1f, -0x1.e3cc06p-26f, 0x1.f564e6p-4f, -0x1.2ad19ep-29f},
+    {0x1.fa7558p-1f, -0x1.eeb5d2p-30f, 0x1.2c8106p-3f, 0x1.d1cc28p-28f},
+    {0x1.f8765p-1f, -0x1.63ad16p-27f, 0x1.5e2144p-3f, 0x1.22cff2p-29f},
+    {0x1.f6297cp-1f, 0x1.feeb96p-26f, 0x1.8f8b84p-3f, -0x1.cb2cfap-30f},
+    {0x1.f38f3ap-1f, 0x1.8c9cb2p-26f, 0x1.c0b826p-3f, 0x1.4fc9ecp-28f},
+    {0x1.f0a7fp-1f, -0x1.1b73cap-27f, 0x1.f19f98p-3f, -0x1.37a83ap-29f},
+    {0x1.ed740ep-1f, 0x1.da1258p-27f, 0x1.111d26p-2f, 0x1.58fb3cp-29f},
+    {0x1.e9f416p-1f, -0x1.273a44p-26f, 0x1.294062p-2f, 0x1.dab3ep-27f},
+    {0x1.e6288ep-1f, 0x1.891c22p-26f, 0x1.4135cap-2f, -0x1.7d134p-27f},
+    {0x1.e2121p-1f, 0x1.3da1bap-27f, 0x1.58f9a8p-2f, -0x1.4a9c04p-27f},
+    {0x1.ddb13cp-1f, -0x1.2667b8p-26f, 0x1.708854p-2f, -0x1.e0b74cp-27f},
+    {0x1.d906bcp-1f, 0x1.e651a8p-26f, 0x1.87de2ap-2f, 0x1.abaa58p-28f},
+    {0x1.d4134ep-1f, -0x1.d646d8p-26f, 0x1.9ef794p-2f, 0x1.d476c6p-29f},
+    {0x1.ced7bp-1f, -0x1.786712p-26f, 0x1.b5d1p-2f, 0x1.3c2b98p-27f},
+    {0x1.c954b2p-1f, 0x1.3411f4p-29f, 0x1.cc66eap-2f, -0x1.b38ee8p-28f},
+    {0x1.c38b3p-1f, -0x1.cfe84ap-26f, 0x1.e2b5d4p-2f, -0x1.fe4272p-28f},
+    {0x1.bd7c0ap-1f, 0x1.8df2a6p-26f, 0x1.f8ba4ep-2f, -0x1.01d952p-28f},
+    {0x1.b72834p-1f, 0x1.465b9p-27f, 0x1.07387ap-1f, -0x1.b74004p-27f},
+    {0x1.b090a6p-1f, -0x1.fabf8p-27f, 0x1.11eb36p-1f, -0x1.7c969cp-26f},
+    {0x1.a9b662p-1f, 0x1.21d434p-26f, 0x1.1c73b4p-1f, -0x1.9465cep-27f},
+    {0x1.a29a7ap-1f, 0x1.189e08p-31f, 0x1.26d054p-1f, 0x1.9ba25cp-26f},
+    {0x1.9b3e04p-1f, 0x1.fce1dp-27f, 0x1.30ff8p-1f, -0x1.8f47e6p-28f},
+    {0x1.93a224p-1f, 0x1.324c8p-26f, 0x1.3affa2p-1f, 0x1.240a18p-26f},
+    {0x1.8bc806p-1f, 0x1.62a2e8p-26f, 0x1.44cf32p-1f, 0x1.424776p-27f},
+    {0x1.83b0ep-1f, 0x1.7ff2eep-26f, 0x1.4e6cacp-1f, -0x1.070686p-27f},
+    {0x1.7b5df2p-1f, 0x1.3557d8p-28f, 0x1.57d694p-1f, -0x1.6e626cp-26f},
+    {0x1.72d084p-1f, -0x1.02000ep-26f, 0x1.610b76p-1f, -0x1.5c5a64p-26f},
+    {0x1.6a09e6p-1f, 0x1.9fcef4p-27f, 0x1.6a09e6p-1f, 0x1.9fcef4p-27f}};
+
+// An exact product's rounding error; sums whose first term is the larger one, or 0.
+__device__ __forceinline__ float product_rest(float a, float b, float p) { return __fmaf_rn(a, b, -p); }
+__device__ __forceinline__ float2 sum_of(float a, float b, float rest) {
+  const float h = __fadd_rn(a, b);
+  return make_float2(h, __fadd_rn(__fsub_rn(b, __fsub_rn(h, a)), rest));
+}
+
+// (cos, sin) of a turn's 2^-64ths, times the gain, each rounded once.
+__device__ __forceinline__ float2 cos_sin(uint64_t turn, float gain, float gain_rest) {
+  const unsigned quarter = unsigned((turn + (1ull << 61)) >> 62);
+  const int64_t r = int64_t(turn - (uint64_t(quarter) << 62));      // |r| <= 2^61: an eighth of a turn
+  const int part = int((r + (int64_t(1) << 55)) >> 56);              // -32 .. 32
+  const int d = int((r - (int64_t(part) << 56)) >> 24);              // 2^-40ths of a turn
+  const float dh = __int2float_rn(d), dl = __int2float_rn(d - __float2int_rn(dh));
+  constexpr float kUnit = 0x1.921fb6p-38f, kUnitRest = -0x1.777a5cp-63f;  // 2 pi 2^-40
+  const float b = __fmul_rn(dh, kUnit);
+  const float b_rest = __fadd_rn(product_rest(dh, kUnit, b), __fmaf_rn(dh, kUnitRest, __fmul_rn(dl, kUnit)));
+  const float b2 = __fmul_rn(b, b);
+  const float sin_rest = __fmaf_rn(-__fmul_rn(b, b2), 1.0f / 6.0f, b_rest);                // sin b = b + this
+  const float cos_less = __fmul_rn(__fmaf_rn(b2, 1.0f / 24.0f, -0.5f), b2);                // cos b - 1
+  float4 t = __ldg(&kParts[abs(part)]);
+  if (part < 0) t.z = -t.z, t.w = -t.w;
+  const float p = __fmul_rn(t.z, b), q = __fmul_rn(t.x, b);
+  const float cr = __fsub_rn(__fmaf_rn(t.x, cos_less, t.y), __fmaf_rn(t.w, b, __fmaf_rn(t.z, sin_rest, product_rest(t.z, b, p))));
+  const float sr = __fadd_rn(__fmaf_rn(t.z, cos_less, t.w), __fmaf_rn(t.y, b, __fmaf_rn(t.x, sin_rest, product_rest(t.x, b, q))));
+  const float2 c = sum_of(t.x, -p, cr), s = sum_of(t.z, q, sr);
+  auto times_gain = [&](float2 x) {
+    const float y = __fmul_rn(x.x, gain);
+    return __fadd_rn(y, __fadd_rn(product_rest(x.x, gain, y), __fmaf_rn(x.y, gain, __fmul_rn(x.x, gain_rest))));
+  };
+  const float gc = times_gain(c), gs = times_gain(s);
+  const float2 v = quarter & 1u ? make_float2(-gs, gc) : make_float2(gc, gs);
+  return quarter & 2u ? make_float2(-v.x, -v.y) : v;
+}
+
 // The (cos, sin) of a token's pairs, times the gain, into a warp's `cs`.
 __device__ __forceinline__ void angles(const Rotation& r, int pos, int lane, float2* cs) {
 #pragma unroll
   for (int i = 0; i < 2; i++) {
     const int pair = lane + 32 * i;
     if (2 * pair < r.rot) {
-      const uint64_t turn = uint64_t(uint32_t(pos)) * __ldg(r.turns + pair);
-      float s, c;
-      sincospif(float(int32_t(turn >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
-      cs[pair] = make_float2(c * r.gain, (r.inverse ? -s : s) * r.gain);
+      const float2 v = cos_sin(uint64_t(uint32_t(pos)) * __ldg(r.turns + pair), r.gain, r.gain_rest);
+      cs[pair] = make_float2(v.x, r.inverse ? -v.y : v.y);
     }
   }
   __syncwarp();
@@ -73,8 +148,10 @@ struct Turn {
       const uint32_t p = INTER ? w[e] : __shfl_sync(0xFFFFFFFFu, w[e], partner);
       const float2 own = make_float2(bf_lo(w[e]), bf_hi(w[e]));
       const float2 other = INTER ? make_float2(own.y, own.x) : make_float2(bf_lo(p), bf_hi(p));
-      const float2 r = ffma2(own, c[e], fmul2(other, s[e]));
-      y[e] = pack_bf16(r.x, r.y);
+      // rounded one by one: packed pairs of products and sums would be merged into a multiply-add (82.8 instead of
+      // 84.9 us for 16384 tokens stored, and some bf16 results another)
+      y[e] = pack_bf16(__fadd_rn(__fmul_rn(own.x, c[e].x), __fmul_rn(other.x, s[e].x)),
+                       __fadd_rn(__fmul_rn(own.y, c[e].y), __fmul_rn(other.y, s[e].y)));
     }
     return turned ? make_uint4(y[0], y[1], y[2], y[3]) : x;
   }

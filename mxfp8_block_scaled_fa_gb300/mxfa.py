@@ -709,7 +709,7 @@ ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 
 class Rotation(ctypes.Structure):
     """mxfa_rotation: the device pointer of a rotation's turns, and its form."""
-    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int), ("layout", ctypes.c_int), ("gain", ctypes.c_float)]
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int), ("layout", ctypes.c_int), ("gain", ctypes.c_double)]
 
 
 def mxfa_rope(x, x_stride, y, y_stride, positions, tokens, H, D, rot: Rotation, inverse, stream=None):

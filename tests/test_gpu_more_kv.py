@@ -41,13 +41,27 @@ def make_rope(mx, rot, inter, gain, rng):
 
 
 def check_rotation(y, x, positions, rp, inverse=False):
+    import torch
     x, y, pos = f64(x), f64(y), np.asarray(host(positions), np.int64)
     rot = 2 * rp.turns.numel()
     angle = more_ref.angles([int(t) for t in host(rp.turns)], pos)
-    want, z = more_ref.rotate(x, angle, rot, rp.interleaved, float(np.float32(rp.gain)), inverse)
+    want, z = more_ref.rotate(x, angle, rot, rp.interleaved, rp.gain, inverse)
     err = np.abs(y - want) - (2.0 ** -8 * np.abs(want) + 2.0 ** -20 * z + 2.0 ** -134)
     assert err.max() <= 0, (float(err.max()), np.unravel_index(err.argmax(), err.shape))
     np.testing.assert_array_equal(y[..., rot:], x[..., rot:])
+    # step by step in fp32, as an elementwise form has it; a cosine or sine may be one step off (2^-23 of it at most)
+    f32 = kv_ref.f32
+    c, s = f32(rp.gain * np.cos(angle))[:, None], f32(rp.gain * np.sin(angle))[:, None] * (-1 if inverse else 1)
+    i = np.arange(rot // 2)
+    a, b = (2 * i, 2 * i + 1) if rp.interleaved else (i, i + rot // 2)
+    v = x.copy()
+    with np.errstate(over="ignore", under="ignore"):
+        v[..., a] = f32(f32(x[..., a] * c) - f32(x[..., b] * s))
+        v[..., b] = f32(f32(x[..., b] * c) + f32(x[..., a] * s))
+    to_bf16 = lambda w: torch.from_numpy(w.astype(np.float32)).bfloat16().double().numpy()
+    low, mid, high = (to_bf16(v + d * z) for d in (-2.0 ** -23, 0.0, 2.0 ** -23))
+    assert ((low <= y) & (y <= high)).all()
+    assert (y != mid).mean() <= 1e-5 + 1.0 / y.size
 
 
 @pytest.mark.parametrize("inverse", [False, True])

@@ -112,7 +112,7 @@ def _rot(mx, **kw):
 
 
 BAD_ROTATIONS = [(dict(turns=None), 1), (dict(rot=0), 1), (dict(rot=256), 1), (dict(layout=2), 1), (dict(gain=float("nan")), 1),
-                 (dict(gain=float("inf")), 1), (dict(rot=24), 2), (dict(turns=0x1004), 3)]
+                 (dict(gain=float("inf")), 1), (dict(gain=1e39), 1), (dict(rot=24), 2), (dict(turns=0x1004), 3)]
 
 
 def test_rope_checks(mx):
