@@ -222,12 +222,13 @@ __device__ __forceinline__ int table_row(const KvAttnArgs& a, int r) {
 }
 __device__ __forceinline__ int tiles_of(const Request& x) { return max(1, (x.kv - x.jump + kTile - 1) / kTile); }
 
-// N = 4 or 8 channels from c of a finished row: `row` = token * Hq + head; m, l, o of its keys.  Records stay as
-// they are, for kv_shared_join_kernel.
+// N = 4 or 8 channels from c of a finished row: `row` = token * Hq + head; m, l, o of its keys.  A record stays as
+// it is, for kv_shared_join_kernel.
 template <int KIND, int N>
-__device__ __forceinline__ void finish(const KvAttnArgs& a, int64_t token, int head, int c, float m, float l, const float (&o)[N], float vst) {
+__device__ __forceinline__ void finish(const KvAttnArgs& a, int64_t token, int head, int c, float m, float l, const float (&o)[N], float vst,
+                                       bool record) {
   const int64_t row = token * a.Hq + head;
-  if constexpr (kRecords<KIND>) {
+  if (kRecords<KIND> && record) {
     float4* dst = reinterpret_cast<float4*>(a.rows_o + row * 128 + c);
 #pragma unroll
     for (int i = 0; i < N / 4; i++) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
@@ -862,6 +863,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
         if (wk.g == 0) *reinterpret_cast<float2*>(mine + 1024 + (t * 8 + 2 * wk.c + i) * 2) = make_float2(wk.m[t][i], v);
       }
     const bool head_part = cur.t0 > 0, cut = cur.t0 + cur.nt < cur.tiles;
+    // for the join: but not a request's whole rows without a prefix
+    const bool record = KIND == kPrefix || (KIND == kTail && (cur.hi > 0 || cut || head_part));
     Partial<NT>* part = &partials[2 * blockIdx.x + (head_part ? 0 : 1)];
     const float* const theirs = reinterpret_cast<const float*>(smem + last_stage(FMT));  // of warp 0
     constexpr int kRing = kStages * stage_bytes(FMT) / 4;                                // floats from warp to warp
@@ -918,9 +921,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
           }
         } else {
           const int rr = cur.row0 + frow, tok = rr / a.G, hd = cur.h * a.G + rr - tok * a.G;
-          finish<KIND, 8>(a, cur.q0 + tok, hd, quad * 4, M, L, o, vst);
+          finish<KIND, 8>(a, cur.q0 + tok, hd, quad * 4, M, L, o, vst, record);
         }
-        if (kRecords<KIND> && !head_part && quad == 0) {
+        if (record && !head_part && quad == 0) {
           const int rr = cur.row0 + frow, tok = rr / a.G, hd = cur.h * a.G + rr - tok * a.G;
           a.places[int64_t(cur.q0 + tok) * a.Hq + hd] =
               make_uint2(blockIdx.x, kv_place(cut ? parts_behind(cur) + 1 : 0, frow, false, cur.hi > 0));
@@ -988,7 +991,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(KvAttnArgs a, int ctas) {
   const float vst = FMT == 1 ? __ldg(a.c.v_scale) : 1.0f;
   const int tok = rr / a.G, head = hd.h * a.G + rr - tok * a.G;
   float o[4] = {s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w};
-  finish<KIND, 4>(a, x.q0 + tok, head, lane * 4, M, L, o, vst);
+  finish<KIND, 4>(a, x.q0 + tok, head, lane * 4, M, L, o, vst, false);
 }
 
 // Tiles of eight query rows in a block: as few blocks of at most 32 rows as there

@@ -873,9 +873,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       const float nanv = __uint_as_float(0x7FC00000u);
       const int hd = it.h * a.G + (it.row0 + idx) - tok * a.G;
       const int64_t out_row = int64_t(it.q0 + tok) * a.Hq + hd;
+      // for the join: but not a request's whole rows without a prefix
+      const bool keep = KIND == kPrefix || (KIND == kTail && (it.hi > 0 || it.slot >= 0));
       const float f = l == 0.0f ? 1.0f : vst / l;
       uint4* orow = reinterpret_cast<uint4*>(a.o + out_row * 128);
-      float4* const record = reinterpret_cast<float4*>(it.slot < 0 ? a.rows_o + out_row * 128 : partials[it.slot].o[idx]);  // kRecords: always one
+      float4* const record = reinterpret_cast<float4*>(it.slot < 0 ? a.rows_o + out_row * 128 : partials[it.slot].o[idx]);
 #pragma unroll
       for (int c = 0; c < 4; c++) {
         float o[32];
@@ -893,7 +895,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
           for (int e = 0; e < 32; e++)
             if ((nan_blocks >> (2 * c + (e >> 4))) & 1u) o[e] = nanv;
         }
-        if (valid && it.slot < 0 && !kRecords<KIND>) {
+        if (valid && it.slot < 0 && !keep) {
 #pragma unroll
           for (int e = 0; e < 4; e++)
             orow[4 * c + e] = make_uint4(pack_bf16(o[8 * e] * f, o[8 * e + 1] * f), pack_bf16(o[8 * e + 2] * f, o[8 * e + 3] * f),
@@ -909,13 +911,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
         if (it.slot >= 0) {
           partials[it.slot].m[idx] = m;
           partials[it.slot].l[idx] = l;
-        } else if (kRecords<KIND>) {
+        } else if (keep) {
           a.rows_ml[out_row] = make_float2(m, l);
         } else {
           a.lse[int64_t(hd) * a.total_q + it.q0 + tok] = l == 0.0f ? -INFINITY : (m - kOffset + log2f(l)) * 0.6931471805599453f;
         }
       }
-      if (kRecords<KIND> && valid && it.t0 == 0) a.places[out_row] = make_uint2(blockIdx.x, kv_place(it.parts, idx, true, kHides && it.hi > 0));
+      if (keep && valid && it.t0 == 0) a.places[out_row] = make_uint2(blockIdx.x, kv_place(it.parts, idx, true, kHides && it.hi > 0));
       st += n_x;
       kt += nmax;
     }

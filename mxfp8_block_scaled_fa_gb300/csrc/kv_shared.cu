@@ -7,6 +7,7 @@
 // end are hidden), by the kernels of kv_attn.cu and kv_prefill.cu, which leave records instead of results:
 //   kv_shared_plan_kernel  checks the groups, writes the prefix of each request, the line that
 //                          kv_prefill.cu works off for the groups, and clears the records' places
+//                          (a request without a prefix has its results at once, unless it is cut)
 //   kPrefix, kTail         neither needs the other's results, so the second starts where the first
 //                          leaves SMs free
 //   kv_shared_join_kernel  a warp a row: its records in the order of the keys
@@ -46,7 +47,7 @@ __global__ void __launch_bounds__(kPlan) kv_shared_plan_kernel(KvAttnArgs a, Sha
     const int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + e);
     if (q0 < 0 || q1 < q0 || q1 > a.total_q || q1 - q0 > s.max_group_q) return -1;
     n = q1 - q0;
-    return p;
+    return e - b > 1 ? p : 0;  // a single request reads its own row
   };
   for (int64_t w = int64_t(blockIdx.x) * kPlan + tid; w < s.words; w += int64_t(gridDim.x) * kPlan) s.places[w] = make_uint4(0, 0, 0, 0);
   if (blockIdx.x > 0) {
