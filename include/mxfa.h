@@ -562,23 +562,29 @@ mxfa_status mxfa_kv_attn_window(const mxfa_kv_cache* cache, const void* q, int64
                                 void* o, float* lse, void* ws, size_t ws_bytes, mxfa_stream_t stream);
 
 /* mxfa_kv_attn_shared -- mxfa_kv_attn (causal) for requests that share prefixes: the keys of a group's
- * prefix are read once for the queries of all its requests.
+ * prefix are read once for the queries of all its requests, where that pays.
  *  group_starts DEVICE int32 [groups + 1], ascending: group g is requests group_starts[g] ..
  *               group_starts[g + 1] - 1; requests of no group are computed as by mxfa_kv_attn
  *  prefix_lens  DEVICE int32 [groups]: the first prefix_lens[g] keys of each request of the group are
  *               those of its first request, whose row of block_table they are read from; each
  *               request's further keys from its own row.  Any length, 0 included
  *  max_group_q  the most query tokens of a group
+ *  share        MXFA_KV_SHARE_AUTO: prefixes are read once for a group where that is estimated to be faster, from the
+ *               lengths and on the GPU (long prefixes, many requests of few tokens), and by each request
+ *               for itself otherwise; _ALWAYS, _NEVER: one or the other
  * Each request with queries has at least the prefix before them (kv - n >= prefix).  One that has not,
  * and the requests of a group whose starts, queries or prefix are outside their bounds, are left out
  * and recorded as failed index checks.  The workspace is of mxfa_kv_attn_shared_workspace_size() bytes,
  * max_k = max_blocks * page; everything else as mxfa_kv_attn.  groups may be 0. */
+#define MXFA_KV_SHARE_AUTO 0
+#define MXFA_KV_SHARE_ALWAYS 1
+#define MXFA_KV_SHARE_NEVER 2
 size_t mxfa_kv_attn_shared_workspace_size(int R, int groups, int64_t total_q, int max_q, int max_group_q, int64_t max_k,
                                           int Hq, int H);
 mxfa_status mxfa_kv_attn_shared(const mxfa_kv_cache* cache, const void* q, int64_t q_stride, int64_t total_q,
                                 const int32_t* cu_q, const int32_t* kv_lens, int R, const int32_t* block_table,
                                 int max_blocks, int max_q, int Hq, float softmax_scale, const int32_t* group_starts,
-                                const int32_t* prefix_lens, int groups, int max_group_q, void* o, float* lse,
+                                const int32_t* prefix_lens, int groups, int max_group_q, int share, void* o, float* lse,
                                 void* ws, size_t ws_bytes, mxfa_stream_t stream);
 
 /* ---------------------------------------------------------- rotary positions

@@ -19,7 +19,7 @@ def __getattr__(name):
                                             "LOWP_MXFP4", "LOWP_MXFP6_E2M3", "LOWP_MXFP6_E3M2",
                                             "LOWP_NVFP4", "LOWP_CODES", "LOWP_MMA", "ELEM_E4M3", "ELEM_E2M3", "ELEM_E3M2",
                                             "ELEM_E2M1",
-                                            "KV_MXFP4", "KV_NVFP4", "KvCache", "KvPages", "KvStep", "kv_ring", "kv_plan",
+                                            "KV_MXFP4", "KV_NVFP4", "KV_SHARE_AUTO", "KV_SHARE_ALWAYS", "KV_SHARE_NEVER", "KvCache", "KvPages", "KvStep", "kv_ring", "kv_plan",
                                             "kv_append", "kv_load", "kv_attention",
                                             "Rope", "Rotation", "ROPE_HALF", "ROPE_INTERLEAVED", "rope", "rope_bwd", "rope_positions",
                                             "kv_append_rope", "kv_attention_shared", "KvFork", "kv_refs", "kv_fork", "kv_free",

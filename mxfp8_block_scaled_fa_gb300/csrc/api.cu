@@ -1073,11 +1073,12 @@ size_t mxfa_kv_attn_shared_workspace_size(int R, int groups, int64_t total_q, in
 mxfa_status mxfa_kv_attn_shared(const mxfa_kv_cache* cache, const void* q, int64_t q_stride, int64_t total_q,
                                 const int32_t* cu_q, const int32_t* kv_lens, int R, const int32_t* block_table,
                                 int max_blocks, int max_q, int Hq, float softmax_scale, const int32_t* group_starts,
-                                const int32_t* prefix_lens, int groups, int max_group_q, void* o, float* lse,
+                                const int32_t* prefix_lens, int groups, int max_group_q, int share, void* o, float* lse,
                                 void* ws, size_t ws_bytes, mxfa_stream_t stream) {
   KvAttnArgs a;
   const mxfa_status s = check_attn(cache, q, q_stride, total_q, cu_q, kv_lens, R, block_table, max_blocks, max_q, Hq, softmax_scale, o, lse, ws, a);
   if (s) return s;
+  if (share != MXFA_KV_SHARE_AUTO && share != MXFA_KV_SHARE_ALWAYS && share != MXFA_KV_SHARE_NEVER) return MXFA_ERR_INVALID_ARG;
   if (groups < 0 || max_group_q < 0 || (groups > 0 && (!group_starts || !prefix_lens))) return MXFA_ERR_INVALID_ARG;
   if (!aligned4(group_starts) || !aligned4(prefix_lens)) return MXFA_ERR_MISALIGNED;
   if (groups > (1 << 20)) return MXFA_ERR_UNSUPPORTED;
@@ -1090,7 +1091,7 @@ mxfa_status mxfa_kv_attn_shared(const mxfa_kv_cache* cache, const void* q, int64
   if (t) return t;
   if (groups == 0) return from_cuda(launch_kv_attn(kAll, a, reinterpret_cast<cudaStream_t>(stream)));
   a.starts = group_starts;
-  return from_cuda(launch_kv_attn_shared(a, prefix_lens, groups, max_group_q, reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_kv_attn_shared(a, prefix_lens, groups, max_group_q, share, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 mxfa_status mxfa_rope(const void* x, int64_t x_stride, void* y, int64_t y_stride, const int32_t* positions,

@@ -170,7 +170,8 @@ struct Request {
   int q0, n;      // first query token and their number
   int kv;         // keys
   // kWindow, kTail: keys lo .. hi - 1 are in no row's sight; the tiles that hold nothing else,
-  // `jump` keys of them from key `at` on, are left out of the line
+  // `jump` keys of them from key `at` on, are left out of the line.  kTail, where prefixes are not
+  // shared after all: hi = 0, and keys before lo are those of the group's first request
   int lo, hi, at, jump;
 };
 // Keys lo .. hi - 1 hidden from every row of a request.
@@ -211,7 +212,10 @@ __device__ __forceinline__ Request request_of(const KvAttnArgs& a, int r) {
     const int p = __ldg(a.prefix + r);  // negative: of a group that is none
     if (p > 0 && e > b && kv - (e - b) < p) atomicOr(&g_status_kv_attn, DEV_BAD_INDEX);
     if (p < 0 || kv - (e - b) < p) x.n = 0;
-    if (x.n > 0) hide(x, 0, p);
+    if (x.n > 0) {
+      if (__ldg(a.share)) hide(x, 0, p);
+      else x.lo = p;
+    }
   }
   return x;
 }
@@ -330,7 +334,11 @@ struct Worker {
     const uint8_t* k = k_src + uint64_t(b0) * block_bytes;
     const uint8_t* sf = sf_src + uint64_t(b0) * (block_bytes / (64 / kSf));
     copy_pass(s, k, k + v_from_k, sf, 0, 0);
-    if (small_pages) {
+    if (KIND == kTail) {  // a prefix may end between the passes
+      k = k_src + uint64_t(b1) * block_bytes;
+      sf = sf_src + uint64_t(b1) * (block_bytes / (64 / kSf));
+      copy_pass(s, k, k + v_from_k, sf, 1, small_pages ? 0 : 16);
+    } else if (small_pages) {
       k = k_src + uint64_t(b1) * block_bytes;
       sf = sf_src + uint64_t(b1) * (block_bytes / (64 / kSf));
       copy_pass(s, k, k + v_from_k, sf, 1, 0);
@@ -691,11 +699,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
     const int key = key_at(place);
     return place < k_end && (key < hide_lo || key >= hide_hi);
   };
-  const int32_t* table;
+  const int32_t *table, *first_table = nullptr;  // kTail, prefixes not shared: of keys before hide_lo
   uint32_t b0 = 0, b1 = 0;
   auto look_up = [&](int step, uint32_t& b0, uint32_t& b1) {
     const int place = k_lo + (lane >> 1) + step * kTile, key = key_at(place);
     const bool second = in_sight(place + 16);
+    if (KIND == kTail && first_table) {
+      auto block = [&](int k) { return uint32_t(__ldg((k < hide_lo ? first_table : table) + (k >> a.c.page_shift))); };
+      b0 = in_sight(place) ? block(key) : 0xFFFFFFFFu;
+      b1 = second ? block(key + 16) : 0xFFFFFFFFu;
+      return;
+    }
     // where keys are hidden, a block of both passes may have only the second one's key in sight
     const bool first = in_sight(place) || (kHides && !small_pages && second);
     b0 = first ? uint32_t(__ldg(table + (key >> a.c.page_shift))) : 0xFFFFFFFFu;
@@ -735,6 +749,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kv_attn_kernel(KvAt
     }
     steps = k_lo < k_end ? (k_end - k_lo + kTile - 1) / kTile : 0;
     table = a.table + int64_t(table_row<KIND>(a, it.r)) * a.width;
+    if (KIND == kTail) first_table = it.hi < it.lo ? a.table + int64_t(__ldg(a.starts + it.r)) * a.width : nullptr;
     wk.aim(a.c, k_lo, it.h);
     // the first three steps' blocks at once, or each would be waited for
     uint32_t e0[3], e1[3];
@@ -1123,6 +1138,7 @@ KvRecords kv_attn_records(uint8_t* ws, int R, int max_q, int64_t max_k, int G) {
   x.many_ws = ws + ((kva::workspace_of(p.nt) + 255) & ~size_t(255));
   x.few = ws + kva::header_bytes(sm_count_current_device() * kva::ctas_per_sm(p.nt));
   x.few_rows = 8 * p.nt;
+  x.split_rows = p.prefill ? p.split_rows : 1 << 30;
   x.many = p.prefill ? kv_prefill_records(x.many_ws, R) : nullptr;
   return x;
 }

@@ -139,7 +139,8 @@ __device__ __forceinline__ float ex2(float x) {
 // A request whose rows belong here: more than a.split_rows of them, offsets and
 // lengths within their tables (a failed check leaves n = 0).
 // kWindow, kTail: keys lo .. hi - 1 are in no row's sight (of an item, as item_of() sets them); the tiles that hold
-// nothing else, `jump` keys of them from key `at` on, are left out of the item's tiles.
+// nothing else, `jump` keys of them from key `at` on, are left out of the item's tiles.  kTail, where prefixes are not
+// shared after all: hi = 0, and keys before lo are those of the group's first request.
 struct Request {
   int q0, n, kv;
   int lo, hi, at, jump;
@@ -177,7 +178,10 @@ __device__ __forceinline__ Request request_of(const KvAttnArgs& a, int r) {
     const int p = __ldg(a.prefix + r);  // negative: of a group that is none
     if (p > 0 && e > b && kv - (e - b) < p) atomicOr(&g_status_kv_prefill, DEV_BAD_INDEX);
     if (p < 0 || kv - (e - b) < p) x.n = 0;
-    if (x.n > 0) hide(x, 0, p);
+    if (x.n > 0) {
+      if (__ldg(a.share)) hide(x, 0, p);
+      else x.lo = p;
+    }
   }
   return x;
 }
@@ -562,10 +566,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
         const int place = (it.t0 + j) * TILE;
         return (kHides && place >= it.at ? place + it.jump : place) + t;
       };
+      const int32_t* first_table = KIND == kTail && it.hi < it.lo ? a.table + int64_t(__ldg(a.starts + it.r)) * a.width : table;
       auto in_sight = [&](int key) { return key < keys && (!kHides || key < it.lo || key >= it.hi); };
       auto entry = [&](int j) -> int {
         const int key = key_of(j);
-        return j < nmax && in_sight(key) ? __ldg(table + (key >> a.c.page_shift)) : -1;
+        return j < nmax && in_sight(key) ? __ldg((KIND == kTail && key < it.lo ? first_table : table) + (key >> a.c.page_shift)) : -1;
       };
       auto find = [&](int b, int j) -> int64_t {
         const int key = key_of(j);

@@ -268,12 +268,13 @@ PyObject* window(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// shared(q, cache, cu_q, kv_lens, block_table, max_q, scale, group_starts, prefix_lens, max_group_q) -> (o, lse), or a status
+// shared(q, cache, cu_q, kv_lens, block_table, max_q, scale, group_starts, prefix_lens, max_group_q, share) -> (o, lse), or a status
 PyObject* shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     Attn x;
-    int64_t most;
-    if (n != 10 || !attn_args(a, x) || !number(a[9], most) || most < 0 || most >= kMost) Py_RETURN_NONE;
+    int64_t most, share;
+    if (n != 11 || !attn_args(a, x) || !number(a[9], most) || most < 0 || most >= kMost || !number(a[10], share) || share < 0 || share > 2)
+      Py_RETURN_NONE;
     const at::Tensor *starts = tensor(a[7]), *prefix = tensor(a[8]);
     if (!flat(starts, at::kInt, x.c->index) || !flat(prefix, at::kInt, x.c->index)) Py_RETURN_NONE;
     const int64_t groups = prefix->numel();
@@ -282,7 +283,7 @@ PyObject* shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* const ws = attn_buffers(x, bytes);
     const mxfa_status s = mxfa_kv_attn_shared(&x.c->c, x.q->data_ptr(), x.qs, x.T, i32(x.cu), i32(x.kv), int(x.R), i32(x.table),
                                               int(x.table->size(1)), int(x.max_q), int(x.Hq), x.scale, i32(starts), i32(prefix), int(groups),
-                                              int(most), x.o.data_ptr(), static_cast<float*>(x.lse.data_ptr()), ws, bytes, stream(x.c->index));
+                                              int(most), int(share), x.o.data_ptr(), static_cast<float*>(x.lse.data_ptr()), ws, bytes, stream(x.c->index));
     return s ? failed(s) : tuple_of({x.o, x.lse});
   });
 }

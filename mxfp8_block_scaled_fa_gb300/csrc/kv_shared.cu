@@ -5,15 +5,24 @@
 // So the prefix of a group is one attention problem for the queries of all its requests (kPrefix: the
 // groups take the requests' places), the rest one of each request (kTail: keys before the prefix's
 // end are hidden), by the kernels of kv_attn.cu and kv_prefill.cu, which leave records instead of results:
-//   kv_shared_plan_kernel  checks the groups, writes the prefix of each request, the line that
-//                          kv_prefill.cu works off for the groups, and clears the records' places
-//                          (a request without a prefix has its results at once, unless it is cut)
+//   kv_shared_plan_kernel  checks the groups, decides whether sharing pays, writes the prefix of each request, the line
+//                          that kv_prefill.cu works off for the groups, and clears the records' places
 //   kPrefix, kTail         neither needs the other's results, so the second starts where the first
 //                          leaves SMs free
-//   kv_shared_join_kernel  a warp a row: its records in the order of the keys
+//   kv_shared_join_kernel  a warp a row: its records in the order of the keys (a request without a prefix
+//                          has its results before, unless it is cut)
+//
+// When it pays.  Read by each request, a prefix's tile of 128 keys takes its kernel's time per block of rows; shared, it
+// takes that of the group's blocks, but records and join are more: 3 us and 0.6 ns a row, by the cases
+// below.  In us, shared and not: 64 requests of 4 rows behind 8192 keys (8 key heads) 51 and 126; 6 x 5 requests of up to 15
+// rows behind up to 3000 28 and 31; 16 of 4 rows behind 1024 27 and 25; 4 x 8 of 8 rows behind up to 4096 38 and 37; 3 x 30 of
+// up to 25 rows behind up to 535 102 and 91; 3 x 8 of up to 636 rows behind up to 3454 157 and 132.  One that is not shared takes 5
+// to 8 us (prompts 20) more than mxfa_kv_attn: the plan, and a kernel without work.
 #include "kv_fp4.cuh"
 #include "mx_ptx.cuh"
 #include "mxfa_internal.h"
+
+#include "../../include/mxfa.h"
 
 namespace mxfa {
 
@@ -27,21 +36,34 @@ constexpr float kOffset = 8.0f;  // log2 offset of P in the records, as in kv_at
 struct SharedArgs {
   const int32_t* prefix_lens;
   int groups, max_group_q;
-  int32_t *gpre, *pre;
-  int64_t* line;    // NULL: the groups are not kv_prefill.cu's
-  uint4* places;    // of both passes, 16 bytes at a time
+  int mode;                 // MXFA_KV_SHARE_*
+  int32_t *gpre, *pre, *first, *share;
+  int64_t* line;            // NULL: the groups are not kv_prefill.cu's
+  uint4* places;            // of both passes, 16 bytes at a time
   int64_t words;
+  int few_rows[2], split_rows[2];  // of the passes' kernels
+  float sms;
 };
 
-// The first CTA goes through the groups: prefix of group g at gpre[g] (0: none, or not as documented), behind them
-// their number of items for kv_prefill.cu; the
-// others take a request a thread: pre[r] (-1: of a group not as documented; 0: of none).
+// SM microseconds of a tile of 128 keys for `rows` rows of one request (or group) and key head: kv_attn.cu's kernel by
+// blocks of few_rows (0.54, 0.68, 0.82 and 0.96 for 8 to 32), kv_prefill.cu's by blocks of 256.
+__device__ __forceinline__ float tile_cost(float rows, int few_rows, int split_rows) {
+  if (rows > float(split_rows)) return ceilf(rows / float(kPrefillRows)) * 1.6f;
+  return ceilf(rows / float(few_rows)) * (0.4f + 0.0175f * float(few_rows));
+}
+
+// The first CTA goes through the groups: prefix of group g at gpre[g] (0: none, not as documented, or not shared), behind them
+// their number of items for kv_prefill.cu, and whether they are shared; the others take a request a thread: pre[r]
+// (-1: of a group not as documented; 0: of none) and the group's first request first[r].
 __global__ void __launch_bounds__(kPlan) kv_shared_plan_kernel(KvAttnArgs a, SharedArgs s) {
   __shared__ int64_t s_sum[kPlan / 32];
+  __shared__ float s_gain[kPlan / 32];
   asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  auto checked = [&](int g, int& n) -> int {  // -1: not as documented
-    const int b = __ldg(a.starts + g), e = __ldg(a.starts + g + 1), p = __ldg(s.prefix_lens + g);
+  int b, e, n;  // of the group that was checked: requests and query tokens
+  auto checked = [&](int g) -> int {  // -1: not as documented
+    b = __ldg(a.starts + g), e = __ldg(a.starts + g + 1);
+    const int p = __ldg(s.prefix_lens + g);
     n = 0;
     if (b < 0 || e < b || e > a.R || p < 0 || p > int64_t(a.width) << a.c.page_shift) return -1;
     const int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + e);
@@ -52,26 +74,47 @@ __global__ void __launch_bounds__(kPlan) kv_shared_plan_kernel(KvAttnArgs a, Sha
   for (int64_t w = int64_t(blockIdx.x) * kPlan + tid; w < s.words; w += int64_t(gridDim.x) * kPlan) s.places[w] = make_uint4(0, 0, 0, 0);
   if (blockIdx.x > 0) {
     for (int r = (int(blockIdx.x) - 1) * kPlan + tid; r < a.R; r += (int(gridDim.x) - 1) * kPlan) {
-      int lo = 0, hi = s.groups, n;  // the group with starts[lo] <= r < starts[hi]
+      int lo = 0, hi = s.groups;  // the group with starts[lo] <= r < starts[hi]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (__ldg(a.starts + mid) <= r) lo = mid;
         else hi = mid;
       }
       const bool in = __ldg(a.starts + lo) <= r && r < __ldg(a.starts + lo + 1);
-      s.pre[r] = in ? checked(lo, n) : 0;
+      const int p = in ? checked(lo) : 0;
+      s.pre[r] = p;
+      s.first[r] = p > 0 ? b : r;
     }
     return;
   }
+  float gain = 0.0f;
+  int first_p = 0, first_n = 0;  // of the first kPlan groups, most often all
+  for (int g = tid; g < s.groups; g += kPlan) {
+    const int p = checked(g);
+    if (g == tid) first_p = p, first_n = n;
+    if (p < 0) atomicOr(&g_status_kv_shared, DEV_BAD_INDEX);
+    if (p <= 0 || n == 0) continue;
+    const float rows = float(n) * float(a.G), m = float(e - b);
+    const float tiles = float(a.c.H) * float((p + kPrefillTile - 1) / kPrefillTile);
+    gain += tiles * (m * tile_cost(rows / m, s.few_rows[1], s.split_rows[1]) - tile_cost(rows, s.few_rows[0], s.split_rows[0])) / s.sms -
+            0.0006f * rows * float(a.c.H);
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) gain += __shfl_xor_sync(0xFFFFFFFFu, gain, o);
+  if (lane == 0) s_gain[warp] = gain;
+  __syncthreads();
+  gain = 0.0f;
+  for (int w = 0; w < kPlan / 32; w++) gain += s_gain[w];
+  const bool share = s.mode == MXFA_KV_SHARE_ALWAYS || (s.mode == MXFA_KV_SHARE_AUTO && gain > 3.0f);
+  if (tid == 0) *s.share = share ? 1 : 0;
   int64_t base = 0;
   int items = 0;
   for (int g0 = 0; g0 < s.groups; g0 += kPlan) {
     const int g = g0 + tid;
     int64_t u = 0;
     if (g < s.groups) {
-      int n;
-      const int p = checked(g, n);
-      if (p < 0) atomicOr(&g_status_kv_shared, DEV_BAD_INDEX);
+      const int p = !share ? 0 : g0 == 0 ? first_p : checked(g);
+      if (g0 == 0) n = first_n;
       s.gpre[g] = max(p, 0);
       if (p > 0) {
         u = kv_prefix_units(n, p, a.G, a.c.H);
@@ -102,9 +145,9 @@ __global__ void __launch_bounds__(kPlan) kv_shared_plan_kernel(KvAttnArgs a, Sha
   if (lane == 0) s_sum[warp] = items;
   __syncthreads();
   if (tid == 0) {
-    int64_t n = 0;
-    for (int w = 0; w < kPlan / 32; w++) n += s_sum[w];
-    s.gpre[s.groups] = int(min(n, int64_t(1) << 20));
+    int64_t k = 0;
+    for (int w = 0; w < kPlan / 32; w++) k += s_sum[w];
+    s.gpre[s.groups] = int(min(k, int64_t(1) << 20));
     s.line[s.groups] = base;
   }
 }
@@ -213,7 +256,7 @@ __global__ void __launch_bounds__(256) kv_shared_join_kernel(KvAttnArgs a, Pass 
 
 // Places in a call's workspace: for either pass its rows in one piece and its records, and what the plan writes.
 struct Places {
-  size_t o[2], ml[2], where, gpre, pre, pass[2], bytes;
+  size_t o[2], ml[2], where, gpre, pre, first, share, pass[2], bytes;
 };
 Places places_of(int R, int groups, int64_t total_q, int max_q, int max_group_q, int64_t max_k, int Hq, int G) {
   size_t at = 0;
@@ -231,6 +274,8 @@ Places places_of(int R, int groups, int64_t total_q, int max_q, int max_group_q,
   p.where = take(rows * 16);
   p.gpre = take(size_t(groups) * 4 + 4);
   p.pre = take(size_t(R) * 4);
+  p.first = take(size_t(R) * 4);
+  p.share = take(4);
   p.pass[0] = take(kv_attn_workspace(groups, max_group_q, max_k, G));
   p.pass[1] = take(kv_attn_workspace(R, max_q, max_k, G));
   p.bytes = at;
@@ -243,7 +288,7 @@ size_t kv_shared_workspace(int R, int groups, int64_t total_q, int max_q, int ma
   return places_of(R, groups, total_q, max_q, max_group_q, max_k, Hq, G).bytes;
 }
 
-cudaError_t launch_kv_attn_shared(const KvAttnArgs& args, const int32_t* prefix_lens, int groups, int max_group_q, cudaStream_t st) {
+cudaError_t launch_kv_attn_shared(const KvAttnArgs& args, const int32_t* prefix_lens, int groups, int max_group_q, int mode, cudaStream_t st) {
   clear_stale_error();
   const int64_t max_k = int64_t(args.width) << args.c.page_shift, rows = args.total_q * args.Hq;
   uint8_t* const ws = args.ws;
@@ -262,13 +307,30 @@ cudaError_t launch_kv_attn_shared(const KvAttnArgs& args, const int32_t* prefix_
   a[0].max_q = max_group_q;
   a[0].causal = 0;
   a[1].causal = 1;
+  a[1].starts = reinterpret_cast<const int32_t*>(ws + p.first);
+  a[1].share = reinterpret_cast<const int32_t*>(ws + p.share);
   for (int i = 0; i < 2; i++) {
     rec[i] = kv_attn_records(a[i].ws, a[i].R, a[i].max_q, max_k, args.G);
     pass[i] = Pass{rec[i].few, rec[i].many, rec[i].few_rows, a[i].rows_o, a[i].rows_ml, a[i].places};
   }
   const bool few[2] = {kv_attn_few(max_group_q, max_k, args.G), kv_attn_few(args.max_q, max_k, args.G)};
-  SharedArgs s{prefix_lens, groups, max_group_q, reinterpret_cast<int32_t*>(ws + p.gpre), reinterpret_cast<int32_t*>(ws + p.pre),
-               few[0] ? nullptr : reinterpret_cast<int64_t*>(rec[0].many_ws), reinterpret_cast<uint4*>(ws + p.where), rows};
+  SharedArgs s;
+  s.prefix_lens = prefix_lens;
+  s.groups = groups;
+  s.max_group_q = max_group_q;
+  s.mode = mode;
+  s.gpre = reinterpret_cast<int32_t*>(ws + p.gpre);
+  s.pre = reinterpret_cast<int32_t*>(ws + p.pre);
+  s.first = reinterpret_cast<int32_t*>(ws + p.first);
+  s.share = reinterpret_cast<int32_t*>(ws + p.share);
+  s.line = few[0] ? nullptr : reinterpret_cast<int64_t*>(rec[0].many_ws);
+  s.places = reinterpret_cast<uint4*>(ws + p.where);
+  s.words = rows;
+  for (int i = 0; i < 2; i++) {
+    s.few_rows[i] = rec[i].few_rows;
+    s.split_rows[i] = i == 0 && !few[0] ? 0 : rec[i].split_rows;  // the prompts' kernel takes all groups or none
+  }
+  s.sms = float(sm_count_current_device());
   const int64_t by_requests = 1 + (int64_t(args.R) + kPlan - 1) / kPlan, by_words = (rows + 4 * kPlan - 1) / (4 * kPlan);
   int64_t grid = by_requests > by_words ? by_requests : by_words;
   grid = grid < 2 ? 2 : grid < 1024 ? grid : 1024;

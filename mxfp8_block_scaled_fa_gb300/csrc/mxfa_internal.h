@@ -251,7 +251,8 @@ struct KvAttnArgs {
   float* lse;             // [Hq][total_q]
   uint8_t* ws;
   int window, sinks;      // kWindow: a query at position p sees keys p - window + 1 .. p, and those before `sinks`
-  const int32_t* starts;  // kPrefix: [R + 1] first requests of the groups, into cu_q and table
+  const int32_t* starts;  // kPrefix: [R + 1] first requests of the groups, into cu_q and table; kTail: [R] each request's group's
+  const int32_t* share;   // kTail: whether kPrefix has done the prefixes; else a request reads its own, by its group's first row
   const int32_t* prefix;  // kPrefix: [R] keys of a group's prefix, and the number of all items; kTail: [R] keys that a request does not read itself
   // kPrefix, kTail: what a row's keys give, for kv_shared_join_kernel: rows in one piece o [total_q][Hq][128], (m, l)
   // [total_q][Hq]; and of all rows [total_q][Hq] (first CTA, kv_place()) of their partial records
@@ -273,6 +274,7 @@ constexpr __host__ __device__ uint32_t kv_place(int parts, int row, bool many, b
 struct KvRecords {
   uint8_t *few, *many;    // records of kv_attn.cu's and of kv_prefill.cu's kernel
   int few_rows;           // rows of one of the former
+  int split_rows;         // rows of a request, above which the latter has it
   uint8_t* many_ws;       // workspace of kv_prefill.cu
 };
 // Launches a kernel that may start before the one before it has ended, and waits for it
@@ -299,7 +301,7 @@ bool kv_attn_few(int max_q, int64_t max_k, int G);  // whether kv_prefill.cu has
 KvRecords kv_attn_records(uint8_t* ws, int R, int max_q, int64_t max_k, int G);
 uint8_t* kv_prefill_records(uint8_t* ws, int R);
 size_t kv_shared_workspace(int R, int groups, int64_t total_q, int max_q, int max_group_q, int64_t max_k, int Hq, int G);
-cudaError_t launch_kv_attn_shared(const KvAttnArgs& a, const int32_t* prefix_lens, int groups, int max_group_q, cudaStream_t s);
+cudaError_t launch_kv_attn_shared(const KvAttnArgs& a, const int32_t* prefix_lens, int groups, int max_group_q, int mode, cudaStream_t s);
 size_t kv_prefill_workspace(int R);
 cudaError_t launch_kv_prefill_line(int kind, const KvAttnArgs& a, uint8_t* ws, bool after_attn, cudaStream_t st);
 // Units of the line that kv_prefill.cu works off, of a group of n query tokens behind p keys.

@@ -148,7 +148,7 @@ def lib() -> ctypes.CDLL:
             "mxfa_kv_attn_window_workspace_size": (S, [I, I, I64, I, I, I, I]),
             "mxfa_kv_attn_window": (I, [P, P, I64, I64, P, P, I, P, I, I, I, F, I, I, P, P, P, S, P]),
             "mxfa_kv_attn_shared_workspace_size": (S, [I, I, I64, I, I, I64, I, I]),
-            "mxfa_kv_attn_shared": (I, [P, P, I64, I64, P, P, I, P, I, I, I, F, P, P, I, I, P, P, P, S, P]),
+            "mxfa_kv_attn_shared": (I, [P, P, I64, I64, P, P, I, P, I, I, I, F, P, P, I, I, I, P, P, P, S, P]),
             "mxfa_rope": (I, [P, I64, P, I64, P, I64, I, I, P, I, P]),
             "mxfa_kv_append_rope": (I, [P, P, I64, I, P, I64, P, I64, I64, P, P, P, P, I64, P]),
             "mxfa_kv_fork": (I, [P, I, I, P, P, P, I, P, I64, P, I64, P, P, I, P, P, P, P]),
@@ -642,6 +642,7 @@ def gemm_quant(a: Mx, b: Mx, bf16: bool = True, row: bool = True, col: bool = Tr
 
 # ------------------------------------------------------------------ 4-bit KV cache
 KV_MXFP4, KV_NVFP4 = 0, 1
+KV_SHARE_AUTO, KV_SHARE_ALWAYS, KV_SHARE_NEVER = 0, 1, 2
 
 
 class KvPages(ctypes.Structure):
@@ -697,10 +698,11 @@ def mxfa_kv_attn_shared_workspace_size(R, groups, total_q, max_q, max_group_q, m
 
 
 def mxfa_kv_attn_shared(pages: KvPages, q, q_stride, total_q, cu_q, kv_lens, R, block_table, max_blocks, max_q,
-                        Hq, scale, group_starts, prefix_lens, groups, max_group_q, o, lse, ws, ws_bytes, stream=None):
+                        Hq, scale, group_starts, prefix_lens, groups, max_group_q, share, o, lse, ws, ws_bytes,
+                        stream=None):
     _check(lib().mxfa_kv_attn_shared(ctypes.byref(pages), _p(q), q_stride, total_q, _p(cu_q), _p(kv_lens), R,
                                      _p(block_table), max_blocks, max_q, Hq, float(scale), _p(group_starts),
-                                     _p(prefix_lens), groups, max_group_q, _p(o), _p(lse), _p(ws), ws_bytes,
+                                     _p(prefix_lens), groups, max_group_q, share, _p(o), _p(lse), _p(ws), ws_bytes,
                                      _stream(stream)), "mxfa_kv_attn_shared")
 
 
@@ -1055,20 +1057,24 @@ def _int32(name: str, value, least: int):
 
 def kv_attention_shared(q: torch.Tensor, cache: KvCache, cu_q: torch.Tensor, kv_lens: torch.Tensor,
                         block_table: torch.Tensor, group_starts: torch.Tensor, prefix_lens: torch.Tensor,
-                        max_q: int, max_group_q: int, scale: float, out=None, ws=None, stream=None):
+                        max_q: int, max_group_q: int, scale: float, out=None, ws=None, stream=None,
+                        share: Optional[bool] = None):
     """kv_attention (causal) of requests that share prefixes: group g is requests group_starts[g] ..
     group_starts[g + 1] - 1 (int32 [groups + 1]), whose first prefix_lens[g] (int32 [groups]) keys are
     read from its first request's row of block_table, once for all of the group's queries, at most
-    max_group_q of them.  Every request with queries has at least its group's prefix before them."""
+    max_group_q of them.  Every request with queries has at least its group's prefix before them.
+    Whether prefixes are in fact read once is decided on the GPU, by what is faster for the lengths,
+    unless `share` says so."""
+    share = KV_SHARE_AUTO if share is None else KV_SHARE_ALWAYS if share else KV_SHARE_NEVER
     if out is None and ws is None and stream is None:
-        made = _fast().shared(q, cache.raw, cu_q, kv_lens, block_table, max_q, scale, group_starts, prefix_lens, max_group_q)
+        made = _fast().shared(q, cache.raw, cu_q, kv_lens, block_table, max_q, scale, group_starts, prefix_lens, max_group_q, share)
         if type(made) is tuple:
             return made
         if made is not None:
             _check(made, "mxfa_kv_attn_shared")
     _int32("max_group_q", max_group_q, 0)
     return _attention(q, cache, cu_q, kv_lens, block_table, max_q, scale, out, ws, stream,
-                      ("shared", group_starts, prefix_lens, max_group_q))
+                      ("shared", group_starts, prefix_lens, max_group_q, share))
 
 
 def _attention(q, cache, cu_q, kv_lens, block_table, max_q, scale, out, ws, stream, form):
@@ -1088,7 +1094,7 @@ def _attention(q, cache, cu_q, kv_lens, block_table, max_q, scale, out, ws, stre
     _flat("kv_lens", kv_lens, i32, index)
     _flat("block_table", block_table, i32, index)
     if form[0] == "shared":
-        _, starts, prefix_lens, max_group_q = form
+        _, starts, prefix_lens, max_group_q, share = form
         groups = prefix_lens.numel()
         if starts.numel() != groups + 1:
             raise ValueError("group_starts and prefix_lens describe different numbers of groups")
@@ -1134,7 +1140,7 @@ def _attention(q, cache, cu_q, kv_lens, block_table, max_q, scale, out, ws, stre
     if form[0] == "window":
         _check(L.mxfa_kv_attn_window(*args, form[1], form[2], *rest), "mxfa_kv_attn_window")
     elif form[0] == "shared":
-        _check(L.mxfa_kv_attn_shared(*args, starts.data_ptr(), prefix_lens.data_ptr(), groups, max_group_q, *rest),
+        _check(L.mxfa_kv_attn_shared(*args, starts.data_ptr(), prefix_lens.data_ptr(), groups, max_group_q, share, *rest),
                "mxfa_kv_attn_shared")
     else:
         _check(L.mxfa_kv_attn(*args, 1 if form[1] else 0, *rest), "mxfa_kv_attn")

@@ -391,19 +391,20 @@ def shared_case(mx, rng, fmt, page, H, G, groups, ahead, behind, **kw):
     return c, q, cu, kv, table, slots, dev(starts), dev([p for _, p, _ in groups]), max(max(q_lens), 1), most, q_lens, kv_lens
 
 
+@pytest.mark.parametrize("share", [True, False, None])
 @pytest.mark.parametrize("case", SHARED)
-def test_shared(mx, case):
+def test_shared(mx, case, share):
     import torch
     rng = np.random.default_rng(len(case[4]) + case[3])
     c, q, cu, kv, table, slots, starts, pre, max_q, most, q_lens, _ = shared_case(mx, rng, *case)
     o, lse = results(q)
-    mx.kv_attention_shared(q, c, cu, kv, table, starts, pre, max_q, most, 128 ** -0.5, out=(o, lse))
+    mx.kv_attention_shared(q, c, cu, kv, table, starts, pre, max_q, most, 128 ** -0.5, out=(o, lse), share=share)
     torch.cuda.synchronize()
     assert mx.device_status() == 0
     compare(c, q, cu, slots, o, lse, lambda r, n, k: more_ref.window_mask(n, k, 1 << 30, 0))
     rest = sum(q_lens)
     assert (o[rest:].float() == 77.0).all() and (lse[:, rest:] == 77.0).all()
-    o2, lse2 = mx.kv_attention_shared(q, c, cu, kv, table, starts, pre, max_q, most, 128 ** -0.5)
+    o2, lse2 = mx.kv_attention_shared(q, c, cu, kv, table, starts, pre, max_q, most, 128 ** -0.5, share=share)
     assert torch.equal(o2[:rest].view(torch.int16), o[:rest].view(torch.int16)) and torch.equal(lse2[:, :rest], lse[:, :rest])
 
 
@@ -417,8 +418,9 @@ def test_shared_without_groups(mx):
     assert torch.equal(got[0][:3].view(torch.int16), want[0][:3].view(torch.int16)) and torch.equal(got[1][:, :3], want[1][:, :3])
 
 
-@pytest.mark.parametrize("rows", [1, 30])
-def test_shared_nan_in_the_prefix(mx, rows):
+@pytest.mark.parametrize("share", [True, False])
+@pytest.mark.parametrize("rows", [2, 30])
+def test_shared_nan_in_the_prefix(mx, rows, share):
     import torch
     rng = np.random.default_rng(3)
     c, q, cu, kv, table, slots, starts, pre, max_q, most, _, _ = shared_case(mx, rng, 0, 16, 1, 4, [([1] * rows, 300, [1] * rows)], [(1, 50)], [])
@@ -426,16 +428,17 @@ def test_shared_nan_in_the_prefix(mx, rows):
     c.v_sf[s // 16, 0, s % 16, 3] = 0xFF
     c.v[s // 16, 0, s % 16, 48:] = 0
     o, lse = results(q)
-    mx.kv_attention_shared(q, c, cu, kv, table, starts, pre, max_q, most, 0.1, out=(o, lse))
+    mx.kv_attention_shared(q, c, cu, kv, table, starts, pre, max_q, most, 0.1, out=(o, lse), share=share)
     bad = torch.isnan(o[: rows + 1].float())
     assert not bad[0].any() and bad[1:, :, 96:].all() and not bad[1:, :, :96].any() and mx.device_status() == 0
     q[1, 2, 7] = float("inf")                                # an infinite query: its row alone
-    mx.kv_attention_shared(q, c, cu, kv, table, starts, pre, max_q, most, 0.1, out=(o, lse))
+    mx.kv_attention_shared(q, c, cu, kv, table, starts, pre, max_q, most, 0.1, out=(o, lse), share=share)
     bad = torch.isnan(o[: rows + 1].float()).all(-1)
     assert bad[1, 2] and bad.sum() == 1
 
 
-def test_shared_outside_its_bounds(mx):
+@pytest.mark.parametrize("share", [True, False])
+def test_shared_outside_its_bounds(mx, share):
     """Groups and requests that are not as documented are left out and recorded; the others are computed."""
     import torch
     rng = np.random.default_rng(8)
@@ -449,7 +452,7 @@ def test_shared_outside_its_bounds(mx):
         for r, n in (kv_of or {}).items():
             kv[r] = n
         o, lse = results(q)
-        mx.kv_attention_shared(q, c, cu, kv, table, st, p, max_q, most, 0.1, out=(o, lse))
+        mx.kv_attention_shared(q, c, cu, kv, table, st, p, max_q, most, 0.1, out=(o, lse), share=share)
         torch.cuda.synchronize()
         assert mx.device_status() == 7
         if lost is None:
@@ -459,7 +462,7 @@ def test_shared_outside_its_bounds(mx):
             assert (o[r].float() == 77.0).all(), (r, starts, pre, kv_of)
     c, q, cu, kv, table, slots, st, p, _, _, _, _ = shared_case(mx, rng, *args)
     o, lse = results(q)
-    mx.kv_attention_shared(q, c, cu, kv, table, st, p, 1, 1, 0.1, out=(o, lse))  # groups of 2 tokens, 1 allowed
+    mx.kv_attention_shared(q, c, cu, kv, table, st, p, 1, 1, 0.1, out=(o, lse), share=share)  # groups of 2 tokens, 1 allowed
     assert mx.device_status() == 7 and (o[:4].float() == 77.0).all()
 
 
@@ -634,7 +637,7 @@ def test_serving(mx, fmt, page, stream):
             to = host(s.table)[r]
             s.slots[r] = [int(to[p // page]) * page + p % page for p in range(261)]
         prefix = 261 // page * page
-        shared = lambda qr, p: mx.kv_attention_shared(qr, s.c, p.cu_q, p.kv_lens, s.table, dev([0, 4]), dev([prefix]), 8, 32, scale)
+        shared = lambda qr, p: mx.kv_attention_shared(qr, s.c, p.cu_q, p.kv_lens, s.table, dev([0, 4]), dev([prefix]), 8, 32, scale, share=fmt == 0)
         for new in ([1, 1, 1, 1, 1, 5], [1, 3, 0, 8, 2, 1], [2, 2, 2, 2, 0, 1]):
             s.check(*s.step(new, shared))
         for window, sinks in ((50, 4), (1, 0), (1000, 3)):
@@ -673,7 +676,7 @@ def test_captured_and_replayed(mx):
     def one():
         mx.kv_plan(ctx, ones, s.table, s.ring, state, page, R, out=step)
         mx.kv_append_rope(s.c, q, k, v, s.rp, step.positions, step.slots, out=turned)
-        a = mx.kv_attention_shared(turned, s.c, step.cu_q, step.kv_lens, s.table, starts, pre, 1, 4, 0.09)
+        a = mx.kv_attention_shared(turned, s.c, step.cu_q, step.kv_lens, s.table, starts, pre, 1, 4, 0.09, share=True)
         b = mx.kv_attention(turned, s.c, step.cu_q, step.kv_lens, s.table, 1, 0.09, window=70, sinks=2)
         return a, b
     side = torch.cuda.Stream()
@@ -730,7 +733,7 @@ def test_two_streams_at_once(mx):
     torch.cuda.synchronize()
     outs = []
     for _ in range(10):
-        a = mx.kv_attention_shared(shared[1], shared[0], *shared[2:5], *shared[6:10], 0.1, stream=st[0])
+        a = mx.kv_attention_shared(shared[1], shared[0], *shared[2:5], *shared[6:10], 0.1, stream=st[0], share=True)
         b = mx.kv_attention(q, c, cu, kv, table, 200, 0.1, stream=st[1], window=333, sinks=5)
         outs.append((a, b))
     torch.cuda.synchronize()
@@ -777,7 +780,8 @@ def test_calls_on_a_given_stream(mx):
     assert mx.device_status() == 0
 
 
-def test_many_requests_behind_many_prefixes(mx):
+@pytest.mark.parametrize("share", [True, False])
+def test_many_requests_behind_many_prefixes(mx, share):
     """Hundreds of groups, of one and of several requests, and more requests than a CTA of the plan has threads."""
     import torch
     rng = np.random.default_rng(61)
@@ -787,12 +791,12 @@ def test_many_requests_behind_many_prefixes(mx):
         groups.append(([1] * m, int(rng.integers(0, 60)), [int(x) for x in rng.integers(1, 40, m)]))
     c, q, cu, kv, table, slots, starts, pre, max_q, most, q_lens, _ = shared_case(mx, rng, 0, 16, 1, 4, groups, [(1, 5)], [(1, 9)])
     o, lse = results(q)
-    mx.kv_attention_shared(q, c, cu, kv, table, starts, pre, max_q, most, 128 ** -0.5, out=(o, lse))
+    mx.kv_attention_shared(q, c, cu, kv, table, starts, pre, max_q, most, 128 ** -0.5, out=(o, lse), share=share)
     assert mx.device_status() == 0
     compare(c, q, cu, slots, o, lse, lambda r, n, k: more_ref.window_mask(n, k, 1 << 30, 0))
     # by the prompts' kernel: every group may have 20 tokens
     o2, lse2 = results(q)
-    mx.kv_attention_shared(q, c, cu, kv, table, starts, pre, max_q, 20, 128 ** -0.5, out=(o2, lse2))
+    mx.kv_attention_shared(q, c, cu, kv, table, starts, pre, max_q, 20, 128 ** -0.5, out=(o2, lse2), share=share)
     assert mx.device_status() == 0
     compare(c, q, cu, slots, o2, lse2, lambda r, n, k: more_ref.window_mask(n, k, 1 << 30, 0))
 
@@ -820,7 +824,7 @@ def test_far_blocks(mx):
     q = mx.kv_append_rope(c, bf16(rng, 400, H, 128).cuda(), k, v, rp, pos, dev(slots, np.int64))
     o, lse = mx.kv_attention(q[-2:], c, dev([0, 2]), dev([400]), table, 2, 0.09, window=140, sinks=130)
     compare(c, q[-2:], dev([0, 2]), [slots], o, lse, lambda r, n, k: more_ref.window_mask(n, k, 140, 130), scale=0.09)
-    o, lse = mx.kv_attention_shared(q[-2:], c, dev([0, 1, 2]), dev([399, 399]), torch.cat([table, table]), dev([0, 2]), dev([256]), 1, 2, 0.09)
+    o, lse = mx.kv_attention_shared(q[-2:], c, dev([0, 1, 2]), dev([399, 399]), torch.cat([table, table]), dev([0, 2]), dev([256]), 1, 2, 0.09, share=True)
     compare(c, q[-2:], dev([0, 1, 2]), [slots[:399]] * 2, o, lse, lambda r, n, k: more_ref.window_mask(n, k, 1 << 30, 0), scale=0.09)
     mx.kv_copy_blocks(c, dev([69999]), dev([60000]))
     assert torch.equal(c.k[60000], c.k[69999]) and torch.equal(c.v_sf[60000], c.v_sf[69999]) and c.k[60000].any()

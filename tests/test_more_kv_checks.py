@@ -191,12 +191,13 @@ def test_window_checks(mx):
 def test_shared_checks(mx):
     L, ref = mx.lib(), ctypes.byref(_cache(mx))
     base = dict(q=0x10000, qs=512, T=3, cu=0x20000, kv=0x30000, R=2, bt=0x40000, nb=64, mq=3, Hq=4, s=0.1, st=0x70000, pl=0x78000,
-                g=1, mg=3, o=0x50000, lse=0x60000, ws=0x10000000, wb=1 << 34)
+                g=1, mg=3, sh=0, o=0x50000, lse=0x60000, ws=0x10000000, wb=1 << 34)
 
     def call(**kw):
         return L.mxfa_kv_attn_shared(ref, *dict(base, **kw).values(), None)
     for n in ("q", "cu", "kv", "bt", "o", "lse", "st", "pl"):
         assert call(**{n: None}) == 1, n
+    assert call(sh=3) == 1 and call(sh=-1) == 1
     assert call(g=-1) == 1 and call(mg=-1) == 1 and call(Hq=3) == 1 and call(ws=None) == 1 and call(wb=16) == 4
     assert call(g=1 << 21) == 2 and call(T=1 << 31) == 2 and call(st=0x70002) == 3 and call(pl=0x78002) == 3
     for kw in (dict(o=0x70000), dict(lse=0x78000), dict(ws=0x70000), dict(o=0x10000), dict(ws=0x50000), dict(lse=0x110000)):
