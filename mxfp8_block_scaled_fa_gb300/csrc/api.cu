@@ -1248,7 +1248,7 @@ mxfa_status mxfa_kv_copy_blocks(const mxfa_kv_cache* cache, const int32_t* from_
   if (s) return s;
   if (n < 0 || !from_blocks || !to_blocks) return MXFA_ERR_INVALID_ARG;
   if (!aligned4(from_blocks) || !aligned4(to_blocks)) return MXFA_ERR_MISALIGNED;
-  if (int64_t(c.H) * c.page > (1 << 24) || int64_t(n) * kv_copy_chunks(c) >= (int64_t(1) << 31)) return MXFA_ERR_UNSUPPORTED;
+  if (n > kKvCopyMost) return MXFA_ERR_UNSUPPORTED;
   if (n == 0) return MXFA_OK;
   const CacheRanges own = ranges_of(c);
   const Range read[] = {{from_blocks, size_t(n) * 4}, {to_blocks, size_t(n) * 4}};

@@ -226,37 +226,70 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScan) kv_col
   }
 }
 
-// Whole blocks: the codes and scales of all heads of one lie in one piece each.
-__global__ void __launch_bounds__(kThreads) kv_copy_kernel(KvPages c, const int32_t* from, const int32_t* to, int chunks, int code_words,
-                                                           int sf_words) {
-  constexpr int N = 4;
-  const int i = int(blockIdx.x) / chunks, chunk = int(blockIdx.x) - i * chunks;
-  const int32_t a = __ldg(from + i), b = __ldg(to + i);
-  if (a < 0 || b < 0 || a == b) return;
-  if (a >= c.blocks || b >= c.blocks) {
-    if (threadIdx.x == 0) atomicOr(&g_status_kv_pages, DEV_BAD_INDEX);
-    return;
-  }
-  uint4 v[N];
-  uint4* dst[N];
-#pragma unroll
-  for (int e = 0; e < N; e++) {
-    int w = (chunk * N + e) * kThreads + threadIdx.x;
+// Whole blocks: the codes and scales of all heads of one lie in one piece each.  A CTA has the same few words of
+// every pair's blocks, and writes when it has read them all, so blocks may be read and written in one call (a
+// list of moves).  2^log2_words words of 16 bytes: eight, a line of memory, or more for few pairs and fewer for very many.
+// A block written by several pairs holds the last one's: while the words are on their way each pair looks itself up
+// by its block in `last`, an open table of at least two places a pair.
+__global__ void __launch_bounds__(kThreads) kv_copy_kernel(KvPages c, const int32_t* from, const int32_t* to, int n, int log2_words, int code_words,
+                                                           int sf_words, int log2_last) {
+  extern __shared__ uint4 stage[];
+  const int count = n << log2_words, mask = (1 << log2_words) - 1;
+  int* last = reinterpret_cast<int*>(stage + count);
+  auto find = [&](int32_t block, auto&& at) {  // at(place) says whether the place is the block's
+    uint32_t h = (uint32_t(block) * 0x9E3779B1u) >> (32 - log2_last);
+    for (int t = 0; t < (1 << log2_last) && !at(last + h); t++) h = (h + 1) & ((1u << log2_last) - 1);
+  };
+  // word i of the CTA: its place in its pair's blocks, NULL where there is none
+  auto place = [&](int i, const int32_t* list) -> uint4* {
+    int w = (int(blockIdx.x) << log2_words) + (i & mask);
     const bool codes = w < 2 * code_words;
     if (!codes) w -= 2 * code_words;
     const int words = codes ? code_words : sf_words;
     const bool second = w >= words;
     if (second) w -= words;
-    dst[e] = nullptr;
-    if (w < words) {
-      uint4* p = reinterpret_cast<uint4*>(codes ? (second ? c.v : c.k) : (second ? c.v_sf : c.k_sf));
-      v[e] = p[int64_t(a) * words + w];
-      dst[e] = p + int64_t(b) * words + w;
-    }
+    if (w >= words) return nullptr;
+    uint4* p = reinterpret_cast<uint4*>(codes ? (second ? c.v : c.k) : (second ? c.v_sf : c.k_sf));
+    return p + int64_t(__ldg(list + (i >> log2_words))) * words + w;
+  };
+  auto live = [&](int pair) {
+    const int32_t a = __ldg(from + pair), b = __ldg(to + pair);
+    if (a < 0 || b < 0) return false;
+    if (a < c.blocks && b < c.blocks) return true;
+    if (blockIdx.x == 0) atomicOr(&g_status_kv_pages, DEV_BAD_INDEX);
+    return false;
+  };
+  for (int i = threadIdx.x; i < count; i += kThreads) {
+    if (!live(i >> log2_words)) continue;
+    const uint4* src = place(i, from);
+    if (src) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(stage + i)), "l"(src) : "memory");
   }
-#pragma unroll
-  for (int e = 0; e < N; e++)
-    if (dst[e]) *dst[e] = v[e];
+  for (int i = threadIdx.x; i < (1 << log2_last); i += kThreads) last[i] = -1;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    if (!live(i)) continue;
+    const int32_t block = __ldg(to + i);
+    find(block, [&](int* p) {
+      const int j = atomicCAS(p, -1, i);
+      if (j >= 0 && __ldg(to + j) != block) return false;
+      if (j >= 0) atomicMax(p, i);
+      return true;
+    });
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  for (int i = threadIdx.x; i < count; i += kThreads) {
+    const int pair = i >> log2_words;
+    if (!live(pair)) continue;
+    const int32_t block = __ldg(to + pair);
+    bool mine = true;
+    find(block, [&](int* p) {
+      mine = *p == pair;
+      return mine || __ldg(to + *p) == block;
+    });
+    uint4* dst = place(i, to);
+    if (mine && dst) *dst = stage[i];
+  }
 }
 
 }  // namespace
@@ -287,15 +320,23 @@ cudaError_t launch_kv_free(const KvFreeArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-int kv_copy_chunks(const KvPages& c) {
-  const int64_t words = 2 * (int64_t(c.H) * c.page * 4 + int64_t(c.H) * c.page / (c.fmt == 0 ? 4 : 2));
-  return int((words + 4 * kThreads - 1) / (4 * kThreads));
-}
-
 cudaError_t launch_kv_copy(const KvPages& c, const int32_t* from, const int32_t* to, int n, cudaStream_t st) {
   clear_stale_error();
-  const int chunks = kv_copy_chunks(c);
-  kv_copy_kernel<<<unsigned(int64_t(n) * chunks), kThreads, 0, st>>>(c, from, to, chunks, c.H * c.page * 4, c.H * c.page / (c.fmt == 0 ? 4 : 2));
+  static std::atomic<unsigned long long> done{0};
+  constexpr int kBytes = kKvCopyMost * (16 + 8);
+  const cudaError_t e = once_per_device(done, [] {
+    return cudaFuncSetAttribute(kv_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  });
+  if (e != cudaSuccess) return e;
+  int log2_words = 3;
+  while (log2_words > 0 && (int64_t(n) << log2_words) > kKvCopyMost) log2_words--;
+  while (log2_words < 6 && (int64_t(n) << log2_words) < 1024) log2_words++;
+  int log2_last = 1;
+  while ((1 << log2_last) < 2 * n) log2_last++;
+  const int codes = c.H * c.page * 4, sf = c.H * c.page / (c.fmt == 0 ? 4 : 2);
+  const int64_t words = 2 * (int64_t(codes) + sf);
+  const unsigned grid = unsigned((words + (1 << log2_words) - 1) >> log2_words);
+  kv_copy_kernel<<<grid, kThreads, (size_t(n) << log2_words) * 16 + (size_t(4) << log2_last), st>>>(c, from, to, n, log2_words, codes, sf, log2_last);
   return cudaGetLastError();
 }
 

@@ -376,7 +376,7 @@ struct KvFreeArgs {
   int64_t* ring_out;
 };
 cudaError_t launch_kv_free(const KvFreeArgs& a, cudaStream_t s);
-int kv_copy_chunks(const KvPages& c);  // CTAs of a block
+constexpr int kKvCopyMost = 8192;  // pairs of a call: a word each in shared memory, and two places
 cudaError_t launch_kv_copy(const KvPages& c, const int32_t* from, const int32_t* to, int n, cudaStream_t s);
 
 // Read (and clear) the device status words of every kernel module.

@@ -1379,7 +1379,8 @@ def kv_free(block_table: torch.Tensor, rows: torch.Tensor, first: torch.Tensor, 
 
 def kv_copy_blocks(cache: KvCache, from_blocks: torch.Tensor, to_blocks: torch.Tensor, stream=None):
     """Copies blocks from_blocks (int32 [n]) of the cache over to_blocks, all heads; pairs with a
-    negative one are skipped.  The blocks written are distinct and none of those read."""
+    negative one are skipped.  All are read before any is written; a block written twice holds the last pair's.
+    At most 8192 pairs."""
     if stream is None:
         status = _fast().copy_blocks(cache.raw, from_blocks, to_blocks)
         if status is not None:

@@ -553,7 +553,7 @@ def test_pages_outside_their_bounds(mx):
     assert mx.device_status() == 7 and host(s).tolist() == [2, 4, 0] and not refs.any()    # given up twice: freed once
 
 
-@pytest.mark.parametrize("fmt,H,page,blocks", [(0, 1, 16, 5), (1, 3, 16, 9), (0, 8, 128, 6), (1, 5, 64, 40)])
+@pytest.mark.parametrize("fmt,H,page,blocks", [(0, 1, 16, 5), (1, 3, 16, 9), (0, 8, 128, 6), (1, 5, 64, 40), (0, 2, 16, 8192), (1, 1, 32, 3000), (0, 3, 16, 300)])
 def test_copy_blocks(mx, fmt, H, page, blocks):
     import torch
     rng = np.random.default_rng(blocks)
@@ -569,6 +569,25 @@ def test_copy_blocks(mx, fmt, H, page, blocks):
     for t, w in zip((c.k, c.v, c.k_sf, c.v_sf), want):
         np.testing.assert_array_equal(host(t), w)
     assert mx.device_status() == 7                           # block `blocks` is past the cache
+    # moves: a block that is read is written too, in a ring and along a line, more of them than a CTA has threads
+    for n in (blocks - 1, blocks):
+        before = [host(t).copy() for t in (c.k, c.v, c.k_sf, c.v_sf)]
+        order = rng.permutation(blocks)[:n]
+        mx.kv_copy_blocks(c, dev(order), dev(np.roll(order, 1)))
+        for t, w in zip((c.k, c.v, c.k_sf, c.v_sf), before):
+            w[np.roll(order, 1)] = w[order]
+            np.testing.assert_array_equal(host(t), w)
+    # blocks written by several pairs: the last one's stays
+    a, b = (rng.integers(-1, blocks, blocks) for _ in range(2))
+    b[: blocks // 2] = b[blocks - blocks // 2:]
+    before = [host(t).copy() for t in (c.k, c.v, c.k_sf, c.v_sf)]
+    mx.kv_copy_blocks(c, dev(a), dev(b))
+    for t, old in zip((c.k, c.v, c.k_sf, c.v_sf), before):
+        w = old.copy()
+        for x, y in zip(a, b):
+            if x >= 0 and y >= 0:
+                w[y] = old[x]
+        np.testing.assert_array_equal(host(t), w)
     mx.kv_copy_blocks(c, dev([]), dev([]))
     assert mx.device_status() == 0
 

@@ -252,8 +252,7 @@ def test_copy_checks(mx):
     assert f(ref, None, 0x2000, 3, None) == 1 and f(ref, 0x1000, None, 3, None) == 1 and f(ref, 0x1000, 0x2000, -1, None) == 1
     assert f(ref, 0x1002, 0x2000, 3, None) == 3 and f(ref, 0x1000, 0x2002, 3, None) == 3
     assert f(ref, 0x100000, 0x2000, 3, None) == 1 and f(ref, 0x1000, 0x130000, 3, None) == 1
-    assert f(ctypes.byref(_cache(mx, H=65536, page=128)), 0x1000, 0x2000, 1, None) != 0
-    assert f(ctypes.byref(_cache(mx, H=4096, page=128)), 0x1000, 0x2000, 1 << 30, None) == 2
+    assert f(ref, 0x1000, 0x2000, 8193, None) == 2
     assert f(ctypes.byref(_cache(mx, D=64)), 0x1000, 0x2000, 3, None) == 2
     assert f(ctypes.byref(_cache(mx, v=0x100000)), 0x1000, 0x2000, 3, None) == 1
     assert f(ref, 0x1000, 0x2000, 0, None) == 0
