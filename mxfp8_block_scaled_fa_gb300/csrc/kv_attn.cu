@@ -46,6 +46,12 @@
 // cache again.  Other forms, in their time: query rows as M 115 us for the first case
 // where keys as M took 88; bulk copies 91 where these took 85; two chains of score
 // products, no change.
+//
+// Windows and prefixes (KvKind).  With a window a row sees the first `sinks` keys and the
+// last `window` ones: the tiles that hold neither are no part of the line, table entries of
+// hidden keys are not read, and steps without a key in sight are left out.  16 requests of up
+// to 32768 keys, window 4096, 4 sinks, 8 key heads, G = 4: 30 us (floor 10): the same chain,
+// and 8 units a CTA to spread its start over.  Prefixes and what is behind them: kv_shared.cu.
 #include "kv_fp4.cuh"
 #include "mx_ptx.cuh"
 #include "mxfa_internal.h"

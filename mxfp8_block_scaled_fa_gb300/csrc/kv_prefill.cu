@@ -30,8 +30,8 @@
 // half as long for the 32768 exponentials.  The products of 64 keys read Q again for
 // each half (6 KB of shared memory in 32 cycles, where 128 B a cycle is the most), and
 // take 50 to 90 cycles each instead of 32.  Chunks of 2048 and 1687 tokens over 8192 and
-// 5331 keys, 8 key heads, G = 4, NVFP4: 309 us, 1180 TFLOP/s, of which the main
-// kernel 290 us; about 3300 cycles a tile (issuers: P V 750, S 1400, waits), and
+// 5331 keys, 8 key heads, G = 4, NVFP4: 304 us, 1200 TFLOP/s, of which the main
+// kernel 285 us; about 3300 cycles a tile (issuers: P V 750, S 1400, waits), and
 // 12000 cycles between items, when the softmax warps bring the next queries (half of
 // them) and write O.  Other forms of it, same case: whole S products of 128 keys and
 // one issuer, softmax, P V and S in turn, 347 us; these with two issuers 360 to 407 us;
@@ -41,7 +41,15 @@
 // 312 us.  For items of up to 128 rows both softmax groups on the same rows, each with
 // half of the keys, 137 against 117 us for 24 x 64 rows over 6000 keys.  Launched ahead
 // of the kernels they wait for, the five kernels of a call take 313 instead of 319 us
-// from a stream (310 from a graph, either way).
+// from a stream (310 from a graph, either way).  These are figures of their time, against 309 us in the end; the
+// issuers' loops over items, no longer than the call needs, then made it 304.
+//
+// Windows and prefixes (KvKind, as in kv_attn.cu).  With a window an item's keys are the tiles of the sinks and those from its
+// first row's window on; the tiles between are no part of the line, and what a row does not see of the others is masked by
+// bits.  The chunks above with a window of 1024 and 64 sinks: 106 us, 8.5 tiles' worth of keys in 10.5 tiles an item, and
+// the 12000 cycles between items on 472 items; a half whose keys no row of a warp sees is computed like the others
+// (left out: no change).  A prefix takes about 21 us for up to eight tiles, of which 4 pass until the item is known, 3 for the
+// queries, 0.85 a tile, and 5 for the records, as each thread stores its row (rows side by side: 2, and 2 us more in the join).
 #include "kv_fp4.cuh"
 #include "mx_ptx.cuh"
 #include "mxfa_internal.h"
