@@ -21,6 +21,7 @@ static __device__ unsigned g_status_kv_pages;
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kCopyThreads = 512;
 constexpr int kSegment = 2048;  // table entries of a CTA
 constexpr int kScan = 1024;     // threads of a CTA that collects
 constexpr int kCluster = 8;
@@ -228,20 +229,57 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScan) kv_col
 
 // Whole blocks: the codes and scales of all heads of one lie in one piece each.  A CTA has the same few words of
 // every pair's blocks, and writes when it has read them all, so blocks may be read and written in one call (a
-// list of moves).  2^log2_words words of 16 bytes: eight, a line of memory, or more for few pairs and fewer for very many.
-// A block written by several pairs holds the last one's: while the words are on their way each pair looks itself up
-// by its block in `last`, an open table of at least two places a pair.
-__global__ void __launch_bounds__(kThreads) kv_copy_kernel(KvPages c, const int32_t* from, const int32_t* to, int n, int log2_words, int code_words,
+// list of moves).  2^log2_words words of 16 bytes: eight, a line of memory; more for few pairs, to fill the CTA, and
+// fewer for many, so that several CTAs fit an SM (1000 pairs of 128 rows, 8 heads: eight words 78 us, four 57, 4.9 TB/s).
+// 512 threads: 200 pairs of 16 rows 3.9 us, of 64 rows 6.7; 256 threads 4.6 and 6.4, 1024 3.6 and 8.2.
+// Of several pairs that write one block the last is kept: each looks itself up by its block in `last`, an open table
+// of at least two places a pair, which lies where the words are put afterwards.
+__global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(KvPages c, const int32_t* from, const int32_t* to, int n, int log2_words, int code_words,
                                                            int sf_words, int log2_last) {
   extern __shared__ uint4 stage[];
   const int count = n << log2_words, mask = (1 << log2_words) - 1;
-  int* last = reinterpret_cast<int*>(stage + count);
-  auto find = [&](int32_t block, auto&& at) {  // at(place) says whether the place is the block's
+  int* last = reinterpret_cast<int*>(stage);
+  const int places = 1 << log2_last;
+  int2* pairs = reinterpret_cast<int2*>(stage + count);  // the table, less than 16 bytes a pair, ends before
+  for (int i = threadIdx.x; i < n; i += kCopyThreads) {
+    int2 p = make_int2(__ldg(from + i), __ldg(to + i));
+    if (p.x >= c.blocks || p.y >= c.blocks) {
+      if (blockIdx.x == 0 && p.x >= 0 && p.y >= 0) atomicOr(&g_status_kv_pages, DEV_BAD_INDEX);
+      p.x = -1;
+    }
+    if (p.y < 0) p.x = -1;
+    pairs[i] = p;
+  }
+  for (int i = threadIdx.x; i < places; i += kCopyThreads) last[i] = -1;
+  __syncthreads();
+  // the place of a block: the first one from its hash on that `at` says is its
+  auto find = [&](int32_t block, auto&& at) {
     uint32_t h = (uint32_t(block) * 0x9E3779B1u) >> (32 - log2_last);
-    for (int t = 0; t < (1 << log2_last) && !at(last + h); t++) h = (h + 1) & ((1u << log2_last) - 1);
+    for (int t = 0; t < places && !at(last + h); t++) h = (h + 1) & uint32_t(places - 1);
   };
-  // word i of the CTA: its place in its pair's blocks, NULL where there is none
-  auto place = [&](int i, const int32_t* list) -> uint4* {
+  for (int i = threadIdx.x; i < n; i += kCopyThreads) {
+    const int2 pair = pairs[i];
+    if (pair.x < 0) continue;
+    find(pair.y, [&](int* p) {
+      const int j = atomicCAS(p, -1, i);
+      if (j >= 0 && pairs[j].y != pair.y) return false;
+      if (j >= 0) atomicMax(p, i);
+      return true;
+    });
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kCopyThreads) {
+    const int2 pair = pairs[i];
+    if (pair.x < 0) continue;
+    find(pair.y, [&](int* p) {
+      if (pairs[*p].y != pair.y) return false;
+      if (*p != i) pairs[i].x = -1;
+      return true;
+    });
+  }
+  __syncthreads();
+  // word i of the CTA in a block: which of the four arrays, and where
+  auto place = [&](int i, int32_t block) -> uint4* {
     int w = (int(blockIdx.x) << log2_words) + (i & mask);
     const bool codes = w < 2 * code_words;
     if (!codes) w -= 2 * code_words;
@@ -250,45 +288,21 @@ __global__ void __launch_bounds__(kThreads) kv_copy_kernel(KvPages c, const int3
     if (second) w -= words;
     if (w >= words) return nullptr;
     uint4* p = reinterpret_cast<uint4*>(codes ? (second ? c.v : c.k) : (second ? c.v_sf : c.k_sf));
-    return p + int64_t(__ldg(list + (i >> log2_words))) * words + w;
+    return p + int64_t(block) * words + w;
   };
-  auto live = [&](int pair) {
-    const int32_t a = __ldg(from + pair), b = __ldg(to + pair);
-    if (a < 0 || b < 0) return false;
-    if (a < c.blocks && b < c.blocks) return true;
-    if (blockIdx.x == 0) atomicOr(&g_status_kv_pages, DEV_BAD_INDEX);
-    return false;
-  };
-  for (int i = threadIdx.x; i < count; i += kThreads) {
-    if (!live(i >> log2_words)) continue;
-    const uint4* src = place(i, from);
+#pragma unroll 4
+  for (int i = threadIdx.x; i < count; i += kCopyThreads) {
+    const int2 pair = pairs[i >> log2_words];
+    const uint4* src = pair.x < 0 ? nullptr : place(i, pair.x);
     if (src) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(stage + i)), "l"(src) : "memory");
-  }
-  for (int i = threadIdx.x; i < (1 << log2_last); i += kThreads) last[i] = -1;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    if (!live(i)) continue;
-    const int32_t block = __ldg(to + i);
-    find(block, [&](int* p) {
-      const int j = atomicCAS(p, -1, i);
-      if (j >= 0 && __ldg(to + j) != block) return false;
-      if (j >= 0) atomicMax(p, i);
-      return true;
-    });
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  for (int i = threadIdx.x; i < count; i += kThreads) {
-    const int pair = i >> log2_words;
-    if (!live(pair)) continue;
-    const int32_t block = __ldg(to + pair);
-    bool mine = true;
-    find(block, [&](int* p) {
-      mine = *p == pair;
-      return mine || __ldg(to + *p) == block;
-    });
-    uint4* dst = place(i, to);
-    if (mine && dst) *dst = stage[i];
+#pragma unroll 4
+  for (int i = threadIdx.x; i < count; i += kCopyThreads) {
+    const int2 pair = pairs[i >> log2_words];
+    uint4* dst = pair.x < 0 ? nullptr : place(i, pair.y);
+    if (dst) *dst = stage[i];
   }
 }
 
@@ -323,20 +337,22 @@ cudaError_t launch_kv_free(const KvFreeArgs& a, cudaStream_t st) {
 cudaError_t launch_kv_copy(const KvPages& c, const int32_t* from, const int32_t* to, int n, cudaStream_t st) {
   clear_stale_error();
   static std::atomic<unsigned long long> done{0};
-  constexpr int kBytes = kKvCopyMost * (16 + 8);
+  constexpr int kBytes = kKvCopyMost * (16 + 8);  // words, and pairs of the largest call
   const cudaError_t e = once_per_device(done, [] {
     return cudaFuncSetAttribute(kv_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   });
   if (e != cudaSuccess) return e;
   int log2_words = 3;
+  while (log2_words > 1 && (int64_t(n) << log2_words) > 4096) log2_words--;
   while (log2_words > 0 && (int64_t(n) << log2_words) > kKvCopyMost) log2_words--;
-  while (log2_words < 6 && (int64_t(n) << log2_words) < 1024) log2_words++;
+  while (log2_words < 6 && (int64_t(n) << log2_words) < kCopyThreads) log2_words++;
   int log2_last = 1;
   while ((1 << log2_last) < 2 * n) log2_last++;
+  const size_t shared = (size_t(n) << log2_words) * 16 + size_t(n) * 8;
   const int codes = c.H * c.page * 4, sf = c.H * c.page / (c.fmt == 0 ? 4 : 2);
   const int64_t words = 2 * (int64_t(codes) + sf);
   const unsigned grid = unsigned((words + (1 << log2_words) - 1) >> log2_words);
-  kv_copy_kernel<<<grid, kThreads, (size_t(n) << log2_words) * 16 + (size_t(4) << log2_last), st>>>(c, from, to, n, log2_words, codes, sf, log2_last);
+  kv_copy_kernel<<<grid, kCopyThreads, shared, st>>>(c, from, to, n, log2_words, codes, sf, log2_last);
   return cudaGetLastError();
 }
 
