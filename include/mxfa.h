@@ -662,7 +662,8 @@ mxfa_status mxfa_kv_free(const int32_t* block_table, int R, int max_blocks, cons
 /* mxfa_kv_copy_blocks -- block from_blocks[i] of the cache (all heads, codes and scales of K and V) over
  * to_blocks[i], n <= 8192; pairs with a negative one are skipped, ones past the cache skipped and
  * recorded.  All blocks are read before any is written, so a block may be read and written (a list of
- * moves); one that is written by several pairs holds the last one's. */
+ * moves); one that is written by several pairs holds the last one's.  mxfa_kv_fork's pairs, of which no
+ * block is both, may be copied in pieces. */
 mxfa_status mxfa_kv_copy_blocks(const mxfa_kv_cache* cache, const int32_t* from_blocks, const int32_t* to_blocks, int n,
                                 mxfa_stream_t stream);
 
