@@ -201,7 +201,9 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(RopeArgs a) {
   }
 }
 
-// The same for q, and k and v into the cache.  A warp has heads of q, or rows of K and V (those of K first).
+// The same for q, and k and v into the cache.  A warp has heads of q, or rows of K and V (those of K first), each in a loop of
+// its own: one for both took 68 us instead of 61 for 16384 tokens of 32 + 8 heads.  The next rows on their way while
+// these are turned: 79 (registers for fewer warps).
 template <int FMT, bool INTER, int N>
 __global__ void __launch_bounds__(kWarps * 32) kv_append_rope_kernel(KvAppendRopeArgs a) {
   __shared__ __align__(16) float2 s_cs[kWarps][64];
@@ -231,37 +233,53 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append_rope_kernel(KvAppendRop
   const uint16_t* v = a.v + token * a.v_stride;
   uint16_t* y = a.y + token * a.y_stride;
   uint4 x[N];
-  auto load = [&](int h) {
+  auto load = [&](int h, auto&& at) {
 #pragma unroll
     for (int i = 0; i < N; i++) {
       const int r = h + 2 * i;
       x[i] = make_uint4(0, 0, 0, 0);
-      if (r < h1) {
-        const uint16_t* src = is_q ? q + r * 128 : r < a.c.H ? k + r * 128 : v + (r - a.c.H) * 128;
-        x[i] = load_stream(reinterpret_cast<const uint4*>(src + l16 * 8));
-      }
+      if (r < h1) x[i] = load_stream(reinterpret_cast<const uint4*>(at(r) + l16 * 8));
     }
   };
   int h = h0 + (lane >> 4);
-  load(h);  // on their way while the angles are computed
+  if (is_q) {
+    auto at = [&](int r) { return q + r * 128; };
+    load(h, at);  // on their way while the angles are computed
+    angles(a.rot, pos, lane, s_cs[warp]);
+    const Turn<INTER> turn(s_cs[warp], a.rot.rot, lane);
+    while (true) {
+#pragma unroll
+      for (int i = 0; i < N; i++) {
+        const int r = h + 2 * i;
+        const uint4 o = turn(x[i]);
+        if (r < h1) __stcs(reinterpret_cast<uint4*>(y + r * 128 + l16 * 8), o);
+      }
+      h += 2 * N;
+      if (h - (lane >> 4) >= h1) break;
+      load(h, at);
+    }
+    return;
+  }
+  auto at = [&](int r) { return r < a.c.H ? k + r * 128 : v + (r - a.c.H) * 128; };
+  load(h, at);
   angles(a.rot, pos, lane, s_cs[warp]);
   const Turn<INTER> turn(s_cs[warp], a.rot.rot, lane);
   while (true) {
 #pragma unroll
     for (int i = 0; i < N; i++) {
       const int r = h + 2 * i;
-      const uint4 o = turn(x[i]);
-      if (is_q) {
-        if (r < h1) *reinterpret_cast<uint4*>(y + r * 128 + l16 * 8) = o;
-      } else {
-        const bool is_v = r >= a.c.H;
-        const int64_t at = (block * a.c.H + (is_v ? r - a.c.H : r)) * a.c.page + (slot & (a.c.page - 1));
-        kv_store_row<FMT>(a.c, r < h1, is_v, at, l16, is_v ? x[i] : o);
+      const bool is_v = r >= a.c.H;
+      uint4 o = x[i];
+      if (r - (lane >> 4) < a.c.H) {  // of K, or the warp's other row is
+        const uint4 t = turn(o);
+        if (!is_v) o = t;
       }
+      const int64_t to = (block * a.c.H + (is_v ? r - a.c.H : r)) * a.c.page + (slot & (a.c.page - 1));
+      kv_store_row<FMT>(a.c, r < h1, is_v, to, l16, o);
     }
     h += 2 * N;
     if (h - (lane >> 4) >= h1) break;
-    load(h);
+    load(h, at);
   }
 }
 
