@@ -148,8 +148,8 @@ struct Turn {
       const uint32_t p = INTER ? w[e] : __shfl_sync(0xFFFFFFFFu, w[e], partner);
       const float2 own = make_float2(bf_lo(w[e]), bf_hi(w[e]));
       const float2 other = INTER ? make_float2(own.y, own.x) : make_float2(bf_lo(p), bf_hi(p));
-      // rounded one by one: packed pairs of products and sums would be merged into a multiply-add (82.8 instead of
-      // 84.9 us for 16384 tokens stored, and some bf16 results another)
+      // rounded one by one: packed pairs of products and sums would be merged into a multiply-add, and some
+      // bf16 results another (16384 tokens stored 2 us sooner at most)
       y[e] = pack_bf16(__fadd_rn(__fmul_rn(own.x, c[e].x), __fmul_rn(other.x, s[e].x)),
                        __fadd_rn(__fmul_rn(own.y, c[e].y), __fmul_rn(other.y, s[e].y)));
     }
@@ -284,8 +284,10 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append_rope_kernel(KvAppendRop
 }
 
 // Heads a warp takes, `most` at most: fewer where there are few tokens, so that the call spreads over the GPU; many
-// share a token's angles.  16384 tokens of 32 + 8 heads stored take 89, 74, 67 and 67 us with 8, 16, 32 and 64, of 32
-// heads turned 47, 43, 44 and 44 us.
+// share a token's angles.  16384 tokens of 32 + 8 heads stored take 65 and 61 us with 16 and 32 (89, 74, 67 and 67 with 8, 16,
+// 32 and 64 while q, k and v had one loop), of 32 heads turned 47, 43, 44 and 44 us with 8 to 64.  For 32 warps an SM;
+// for 64, 1024 to 4096 tokens of 32 + 8 heads take 9.4, 11.8 and 17.6 us instead of 7.9, 11.6 and 16.0, for 16, 1531 of 20 + 5 in
+// NVFP4 12.4 instead of 10.5.
 int heads_per_part(int64_t tokens, int heads, int most) {
   const int64_t warps = int64_t(sm_count_current_device()) * 32;
   for (int n = most; n > 2; n /= 2)
