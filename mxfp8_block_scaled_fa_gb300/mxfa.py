@@ -1168,30 +1168,43 @@ class Rope:
 
     @staticmethod
     def make(rot: int = 128, base: float = 10000.0, interleaved: bool = False, scaling: Optional[str] = None,
-             factor: float = 1.0, original: int = 4096, device="cuda") -> "Rope":
+             factor: float = 1.0, original: int = 4096, device="cuda", fast: float = 32.0, slow: float = 1.0,
+             rounded: bool = True, gain: Optional[float] = None) -> "Rope":
         """Frequencies base^(-2 i / rot), for a context `factor` times the `original` one scaled
           "linear"  all of them divided by factor,
           "ntk"     with base * factor^(rot / (rot - 2)): the slowest divided by factor, the fastest as it was,
-          "yarn"    divided by factor where a pair turns less than once in the original context, kept
-                    where it turns 32 times or more, blended in between over the logarithm of its
-                    wavelength's inverse, and the gain 0.1 ln(factor) + 1."""
+          "yarn"    kept up to pair low, divided by factor from pair high on, and blended in between, linearly in
+                    the pair's index: low and high are the places, among pairs, of one that turns `fast` and
+                    `slow` times in the original context, rot / 2 ln(original / (2 pi turns)) / ln(base), `rounded`
+                    down and up to whole pairs, within 0 .. rot - 1.  This is the form that models were
+                    trained with, not the method's paper's ramp over the number of turns.
+        gain: 0.1 ln(factor) + 1 with "yarn", else 1, unless given."""
         if rot <= 0 or rot % 16 or rot > 128:
             raise ValueError(f"{rot} rotated channels, expected 16, 32, .., 128")
         if not base > 1.0 or not factor >= 1.0 or original < 1:
             raise ValueError("base is above 1, factor and original at least 1")
         if scaling not in (None, "linear", "ntk", "yarn"):
             raise ValueError(f"unknown scaling {scaling!r}")
+        if not fast > slow or not slow > 0.0:
+            raise ValueError("fast is above slow, and slow above 0")
+        if gain is not None and not math.isfinite(gain):
+            raise ValueError(f"gain is {gain}")
         if scaling == "ntk":
             base = base * factor ** (rot / (rot - 2))
         f = [base ** (-2 * i / rot) for i in range(rot // 2)]
-        gain = 1.0
         if scaling == "linear":
             f = [x / factor for x in f]
         elif scaling == "yarn":
-            keep = [min(1.0, max(0.0, math.log(original * x / (2 * math.pi)) / math.log(32.0))) for x in f]
+            low, high = (rot / 2 * math.log(original / (2 * math.pi * turns)) / math.log(base) for turns in (fast, slow))
+            if rounded:
+                low, high = math.floor(low), math.ceil(high)
+            low, high = max(low, 0), min(high, rot - 1)
+            width = max(high - low, 1e-3)                    # bounds that meet: a step
+            keep = [1.0 - min(1.0, max(0.0, (i - low) / width)) for i in range(rot // 2)]
             f = [x * (k + (1.0 - k) / factor) for x, k in zip(f, keep)]
-            gain = 0.1 * math.log(factor) + 1.0
-        return Rope.from_freqs(f, interleaved, gain, device)
+            if gain is None:
+                gain = 0.1 * math.log(factor) + 1.0
+        return Rope.from_freqs(f, interleaved, 1.0 if gain is None else float(gain), device)
 
 
 def rope_positions(seqs: Seqs, device="cuda") -> torch.Tensor:
