@@ -642,8 +642,8 @@ mxfa_status mxfa_kv_append_rope(const mxfa_kv_cache* cache, const void* q, int64
  *               (ring_out[2] counts them) the whole pages of it alone, with -1 behind them in the table
  *  free_ring, ring_in/out  as mxfa_kv_plan; ring_out may be ring_in
  * Other entries of row dst stay.  Forks outside their bounds give nothing (lens_out 0), and entries that are no
- * blocks are copied as -1 without an owner; both are recorded as failed index checks.  Other buffers that
- * overlap are MXFA_ERR_INVALID_ARG. */
+ * blocks are copied as -1 without an owner (a last page's takes no block of the ring: lens_out is the whole pages
+ * alone); both are recorded as failed index checks.  Other buffers that overlap are MXFA_ERR_INVALID_ARG. */
 mxfa_status mxfa_kv_fork(int32_t* block_table, int R, int max_blocks, const int32_t* src, const int32_t* dst,
                          const int32_t* lens, int F, int32_t* refs, int64_t num_blocks, const int32_t* free_ring,
                          int64_t ring_size, const int64_t* ring_in, int64_t* ring_out, int page, int32_t* from_blocks,

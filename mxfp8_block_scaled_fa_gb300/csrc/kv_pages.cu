@@ -31,25 +31,32 @@ constexpr int64_t kInside = 4096;
 
 struct Fork {
   int src, dst, whole;
-  bool part;   // a last page that is not full
+  bool part;    // a last page that is not full
+  int32_t old;  // its block, -1: none, or no block of the cache
+  __device__ __forceinline__ bool takes() const { return part && old >= 0; }  // a place of the ring
 };
 __device__ __forceinline__ bool fork_of(const KvForkArgs& a, int f, Fork& x) {
   x.src = __ldg(a.src + f), x.dst = __ldg(a.dst + f);
   const int len = __ldg(a.lens + f);
   x.whole = 0;
   x.part = false;
+  x.old = -1;
   if (x.src < 0 || x.src >= a.R || x.dst < 0 || x.dst >= a.R || x.src == x.dst || len < 0 || len > int64_t(a.width) << a.page_shift) return false;
   x.whole = len >> a.page_shift;
   x.part = (len & ((1 << a.page_shift) - 1)) != 0;
+  if (x.part) {
+    const int32_t b = a.table[int64_t(x.src) * a.width + x.whole];
+    if (b >= 0 && b < a.blocks) x.old = b;
+  }
   return true;
 }
 
-// Forks before f that need a block; all threads of the CTA.
+// Forks before f that take a block; all threads of the CTA.
 __device__ __forceinline__ int parts_before(const KvForkArgs& a, int f, int* s_sum) {
   int n = 0;
   for (int i = threadIdx.x; i < f; i += kThreads) {
     Fork x;
-    n += fork_of(a, i, x) && x.part;
+    n += fork_of(a, i, x) && x.takes();
   }
   n = __reduce_add_sync(0xFFFFFFFFu, n);
   if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = n;
@@ -69,6 +76,7 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvForkArgs a) {
   Fork x;
   x.src = x.dst = x.whole = 0;
   x.part = false;
+  x.old = -1;
   const bool good = f < a.F && fork_of(a, f, x);
   if (good) {
     const int32_t* from = a.table + int64_t(x.src) * a.width;
@@ -92,16 +100,18 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvForkArgs a) {
   const int64_t room = tail - head;
   const int64_t avail = room < 0 ? 0 : room < a.ring_size ? room : a.ring_size;
   int rank = 0;
-  if (x.part || last) rank = parts_before(a, min(f, a.F), s_sum);
+  if (x.takes() || last) rank = parts_before(a, min(f, a.F), s_sum);
   if (threadIdx.x != 0) return;
   if (f < a.F) {
     int32_t old = -1, fresh = -1;
     int len = good ? __ldg(a.lens + f) : 0;
     if (x.part) {
-      if (rank < avail) {
-        old = a.table[int64_t(x.src) * a.width + x.whole];
+      if (!x.takes()) {
+        atomicOr(&g_status_kv_pages, DEV_BAD_INDEX);
+      } else if (rank < avail) {
+        old = x.old;
         fresh = a.ring[in_ring(head + rank, a.ring_size)];
-        if (old < 0 || old >= a.blocks || fresh < 0 || fresh >= a.blocks) {
+        if (fresh < 0 || fresh >= a.blocks) {
           atomicOr(&g_status_kv_pages, DEV_BAD_INDEX);
           old = fresh = -1;
         }
@@ -114,7 +124,7 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvForkArgs a) {
     a.lens_out[f] = len;
   }
   if (last && a.ring_out) {
-    const int64_t want = rank + (x.part ? 1 : 0), took = want < avail ? want : avail;
+    const int64_t want = rank + (x.takes() ? 1 : 0), took = want < avail ? want : avail;
     a.ring_out[0] = head + took;
     a.ring_out[1] = tail;
     a.ring_out[2] = want - took;
