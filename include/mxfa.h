@@ -649,10 +649,21 @@ mxfa_status mxfa_kv_fork(int32_t* block_table, int R, int max_blocks, const int3
                          int64_t ring_size, const int64_t* ring_in, int64_t* ring_out, int page, int32_t* from_blocks,
                          int32_t* to_blocks, int32_t* lens_out, mxfa_stream_t stream);
 
+/* mxfa_kv_fork_gap -- mxfa_kv_fork of requests that have given pages up (behind a window, its sinks' pages kept):
+ * entries gap_first[f] .. gap_end[f] - 1 of row src[f] are neither read nor shared, and are -1 in row dst[f].
+ * mxfa_kv_fork would count an owner for them, although such a block is in the ring or another request's by then.
+ *  gap_first, gap_end  DEVICE int32 [F], 0 <= gap_first <= gap_end <= lens / page (else the fork is outside its
+ *               bounds); equal: none.  Both NULL: as mxfa_kv_fork */
+mxfa_status mxfa_kv_fork_gap(int32_t* block_table, int R, int max_blocks, const int32_t* src, const int32_t* dst,
+                             const int32_t* lens, const int32_t* gap_first, const int32_t* gap_end, int F, int32_t* refs,
+                             int64_t num_blocks, const int32_t* free_ring, int64_t ring_size, const int64_t* ring_in,
+                             int64_t* ring_out, int page, int32_t* from_blocks, int32_t* to_blocks, int32_t* lens_out,
+                             mxfa_stream_t stream);
+
 /* mxfa_kv_free -- pages given up: for each f, entries first[f] .. end[f] - 1 of row rows[f] (ended requests,
  * rejected continuations, pages behind a window) have one owner fewer; negative entries are skipped.  Blocks left
  * without an owner go to the ring in ascending order.  The table stays as it is: an entry given up is not given
- * up again.  ring_size is at least num_blocks (MXFA_ERR_INVALID_ARG); ring_out may be ring_in; ring_out[2] is ring_in[2].  Rows and ranges
+ * up again, and a row that has some is forked by mxfa_kv_fork_gap.  ring_size is at least num_blocks (MXFA_ERR_INVALID_ARG); ring_out may be ring_in; ring_out[2] is ring_in[2].  Rows and ranges
  * outside the table, entries past num_blocks and blocks given up more often than owned are recorded as failed
  * index checks.  Other buffers that overlap are MXFA_ERR_INVALID_ARG. */
 mxfa_status mxfa_kv_free(const int32_t* block_table, int R, int max_blocks, const int32_t* rows, const int32_t* first,

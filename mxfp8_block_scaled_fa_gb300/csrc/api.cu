@@ -1175,18 +1175,30 @@ mxfa_status mxfa_kv_fork(int32_t* block_table, int R, int max_blocks, const int3
                          const int32_t* lens, int F, int32_t* refs, int64_t num_blocks, const int32_t* free_ring,
                          int64_t ring_size, const int64_t* ring_in, int64_t* ring_out, int page, int32_t* from_blocks,
                          int32_t* to_blocks, int32_t* lens_out, mxfa_stream_t stream) {
+  return mxfa_kv_fork_gap(block_table, R, max_blocks, src, dst, lens, nullptr, nullptr, F, refs, num_blocks, free_ring, ring_size, ring_in,
+                          ring_out, page, from_blocks, to_blocks, lens_out, stream);
+}
+
+mxfa_status mxfa_kv_fork_gap(int32_t* block_table, int R, int max_blocks, const int32_t* src, const int32_t* dst,
+                             const int32_t* lens, const int32_t* gap_first, const int32_t* gap_end, int F, int32_t* refs,
+                             int64_t num_blocks, const int32_t* free_ring, int64_t ring_size, const int64_t* ring_in,
+                             int64_t* ring_out, int page, int32_t* from_blocks, int32_t* to_blocks, int32_t* lens_out,
+                             mxfa_stream_t stream) {
   mxfa_status s = check_pages(block_table, R, max_blocks, F, refs, num_blocks, free_ring, ring_size, ring_in, ring_out);
   if (s) return s;
+  if ((gap_first == nullptr) != (gap_end == nullptr)) return MXFA_ERR_INVALID_ARG;
   if (F > 0 && (!src || !dst || !lens || !from_blocks || !to_blocks || !lens_out)) return MXFA_ERR_INVALID_ARG;
   if (page != 16 && page != 32 && page != 64 && page != 128) return MXFA_ERR_UNSUPPORTED;
   if (int64_t(max_blocks) * page > (int64_t(1) << 30)) return MXFA_ERR_UNSUPPORTED;
   for (const void* p : {static_cast<const void*>(src), static_cast<const void*>(dst), static_cast<const void*>(lens),
+                        static_cast<const void*>(gap_first), static_cast<const void*>(gap_end),
                         static_cast<const void*>(from_blocks), static_cast<const void*>(to_blocks), static_cast<const void*>(lens_out)})
     if (!aligned4(p)) return MXFA_ERR_MISALIGNED;
   const size_t list = size_t(F) * 4;
   const Range written[] = {{block_table, size_t(R) * size_t(max_blocks) * 4}, {refs, size_t(num_blocks) * 4}, {from_blocks, list},
                            {to_blocks, list}, {lens_out, list}, {ring_out, 24}};
-  const Range read[] = {{src, list}, {dst, list}, {lens, list}, {free_ring, size_t(ring_size) * 4}, {ring_in, 24}};
+  const size_t gaps = gap_first ? list : 0;
+  const Range read[] = {{src, list}, {dst, list}, {lens, list}, {gap_first, gaps}, {gap_end, gaps}, {free_ring, size_t(ring_size) * 4}, {ring_in, 24}};
   if (clash(written, read, ring_in == ring_out ? &written[5] : nullptr)) return MXFA_ERR_INVALID_ARG;
   KvForkArgs a;
   memset(&a, 0, sizeof(a));
@@ -1196,6 +1208,8 @@ mxfa_status mxfa_kv_fork(int32_t* block_table, int R, int max_blocks, const int3
   a.src = src;
   a.dst = dst;
   a.lens = lens;
+  a.gap_first = gap_first;
+  a.gap_end = gap_end;
   a.F = F;
   a.refs = refs;
   a.blocks = num_blocks;

@@ -4,7 +4,8 @@
 // refs[b] counts the owners of block b beside the first: kv_plan's blocks have 0.
 //   fork   request d gets the first c tokens of request s: each whole page has one owner more; a last page
 //          that is not full is written again by both, so d gets a new block for it (the k-th such fork the
-//          k-th free block) and the pair (old, new) is a block to copy, layer by layer
+//          k-th free block) and the pair (old, new) is a block to copy, layer by layer.  Entries that s has given up
+//          are not shared
 //   free   each page given up has one owner fewer; blocks without an owner go to the ring, in ascending order
 // Counts change by whole-number atomics, so no result depends on timing: which of a block's owners comes last
 // is not seen, as blocks are collected by looking at the counts afterwards.
@@ -31,6 +32,7 @@ constexpr int64_t kInside = 4096;
 
 struct Fork {
   int src, dst, whole;
+  int gap, gap_end;  // entries gap .. gap_end - 1 were given up
   bool part;    // a last page that is not full
   int32_t old;  // its block, -1: none, or no block of the cache
   __device__ __forceinline__ bool takes() const { return part && old >= 0; }  // a place of the ring
@@ -41,7 +43,10 @@ __device__ __forceinline__ bool fork_of(const KvForkArgs& a, int f, Fork& x) {
   x.whole = 0;
   x.part = false;
   x.old = -1;
+  x.gap = a.gap_first ? __ldg(a.gap_first + f) : 0;
+  x.gap_end = a.gap_first ? __ldg(a.gap_end + f) : 0;
   if (x.src < 0 || x.src >= a.R || x.dst < 0 || x.dst >= a.R || x.src == x.dst || len < 0 || len > int64_t(a.width) << a.page_shift) return false;
+  if (x.gap < 0 || x.gap_end < x.gap || x.gap_end > len >> a.page_shift) return false;
   x.whole = len >> a.page_shift;
   x.part = (len & ((1 << a.page_shift) - 1)) != 0;
   if (x.part) {
@@ -74,7 +79,7 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvForkArgs a) {
   __shared__ int s_sum[kThreads / 32];
   const int f = blockIdx.x, j0 = blockIdx.y * kSegment;
   Fork x;
-  x.src = x.dst = x.whole = 0;
+  x.src = x.dst = x.whole = x.gap = x.gap_end = 0;
   x.part = false;
   x.old = -1;
   const bool good = f < a.F && fork_of(a, f, x);
@@ -83,6 +88,10 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvForkArgs a) {
     int32_t* to = a.table + int64_t(x.dst) * a.width;
     const int end = min(x.whole, j0 + kSegment);
     for (int j = j0 + threadIdx.x; j < end; j += kThreads) {
+      if (j >= x.gap && j < x.gap_end) {  // may be the ring's or another request's by now
+        to[j] = -1;
+        continue;
+      }
       int32_t b = from[j];
       if (b < 0 || b >= a.blocks) {
         atomicOr(&g_status_kv_pages, DEV_BAD_INDEX);

@@ -369,18 +369,26 @@ bool pages_args(PyObject* const* a, Pages& x) {
          current(x.index);
 }
 
-// fork(block_table, src, dst, lens, refs, free_ring, ring_state, page) -> (from, to, lens, ring_state), or a status
+// fork(block_table, src, dst, lens, refs, free_ring, ring_state, page, gap_first or None, gap_end or None) ->
+// (from, to, lens, ring_state), or a status
 PyObject* fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     Pages x;
     int64_t page;
-    if (n != 8 || !pages_args(a, x) || !number(a[7], page) || page < 0 || page > 128) Py_RETURN_NONE;
+    if (n != 10 || !pages_args(a, x) || !number(a[7], page) || page < 0 || page > 128) Py_RETURN_NONE;
+    const int32_t* gap[2] = {nullptr, nullptr};
+    for (int i = 0; i < 2; i++) {
+      if (a[8 + i] == Py_None) continue;
+      const at::Tensor* t = tensor(a[8 + i]);
+      if (!flat(t, at::kInt, x.index) || t->numel() != x.F) Py_RETURN_NONE;
+      gap[i] = i32(t);
+    }
     at::Tensor from = empty({x.F}, at::kInt, x.index), to = empty({x.F}, at::kInt, x.index), lens = empty({x.F}, at::kInt, x.index),
                out = empty({3}, at::kLong, x.index);
-    const mxfa_status s = mxfa_kv_fork(static_cast<int32_t*>(x.table->data_ptr()), int(x.table->size(0)), int(x.table->size(1)), i32(x.l[0]),
-                                       i32(x.l[1]), i32(x.l[2]), int(x.F), static_cast<int32_t*>(x.refs->data_ptr()), x.refs->numel(), i32(x.ring),
-                                       x.ring->numel(), i64(x.state), static_cast<int64_t*>(out.data_ptr()), int(page), i32(from), i32(to),
-                                       i32(lens), stream(x.index));
+    const mxfa_status s = mxfa_kv_fork_gap(static_cast<int32_t*>(x.table->data_ptr()), int(x.table->size(0)), int(x.table->size(1)),
+                                           i32(x.l[0]), i32(x.l[1]), i32(x.l[2]), gap[0], gap[1], int(x.F),
+                                           static_cast<int32_t*>(x.refs->data_ptr()), x.refs->numel(), i32(x.ring), x.ring->numel(), i64(x.state),
+                                           static_cast<int64_t*>(out.data_ptr()), int(page), i32(from), i32(to), i32(lens), stream(x.index));
     return s ? failed(s) : tuple_of({from, to, lens, out});
   });
 }

@@ -350,7 +350,8 @@ cudaError_t launch_kv_append_rope(const KvAppendRopeArgs& a, cudaStream_t s);
 struct KvForkArgs {
   int32_t* table;       // [R][width]
   int R, width;
-  const int32_t *src, *dst, *lens;  // [F]
+  const int32_t *src, *dst, *lens;     // [F]
+  const int32_t *gap_first, *gap_end;  // [F], or NULL: entries of src that were given up
   int F;
   int32_t* refs;        // [blocks] owners beside the first
   int64_t blocks;

@@ -40,6 +40,8 @@ last w keys and the first s.  Requests that continue others share their pages:
     o, lse = kv_attention_shared(q, cache, cu_q, kv_lens, block_table, group_starts, prefix_lens,
                                  max_q, max_group_q, scale)
     state = kv_free(block_table, rows, first, end, refs, free, f.ring_state)
+
+A request whose pages behind a window were given up is forked with gap=(first, end) of them.
 """
 from __future__ import annotations
 
@@ -152,6 +154,7 @@ def lib() -> ctypes.CDLL:
             "mxfa_rope": (I, [P, I64, P, I64, P, I64, I, I, P, I, P]),
             "mxfa_kv_append_rope": (I, [P, P, I64, I, P, I64, P, I64, I64, P, P, P, P, I64, P]),
             "mxfa_kv_fork": (I, [P, I, I, P, P, P, I, P, I64, P, I64, P, P, I, P, P, P, P]),
+            "mxfa_kv_fork_gap": (I, [P, I, I, P, P, P, P, P, I, P, I64, P, I64, P, P, I, P, P, P, P]),
             "mxfa_kv_free": (I, [P, I, I, P, P, P, I, P, I64, P, I64, P, P, P]),
             "mxfa_kv_copy_blocks": (I, [P, P, P, I, P]),
         }
@@ -731,6 +734,13 @@ def mxfa_kv_fork(block_table, R, max_blocks, src, dst, lens, F, refs, num_blocks
     _check(lib().mxfa_kv_fork(_p(block_table), R, max_blocks, _p(src), _p(dst), _p(lens), F, _p(refs), num_blocks,
                               _p(free_ring), ring_size, _p(ring_in), _p(ring_out), page, _p(from_blocks),
                               _p(to_blocks), _p(lens_out), _stream(stream)), "mxfa_kv_fork")
+
+
+def mxfa_kv_fork_gap(block_table, R, max_blocks, src, dst, lens, gap_first, gap_end, F, refs, num_blocks, free_ring,
+                     ring_size, ring_in, ring_out, page, from_blocks, to_blocks, lens_out, stream=None):
+    _check(lib().mxfa_kv_fork_gap(_p(block_table), R, max_blocks, _p(src), _p(dst), _p(lens), _p(gap_first), _p(gap_end), F,
+                                  _p(refs), num_blocks, _p(free_ring), ring_size, _p(ring_in), _p(ring_out), page,
+                                  _p(from_blocks), _p(to_blocks), _p(lens_out), _stream(stream)), "mxfa_kv_fork_gap")
 
 
 def mxfa_kv_free(block_table, R, max_blocks, rows, first, end, F, refs, num_blocks, free_ring, ring_size, ring_in,
@@ -1337,31 +1347,37 @@ def _pages(block_table, refs, free_ring, ring_state, lists):
 
 def kv_fork(block_table: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
             free_ring: torch.Tensor, ring_state: torch.Tensor, page: int, out: Optional[KvFork] = None,
-            stream=None) -> KvFork:
+            stream=None, gap=None) -> KvFork:
     """Rows dst (int32 [F]) of block_table get the first lens tokens of rows src: whole pages shared
     (refs counts their owners), a last page that is not full in a block of its own, to be copied by
-    kv_copy_blocks in each layer's cache.  `out` gives the result's buffers; its ring_state may be
-    ring_state."""
+    kv_copy_blocks in each layer's cache.  `gap` (two int32 [F], first and end): entries first .. end - 1 of rows
+    src were given up (kv_free of the pages behind a window) and are not shared; they are -1 in rows dst.
+    `out` gives the result's buffers; its ring_state may be ring_state."""
+    gap_first, gap_end = (None, None) if gap is None else gap
     if out is None and stream is None:
-        made = _fast().fork(block_table, src, dst, lens, refs, free_ring, ring_state, page)
+        made = _fast().fork(block_table, src, dst, lens, refs, free_ring, ring_state, page, gap_first, gap_end)
         if type(made) is tuple:
             return KvFork(*made)
         if made is not None:
-            _check(made, "mxfa_kv_fork")
-    index, F = _pages(block_table, refs, free_ring, ring_state, (("src", "dst", "lens"), (src, dst, lens)))
+            _check(made, "mxfa_kv_fork_gap")
+    lists = (("src", "dst", "lens"), (src, dst, lens))
+    if gap is not None:
+        lists = (lists[0] + ("gap[0]", "gap[1]"), lists[1] + (gap_first, gap_end))
+    index, F = _pages(block_table, refs, free_ring, ring_state, lists)
     if not _here(index, stream):
         with _place(index, stream):
-            return kv_fork(block_table, src, dst, lens, refs, free_ring, ring_state, page, out)
+            return kv_fork(block_table, src, dst, lens, refs, free_ring, ring_state, page, out, gap=gap)
     if out is None:
         i32 = dict(dtype=torch.int32, device=block_table.device)
         out = KvFork(torch.empty(F, **i32), torch.empty(F, **i32), torch.empty(F, **i32), torch.empty_like(ring_state))
     else:
         _pages(block_table, refs, free_ring, out.ring_state,
                (("out.from_blocks", "out.to_blocks", "out.lens", "src"), (out.from_blocks, out.to_blocks, out.lens, src)))
-    _check(lib().mxfa_kv_fork(block_table.data_ptr(), block_table.shape[0], block_table.shape[1], src.data_ptr(), dst.data_ptr(),
-                              lens.data_ptr(), F, refs.data_ptr(), refs.numel(), free_ring.data_ptr(), free_ring.numel(),
-                              ring_state.data_ptr(), out.ring_state.data_ptr(), page, out.from_blocks.data_ptr(),
-                              out.to_blocks.data_ptr(), out.lens.data_ptr(), _raw_stream(index)), "mxfa_kv_fork")
+    _check(lib().mxfa_kv_fork_gap(block_table.data_ptr(), block_table.shape[0], block_table.shape[1], src.data_ptr(), dst.data_ptr(),
+                                  lens.data_ptr(), _p(gap_first), _p(gap_end), F, refs.data_ptr(), refs.numel(), free_ring.data_ptr(),
+                                  free_ring.numel(), ring_state.data_ptr(), out.ring_state.data_ptr(), page,
+                                  out.from_blocks.data_ptr(), out.to_blocks.data_ptr(), out.lens.data_ptr(),
+                                  _raw_stream(index)), "mxfa_kv_fork_gap")
     return out
 
 

@@ -1,9 +1,10 @@
-"""Pages of the 4-bit cache at their edges: entries that are no blocks, as many forks as a call takes."""
+"""Pages of the 4-bit cache at their edges: entries that are no blocks, pages given up behind a window, as many forks as a call
+takes."""
 import numpy as np
 import pytest
 
 from tests.helpers import host
-from tests.test_gpu_more_kv import dev, mx  # noqa: F401
+from tests.test_gpu_more_kv import Server, dev, mx  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +64,124 @@ def test_fork_many(mx):
         x = table[src[whole > w], w]
         np.add.at(shared, x[x >= 0], 1)
     assert host(refs).tolist() == shared.tolist()
+
+
+def fork_with_gaps(table, src, dst, lens, gaps, refs, ring, head, tail, page):
+    """Fork by fork; table and refs are updated -> (from, to, lens, state)."""
+    a, b, kept, want = [], [], [], 0
+    for s, d, n, (g0, g1) in zip(src, dst, lens, gaps):
+        whole, pair = n // page, (-1, -1)
+        for j in range(whole):
+            gone = g0 <= j < g1
+            table[d][j] = -1 if gone else table[s][j]
+            if not gone:
+                refs[table[s][j]] += 1
+        if n % page:
+            if want < tail - head:
+                pair = (table[s][whole], ring[(head + want) % len(ring)])
+            else:
+                n = whole * page
+            want += 1
+            table[d][whole] = pair[1]
+        a.append(pair[0])
+        b.append(pair[1])
+        kept.append(n)
+    took = min(want, tail - head)
+    return a, b, kept, [head + took, tail, want - took]
+
+
+@pytest.mark.parametrize("given_stream", [False, True])
+@pytest.mark.parametrize("R,F,page,width,spare", [(2, 1, 16, 3, 1), (9, 7, 32, 7, 3), (30, 25, 16, 3000, 40), (500, 400, 64, 5, 500)])
+def test_fork_with_gaps(mx, R, F, page, width, spare, given_stream):
+    """Entries in the gap are not looked at, whatever they hold; without a gap the call is the one without it."""
+    import torch
+    rng = np.random.default_rng(R)
+    lens = rng.integers(0, width * page + 1, F)
+    src, whole = rng.integers(0, R, F), lens // page
+    g0 = rng.integers(0, whole + 1)
+    g1 = rng.integers(g0, whole + 1)
+    g0[0], g1[0] = 0, whole[0]
+    blocks = R * width + spare
+    table = np.concatenate([rng.permutation(R * width).reshape(R, width), np.full((F, width), -5)])
+    ring = np.concatenate([R * width + rng.permutation(spare), np.full(blocks - spare, -9)])
+    wt, wr = table.tolist(), [0] * blocks
+    want = fork_with_gaps(wt, src.tolist(), list(range(R, R + F)), lens.tolist(), list(zip(g0, g1)), wr, ring.tolist(), 0, spare, page)
+    t, refs, st = dev(table), mx.kv_refs(blocks), torch.cuda.Stream() if given_stream else None
+    args = (dev(src), dev(R + np.arange(F)), dev(lens), refs, dev(ring), dev([0, spare, 0], np.int64), page)
+    gap = (dev(g0), dev(g1))
+    torch.cuda.synchronize()
+    got = mx.kv_fork(t, *args, gap=gap, stream=st)
+    torch.cuda.synchronize()
+    for g, w in zip((got.from_blocks, got.to_blocks, got.lens, got.ring_state), want):
+        assert host(g).tolist() == w
+    assert host(t).tolist() == wt and host(refs).tolist() == wr and mx.device_status() == 0
+    one, two = dev(table), dev(table)
+    none = torch.zeros_like(gap[0])
+    a, b = mx.kv_fork(one, *args, gap=(none, none)), mx.kv_fork(two, *args)
+    assert torch.equal(one, two) and all(torch.equal(getattr(a, n), getattr(b, n)) for n in ("from_blocks", "to_blocks", "lens", "ring_state"))
+
+
+def test_gaps_outside_their_bounds(mx):
+    t, refs, ring = dev([[7, 8, 9], [-5] * 3, [-5] * 3, [-5] * 3, [-5] * 3, [-5] * 3]), mx.kv_refs(10), dev([0, 1, 2, 3, 4, 5, 6, 0, 0, 0])
+    gap = (dev([-1, 0, 2, 1, 3]), dev([1, 3, 1, 2, 3]))
+    f = mx.kv_fork(t, dev([0] * 5), dev([1, 2, 3, 4, 5]), dev([40, 40, 40, 40, 48]), refs, ring, dev([0, 7, 0], np.int64), 16, gap=gap)
+    assert mx.device_status() == 7                          # before the first page, behind the whole ones, end before first
+    assert host(f.lens).tolist() == [0, 0, 0, 40, 48] and host(f.to_blocks).tolist() == [-1, -1, -1, 0, -1]
+    assert host(t)[1:].tolist() == [[-5] * 3] * 3 + [[7, -1, 0], [7, 8, 9]] and host(f.ring_state).tolist() == [1, 7, 0]
+    assert host(refs).tolist() == [0] * 7 + [2, 1, 1]
+    t = dev([[7, 1 << 30, 9], [-5] * 3])                     # what was given up may be anything
+    f = mx.kv_fork(t, dev([0]), dev([1]), dev([33]), refs, ring, dev([0, 7, 0], np.int64), 16, gap=(dev([1]), dev([2])))
+    assert host(t)[1].tolist() == [7, -1, 0] and host(f.lens).tolist() == [33] and mx.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt,page,window,sinks", [(0, 16, 50, 4), (1, 32, 33, 0), (0, 16, 1, 17)])
+def test_window_run_that_gives_pages_up(mx, fmt, page, window, sinks):
+    """Pages behind a window go back as requests grow, others take their blocks, a request is forked with the gap and
+    both go on; at the end the ring holds every block once."""
+    rng = np.random.default_rng(page + window)
+    R, width, blocks = 5, 900 // page, 1100 // page
+    s = Server(mx, rng, fmt, page, 2, 4, R, width, blocks)
+    scale, kept = 128 ** -0.5, -(-sinks // page)             # pages that hold a sink stay
+    gone = [kept] * R                                        # entries kept .. gone - 1 of a row were given up
+
+    def give_up():
+        first = list(gone)
+        for r in range(R):
+            # the next query, at position ctx, sees the keys from ctx - window + 1 on
+            gone[r] = max(gone[r], (s.ctx[r] - window + 1) // page)
+        s.state = mx.kv_free(s.table, dev(range(R)), dev(first), dev(gone), s.refs, s.ring, s.state)
+
+    def step(new):
+        inside = lambda qr, p: mx.kv_attention(qr, s.c, p.cu_q, p.kv_lens, s.table, max(new), scale, window=window, sinks=sinks)
+        s.check(*s.step(new, inside), window, sinks)
+        give_up()
+
+    def ended(rows):
+        used = [-(-s.ctx[r] // page) for r in rows]
+        whole = [(r, 0, min(kept, u)) for r, u in zip(rows, used)] + [(r, gone[r], max(gone[r], u)) for r, u in zip(rows, used)]
+        s.state = mx.kv_free(s.table, *(dev([x[i] for x in whole]) for i in range(3)), s.refs, s.ring, s.state)
+        for r in rows:
+            s.ctx[r], s.slots[r], gone[r] = 0, [], kept
+    for new in ([300, 0, 0, 100, 5], [3, 0, 0, 200, 1], [70, 0, 0, 1, 150], [1, 0, 0, 2, 60]):
+        step(new)
+    ended([3])
+    step([20, 0, 0, 400, 1])
+    lens = [s.ctx[0], gone[0] * page + window - 1]           # the whole of it; and the fewest tokens whose window is still there
+    gaps = [gone[0]] * 2
+    f = mx.kv_fork(s.table, dev([0, 0]), dev([1, 2]), dev(lens), s.refs, s.ring, s.state, page, gap=(dev([kept] * 2), dev(gaps)))
+    mx.kv_copy_blocks(s.c, f.from_blocks, f.to_blocks)
+    s.state = f.ring_state
+    assert mx.device_status() == 0 and host(f.lens).tolist() == lens
+    for r, n, g in zip((1, 2), lens, gaps):
+        s.ctx[r], gone[r] = n, g
+        assert (host(s.table)[r, kept:g] == -1).all() and g > kept
+        s.slots[r] = list(s.slots[0][:n])
+        for p in range(n // page * page, n):
+            s.slots[r][p] = int(host(s.table)[r][p // page]) * page + p % page
+    assert lens[1] < lens[0]
+    for new in ([1, 1, 1, 0, 1], [4, 6, 2, 1, 1], [30, 1, 5, 200, 1], [1, 40, 1, 1, 90]):
+        step(new)
+    ended(range(R))
+    head, tail, lacked = host(s.state).tolist()
+    assert (tail - head, lacked) == (blocks, 0) and not s.refs.any() and mx.device_status() == 0
+    assert sorted(host(s.ring)[(head + np.arange(blocks)) % blocks].tolist()) == list(range(blocks))
