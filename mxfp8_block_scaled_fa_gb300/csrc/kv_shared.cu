@@ -54,7 +54,7 @@ __device__ __forceinline__ float tile_cost(float rows, int few_rows, int split_r
 
 // The first CTA goes through the groups: prefix of group g at gpre[g] (0: none, not as documented, or not shared), behind them
 // their number of items for kv_prefill.cu, and whether they are shared; the others take a request a thread: pre[r]
-// (-1: of a group not as documented; 0: of none) and the group's first request first[r].
+// (-1: of a group not as documented; 0: of none, or alone in its group) and the group's first request first[r].
 __global__ void __launch_bounds__(kPlan) kv_shared_plan_kernel(KvAttnArgs a, SharedArgs s) {
   __shared__ int64_t s_sum[kPlan / 32];
   __shared__ float s_gain[kPlan / 32];
@@ -69,7 +69,11 @@ __global__ void __launch_bounds__(kPlan) kv_shared_plan_kernel(KvAttnArgs a, Sha
     const int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + e);
     if (q0 < 0 || q1 < q0 || q1 > a.total_q || q1 - q0 > s.max_group_q) return -1;
     n = q1 - q0;
-    return e - b > 1 ? p : 0;  // a single request reads its own row
+    return p;
+  };
+  auto common = [&](int g) -> int {  // a single request reads its own row
+    const int p = checked(g);
+    return p > 0 && e - b < 2 ? 0 : p;
   };
   for (int64_t w = int64_t(blockIdx.x) * kPlan + tid; w < s.words; w += int64_t(gridDim.x) * kPlan) s.places[w] = make_uint4(0, 0, 0, 0);
   if (blockIdx.x > 0) {
@@ -81,7 +85,13 @@ __global__ void __launch_bounds__(kPlan) kv_shared_plan_kernel(KvAttnArgs a, Sha
         else hi = mid;
       }
       const bool in = __ldg(a.starts + lo) <= r && r < __ldg(a.starts + lo + 1);
-      const int p = in ? checked(lo) : 0;
+      int p = in ? checked(lo) : 0;
+      if (p > 0 && e - b == 1) {  // has no prefix for the kernels to come, but its queries behind one
+        const int own = __ldg(a.cu_q + r + 1) - __ldg(a.cu_q + r);
+        const bool short_of = own > 0 && int64_t(__ldg(a.kv_lens + r)) - own < p;
+        if (short_of) atomicOr(&g_status_kv_shared, DEV_BAD_INDEX);
+        p = short_of ? -1 : 0;
+      }
       s.pre[r] = p;
       s.first[r] = p > 0 ? b : r;
     }
@@ -90,7 +100,7 @@ __global__ void __launch_bounds__(kPlan) kv_shared_plan_kernel(KvAttnArgs a, Sha
   float gain = 0.0f;
   int first_p = 0, first_n = 0;  // of the first kPlan groups, most often all
   for (int g = tid; g < s.groups; g += kPlan) {
-    const int p = checked(g);
+    const int p = common(g);
     if (g == tid) first_p = p, first_n = n;
     if (p < 0) atomicOr(&g_status_kv_shared, DEV_BAD_INDEX);
     if (p <= 0 || n == 0) continue;
@@ -113,7 +123,7 @@ __global__ void __launch_bounds__(kPlan) kv_shared_plan_kernel(KvAttnArgs a, Sha
     const int g = g0 + tid;
     int64_t u = 0;
     if (g < s.groups) {
-      const int p = !share ? 0 : g0 == 0 ? first_p : checked(g);
+      const int p = !share ? 0 : g0 == 0 ? first_p : common(g);
       if (g0 == 0) n = first_n;
       s.gpre[g] = max(p, 0);
       if (p > 0) {

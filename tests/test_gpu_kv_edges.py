@@ -1,10 +1,11 @@
-"""Pages of the 4-bit cache at their edges: entries that are no blocks, pages given up behind a window, as many forks as a call
-takes."""
+"""Pages and shared prefixes of the 4-bit cache at their edges: entries that are no blocks, pages given up behind a window, as
+many forks as a call takes, groups of one request.  Bounds as in test_gpu_more_kv.py."""
 import numpy as np
 import pytest
 
+from tests import more_ref
 from tests.helpers import host
-from tests.test_gpu_more_kv import Server, dev, mx  # noqa: F401
+from tests.test_gpu_more_kv import Server, build, compare, dev, mx, results  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -185,3 +186,20 @@ def test_window_run_that_gives_pages_up(mx, fmt, page, window, sinks):
     head, tail, lacked = host(s.state).tolist()
     assert (tail - head, lacked) == (blocks, 0) and not s.refs.any() and mx.device_status() == 0
     assert sorted(host(s.ring)[(head + np.arange(blocks)) % blocks].tolist()) == list(range(blocks))
+
+
+@pytest.mark.parametrize("share", [True, False, None])
+def test_group_of_one_request_short_of_its_prefix(mx, share):
+    """A request whose queries do not lie behind its group's prefix is left out and recorded, alone in its group too."""
+    import torch
+    rng = np.random.default_rng(4)
+    for rows, kv_lens, lost in (([1, 1, 1], [70, 64, 90], {1}), ([1, 2, 1], [70, 65, 90], {1}), ([1, 0, 1], [70, 3, 90], set()),
+                                ([1, 60, 40], [70, 120, 90], {1}), ([1, 1, 1], [70, 65, 90], set())):
+        c, q, cu, kv, table, slots = build(mx, rng, 0, 16, 2, 4, rows, kv_lens)
+        o, lse = results(q)
+        mx.kv_attention_shared(q, c, cu, kv, table, dev([1, 2, 3]), dev([64, 20]), max(rows), max(rows), 0.1, out=(o, lse), share=share)
+        torch.cuda.synchronize()
+        assert mx.device_status() == (7 if lost else 0), (rows, kv_lens)
+        compare(c, q, cu, slots, o, lse, lambda r, n, k: more_ref.window_mask(n, k, 1 << 30, 0), rows={0, 1, 2} - lost, scale=0.1)
+        if lost:
+            assert (o[rows[0]: rows[0] + rows[1]].float() == 77.0).all()
