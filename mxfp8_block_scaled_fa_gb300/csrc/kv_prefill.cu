@@ -385,8 +385,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       int sn = 0, qn = 0;     // S products and items of this tile so far
       bool ok = true;
       // The loops over items have trip counts of the call's arguments (a.item_loops^3 is no fewer than
-      // a run can have) and skip their turns once the run is over: a loop that ended on a loaded item
-      // would not be warp-uniform to the compiler, and the issue code in it took 130
+      // a run can have, by the tokens of the call) and skip their turns once the run is over: a loop that ended on
+      // a loaded item would not be warp-uniform to the compiler, and the issue code in it took 130
       // cycles a product instead of 64.  A skipped turn takes 60 ns: four loops of 64, whatever the
       // call, cost it 16 us.
       bool over = false;
@@ -486,6 +486,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
         return true;
       };
       bool ok = true;
+      // items that the issuers' loops have turns for beside the record that ends them; offsets that are none can make
+      // requests that hold more rows together than the call has tokens
+      const int64_t most = int64_t(a.item_loops) * a.item_loops * a.item_loops - 1;
       while (ok && pos < end && r < a.R) {
         const int64_t lr = __ldcg(line + r), next_r = __ldcg(line + r + 1);
         if (pos >= next_r) {
@@ -514,7 +517,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
           const int u0 = int(pos - at), u1 = int(min(int64_t(units), u0 + (end - pos)));
           const int t0 = max(0, u0 - kItemTiles), t1 = max(0, u1 - kItemTiles);
           pos += u1 - u0;
-          if (t1 > t0) {
+          if (t1 > t0 && i >= most) {
+            atomicOr(status, DEV_BAD_INDEX);
+            pos = end;
+          } else if (t1 > t0) {
             Item it;
             it.r = r, it.h = h, it.row0 = row0;
             it.rows = min(ROWS, x.n * a.G - row0);
@@ -1040,8 +1046,14 @@ cudaError_t launch_kv_prefill_line(int kind, const KvAttnArgs& a, uint8_t* ws, b
 
 cudaError_t launch_kv_prefill(int kind, const KvAttnArgs& args, uint8_t* ws, cudaStream_t st) {
   KvAttnArgs a = args;
-  // every request's blocks for every head in one run, and the record that ends it
-  const int64_t items = int64_t(a.R) * a.c.H * ((int64_t(a.max_q) * a.G + kvp::ROWS - 1) / kvp::ROWS) + 1;
+  // Every block for every head in one run, and the record that ends it.  Blocks: those of the requests that can have more
+  // than split_rows rows, by the most tokens of one and by the tokens of all, a part of a block more for each.  The second
+  // counts where max_q is a capacity: 63 requests of one token beside one of 60 take 47 us with max_q = 60 as with 2^30 (282
+  // by the first alone).
+  const int64_t rows = a.total_q * a.G, most_q = a.max_q < a.total_q ? a.max_q : a.total_q;
+  const int64_t above = rows / (int64_t(a.split_rows) + 1), requests = a.R < above ? a.R : above;
+  const int64_t by_one = requests * ((most_q * a.G + kvp::ROWS - 1) / kvp::ROWS), by_all = rows / kvp::ROWS + requests;
+  const int64_t items = (by_one < by_all ? by_one : by_all) * a.c.H + 1;
   a.item_loops = int(ceil(cbrt(double(items)))) + 1;
   switch (kind) {
     case kAll: return launch_kind<kAll>(a, ws, st);

@@ -1,5 +1,5 @@
 """Pages and shared prefixes of the 4-bit cache at their edges: entries that are no blocks, pages given up behind a window, as
-many forks as a call takes, groups of one request.  Bounds as in test_gpu_more_kv.py."""
+many forks as a call takes, groups of one request, a max_q far above the tokens there are.  Bounds as in test_gpu_more_kv.py."""
 import numpy as np
 import pytest
 
@@ -203,3 +203,37 @@ def test_group_of_one_request_short_of_its_prefix(mx, share):
         compare(c, q, cu, slots, o, lse, lambda r, n, k: more_ref.window_mask(n, k, 1 << 30, 0), rows={0, 1, 2} - lost, scale=0.1)
         if lost:
             assert (o[rows[0]: rows[0] + rows[1]].float() == 77.0).all()
+
+
+def test_capacity_costs_no_time(mx):
+    """max_q is a bound that a captured step sets to what it may ever hold: the time goes by the tokens there are."""
+    import torch
+    rng = np.random.default_rng(5)
+    R, H, G = 64, 8, 4
+    q_lens = [60] + [1] * (R - 1)
+    c, q, cu, kv, table, slots = build(mx, rng, 0, 64, H, G, q_lens, [300] * R)
+    out = results(q)
+    ws = torch.empty(mx.mxfa_kv_attn_workspace_size(R, 60, table.shape[1] * 64, H * G, H), dtype=torch.uint8, device="cuda")
+
+    def time(max_q):
+        call = lambda: mx.kv_attention(q, c, cu, kv, table, max_q, 0.1, out=out, ws=ws)
+        g = torch.cuda.CUDAGraph()
+        call()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            for _ in range(20):
+                call()
+        best = 1e9
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            g.replay()
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b) * 1000 / 20)
+        return best
+    exact, most = time(60), time(1 << 30)
+    # 60 ns for each turn of a loop of 2^30 tokens' blocks would be 370 us
+    assert most <= 2 * exact + 60, (exact, most)
+    compare(c, q, cu, slots, *out, lambda r, n, k: more_ref.window_mask(n, k, 1 << 30, 0), scale=0.1)
+    assert mx.device_status() == 0
