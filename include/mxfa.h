@@ -574,13 +574,17 @@ mxfa_status mxfa_kv_attn_window(const mxfa_kv_cache* cache, const void* q, int64
  *               for itself otherwise; _ALWAYS, _NEVER: one or the other
  * Each request with queries has at least the prefix before them (kv - n >= prefix).  One that has not,
  * and the requests of a group whose starts, queries or prefix are outside their bounds, are left out
- * and recorded as failed index checks.  The workspace is of mxfa_kv_attn_shared_workspace_size() bytes,
- * max_k = max_blocks * page; everything else as mxfa_kv_attn.  groups may be 0. */
+ * and recorded as failed index checks.  The workspace is of mxfa_kv_attn_shared_workspace_size_mode() bytes for
+ * the same share, max_k = max_blocks * page: 1056 bytes a token and query head (results of prefixes and of what is
+ * behind them, in fp32), or 8 with _NEVER, beside what mxfa_kv_attn needs, twice or once;
+ * mxfa_kv_attn_shared_workspace_size() bytes suffice for any.  Everything else as mxfa_kv_attn.  groups may be 0. */
 #define MXFA_KV_SHARE_AUTO 0
 #define MXFA_KV_SHARE_ALWAYS 1
 #define MXFA_KV_SHARE_NEVER 2
 size_t mxfa_kv_attn_shared_workspace_size(int R, int groups, int64_t total_q, int max_q, int max_group_q, int64_t max_k,
                                           int Hq, int H);
+size_t mxfa_kv_attn_shared_workspace_size_mode(int R, int groups, int64_t total_q, int max_q, int max_group_q, int64_t max_k,
+                                               int Hq, int H, int share);
 mxfa_status mxfa_kv_attn_shared(const mxfa_kv_cache* cache, const void* q, int64_t q_stride, int64_t total_q,
                                 const int32_t* cu_q, const int32_t* kv_lens, int R, const int32_t* block_table,
                                 int max_blocks, int max_q, int Hq, float softmax_scale, const int32_t* group_starts,

@@ -1065,9 +1065,15 @@ mxfa_status mxfa_kv_attn_window(const mxfa_kv_cache* cache, const void* q, int64
 
 size_t mxfa_kv_attn_shared_workspace_size(int R, int groups, int64_t total_q, int max_q, int max_group_q, int64_t max_k,
                                           int Hq, int H) {
+  return mxfa_kv_attn_shared_workspace_size_mode(R, groups, total_q, max_q, max_group_q, max_k, Hq, H, MXFA_KV_SHARE_AUTO);
+}
+
+size_t mxfa_kv_attn_shared_workspace_size_mode(int R, int groups, int64_t total_q, int max_q, int max_group_q, int64_t max_k,
+                                               int Hq, int H, int share) {
+  if (share != MXFA_KV_SHARE_AUTO && share != MXFA_KV_SHARE_ALWAYS && share != MXFA_KV_SHARE_NEVER) return 0;
   if (R < 0 || groups < 0 || total_q < 0 || max_q < 0 || max_group_q < 0 || max_k < 0 || H <= 0 || Hq <= 0 || Hq % H) return 0;
   if (groups == 0) return kv_attn_workspace(R, max_q, max_k, Hq / H);
-  return kv_shared_workspace(R, groups, total_q, max_q, max_group_q, max_k, Hq, Hq / H);
+  return kv_shared_workspace(R, groups, total_q, max_q, max_group_q, max_k, Hq, Hq / H, share);
 }
 
 mxfa_status mxfa_kv_attn_shared(const mxfa_kv_cache* cache, const void* q, int64_t q_stride, int64_t total_q,
@@ -1086,7 +1092,7 @@ mxfa_status mxfa_kv_attn_shared(const mxfa_kv_cache* cache, const void* q, int64
   a.causal = 1;
   const int64_t max_k = int64_t(max_blocks) * a.c.page;
   if (!kv_attn_reaches(max_q, max_k, a.G) || (groups > 0 && !kv_attn_reaches(max_group_q, max_k, a.G))) return MXFA_ERR_UNSUPPORTED;
-  const size_t need = mxfa_kv_attn_shared_workspace_size(R, groups, total_q, max_q, max_group_q, max_k, Hq, a.c.H);
+  const size_t need = mxfa_kv_attn_shared_workspace_size_mode(R, groups, total_q, max_q, max_group_q, max_k, Hq, a.c.H, share);
   const mxfa_status t = check_attn_buffers(a, need, ws_bytes, group_starts, prefix_lens, groups);
   if (t) return t;
   if (groups == 0) return from_cuda(launch_kv_attn(kAll, a, reinterpret_cast<cudaStream_t>(stream)));

@@ -279,7 +279,8 @@ PyObject* shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!flat(starts, at::kInt, x.c->index) || !flat(prefix, at::kInt, x.c->index)) Py_RETURN_NONE;
     const int64_t groups = prefix->numel();
     if (groups == 0 || groups >= kMost || starts->numel() != groups + 1) Py_RETURN_NONE;
-    const size_t bytes = mxfa_kv_attn_shared_workspace_size(int(x.R), int(groups), x.T, int(x.max_q), int(most), x.most, int(x.Hq), x.c->c.H);
+    const size_t bytes = mxfa_kv_attn_shared_workspace_size_mode(int(x.R), int(groups), x.T, int(x.max_q), int(most), x.most, int(x.Hq),
+                                                                 x.c->c.H, int(share));
     void* const ws = attn_buffers(x, bytes);
     const mxfa_status s = mxfa_kv_attn_shared(&x.c->c, x.q->data_ptr(), x.qs, x.T, i32(x.cu), i32(x.kv), int(x.R), i32(x.table),
                                               int(x.table->size(1)), int(x.max_q), int(x.Hq), x.scale, i32(starts), i32(prefix), int(groups),

@@ -17,7 +17,8 @@
 // below.  In us, shared and not: 64 requests of 4 rows behind 8192 keys (8 key heads) 51 and 126; 6 x 5 requests of up to 15
 // rows behind up to 3000 28 and 31; 16 of 4 rows behind 1024 27 and 25; 4 x 8 of 8 rows behind up to 4096 38 and 37; 3 x 30 of
 // up to 25 rows behind up to 535 102 and 91; 3 x 8 of up to 636 rows behind up to 3454 157 and 132.  One that is not shared takes 5
-// to 8 us (prompts 20) more than mxfa_kv_attn: the plan, and a kernel without work.
+// to 11 us (prompts 20 to 38) more than mxfa_kv_attn: the plan, a kernel without work, the second pass's masks.  With
+// MXFA_KV_SHARE_NEVER, which has no such kernel, 3 to 10 (prompts 35).
 #include "kv_fp4.cuh"
 #include "mx_ptx.cuh"
 #include "mxfa_internal.h"
@@ -264,12 +265,15 @@ __global__ void __launch_bounds__(256) kv_shared_join_kernel(KvAttnArgs a, Pass 
   if (lane == 0) a.lse[(r - token * a.Hq) * a.total_q + token] = L == 0.0f ? -INFINITY : (M - kOffset + log2f(L)) * 0.6931471805599453f;
 }
 
-// Places in a call's workspace: for either pass its rows in one piece and its records, and what the plan writes.
+// Places in a call's workspace: for either pass its rows in one piece and its records, and what the plan writes.  Where
+// nothing is shared (MXFA_KV_SHARE_NEVER) there is no first pass, and rows in one piece are results: of a row only
+// the second pass's place is left, 8 bytes instead of 1056.
 struct Places {
   size_t o[2], ml[2], where, gpre, pre, first, share, pass[2], bytes;
 };
-Places places_of(int R, int groups, int64_t total_q, int max_q, int max_group_q, int64_t max_k, int Hq, int G) {
+Places places_of(int R, int groups, int64_t total_q, int max_q, int max_group_q, int64_t max_k, int Hq, int G, int mode) {
   size_t at = 0;
+  const bool never = mode == MXFA_KV_SHARE_NEVER;
   auto take = [&](size_t n) {
     const size_t x = at;
     at += (n + 255) & ~size_t(255);
@@ -278,15 +282,15 @@ Places places_of(int R, int groups, int64_t total_q, int max_q, int max_group_q,
   const size_t rows = size_t(total_q) * size_t(Hq);
   Places p;
   for (int i = 0; i < 2; i++) {
-    p.o[i] = take(rows * 512);
-    p.ml[i] = take(rows * 8);
+    p.o[i] = take(never ? 0 : rows * 512);
+    p.ml[i] = take(never ? 0 : rows * 8);
   }
-  p.where = take(rows * 16);
+  p.where = take(rows * (never ? 8 : 16));
   p.gpre = take(size_t(groups) * 4 + 4);
   p.pre = take(size_t(R) * 4);
   p.first = take(size_t(R) * 4);
   p.share = take(4);
-  p.pass[0] = take(kv_attn_workspace(groups, max_group_q, max_k, G));
+  p.pass[0] = take(never ? 0 : kv_attn_workspace(groups, max_group_q, max_k, G));
   p.pass[1] = take(kv_attn_workspace(R, max_q, max_k, G));
   p.bytes = at;
   return p;
@@ -294,15 +298,17 @@ Places places_of(int R, int groups, int64_t total_q, int max_q, int max_group_q,
 
 }  // namespace
 
-size_t kv_shared_workspace(int R, int groups, int64_t total_q, int max_q, int max_group_q, int64_t max_k, int Hq, int G) {
-  return places_of(R, groups, total_q, max_q, max_group_q, max_k, Hq, G).bytes;
+size_t kv_shared_workspace(int R, int groups, int64_t total_q, int max_q, int max_group_q, int64_t max_k, int Hq, int G,
+                           int mode) {
+  return places_of(R, groups, total_q, max_q, max_group_q, max_k, Hq, G, mode).bytes;
 }
 
 cudaError_t launch_kv_attn_shared(const KvAttnArgs& args, const int32_t* prefix_lens, int groups, int max_group_q, int mode, cudaStream_t st) {
   clear_stale_error();
   const int64_t max_k = int64_t(args.width) << args.c.page_shift, rows = args.total_q * args.Hq;
   uint8_t* const ws = args.ws;
-  const Places p = places_of(args.R, groups, args.total_q, args.max_q, max_group_q, max_k, args.Hq, args.G);
+  const bool never = mode == MXFA_KV_SHARE_NEVER;
+  const Places p = places_of(args.R, groups, args.total_q, args.max_q, max_group_q, max_k, args.Hq, args.G, mode);
   KvAttnArgs a[2] = {args, args};  // the groups as requests, whose keys are the prefixes; the requests behind them
   KvRecords rec[2];
   Pass pass[2];
@@ -310,7 +316,7 @@ cudaError_t launch_kv_attn_shared(const KvAttnArgs& args, const int32_t* prefix_
     a[i].ws = ws + p.pass[i];
     a[i].rows_o = reinterpret_cast<float*>(ws + p.o[i]);
     a[i].rows_ml = reinterpret_cast<float2*>(ws + p.ml[i]);
-    a[i].places = reinterpret_cast<uint2*>(ws + p.where) + i * rows;
+    a[i].places = reinterpret_cast<uint2*>(ws + p.where) + (never ? 0 : i * rows);
     a[i].prefix = reinterpret_cast<const int32_t*>(ws + (i ? p.pre : p.gpre));
   }
   a[0].R = groups;
@@ -333,9 +339,9 @@ cudaError_t launch_kv_attn_shared(const KvAttnArgs& args, const int32_t* prefix_
   s.pre = reinterpret_cast<int32_t*>(ws + p.pre);
   s.first = reinterpret_cast<int32_t*>(ws + p.first);
   s.share = reinterpret_cast<int32_t*>(ws + p.share);
-  s.line = few[0] ? nullptr : reinterpret_cast<int64_t*>(rec[0].many_ws);
+  s.line = never || few[0] ? nullptr : reinterpret_cast<int64_t*>(rec[0].many_ws);
   s.places = reinterpret_cast<uint4*>(ws + p.where);
-  s.words = rows;
+  s.words = never ? (rows + 1) / 2 : rows;
   for (int i = 0; i < 2; i++) {
     s.few_rows[i] = rec[i].few_rows;
     s.split_rows[i] = i == 0 && !few[0] ? 0 : rec[i].split_rows;  // the prompts' kernel takes all groups or none
@@ -347,8 +353,8 @@ cudaError_t launch_kv_attn_shared(const KvAttnArgs& args, const int32_t* prefix_
   kv_shared_plan_kernel<<<unsigned(grid), kPlan, 0, st>>>(args, s);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if ((e = launch_kv_attn(kPrefix, a[0], st)) != cudaSuccess) return e;
-  a[1].late = few[1];  // one kernel, which needs nothing of the pass before
+  if (!never && (e = launch_kv_attn(kPrefix, a[0], st)) != cudaSuccess) return e;
+  a[1].late = few[1] && !never;  // one kernel, which needs nothing of the pass before
   if ((e = launch_kv_attn(kTail, a[1], st)) != cudaSuccess) return e;
   return launch_early(kv_shared_join_kernel, dim3(unsigned((rows + 7) / 8)), 256, 0, st, args, pass[0], pass[1]);
 }

@@ -300,7 +300,7 @@ int64_t kv_window_reach(int max_q, int64_t max_k, int window, int sinks);
 bool kv_attn_few(int max_q, int64_t max_k, int G);  // whether kv_prefill.cu has no part in a call
 KvRecords kv_attn_records(uint8_t* ws, int R, int max_q, int64_t max_k, int G);
 uint8_t* kv_prefill_records(uint8_t* ws, int R);
-size_t kv_shared_workspace(int R, int groups, int64_t total_q, int max_q, int max_group_q, int64_t max_k, int Hq, int G);
+size_t kv_shared_workspace(int R, int groups, int64_t total_q, int max_q, int max_group_q, int64_t max_k, int Hq, int G, int mode);
 cudaError_t launch_kv_attn_shared(const KvAttnArgs& a, const int32_t* prefix_lens, int groups, int max_group_q, int mode, cudaStream_t s);
 size_t kv_prefill_workspace(int R);
 cudaError_t launch_kv_prefill_line(int kind, const KvAttnArgs& a, uint8_t* ws, bool after_attn, cudaStream_t st);

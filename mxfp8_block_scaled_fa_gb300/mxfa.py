@@ -150,6 +150,7 @@ def lib() -> ctypes.CDLL:
             "mxfa_kv_attn_window_workspace_size": (S, [I, I, I64, I, I, I, I]),
             "mxfa_kv_attn_window": (I, [P, P, I64, I64, P, P, I, P, I, I, I, F, I, I, P, P, P, S, P]),
             "mxfa_kv_attn_shared_workspace_size": (S, [I, I, I64, I, I, I64, I, I]),
+            "mxfa_kv_attn_shared_workspace_size_mode": (S, [I, I, I64, I, I, I64, I, I, I]),
             "mxfa_kv_attn_shared": (I, [P, P, I64, I64, P, P, I, P, I, I, I, F, P, P, I, I, I, P, P, P, S, P]),
             "mxfa_rope": (I, [P, I64, P, I64, P, I64, I, I, P, I, P]),
             "mxfa_kv_append_rope": (I, [P, P, I64, I, P, I64, P, I64, I64, P, P, P, P, I64, P]),
@@ -700,6 +701,10 @@ def mxfa_kv_attn_shared_workspace_size(R, groups, total_q, max_q, max_group_q, m
     return int(lib().mxfa_kv_attn_shared_workspace_size(R, groups, total_q, max_q, max_group_q, max_k, Hq, H))
 
 
+def mxfa_kv_attn_shared_workspace_size_mode(R, groups, total_q, max_q, max_group_q, max_k, Hq, H, share) -> int:
+    return int(lib().mxfa_kv_attn_shared_workspace_size_mode(R, groups, total_q, max_q, max_group_q, max_k, Hq, H, share))
+
+
 def mxfa_kv_attn_shared(pages: KvPages, q, q_stride, total_q, cu_q, kv_lens, R, block_table, max_blocks, max_q,
                         Hq, scale, group_starts, prefix_lens, groups, max_group_q, share, o, lse, ws, ws_bytes,
                         stream=None):
@@ -1074,7 +1079,7 @@ def kv_attention_shared(q: torch.Tensor, cache: KvCache, cu_q: torch.Tensor, kv_
     read from its first request's row of block_table, once for all of the group's queries, at most
     max_group_q of them.  Every request with queries has at least its group's prefix before them.
     Whether prefixes are in fact read once is decided on the GPU, by what is faster for the lengths,
-    unless `share` says so."""
+    unless `share` says so.  The workspace is 1056 bytes a token and query head, with share=False 8."""
     share = KV_SHARE_AUTO if share is None else KV_SHARE_ALWAYS if share else KV_SHARE_NEVER
     if out is None and ws is None and stream is None:
         made = _fast().shared(q, cache.raw, cu_q, kv_lens, block_table, max_q, scale, group_starts, prefix_lens, max_group_q, share)
@@ -1132,7 +1137,7 @@ def _attention(q, cache, cu_q, kv_lens, block_table, max_q, scale, out, ws, stre
         if form[0] == "window":
             ws_bytes = L.mxfa_kv_attn_window_workspace_size(R, max_q, most, Hq, H, form[1], form[2])
         elif form[0] == "shared":
-            ws_bytes = L.mxfa_kv_attn_shared_workspace_size(R, groups, T, max_q, max_group_q, most, Hq, H)
+            ws_bytes = L.mxfa_kv_attn_shared_workspace_size_mode(R, groups, T, max_q, max_group_q, most, Hq, H, share)
         else:
             ws_bytes = L.mxfa_kv_attn_workspace_size(R, max_q, most, Hq, H)
         if ws_bytes:

@@ -5,7 +5,7 @@ import pytest
 
 from tests import more_ref
 from tests.helpers import host
-from tests.test_gpu_more_kv import Server, build, compare, dev, mx, results  # noqa: F401
+from tests.test_gpu_more_kv import Server, build, compare, dev, mx, results, shared_case  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -237,3 +237,27 @@ def test_capacity_costs_no_time(mx):
     assert most <= 2 * exact + 60, (exact, most)
     compare(c, q, cu, slots, *out, lambda r, n, k: more_ref.window_mask(n, k, 1 << 30, 0), scale=0.1)
     assert mx.device_status() == 0
+
+
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("fmt,page,G,groups,behind", [
+    (0, 16, 4, [([1] * 9, 1024, [1, 5, 64, 65, 200, 900, 1, 2, 3]), ([1], 40, [5])], [(1, 70)]),
+    (1, 64, 8, [([4, 6, 1], 3000, [4, 100, 1]), ([2, 0, 5], 17, [9, 0, 129])], []),
+    (0, 32, 2, [([100, 20, 1], 700, [100, 150, 1])], [(1, 2000)]),
+    (0, 16, 40, [([2, 1], 700, [100, 150])], [(3, 90)])])
+def test_never_shared_in_its_own_workspace(mx, fmt, page, G, groups, behind, given):
+    """share=False in a workspace of that mode's bytes, from contents of any kind, and nothing behind it is written."""
+    import torch
+    rng = np.random.default_rng(G)
+    c, q, cu, kv, table, slots, starts, pre, max_q, most, _, _ = shared_case(mx, rng, fmt, page, 2, G, groups, [], behind)
+    need = mx.mxfa_kv_attn_shared_workspace_size_mode(kv.numel(), pre.numel(), q.shape[0], max_q, most, table.shape[1] * page, 2 * G, 2, mx.KV_SHARE_NEVER)
+    ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device="cuda") if given else None
+    o, lse = results(q)
+    mx.kv_attention_shared(q, c, cu, kv, table, starts, pre, max_q, most, 0.1, out=(o, lse), share=False, ws=None if ws is None else ws[:need])
+    torch.cuda.synchronize()
+    assert mx.device_status() == 0
+    compare(c, q, cu, slots, o, lse, lambda r, n, k: more_ref.window_mask(n, k, 1 << 30, 0), scale=0.1)
+    if given:
+        assert (ws[need:] == 0xFF).all()
+        with pytest.raises(mx.MxfaError):
+            mx.kv_attention_shared(q, c, cu, kv, table, starts, pre, max_q, most, 0.1, out=(o, lse), share=True, ws=ws[:need])

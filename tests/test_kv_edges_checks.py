@@ -1,8 +1,10 @@
 """Refusals of the 4-bit cache's calls for pages and shared prefixes, without a GPU (all before any launch)."""
+import ctypes
+
 import pytest
 import torch
 
-from tests.test_more_kv_checks import mx  # noqa: F401
+from tests.test_more_kv_checks import _cache, mx  # noqa: F401
 
 
 def test_fork_gap_checks(mx):
@@ -31,3 +33,25 @@ def test_fork_gap_refusals(mx):
         mx.kv_fork(*args, gap=(i32(2).long(), i32(2)))
     with pytest.raises(ValueError):
         mx.kv_fork(*args, gap=(i32(2), i32(2)))              # not on a GPU
+
+
+def test_shared_workspace_by_mode(mx):
+    """What is never shared needs no rows and no records of prefixes; the size without a mode suffices for every one."""
+    L = mx.lib()
+    size, any_mode = L.mxfa_kv_attn_shared_workspace_size_mode, L.mxfa_kv_attn_shared_workspace_size
+    for R, groups, T, mq, mg, k, Hq, H in ((64, 1, 64, 1, 64, 16384, 32, 8), (8, 2, 16384, 4096, 16384, 32768, 32, 8), (3, 1, 3, 1, 3, 64, 4, 2)):
+        auto, always, never = (size(R, groups, T, mq, mg, k, Hq, H, m) for m in (mx.KV_SHARE_AUTO, mx.KV_SHARE_ALWAYS, mx.KV_SHARE_NEVER))
+        alone = L.mxfa_kv_attn_workspace_size(R, mq, k, Hq, H)
+        assert auto == always == any_mode(R, groups, T, mq, mg, k, Hq, H) >= 1056 * T * Hq + alone
+        lists = 4 * (groups + 1) + 8 * R + 4
+        assert 8 * T * Hq + alone <= never <= 8 * T * Hq + alone + lists + 10 * 256
+    assert size(2, 0, 3, 3, 3, 1024, 4, 2, 2) == L.mxfa_kv_attn_workspace_size(2, 3, 1024, 4, 2)
+    assert size(2, 1, 3, 3, 3, 1024, 4, 2, 3) == 0 and size(2, 1, 3, 3, 3, 1024, 4, 2, -1) == 0 and size(2, 1, 3, 3, 3, 1024, 5, 2, 2) == 0
+    # a call is refused for fewer bytes than its own mode needs
+    c = _cache(mx)
+    base = dict(q=0x10000, qs=512, T=3, cu=0x20000, kv=0x30000, R=2, bt=0x40000, nb=64, mq=3, Hq=4, s=0.1, st=0x70000, pl=0x78000,
+                g=1, mg=3, sh=0, o=0x50000, lse=0x60000, ws=0x10000000, wb=0)
+    call = lambda **kw: L.mxfa_kv_attn_shared(ctypes.byref(c), *dict(base, **kw).values(), None)
+    for mode in (0, 1, 2):
+        assert call(sh=mode, wb=size(2, 1, 3, 3, 3, 1024, 4, 2, mode) - 1) == 4
+    assert call(sh=1, wb=size(2, 1, 3, 3, 3, 1024, 4, 2, 2)) == 4
