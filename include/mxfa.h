@@ -574,7 +574,10 @@ mxfa_status mxfa_kv_attn_window(const mxfa_kv_cache* cache, const void* q, int64
  *               for itself otherwise; _ALWAYS, _NEVER: one or the other
  * Each request with queries has at least the prefix before them (kv - n >= prefix).  One that has not,
  * and the requests of a group whose starts, queries or prefix are outside their bounds, are left out
- * and recorded as failed index checks.  The workspace is of mxfa_kv_attn_shared_workspace_size_mode() bytes for
+ * and recorded as failed index checks.  (After a step that lacked blocks, ring_out[2] > 0, mxfa_kv_plan leaves some
+ * kv_lens at the old contexts: those requests' rows mean nothing, and one that is no longer behind its prefix
+ * by its kv_lens is left out and recorded here, where mxfa_kv_attn computes it.)
+ * The workspace is of mxfa_kv_attn_shared_workspace_size_mode() bytes for
  * the same share, max_k = max_blocks * page: 1056 bytes a token and query head (results of prefixes and of what is
  * behind them, in fp32), or 8 with _NEVER, beside what mxfa_kv_attn needs, twice or once;
  * mxfa_kv_attn_shared_workspace_size() bytes suffice for any.  Everything else as mxfa_kv_attn.  groups may be 0. */

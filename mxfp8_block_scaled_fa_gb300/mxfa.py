@@ -1077,7 +1077,8 @@ def kv_attention_shared(q: torch.Tensor, cache: KvCache, cu_q: torch.Tensor, kv_
     """kv_attention (causal) of requests that share prefixes: group g is requests group_starts[g] ..
     group_starts[g + 1] - 1 (int32 [groups + 1]), whose first prefix_lens[g] (int32 [groups]) keys are
     read from its first request's row of block_table, once for all of the group's queries, at most
-    max_group_q of them.  Every request with queries has at least its group's prefix before them.
+    max_group_q of them.  Every request with queries has at least its group's prefix before them; one that has
+    not, as after a kv_plan whose ring lacked its block, is left out and recorded in device_status().
     Whether prefixes are in fact read once is decided on the GPU, by what is faster for the lengths,
     unless `share` says so.  The workspace is 1056 bytes a token and query head, with share=False 8."""
     share = KV_SHARE_AUTO if share is None else KV_SHARE_ALWAYS if share else KV_SHARE_NEVER

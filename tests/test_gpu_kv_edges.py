@@ -261,3 +261,24 @@ def test_never_shared_in_its_own_workspace(mx, fmt, page, G, groups, behind, giv
         assert (ws[need:] == 0xFF).all()
         with pytest.raises(mx.MxfaError):
             mx.kv_attention_shared(q, c, cu, kv, table, starts, pre, max_q, most, 0.1, out=(o, lse), share=True, ws=ws[:need])
+
+
+@pytest.mark.parametrize("share", [True, False, None])
+def test_shared_after_a_step_that_lacked_blocks(mx, share):
+    """The requests that got no block keep their old kv_lens: just behind the prefix they are left out and recorded, and
+    the others are as ever; kv_attention computes them all."""
+    import torch
+    rng = np.random.default_rng(12)
+    c, q, cu, kv, table, slots = build(mx, rng, 0, 16, 2, 4, [1, 1, 1, 1], [33, 32, 32, 70], groups=[([0, 1, 2], 32)], extra=3)
+    t = table.clone()
+    t[0, 2] = -1
+    plan = mx.kv_plan(dev([32, 32, 32, 69]), dev([1, 1, 1, 1]), t, table[0, 2:3].clone(), dev([0, 1, 0], np.int64), 16, 4)
+    assert host(plan.kv_lens).tolist() == [33, 32, 32, 70] and host(plan.ring_state).tolist() == [1, 1, 2] and torch.equal(t, table)
+    o, lse = results(q)
+    mx.kv_attention(q, c, plan.cu_q, plan.kv_lens, t, 1, 0.1, out=(o, lse))
+    assert mx.device_status() == 0
+    o, lse = results(q)
+    mx.kv_attention_shared(q, c, plan.cu_q, plan.kv_lens, t, dev([0, 3]), dev([32]), 1, 3, 0.1, out=(o, lse), share=share)
+    assert mx.device_status() == 7
+    compare(c, q, cu, slots, o, lse, lambda r, n, k: more_ref.window_mask(n, k, 1 << 30, 0), rows={0, 3}, scale=0.1)
+    assert (o[1:3].float() == 77.0).all() and (lse[:, 1:3] == 77.0).all()
