@@ -1002,9 +1002,11 @@ cudaError_t launch(const KvAttnArgs& a, uint8_t* ws, cudaStream_t st) {
   Partial* partials = reinterpret_cast<Partial*>(ws + line_bytes(a.R) + header_bytes(ctas));
   e = launch_early(kv_prefill_kernel<KIND, FMT>, dim3(unsigned(ctas)), NTHREADS, SMEM_BYTES, st, a, static_cast<const int64_t*>(line), headers,
                    partials);
-  if (e != cudaSuccess || kRecords<KIND>) return e;
-  return launch_early(kv_prefill_join_kernel<KIND, FMT>, dim3(unsigned(ctas), ROWS / 8), 256, 0, st, a, static_cast<const Header*>(headers),
-                      static_cast<const Partial*>(partials));
+  if constexpr (kRecords<KIND>) return e;  // joined by kv_shared_join_kernel
+  else
+    return e != cudaSuccess ? e
+                            : launch_early(kv_prefill_join_kernel<KIND, FMT>, dim3(unsigned(ctas), ROWS / 8), 256, 0, st, a,
+                                           static_cast<const Header*>(headers), static_cast<const Partial*>(partials));
 }
 
 }  // namespace kvp
@@ -1039,8 +1041,8 @@ cudaError_t launch_kv_prefill_line(int kind, const KvAttnArgs& a, uint8_t* ws, b
   switch (kind) {
     case kAll: return launch_line<kAll>(a, line, after_attn, st);
     case kWindow: return launch_line<kWindow>(a, line, after_attn, st);
-    case kPrefix: return launch_line<kPrefix>(a, line, after_attn, st);
-    default: return launch_line<kTail>(a, line, after_attn, st);
+    case kTail: return launch_line<kTail>(a, line, after_attn, st);
+    default: return cudaErrorInvalidValue;  // the groups' line is kv_shared_plan_kernel's
   }
 }
 
