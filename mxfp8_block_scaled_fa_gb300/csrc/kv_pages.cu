@@ -22,6 +22,7 @@ static __device__ unsigned g_status_kv_pages;
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kForkThreads = 512;
 constexpr int kCopyThreads = 512;
 constexpr int kSegment = 2048;  // table entries of a CTA
 constexpr int kScan = 1024;     // threads of a CTA that collects
@@ -31,127 +32,121 @@ constexpr int kCluster = 8;
 constexpr int64_t kInside = 4096;
 
 struct Fork {
-  int src, dst, whole;
-  int gap, gap_end;  // entries gap .. gap_end - 1 were given up
-  bool part;    // a last page that is not full
-  int32_t old;  // its block, -1: none, or no block of the cache
-  __device__ __forceinline__ bool takes() const { return part && old >= 0; }  // a place of the ring
+  int src, dst, len, whole;  // whole pages
+  int gap, gap_end;          // entries gap .. gap_end - 1 were given up
 };
 __device__ __forceinline__ bool fork_of(const KvForkArgs& a, int f, Fork& x) {
-  x.src = __ldg(a.src + f), x.dst = __ldg(a.dst + f);
-  const int len = __ldg(a.lens + f);
-  x.whole = 0;
-  x.part = false;
-  x.old = -1;
+  x.src = __ldg(a.src + f), x.dst = __ldg(a.dst + f), x.len = __ldg(a.lens + f);
   x.gap = a.gap_first ? __ldg(a.gap_first + f) : 0;
   x.gap_end = a.gap_first ? __ldg(a.gap_end + f) : 0;
-  if (x.src < 0 || x.src >= a.R || x.dst < 0 || x.dst >= a.R || x.src == x.dst || len < 0 || len > int64_t(a.width) << a.page_shift) return false;
-  if (x.gap < 0 || x.gap_end < x.gap || x.gap_end > len >> a.page_shift) return false;
-  x.whole = len >> a.page_shift;
-  x.part = (len & ((1 << a.page_shift) - 1)) != 0;
-  if (x.part) {
-    const int32_t b = a.table[int64_t(x.src) * a.width + x.whole];
-    if (b >= 0 && b < a.blocks) x.old = b;
-  }
-  return true;
-}
-
-// Forks before f that take a block; all threads of the CTA.
-__device__ __forceinline__ int parts_before(const KvForkArgs& a, int f, int* s_sum) {
-  int n = 0;
-  for (int i = threadIdx.x; i < f; i += kThreads) {
-    Fork x;
-    n += fork_of(a, i, x) && x.takes();
-  }
-  n = __reduce_add_sync(0xFFFFFFFFu, n);
-  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = n;
-  __syncthreads();
-  n = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; w++) n += s_sum[w];
-  return n;
+  if (x.src < 0 || x.src >= a.R || x.dst < 0 || x.dst >= a.R || x.src == x.dst) return false;
+  if (x.len < 0 || x.len > int64_t(a.width) << a.page_shift) return false;
+  x.whole = x.len >> a.page_shift;
+  return x.gap >= 0 && x.gap_end >= x.gap && x.gap_end <= x.whole;
 }
 
 __device__ __forceinline__ int64_t in_ring(int64_t i, int64_t size) { return (i % size + size) % size; }
 
-// One fork and kSegment entries of its row a CTA; the CTA with the last page looks for a block.
-__global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvForkArgs a) {
-  __shared__ int s_sum[kThreads / 32];
-  const int f = blockIdx.x, j0 = blockIdx.y * kSegment;
-  Fork x;
-  x.src = x.dst = x.whole = x.gap = x.gap_end = 0;
-  x.part = false;
-  x.old = -1;
-  const bool good = f < a.F && fork_of(a, f, x);
-  if (good) {
-    const int32_t* from = a.table + int64_t(x.src) * a.width;
-    int32_t* to = a.table + int64_t(x.dst) * a.width;
-    const int end = min(x.whole, j0 + kSegment);
-    for (int j = j0 + threadIdx.x; j < end; j += kThreads) {
-      if (j >= x.gap && j < x.gap_end) {  // may be the ring's or another request's by now
-        to[j] = -1;
-        continue;
-      }
-      int32_t b = from[j];
-      if (b < 0 || b >= a.blocks) {
-        atomicOr(&g_status_kv_pages, DEV_BAD_INDEX);
-        b = -1;
-      } else {
-        atomicAdd(a.refs + b, 1);
-      }
-      to[j] = b;
-    }
-  }
-  if (blockIdx.y != 0) return;
-  const bool last = f + 1 >= a.F;
-  if (f < a.F && !good && threadIdx.x == 0) atomicOr(&g_status_kv_pages, DEV_BAD_INDEX);
+// The last pages of all forks that are not full, and the ring: one CTA, so that a fork's place in the ring is a sum over
+// those before it, each looked at once, and the ring's counters may be written over.  N forks of a thread one behind another.
+template <int N>
+__device__ __forceinline__ void fork_parts(const KvForkArgs& a) {
+  __shared__ int s_sum[kForkThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t head = a.ring_in[0], tail = a.ring_in[1];
   const int64_t room = tail - head;
   const int64_t avail = room < 0 ? 0 : room < a.ring_size ? room : a.ring_size;
-  int rank = 0;
-  if (x.takes() || last) rank = parts_before(a, min(f, a.F), s_sum);
-  if (threadIdx.x != 0) return;
-  if (f < a.F) {
-    int32_t old = -1, fresh = -1;
-    int len = good ? __ldg(a.lens + f) : 0;
-    if (x.part) {
-      if (!x.takes()) {
-        atomicOr(&g_status_kv_pages, DEV_BAD_INDEX);
-      } else if (rank < avail) {
-        old = x.old;
-        fresh = a.ring[in_ring(head + rank, a.ring_size)];
-        if (fresh < 0 || fresh >= a.blocks) {
-          atomicOr(&g_status_kv_pages, DEV_BAD_INDEX);
-          old = fresh = -1;
-        }
-      }
-      if (fresh < 0) len = x.whole << a.page_shift;
-      a.table[int64_t(x.dst) * a.width + x.whole] = fresh;
+  const int64_t first = in_ring(head, a.ring_size);
+  int64_t want = 0;  // blocks of the forks so far
+  __syncthreads();   // every thread has the counters
+  for (int f0 = 0; f0 < a.F; f0 += kForkThreads * N) {
+    Fork x[N];
+    bool good[N], part[N];
+    int32_t old[N];  // the last page's block, -1: none, or no block of the cache
+    int own = 0;
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+      const int f = f0 + tid * N + j;
+      good[j] = f < a.F && fork_of(a, f, x[j]);
+      part[j] = good[j] && (x[j].len & ((1 << a.page_shift) - 1)) != 0;
+      old[j] = part[j] ? a.table[int64_t(x[j].src) * a.width + x[j].whole] : -1;
     }
-    a.from_blocks[f] = old;
-    a.to_blocks[f] = fresh;
-    a.lens_out[f] = len;
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+      if (old[j] < 0 || old[j] >= a.blocks) old[j] = -1;
+      own += old[j] >= 0;  // takes a block
+    }
+    int upto = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += t;
+    }
+    if (lane == 31) s_sum[warp] = upto;
+    __syncthreads();
+    int64_t rank = want + upto - own;
+#pragma unroll
+    for (int w = 0; w < kForkThreads / 32; w++) {
+      if (w < warp) rank += s_sum[w];
+      want += s_sum[w];
+    }
+    int32_t fresh[N];
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+      const int64_t at = first + rank;  // rank < avail <= ring_size
+      fresh[j] = old[j] >= 0 && rank < avail ? a.ring[at < a.ring_size ? at : at - a.ring_size] : -1;
+      if (old[j] >= 0 && rank >= avail) old[j] = -2;  // none left
+      rank += old[j] != -1;
+    }
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+      const int f = f0 + tid * N + j;
+      if (f >= a.F) continue;
+      const bool none = fresh[j] < 0 || fresh[j] >= a.blocks;
+      if (!good[j] || (part[j] && none && old[j] != -2)) atomicOr(&g_status_kv_pages, DEV_BAD_INDEX);
+      if (part[j]) a.table[int64_t(x[j].dst) * a.width + x[j].whole] = none ? -1 : fresh[j];
+      a.from_blocks[f] = none ? -1 : old[j];
+      a.to_blocks[f] = none ? -1 : fresh[j];
+      a.lens_out[f] = !good[j] ? 0 : part[j] && none ? x[j].whole << a.page_shift : x[j].len;
+    }
+    __syncthreads();  // s_sum has been read
   }
-  if (last && a.ring_out) {
-    const int64_t want = rank + (x.takes() ? 1 : 0), took = want < avail ? want : avail;
+  if (tid == 0) {
+    const int64_t took = want < avail ? want : avail;
     a.ring_out[0] = head + took;
     a.ring_out[1] = tail;
     a.ring_out[2] = want - took;
   }
 }
 
-// The ring's counters behind a fork that writes them in place.
-__global__ void __launch_bounds__(kThreads) kv_fork_ring_kernel(KvForkArgs a, int64_t* ring_out) {
-  __shared__ int s_sum[kThreads / 32];
-  const int64_t want = parts_before(a, a.F, s_sum);
-  if (threadIdx.x != 0) return;
-  const int64_t head = a.ring_in[0], tail = a.ring_in[1];
-  const int64_t room = tail - head;
-  const int64_t avail = room < 0 ? 0 : room < a.ring_size ? room : a.ring_size;
-  const int64_t took = want < avail ? want : avail;
-  ring_out[0] = head + took;
-  ring_out[1] = tail;
-  ring_out[2] = want - took;
+// The first CTA has the last pages; of the others each has one fork and kSegment entries of its row.  Forks of 62 whole pages
+// and a partial one take 2.9 us for 4 (three dependent reads: lengths, table, ring), 3.4 for 256, 12 for 4096 and 70 for
+// 16384 (a million counts of shared pages); each fork's CTA counting those before it 2.9, 3.4, 40 and 533.
+__global__ void __launch_bounds__(kForkThreads) kv_fork_kernel(KvForkArgs a) {
+  if (blockIdx.x == 0) {
+    if (blockIdx.y > 0) return;
+    if (a.F <= kForkThreads) fork_parts<1>(a);
+    else fork_parts<4>(a);
+    return;
+  }
+  Fork x;
+  if (!fork_of(a, int(blockIdx.x) - 1, x)) return;
+  const int32_t* from = a.table + int64_t(x.src) * a.width;
+  int32_t* to = a.table + int64_t(x.dst) * a.width;
+  const int j0 = blockIdx.y * kSegment, end = min(x.whole, j0 + kSegment);
+  for (int j = j0 + threadIdx.x; j < end; j += kForkThreads) {
+    int32_t b = -1;
+    if (j < x.gap || j >= x.gap_end) {  // what was given up may be the ring's or another request's by now
+      b = from[j];
+      if (b < 0 || b >= a.blocks) {
+        atomicOr(&g_status_kv_pages, DEV_BAD_INDEX);
+        b = -1;
+      } else {
+        atomicAdd(a.refs + b, 1);
+      }
+    }
+    to[j] = b;
+  }
 }
 
 // One owner fewer for the blocks of entries j, j + step, .. of a range of pages.
@@ -327,16 +322,10 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(KvPages c, const 
 
 }  // namespace
 
-cudaError_t launch_kv_fork(const KvForkArgs& args, cudaStream_t st) {
+cudaError_t launch_kv_fork(const KvForkArgs& a, cudaStream_t st) {
   clear_stale_error();
-  KvForkArgs a = args;
-  const bool in_place = a.ring_out == a.ring_in;
-  if (in_place) a.ring_out = nullptr;
-  const dim3 grid(unsigned(a.F > 0 ? a.F : 1), unsigned((a.width + kSegment - 1) / kSegment));
-  kv_fork_kernel<<<grid, kThreads, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !in_place) return e;
-  kv_fork_ring_kernel<<<1, kThreads, 0, st>>>(a, args.ring_out);
+  const dim3 grid(unsigned(a.F + 1), unsigned((a.width + kSegment - 1) / kSegment));
+  kv_fork_kernel<<<grid, kForkThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -10,11 +10,12 @@ from tests.test_gpu_more_kv import Server, build, compare, dev, mx, results, sha
 pytestmark = pytest.mark.gpu
 
 
+@pytest.mark.parametrize("none", [-1, -2, -2 ** 31])
 @pytest.mark.parametrize("inplace", [False, True])
-def test_fork_of_a_partial_page_that_is_not_there(mx, inplace):
+def test_fork_of_a_partial_page_that_is_not_there(mx, inplace, none):
     """Such a fork takes no place of the ring: the next ones get the blocks, and none is lost."""
     import torch
-    table = [[1, -1, -1, -1], [2, 3, -1, -1], [4, 99, -1, -1]] + [[-9] * 4 for _ in range(5)]
+    table = [[1, none, -1, -1], [2, 3, -1, -1], [4, 99, -1, -1]] + [[-9] * 4 for _ in range(5)]
     t, refs, ring, state = dev(table), mx.kv_refs(8), dev([0, 5, 6, 7, -1, -1, -1, -1]), dev([0, 4, 0], np.int64)
     out = mx.KvFork(*(torch.full((5,), -7, dtype=torch.int32, device="cuda") for _ in range(3)), state) if inplace else None
     # rows 0 and 2 hold one good page each: their second one is not there, or past the cache
@@ -282,3 +283,32 @@ def test_shared_after_a_step_that_lacked_blocks(mx, share):
     assert mx.device_status() == 7
     compare(c, q, cu, slots, o, lse, lambda r, n, k: more_ref.window_mask(n, k, 1 << 30, 0), rows={0, 3}, scale=0.1)
     assert (o[1:3].float() == 77.0).all() and (lse[:, 1:3] == 77.0).all()
+
+
+def test_fork_time_grows_with_the_forks(mx):
+    """Eight times the forks take no more than sixteen times as long: no fork looks at all those before it."""
+    import torch
+
+    def time(F, R=40, width=64, page=16):
+        blocks = R * width + F
+        t = torch.cat([torch.arange(R * width, dtype=torch.int32).view(R, width), torch.full((F, width), -1, dtype=torch.int32)]).cuda()
+        ring = R * width + torch.arange(blocks, dtype=torch.int32, device="cuda") % F
+        args = (t, dev(np.arange(F) % R), dev(R + np.arange(F)), dev([1001] * F), mx.kv_refs(blocks), ring, dev([0, F, 0], np.int64), page)
+        mx.kv_fork(*args)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(10):
+                mx.kv_fork(*args)
+        best = 1e9
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            g.replay()
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b) * 100)
+        return best
+    few, many = time(2048), time(16384)
+    assert many <= 16 * few + 20, (few, many)                # all pairs of forks: 64 times
+    assert mx.device_status() == 0
