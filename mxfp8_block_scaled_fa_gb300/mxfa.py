@@ -1081,6 +1081,8 @@ def kv_attention_shared(q: torch.Tensor, cache: KvCache, cu_q: torch.Tensor, kv_
     not, as after a kv_plan whose ring lacked its block, is left out and recorded in device_status().
     Whether prefixes are in fact read once is decided on the GPU, by what is faster for the lengths,
     unless `share` says so.  The workspace is 1056 bytes a token and query head, with share=False 8."""
+    if share is not None and not isinstance(share, bool):
+        raise TypeError(f"share is {share!r}, expected True, False or None")
     share = KV_SHARE_AUTO if share is None else KV_SHARE_ALWAYS if share else KV_SHARE_NEVER
     if out is None and ws is None and stream is None:
         made = _fast().shared(q, cache.raw, cu_q, kv_lens, block_table, max_q, scale, group_starts, prefix_lens, max_group_q, share)

@@ -55,3 +55,17 @@ def test_shared_workspace_by_mode(mx):
     for mode in (0, 1, 2):
         assert call(sh=mode, wb=size(2, 1, 3, 3, 3, 1024, 4, 2, mode) - 1) == 4
     assert call(sh=1, wb=size(2, 1, 3, 3, 3, 1024, 4, 2, 2)) == 4
+
+
+def test_share_is_yes_no_or_none(mx):
+    """The C values are other numbers than Python's truth values: KV_SHARE_NEVER would read as yes, KV_SHARE_AUTO as no."""
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    rows = torch.zeros((5, 4, 128), dtype=torch.bfloat16)
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    c = mx.KvCache(u8(3, 2, 16, 64), u8(3, 2, 16, 64), u8(3, 2, 16, 4), u8(3, 2, 16, 4), 0)
+    for share in (mx.KV_SHARE_AUTO, mx.KV_SHARE_ALWAYS, mx.KV_SHARE_NEVER, "auto", 1.0):
+        with pytest.raises(TypeError):
+            mx.kv_attention_shared(rows, c, i32(2), i32(1), i32(1, 4), i32(2), i32(1), 5, 5, 0.1, share=share)
+    for share in (None, True, False):
+        with pytest.raises(ValueError):                      # not on a GPU
+            mx.kv_attention_shared(rows, c, i32(2), i32(1), i32(1, 4), i32(2), i32(1), 5, 5, 0.1, share=share)
