@@ -474,6 +474,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
       }
       int r = lo, i = 0;
       auto publish = [&](const Item& it) -> bool {
+        // beyond the issuers' turns: of offsets that are none, whose requests hold more rows than the call has tokens
+        if (i >= a.item_most && it.rows > 0) {
+          atomicOr(status, DEV_BAD_INDEX);
+          return false;
+        }
         if (i >= 2 && !mbar_wait(BAR(B_IEMPTY + (i & 1)), ((i >> 1) - 1) & 1, abort_flag, status)) return false;
         volatile Item* v = reinterpret_cast<volatile Item*>(smem + OFF_ITEM) + (i & 1);
         v->r = it.r, v->h = it.h, v->row0 = it.row0, v->rows = it.rows;
@@ -486,9 +491,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
         return true;
       };
       bool ok = true;
-      // items that the issuers' loops have turns for beside the record that ends them; offsets that are none can make
-      // requests that hold more rows together than the call has tokens
-      const int64_t most = int64_t(a.item_loops) * a.item_loops * a.item_loops - 1;
       while (ok && pos < end && r < a.R) {
         const int64_t lr = __ldcg(line + r), next_r = __ldcg(line + r + 1);
         if (pos >= next_r) {
@@ -517,10 +519,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
           const int u0 = int(pos - at), u1 = int(min(int64_t(units), u0 + (end - pos)));
           const int t0 = max(0, u0 - kItemTiles), t1 = max(0, u1 - kItemTiles);
           pos += u1 - u0;
-          if (t1 > t0 && i >= most) {
-            atomicOr(status, DEV_BAD_INDEX);
-            pos = end;
-          } else if (t1 > t0) {
+          if (t1 > t0) {
             Item it;
             it.r = r, it.h = h, it.row0 = row0;
             it.rows = min(ROWS, x.n * a.G - row0);
@@ -545,7 +544,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv_prefill_kernel(const __grid_co
         }
         r++;
       }
-      if (ok) {
+      {
         Item none;
         none.r = none.h = none.row0 = none.rows = none.q0 = none.n = none.kv = none.t0 = none.na = none.nb = none.slot = 0;
         none.lo = none.hi = none.at = none.jump = none.parts = 0;
@@ -1057,6 +1056,7 @@ cudaError_t launch_kv_prefill(int kind, const KvAttnArgs& args, uint8_t* ws, cud
   const int64_t by_one = requests * ((most_q * a.G + kvp::ROWS - 1) / kvp::ROWS), by_all = rows / kvp::ROWS + requests;
   const int64_t items = (by_one < by_all ? by_one : by_all) * a.c.H + 1;
   a.item_loops = int(ceil(cbrt(double(items)))) + 1;
+  a.item_most = int(items < (int64_t(1) << 30) ? items : int64_t(1) << 30);
   switch (kind) {
     case kAll: return launch_kind<kAll>(a, ws, st);
     case kWindow: return launch_kind<kWindow>(a, ws, st);

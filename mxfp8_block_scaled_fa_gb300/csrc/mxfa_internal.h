@@ -246,6 +246,7 @@ struct KvAttnArgs {
   int causal;
   int whole;              // no context is long enough to be cut (set by launch_kv_attn)
   int item_loops;         // trip count of kv_prefill.cu's loops over items (set by launch_kv_prefill)
+  int item_most;          // items that they have turns for beside the record that ends a run
   int split_rows;         // requests of more query rows (tokens x G) belong to kv_prefill.cu (set by launch_kv_attn)
   uint16_t* o;            // bf16 [total_q][Hq][128]
   float* lse;             // [Hq][total_q]
