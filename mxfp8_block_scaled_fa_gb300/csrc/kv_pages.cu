@@ -244,8 +244,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScan) kv_col
 // Whole blocks: the codes and scales of all heads of one lie in one piece each.  A CTA has the same few words of
 // every pair's blocks, and writes when it has read them all, so blocks may be read and written in one call (a
 // list of moves).  2^log2_words words of 16 bytes: eight, a line of memory; more for few pairs, to fill the CTA, and
-// fewer for many, so that several CTAs fit an SM (1000 pairs of 128 rows, 8 heads: eight words 78 us, four 57, 4.9 TB/s).
-// 512 threads: 200 pairs of 16 rows 3.9 us, of 64 rows 6.7; 256 threads 4.6 and 6.4, 1024 3.6 and 8.2.
+// fewer for many, so that several CTAs fit an SM (1000 pairs of 128 rows, 8 heads: eight words 78 us, four 55, 5.0 TB/s).
+// 512 threads: 200 pairs of 16 rows 3.8 us, of 64 rows 6.3; in their time 256 threads 4.6 and 6.4, 512 3.9 and 6.7, 1024 3.6 and 8.2.
 // Of several pairs that write one block the last is kept: each looks itself up by its block in `last`, an open table
 // of at least two places a pair, which lies where the words are put afterwards.
 __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(KvPages c, const int32_t* from, const int32_t* to, int n, int log2_words, int code_words,

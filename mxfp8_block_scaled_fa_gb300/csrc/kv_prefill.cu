@@ -42,7 +42,7 @@
 // half of the keys, 137 against 117 us for 24 x 64 rows over 6000 keys.  Launched ahead
 // of the kernels they wait for, the five kernels of a call take 313 instead of 319 us
 // from a stream (310 from a graph, either way).  These are figures of their time, against 309 us in the end; the
-// issuers' loops over items, no longer than the call needs, then made it 304.
+// issuers' loops over items, no longer than the call's tokens need, then made it 304.
 //
 // Windows and prefixes (KvKind, as in kv_attn.cu).  With a window an item's keys are the tiles of the sinks and those from its
 // first row's window on; the tiles between are no part of the line, and what a row does not see of the others is masked by
