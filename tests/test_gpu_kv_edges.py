@@ -312,3 +312,70 @@ def test_fork_time_grows_with_the_forks(mx):
     few, many = time(2048), time(16384)
     assert many <= 16 * few + 20, (few, many)                # all pairs of forks: 64 times
     assert mx.device_status() == 0
+
+
+@pytest.mark.parametrize("G,groups", [(4, [([1] * 9, 1024, [1, 5, 64, 65, 200, 900, 1, 2, 3])]), (4, [([100, 20, 1], 700, [100, 150, 1])]),
+                                      (40, [([2, 1], 700, [100, 150])])])
+def test_every_mode_captured_in_one_workspace(mx, G, groups):
+    """Calls of all modes one behind another in one workspace, captured, replayed for other queries and lengths, beside the same
+    on another stream with a workspace of its own."""
+    import torch
+    rng = np.random.default_rng(G)
+    c, q, cu, kv, table, slots, starts, pre, max_q, most, q_lens, kv_lens = shared_case(mx, rng, 0, 16, 2, G, groups, [], [(1, 300)])
+    n, Hq = q.shape[0], 2 * G
+    size = mx.mxfa_kv_attn_shared_workspace_size(kv.numel(), pre.numel(), n, max_q, most, table.shape[1] * 16, Hq, 2)
+    modes, sides = (True, False, None), []
+    for _ in range(2):
+        ws, outs, st = torch.empty(size, dtype=torch.uint8, device="cuda"), [results(q) for _ in modes], torch.cuda.Stream()
+
+        def one():
+            for share, out in zip(modes, outs):
+                mx.kv_attention_shared(q, c, cu, kv, table, starts, pre, max_q, most, 0.1, out=out, ws=ws, share=share)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            one()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            one()
+        sides.append((g, st, outs, ws))                      # a graph keeps no tensor: its workspace has to live as long
+    for shorter in (0, 1, 0):
+        q.copy_(torch.randn(q.shape, device="cuda"))
+        lens = [k - shorter if r == 0 and k - shorter >= int(pre[0]) + q_lens[0] else k for r, k in enumerate(kv_lens)]
+        kv.copy_(dev(lens))
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for g, st, _, _ in sides:
+                with torch.cuda.stream(st):
+                    g.replay()
+        torch.cuda.synchronize()
+        assert mx.device_status() == 0
+        for _, _, outs, _ in sides:
+            for o, lse in outs:
+                compare(c, q, cu, [s[:k] for s, k in zip(slots, lens)], o, lse, lambda r, n, k: more_ref.window_mask(n, k, 1 << 30, 0), scale=0.1)
+
+
+def test_fork_with_gaps_captured(mx):
+    """A fork with a gap whose counters are in place, captured once and replayed with other lists."""
+    import torch
+    table = np.array([[4, 5, 6, 7], [8, 9, 10, 11], [-1] * 4, [-1] * 4])
+    t, refs, ring, state = dev(table), mx.kv_refs(20), dev(list(range(12, 20)) + [0] * 12), dev([0, 8, 0], np.int64)
+    src, dst, lens, g0, g1 = (dev([0, 0]) for _ in range(5))
+    out = mx.KvFork(*(torch.empty(2, dtype=torch.int32, device="cuda") for _ in range(3)), state)
+    mx.kv_fork(t.clone(), dev([0]), dev([2]), dev([0]), refs.clone(), ring, state.clone(), 16)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mx.kv_fork(t, src, dst, lens, refs, ring, state, 16, out=out, gap=(g0, g1))
+    wt, wr, head = table.tolist(), [0] * 20, 0
+    for a, b, n, gaps in (([0, 1], [2, 3], [50, 33], [(1, 2), (0, 0)]), ([1, 0], [3, 2], [64, 17], [(0, 4), (0, 1)]), ([1, 1], [2, 3], [1, 0], [(0, 0), (0, 0)])):
+        for x, v in zip((src, dst, lens, g0, g1), (a, b, n, [x for x, _ in gaps], [y for _, y in gaps])):
+            x.copy_(dev(v))
+        g.replay()
+        torch.cuda.synchronize()
+        want = fork_with_gaps(wt, a, b, n, gaps, wr, host(ring).tolist(), head, 8, 16)
+        head = want[3][0]
+        for x, w in zip((out.from_blocks, out.to_blocks, out.lens, state), want):
+            assert host(x).tolist() == w
+        assert host(t).tolist() == wt and host(refs).tolist() == wr
+    assert mx.device_status() == 0
